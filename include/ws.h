@@ -394,6 +394,170 @@ void ws_graph_free(ws_graph* graph);
 int ws_argmax_rows_noalloc(const float* logits, int rows, int vocab, const uint32_t* suppress,
                            int32_t* out, ws_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Decode-serving operators on the caller's own buffers.  Like
+ * ws_argmax_rows_noalloc they need no context: arguments are described by a
+ * host struct that is read during the call, errors go to
+ * ws_last_error(NULL), nothing synchronises, nothing is allocated (scratch
+ * is the caller's workspace) and every call can be captured into a CUDA
+ * graph.  The stream, the device current in the calling thread and all
+ * pointers must belong to the same device.  Two calls that may overlap on
+ * the GPU (two streams, two graphs) need a workspace each.
+ * ------------------------------------------------------------------------ */
+
+/* A paged key/value cache with head width 64.  Element x (0..63) of token t
+ * of head h on page p is at
+ *   p * page_stride + h * head_stride + t * token_stride + x
+ * elements from k (keys) and from v (values), so the contexts' own pools
+ * ([page][K|V][head][token][64]), token-major pools ([page][token][head][64])
+ * and one slab per request (page_size = its length) are all described.
+ * Position j of a slot is token j % page_size of page
+ * page_table[slot * table_stride + j / page_size].  A page id outside
+ * [0, n_pages) is never read: its positions take no part in attention, and
+ * ws_cache_evict moves nothing from or to it. */
+typedef struct {
+  int32_t dtype;               /* WS_F32 or WS_BF16 (keys, values, queries, outputs) */
+  int32_t n_kv_heads;          /* >= 1 */
+  int32_t page_size;           /* tokens per page, >= 1 (a divisor of 64 that is >= 8, or >= 64, is fastest) */
+  int32_t n_pages;             /* >= 1 */
+  void* k;                     /* 16-byte aligned */
+  void* v;                     /* 16-byte aligned */
+  int64_t page_stride, head_stride, token_stride;   /* elements, >= 0; multiples of 16 bytes */
+  const int32_t* page_table;   /* [n_slots, table_stride] (device) */
+  int32_t n_slots;             /* >= 1 */
+  int32_t table_stride;        /* pages listed per slot, >= 1 */
+} ws_paged_cache;
+
+/* Arguments of ws_paged_attention (device pointers; sizes are host ints). */
+typedef struct {
+  int32_t n_req;               /* >= 0 */
+  const int32_t* req_ids;      /* [n_req] slots, distinct, or NULL (= 0..n_req-1) */
+  const int32_t* kv_len;       /* [n_slots] positions in the cache, the chunk's own included */
+  const int32_t* cu_q;         /* [n_req + 1] prefix sums of the chunk lengths (cu_q[0] = 0) */
+  int32_t total_q;             /* cu_q[n_req]: rows of q, out and lse (bounds every access to them) */
+  int32_t max_q;               /* >= every chunk length; longer chunks are cut off at it */
+  int32_t max_kv;              /* >= every kv_len; longer caches are cut off at it */
+  int32_t n_heads;             /* query heads, a multiple of n_kv_heads; head u reads KV head u / (n_heads / n_kv_heads) */
+  int32_t causal;              /* 1: row r of a chunk of c rows sees positions 0 .. kv_len - c + r; 0: all kv_len */
+  float scale;                 /* multiplies q . k (1/8 for the usual 1/sqrt(64)); finite */
+  const void* q;               /* row r, head u at r * q_stride + u * 64 elements; 16-byte aligned rows */
+  int64_t q_stride;
+  void* out;                   /* row r, head u at r * out_stride + u * 64; 16-byte aligned rows */
+  int64_t out_stride;
+  float* lse;                  /* [total_q, n_heads] out: log sum exp of the row's scores, or NULL */
+  float* mass;                 /* [n_slots, n_kv_heads, mass_stride] in/out, or NULL */
+  int64_t mass_stride;         /* >= max_kv */
+} ws_attention_args;
+
+/* Workspace bytes of the call (0: no workspace needed, or invalid arguments,
+ * which ws_paged_attention reports).  Depends on the host sizes alone. */
+size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attention_args* args);
+
+/* Attention of a chunk of new tokens over a paged cache: the step of
+ * ws_verify between the projections (Whisper-Flash Appendix A.1 keeps the
+ * decoder's keys and values in pages), for chunks of any length, shared
+ * key/value heads and the caller's own cache.  For every row and head
+ *   s_j = scale * q . k_j over the visible positions j,
+ *   lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
+ * with fp32 scores, statistics and sums (bf16: the weights enter the value
+ * product as bf16).  The chunk's own keys and values are already in the
+ * cache.  With `mass`, every position's weight exp(s_j - lse), summed over
+ * the chunk's rows and the query heads that share its KV head, is added to
+ * mass[slot, kv head, j]: the accumulated attention weight ws_cache_evict
+ * selects by.  Sums run in an order fixed by the sizes: the same call gives
+ * the same bits.
+ * A row that sees no position gets out = 0 and lse = -inf and adds no mass.
+ * Rows of requests with kv_len <= 0, or with an id outside [0, n_slots), see
+ * nothing.  Cached values behind kv_len are not read into any result.  Rows
+ * outside every chunk and mass behind kv_len are left as they were. */
+int ws_paged_attention(const ws_paged_cache* cache, const ws_attention_args* args, void* workspace,
+                       size_t workspace_bytes, ws_stream stream);
+
+/* Arguments of ws_cache_evict (device pointers; sizes are host ints). */
+typedef struct {
+  int32_t n_req;               /* >= 0 */
+  const int32_t* req_ids;      /* [n_req] slots, distinct, or NULL (= 0..n_req-1) */
+  const int32_t* kv_len;       /* [n_slots] positions before the call */
+  int32_t* kv_len_out;         /* [n_slots] out: min(kv_len, keep); may be kv_len */
+  int32_t max_kv;              /* >= every kv_len; longer caches are cut off at it */
+  int32_t keep;                /* positions kept per slot and head, 1..max_kv */
+  int32_t sink;                /* the first `sink` positions are always kept ... */
+  int32_t recent;              /* ... and the last `recent`; sink + recent <= keep */
+  const float* mass;           /* [n_slots, n_kv_heads, mass_stride] accumulated weights */
+  int64_t mass_stride;         /* >= max_kv */
+  float* mass_out;             /* [n_slots, n_kv_heads, mass_out_stride] out, or NULL; may be mass */
+  int64_t mass_out_stride;     /* >= keep */
+  const int32_t* pos;          /* [n_slots, n_kv_heads, pos_stride] a label per position, or NULL */
+  int64_t pos_stride;          /* >= max_kv */
+  int32_t* pos_out;            /* [n_slots, n_kv_heads, pos_out_stride] out, or NULL; may be pos */
+  int64_t pos_out_stride;      /* >= keep */
+  const int32_t* page_table_out;   /* [n_slots, table_out_stride] pages that receive the kept positions, or NULL */
+  int32_t table_out_stride;        /* (= the cache's own page table: compaction in place) */
+} ws_evict_args;
+
+size_t ws_cache_evict_workspace(const ws_paged_cache* cache, const ws_evict_args* args);
+
+/* Eviction from a paged cache by accumulated attention weight.  For every
+ * slot and KV head the kept positions are the first `sink`, the last
+ * `recent`, and of the others those of the largest mass (equal: the lower
+ * position; negative and NaN masses count as 0), min(kv_len, keep) in all.
+ * Their keys, values, masses and labels move, in their order, to positions
+ * 0, 1, ... of the destination pages.  pos_out holds for each its label pos,
+ * or, with pos NULL, its position before the call.  A cache that already
+ * fits keeps all its positions.  Pages given by page_table_out are disjoint
+ * from every page that the call reads, or page_table_out is NULL or the
+ * cache's page_table and the move is in place; mass_out = mass and
+ * pos_out = pos are in place with equal strides, and otherwise the arrays
+ * are disjoint.  Slots must not share pages that the call writes.  Contents
+ * behind the new length, and slots not listed, are left as they were. */
+int ws_cache_evict(const ws_paged_cache* cache, const ws_evict_args* args, void* workspace,
+                   size_t workspace_bytes, ws_stream stream);
+
+/* Arguments of ws_logits_rules (device pointers; sizes are host ints). */
+typedef struct {
+  int32_t n, H, vocab;         /* requests, block rows per request, vocabulary (1..2^24) */
+  const float* logits;         /* row (i, j) at (i * H + j) * ld */
+  int64_t ld;                  /* >= vocab */
+  float* out;                  /* row (i, j) at (i * H + j) * ld_out; may be logits with ld_out = ld */
+  int64_t ld_out;
+  const int32_t* block_len;    /* [n] rows in use, or NULL (= H) */
+  const int32_t* history;      /* [n, hist_stride] tokens so far, the block's anchor included, or NULL (none) */
+  const int32_t* hist_len;     /* [n] */
+  int32_t hist_stride;         /* 0..32768 */
+  const int32_t* block;        /* [n, block_stride] the block (column 0 the anchor), or NULL */
+  int32_t block_stride;        /* >= H */
+  int32_t window;              /* only the last `window` tokens of a row's sequence count; 0: all */
+  const float* repetition;     /* [n] theta > 0, or NULL (1) */
+  const float* presence;       /* [n], or NULL (0) */
+  const float* frequency;      /* [n], or NULL (0) */
+  const int32_t* bias_ids;     /* [n, bias_stride] tokens with a bias, or NULL (none) */
+  const float* bias_vals;      /* [n, bias_stride] */
+  const int32_t* bias_len;     /* [n] entries in use */
+  int32_t bias_stride;         /* 0..32768 */
+  const uint32_t* masks;       /* [n_masks, ceil(vocab/32)] grammar states: bit set = token allowed, or NULL */
+  int32_t n_masks;
+  const int32_t* mask_row;     /* [n, H] the row's grammar state; outside [0, n_masks): no constraint */
+  int32_t* target;             /* [n, H] out: argmax of the row's new logits, or NULL */
+  float* logprob;              /* [n, H] out: log softmax of the row's new logits at target, or NULL */
+} ws_rules_args;
+
+/* Penalties for repeated tokens, biases and grammar masks on the logits of a
+ * verified block (the rows ws_verify wrote), with the greedy choice under
+ * them.  Row j of request i follows the tokens S = history[i, 0:hist_len[i]],
+ * block[i, 1:j+1] (the proposals before it), of which the last `window`
+ * count.  For a token v that S holds c times, z its logit:
+ *   c > 0:      z = z > 0 ? z / repetition : z * repetition
+ *               z = z - (frequency * c + presence)
+ *   v biased:   z = z + bias (the first entry that lists v)
+ *   v excluded by the row's grammar state:  z = -inf
+ * each step rounded to fp32.  Token ids outside [0, vocab) are ignored.
+ *   target   lowest id among the largest new logits; -1 for rows >=
+ *            block_len and where no token is left above -inf
+ *   logprob  0 for rows >= block_len, -inf where target is -1
+ * A NaN logit is never chosen (its row's logprob is NaN).  Rows >= block_len of `out` are left as they
+ * were.  ws_accept takes target (GREEDY) or out (SAMPLE) as its own. */
+int ws_logits_rules(const ws_rules_args* args, ws_stream stream);
+
 /* Number of CUDA kernels this library has launched in the process so far
  * (all contexts; host-side counter, for instrumentation). */
 unsigned long long ws_launch_count(void);

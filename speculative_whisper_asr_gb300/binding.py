@@ -26,7 +26,9 @@ EXPORTS = ("ws_query_workspace", "ws_load_weights", "ws_reset", "ws_cross_kv", "
            "ws_get_centers", "ws_set_tree", "ws_tree_tokens", "ws_verify_tree",
            "ws_encoder_workspace", "ws_encoder_load", "ws_encode", "ws_encoder_status", "ws_encoder_error",
            "ws_encoder_free", "ws_encoder_attention",
-           "ws_fused_layernorm")
+           "ws_fused_layernorm",
+           "ws_paged_attention_workspace", "ws_paged_attention", "ws_cache_evict_workspace", "ws_cache_evict",
+           "ws_logits_rules")
 
 
 class WSError(RuntimeError):
@@ -51,6 +53,41 @@ class AcceptArgs(C.Structure):
                 ("next_block", C.c_void_p), ("next_stride", C.c_int32), ("next_len", C.c_void_p),
                 ("transcript", C.c_void_p), ("out_len", C.c_void_p), ("tcap", C.c_int32),
                 ("n_done", C.c_void_p)]
+
+
+class PagedCacheDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_kv_heads", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("token_stride", C.c_int64), ("page_table", C.c_void_p), ("n_slots", C.c_int32),
+                ("table_stride", C.c_int32)]
+
+
+class AttentionArgs(C.Structure):
+    _fields_ = [("n_req", C.c_int32), ("req_ids", C.c_void_p), ("kv_len", C.c_void_p), ("cu_q", C.c_void_p),
+                ("total_q", C.c_int32), ("max_q", C.c_int32), ("max_kv", C.c_int32), ("n_heads", C.c_int32),
+                ("causal", C.c_int32), ("scale", C.c_float), ("q", C.c_void_p), ("q_stride", C.c_int64),
+                ("out", C.c_void_p), ("out_stride", C.c_int64), ("lse", C.c_void_p), ("mass", C.c_void_p),
+                ("mass_stride", C.c_int64)]
+
+
+class EvictArgs(C.Structure):
+    _fields_ = [("n_req", C.c_int32), ("req_ids", C.c_void_p), ("kv_len", C.c_void_p), ("kv_len_out", C.c_void_p),
+                ("max_kv", C.c_int32), ("keep", C.c_int32), ("sink", C.c_int32), ("recent", C.c_int32),
+                ("mass", C.c_void_p), ("mass_stride", C.c_int64), ("mass_out", C.c_void_p),
+                ("mass_out_stride", C.c_int64), ("pos", C.c_void_p), ("pos_stride", C.c_int64),
+                ("pos_out", C.c_void_p), ("pos_out_stride", C.c_int64), ("page_table_out", C.c_void_p),
+                ("table_out_stride", C.c_int32)]
+
+
+class RulesArgs(C.Structure):
+    _fields_ = [("n", C.c_int32), ("H", C.c_int32), ("vocab", C.c_int32), ("logits", C.c_void_p), ("ld", C.c_int64),
+                ("out", C.c_void_p), ("ld_out", C.c_int64), ("block_len", C.c_void_p), ("history", C.c_void_p),
+                ("hist_len", C.c_void_p), ("hist_stride", C.c_int32), ("block", C.c_void_p),
+                ("block_stride", C.c_int32), ("window", C.c_int32), ("repetition", C.c_void_p),
+                ("presence", C.c_void_p), ("frequency", C.c_void_p), ("bias_ids", C.c_void_p),
+                ("bias_vals", C.c_void_p), ("bias_len", C.c_void_p), ("bias_stride", C.c_int32),
+                ("masks", C.c_void_p), ("n_masks", C.c_int32), ("mask_row", C.c_void_p), ("target", C.c_void_p),
+                ("logprob", C.c_void_p)]
 
 
 class EncoderDesc(C.Structure):
@@ -94,6 +131,11 @@ def _load():
         "ws_set_tree": (I, [P, I, P, P]),
         "ws_tree_tokens": (I, [P, I, P, P, I, P, P, I, P, S]),
         "ws_verify_tree": (I, [P, I, P, I, P, P, P, P, S]),
+        "ws_paged_attention_workspace": (C.c_size_t, [P, P]),
+        "ws_paged_attention": (I, [P, P, P, C.c_size_t, S]),
+        "ws_cache_evict_workspace": (C.c_size_t, [P, P]),
+        "ws_cache_evict": (I, [P, P, P, C.c_size_t, S]),
+        "ws_logits_rules": (I, [P, S]),
         "ws_encoder_workspace": (C.c_size_t, [C.POINTER(EncoderDesc)]),
         "ws_encoder_load": (I, [C.POINTER(P), C.POINTER(EncoderDesc), P, C.c_size_t, P, S]),
         "ws_encode": (I, [P, I, P, P, S]),
@@ -317,3 +359,23 @@ def ws_encoder_free(enc):
 
 def ws_argmax_rows_noalloc(logits, rows, vocab, suppress, out, stream):
     return _check(None, lib.ws_argmax_rows_noalloc(logits, rows, vocab, suppress or None, out, stream))
+
+
+def ws_paged_attention_workspace(cache: PagedCacheDesc, args: AttentionArgs) -> int:
+    return lib.ws_paged_attention_workspace(C.addressof(cache), C.addressof(args))
+
+
+def ws_paged_attention(cache: PagedCacheDesc, args: AttentionArgs, workspace, nbytes, stream):
+    return _check(None, lib.ws_paged_attention(C.addressof(cache), C.addressof(args), workspace or None, nbytes, stream))
+
+
+def ws_cache_evict_workspace(cache: PagedCacheDesc, args: EvictArgs) -> int:
+    return lib.ws_cache_evict_workspace(C.addressof(cache), C.addressof(args))
+
+
+def ws_cache_evict(cache: PagedCacheDesc, args: EvictArgs, workspace, nbytes, stream):
+    return _check(None, lib.ws_cache_evict(C.addressof(cache), C.addressof(args), workspace or None, nbytes, stream))
+
+
+def ws_logits_rules(args: RulesArgs, stream):
+    return _check(None, lib.ws_logits_rules(C.addressof(args), stream))

@@ -452,3 +452,198 @@ class Encoder:
     def set_attention(self, tcgen05: bool):
         """Attention kernel: tcgen05 flash attention (default) or the legacy mma.sync one."""
         B.ws_encoder_attention(self.enc, 1 if tcgen05 else 0)
+
+
+# ---------------------------------------------------------------------- operators on the caller's tensors
+def _check_tensor(name, t, dtype, ndim, device, dense=True):
+    """A device tensor of the given type; dense: its last dimension is contiguous."""
+    if t.dtype is not dtype or t.dim() != ndim or t.device != device:
+        raise ValueError(f"{name}: a {ndim}-d {dtype} tensor on {device} is needed")
+    if dense and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _rows(name, t, dtype, shape, device):
+    """A contiguous device tensor of exactly this type and shape."""
+    if t.dtype is not dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is needed")
+    return t.data_ptr()
+
+
+def _on(device):
+    """The stream handle of the current stream, with `device` the current device."""
+    s = torch.cuda.current_stream()
+    if s.device != device:
+        raise ValueError(f"the tensors are on {device}, the current stream is on {s.device}")
+    return s.cuda_stream
+
+
+class PagedCache:
+    """A paged key/value cache in the caller's tensors (ws_paged_cache):
+    k, v [pages, KV heads, page_size, 64] with any strides that are multiples
+    of 16 bytes (the same for both), page_table [slots, pages per slot] int32.
+    The object keeps scratch for each stream that called it; graphs captured
+    on one stream share it, so those that may replay at the same time need a
+    PagedCache each."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
+        if k.dtype not in (torch.bfloat16, torch.float32) or k.dim() != 4 or k.shape[3] != 64 or not k.is_cuda:
+            raise ValueError("k: a CUDA tensor [pages, heads, page_size, 64] in bf16 or fp32 is needed")
+        if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+            raise ValueError("v must have the type, shape, strides and device of k")
+        if k.stride(3) != 1:
+            raise ValueError("the head dimension must be contiguous")
+        _check_tensor("page_table", page_table, torch.int32, 2, k.device)
+        self.k, self.v, self.page_table = k, v, page_table
+        self.dev, self.dtype = k.device, k.dtype
+        self.pages, self.heads, self.page_size, _ = k.shape
+        self.slots = page_table.shape[0]
+        self.desc = B.PagedCacheDesc(
+            B.WS_BF16 if k.dtype is torch.bfloat16 else B.WS_F32, self.heads, self.page_size, self.pages, k.data_ptr(),
+            v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(), self.slots,
+            page_table.stride(0) if self.slots > 1 else page_table.shape[1])
+        if self.slots > 1 and page_table.stride(0) < page_table.shape[1]:
+            raise ValueError("page_table rows must not overlap")
+        self._attn, self._evict = B.AttentionArgs(), B.EvictArgs()
+        self._ws, self._kept = {}, []
+
+    def _workspace(self, nbytes, stream):
+        """Scratch of this stream.  Outgrown scratch is kept: work in flight or a captured graph may still use it."""
+        if nbytes == 0:
+            return 0
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < nbytes:
+            if ws is not None:
+                self._kept.append(ws)
+                nbytes = max(nbytes, 2 * ws.numel())
+            ws = self._ws[stream] = torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
+        return ws.data_ptr()
+
+    def _slots(self, req_ids, n):
+        return 0 if req_ids is None else _rows("req_ids", req_ids, torch.int32, (n,), self.dev)
+
+    def attend(self, q, kv_len, cu_q, max_q: int, max_kv: int, causal: bool = True, scale: float = 0.125, out=None,
+               lse=None, mass=None, req_ids=None):
+        """Attention of the chunks q [total_q, heads, 64] over the cache (ws_paged_attention).  kv_len [slots] int32
+        counts the chunk's own positions; cu_q [requests + 1] int32.  lse [total_q, heads] fp32 receives the
+        log-sum-exp; mass [slots, KV heads, >= max_kv] fp32 is added to.  Returns out."""
+        _check_tensor("q", q, self.dtype, 3, self.dev)
+        if out is None:
+            out = torch.zeros_like(q, memory_format=torch.contiguous_format)
+        _check_tensor("out", out, self.dtype, 3, self.dev)
+        if out.shape != q.shape or q.shape[2] != 64 or (q.shape[1] > 1 and (q.stride(1) != 64 or out.stride(1) != 64)):
+            raise ValueError("q and out: [rows, heads, 64] with contiguous heads are needed")
+        a = self._attn
+        rows, heads, _ = q.shape
+        n = cu_q.shape[0] - 1
+        a.n_req, a.req_ids = n, self._slots(req_ids, n)
+        a.kv_len = _rows("kv_len", kv_len, torch.int32, (self.slots,), self.dev)
+        a.cu_q = _rows("cu_q", cu_q, torch.int32, (n + 1,), self.dev)
+        a.total_q, a.max_q, a.max_kv, a.n_heads = rows, max_q, max_kv, heads
+        a.causal, a.scale = int(causal), scale
+        a.q, a.q_stride = q.data_ptr(), q.stride(0) if rows > 1 else heads * 64
+        a.out, a.out_stride = out.data_ptr(), out.stride(0) if rows > 1 else heads * 64
+        a.lse = 0 if lse is None else _rows("lse", lse, torch.float32, (rows, heads), self.dev)
+        a.mass = 0
+        if mass is not None:
+            a.mass_stride = mass.shape[2] if mass.dim() == 3 else 0
+            a.mass = _rows("mass", mass, torch.float32, (self.slots, self.heads, a.mass_stride), self.dev)
+        s = _on(self.dev)
+        need = B.ws_paged_attention_workspace(self.desc, a)
+        B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
+        return out
+
+    def evict(self, kv_len, mass, keep: int, max_kv: int, sink: int = 0, recent: int = 0, page_table_out=None,
+              kv_len_out=None, mass_out=None, pos=None, pos_out=None, req_ids=None):
+        """Keep min(kv_len, keep) positions per slot and head (ws_cache_evict): the first `sink`, the last `recent`,
+        then those of the largest mass.  Without page_table_out the cache, and without kv_len_out / mass_out / pos_out
+        the lengths, masses and labels, are compacted in place."""
+        a = self._evict
+        n = self.slots if req_ids is None else req_ids.shape[0]
+        a.n_req, a.req_ids = n, self._slots(req_ids, n)
+        a.kv_len = _rows("kv_len", kv_len, torch.int32, (self.slots,), self.dev)
+        a.kv_len_out = a.kv_len if kv_len_out is None else _rows("kv_len_out", kv_len_out, torch.int32, (self.slots,),
+                                                                 self.dev)
+        a.max_kv, a.keep, a.sink, a.recent = max_kv, keep, sink, recent
+
+        def per_position(name, t, dtype):
+            return _rows(name, t, dtype, (self.slots, self.heads, t.shape[-1]), self.dev), t.shape[-1]
+        a.mass, a.mass_stride = per_position("mass", mass, torch.float32)
+        a.mass_out, a.mass_out_stride = ((a.mass, a.mass_stride) if mass_out is None
+                                         else per_position("mass_out", mass_out, torch.float32))
+        a.pos, a.pos_stride = (0, 0) if pos is None else per_position("pos", pos, torch.int32)
+        a.pos_out, a.pos_out_stride = ((a.pos, a.pos_stride) if pos_out is None
+                                       else per_position("pos_out", pos_out, torch.int32))
+        a.page_table_out = 0
+        if page_table_out is not None:
+            a.table_out_stride = page_table_out.shape[1]
+            a.page_table_out = _rows("page_table_out", page_table_out, torch.int32, (self.slots, a.table_out_stride),
+                                     self.dev)
+        s = _on(self.dev)
+        need = B.ws_cache_evict_workspace(self.desc, a)
+        B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
+
+
+class LogitsRules:
+    """Penalties, biases and grammar masks of a batch of requests
+    (ws_logits_rules).  repetition / presence / frequency: [n] fp32; bias_ids
+    [n, entries] int32 with bias_vals and bias_len [n]; masks [states,
+    ceil(vocab / 32)] int32 words, bit set = token allowed; window: how many
+    of the latest tokens count (0: all)."""
+
+    def __init__(self, repetition=None, presence=None, frequency=None, window: int = 0, bias_ids=None, bias_vals=None,
+                 bias_len=None, masks=None):
+        self.repetition, self.presence, self.frequency, self.window = repetition, presence, frequency, window
+        self.bias_ids, self.bias_vals, self.bias_len, self.masks = bias_ids, bias_vals, bias_len, masks
+        self._args = B.RulesArgs()
+
+    def apply(self, logits, history=None, hist_len=None, block=None, block_len=None, mask_row=None, out=None,
+              target=None, logprob=None):
+        """New logits of rows [n, H, vocab] fp32 into out (default: in place).  history [n, tokens] with hist_len [n]:
+        the tokens so far, the anchor included; block [n, >= H]: the block, whose columns 1..j precede row j;
+        mask_row [n, H]: each row's grammar state.  target [n, H] int32 and logprob [n, H] fp32 receive the greedy
+        choice.  Returns out."""
+        dev = logits.device
+        out = logits if out is None else out
+        _check_tensor("logits", logits, torch.float32, 3, dev)
+        _check_tensor("out", out, torch.float32, 3, dev)
+        n, H, V = logits.shape
+        for t in (logits, out):
+            if t.shape != logits.shape or (n > 1 and t.stride(0) != H * t.stride(1)):
+                raise ValueError("logits and out: [n, H, vocab] with evenly spaced rows are needed")
+        a = self._args
+        a.n, a.H, a.vocab = n, H, V
+        a.logits, a.ld = logits.data_ptr(), logits.stride(1) if H > 1 else logits.stride(0) if n > 1 else V
+        a.out, a.ld_out = out.data_ptr(), out.stride(1) if H > 1 else out.stride(0) if n > 1 else V
+
+        def per_request(name, t, dtype):
+            return 0 if t is None else _rows(name, t, dtype, (n,), dev)
+        a.block_len = per_request("block_len", block_len, torch.int32)
+        a.history = a.hist_len = a.hist_stride = 0
+        if history is not None:
+            a.hist_stride = history.shape[1]
+            a.history = _rows("history", history, torch.int32, (n, a.hist_stride), dev)
+            a.hist_len = per_request("hist_len", hist_len, torch.int32)
+        a.block = a.block_stride = 0
+        if block is not None:
+            a.block_stride = block.shape[1]
+            a.block = _rows("block", block, torch.int32, (n, a.block_stride), dev)
+        a.window = self.window
+        a.repetition = per_request("repetition", self.repetition, torch.float32)
+        a.presence = per_request("presence", self.presence, torch.float32)
+        a.frequency = per_request("frequency", self.frequency, torch.float32)
+        a.bias_ids = a.bias_vals = a.bias_len = a.bias_stride = 0
+        if self.bias_ids is not None:
+            a.bias_stride = self.bias_ids.shape[1]
+            a.bias_ids = _rows("bias_ids", self.bias_ids, torch.int32, (n, a.bias_stride), dev)
+            a.bias_vals = _rows("bias_vals", self.bias_vals, torch.float32, (n, a.bias_stride), dev)
+            a.bias_len = per_request("bias_len", self.bias_len, torch.int32)
+        a.masks = a.n_masks = a.mask_row = 0
+        if self.masks is not None and mask_row is not None:
+            a.n_masks = self.masks.shape[0]
+            a.masks = _rows("masks", self.masks, torch.int32, (a.n_masks, (V + 31) // 32), dev)
+            a.mask_row = _rows("mask_row", mask_row, torch.int32, (n, H), dev)
+        a.target = 0 if target is None else _rows("target", target, torch.int32, (n, H), dev)
+        a.logprob = 0 if logprob is None else _rows("logprob", logprob, torch.float32, (n, H), dev)
+        B.ws_logits_rules(a, _on(dev))
+        return out
