@@ -719,6 +719,25 @@ bool tc_encode_map(TcMap* m, const void* base, uint64_t rows, uint64_t cols, uin
   return r == CUDA_SUCCESS;
 }
 
+// Keys or values of a paged cache as a 4-D map {64 dims, tokens, heads,
+// pages} with boxes of box_rows tokens of one head and page, 128-byte
+// swizzle.  Tokens behind the page's end and pages outside the pool read as 0.
+bool tc_encode_paged(TcMap* m, const void* base, const ws_paged_cache& c, uint32_t box_rows) {
+  if (!tc_engine_available()) return false;
+  cuuint64_t dims[4] = {WS_DH, (cuuint64_t)c.page_size, (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
+  // a dimension of one entry is never stepped through: any valid stride does
+  auto bytes = [](int64_t stride, int64_t n) { return (cuuint64_t)(n > 1 || stride > 0 ? stride * 2 : WS_DH * 2); };
+  cuuint64_t strides[3] = {bytes(c.token_stride, c.page_size), bytes(c.head_stride, c.n_kv_heads),
+                           bytes(c.page_stride, c.n_pages)};
+  cuuint32_t box[4] = {WS_DH, box_rows, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(reinterpret_cast<CUtensorMap*>(m), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Row-major fp32 matrix [rows, cols] (cols a multiple of 256) as a 3-D TMA
 // map {256, cols / 256, rows} whose box holds box_rows whole rows, stored
 // row after row in shared memory (no swizzle).  Rows beyond `rows` read as 0.

@@ -1,34 +1,11 @@
 // Attention of a chunk of new tokens over a paged cache
 // (ws_paged_attention in include/ws.h gives the formulas).
-#include "ws_paged.cuh"
+#include "ws_attn_mma.cuh"
+#include "ws_pattn.cuh"
 
 namespace {
 
-struct AttnP {
-  ws_paged_cache c;
-  ws_attention_args a;
-  int G;                                   // query heads per KV head
-};
-
-struct Req {
-  int slot, row0, c, L;                    // cache slot, first row, chunk length, visible positions
-};
-__device__ __forceinline__ Req request(const AttnP& p, int i) {
-  Req r;
-  r.slot = p.a.req_ids ? p.a.req_ids[i] : i;
-  r.row0 = p.a.cu_q[i];
-  const int end = min(p.a.cu_q[i + 1], p.a.total_q);
-  r.c = r.row0 >= 0 ? min(max(end - r.row0, 0), p.a.max_q) : 0;
-  r.L = 0;
-  if (r.slot >= 0 && r.slot < p.c.n_slots)
-    r.L = (int)min((long long)min(max(p.a.kv_len[r.slot], 0), p.a.max_kv), (long long)p.c.table_stride * p.c.page_size);
-  return r;
-}
-// Positions 0 .. limit - 1 are visible to row t of the chunk.
-__device__ __forceinline__ int row_limit(const AttnP& p, const Req& r, int t) {
-  return p.a.causal ? max(0, min(r.L, r.L - r.c + t + 1)) : r.L;
-}
-
+// ------------------------------------------------------------------ fp32
 // One warp per (row, query head), two dims per lane.
 template <typename T>
 __global__ void simple_attn(const AttnP p) {
@@ -57,12 +34,12 @@ __global__ void simple_attn(const AttnP p) {
   T* out = (T*)p.a.out + (size_t)row * p.a.out_stride + (size_t)u * WS_DH;
   out[lane] = from_f<T>(o0 * inv);
   out[lane + 32] = from_f<T>(o1 * inv);
-  if (p.a.lse && lane == 0) p.a.lse[(size_t)row * p.a.n_heads + u] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (p.lse && lane == 0) p.lse[(size_t)row * p.a.n_heads + u] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 // One warp per (slot, KV head, position): the weights of every row and head.
 template <typename T>
-__global__ void simple_mass(const AttnP p, const float* lse) {
+__global__ void simple_mass(const AttnP p) {
   const int j = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.y, h = blockIdx.z;
   const Req r = request(p, i);
@@ -80,12 +57,415 @@ __global__ void simple_mass(const AttnP p, const float* lse) {
       float s = to_f(q[lane]) * k0 + to_f(q[lane + 32]) * k1;
 #pragma unroll
       for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-      sum += expf(s * p.a.scale - lse[(size_t)(r.row0 + t) * p.a.n_heads + u]);
+      sum += expf(s * p.a.scale - p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u]);
     }
   }
   if (lane == 0) p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + j] += sum;
 }
 
+// ------------------------------------------------------------------ bf16, few rows: stream the cache once
+// The rows of a (request, KV head) — chunk rows x the query heads that share
+// the KV head — are cut into row tiles of 8 * NT.  One CTA takes a row tile
+// and a range of key tiles; its four warps take every fourth tile of 32 keys
+// through private rings of three TMA slots each (K and V, 128-byte swizzle),
+// so no warp waits for another until the end.  HBM bounds the kernel, so the
+// instruction count per byte matters: the products are taken transposed,
+//   S^T = K Q^T    (16 keys x 8 rows per mma m16n8k16),
+//   O^T = V^T P^T  (16 dims x 8 rows),
+// which puts 8 rows, not 16, into an instruction.  S^T leaves the tensor core
+// with keys along lanes; movmatrix turns the bf16 weights into the second
+// product's operand.  Scores stay raw; p = 2^(s * sl - m * sl) with one FMA
+// and one exponential.  The reference m of a row moves only when a score
+// exceeds it by more than 2^8 (p <= 256), which a vote detects, so the
+// common tile needs no reduction across lanes.  Statistics and sums are
+// fp32; the weights are rounded to bf16 for the value product alone (2^-8
+// relative at most, the output's own step).
+constexpr int SP_TK = 32;                  // keys per tile
+constexpr int SP_NS = 3;                   // ring slots per warp
+constexpr int SP_W = 4;                    // warps
+constexpr int SP_KB = SP_TK * WS_DH * 2;   // bytes of a K or V tile
+constexpr int SP_RING = SP_W * SP_NS * 2 * SP_KB;
+constexpr int SP_SMEM = SP_RING + 1024;
+constexpr float SP_HOLD = 8.0f;
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int t, int h, int p) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(tc::smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(t), "r"(h), "r"(p), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// A warp's walk over every step-th tile from t0 on: position of the tile and
+// the page(s) of its keys.
+struct TileWalk {
+  int t, pi, sub, step;
+  __device__ __forceinline__ void start(const TileGeo& g, int t0, int st) {
+    t = t0; step = st;
+    if (g.tpp) { pi = t0 / g.tpp; sub = t0 - pi * g.tpp; }
+  }
+  __device__ __forceinline__ void next(const TileGeo& g) {
+    t += step;
+    if (g.tpp) { sub += step; while (sub >= g.tpp) { sub -= g.tpp; ++pi; } }
+  }
+  // first position of the tile, keys it may hold, and for key j its table entry
+  __device__ __forceinline__ int base(const TileGeo& g, int ps, int tk) const { return g.tpp ? pi * ps + sub * tk : t * tk; }
+  __device__ __forceinline__ int room(const TileGeo& g, int ps, int tk) const { return g.tpp ? min(tk, ps - sub * tk) : tk; }
+  __device__ __forceinline__ int entry(const TileGeo& g, int j) const { return g.tpp ? pi : (t << g.ppt_log) + (j >> g.page_log); }
+};
+
+struct SpMeta { uint32_t valid; int base; };   // keys of a tile that count; its first position
+
+// Query fragments of 8 * NT rows (B operand): rows r0 + 8 nt + lane / 4.
+template <int NT>
+__device__ __forceinline__ void sp_load_q(const AttnP& p, const Req& r, int h, int r0, int R, uint32_t qf[4][NT][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int rho = r0 + 8 * nt + g;
+    const bool on = rho < R;
+    const int t = on ? rho / p.G : 0;
+    const bf16* q = (const bf16*)p.a.q + (size_t)(r.row0 + t) * p.a.q_stride + (size_t)(h * p.G + (on ? rho - t * p.G : 0)) * WS_DH;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t v = on ? __ldg(reinterpret_cast<const unsigned int*>(q + 16 * s + 8 * e + 2 * c)) : 0u;
+        qf[s][nt][e] = on ? (v & p.q_and) ^ p.q_xor : 0u;
+      }
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(SP_W * 32, NT == 4 ? 1 : 2)
+split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  extern __shared__ uint8_t dsm[];
+  __shared__ __align__(8) uint64_t full[SP_W][SP_NS];
+  __shared__ SpMeta meta[SP_W][SP_NS];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int rt = blockIdx.x / p.nsplit, split = blockIdx.x - rt * p.nsplit, h = blockIdx.y, i = blockIdx.z;
+  const Req r = request(p, i);
+  const int R = r.c * p.G, r0 = rt * 8 * NT;
+  if (r0 >= R) return;
+  if (lane == 0)
+    for (int s = 0; s < SP_NS; ++s) tc::mbar_init(&full[warp][s], 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
+  // positions that some row of this tile sees, and those that all see
+  const int last = min(R, r0 + 8 * NT) - 1;
+  const int Lmax = row_limit(p, r, last / p.G), Lmin = row_limit(p, r, r0 / p.G);
+  const int nt_all = tile_count(p.geo, p.c.page_size, SP_TK, Lmax);
+  const int tb = min(nt_all, split * p.tps), te = min(nt_all, tb + p.tps);
+  const int n_my = max(0, (te - tb - warp + SP_W - 1) / SP_W);
+  const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
+  uint8_t* ring = sm + warp * (SP_NS * 2 * SP_KB);
+
+  TileWalk w;
+  w.start(p.geo, tb + warp, SP_W);
+  auto page_of = [&]() -> int {             // this lane's key's page in the walk's tile, -1: none
+    const int j = lane, e = w.entry(p.geo, j);
+    const int pos = w.base(p.geo, p.c.page_size, SP_TK) + j;
+    if (j >= w.room(p.geo, p.c.page_size, SP_TK) || pos >= Lmax || e >= p.c.table_stride) return -1;
+    return __ldg(table + e);
+  };
+  auto issue = [&](int slot, int page) {
+    const bool ok = page >= 0 && page < p.c.n_pages;
+    const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+    const bool go = ok && (p.geo.tpp ? (valid & ((1u << lane) - 1u)) == 0u : (lane & (p.geo.box - 1)) == 0);
+    const unsigned boxes = __ballot_sync(0xffffffffu, go);
+    if (lane == 0) {
+      meta[warp][slot].valid = valid;
+      meta[warp][slot].base = w.base(p.geo, p.c.page_size, SP_TK);
+      tc::mbar_expect_tx(&full[warp][slot], (uint32_t)__popc(boxes) * 2u * (uint32_t)p.geo.box * 128u);
+    }
+    __syncwarp();
+    if (go) {
+      uint8_t* dst = ring + slot * (2 * SP_KB) + (p.geo.tpp ? 0 : lane * 128);
+      const int tok = p.geo.tpp ? w.sub * SP_TK : 0;
+      tma_load_4d(dst, &mk, &full[warp][slot], 0, tok, h, page);
+      tma_load_4d(dst + SP_KB, &mv, &full[warp][slot], 0, tok, h, page);
+    }
+  };
+  for (int s = 0; s < SP_NS && s < n_my; ++s) { issue(s, page_of()); w.next(p.geo); }
+
+  uint32_t qf[4][NT][2];
+  sp_load_q<NT>(p, r, h, r0, R, qf);
+  int lim[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) lim[nt][e] = row_limit(p, r, min(r0 + 8 * nt + 2 * c + e, R - 1) / p.G);
+  float o[4][NT][4], m[NT][2], msl[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) { m[nt][e] = -INFINITY; msl[nt][e] = 0.f; l[nt][e] = 0.f; }
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
+  }
+  const float sl = p.sl, hold = fminf(SP_HOLD / sl, 1e30f);
+  bool dead = false;
+  for (int it = 0; it < n_my; ++it) {
+    const int slot = it % SP_NS;
+    const bool more = it + SP_NS < n_my;
+    const int page_next = more ? page_of() : -1;      // in flight while this tile is computed
+    if (!tc::mbar_wait(&full[warp][slot], (uint32_t)((it / SP_NS) & 1))) { dead = true; break; }
+    const SpMeta mt_ = meta[warp][slot];
+    uint8_t* Kt = ring + slot * (2 * SP_KB);
+    uint8_t* Vt = Kt + SP_KB;
+    if (mt_.valid != 0xffffffffu) {
+      // rows that do not count may hold anything: 0 * inf would reach the sums
+      if (!((mt_.valid >> lane) & 1u)) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(Vt + lane * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next copy
+      __syncwarp();
+    }
+    const uint32_t kb = tc::smem_u32(Kt), vb = tc::smem_u32(Vt);
+    float sc[2][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        uint32_t a[4];
+        const int mtx = lane >> 3, key = 16 * mt + ((mtx & 1) << 3) + (lane & 7);
+        ldsm_x4(kb + kv_off<true>(key, 2 * s + (mtx >> 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[mt][nt], a, qf[s][nt][0], qf[s][nt][1]);
+      }
+    }
+    if (mt_.valid != 0xffffffffu || mt_.base + SP_TK > Lmin) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const int j = 16 * mt + 8 * e2 + g;
+          const bool ok = (mt_.valid >> j) & 1u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!ok || mt_.base + j >= lim[nt][e]) sc[mt][nt][2 * e2 + e] = -INFINITY;
+        }
+    }
+    // ---- does a score pass its row's reference by more than 2^8?
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float t4 = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
+        grow |= t4 > m[nt][e] + hold;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t4 = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
+          t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 4));
+          t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 8));
+          t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 16));
+          const float mn = fmaxf(m[nt][e], t4);
+          const float f = m[nt][e] > -INFINITY ? ex2((m[nt][e] - mn) * sl) : 0.f;
+          m[nt][e] = mn;
+          msl[nt][e] = mn > -INFINITY ? mn * sl : 0.f;
+          l[nt][e] *= f;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) { o[d][nt][e] *= f; o[d][nt][2 + e] *= f; }
+        }
+    }
+    uint32_t pf[2][NT][2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const float p0 = ex2(fmaf(sc[mt][nt][2 * e2], sl, -msl[nt][0]));
+          const float p1 = ex2(fmaf(sc[mt][nt][2 * e2 + 1], sl, -msl[nt][1]));
+          l[nt][0] += p0;
+          l[nt][1] += p1;
+          pf[mt][nt][e2] = movm(pack_bf16(p0, p1));
+        }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        uint32_t a[4];
+        const int mtx = lane >> 3, key = 16 * ks + ((mtx >> 1) << 3) + (lane & 7);
+        ldsm_x4_t(vb + kv_off<true>(key, 2 * d + (mtx & 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[d][nt], a, pf[ks][nt][0], pf[ks][nt][1]);
+      }
+    __syncwarp();                           // every lane has read the slot
+    if (more) { issue(slot, page_next); w.next(p.geo); }
+  }
+  // ---- the four warps' partials meet in shared memory
+  __syncthreads();
+  constexpr int OP = WS_DH + 4;             // row pitch
+  float* so = reinterpret_cast<float*>(sm); // [warp][8 NT][OP]
+  float* sml = so + SP_W * 8 * NT * OP;     // [warp][8 NT][2]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float s = l[nt][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      const int row = 8 * nt + 2 * c + e;
+      float* dst = so + (warp * 8 * NT + row) * OP;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) { dst[16 * d + g] = o[d][nt][e]; dst[16 * d + 8 + g] = o[d][nt][2 + e]; }
+      if (g == 0) {
+        sml[(warp * 8 * NT + row) * 2] = dead ? NAN : m[nt][e];
+        sml[(warp * 8 * NT + row) * 2 + 1] = dead ? NAN : s;
+      }
+    }
+  __syncthreads();
+  for (int x = threadIdx.x; x < 8 * NT * 16; x += SP_W * 32) {
+    const int row = x >> 4, d4 = x & 15, rho = r0 + row;
+    if (rho >= R) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < SP_W; ++k) M = fmaxf(M, sml[(k * 8 * NT + row) * 2]);
+    float sum = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+    for (int k = 0; k < SP_W; ++k) {
+      const float mk_ = sml[(k * 8 * NT + row) * 2];
+      const float f = mk_ == -INFINITY ? 0.f : ex2((mk_ - M) * sl);
+      const float4 v = *reinterpret_cast<const float4*>(so + (k * 8 * NT + row) * OP + 4 * d4);
+      sum = fmaf(f, sml[(k * 8 * NT + row) * 2 + 1], sum);
+      a0 = fmaf(f, v.x, a0); a1 = fmaf(f, v.y, a1); a2 = fmaf(f, v.z, a2); a3 = fmaf(f, v.w, a3);
+    }
+    if (p.nsplit > 1) {
+      const size_t at = (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split;
+      *reinterpret_cast<float4*>(p.part_o + at * WS_DH + 4 * d4) = make_float4(a0, a1, a2, a3);
+      if (d4 == 0) p.part_ml[at] = make_float2(M == -INFINITY ? M : M * sl, sum);
+      continue;
+    }
+    const int t = rho / p.G, u = h * p.G + rho - t * p.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    bf16* out = (bf16*)p.a.out + (size_t)(r.row0 + t) * p.a.out_stride + (size_t)u * WS_DH + 4 * d4;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(a0 * inv, a1 * inv), pack_bf16(a2 * inv, a3 * inv));
+    if (p.lse && d4 == 0) p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u] = sum == 0.f ? -INFINITY : (M * sl + lg2(sum)) * LN2;
+  }
+  // a wait that ran out leaves copies in flight: see them land before the memory is given back
+  if (dead)
+    for (int s = 0; s < SP_NS; ++s) { tc::mbar_wait(&full[warp][s], 0); tc::mbar_wait(&full[warp][s], 1); }
+}
+
+// Joins the key splits of a row: one warp per row, splits in order.
+template <typename T>
+__global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
+  const int lane = threadIdx.x & 31, h = blockIdx.y, i = blockIdx.z;
+  const int rho = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const Req r = request(p, i);
+  if (rho >= r.c * p.G) return;
+  const size_t at = (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit;
+  float M = -INFINITY;
+  for (int s = lane; s < p.nsplit; s += 32) M = fmaxf(M, p.part_ml[at + s].x);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+  float sum = 0.f, a0 = 0.f, a1 = 0.f;
+  for (int s = 0; s < p.nsplit; ++s) {
+    const float2 ml = p.part_ml[at + s];
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    const float2 v = *reinterpret_cast<const float2*>(p.part_o + (at + s) * WS_DH + 2 * lane);
+    sum = fmaf(f, ml.y, sum);
+    a0 = fmaf(f, v.x, a0);
+    a1 = fmaf(f, v.y, a1);
+  }
+  const int t = rho / p.G, u = h * p.G + rho - t * p.G;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* out = (T*)p.a.out + (size_t)(r.row0 + t) * p.a.out_stride + (size_t)u * WS_DH + 2 * lane;
+  out[0] = from_f<T>(a0 * inv);
+  out[1] = from_f<T>(a1 * inv);
+  if (p.lse && lane == 0) p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u] = sum == 0.f ? -INFINITY : (M + lg2(sum)) * LN2;
+}
+
+// ------------------------------------------------------------------ bf16: accumulated weights
+// With every row's log-sum-exp known, a second look at the keys: a warp holds
+// 32 keys as matrix operands in registers and walks over all rows, eight at
+// a time, adding 2^(s * sl - lse * log2 e) per key.  A position belongs to
+// one warp, so the sum has a fixed order and needs no atomics.
+__global__ void __launch_bounds__(128) mass_kernel(const AttnP p) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int h = blockIdx.y, i = blockIdx.z;
+  const Req r = request(p, i);
+  const int k0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 32;
+  if (k0 >= r.L || r.c == 0) return;
+  uint32_t ka[2][4][4];
+  uint32_t valid = 0;
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = 16 * mt + 8 * e + g, pos = k0 + j;
+      const int page = pos < r.L ? paged_page(p.c, p.c.page_table, p.c.table_stride, r.slot, pos) : -1;
+      const bf16* k = (const bf16*)p.c.k + (page >= 0 ? paged_off(p.c, page, h, pos) : 0);
+      if (page >= 0) valid |= 1u << (2 * mt + e);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        ka[mt][s][e] = page >= 0 ? __ldg(reinterpret_cast<const unsigned int*>(k + 16 * s + 2 * c)) : 0u;
+        ka[mt][s][2 + e] = page >= 0 ? __ldg(reinterpret_cast<const unsigned int*>(k + 16 * s + 8 + 2 * c)) : 0u;
+      }
+    }
+  const int R = r.c * p.G;
+  float sum[2][2] = {};
+  // rows before the first that sees position k0 add nothing
+  const int first = p.a.causal ? max(0, k0 - (r.L - r.c)) * p.G : 0;
+  for (int r0 = first; r0 < R; r0 += 8) {
+    uint32_t qf[4][1][2];
+    sp_load_q<1>(p, r, h, r0, R, qf);
+    float nl[2];
+    int lim[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rho = r0 + 2 * c + e;
+      const bool on = rho < R;
+      const int t = on ? rho / p.G : 0;
+      const float x = on ? p.lse[(size_t)(r.row0 + t) * p.a.n_heads + h * p.G + rho - t * p.G] : -INFINITY;
+      lim[e] = on && x > -INFINITY ? row_limit(p, r, t) : 0;
+      nl[e] = x * LOG2E;
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) mma_bf16_16816(sc, ka[mt][s], qf[s][0][0], qf[s][0][1]);
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (k0 + 16 * mt + 8 * e2 + g < lim[e]) sum[mt][e2] += ex2(fmaf(sc[2 * e2 + e], p.sl, -nl[e]));
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float s = sum[mt][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      const int pos = k0 + 16 * mt + 8 * e + g;
+      if (c == 0 && ((valid >> (2 * mt + e)) & 1u) && pos < r.L)
+        p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + pos] += s;
+    }
+}
+
+// ------------------------------------------------------------------ host
 const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
   if (const char* e = check_paged_cache(c)) return e;
   if (!a) return "null arguments";
@@ -93,6 +473,8 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
   if (a->total_q < 0 || a->max_q < 0 || a->max_kv < 0) return "negative size";
   if (a->n_heads < 1 || a->n_heads % c->n_kv_heads || a->n_heads > 65535)
     return "n_heads must be a multiple of n_kv_heads, at most 65535";
+  if ((long long)a->max_q * (a->n_heads / c->n_kv_heads) > (1ll << 28) || a->max_kv > (1 << 30))
+    return "max_q times the heads that share a KV head must be at most 2^28, max_kv at most 2^30";
   if (a->causal != 0 && a->causal != 1) return "causal must be 0 or 1";
   if (!isfinite(a->scale)) return "scale must be finite";
   if (a->n_req == 0 || a->total_q == 0) return nullptr;
@@ -108,41 +490,105 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
   return nullptr;
 }
 
-template <typename T>
-cudaError_t run_simple(const AttnP& p, float* lse, cudaStream_t s) {
-  AttnP q = p;
-  q.a.lse = lse;
-  if (p.a.max_q > 0)
-    simple_attn<T><<<dim3((p.a.max_q + 3) / 4, p.a.n_req, p.a.n_heads), 128, 0, s>>>(q);
-  if (p.a.mass && p.a.max_kv > 0)
-    simple_mass<T><<<dim3((p.a.max_kv + 3) / 4, p.a.n_req, p.c.n_kv_heads), 128, 0, s>>>(q, lse);
-  ws_count_launches(2);
+// The launch shape and the workspace of a call: a function of the host sizes.
+struct Plan {
+  int nt = 1;                              // row tile: 8 * nt rows
+  int row_tiles = 1, nsplit = 1, tps = 1;
+  TileGeo geo;
+  size_t lse = 0, ml = 0, o = 0, bytes = 0;
+};
+constexpr int SLOTS = 304;                 // two CTAs on each of 152 SMs
+
+Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
+  Plan q;
+  const long long R = (long long)a.max_q * (a.n_heads / c.n_kv_heads);
+  auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += (n + 255) / 256 * 256; return at; };
+  if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
+  if (c.dtype != WS_BF16) return q;
+  q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+  q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
+  q.geo = tile_geo(c.page_size, SP_TK);
+  const int tiles = max(1, tile_count(q.geo, c.page_size, SP_TK, a.max_kv));
+  const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
+  // enough CTAs for about four rounds of the machine, none shorter than 16 tiles (512 keys)
+  const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, tiles / 16));
+  q.tps = (tiles + want - 1) / want;
+  q.nsplit = (tiles + q.tps - 1) / q.tps;
+  if (q.nsplit > 1) {
+    const size_t rows = (size_t)a.n_req * c.n_kv_heads * R * q.nsplit;
+    q.ml = take(rows * 8);
+    q.o = take(rows * WS_DH * 4);
+  }
+  return q;
+}
+
+template <int NT>
+cudaError_t run_split(const AttnP& p, const Plan& q, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM);
+  if (e != cudaSuccess) return e;
+  split_kernel<NT><<<dim3(q.row_tiles * q.nsplit, p.c.n_kv_heads, p.a.n_req), SP_W * 32, SP_SMEM, s>>>(
+      p, reinterpret_cast<const CUtensorMap&>(mk), reinterpret_cast<const CUtensorMap&>(mv));
+  ws_count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
+  TcMap mk, mv;
+  if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)q.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)q.geo.box))
+    return cudaErrorInvalidValue;
+  cudaError_t e = q.nt == 1 ? run_split<1>(p, q, mk, mv, s) : q.nt == 2 ? run_split<2>(p, q, mk, mv, s)
+                                                                        : run_split<4>(p, q, mk, mv, s);
+  if (e != cudaSuccess) return e;
+  if (q.nsplit > 1) {
+    combine_kernel<bf16><<<dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
+    ws_count_launches(1);
+  }
+  if (p.a.mass && p.a.max_kv > 0) {
+    mass_kernel<<<dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
+    ws_count_launches(1);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t run_f32(const AttnP& p, cudaStream_t s) {
+  simple_attn<float><<<dim3((p.a.max_q + 3) / 4, p.a.n_req, p.a.n_heads), 128, 0, s>>>(p);
+  ws_count_launches(1);
+  if (p.a.mass && p.a.max_kv > 0) {
+    simple_mass<float><<<dim3((p.a.max_kv + 3) / 4, p.a.n_req, p.c.n_kv_heads), 128, 0, s>>>(p);
+    ws_count_launches(1);
+  }
   return cudaGetLastError();
 }
 
 }  // namespace
 
 extern "C" size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attention_args* args) {
-  if (check_attn(cache, args)) return 0;
-  return args->mass && !args->lse ? (size_t)args->total_q * args->n_heads * 4 : 0;
+  if (check_attn(cache, args) || args->n_req == 0 || args->total_q == 0 || args->max_q == 0) return 0;
+  return make_plan(*cache, *args).bytes;
 }
 
 extern "C" int ws_paged_attention(const ws_paged_cache* cache, const ws_attention_args* args, void* workspace,
                                   size_t workspace_bytes, ws_stream stream) {
   if (const char* e = check_attn(cache, args)) return paged_fail(WS_EINVAL, e);
   if (args->n_req == 0 || args->total_q == 0 || args->max_q == 0) return WS_OK;
-  const size_t need = ws_paged_attention_workspace(cache, args);
-  if (need && !workspace) return paged_fail(WS_EINVAL, "null workspace");
-  if (need > workspace_bytes) return paged_fail(WS_ENOSPACE, "workspace smaller than ws_paged_attention_workspace()");
+  const Plan q = make_plan(*cache, *args);
+  if (q.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return paged_fail(WS_EINVAL, "workspace must be 16-byte aligned and not null");
+  if (q.bytes > workspace_bytes) return paged_fail(WS_ENOSPACE, "workspace smaller than ws_paged_attention_workspace()");
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
-  AttnP p;
+  AttnP p = {};
   p.c = *cache;
   p.a = *args;
   p.G = args->n_heads / cache->n_kv_heads;
-  float* lse = args->lse ? args->lse : (float*)workspace;
-  const cudaError_t e = cache->dtype == WS_BF16 ? run_simple<bf16>(p, lse, (cudaStream_t)stream)
-                                                : run_simple<float>(p, lse, (cudaStream_t)stream);
+  p.sl = args->scale == 0.f ? 1.f : fabsf(args->scale) * LOG2E;
+  p.q_and = args->scale == 0.f ? 0u : 0xffffffffu;
+  p.q_xor = args->scale < 0.f ? 0x80008000u : 0u;
+  p.nsplit = q.nsplit; p.tps = q.tps; p.geo = q.geo;
+  char* ws = (char*)workspace;
+  p.lse = args->lse ? args->lse : args->mass ? (float*)(ws + q.lse) : nullptr;
+  if (q.nsplit > 1) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
+  const cudaError_t e = cache->dtype == WS_BF16 ? run_bf16(p, q, (cudaStream_t)stream) : run_f32(p, (cudaStream_t)stream);
   if (e != cudaSuccess) return paged_fail(WS_ECUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
   return WS_OK;
 }

@@ -1,0 +1,77 @@
+// Shared by the kernels of ws_paged_attention.
+#pragma once
+#include "ws_paged.cuh"
+#include "ws_tc.cuh"
+
+// How key tiles of TK positions lie in the pages.  A tile is either one box
+// of at most TK tokens of one page (page_size >= TK, or one that does not
+// divide TK: `tpp` tiles per page) or, with small pages that divide TK,
+// `ppt` whole pages.  Either way a tile's positions are consecutive.
+struct TileGeo {
+  int box;                                 // tokens per copy
+  int tpp;                                 // tiles per page (0: several pages per tile)
+  int ppt_log;                             // log2 pages per tile, page_log: log2 page_size
+  int page_log;
+};
+inline TileGeo tile_geo(int page_size, int tk) {
+  TileGeo g = {};
+  if (page_size < tk && tk % page_size == 0 && page_size >= 8) {
+    g.box = page_size;
+    while ((1 << g.page_log) < page_size) ++g.page_log;
+    while ((page_size << g.ppt_log) < tk) ++g.ppt_log;
+  } else {
+    g.box = page_size < tk ? page_size : tk;
+    g.tpp = (page_size + tk - 1) / tk;
+  }
+  return g;
+}
+// Tiles that hold L positions (an upper bound grows with L).
+__host__ __device__ __forceinline__ int tile_count(const TileGeo& g, int page_size, int tk, int L) {
+  if (g.tpp == 0) return (L + tk - 1) / tk;
+  return L / page_size * g.tpp + (L % page_size + tk - 1) / tk;
+}
+
+struct AttnP {
+  ws_paged_cache c;
+  ws_attention_args a;
+  int G;                                   // query heads per KV head
+  float sl;                                // |scale| * log2(e): scores in log2 units (1 when scale is 0)
+  uint32_t q_and, q_xor;                   // applied to bf16 query pairs: the sign of scale, or all zero
+  int nsplit;                              // key splits per row tile
+  int tps;                                 // key tiles per split
+  TileGeo geo;
+  float2* part_ml;                         // split partials: (max in log2 units, sum) [unit row][nsplit] ...
+  float* part_o;                           // ... and values [unit row][nsplit][64], unit row = (i * Hkv + h) * max_q * G + r * G + g
+  float* lse;                              // [total_q][n_heads], or null
+};
+
+struct Req {
+  int slot, row0, c, L;                    // cache slot, first row, chunk length, visible positions
+};
+__device__ __forceinline__ Req request(const AttnP& p, int i) {
+  Req r;
+  r.slot = p.a.req_ids ? p.a.req_ids[i] : i;
+  r.row0 = p.a.cu_q[i];
+  const int end = min(p.a.cu_q[i + 1], p.a.total_q);
+  r.c = r.row0 >= 0 ? min(max(end - r.row0, 0), p.a.max_q) : 0;
+  r.L = 0;
+  if (r.slot >= 0 && r.slot < p.c.n_slots)
+    r.L = (int)min((long long)min(max(p.a.kv_len[r.slot], 0), p.a.max_kv), (long long)p.c.table_stride * p.c.page_size);
+  return r;
+}
+// Positions 0 .. limit - 1 are visible to row t of the chunk.
+__device__ __forceinline__ int row_limit(const AttnP& p, const Req& r, int t) {
+  return p.a.causal ? max(0, min(r.L, r.L - r.c + t + 1)) : r.L;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float LN2 = 0.69314718055994531f, LOG2E = 1.4426950408889634f;
