@@ -80,12 +80,25 @@ __global__ void simple_mass(const AttnP p) {
 // common tile needs no reduction across lanes.  Statistics and sums are
 // fp32; the weights are rounded to bf16 for the value product alone (2^-8
 // relative at most, the output's own step).
+//
+// With STASH the raw scores stay in tensor memory, which this kernel has no
+// other use for: each of the four warps owns a lane quarter and parks a
+// tile's score fragment in its next 8 NT columns (256 columns per CTA, 512
+// for NT = 4: 4096 / 2048 / 2048 keys).  Once the rows' log-sum-exp is known
+// (the CTA has the whole cache: no splits) each warp reads its fragments
+// back and adds its positions' weights, so the mass costs neither a second
+// read of the keys nor shared memory that the rings need.  Measured at 96
+// requests x 20 heads x 9 rows over 375-1500 positions: a second pass over
+// the keys 176 us, scores in shared memory 126 us.
 constexpr int SP_TK = 32;                  // keys per tile
-constexpr int SP_NS = 3;                   // ring slots per warp
 constexpr int SP_W = 4;                    // warps
+constexpr int SP_NS = 3;                   // ring slots per warp
 constexpr int SP_KB = SP_TK * WS_DH * 2;   // bytes of a K or V tile
-constexpr int SP_RING = SP_W * SP_NS * 2 * SP_KB;
-constexpr int SP_SMEM = SP_RING + 1024;
+constexpr int SP_SMEM = SP_W * SP_NS * 2 * SP_KB + 1024;
+constexpr int SP_OP = WS_DH + 4;           // row pitch of the CTA's merge area, which reuses the rings
+static_assert(SP_W * 32 * (SP_OP + 2) * 4 <= SP_W * SP_NS * 2 * SP_KB, "the merge area fits the rings");
+constexpr int sp_cols(int nt) { return nt == 4 ? 512 : 256; }                  // tensor memory columns
+constexpr int sp_stash_tiles(int nt) { return sp_cols(nt) / (8 * nt); }        // tiles per warp
 constexpr float SP_HOLD = 8.0f;
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int t, int h, int p) {
@@ -140,12 +153,39 @@ __device__ __forceinline__ void sp_load_q(const AttnP& p, const Req& r, int h, i
   }
 }
 
-template <int NT>
+// N consecutive tensor memory columns of the warp's lane quarter.
+template <int N>
+__device__ __forceinline__ void tm_st(uint32_t addr, const float* v) {
+#pragma unroll
+  for (int q = 0; q < N; q += 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr + q),
+                 "r"(__float_as_uint(v[q])), "r"(__float_as_uint(v[q + 1])), "r"(__float_as_uint(v[q + 2])),
+                 "r"(__float_as_uint(v[q + 3])), "r"(__float_as_uint(v[q + 4])), "r"(__float_as_uint(v[q + 5])),
+                 "r"(__float_as_uint(v[q + 6])), "r"(__float_as_uint(v[q + 7])) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_ld(uint32_t addr, float* v) {
+#pragma unroll
+  for (int q = 0; q < N; q += 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr + q));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[q + e] = __uint_as_float(r[e]);
+  }
+}
+
+template <int NT, bool STASH>
 __global__ void __launch_bounds__(SP_W * 32, NT == 4 ? 1 : 2)
 split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  constexpr int MT = SP_TK / 16;           // key steps of 16
+  constexpr uint32_t ALL = 0xffffffffu;
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t full[SP_W][SP_NS];
   __shared__ SpMeta meta[SP_W][SP_NS];
+  __shared__ float row_lse[8 * NT];
+  __shared__ uint32_t s_tmem;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rt = blockIdx.x / p.nsplit, split = blockIdx.x - rt * p.nsplit, h = blockIdx.y, i = blockIdx.z;
@@ -156,6 +196,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
     for (int s = 0; s < SP_NS; ++s) tc::mbar_init(&full[warp][s], 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
+  if (STASH && warp == 0) tc::tmem_alloc(&s_tmem, sp_cols(NT));
   // positions that some row of this tile sees, and those that all see
   const int last = min(R, r0 + 8 * NT) - 1;
   const int Lmax = row_limit(p, r, last / p.G), Lmin = row_limit(p, r, r0 / p.G);
@@ -211,6 +252,13 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
   }
   const float sl = p.sl, hold = fminf(SP_HOLD / sl, 1e30f);
+  uint32_t tmem = 0;                        // this warp's columns
+  if (STASH) {
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    tmem = s_tmem + ((uint32_t)warp << 21);
+  }
   bool dead = false;
   for (int it = 0; it < n_my; ++it) {
     const int slot = it % SP_NS;
@@ -220,7 +268,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
     const SpMeta mt_ = meta[warp][slot];
     uint8_t* Kt = ring + slot * (2 * SP_KB);
     uint8_t* Vt = Kt + SP_KB;
-    if (mt_.valid != 0xffffffffu) {
+    if (mt_.valid != ALL) {
       // rows that do not count may hold anything: 0 * inf would reach the sums
       if (!((mt_.valid >> lane) & 1u)) {
 #pragma unroll
@@ -230,9 +278,9 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       __syncwarp();
     }
     const uint32_t kb = tc::smem_u32(Kt), vb = tc::smem_u32(Vt);
-    float sc[2][NT][4];
+    float sc[MT][NT][4];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.f;
 #pragma unroll
@@ -244,9 +292,9 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
         for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[mt][nt], a, qf[s][nt][0], qf[s][nt][1]);
       }
     }
-    if (mt_.valid != 0xffffffffu || mt_.base + SP_TK > Lmin) {
+    if (mt_.valid != ALL || mt_.base + SP_TK > Lmin) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
           const int j = 16 * mt + 8 * e2 + g;
@@ -258,6 +306,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
               if (!ok || mt_.base + j >= lim[nt][e]) sc[mt][nt][2 * e2 + e] = -INFINITY;
         }
     }
+    if (STASH) tm_st<8 * NT>(tmem + (uint32_t)(it * 8 * NT), &sc[0][0][0]);
     // ---- does a score pass its row's reference by more than 2^8?
     bool grow = false;
 #pragma unroll
@@ -285,9 +334,9 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
           for (int d = 0; d < 4; ++d) { o[d][nt][e] *= f; o[d][nt][2 + e] *= f; }
         }
     }
-    uint32_t pf[2][NT][2];
+    uint32_t pf[MT][NT][2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -299,7 +348,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
           pf[mt][nt][e2] = movm(pack_bf16(p0, p1));
         }
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (int ks = 0; ks < MT; ++ks)
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         uint32_t a[4];
@@ -313,7 +362,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
   }
   // ---- the four warps' partials meet in shared memory
   __syncthreads();
-  constexpr int OP = WS_DH + 4;             // row pitch
+  constexpr int OP = SP_OP;
   float* so = reinterpret_cast<float*>(sm); // [warp][8 NT][OP]
   float* sml = so + SP_W * 8 * NT * OP;     // [warp][8 NT][2]
 #pragma unroll
@@ -357,9 +406,60 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
     }
     const int t = rho / p.G, u = h * p.G + rho - t * p.G;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (STASH && d4 == 0) row_lse[row] = sum == 0.f ? INFINITY : M * sl + lg2(sum);
     bf16* out = (bf16*)p.a.out + (size_t)(r.row0 + t) * p.a.out_stride + (size_t)u * WS_DH + 4 * d4;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(a0 * inv, a1 * inv), pack_bf16(a2 * inv, a3 * inv));
     if (p.lse && d4 == 0) p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u] = sum == 0.f ? -INFINITY : (M * sl + lg2(sum)) * LN2;
+  }
+  if (STASH) {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    __syncthreads();
+    float nl[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) nl[nt][e] = r0 + 8 * nt + 2 * c + e < R ? row_lse[8 * nt + 2 * c + e] : INFINITY;
+    float* mass = p.a.mass + ((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride;
+    // a quad ends up with the sums of four keys per step of 32; its lane c
+    // adds key 8 c + g
+    constexpr int U = 4;
+    w.start(p.geo, tb + warp, SP_W);
+    for (int it = 0; it < n_my; it += U) {
+      int pos[U];
+      float old[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int j = 8 * c + g, b = w.base(p.geo, p.c.page_size, SP_TK);
+        pos[k] = it + k < n_my && j < w.room(p.geo, p.c.page_size, SP_TK) && b + j < Lmax ? b + j : -1;
+        old[k] = pos[k] >= 0 ? mass[pos[k]] : 0.f;
+        w.next(p.geo);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (it + k >= n_my) break;
+        float sv[MT][NT][4];
+        tm_ld<8 * NT>(tmem + (uint32_t)((it + k) * 8 * NT), &sv[0][0][0]);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        float part[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {       // keys 8 q + g
+          float s = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s += ex2(fmaf(sv[q >> 1][nt][2 * (q & 1) + e], sl, -nl[nt][e]));
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          part[q] = s;
+        }
+        const float add = c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : part[3];
+        if (pos[k] >= 0) mass[pos[k]] = old[k] + add;
+      }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == 0) tc::tmem_dealloc(s_tmem, sp_cols(NT));
   }
   // a wait that ran out leaves copies in flight: see them land before the memory is given back
   if (dead)
@@ -399,27 +499,34 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
 // With every row's log-sum-exp known, a second look at the keys: a warp holds
 // 32 keys as matrix operands in registers and walks over all rows, eight at
 // a time, adding 2^(s * sl - lse * log2 e) per key.  A position belongs to
-// one warp, so the sum has a fixed order and needs no atomics.
+// one warp, so the sum has a fixed order and needs no atomics.  A dot
+// product does not care which dim stands at which k of the instruction, so
+// lane c of a quad takes dims 16 c .. 16 c + 15 of its key and of its query
+// row: two 16-byte loads each, whole lines per warp.
+__device__ __forceinline__ void mass_load(const bf16* row, int c, uint32_t f[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + 16 * c)), b = __ldg(reinterpret_cast<const uint4*>(row + 16 * c) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
 __global__ void __launch_bounds__(128) mass_kernel(const AttnP p) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int h = blockIdx.y, i = blockIdx.z;
   const Req r = request(p, i);
   const int k0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 32;
   if (k0 >= r.L || r.c == 0) return;
-  uint32_t ka[2][4][4];
+  uint32_t ka[2][2][8];                    // [16-key step][key g or g + 8][2 * step of 16 dims + half]
   uint32_t valid = 0;
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int j = 16 * mt + 8 * e + g, pos = k0 + j;
+      const int pos = k0 + 16 * mt + 8 * e + g;
       const int page = pos < r.L ? paged_page(p.c, p.c.page_table, p.c.table_stride, r.slot, pos) : -1;
-      const bf16* k = (const bf16*)p.c.k + (page >= 0 ? paged_off(p.c, page, h, pos) : 0);
-      if (page >= 0) valid |= 1u << (2 * mt + e);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        ka[mt][s][e] = page >= 0 ? __ldg(reinterpret_cast<const unsigned int*>(k + 16 * s + 2 * c)) : 0u;
-        ka[mt][s][2 + e] = page >= 0 ? __ldg(reinterpret_cast<const unsigned int*>(k + 16 * s + 8 + 2 * c)) : 0u;
+      for (int q = 0; q < 8; ++q) ka[mt][e][q] = 0u;
+      if (page >= 0) {
+        valid |= 1u << (2 * mt + e);
+        mass_load((const bf16*)p.c.k + paged_off(p.c, page, h, pos), c, ka[mt][e]);
       }
     }
   const int R = r.c * p.G;
@@ -427,8 +534,15 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnP p) {
   // rows before the first that sees position k0 add nothing
   const int first = p.a.causal ? max(0, k0 - (r.L - r.c)) * p.G : 0;
   for (int r0 = first; r0 < R; r0 += 8) {
-    uint32_t qf[4][1][2];
-    sp_load_q<1>(p, r, h, r0, R, qf);
+    uint32_t qf[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) qf[q] = 0u;
+    if (r0 + g < R) {
+      const int t = (r0 + g) / p.G;
+      mass_load((const bf16*)p.a.q + (size_t)(r.row0 + t) * p.a.q_stride + (size_t)(h * p.G + r0 + g - t * p.G) * WS_DH, c, qf);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) qf[q] = (qf[q] & p.q_and) ^ p.q_xor;
+    }
     float nl[2];
     int lim[2];
 #pragma unroll
@@ -437,14 +551,17 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnP p) {
       const bool on = rho < R;
       const int t = on ? rho / p.G : 0;
       const float x = on ? p.lse[(size_t)(r.row0 + t) * p.a.n_heads + h * p.G + rho - t * p.G] : -INFINITY;
-      lim[e] = on && x > -INFINITY ? row_limit(p, r, t) : 0;
+      lim[e] = on && x != -INFINITY ? row_limit(p, r, t) : 0;
       nl[e] = x * LOG2E;
     }
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       float sc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < 4; ++s) mma_bf16_16816(sc, ka[mt][s], qf[s][0][0], qf[s][0][1]);
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t a[4] = {ka[mt][0][2 * s], ka[mt][1][2 * s], ka[mt][0][2 * s + 1], ka[mt][1][2 * s + 1]};
+        mma_bf16_16816(sc, a, qf[2 * s], qf[2 * s + 1]);
+      }
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2)
 #pragma unroll
@@ -459,9 +576,8 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnP p) {
       float s = sum[mt][e];
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      const int pos = k0 + 16 * mt + 8 * e + g;
-      if (c == 0 && ((valid >> (2 * mt + e)) & 1u) && pos < r.L)
-        p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + pos] += s;
+      if (c == 0 && ((valid >> (2 * mt + e)) & 1u))
+        p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + k0 + 16 * mt + 8 * e + g] += s;
     }
 }
 
@@ -494,6 +610,7 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
 struct Plan {
   int nt = 1;                              // row tile: 8 * nt rows
   int row_tiles = 1, nsplit = 1, tps = 1;
+  bool stash = false;                      // the streaming kernel adds the mass itself
   TileGeo geo;
   size_t lse = 0, ml = 0, o = 0, bytes = 0;
 };
@@ -507,13 +624,14 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   if (c.dtype != WS_BF16) return q;
   q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
   q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
+  const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
+  // enough CTAs for about four rounds of the machine, none shorter than 512 keys
+  const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
   q.geo = tile_geo(c.page_size, SP_TK);
   const int tiles = max(1, tile_count(q.geo, c.page_size, SP_TK, a.max_kv));
-  const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
-  // enough CTAs for about four rounds of the machine, none shorter than 16 tiles (512 keys)
-  const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, tiles / 16));
   q.tps = (tiles + want - 1) / want;
   q.nsplit = (tiles + q.tps - 1) / q.tps;
+  q.stash = a.mass && q.nsplit == 1 && q.row_tiles == 1 && tiles <= SP_W * sp_stash_tiles(q.nt);
   if (q.nsplit > 1) {
     const size_t rows = (size_t)a.n_req * c.n_kv_heads * R * q.nsplit;
     q.ml = take(rows * 8);
@@ -522,11 +640,11 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   return q;
 }
 
-template <int NT>
+template <int NT, bool STASH>
 cudaError_t run_split(const AttnP& p, const Plan& q, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM);
+  cudaError_t e = cudaFuncSetAttribute(split_kernel<NT, STASH>, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM);
   if (e != cudaSuccess) return e;
-  split_kernel<NT><<<dim3(q.row_tiles * q.nsplit, p.c.n_kv_heads, p.a.n_req), SP_W * 32, SP_SMEM, s>>>(
+  split_kernel<NT, STASH><<<dim3(q.row_tiles * q.nsplit, p.c.n_kv_heads, p.a.n_req), SP_W * 32, SP_SMEM, s>>>(
       p, reinterpret_cast<const CUtensorMap&>(mk), reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
   return cudaGetLastError();
@@ -536,14 +654,16 @@ cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
   TcMap mk, mv;
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)q.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)q.geo.box))
     return cudaErrorInvalidValue;
-  cudaError_t e = q.nt == 1 ? run_split<1>(p, q, mk, mv, s) : q.nt == 2 ? run_split<2>(p, q, mk, mv, s)
-                                                                        : run_split<4>(p, q, mk, mv, s);
+  cudaError_t e;
+  if (q.nt == 1) e = q.stash ? run_split<1, true>(p, q, mk, mv, s) : run_split<1, false>(p, q, mk, mv, s);
+  else if (q.nt == 2) e = q.stash ? run_split<2, true>(p, q, mk, mv, s) : run_split<2, false>(p, q, mk, mv, s);
+  else e = q.stash ? run_split<4, true>(p, q, mk, mv, s) : run_split<4, false>(p, q, mk, mv, s);
   if (e != cudaSuccess) return e;
   if (q.nsplit > 1) {
     combine_kernel<bf16><<<dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
     ws_count_launches(1);
   }
-  if (p.a.mass && p.a.max_kv > 0) {
+  if (p.a.mass && p.a.max_kv > 0 && !q.stash) {
     mass_kernel<<<dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
     ws_count_launches(1);
   }
