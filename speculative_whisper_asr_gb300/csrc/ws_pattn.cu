@@ -189,6 +189,19 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rt = blockIdx.x / p.nsplit, split = blockIdx.x - rt * p.nsplit, h = blockIdx.y, i = blockIdx.z;
+  // the first tiles' pages are asked for together with the lengths: the
+  // entries exist whatever the lengths turn out to be
+  const int slot0 = p.a.req_ids ? p.a.req_ids[i] : i;
+  const int32_t* table = p.c.page_table + (size_t)min(max(slot0, 0), p.c.n_slots - 1) * p.c.table_stride;
+  TileWalk w;
+  auto page_of = [&]() -> int {             // table entry of this lane's key in the walk's tile, -1: none
+    const int e = w.entry(p.geo, lane);
+    return e < p.c.table_stride ? __ldg(table + e) : -1;
+  };
+  w.start(p.geo, split * p.tps + warp, SP_W);
+  int page0[SP_NS];
+#pragma unroll
+  for (int s = 0; s < SP_NS; ++s) { page0[s] = page_of(); w.next(p.geo); }
   const Req r = request(p, i);
   const int R = r.c * p.G, r0 = rt * 8 * NT;
   if (r0 >= R) return;
@@ -203,25 +216,16 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
   const int nt_all = tile_count(p.geo, p.c.page_size, SP_TK, Lmax);
   const int tb = min(nt_all, split * p.tps), te = min(nt_all, tb + p.tps);
   const int n_my = max(0, (te - tb - warp + SP_W - 1) / SP_W);
-  const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
   uint8_t* ring = sm + warp * (SP_NS * 2 * SP_KB);
-
-  TileWalk w;
-  w.start(p.geo, tb + warp, SP_W);
-  auto page_of = [&]() -> int {             // this lane's key's page in the walk's tile, -1: none
-    const int j = lane, e = w.entry(p.geo, j);
-    const int pos = w.base(p.geo, p.c.page_size, SP_TK) + j;
-    if (j >= w.room(p.geo, p.c.page_size, SP_TK) || pos >= Lmax || e >= p.c.table_stride) return -1;
-    return __ldg(table + e);
-  };
   auto issue = [&](int slot, int page) {
-    const bool ok = page >= 0 && page < p.c.n_pages;
+    const int base = w.base(p.geo, p.c.page_size, SP_TK);
+    const bool ok = page >= 0 && page < p.c.n_pages && lane < w.room(p.geo, p.c.page_size, SP_TK) && base + lane < Lmax;
     const uint32_t valid = __ballot_sync(0xffffffffu, ok);
     const bool go = ok && (p.geo.tpp ? (valid & ((1u << lane) - 1u)) == 0u : (lane & (p.geo.box - 1)) == 0);
     const unsigned boxes = __ballot_sync(0xffffffffu, go);
     if (lane == 0) {
       meta[warp][slot].valid = valid;
-      meta[warp][slot].base = w.base(p.geo, p.c.page_size, SP_TK);
+      meta[warp][slot].base = base;
       tc::mbar_expect_tx(&full[warp][slot], (uint32_t)__popc(boxes) * 2u * (uint32_t)p.geo.box * 128u);
     }
     __syncwarp();
@@ -232,7 +236,10 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       tma_load_4d(dst + SP_KB, &mv, &full[warp][slot], 0, tok, h, page);
     }
   };
-  for (int s = 0; s < SP_NS && s < n_my; ++s) { issue(s, page_of()); w.next(p.geo); }
+  w.start(p.geo, split * p.tps + warp, SP_W);
+#pragma unroll
+  for (int s = 0; s < SP_NS; ++s)
+    if (s < n_my) { issue(s, page0[s]); w.next(p.geo); }
 
   uint32_t qf[4][NT][2];
   sp_load_q<NT>(p, r, h, r0, R, qf);
@@ -421,40 +428,29 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       for (int e = 0; e < 2; ++e) nl[nt][e] = r0 + 8 * nt + 2 * c + e < R ? row_lse[8 * nt + 2 * c + e] : INFINITY;
     float* mass = p.a.mass + ((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride;
     // a quad ends up with the sums of four keys per step of 32; its lane c
-    // adds key 8 c + g
-    constexpr int U = 4;
+    // adds key 8 c + g.  The position is this thread's alone, so the atomic
+    // (which does not wait for the old value) has nothing to race with.
     w.start(p.geo, tb + warp, SP_W);
-    for (int it = 0; it < n_my; it += U) {
-      int pos[U];
-      float old[U];
+    for (int it = 0; it < n_my; ++it) {
+      float sv[MT][NT][4];
+      tm_ld<8 * NT>(tmem + (uint32_t)(it * 8 * NT), &sv[0][0][0]);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      float part[4];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int j = 8 * c + g, b = w.base(p.geo, p.c.page_size, SP_TK);
-        pos[k] = it + k < n_my && j < w.room(p.geo, p.c.page_size, SP_TK) && b + j < Lmax ? b + j : -1;
-        old[k] = pos[k] >= 0 ? mass[pos[k]] : 0.f;
-        w.next(p.geo);
+      for (int q = 0; q < 4; ++q) {         // keys 8 q + g
+        float s = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s += ex2(fmaf(sv[q >> 1][nt][2 * (q & 1) + e], sl, -nl[nt][e]));
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        part[q] = s;
       }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (it + k >= n_my) break;
-        float sv[MT][NT][4];
-        tm_ld<8 * NT>(tmem + (uint32_t)((it + k) * 8 * NT), &sv[0][0][0]);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        float part[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {       // keys 8 q + g
-          float s = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s += ex2(fmaf(sv[q >> 1][nt][2 * (q & 1) + e], sl, -nl[nt][e]));
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
-          part[q] = s;
-        }
-        const float add = c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : part[3];
-        if (pos[k] >= 0) mass[pos[k]] = old[k] + add;
-      }
+      const int j = 8 * c + g, pos = w.base(p.geo, p.c.page_size, SP_TK) + j;
+      if (j < w.room(p.geo, p.c.page_size, SP_TK) && pos < Lmax)
+        atomicAdd(mass + pos, c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : part[3]);
+      w.next(p.geo);
     }
     tc::tc_fence_before();
     __syncthreads();
