@@ -738,6 +738,23 @@ bool tc_encode_paged(TcMap* m, const void* base, const ws_paged_cache& c, uint32
   return r == CUDA_SUCCESS;
 }
 
+// Rows of heads x 64 bf16 as a 3-D map {64 dims, heads, rows} with boxes of
+// box_rows rows x box_heads heads, 128-byte swizzle: a box is a tile of
+// box_rows * box_heads rows of 64.  Rows behind the last read as 0.
+bool tc_encode_heads(TcMap* m, const void* base, int64_t stride, uint64_t rows, uint32_t heads, uint32_t box_heads,
+                     uint32_t box_rows) {
+  if (!tc_engine_available()) return false;
+  cuuint64_t dims[3] = {WS_DH, heads, rows};
+  cuuint64_t strides[2] = {WS_DH * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {WS_DH, box_heads, box_rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = g_encode(reinterpret_cast<CUtensorMap*>(m), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Row-major fp32 matrix [rows, cols] (cols a multiple of 256) as a 3-D TMA
 // map {256, cols / 256, rows} whose box holds box_rows whole rows, stored
 // row after row in shared memory (no swizzle).  Rows beyond `rows` read as 0.

@@ -101,12 +101,6 @@ constexpr int sp_cols(int nt) { return nt == 4 ? 512 : 256; }                  /
 constexpr int sp_stash_tiles(int nt) { return sp_cols(nt) / (8 * nt); }        // tiles per warp
 constexpr float SP_HOLD = 8.0f;
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int t, int h, int p) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(tc::smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(t), "r"(h), "r"(p), "r"(tc::smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -604,20 +598,41 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
 
 // The launch shape and the workspace of a call: a function of the host sizes.
 struct Plan {
-  int nt = 1;                              // row tile: 8 * nt rows
+  bool fa = false;                         // tcgen05 row tiles instead of streaming ones
+  int nt = 1;                              // streaming row tile: 8 * nt rows
   int row_tiles = 1, nsplit = 1, tps = 1;
   bool stash = false;                      // the streaming kernel adds the mass itself
   TileGeo geo;
   size_t lse = 0, ml = 0, o = 0, bytes = 0;
 };
-constexpr int SLOTS = 304;                 // two CTAs on each of 152 SMs
+constexpr int SMS = 152, SLOTS = 2 * SMS;  // two streaming CTAs on each of 152 SMs
 
 Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   Plan q;
   const long long R = (long long)a.max_q * (a.n_heads / c.n_kv_heads);
   auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += (n + 255) / 256 * 256; return at; };
   if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
+  auto partials = [&](long long R_) {
+    if (q.nsplit <= 1) return;
+    const size_t rows = (size_t)a.n_req * c.n_kv_heads * R_ * q.nsplit;
+    q.ml = take(rows * 8);
+    q.o = take(rows * WS_DH * 4);
+  };
   if (c.dtype != WS_BF16) return q;
+  const int G = a.n_heads / c.n_kv_heads;
+  if (R > 32 && G <= FA_ROWS && a.scale > 0.f) {
+    q.fa = true;
+    q.row_tiles = (a.max_q + FA_ROWS / G - 1) / (FA_ROWS / G);
+    q.geo = tile_geo(c.page_size, FA_KEYS);
+    const int tiles = max(1, tile_count(q.geo, c.page_size, FA_KEYS, a.max_kv));
+    const long long units = (long long)a.n_req * c.n_kv_heads * ((q.row_tiles + 1) / 2);
+    // about two CTAs per SM, none shorter than four key tiles
+    const int want = (int)min((2ll * SMS + units - 1) / units, (long long)max(1, tiles / 4));
+    q.tps = (tiles + want - 1) / want;
+    q.nsplit = (tiles + q.tps - 1) / q.tps;
+    partials(R);
+    return q;
+  }
   q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
   q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
   const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
@@ -628,11 +643,7 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   q.tps = (tiles + want - 1) / want;
   q.nsplit = (tiles + q.tps - 1) / q.tps;
   q.stash = a.mass && q.nsplit == 1 && q.row_tiles == 1 && tiles <= SP_W * sp_stash_tiles(q.nt);
-  if (q.nsplit > 1) {
-    const size_t rows = (size_t)a.n_req * c.n_kv_heads * R * q.nsplit;
-    q.ml = take(rows * 8);
-    q.o = take(rows * WS_DH * 4);
-  }
+  partials(R);
   return q;
 }
 
@@ -646,23 +657,26 @@ cudaError_t run_split(const AttnP& p, const Plan& q, const TcMap& mk, const TcMa
   return cudaGetLastError();
 }
 
-cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
+cudaError_t run_streaming(const AttnP& p, const Plan& q, cudaStream_t s) {
   TcMap mk, mv;
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)q.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)q.geo.box))
     return cudaErrorInvalidValue;
-  cudaError_t e;
-  if (q.nt == 1) e = q.stash ? run_split<1, true>(p, q, mk, mv, s) : run_split<1, false>(p, q, mk, mv, s);
-  else if (q.nt == 2) e = q.stash ? run_split<2, true>(p, q, mk, mv, s) : run_split<2, false>(p, q, mk, mv, s);
-  else e = q.stash ? run_split<4, true>(p, q, mk, mv, s) : run_split<4, false>(p, q, mk, mv, s);
+  if (q.nt == 1) return q.stash ? run_split<1, true>(p, q, mk, mv, s) : run_split<1, false>(p, q, mk, mv, s);
+  if (q.nt == 2) return q.stash ? run_split<2, true>(p, q, mk, mv, s) : run_split<2, false>(p, q, mk, mv, s);
+  return q.stash ? run_split<4, true>(p, q, mk, mv, s) : run_split<4, false>(p, q, mk, mv, s);
+}
+
+cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
+  const cudaError_t e = q.fa ? launch_fa(p, q.row_tiles, s) : run_streaming(p, q, s);
   if (e != cudaSuccess) return e;
   if (q.nsplit > 1) {
     combine_kernel<bf16><<<dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
     ws_count_launches(1);
   }
-  if (p.a.mass && p.a.max_kv > 0 && !q.stash) {
-    mass_kernel<<<dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
-    ws_count_launches(1);
-  }
+  if (!p.a.mass || p.a.max_kv == 0 || q.stash) return cudaGetLastError();
+  if (q.fa) return launch_fa_mass(p, q.row_tiles, s);
+  mass_kernel<<<dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
+  ws_count_launches(1);
   return cudaGetLastError();
 }
 

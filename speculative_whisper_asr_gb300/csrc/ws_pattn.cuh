@@ -75,3 +75,18 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 constexpr float LN2 = 0.69314718055994531f, LOG2E = 1.4426950408889634f;
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int t, int h, int p) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(tc::smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(t), "r"(h), "r"(p), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// Long chunks on tcgen05 (ws_pattn_fa.cu): tiles of fa_rows(G) rows (whole
+// chunk rows) against tiles of FA_KEYS keys.  Rows of unsplit calls go to
+// out / lse, those of split calls to the partials.
+constexpr int FA_ROWS = 128, FA_KEYS = 128;
+inline int fa_rows(int G) { return G * (FA_ROWS / G); }                        // G <= 128
+cudaError_t launch_fa(const AttnP& p, int row_tiles, cudaStream_t s);
+cudaError_t launch_fa_mass(const AttnP& p, int row_tiles, cudaStream_t s);

@@ -1,0 +1,674 @@
+// ws_paged_attention for long chunks of the bf16 model, on tcgen05.
+//
+// fa_kernel.  One CTA per (request, KV head, two row tiles of up to 128 rows)
+// and key range; rows are chunk rows x the query heads that share the KV
+// head, so a box of the query map is a row tile.  The two row tiles A and B
+// share every key tile of 128 keys:
+//   warp 0      producer: Q once, then K and V tiles (page by page) through
+//               four stages; zeroes value rows that do not count
+//   warp 1      MMA issuer: S = Q K^T (128 x 128, both from shared memory),
+//               O += P V with P from tensor memory and V as it lies in the
+//               pages (the "N-major" operand form: no transpose)
+//   warps 2..5  softmax of A, warps 6..9 of B: one thread per row
+// Tensor memory (512 columns): S, P and O of each tile have columns of their
+// own, so the next S is computed as soon as the softmax has S in registers.
+// The row's reference maximum moves only when a score passes it by more than
+// 2^8; then O is rescaled in tensor memory.  With head width 64 a score costs
+// 256 FLOP and one exponential, so the exponentials bound the kernel as much
+// as the tensor core does; scaling and sums are packed pairs (f32x2).
+//
+// fa_mass_kernel.  The weights summed per key, once every row's log-sum-exp
+// is known: S^T = K Q^T puts a key into each thread, which adds
+// 2^(s * sl - lse * log2 e) over the rows of a tile in order; no reduction
+// across threads, no atomics.
+#include "ws_pattn.cuh"
+
+namespace {
+
+constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
+constexpr int NST = 4;                             // key stages
+constexpr int THREADS = 320;
+constexpr int FA_SMEM = 2 * TILE + NST * 2 * TILE + 1024;
+constexpr uint32_t TM_S = 0, TM_P = 256, TM_O = 384;   // + 128 w, + 64 w, + 64 w
+constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
+constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, 64) | (1u << 16);   // B (V) is N-major
+constexpr float HOLD = 8.0f;
+
+struct Meta { uint32_t valid[4]; int base; int full; };
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(tc::smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+// Bounded wait that also gives up once another role has.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > tc::WAIT_BUDGET) { *abort = 1; return false; }
+  }
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, abort);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Operand whose rows of 128 bytes (128-byte swizzle) run along K: 64 N
+// elements per row, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_nmajor(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(1024 >> 4) << 16;                // between groups of 64 N elements (there is one)
+  d |= (uint64_t)(1024 >> 4) << 32;                // between groups of 8 K rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+template <int N>
+__device__ __forceinline__ void tm_ld(uint32_t taddr, float* v) {
+#pragma unroll
+  for (int q = 0; q < N; q += 16) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr + q));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[q + e] = __uint_as_float(r[e]);
+  }
+}
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// A warp's look-up of one key tile: where its pages are and which keys count.
+struct TileInfo {
+  int page;                                        // this lane's page to copy, or -1
+  int tok, base, dst;                              // first token in it, the tile's first position, byte offset of the copy
+  uint32_t valid[4];
+};
+__device__ __forceinline__ int tile_entry(const AttnP& p, int t, int lane) {
+  return p.geo.tpp ? t / p.geo.tpp : (t << p.geo.ppt_log) + lane;
+}
+__device__ __forceinline__ int tile_page(const AttnP& p, const int32_t* table, int t, int lane) {
+  const int e = tile_entry(p, t, lane);
+  return (p.geo.tpp || lane < (1 << p.geo.ppt_log)) && e < p.c.table_stride ? __ldg(table + e) : -1;
+}
+__device__ __forceinline__ TileInfo tile_info(const AttnP& p, int t, int page, int limit, int lane) {
+  TileInfo f;
+  const bool ok = page >= 0 && page < p.c.n_pages;
+  if (p.geo.tpp) {
+    const int pi = t / p.geo.tpp, sub = t - pi * p.geo.tpp, room = min(FA_KEYS, p.c.page_size - sub * FA_KEYS);
+    f.tok = sub * FA_KEYS;
+    f.base = pi * p.c.page_size + f.tok;
+    f.dst = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      f.valid[q] = __ballot_sync(0xffffffffu, ok && 32 * q + lane < room && f.base + 32 * q + lane < limit);
+    f.page = lane == 0 && ok && f.base < limit ? page : -1;
+  } else {
+    const int ps = 1 << p.geo.page_log;
+    f.tok = 0;
+    f.base = t * FA_KEYS;
+    f.dst = lane * ps * 128;
+    const uint32_t okm = __ballot_sync(0xffffffffu, ok && f.base + lane * ps < limit);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int j = 32 * q + lane;
+      f.valid[q] = __ballot_sync(0xffffffffu, ((okm >> (j >> p.geo.page_log)) & 1u) && f.base + j < limit);
+    }
+    f.page = (okm >> lane) & 1u ? page : -1;
+  }
+  return f;
+}
+
+struct Bars {
+  uint64_t q_full[2], k_full[NST], v_full[NST], v_fix[NST], empty[NST], s_full[2], s_free[2], p_full[2], pv_done[2];
+};
+
+__global__ void __launch_bounds__(THREADS, 1)
+fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+          const __grid_constant__ CUtensorMap mv) {
+  extern __shared__ uint8_t dsm[];
+  __shared__ __align__(8) Bars B;
+  __shared__ Meta meta[NST];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  const int pairs = (row_tiles + 1) / 2;
+  const int pair = pairs - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
+  const int h = blockIdx.y, i = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Req r = request(p, i);
+  const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
+  const int rho0 = pair * 2 * TR;
+  if (rho0 >= R) return;
+  // key tiles of each row tile within this split
+  int n[2], lo;
+  {
+    const int ps = p.c.page_size;
+    lo = split * p.tps;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int first = rho0 + w * TR, last = min(R, first + TR) - 1;
+      const int nt = last >= first ? tile_count(p.geo, ps, FA_KEYS, row_limit(p, r, last / p.G)) : 0;
+      n[w] = max(0, min(nt, lo + p.tps) - lo);
+    }
+  }
+  const int nmax = max(n[0], n[1]);
+  volatile int* abort = &s_abort;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < NST; ++b) {
+      tc::mbar_init(&B.k_full[b], 1); tc::mbar_init(&B.v_full[b], 1); tc::mbar_init(&B.v_fix[b], 1);
+      tc::mbar_init(&B.empty[b], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&B.q_full[w], 1); tc::mbar_init(&B.s_full[w], 1); tc::mbar_init(&B.s_free[w], 4);
+      tc::mbar_init(&B.p_full[w], 4); tc::mbar_init(&B.pv_done[w], 1);
+    }
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tc::tmem_alloc(&s_tmem, 512);
+  uint8_t* sQ = sm;
+  auto sK = [&](int b) { return sm + 2 * TILE + b * 2 * TILE; };
+  auto sV = [&](int b) { return sm + 3 * TILE + b * 2 * TILE; };
+  if (p.geo.tpp && p.geo.box < FA_KEYS)            // value rows that no copy writes
+    for (int x = threadIdx.x; x < NST * TILE / 16; x += THREADS)
+      reinterpret_cast<uint4*>(sV(x / (TILE / 16)))[x % (TILE / 16)] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    // ---- producer
+    if (lane == 0) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (n[w]) {
+          tc::mbar_expect_tx(&B.q_full[w], (uint32_t)TR * 128u);
+          tma_load_3d(sQ + w * TILE, &mq, &B.q_full[w], 0, h * p.G, r.row0 + pair * 2 * RB + w * RB);
+        }
+    }
+    const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
+    int page = tile_page(p, table, lo, lane), issued = 0;
+    for (int j = 0; j < nmax; ++j) {
+      const int s = j % NST;
+      const TileInfo f = tile_info(p, lo + j, page, r.L, lane);
+      if (j + 1 < nmax) page = tile_page(p, table, lo + j + 1, lane);
+      if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
+      const bool go = f.page >= 0;
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 128u;
+      const bool full = (f.valid[0] & f.valid[1] & f.valid[2] & f.valid[3]) == 0xffffffffu;
+      if (lane == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) meta[s].valid[q] = f.valid[q];
+        meta[s].base = f.base;
+        meta[s].full = full;
+        tc::mbar_expect_tx(&B.k_full[s], bytes);
+        tc::mbar_expect_tx(&B.v_full[s], bytes);
+      }
+      __syncwarp();
+      if (go) {
+        tma_load_4d(sK(s) + f.dst, &mk, &B.k_full[s], 0, f.tok, h, f.page);
+        tma_load_4d(sV(s) + f.dst, &mv, &B.v_full[s], 0, f.tok, h, f.page);
+      }
+      ++issued;
+      if (!full) {
+        // rows behind the cache's length, or of skipped pages, may hold
+        // anything: 0 * inf would reach the sums
+        if (!wait_warp(&B.v_full[s], (uint32_t)((j / NST) & 1), abort)) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (!((f.valid[q] >> lane) & 1u))
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<uint4*>(sV(s) + (32 * q + lane) * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      if (lane == 0) arrive(&B.v_fix[s]);
+    }
+    if (*abort && lane == 0)                       // see the copies in flight land
+      for (int j = max(0, issued - NST); j < issued; ++j) {
+        tc::mbar_wait(&B.k_full[j % NST], (uint32_t)((j / NST) & 1));
+        tc::mbar_wait(&B.v_full[j % NST], (uint32_t)((j / NST) & 1));
+      }
+  } else if (warp == 1) {
+    // ---- MMA issuer
+    if (lane == 0) {
+      int sc[2] = {0, 0}, pc[2] = {0, 0};
+      auto qk = [&](int w, int j) -> bool {
+        const int s = j % NST;
+        if (!wait(&B.k_full[s], (uint32_t)((j / NST) & 1), abort)) return false;
+        if (j > 0 && !wait(&B.s_free[w], (uint32_t)((j - 1) & 1), abort)) return false;
+        tc::tc_fence_after();
+        const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sQ + w * TILE)), kd = tc::sdesc_sw128(tc::smem_u32(sK(s)));
+#pragma unroll
+        for (int kk = 0; kk < WS_DH / 16; ++kk)
+          tc::umma_bf16(tmem + TM_S + 128u * w, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), IDESC_S, kk ? 1u : 0u);
+        tc::umma_commit(&B.s_full[w]);
+        ++sc[w];
+        return true;
+      };
+      auto pv = [&](int w, int j) -> bool {
+        const int s = j % NST;
+        if (!wait(&B.p_full[w], (uint32_t)(j & 1), abort) || !wait(&B.v_full[s], (uint32_t)((j / NST) & 1), abort) ||
+            !wait(&B.v_fix[s], (uint32_t)((j / NST) & 1), abort))
+          return false;
+        tc::tc_fence_after();
+        const uint64_t vd = sdesc_nmajor(tc::smem_u32(sV(s)));
+#pragma unroll
+        for (int kk = 0; kk < FA_KEYS / 16; ++kk)
+          umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), IDESC_PV,
+                  (j | kk) ? 1u : 0u);
+        tc::umma_commit(&B.pv_done[w]);
+        ++pc[w];
+        if (w == 1 || j >= n[1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
+        return true;
+      };
+      bool ok = true;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (ok && n[w]) ok = wait(&B.q_full[w], 0, abort) && qk(w, 0);
+      for (int j = 0; j < nmax && ok; ++j)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (ok && j + 1 < n[w]) ok = qk(w, j + 1);
+          if (ok && j < n[w]) ok = pv(w, j);
+        }
+      if (*abort)                                  // nothing may be in flight when the CTA ends
+        for (int w = 0; w < 2; ++w) {
+          if (n[w]) tc::mbar_wait(&B.q_full[w], 0);
+          if (sc[w]) tc::mbar_wait(&B.s_full[w], (uint32_t)((sc[w] - 1) & 1));
+          if (pc[w]) tc::mbar_wait(&B.pv_done[w], (uint32_t)((pc[w] - 1) & 1));
+        }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = row
+    const int w = warp >= 6 ? 1 : 0, quarter = warp & 3, x = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tS = tl + TM_S + 128u * w, tP = tl + TM_P + 64u * w, tO = tl + TM_O + 64u * w;
+    const int first = rho0 + w * TR, rho = first + x;
+    const bool on = x < TR && rho < R;
+    const int t = on ? rho / p.G : 0;
+    const int lim = on ? row_limit(p, r, t) : 0, lim_all = first < R ? row_limit(p, r, first / p.G) : 0;
+    const float sl = p.sl, hold = fminf(HOLD / sl, 1e30f);
+    const uint64_t sl2 = pack2(sl, sl);
+    float m = -INFINITY, msl = 0.f, l = 0.f;
+    bool ok = true;
+    const int nw = n[w];
+    for (int j = 0; j < nw; ++j) {
+      if (!wait_warp(&B.s_full[w], (uint32_t)(j & 1), abort)) { ok = false; break; }
+      tc::tc_fence_after();
+      float sv[FA_KEYS];
+      tm_ld<FA_KEYS>(tS, sv);
+      ld_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&B.s_free[w]);
+      const Meta& mt = meta[j % NST];
+      const int base = mt.base;
+      if (!mt.full || base + FA_KEYS > lim_all) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int room = lim - base - 32 * q;    // columns of this word below the row's limit
+          const uint32_t see = mt.valid[q] & (room >= 32 ? 0xffffffffu : room <= 0 ? 0u : (1u << room) - 1u);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1u)) sv[32 * q + e] = -INFINITY;
+        }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < FA_KEYS; e += 8)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(fmaxf(mx[q], sv[e + 2 * q]), sv[e + 2 * q + 1]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // P and O are free once the previous product has finished
+      if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
+      const bool grow = top > m + hold;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? top : m;
+        const float f = m > -INFINITY ? ex2((m - mn) * sl) : (mn > -INFINITY ? 0.f : 1.f);
+        m = mn;
+        msl = mn > -INFINITY ? mn * sl : 0.f;
+        l *= f;
+        if (j > 0) {
+          tc::tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float o[16];
+            uint32_t u[16];
+            tm_ld<16>(tO + 16 * q, o);
+            ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+            tm_st16(tO + 16 * q, u);
+          }
+        }
+      }
+      const uint64_t nm2 = pack2(-msl, -msl);
+      uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t u[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float a, b;
+          unpack2(fma2(pack2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), sl2, nm2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          sum2[e & 1] = add2(sum2[e & 1], pack2(a, b));
+          u[e] = pack_bf(a, b);
+        }
+        tm_st16(tP + 16 * q, u);
+      }
+      float a, b;
+      unpack2(add2(sum2[0], sum2[1]), a, b);
+      l += a + b;
+      st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&B.p_full[w]);
+    }
+    if (ok && nw > 0) ok = wait_warp(&B.pv_done[w], (uint32_t)((nw - 1) & 1), abort);
+    tc::tc_fence_after();
+    if (p.nsplit > 1) {
+      const size_t at = on ? (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split : 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float o[16];
+        if (nw > 0) { tm_ld<16>(tO + 16 * q, o); ld_wait(); }
+        if (on)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(p.part_o + at * WS_DH + 16 * q + e) =
+                nw > 0 ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (on) p.part_ml[at] = make_float2(m == -INFINITY ? m : msl, ok ? l : NAN);
+    } else {
+      const float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / l;
+      const int u_ = h * p.G + (on ? rho - t * p.G : 0);
+      bf16* out = (bf16*)p.a.out + (size_t)(r.row0 + t) * p.a.out_stride + (size_t)u_ * WS_DH;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float o[16];
+        if (nw > 0) { tm_ld<16>(tO + 16 * q, o); ld_wait(); }
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = nw > 0 ? pack_bf(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+        // a row that sees nothing inside a tile that does has P = 0, l = 0
+        if (on) {
+          reinterpret_cast<uint4*>(out + 16 * q)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+          reinterpret_cast<uint4*>(out + 16 * q)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        }
+      }
+      if (on && p.lse)
+        p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u_] = !ok ? NAN : l == 0.f ? -INFINITY : (msl + lg2(l)) * LN2;
+    }
+    tc::tc_fence_before();
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ accumulated weights
+constexpr int MST = 4;                             // row tile stages
+constexpr int MASS_SMEM = 2 * TILE + MST * TILE + 1024;
+
+struct MassBars { uint64_t k_full, q_full[MST], empty[MST], s_full[2][2], s_free[2][2]; };
+
+__global__ void __launch_bounds__(THREADS, 1)
+fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
+  extern __shared__ uint8_t dsm[];
+  __shared__ __align__(8) MassBars B;
+  __shared__ Meta meta[2];
+  __shared__ __align__(16) float nlse[MST][FA_ROWS];   // -lse * log2(e) of a tile's rows
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  const int h = blockIdx.y, i = blockIdx.z, kt0 = blockIdx.x * 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Req r = request(p, i);
+  const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
+  const int nk = tile_count(p.geo, p.c.page_size, FA_KEYS, r.L);
+  if (kt0 >= nk || R == 0) return;
+  const int nq = (R + TR - 1) / TR;
+  const int base0 = p.geo.tpp ? kt0 / p.geo.tpp * p.c.page_size + kt0 % p.geo.tpp * FA_KEYS : kt0 * FA_KEYS;
+  // row tiles before the first row that sees position base0 add nothing
+  const int q_lo = p.a.causal ? max(0, base0 - (r.L - r.c)) / RB : 0;
+  const int nt = max(0, nq - q_lo);
+  volatile int* abort = &s_abort;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&B.k_full, 1);
+    for (int b = 0; b < MST; ++b) { tc::mbar_init(&B.q_full[b], 1); tc::mbar_init(&B.empty[b], 8); }
+    for (int w = 0; w < 2; ++w)
+      for (int b = 0; b < 2; ++b) { tc::mbar_init(&B.s_full[w][b], 1); tc::mbar_init(&B.s_free[w][b], 4); }
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tc::tmem_alloc(&s_tmem, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  uint8_t* sK = sm;
+  auto sQ = [&](int b) { return sm + 2 * TILE + b * TILE; };
+  const bool two = kt0 + 1 < nk;
+
+  if (warp == 0) {
+    // ---- producer: both key tiles, then the row tiles with their log-sum-exps
+    const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
+    TileInfo f[2];
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      f[w] = tile_info(p, kt0 + w, w == 0 || two ? tile_page(p, table, kt0 + w, lane) : -1, r.L, lane);
+      bytes += (uint32_t)__popc(__ballot_sync(0xffffffffu, f[w].page >= 0)) * (uint32_t)p.geo.box * 128u;
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) meta[w].valid[q] = f[w].valid[q];
+        meta[w].base = f[w].base;
+      }
+      tc::mbar_expect_tx(&B.k_full, bytes);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      if (f[w].page >= 0) tma_load_4d(sK + w * TILE + f[w].dst, &mk, &B.k_full, 0, f[w].tok, h, f[w].page);
+    int issued = 0;
+    for (int j = 0; j < nt; ++j) {
+      const int s = j % MST;
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int x = 32 * q + lane, rho = (q_lo + j) * TR + x;
+        v[q] = -INFINITY;
+        if (x < TR && rho < R) {
+          const int t = rho / p.G;
+          const float y = p.lse[(size_t)(r.row0 + t) * p.a.n_heads + h * p.G + rho - t * p.G];
+          v[q] = y == -INFINITY ? -INFINITY : -y * LOG2E;
+        }
+      }
+      if (j >= MST && !wait_warp(&B.empty[s], (uint32_t)((j / MST - 1) & 1), abort)) break;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) nlse[s][32 * q + lane] = v[q];
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_expect_tx(&B.q_full[s], (uint32_t)TR * 128u);
+        tma_load_3d(sQ(s), &mq, &B.q_full[s], 0, h * p.G, r.row0 + (q_lo + j) * RB);
+      }
+      ++issued;
+    }
+    if (*abort && lane == 0) {
+      tc::mbar_wait(&B.k_full, 0);
+      for (int j = max(0, issued - MST); j < issued; ++j) tc::mbar_wait(&B.q_full[j % MST], (uint32_t)((j / MST) & 1));
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = wait(&B.k_full, 0, abort);
+      int done = 0;
+      for (int j = 0; j < nt && ok; ++j) {
+        const int s = j % MST, b = j & 1;
+        if (!wait(&B.q_full[s], (uint32_t)((j / MST) & 1), abort)) break;
+        const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sQ(s)));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (j >= 2 && ok) ok = wait(&B.s_free[w][b], (uint32_t)((j / 2 - 1) & 1), abort);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sK + w * TILE));
+#pragma unroll
+          for (int kk = 0; kk < WS_DH / 16; ++kk)
+            tc::umma_bf16(tmem + 256u * w + 128u * b, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), IDESC_S,
+                          kk ? 1u : 0u);
+          tc::umma_commit(&B.s_full[w][b]);
+        }
+        ++done;
+      }
+      if (*abort)
+        for (int j = max(0, done - 2); j < done; ++j)
+          for (int w = 0; w < 2; ++w) tc::mbar_wait(&B.s_full[w][j & 1], (uint32_t)((j / 2) & 1));
+    }
+    __syncwarp();
+  } else {
+    // ---- sums: thread = key
+    const int w = warp >= 6 ? 1 : 0, quarter = warp & 3, x = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + 256u * w;
+    bool ok = wait_warp(&B.k_full, 0, abort);
+    const int pos = meta[w].base + x;
+    const bool on = (meta[w].valid[quarter] >> lane) & 1u;
+    const uint64_t sl2 = pack2(p.sl, p.sl);
+    float total = 0.f;
+    for (int j = 0; j < nt && ok; ++j) {
+      const int s = j % MST, b = j & 1, rho = (q_lo + j) * TR;
+      if (!wait_warp(&B.s_full[w][b], (uint32_t)((j / 2) & 1), abort)) { ok = false; break; }
+      tc::tc_fence_after();
+      float sv[FA_ROWS];
+      tm_ld<FA_ROWS>(tl + 128u * b, sv);
+      ld_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&B.s_free[w][b]);
+      // columns of rows that see this key: from the row whose position it is
+      const int cmin = p.a.causal ? max(0, pos - (r.L - r.c)) * p.G - rho : 0, cmax = min(TR, R - rho);
+      uint64_t sum2[2] = {0ull, 0ull};
+      const float4* nl = reinterpret_cast<const float4*>(nlse[s]);
+      const bool whole = cmin <= 0 && cmax == FA_ROWS;
+      if (__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+        for (int e = 0; e < FA_ROWS / 4; ++e) {
+          const float4 n4 = nl[e];
+          float a0, a1, a2, a3;
+          unpack2(fma2(pack2(sv[4 * e], sv[4 * e + 1]), sl2, pack2(n4.x, n4.y)), a0, a1);
+          unpack2(fma2(pack2(sv[4 * e + 2], sv[4 * e + 3]), sl2, pack2(n4.z, n4.w)), a2, a3);
+          sum2[0] = add2(sum2[0], pack2(ex2(a0), ex2(a1)));
+          sum2[1] = add2(sum2[1], pack2(ex2(a2), ex2(a3)));
+        }
+        float a, c;
+        unpack2(add2(sum2[0], sum2[1]), a, c);
+        total += a + c;
+      } else {
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < FA_ROWS; ++e) {
+          const float y = ex2(fmaf(sv[e], p.sl, nlse[s][e]));
+          if (e >= cmin && e < cmax && nlse[s][e] > -INFINITY) part[e & 3] += y;
+        }
+        total += (part[0] + part[1]) + (part[2] + part[3]);
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&B.empty[s]);          // the tile's S is computed and its log-sum-exps are read
+    }
+    if (on) p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + pos] += ok ? total : NAN;
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_fa(const AttnP& p, int row_tiles, cudaStream_t s) {
+  TcMap mq, mk, mv;
+  if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
+                       (uint32_t)(FA_ROWS / p.G)) ||
+      !tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(fa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FA_SMEM);
+  if (e != cudaSuccess) return e;
+  fa_kernel<<<dim3((row_tiles + 1) / 2 * p.nsplit, p.c.n_kv_heads, p.a.n_req), THREADS, FA_SMEM, s>>>(
+      p, row_tiles, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
+      reinterpret_cast<const CUtensorMap&>(mv));
+  ws_count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fa_mass(const AttnP& p, int row_tiles, cudaStream_t s) {
+  (void)row_tiles;
+  TcMap mq, mk;
+  if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
+                       (uint32_t)(FA_ROWS / p.G)) ||
+      !tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(fa_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MASS_SMEM);
+  if (e != cudaSuccess) return e;
+  const int tiles = tile_count(p.geo, p.c.page_size, FA_KEYS, p.a.max_kv);
+  fa_mass_kernel<<<dim3((tiles + 1) / 2, p.c.n_kv_heads, p.a.n_req), THREADS, MASS_SMEM, s>>>(
+      p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk));
+  ws_count_launches(1);
+  return cudaGetLastError();
+}
