@@ -60,6 +60,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, abort);
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p;
+}
 // D[tmem] (+)= A[tmem] B[smem]
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -168,7 +173,7 @@ __device__ __forceinline__ TileInfo tile_info(const AttnP& p, int t, int page, i
 }
 
 struct Bars {
-  uint64_t q_full[2], k_full[NST], v_full[NST], v_fix[NST], empty[NST], s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], full[NST], empty[NST], raw, s_full[2], s_free[2], p_full[2], pv_done[2];
 };
 
 __global__ void __launch_bounds__(THREADS, 1)
@@ -183,7 +188,7 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
   const int pairs = (row_tiles + 1) / 2;
   const int pair = pairs - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
   const int h = blockIdx.y, i = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Req r = request(p, i);
   const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
   const int rho0 = pair * 2 * TR;
@@ -204,9 +209,10 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int b = 0; b < NST; ++b) {
-      tc::mbar_init(&B.k_full[b], 1); tc::mbar_init(&B.v_full[b], 1); tc::mbar_init(&B.v_fix[b], 1);
+      tc::mbar_init(&B.full[b], 1);
       tc::mbar_init(&B.empty[b], 1);
     }
+    tc::mbar_init(&B.raw, 1);
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(&B.q_full[w], 1); tc::mbar_init(&B.s_full[w], 1); tc::mbar_init(&B.s_free[w], 4);
       tc::mbar_init(&B.p_full[w], 4); tc::mbar_init(&B.pv_done[w], 1);
@@ -225,7 +231,7 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
   if (warp == 0) {
     // ---- producer
@@ -238,33 +244,35 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
         }
     }
     const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
-    int page = tile_page(p, table, lo, lane), issued = 0;
+    int page = tile_page(p, table, lo, lane), issued = 0, raws = 0;
     for (int j = 0; j < nmax; ++j) {
       const int s = j % NST;
       const TileInfo f = tile_info(p, lo + j, page, r.L, lane);
       if (j + 1 < nmax) page = tile_page(p, table, lo + j + 1, lane);
       if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
       const bool go = f.page >= 0;
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 128u;
-      const bool full = (f.valid[0] & f.valid[1] & f.valid[2] & f.valid[3]) == 0xffffffffu;
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 256u;
+      const bool whole = (f.valid[0] & f.valid[1] & f.valid[2] & f.valid[3]) == 0xffffffffu;
+      uint64_t* bar = whole ? &B.full[s] : &B.raw;
       if (lane == 0) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) meta[s].valid[q] = f.valid[q];
         meta[s].base = f.base;
-        meta[s].full = full;
-        tc::mbar_expect_tx(&B.k_full[s], bytes);
-        tc::mbar_expect_tx(&B.v_full[s], bytes);
+        meta[s].full = whole;
+        tc::mbar_expect_tx(bar, bytes);
       }
       __syncwarp();
       if (go) {
-        tma_load_4d(sK(s) + f.dst, &mk, &B.k_full[s], 0, f.tok, h, f.page);
-        tma_load_4d(sV(s) + f.dst, &mv, &B.v_full[s], 0, f.tok, h, f.page);
+        tma_load_4d(sK(s) + f.dst, &mk, bar, 0, f.tok, h, f.page);
+        tma_load_4d(sV(s) + f.dst, &mv, bar, 0, f.tok, h, f.page);
       }
       ++issued;
-      if (!full) {
-        // rows behind the cache's length, or of skipped pages, may hold
-        // anything: 0 * inf would reach the sums
-        if (!wait_warp(&B.v_full[s], (uint32_t)((j / NST) & 1), abort)) break;
+      if (!whole) {
+        // value rows behind the cache's length, or of skipped pages, may hold
+        // anything (0 * inf would reach the sums): cleared before the tile is
+        // handed over
+        ++raws;
+        if (!wait_warp(&B.raw, (uint32_t)((raws - 1) & 1), abort)) break;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (!((f.valid[q] >> lane) & 1u))
@@ -273,64 +281,67 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
               *reinterpret_cast<uint4*>(sV(s) + (32 * q + lane) * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
+        if (lane == 0) arrive(&B.full[s]);
       }
-      if (lane == 0) arrive(&B.v_fix[s]);
     }
-    if (*abort && lane == 0)                       // see the copies in flight land
-      for (int j = max(0, issued - NST); j < issued; ++j) {
-        tc::mbar_wait(&B.k_full[j % NST], (uint32_t)((j / NST) & 1));
-        tc::mbar_wait(&B.v_full[j % NST], (uint32_t)((j / NST) & 1));
-      }
+    if (*abort && lane == 0) {                     // see the copies in flight land
+      for (int j = max(0, issued - NST); j < issued; ++j) tc::mbar_wait(&B.full[j % NST], (uint32_t)((j / NST) & 1));
+      if (raws) tc::mbar_wait(&B.raw, (uint32_t)((raws - 1) & 1));
+    }
   } else if (warp == 1) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      int sc[2] = {0, 0}, pc[2] = {0, 0};
-      auto qk = [&](int w, int j) -> bool {
-        const int s = j % NST;
-        if (!wait(&B.k_full[s], (uint32_t)((j / NST) & 1), abort)) return false;
-        if (j > 0 && !wait(&B.s_free[w], (uint32_t)((j - 1) & 1), abort)) return false;
-        tc::tc_fence_after();
-        const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sQ + w * TILE)), kd = tc::sdesc_sw128(tc::smem_u32(sK(s)));
+    // ---- MMA issuer: the whole warp walks along, so that descriptors stay
+    // in uniform registers; one elected lane issues
+    const uint32_t lead = elect_one();
+    const uint64_t qd0 = tc::sdesc_sw128(tc::smem_u32(sQ)), kd0 = tc::sdesc_sw128(tc::smem_u32(sK(0))),
+                   vd0 = sdesc_nmajor(tc::smem_u32(sV(0)));
+    auto qk = [&](int w, int j) -> bool {
+      const int s = j % NST;
+      if ((w == 0 || j >= n[0]) && !wait(&B.full[s], (uint32_t)((j / NST) & 1), abort)) return false;
+      if (j > 0 && !wait(&B.s_free[w], (uint32_t)((j - 1) & 1), abort)) return false;
+      tc::tc_fence_after();
+      if (lead) {
+        const uint64_t qd = qd0 + (uint64_t)(w * (TILE >> 4)), kd = kd0 + (uint64_t)(s * (2 * TILE >> 4));
 #pragma unroll
         for (int kk = 0; kk < WS_DH / 16; ++kk)
           tc::umma_bf16(tmem + TM_S + 128u * w, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), IDESC_S, kk ? 1u : 0u);
         tc::umma_commit(&B.s_full[w]);
-        ++sc[w];
-        return true;
-      };
-      auto pv = [&](int w, int j) -> bool {
-        const int s = j % NST;
-        if (!wait(&B.p_full[w], (uint32_t)(j & 1), abort) || !wait(&B.v_full[s], (uint32_t)((j / NST) & 1), abort) ||
-            !wait(&B.v_fix[s], (uint32_t)((j / NST) & 1), abort))
-          return false;
-        tc::tc_fence_after();
-        const uint64_t vd = sdesc_nmajor(tc::smem_u32(sV(s)));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto pv = [&](int w, int j) -> bool {
+      const int s = j % NST;
+      if (!wait(&B.p_full[w], (uint32_t)(j & 1), abort)) return false;
+      tc::tc_fence_after();
+      if (lead) {
+        const uint64_t vd = vd0 + (uint64_t)(s * (2 * TILE >> 4));
 #pragma unroll
         for (int kk = 0; kk < FA_KEYS / 16; ++kk)
           umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), IDESC_PV,
                   (j | kk) ? 1u : 0u);
         tc::umma_commit(&B.pv_done[w]);
-        ++pc[w];
         if (w == 1 || j >= n[1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
-        return true;
-      };
-      bool ok = true;
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    int sc[2] = {0, 0}, pc[2] = {0, 0};
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (ok && n[w]) ok = wait(&B.q_full[w], 0, abort) && qk(w, 0);
-      for (int j = 0; j < nmax && ok; ++j)
+    for (int w = 0; w < 2; ++w)
+      if (ok && n[w]) { ok = wait(&B.q_full[w], 0, abort) && qk(w, 0); sc[w] = ok; }
+    for (int j = 0; j < nmax && ok; ++j)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (ok && j + 1 < n[w]) ok = qk(w, j + 1);
-          if (ok && j < n[w]) ok = pv(w, j);
-        }
-      if (*abort)                                  // nothing may be in flight when the CTA ends
-        for (int w = 0; w < 2; ++w) {
-          if (n[w]) tc::mbar_wait(&B.q_full[w], 0);
-          if (sc[w]) tc::mbar_wait(&B.s_full[w], (uint32_t)((sc[w] - 1) & 1));
-          if (pc[w]) tc::mbar_wait(&B.pv_done[w], (uint32_t)((pc[w] - 1) & 1));
-        }
-    }
+      for (int w = 0; w < 2; ++w) {
+        if (ok && j + 1 < n[w]) { ok = qk(w, j + 1); sc[w] += ok; }
+        if (ok && j < n[w]) { ok = pv(w, j); pc[w] += ok; }
+      }
+    if (*abort && lane == 0)                       // nothing may be in flight when the CTA ends
+      for (int w = 0; w < 2; ++w) {
+        if (n[w]) tc::mbar_wait(&B.q_full[w], 0);
+        if (sc[w]) tc::mbar_wait(&B.s_full[w], (uint32_t)((sc[w] - 1) & 1));
+        if (pc[w]) tc::mbar_wait(&B.pv_done[w], (uint32_t)((pc[w] - 1) & 1));
+      }
     __syncwarp();
   } else {
     // ---- softmax: thread = row
@@ -478,7 +489,7 @@ fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __gr
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   const int h = blockIdx.y, i = blockIdx.z, kt0 = blockIdx.x * 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Req r = request(p, i);
   const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
   const int nk = tile_count(p.geo, p.c.page_size, FA_KEYS, r.L);
@@ -501,7 +512,7 @@ fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __gr
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   uint8_t* sK = sm;
   auto sQ = [&](int b) { return sm + 2 * TILE + b * TILE; };
   const bool two = kt0 + 1 < nk;
@@ -558,31 +569,33 @@ fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __gr
       for (int j = max(0, issued - MST); j < issued; ++j) tc::mbar_wait(&B.q_full[j % MST], (uint32_t)((j / MST) & 1));
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      bool ok = wait(&B.k_full, 0, abort);
-      int done = 0;
-      for (int j = 0; j < nt && ok; ++j) {
-        const int s = j % MST, b = j & 1;
-        if (!wait(&B.q_full[s], (uint32_t)((j / MST) & 1), abort)) break;
-        const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sQ(s)));
+    const uint32_t lead = elect_one();
+    const uint64_t kd0 = tc::sdesc_sw128(tc::smem_u32(sK)), qd0 = tc::sdesc_sw128(tc::smem_u32(sQ(0)));
+    bool ok = wait(&B.k_full, 0, abort);
+    int done = 0;
+    for (int j = 0; j < nt && ok; ++j) {
+      const int s = j % MST, b = j & 1;
+      if (!wait(&B.q_full[s], (uint32_t)((j / MST) & 1), abort)) break;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (j >= 2 && ok) ok = wait(&B.s_free[w][b], (uint32_t)((j / 2 - 1) & 1), abort);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sK + w * TILE));
+      for (int w = 0; w < 2; ++w) {
+        if (j >= 2 && ok) ok = wait(&B.s_free[w][b], (uint32_t)((j / 2 - 1) & 1), abort);
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (lead) {
+          const uint64_t kd = kd0 + (uint64_t)(w * (TILE >> 4)), qd = qd0 + (uint64_t)(s * (TILE >> 4));
 #pragma unroll
           for (int kk = 0; kk < WS_DH / 16; ++kk)
             tc::umma_bf16(tmem + 256u * w + 128u * b, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), IDESC_S,
                           kk ? 1u : 0u);
           tc::umma_commit(&B.s_full[w][b]);
         }
-        ++done;
+        __syncwarp();
       }
-      if (*abort)
-        for (int j = max(0, done - 2); j < done; ++j)
-          for (int w = 0; w < 2; ++w) tc::mbar_wait(&B.s_full[w][j & 1], (uint32_t)((j / 2) & 1));
+      done += ok;
     }
+    if (*abort && lane == 0)
+      for (int j = max(0, done - 2); j < done; ++j)
+        for (int w = 0; w < 2; ++w) tc::mbar_wait(&B.s_full[w][j & 1], (uint32_t)((j / 2) & 1));
     __syncwarp();
   } else {
     // ---- sums: thread = key
