@@ -674,7 +674,7 @@ cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
     ws_count_launches(1);
   }
   if (!p.a.mass || p.a.max_kv == 0 || q.stash) return cudaGetLastError();
-  if (q.fa) return launch_fa_mass(p, q.row_tiles, s);
+  if (q.fa) return launch_fa_mass(p, s);
   mass_kernel<<<dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
   ws_count_launches(1);
   return cudaGetLastError();

@@ -89,4 +89,4 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 constexpr int FA_ROWS = 128, FA_KEYS = 128;
 inline int fa_rows(int G) { return G * (FA_ROWS / G); }                        // G <= 128
 cudaError_t launch_fa(const AttnP& p, int row_tiles, cudaStream_t s);
-cudaError_t launch_fa_mass(const AttnP& p, int row_tiles, cudaStream_t s);
+cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s);

@@ -27,7 +27,7 @@ namespace {
 
 constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
 constexpr int NST = 4;                             // key stages
-constexpr int THREADS = 320;
+constexpr int THREADS = 384;                        // producer, MMA, two idle | softmax A | softmax B
 constexpr int FA_SMEM = 2 * TILE + NST * 2 * TILE + 1024;
 constexpr uint32_t TM_S = 0, TM_P = 256, TM_O = 384;   // + 128 w, + 64 w, + 64 w
 constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
@@ -85,19 +85,23 @@ __device__ __forceinline__ uint64_t sdesc_nmajor(uint32_t saddr) {
   d |= (uint64_t)2 << 61;
   return d;
 }
-template <int N>
-__device__ __forceinline__ void tm_ld(uint32_t taddr, float* v) {
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
 #pragma unroll
-  for (int q = 0; q < N; q += 16) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr + q));
+  for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+}
+__device__ __forceinline__ void tm_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[q + e] = __uint_as_float(r[e]);
-  }
+  for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
 }
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -108,23 +112,10 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -233,6 +224,8 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // ---- producer
     if (lane == 0) {
@@ -343,9 +336,11 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
         if (pc[w]) tc::mbar_wait(&B.pv_done[w], (uint32_t)((pc[w] - 1) & 1));
       }
     __syncwarp();
+  }
   } else {
     // ---- softmax: thread = row
-    const int w = warp >= 6 ? 1 : 0, quarter = warp & 3, x = quarter * 32 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int w = (warp >> 2) - 1, quarter = warp & 3, x = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tS = tl + TM_S + 128u * w, tP = tl + TM_P + 64u * w, tO = tl + TM_O + 64u * w;
     const int first = rho0 + w * TR, rho = first + x;
@@ -353,7 +348,7 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
     const int t = on ? rho / p.G : 0;
     const int lim = on ? row_limit(p, r, t) : 0, lim_all = first < R ? row_limit(p, r, first / p.G) : 0;
     const float sl = p.sl, hold = fminf(HOLD / sl, 1e30f);
-    const uint64_t sl2 = pack2(sl, sl);
+    const float2 sl2 = make_float2(sl, sl);
     float m = -INFINITY, msl = 0.f, l = 0.f;
     bool ok = true;
     const int nw = n[w];
@@ -361,14 +356,16 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
       if (!wait_warp(&B.s_full[w], (uint32_t)(j & 1), abort)) { ok = false; break; }
       tc::tc_fence_after();
       float sv[FA_KEYS];
-      tm_ld<FA_KEYS>(tS, sv);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) tm_ld16(tS + 16 * q, sv + 16 * q);
+      const Meta& mt = meta[j % NST];
+      const int base = mt.base;
+      const bool dense = mt.full && base + FA_KEYS <= lim_all;
       ld_wait();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive(&B.s_free[w]);
-      const Meta& mt = meta[j % NST];
-      const int base = mt.base;
-      if (!mt.full || base + FA_KEYS > lim_all) {
+      if (!dense) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int room = lim - base - 32 * q;    // columns of this word below the row's limit
@@ -382,8 +379,8 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
 #pragma unroll
       for (int e = 0; e < FA_KEYS; e += 8)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(fmaxf(mx[q], sv[e + 2 * q]), sv[e + 2 * q + 1]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
+      const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
       // P and O are free once the previous product has finished
       if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
       const bool grow = top > m + hold;
@@ -396,36 +393,33 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
         if (j > 0) {
           tc::tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int d = 0; d < 4; ++d) {
             float o[16];
-            uint32_t u[16];
-            tm_ld<16>(tO + 16 * q, o);
+            uint32_t v[16];
+            tm_ld16(tO + 16 * d, o);
             ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
-            tm_st16(tO + 16 * q, u);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * f);
+            tm_st16(tO + 16 * d, v);
           }
         }
       }
-      const uint64_t nm2 = pack2(-msl, -msl);
-      uint64_t sum2[2] = {0ull, 0ull};
+      const float2 nm2 = make_float2(-msl, -msl);
+      float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t u[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float a, b;
-          unpack2(fma2(pack2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), sl2, nm2), a, b);
-          a = ex2(a);
-          b = ex2(b);
-          sum2[e & 1] = add2(sum2[e & 1], pack2(a, b));
-          u[e] = pack_bf(a, b);
+          float2 y = __ffma2_rn(make_float2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), sl2, nm2);
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          sum2[e & 1] = __fadd2_rn(sum2[e & 1], y);
+          u[e] = pack_bf(y.x, y.y);
         }
         tm_st16(tP + 16 * q, u);
       }
-      float a, b;
-      unpack2(add2(sum2[0], sum2[1]), a, b);
-      l += a + b;
+      l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
       st_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -438,7 +432,7 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float o[16];
-        if (nw > 0) { tm_ld<16>(tO + 16 * q, o); ld_wait(); }
+        if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
         if (on)
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
@@ -453,7 +447,7 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float o[16];
-        if (nw > 0) { tm_ld<16>(tO + 16 * q, o); ld_wait(); }
+        if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
         uint32_t u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e] = nw > 0 ? pack_bf(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
@@ -474,95 +468,90 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
 }
 
 // ------------------------------------------------------------------ accumulated weights
+// One key tile per CTA and two CTAs per SM (256 tensor memory columns each:
+// S twice), so that one CTA's start and end lie under the other's work.
 constexpr int MST = 4;                             // row tile stages
-constexpr int MASS_SMEM = 2 * TILE + MST * TILE + 1024;
+constexpr int MTHREADS = 192;                      // producer, MMA, four summing warps
+constexpr int MASS_SMEM = TILE + MST * TILE + 1024;
 
-struct MassBars { uint64_t k_full, q_full[MST], empty[MST], s_full[2][2], s_free[2][2]; };
+struct MassBars { uint64_t k_full, q_full[MST], empty[MST], s_full[2], s_free[2]; };
 
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(MTHREADS, 2)
 fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) MassBars B;
-  __shared__ Meta meta[2];
+  __shared__ Meta meta;
   __shared__ __align__(16) float nlse[MST][FA_ROWS];   // -lse * log2(e) of a tile's rows
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
-  const int h = blockIdx.y, i = blockIdx.z, kt0 = blockIdx.x * 2;
+  const int h = blockIdx.y, i = blockIdx.z, kt = blockIdx.x;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Req r = request(p, i);
   const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
   const int nk = tile_count(p.geo, p.c.page_size, FA_KEYS, r.L);
-  if (kt0 >= nk || R == 0) return;
+  if (kt >= nk || R == 0) return;
   const int nq = (R + TR - 1) / TR;
-  const int base0 = p.geo.tpp ? kt0 / p.geo.tpp * p.c.page_size + kt0 % p.geo.tpp * FA_KEYS : kt0 * FA_KEYS;
+  const int base0 = p.geo.tpp ? kt / p.geo.tpp * p.c.page_size + kt % p.geo.tpp * FA_KEYS : kt * FA_KEYS;
   // row tiles before the first row that sees position base0 add nothing
   const int q_lo = p.a.causal ? max(0, base0 - (r.L - r.c)) / RB : 0;
   const int nt = max(0, nq - q_lo);
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
     tc::mbar_init(&B.k_full, 1);
-    for (int b = 0; b < MST; ++b) { tc::mbar_init(&B.q_full[b], 1); tc::mbar_init(&B.empty[b], 8); }
-    for (int w = 0; w < 2; ++w)
-      for (int b = 0; b < 2; ++b) { tc::mbar_init(&B.s_full[w][b], 1); tc::mbar_init(&B.s_free[w][b], 4); }
+    for (int b = 0; b < MST; ++b) { tc::mbar_init(&B.q_full[b], 1); tc::mbar_init(&B.empty[b], 4); }
+    for (int b = 0; b < 2; ++b) { tc::mbar_init(&B.s_full[b], 1); tc::mbar_init(&B.s_free[b], 4); }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tc::tmem_alloc(&s_tmem, 512);
+  if (warp == 1) tc::tmem_alloc(&s_tmem, 256);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   uint8_t* sK = sm;
-  auto sQ = [&](int b) { return sm + 2 * TILE + b * TILE; };
-  const bool two = kt0 + 1 < nk;
+  auto sQ = [&](int b) { return sm + TILE + b * TILE; };
 
   if (warp == 0) {
-    // ---- producer: both key tiles, then the row tiles with their log-sum-exps
+    // ---- producer: the key tile, then the row tiles with their
+    // log-sum-exps, which are asked for one tile ahead
     const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
-    TileInfo f[2];
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      f[w] = tile_info(p, kt0 + w, w == 0 || two ? tile_page(p, table, kt0 + w, lane) : -1, r.L, lane);
-      bytes += (uint32_t)__popc(__ballot_sync(0xffffffffu, f[w].page >= 0)) * (uint32_t)p.geo.box * 128u;
-    }
+    const TileInfo f = tile_info(p, kt, tile_page(p, table, kt, lane), r.L, lane);
+    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, f.page >= 0)) * (uint32_t)p.geo.box * 128u;
     if (lane == 0) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) meta[w].valid[q] = f[w].valid[q];
-        meta[w].base = f[w].base;
-      }
+      for (int q = 0; q < 4; ++q) meta.valid[q] = f.valid[q];
+      meta.base = f.base;
       tc::mbar_expect_tx(&B.k_full, bytes);
     }
     __syncwarp();
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-      if (f[w].page >= 0) tma_load_4d(sK + w * TILE + f[w].dst, &mk, &B.k_full, 0, f[w].tok, h, f[w].page);
-    int issued = 0;
-    for (int j = 0; j < nt; ++j) {
-      const int s = j % MST;
-      float v[4];
+    if (f.page >= 0) tma_load_4d(sK + f.dst, &mk, &B.k_full, 0, f.tok, h, f.page);
+    float v[4];
+    auto ask = [&](int j) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int x = 32 * q + lane, rho = (q_lo + j) * TR + x;
         v[q] = -INFINITY;
-        if (x < TR && rho < R) {
+        if (j < nt && x < TR && rho < R) {
           const int t = rho / p.G;
-          const float y = p.lse[(size_t)(r.row0 + t) * p.a.n_heads + h * p.G + rho - t * p.G];
-          v[q] = y == -INFINITY ? -INFINITY : -y * LOG2E;
+          v[q] = p.lse[(size_t)(r.row0 + t) * p.a.n_heads + h * p.G + rho - t * p.G];
         }
       }
+    };
+    ask(0);
+    int issued = 0;
+    for (int j = 0; j < nt; ++j) {
+      const int s = j % MST;
       if (j >= MST && !wait_warp(&B.empty[s], (uint32_t)((j / MST - 1) & 1), abort)) break;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) nlse[s][32 * q + lane] = v[q];
+      for (int q = 0; q < 4; ++q) nlse[s][32 * q + lane] = v[q] == -INFINITY ? -INFINITY : -v[q] * LOG2E;
       __syncwarp();
       if (lane == 0) {
         tc::mbar_expect_tx(&B.q_full[s], (uint32_t)TR * 128u);
         tma_load_3d(sQ(s), &mq, &B.q_full[s], 0, h * p.G, r.row0 + (q_lo + j) * RB);
       }
       ++issued;
+      ask(j + 1);
     }
     if (*abort && lane == 0) {
       tc::mbar_wait(&B.k_full, 0);
@@ -570,70 +559,63 @@ fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __gr
     }
   } else if (warp == 1) {
     const uint32_t lead = elect_one();
-    const uint64_t kd0 = tc::sdesc_sw128(tc::smem_u32(sK)), qd0 = tc::sdesc_sw128(tc::smem_u32(sQ(0)));
+    const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sK)), qd0 = tc::sdesc_sw128(tc::smem_u32(sQ(0)));
     bool ok = wait(&B.k_full, 0, abort);
     int done = 0;
     for (int j = 0; j < nt && ok; ++j) {
       const int s = j % MST, b = j & 1;
       if (!wait(&B.q_full[s], (uint32_t)((j / MST) & 1), abort)) break;
+      if (j >= 2 && !wait(&B.s_free[b], (uint32_t)((j / 2 - 1) & 1), abort)) break;
+      tc::tc_fence_after();
+      if (lead) {
+        const uint64_t qd = qd0 + (uint64_t)(s * (TILE >> 4));
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (j >= 2 && ok) ok = wait(&B.s_free[w][b], (uint32_t)((j / 2 - 1) & 1), abort);
-        if (!ok) break;
-        tc::tc_fence_after();
-        if (lead) {
-          const uint64_t kd = kd0 + (uint64_t)(w * (TILE >> 4)), qd = qd0 + (uint64_t)(s * (TILE >> 4));
-#pragma unroll
-          for (int kk = 0; kk < WS_DH / 16; ++kk)
-            tc::umma_bf16(tmem + 256u * w + 128u * b, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), IDESC_S,
-                          kk ? 1u : 0u);
-          tc::umma_commit(&B.s_full[w][b]);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < WS_DH / 16; ++kk)
+          tc::umma_bf16(tmem + 128u * b, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), IDESC_S, kk ? 1u : 0u);
+        tc::umma_commit(&B.s_full[b]);
       }
-      done += ok;
+      __syncwarp();
+      ++done;
     }
     if (*abort && lane == 0)
-      for (int j = max(0, done - 2); j < done; ++j)
-        for (int w = 0; w < 2; ++w) tc::mbar_wait(&B.s_full[w][j & 1], (uint32_t)((j / 2) & 1));
+      for (int j = max(0, done - 2); j < done; ++j) tc::mbar_wait(&B.s_full[j & 1], (uint32_t)((j / 2) & 1));
     __syncwarp();
   } else {
     // ---- sums: thread = key
-    const int w = warp >= 6 ? 1 : 0, quarter = warp & 3, x = quarter * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + 256u * w;
+    const int quarter = warp & 3;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     bool ok = wait_warp(&B.k_full, 0, abort);
-    const int pos = meta[w].base + x;
-    const bool on = (meta[w].valid[quarter] >> lane) & 1u;
-    const uint64_t sl2 = pack2(p.sl, p.sl);
+    const int pos = meta.base + quarter * 32 + lane;
+    const bool on = (meta.valid[quarter] >> lane) & 1u;
+    const float2 sl2 = make_float2(p.sl, p.sl);
     float total = 0.f;
     for (int j = 0; j < nt && ok; ++j) {
       const int s = j % MST, b = j & 1, rho = (q_lo + j) * TR;
-      if (!wait_warp(&B.s_full[w][b], (uint32_t)((j / 2) & 1), abort)) { ok = false; break; }
+      if (!wait_warp(&B.s_full[b], (uint32_t)((j / 2) & 1), abort)) { ok = false; break; }
       tc::tc_fence_after();
       float sv[FA_ROWS];
-      tm_ld<FA_ROWS>(tl + 128u * b, sv);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tm_ld32(tl + 128u * b + 32 * q, sv + 32 * q);
       ld_wait();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive(&B.s_free[w][b]);
+      if (lane == 0) arrive(&B.s_free[b]);
       // columns of rows that see this key: from the row whose position it is
       const int cmin = p.a.causal ? max(0, pos - (r.L - r.c)) * p.G - rho : 0, cmax = min(TR, R - rho);
-      uint64_t sum2[2] = {0ull, 0ull};
       const float4* nl = reinterpret_cast<const float4*>(nlse[s]);
-      const bool whole = cmin <= 0 && cmax == FA_ROWS;
-      if (__all_sync(0xffffffffu, whole)) {
+      if (__all_sync(0xffffffffu, cmin <= 0 && cmax == FA_ROWS)) {
+        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int e = 0; e < FA_ROWS / 4; ++e) {
           const float4 n4 = nl[e];
-          float a0, a1, a2, a3;
-          unpack2(fma2(pack2(sv[4 * e], sv[4 * e + 1]), sl2, pack2(n4.x, n4.y)), a0, a1);
-          unpack2(fma2(pack2(sv[4 * e + 2], sv[4 * e + 3]), sl2, pack2(n4.z, n4.w)), a2, a3);
-          sum2[0] = add2(sum2[0], pack2(ex2(a0), ex2(a1)));
-          sum2[1] = add2(sum2[1], pack2(ex2(a2), ex2(a3)));
+          float2 a = __ffma2_rn(make_float2(sv[4 * e], sv[4 * e + 1]), sl2, make_float2(n4.x, n4.y));
+          float2 c = __ffma2_rn(make_float2(sv[4 * e + 2], sv[4 * e + 3]), sl2, make_float2(n4.z, n4.w));
+          a.x = ex2(a.x); a.y = ex2(a.y);
+          c.x = ex2(c.x); c.y = ex2(c.y);
+          sum2[0] = __fadd2_rn(sum2[0], a);
+          sum2[1] = __fadd2_rn(sum2[1], c);
         }
-        float a, c;
-        unpack2(add2(sum2[0], sum2[1]), a, c);
-        total += a + c;
+        total += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
       } else {
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -647,10 +629,11 @@ fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __gr
       if (lane == 0) arrive(&B.empty[s]);          // the tile's S is computed and its log-sum-exps are read
     }
     if (on) p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + pos] += ok ? total : NAN;
+    tc::tc_fence_before();
   }
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (warp == 1) tc::tmem_dealloc(tmem, 256);
 }
 
 }  // namespace
@@ -670,8 +653,7 @@ cudaError_t launch_fa(const AttnP& p, int row_tiles, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_fa_mass(const AttnP& p, int row_tiles, cudaStream_t s) {
-  (void)row_tiles;
+cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s) {
   TcMap mq, mk;
   if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
                        (uint32_t)(FA_ROWS / p.G)) ||
@@ -680,7 +662,7 @@ cudaError_t launch_fa_mass(const AttnP& p, int row_tiles, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(fa_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MASS_SMEM);
   if (e != cudaSuccess) return e;
   const int tiles = tile_count(p.geo, p.c.page_size, FA_KEYS, p.a.max_kv);
-  fa_mass_kernel<<<dim3((tiles + 1) / 2, p.c.n_kv_heads, p.a.n_req), THREADS, MASS_SMEM, s>>>(
+  fa_mass_kernel<<<dim3(tiles, p.c.n_kv_heads, p.a.n_req), MTHREADS, MASS_SMEM, s>>>(
       p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk));
   ws_count_launches(1);
   return cudaGetLastError();
