@@ -482,7 +482,13 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
   T* out = (T*)p.a.out + (size_t)(r.row0 + t) * p.a.out_stride + (size_t)u * WS_DH + 2 * lane;
   out[0] = from_f<T>(a0 * inv);
   out[1] = from_f<T>(a1 * inv);
-  if (p.lse && lane == 0) p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u] = sum == 0.f ? -INFINITY : (M + lg2(sum)) * LN2;
+  if (lane != 0) return;
+  const float x = sum == 0.f ? -INFINITY : M + lg2(sum);
+  if (p.lse) p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u] = x * LN2;
+  if (p.nl) {
+    const int TR = p.G * (FA_ROWS / p.G), rt = rho / TR;
+    p.nl[(((size_t)i * p.c.n_kv_heads + h) * p.row_tiles + rt) * FA_ROWS + rho - rt * TR] = x == -INFINITY ? x : -x;
+  }
 }
 
 // ------------------------------------------------------------------ bf16: accumulated weights
@@ -603,7 +609,7 @@ struct Plan {
   int row_tiles = 1, nsplit = 1, tps = 1;
   bool stash = false;                      // the streaming kernel adds the mass itself
   TileGeo geo;
-  size_t lse = 0, ml = 0, o = 0, bytes = 0;
+  size_t lse = 0, ml = 0, o = 0, nl = 0, bytes = 0;
 };
 constexpr int SMS = 152, SLOTS = 2 * SMS;  // two streaming CTAs on each of 152 SMs
 
@@ -611,14 +617,16 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   Plan q;
   const long long R = (long long)a.max_q * (a.n_heads / c.n_kv_heads);
   auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += (n + 255) / 256 * 256; return at; };
-  if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
   auto partials = [&](long long R_) {
     if (q.nsplit <= 1) return;
     const size_t rows = (size_t)a.n_req * c.n_kv_heads * R_ * q.nsplit;
     q.ml = take(rows * 8);
     q.o = take(rows * WS_DH * 4);
   };
-  if (c.dtype != WS_BF16) return q;
+  if (c.dtype != WS_BF16) {
+    if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
+    return q;
+  }
   const int G = a.n_heads / c.n_kv_heads;
   if (R > 32 && G <= FA_ROWS && a.scale > 0.f) {
     q.fa = true;
@@ -631,8 +639,10 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
     q.tps = (tiles + want - 1) / want;
     q.nsplit = (tiles + q.tps - 1) / q.tps;
     partials(R);
+    if (a.mass) q.nl = take((size_t)a.n_req * c.n_kv_heads * q.row_tiles * FA_ROWS * 4);
     return q;
   }
+  if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
   q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
   q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
   const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
@@ -667,7 +677,7 @@ cudaError_t run_streaming(const AttnP& p, const Plan& q, cudaStream_t s) {
 }
 
 cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
-  const cudaError_t e = q.fa ? launch_fa(p, q.row_tiles, s) : run_streaming(p, q, s);
+  const cudaError_t e = q.fa ? launch_fa(p, s) : run_streaming(p, q, s);
   if (e != cudaSuccess) return e;
   if (q.nsplit > 1) {
     combine_kernel<bf16><<<dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
@@ -716,7 +726,9 @@ extern "C" int ws_paged_attention(const ws_paged_cache* cache, const ws_attentio
   p.q_xor = args->scale < 0.f ? 0x80008000u : 0u;
   p.nsplit = q.nsplit; p.tps = q.tps; p.geo = q.geo;
   char* ws = (char*)workspace;
-  p.lse = args->lse ? args->lse : args->mass ? (float*)(ws + q.lse) : nullptr;
+  p.lse = args->lse ? args->lse : args->mass && !q.fa ? (float*)(ws + q.lse) : nullptr;
+  p.row_tiles = q.row_tiles;
+  if (q.fa && args->mass) p.nl = (float*)(ws + q.nl);
   if (q.nsplit > 1) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
   const cudaError_t e = cache->dtype == WS_BF16 ? run_bf16(p, q, (cudaStream_t)stream) : run_f32(p, (cudaStream_t)stream);
   if (e != cudaSuccess) return paged_fail(WS_ECUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));

@@ -43,6 +43,9 @@ struct AttnP {
   float2* part_ml;                         // split partials: (max in log2 units, sum) [unit row][nsplit] ...
   float* part_o;                           // ... and values [unit row][nsplit][64], unit row = (i * Hkv + h) * max_q * G + r * G + g
   float* lse;                              // [total_q][n_heads], or null
+  int row_tiles;                           // row tiles per (request, KV head)
+  float* nl;                               // tcgen05 path with mass: -lse * log2(e) of every row tile's rows
+                                           // [n_req][Hkv][row_tiles][128], 16-byte aligned; else null
 };
 
 struct Req {
@@ -88,5 +91,5 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // out / lse, those of split calls to the partials.
 constexpr int FA_ROWS = 128, FA_KEYS = 128;
 inline int fa_rows(int G) { return G * (FA_ROWS / G); }                        // G <= 128
-cudaError_t launch_fa(const AttnP& p, int row_tiles, cudaStream_t s);
+cudaError_t launch_fa(const AttnP& p, cudaStream_t s);
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s);

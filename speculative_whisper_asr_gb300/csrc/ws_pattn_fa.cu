@@ -168,7 +168,7 @@ struct Bars {
 };
 
 __global__ void __launch_bounds__(THREADS, 1)
-fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) Bars B;
@@ -176,7 +176,7 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
-  const int pairs = (row_tiles + 1) / 2;
+  const int pairs = (p.row_tiles + 1) / 2;
   const int pair = pairs - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
   const int h = blockIdx.y, i = blockIdx.z;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -457,6 +457,9 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
           reinterpret_cast<uint4*>(out + 16 * q)[1] = make_uint4(u[4], u[5], u[6], u[7]);
         }
       }
+      if (on && p.nl)
+        p.nl[(((size_t)i * p.c.n_kv_heads + h) * p.row_tiles + pair * 2 + w) * FA_ROWS + x] =
+            !ok ? NAN : l == 0.f ? -INFINITY : -(msl + lg2(l));
       if (on && p.lse)
         p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u_] = !ok ? NAN : l == 0.f ? -INFINITY : (msl + lg2(l)) * LN2;
     }
@@ -468,39 +471,42 @@ fa_kernel(const AttnP p, int row_tiles, const __grid_constant__ CUtensorMap mq, 
 }
 
 // ------------------------------------------------------------------ accumulated weights
-// One key tile per CTA and two CTAs per SM (256 tensor memory columns each:
-// S twice), so that one CTA's start and end lie under the other's work.
+// Work items are key tiles of (request, KV head); a CTA takes every
+// gridDim-th, two CTAs per SM (256 tensor memory columns each: S twice).  The
+// producer runs up to MST row tiles ahead, across items, so that the next
+// item's lengths, pages and keys arrive under the current one's sums: a CTA
+// per item spent a third of its time on its first tile.
 constexpr int MST = 4;                             // row tile stages
 constexpr int MTHREADS = 192;                      // producer, MMA, four summing warps
-constexpr int MASS_SMEM = TILE + MST * TILE + 1024;
+constexpr int MASS_SMEM = 2 * TILE + MST * TILE + 1024;
 
-struct MassBars { uint64_t k_full, q_full[MST], empty[MST], s_full[2], s_free[2]; };
+struct MassItem {
+  uint32_t valid[4];
+  int base, nt;                                    // first position; row tiles (-1: no more items)
+  int q_lo, R, c, L;                               // first row tile; rows, chunk length, cache length
+  float* mass;
+};
+struct MassBars { uint64_t k_full[2], k_empty[2], q_full[MST], empty[MST], s_full[2], s_free[2]; };
 
 __global__ void __launch_bounds__(MTHREADS, 2)
-fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
+fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant__ CUtensorMap mq,
+               const __grid_constant__ CUtensorMap mk) {
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) MassBars B;
-  __shared__ Meta meta;
+  __shared__ MassItem item[2];
   __shared__ __align__(16) float nlse[MST][FA_ROWS];   // -lse * log2(e) of a tile's rows
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
-  const int h = blockIdx.y, i = blockIdx.z, kt = blockIdx.x;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const Req r = request(p, i);
-  const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
-  const int nk = tile_count(p.geo, p.c.page_size, FA_KEYS, r.L);
-  if (kt >= nk || R == 0) return;
-  const int nq = (R + TR - 1) / TR;
-  const int base0 = p.geo.tpp ? kt / p.geo.tpp * p.c.page_size + kt % p.geo.tpp * FA_KEYS : kt * FA_KEYS;
-  // row tiles before the first row that sees position base0 add nothing
-  const int q_lo = p.a.causal ? max(0, base0 - (r.L - r.c)) / RB : 0;
-  const int nt = max(0, nq - q_lo);
+  const int RB = FA_ROWS / p.G, TR = RB * p.G;
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
-    tc::mbar_init(&B.k_full, 1);
     for (int b = 0; b < MST; ++b) { tc::mbar_init(&B.q_full[b], 1); tc::mbar_init(&B.empty[b], 4); }
-    for (int b = 0; b < 2; ++b) { tc::mbar_init(&B.s_full[b], 1); tc::mbar_init(&B.s_free[b], 4); }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&B.k_full[b], 1); tc::mbar_init(&B.k_empty[b], 4);
+      tc::mbar_init(&B.s_full[b], 1); tc::mbar_init(&B.s_free[b], 4);
+    }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -509,126 +515,161 @@ fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __gr
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-  uint8_t* sK = sm;
-  auto sQ = [&](int b) { return sm + TILE + b * TILE; };
+  auto sK = [&](int b) { return sm + b * TILE; };
+  auto sQ = [&](int b) { return sm + 2 * TILE + b * TILE; };
 
   if (warp == 0) {
-    // ---- producer: the key tile, then the row tiles with their
-    // log-sum-exps, which are asked for one tile ahead
-    const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
-    const TileInfo f = tile_info(p, kt, tile_page(p, table, kt, lane), r.L, lane);
-    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, f.page >= 0)) * (uint32_t)p.geo.box * 128u;
-    if (lane == 0) {
+    // ---- producer: key tiles, and row tiles with their log-sum-exps
+    int n = 0, g = 0;                              // items and row tiles handed over
+    long long it = blockIdx.x;
+    auto where = [&](long long x, int& kt, int& h, int& i) {
+      const long long u = x / tiles;
+      kt = (int)(x - u * tiles); i = (int)(u / p.c.n_kv_heads); h = (int)(u - (long long)i * p.c.n_kv_heads);
+    };
+    bool ok = true;
+    int kt = 0, h = 0, i = 0;
+    Req r = {};
+    if (it < items) { where(it, kt, h, i); r = request(p, i); }
+    while (it < items && ok) {
+      // the next item's lengths are asked for now
+      const long long it2 = it + gridDim.x;
+      int kt2 = 0, h2 = 0, i2 = 0;
+      Req r2 = {};
+      if (it2 < items) { where(it2, kt2, h2, i2); r2 = request(p, i2); }
+      const int R = r.c * p.G, nq = (R + TR - 1) / TR;
+      const int base0 = p.geo.tpp ? kt / p.geo.tpp * p.c.page_size + kt % p.geo.tpp * FA_KEYS : kt * FA_KEYS;
+      // row tiles before the first row that sees position base0 add nothing
+      const int q_lo = p.a.causal ? max(0, base0 - (r.L - r.c)) / RB : 0;
+      const int nt = kt < tile_count(p.geo, p.c.page_size, FA_KEYS, r.L) ? max(0, nq - q_lo) : 0;
+      if (nt > 0) {
+        const int kb = n & 1;
+        const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
+        const TileInfo f = tile_info(p, kt, tile_page(p, table, kt, lane), r.L, lane);
+        const float* nl = p.nl + ((size_t)i * p.c.n_kv_heads + h) * p.row_tiles * FA_ROWS;
+        if (n >= 2 && !wait_warp(&B.k_empty[kb], (uint32_t)((n / 2 - 1) & 1), abort)) { ok = false; break; }
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, f.page >= 0)) * (uint32_t)p.geo.box * 128u;
+        if (lane == 0) {
+          MassItem& m = item[kb];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) meta.valid[q] = f.valid[q];
-      meta.base = f.base;
-      tc::mbar_expect_tx(&B.k_full, bytes);
-    }
-    __syncwarp();
-    if (f.page >= 0) tma_load_4d(sK + f.dst, &mk, &B.k_full, 0, f.tok, h, f.page);
-    float v[4];
-    auto ask = [&](int j) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int x = 32 * q + lane, rho = (q_lo + j) * TR + x;
-        v[q] = -INFINITY;
-        if (j < nt && x < TR && rho < R) {
-          const int t = rho / p.G;
-          v[q] = p.lse[(size_t)(r.row0 + t) * p.a.n_heads + h * p.G + rho - t * p.G];
+          for (int q = 0; q < 4; ++q) m.valid[q] = f.valid[q];
+          m.base = f.base; m.nt = nt; m.q_lo = q_lo; m.R = R; m.c = r.c; m.L = r.L;
+          m.mass = p.a.mass + ((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride;
+          tc::mbar_expect_tx(&B.k_full[kb], bytes);
+        }
+        __syncwarp();
+        if (f.page >= 0) tma_load_4d(sK(kb) + f.dst, &mk, &B.k_full[kb], 0, f.tok, h, f.page);
+        ++n;
+        for (int j = 0; j < nt; ++j, ++g) {
+          const int s = g % MST;
+          if (g >= MST && !wait_warp(&B.empty[s], (uint32_t)((g / MST - 1) & 1), abort)) { ok = false; break; }
+          if (lane == 0) {
+            tc::mbar_expect_tx(&B.q_full[s], (uint32_t)TR * 128u + FA_ROWS * 4u);
+            tma_load_3d(sQ(s), &mq, &B.q_full[s], 0, h * p.G, r.row0 + (q_lo + j) * RB);
+            tc::bulk_g2s(nlse[s], nl + (size_t)(q_lo + j) * FA_ROWS, FA_ROWS * 4, &B.q_full[s]);
+          }
         }
       }
-    };
-    ask(0);
-    int issued = 0;
-    for (int j = 0; j < nt; ++j) {
-      const int s = j % MST;
-      if (j >= MST && !wait_warp(&B.empty[s], (uint32_t)((j / MST - 1) & 1), abort)) break;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) nlse[s][32 * q + lane] = v[q] == -INFINITY ? -INFINITY : -v[q] * LOG2E;
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_expect_tx(&B.q_full[s], (uint32_t)TR * 128u);
-        tma_load_3d(sQ(s), &mq, &B.q_full[s], 0, h * p.G, r.row0 + (q_lo + j) * RB);
-      }
-      ++issued;
-      ask(j + 1);
+      it = it2; kt = kt2; h = h2; i = i2; r = r2;
     }
-    if (*abort && lane == 0) {
-      tc::mbar_wait(&B.k_full, 0);
-      for (int j = max(0, issued - MST); j < issued; ++j) tc::mbar_wait(&B.q_full[j % MST], (uint32_t)((j / MST) & 1));
+    if (ok && (n < 2 || wait_warp(&B.k_empty[n & 1], (uint32_t)((n / 2 - 1) & 1), abort)) && lane == 0) {
+      item[n & 1].nt = -1;
+      arrive(&B.k_full[n & 1]);
+    }
+    if (*abort && lane == 0) {                     // see the copies in flight land
+      for (int x = max(0, n - 2); x < n; ++x) tc::mbar_wait(&B.k_full[x & 1], (uint32_t)((x / 2) & 1));
+      for (int x = max(0, g - MST); x < g; ++x) tc::mbar_wait(&B.q_full[x % MST], (uint32_t)((x / MST) & 1));
     }
   } else if (warp == 1) {
     const uint32_t lead = elect_one();
-    const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sK)), qd0 = tc::sdesc_sw128(tc::smem_u32(sQ(0)));
-    bool ok = wait(&B.k_full, 0, abort);
-    int done = 0;
-    for (int j = 0; j < nt && ok; ++j) {
-      const int s = j % MST, b = j & 1;
-      if (!wait(&B.q_full[s], (uint32_t)((j / MST) & 1), abort)) break;
-      if (j >= 2 && !wait(&B.s_free[b], (uint32_t)((j / 2 - 1) & 1), abort)) break;
-      tc::tc_fence_after();
-      if (lead) {
-        const uint64_t qd = qd0 + (uint64_t)(s * (TILE >> 4));
+    const uint64_t kd0 = tc::sdesc_sw128(tc::smem_u32(sK(0))), qd0 = tc::sdesc_sw128(tc::smem_u32(sQ(0)));
+    int g = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int kb = n & 1;
+      if (!wait(&B.k_full[kb], (uint32_t)((n / 2) & 1), abort)) break;
+      const int nt = item[kb].nt;
+      if (nt < 0) break;
+      for (int j = 0; j < nt; ++j) {
+        const int s = g % MST, b = g & 1;
+        ok = wait(&B.q_full[s], (uint32_t)((g / MST) & 1), abort) &&
+             (g < 2 || wait(&B.s_free[b], (uint32_t)((g / 2 - 1) & 1), abort));
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (lead) {
+          const uint64_t kd = kd0 + (uint64_t)(kb * (TILE >> 4)), qd = qd0 + (uint64_t)(s * (TILE >> 4));
 #pragma unroll
-        for (int kk = 0; kk < WS_DH / 16; ++kk)
-          tc::umma_bf16(tmem + 128u * b, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), IDESC_S, kk ? 1u : 0u);
-        tc::umma_commit(&B.s_full[b]);
+          for (int kk = 0; kk < WS_DH / 16; ++kk)
+            tc::umma_bf16(tmem + 128u * b, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), IDESC_S, kk ? 1u : 0u);
+          tc::umma_commit(&B.s_full[b]);
+        }
+        __syncwarp();
+        ++g;
       }
-      __syncwarp();
-      ++done;
     }
     if (*abort && lane == 0)
-      for (int j = max(0, done - 2); j < done; ++j) tc::mbar_wait(&B.s_full[j & 1], (uint32_t)((j / 2) & 1));
+      for (int x = max(0, g - 2); x < g; ++x) tc::mbar_wait(&B.s_full[x & 1], (uint32_t)((x / 2) & 1));
     __syncwarp();
   } else {
     // ---- sums: thread = key
     const int quarter = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    bool ok = wait_warp(&B.k_full, 0, abort);
-    const int pos = meta.base + quarter * 32 + lane;
-    const bool on = (meta.valid[quarter] >> lane) & 1u;
     const float2 sl2 = make_float2(p.sl, p.sl);
-    float total = 0.f;
-    for (int j = 0; j < nt && ok; ++j) {
-      const int s = j % MST, b = j & 1, rho = (q_lo + j) * TR;
-      if (!wait_warp(&B.s_full[b], (uint32_t)((j / 2) & 1), abort)) { ok = false; break; }
-      tc::tc_fence_after();
-      float sv[FA_ROWS];
+    bool ok = true;
+    int g = 0;
+    for (int n = 0; ok; ++n) {
+      const int kb = n & 1;
+      if (!wait_warp(&B.k_full[kb], (uint32_t)((n / 2) & 1), abort)) break;
+      const MassItem& m = item[kb];
+      const int nt = m.nt;
+      if (nt < 0) break;
+      const int pos = m.base + quarter * 32 + lane, R = m.R, q_lo = m.q_lo;
+      const int first = p.a.causal ? max(0, pos - (m.L - m.c)) * p.G : 0;      // first row that sees this key
+      float* mass = m.mass + pos;
+      const bool on = (m.valid[quarter] >> lane) & 1u;
+      float total = 0.f;
+      for (int j = 0; j < nt; ++j, ++g) {
+        const int s = g % MST, b = g & 1, rho = (q_lo + j) * TR;
+        if (!wait_warp(&B.s_full[b], (uint32_t)((g / 2) & 1), abort)) { ok = false; break; }
+        tc::tc_fence_after();
+        float sv[FA_ROWS];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tm_ld32(tl + 128u * b + 32 * q, sv + 32 * q);
-      ld_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(&B.s_free[b]);
-      // columns of rows that see this key: from the row whose position it is
-      const int cmin = p.a.causal ? max(0, pos - (r.L - r.c)) * p.G - rho : 0, cmax = min(TR, R - rho);
-      const float4* nl = reinterpret_cast<const float4*>(nlse[s]);
-      if (__all_sync(0xffffffffu, cmin <= 0 && cmax == FA_ROWS)) {
-        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int q = 0; q < 4; ++q) tm_ld32(tl + 128u * b + 32 * q, sv + 32 * q);
+        ld_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(&B.s_free[b]);
+        const int cmin = first - rho, cmax = min(TR, R - rho);                 // columns that see this key
+        const float4* nl = reinterpret_cast<const float4*>(nlse[s]);
+        if (__all_sync(0xffffffffu, cmin <= 0 && cmax == FA_ROWS)) {
+          float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < FA_ROWS / 4; ++e) {
-          const float4 n4 = nl[e];
-          float2 a = __ffma2_rn(make_float2(sv[4 * e], sv[4 * e + 1]), sl2, make_float2(n4.x, n4.y));
-          float2 c = __ffma2_rn(make_float2(sv[4 * e + 2], sv[4 * e + 3]), sl2, make_float2(n4.z, n4.w));
-          a.x = ex2(a.x); a.y = ex2(a.y);
-          c.x = ex2(c.x); c.y = ex2(c.y);
-          sum2[0] = __fadd2_rn(sum2[0], a);
-          sum2[1] = __fadd2_rn(sum2[1], c);
+          for (int e = 0; e < FA_ROWS / 4; ++e) {
+            const float4 n4 = nl[e];
+            float2 a = __ffma2_rn(make_float2(sv[4 * e], sv[4 * e + 1]), sl2, make_float2(n4.x, n4.y));
+            float2 c = __ffma2_rn(make_float2(sv[4 * e + 2], sv[4 * e + 3]), sl2, make_float2(n4.z, n4.w));
+            a.x = ex2(a.x); a.y = ex2(a.y);
+            c.x = ex2(c.x); c.y = ex2(c.y);
+            sum2[0] = __fadd2_rn(sum2[0], a);
+            sum2[1] = __fadd2_rn(sum2[1], c);
+          }
+          total += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+        } else {
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < FA_ROWS; ++e) {
+            const float y = ex2(fmaf(sv[e], p.sl, nlse[s][e]));
+            if (e >= cmin && e < cmax && nlse[s][e] > -INFINITY) part[e & 3] += y;
+          }
+          total += (part[0] + part[1]) + (part[2] + part[3]);
         }
-        total += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-      } else {
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < FA_ROWS; ++e) {
-          const float y = ex2(fmaf(sv[e], p.sl, nlse[s][e]));
-          if (e >= cmin && e < cmax && nlse[s][e] > -INFINITY) part[e & 3] += y;
-        }
-        total += (part[0] + part[1]) + (part[2] + part[3]);
+        __syncwarp();
+        if (lane == 0) arrive(&B.empty[s]);        // the tile's S is computed and its log-sum-exps are read
       }
       __syncwarp();
-      if (lane == 0) arrive(&B.empty[s]);          // the tile's S is computed and its log-sum-exps are read
+      if (lane == 0) arrive(&B.k_empty[kb]);       // the item's keys and description are read
+      // the position is this thread's alone: the atomic has nothing to race with
+      if (on) atomicAdd(mass, ok ? total : NAN);
     }
-    if (on) p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + pos] += ok ? total : NAN;
     tc::tc_fence_before();
   }
   __syncthreads();
@@ -638,7 +679,7 @@ fa_mass_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __gr
 
 }  // namespace
 
-cudaError_t launch_fa(const AttnP& p, int row_tiles, cudaStream_t s) {
+cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
   TcMap mq, mk, mv;
   if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
                        (uint32_t)(FA_ROWS / p.G)) ||
@@ -646,8 +687,8 @@ cudaError_t launch_fa(const AttnP& p, int row_tiles, cudaStream_t s) {
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(fa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FA_SMEM);
   if (e != cudaSuccess) return e;
-  fa_kernel<<<dim3((row_tiles + 1) / 2 * p.nsplit, p.c.n_kv_heads, p.a.n_req), THREADS, FA_SMEM, s>>>(
-      p, row_tiles, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
+  fa_kernel<<<dim3((p.row_tiles + 1) / 2 * p.nsplit, p.c.n_kv_heads, p.a.n_req), THREADS, FA_SMEM, s>>>(
+      p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
       reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
   return cudaGetLastError();
@@ -662,8 +703,10 @@ cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(fa_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MASS_SMEM);
   if (e != cudaSuccess) return e;
   const int tiles = tile_count(p.geo, p.c.page_size, FA_KEYS, p.a.max_kv);
-  fa_mass_kernel<<<dim3(tiles, p.c.n_kv_heads, p.a.n_req), MTHREADS, MASS_SMEM, s>>>(
-      p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk));
+  const long long items = (long long)tiles * p.c.n_kv_heads * p.a.n_req;
+  if (items == 0) return cudaSuccess;
+  fa_mass_kernel<<<(unsigned)(items < 2 * 152 ? items : 2 * 152), MTHREADS, MASS_SMEM, s>>>(
+      p, tiles, items, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk));
   ws_count_launches(1);
   return cudaGetLastError();
 }
