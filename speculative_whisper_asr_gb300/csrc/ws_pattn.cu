@@ -5,64 +5,6 @@
 
 namespace {
 
-// ------------------------------------------------------------------ fp32
-// One warp per (row, query head), two dims per lane.
-template <typename T>
-__global__ void simple_attn(const AttnP p) {
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.y, u = blockIdx.z, t = warp;
-  const Req r = request(p, i);
-  if (t >= r.c) return;
-  const int row = r.row0 + t, lim = row_limit(p, r, t), h = u / p.G;
-  const T* q = (const T*)p.a.q + (size_t)row * p.a.q_stride + (size_t)u * WS_DH;
-  const float q0 = to_f(q[lane]), q1 = to_f(q[lane + 32]);
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int j = 0; j < lim; ++j) {
-    const int page = paged_page(p.c, p.c.page_table, p.c.table_stride, r.slot, j);
-    if (page < 0) continue;
-    const size_t off = paged_off(p.c, page, h, j);
-    const T *k = (const T*)p.c.k + off, *v = (const T*)p.c.v + off;
-    float s = q0 * to_f(k[lane]) + q1 * to_f(k[lane + 32]);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= p.a.scale;
-    const float mn = fmaxf(m, s), f = m == mn ? 1.f : expf(m - mn), e = s == mn ? 1.f : expf(s - mn);
-    l = l * f + e; o0 = o0 * f + e * to_f(v[lane]); o1 = o1 * f + e * to_f(v[lane + 32]);
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  T* out = (T*)p.a.out + (size_t)row * p.a.out_stride + (size_t)u * WS_DH;
-  out[lane] = from_f<T>(o0 * inv);
-  out[lane + 32] = from_f<T>(o1 * inv);
-  if (p.lse && lane == 0) p.lse[(size_t)row * p.a.n_heads + u] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
-// One warp per (slot, KV head, position): the weights of every row and head.
-template <typename T>
-__global__ void simple_mass(const AttnP p) {
-  const int j = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.y, h = blockIdx.z;
-  const Req r = request(p, i);
-  if (j >= r.L) return;
-  const int page = paged_page(p.c, p.c.page_table, p.c.table_stride, r.slot, j);
-  if (page < 0) return;
-  const T* k = (const T*)p.c.k + paged_off(p.c, page, h, j);
-  const float k0 = to_f(k[lane]), k1 = to_f(k[lane + 32]);
-  float sum = 0.f;
-  for (int t = 0; t < r.c; ++t) {
-    if (j >= row_limit(p, r, t)) continue;
-    for (int g = 0; g < p.G; ++g) {
-      const int u = h * p.G + g;
-      const T* q = (const T*)p.a.q + (size_t)(r.row0 + t) * p.a.q_stride + (size_t)u * WS_DH;
-      float s = to_f(q[lane]) * k0 + to_f(q[lane + 32]) * k1;
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-      sum += expf(s * p.a.scale - p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u]);
-    }
-  }
-  if (lane == 0) p.a.mass[((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride + j] += sum;
-}
-
 // ------------------------------------------------------------------ bf16, few rows: stream the cache once
 // The rows of a (request, KV head) — chunk rows x the query heads that share
 // the KV head — are cut into row tiles of 8 * NT.  One CTA takes a row tile
@@ -604,6 +546,7 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
 
 // The launch shape and the workspace of a call: a function of the host sizes.
 struct Plan {
+  bool wide = false;                       // fp32: row tiles of 64 rows, not 16
   bool fa = false;                         // tcgen05 row tiles instead of streaming ones
   int nt = 1;                              // streaming row tile: 8 * nt rows
   int row_tiles = 1, nsplit = 1, tps = 1;
@@ -625,6 +568,15 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   };
   if (c.dtype != WS_BF16) {
     if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
+    q.wide = R > 16;
+    q.row_tiles = (int)((R + (q.wide ? 63 : 15)) / (q.wide ? 64 : 16));
+    const int tiles = max(1, (a.max_kv + F32_KEYS - 1) / F32_KEYS);
+    const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
+    // enough CTAs for two rounds of two per SM
+    const int want = (int)min((2ll * SLOTS + units - 1) / units, (long long)tiles);
+    q.tps = (tiles + want - 1) / want;
+    q.nsplit = (tiles + q.tps - 1) / q.tps;
+    partials(R);
     return q;
   }
   const int G = a.n_heads / c.n_kv_heads;
@@ -690,14 +642,15 @@ cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t run_f32(const AttnP& p, cudaStream_t s) {
-  simple_attn<float><<<dim3((p.a.max_q + 3) / 4, p.a.n_req, p.a.n_heads), 128, 0, s>>>(p);
-  ws_count_launches(1);
-  if (p.a.mass && p.a.max_kv > 0) {
-    simple_mass<float><<<dim3((p.a.max_kv + 3) / 4, p.a.n_req, p.c.n_kv_heads), 128, 0, s>>>(p);
+cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
+  const cudaError_t e = launch_f32(p, q.wide, s);
+  if (e != cudaSuccess) return e;
+  if (q.nsplit > 1) {
+    combine_kernel<float><<<dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
     ws_count_launches(1);
   }
-  return cudaGetLastError();
+  if (!p.a.mass || p.a.max_kv == 0) return cudaGetLastError();
+  return launch_f32_mass(p, q.wide, s);
 }
 
 }  // namespace
@@ -730,7 +683,7 @@ extern "C" int ws_paged_attention(const ws_paged_cache* cache, const ws_attentio
   p.row_tiles = q.row_tiles;
   if (q.fa && args->mass) p.nl = (float*)(ws + q.nl);
   if (q.nsplit > 1) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
-  const cudaError_t e = cache->dtype == WS_BF16 ? run_bf16(p, q, (cudaStream_t)stream) : run_f32(p, (cudaStream_t)stream);
+  const cudaError_t e = cache->dtype == WS_BF16 ? run_bf16(p, q, (cudaStream_t)stream) : run_f32(p, q, (cudaStream_t)stream);
   if (e != cudaSuccess) return paged_fail(WS_ECUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
   return WS_OK;
 }

@@ -93,3 +93,9 @@ constexpr int FA_ROWS = 128, FA_KEYS = 128;
 inline int fa_rows(int G) { return G * (FA_ROWS / G); }                        // G <= 128
 cudaError_t launch_fa(const AttnP& p, cudaStream_t s);
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s);
+
+// The fp32 model (ws_pattn_f32.cu): row tiles of 64 rows (wide) or 16, key
+// tiles of F32_KEYS positions.
+constexpr int F32_KEYS = 64;
+cudaError_t launch_f32(const AttnP& p, bool wide, cudaStream_t s);
+cudaError_t launch_f32_mass(const AttnP& p, bool wide, cudaStream_t s);

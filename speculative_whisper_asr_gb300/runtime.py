@@ -465,17 +465,16 @@ def _check_tensor(name, t, dtype, ndim, device, dense=True):
 
 def _rows(name, t, dtype, shape, device):
     """A contiguous device tensor of exactly this type and shape."""
-    if t.dtype is not dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is needed")
     return t.data_ptr()
 
 
 def _on(device):
-    """The stream handle of the current stream, with `device` the current device."""
-    s = torch.cuda.current_stream()
-    if s.device != device:
-        raise ValueError(f"the tensors are on {device}, the current stream is on {s.device}")
-    return s.cuda_stream
+    """The handle of the current stream; `device` has to be the current device."""
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the tensors are on {device}, the current device is {torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class PagedCache:
