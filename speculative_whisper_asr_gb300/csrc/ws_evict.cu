@@ -1,5 +1,18 @@
 // Eviction from a paged cache by accumulated attention weight
 // (ws_cache_evict in include/ws.h gives the rule).
+//
+// evict_select finds, per (request, KV head), the keep-th largest key by four
+// 8-bit histogram passes over keys held in shared memory, then writes the
+// kept positions in ascending order.  A cluster of up to 8 CTAs shares a
+// (request, head), so that few long caches still fill the machine: the
+// histograms and counts meet through distributed shared memory.  All counts
+// are integers, so their order does not matter.
+//
+// evict_move copies the kept rows.  Its floor is HBM: every kept key and value
+// is read and written once.  To fresh pages, all rows move at once.  In
+// place, a destination is never behind its source, so a CTA goes through the
+// rows in order, a batch read before the batch is written; the parallelism
+// comes from cutting the rows into 32-byte columns, which never mix.
 #include "ws_paged.cuh"
 
 namespace {
@@ -9,12 +22,14 @@ struct EvictP {
   ws_evict_args a;
   const int32_t* tout;
   int tout_stride;
-  int in_place;
   int32_t* idx;                            // [n_req][heads][keep] kept positions, ascending
   int32_t* len;                            // [n_req] kv_len before the call
+  int cs;                                  // CTAs per (request, head) in evict_select
+  int cached;                              // keys kept in shared memory per CTA (0: read again each pass)
+  int ordered;                             // masses or labels move in place: one CTA takes a slot and head's in order
 };
 
-constexpr int NT = 1024;
+constexpr int MAX_CS = 8;
 
 // Order of a position: protected first, then the mass as an unsigned integer
 // (masses are >= 0 here, so their bits are ordered).
@@ -23,122 +38,268 @@ __device__ __forceinline__ uint32_t evict_key(const EvictP& p, const float* mass
   return __float_as_uint(fmaxf(mass[j], 0.f)) & 0x7FFFFFFFu;
 }
 
-// One CTA per (request, head): the kept positions.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int remote_int(const int* local, uint32_t rank) {
+  uint32_t addr;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// grid (cs, heads, requests), cluster (cs, 1, 1)
+template <int NT>
 __global__ void __launch_bounds__(NT) evict_select(const EvictP p) {
-  __shared__ int hist[256];
-  __shared__ int s_warp[NT / 32];
-  __shared__ int s_prefix, s_need;
-  const int i = blockIdx.x, h = blockIdx.y, H = p.c.n_kv_heads;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[2][256];
+  __shared__ int counts[2];                // keys of this CTA above the threshold, and equal to it
+  __shared__ int wgt[NT / 32], weq[NT / 32];
+  __shared__ int s_bin, s_left;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int i = blockIdx.z, h = blockIdx.y, H = p.c.n_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cs = p.cs;
+  const uint32_t rank = cs > 1 ? cluster_rank() : 0u;
   const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
   int L = 0;
   if (slot >= 0 && slot < p.c.n_slots)
     L = (int)min((long long)min(max(p.a.kv_len[slot], 0), p.a.max_kv), (long long)p.c.table_stride * p.c.page_size);
-  if (h == 0 && tid == 0) p.len[i] = L;
+  if (h == 0 && rank == 0 && tid == 0) p.len[i] = L;
   const int keep = min(L, p.a.keep);
   int32_t* idx = p.idx + ((size_t)i * H + h) * p.a.keep;
-  if (keep == L) {
-    for (int j = tid; j < L; j += NT) idx[j] = j;
+  if (keep == L) {                         // the whole cluster leaves
+    for (int j = rank * NT + tid; j < L; j += cs * NT) idx[j] = j;
     return;
   }
   const float* mass = p.a.mass + ((size_t)slot * H + h) * p.a.mass_stride;
-  // the keep-th largest key, 8 bits at a time
+  // this CTA's positions, and each warp's part of them (whole steps of 32)
+  const int seg = (L + cs - 1) / cs, lo = min(L, (int)rank * seg), hi = min(L, lo + seg), n = hi - lo;
+  const bool cached = p.cached > 0;
+  auto key = [&](int x) { return cached ? keys[x] : evict_key(p, mass, L, lo + x); };
+  if (cached)
+    for (int x = tid; x < n; x += NT) keys[x] = evict_key(p, mass, L, lo + x);
+  for (int b = tid; b < 512; b += NT) hist[b >> 8][b & 255] = 0;
+  __syncthreads();
+  // ---- the keep-th largest key, 8 bits at a time
   uint32_t prefix = 0;
   int need = keep;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int b = tid; b < 256; b += NT) hist[b] = 0;
-    __syncthreads();
-    for (int j = tid; j < L; j += NT) {
-      const uint32_t k = evict_key(p, mass, L, j);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass, buf = pass & 1;
+    for (int x = tid; x < n; x += NT) {
+      const uint32_t k = key(x);
+      if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[buf][(k >> shift) & 255], 1);
     }
-    __syncthreads();
-    if (tid == 0) {
-      int b = 255, left = need;
-      for (; b > 0 && hist[b] < left; --b) left -= hist[b];
-      s_prefix = (int)(prefix | ((uint32_t)b << shift));
-      s_need = left;
+    if (cs > 1) cluster_sync(); else __syncthreads();
+    // warp 0 takes the bins from the top: lane x bins 255 - 8 x .. 248 - 8 x
+    if (warp == 0) {
+      int c[8], sum = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int* at = &hist[buf][255 - 8 * lane - q];
+        c[q] = 0;
+        if (cs > 1)
+          for (int r = 0; r < cs; ++r) c[q] += remote_int(at, (uint32_t)r);
+        else
+          c[q] = *at;
+        sum += c[q];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += o;
+      }
+      int before = incl - sum;
+      if (before < need && incl >= need) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (before < need && before + c[q] >= need) { s_bin = 255 - 8 * lane - q; s_left = need - before; }
+          before += c[q];
+        }
+      }
     }
+    for (int b = tid; b < 256; b += NT) hist[buf ^ 1][b] = 0;   // read by nobody since the last barrier
     __syncthreads();
-    prefix = (uint32_t)s_prefix;
-    need = s_need;
+    prefix |= (uint32_t)s_bin << shift;
+    need = s_left;
+    if (cs > 1) cluster_sync(); else __syncthreads();           // the histograms are read everywhere
+  }
+  // ---- keys above the threshold, and the first `need` that equal it, in order
+  const int wlen = (((n + NT / 32 - 1) / (NT / 32)) + 31) & ~31;
+  const int wb = min(n, warp * wlen), we = min(n, wb + wlen);
+  int gt = 0, eq = 0;
+  for (int x = wb + lane; x < we; x += 32) {
+    const uint32_t k = key(x);
+    gt += k > prefix;
+    eq += k == prefix;
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    gt += __shfl_xor_sync(0xffffffffu, gt, s);
+    eq += __shfl_xor_sync(0xffffffffu, eq, s);
+  }
+  if (lane == 0) { wgt[warp] = gt; weq[warp] = eq; }
+  __syncthreads();
+  if (tid == 0) {
+    int a = 0, b = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+      const int x = wgt[w], y = weq[w];
+      wgt[w] = a; weq[w] = b;
+      a += x; b += y;
+    }
+    counts[0] = a; counts[1] = b;
+  }
+  int g0 = 0, e0 = 0;                      // in the CTAs before this one
+  if (cs > 1) {
+    cluster_sync();
+    for (int r = 0; r < (int)rank; ++r) { g0 += remote_int(&counts[0], (uint32_t)r); e0 += remote_int(&counts[1], (uint32_t)r); }
+    cluster_sync();                        // nobody leaves while its counts are read
+  } else {
     __syncthreads();
   }
-  // positions above the threshold, and the first `need` that equal it
-  int base = 0, eq_base = 0;
-  for (int j0 = 0; j0 < L; j0 += NT) {
-    const int j = j0 + tid;
-    const uint32_t k = j < L ? evict_key(p, mass, L, j) : 0u;
-    const bool eq = j < L && k == prefix;
-    const unsigned be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_warp[warp] = __popc(be);
-    __syncthreads();
-    int before = eq_base, all = 0;
-    for (int w = 0; w < NT / 32; ++w) { if (w < warp) before += s_warp[w]; all += s_warp[w]; }
-    before += __popc(be & ((1u << lane) - 1u));
-    eq_base += all;
-    __syncthreads();
-    const bool on = j < L && (k > prefix || (eq && before < need));
-    const unsigned bo = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) s_warp[warp] = __popc(bo);
-    __syncthreads();
-    int at = base;
-    all = 0;
-    for (int w = 0; w < NT / 32; ++w) { if (w < warp) at += s_warp[w]; all += s_warp[w]; }
-    at += __popc(bo & ((1u << lane) - 1u));
-    if (on) idx[at] = j;
-    base += all;
-    __syncthreads();
+  g0 += wgt[warp];
+  e0 += weq[warp];
+  for (int x0 = wb; x0 < we; x0 += 32) {
+    const int x = x0 + lane;
+    const uint32_t k = x < we ? key(x) : 0u;
+    const bool is_eq = x < we && k == prefix, is_gt = x < we && k > prefix;
+    const unsigned be = __ballot_sync(0xffffffffu, is_eq), bg = __ballot_sync(0xffffffffu, is_gt);
+    const unsigned below = (1u << lane) - 1u;
+    const int e = e0 + __popc(be & below);
+    // kept before this one: all above the threshold, and the equal ones among the first `need`
+    if (is_gt || (is_eq && e < need)) idx[g0 + __popc(bg & below) + min(e, need)] = lo + x;
+    g0 += __popc(bg);
+    e0 += __popc(be);
   }
 }
 
-// One CTA per (request, head); in order, so that a place is read before
-// anything is written over it.
+// The row of a kept position in the source pages and its new row, as offsets
+// in 16-byte units (-1: a bad page, nothing moves).
+struct Move { long long src, dst; };
 template <typename T>
-__global__ void __launch_bounds__(NT) evict_move(const EvictP p) {
-  const int i = blockIdx.x, h = blockIdx.y, H = p.c.n_kv_heads;
-  const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
-  const int L = p.len[i], keep = min(L, p.a.keep);
-  if (slot < 0 || slot >= p.c.n_slots) return;
-  if (h == 0 && threadIdx.x == 0) p.a.kv_len_out[slot] = keep;
-  const int32_t* idx = p.idx + ((size_t)i * H + h) * p.a.keep;
+__device__ __forceinline__ Move move_of(const EvictP& p, int slot, int h, int src, int dst) {
+  const int ps = paged_page(p.c, p.c.page_table, p.c.table_stride, slot, src);
+  const int pd = paged_page(p.c, p.tout, p.tout_stride, slot, dst);
+  Move m;
+  m.src = m.dst = -1;
+  if (ps >= 0 && pd >= 0) {
+    m.src = (long long)(paged_off(p.c, ps, h, src) * sizeof(T) / 16);
+    m.dst = (long long)(paged_off(p.c, pd, h, dst) * sizeof(T) / 16);
+  }
+  return m;
+}
+
+// To fresh pages: one CTA per ROWS kept positions.
+constexpr int MV_NT = 256;
+template <typename T>
+__global__ void __launch_bounds__(MV_NT) evict_move(const EvictP p) {
   constexpr int V = WS_DH * sizeof(T) / 16;     // 16-byte pieces of a row
-  const int sub = threadIdx.x % V, r = threadIdx.x / V;
-  const float* mass = p.a.mass + ((size_t)slot * H + h) * p.a.mass_stride;
-  for (int j0 = 0; j0 < keep; j0 += NT / V) {
-    const int j = j0 + r;
-    const int src = j < keep ? idx[j] : 0;
-    const int ps = j < keep ? paged_page(p.c, p.c.page_table, p.c.table_stride, slot, src) : -1;
-    const int pd = j < keep ? paged_page(p.c, p.tout, p.tout_stride, slot, j) : -1;
-    uint4 k, v;
-    float m = 0.f;
-    int pos = 0;
-    const bool go = ps >= 0 && pd >= 0;
-    if (go) {
-      k = reinterpret_cast<const uint4*>((const T*)p.c.k + paged_off(p.c, ps, h, src))[sub];
-      v = reinterpret_cast<const uint4*>((const T*)p.c.v + paged_off(p.c, ps, h, src))[sub];
+  constexpr int U = 8;                          // copies in flight per thread
+  constexpr int ROWS = U * MV_NT / (2 * V);
+  __shared__ Move mv[ROWS];
+  const int h = blockIdx.y, i = blockIdx.z, H = p.c.n_kv_heads, j0 = blockIdx.x * ROWS;
+  const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (slot < 0 || slot >= p.c.n_slots) return;
+  const int keep = min(p.len[i], p.a.keep), n = min(ROWS, keep - j0);
+  if (h == 0 && j0 == 0 && threadIdx.x == 0) p.a.kv_len_out[slot] = keep;
+  if (n <= 0) return;
+  const int32_t* idx = p.idx + ((size_t)i * H + h) * p.a.keep + j0;
+  const size_t unit = (size_t)slot * H + h;
+  if (p.ordered && j0 == 0)
+    for (int b = 0; b < keep; b += MV_NT) {
+      const int j = b + threadIdx.x, src = j < keep ? idx[j] : 0;
+      const float m = j < keep ? p.a.mass[unit * p.a.mass_stride + src] : 0.f;
+      const int q = j < keep && p.a.pos ? p.a.pos[unit * p.a.pos_stride + src] : src;
+      __syncthreads();                          // the batch is read before any of it is written
+      if (j < keep && p.a.mass_out) p.a.mass_out[unit * p.a.mass_out_stride + j] = m;
+      if (j < keep && p.a.pos_out) p.a.pos_out[unit * p.a.pos_out_stride + j] = q;
     }
-    if (j < keep && sub == 0) {
-      m = mass[src];
-      pos = p.a.pos ? p.a.pos[((size_t)slot * H + h) * p.a.pos_stride + src] : src;
+  for (int x = threadIdx.x; x < n; x += MV_NT) {
+    const int src = idx[x];
+    mv[x] = move_of<T>(p, slot, h, src, j0 + x);
+    if (p.ordered) continue;
+    if (p.a.mass_out) p.a.mass_out[unit * p.a.mass_out_stride + j0 + x] = p.a.mass[unit * p.a.mass_stride + src];
+    if (p.a.pos_out) p.a.pos_out[unit * p.a.pos_out_stride + j0 + x] = p.a.pos ? p.a.pos[unit * p.a.pos_stride + src] : src;
+  }
+  __syncthreads();
+  const uint4 *k = (const uint4*)p.c.k, *v = (const uint4*)p.c.v;
+  uint4 reg[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int x = u * MV_NT + threadIdx.x, row = x / (2 * V), piece = x % (2 * V);
+    if (row < n && mv[row].src >= 0) reg[u] = __ldcs((piece < V ? k : v) + mv[row].src + piece % V);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int x = u * MV_NT + threadIdx.x, row = x / (2 * V), piece = x % (2 * V);
+    if (row < n && mv[row].src >= 0) ((uint4*)(piece < V ? p.c.k : p.c.v))[mv[row].dst + piece % V] = reg[u];
+  }
+}
+
+// In place: one CTA per (request, head, keys or values, 32-byte column).
+template <typename T>
+__global__ void __launch_bounds__(MV_NT) evict_compact(const EvictP p) {
+  constexpr int COLS = WS_DH * sizeof(T) / 32, U = 4, STEP = MV_NT / 2 * U;
+  const int h = blockIdx.y, i = blockIdx.z, H = p.c.n_kv_heads;
+  const int col = blockIdx.x % COLS, which = blockIdx.x / COLS;
+  const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (slot < 0 || slot >= p.c.n_slots) return;
+  const int keep = min(p.len[i], p.a.keep);
+  if (h == 0 && blockIdx.x == 0 && threadIdx.x == 0) p.a.kv_len_out[slot] = keep;
+  const int32_t* idx = p.idx + ((size_t)i * H + h) * p.a.keep;
+  const size_t unit = (size_t)slot * H + h;
+  uint4* base = (uint4*)(which ? p.c.v : p.c.k) + 2 * col + (threadIdx.x & 1);
+  const int r = threadIdx.x >> 1;
+  const bool marks = blockIdx.x == 0 && (threadIdx.x & 1) == 0;     // this thread also moves the masses and labels
+  for (int j0 = 0; j0 < keep; j0 += STEP) {
+    uint4 reg[U];
+    long long dst[U];
+    float ms[U];
+    int ps[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * (MV_NT / 2) + r;
+      dst[u] = -1;
+      if (j < keep) {
+        const int src = idx[j];
+        if (src != j) {
+          const Move m = move_of<T>(p, slot, h, src, j);
+          if (m.src >= 0) { reg[u] = base[m.src]; dst[u] = m.dst; }
+        }
+        if (marks) {
+          ms[u] = p.a.mass[unit * p.a.mass_stride + src];
+          ps[u] = p.a.pos ? p.a.pos[unit * p.a.pos_stride + src] : src;
+        }
+      }
     }
-    __syncthreads();
-    if (go) {
-      reinterpret_cast<uint4*>((T*)p.c.k + paged_off(p.c, pd, h, j))[sub] = k;
-      reinterpret_cast<uint4*>((T*)p.c.v + paged_off(p.c, pd, h, j))[sub] = v;
+    __syncthreads();                            // the batch is read before any of it is written
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * (MV_NT / 2) + r;
+      if (dst[u] >= 0) base[dst[u]] = reg[u];
+      if (marks && j < keep) {
+        if (p.a.mass_out) p.a.mass_out[unit * p.a.mass_out_stride + j] = ms[u];
+        if (p.a.pos_out) p.a.pos_out[unit * p.a.pos_out_stride + j] = ps[u];
+      }
     }
-    if (j < keep && sub == 0) {
-      if (p.a.mass_out) p.a.mass_out[((size_t)slot * H + h) * p.a.mass_out_stride + j] = m;
-      if (p.a.pos_out) p.a.pos_out[((size_t)slot * H + h) * p.a.pos_out_stride + j] = pos;
-    }
-    __syncthreads();
+    // a later batch reads positions behind all of this one's destinations,
+    // and rows are read and written by the same columns' CTA alone
   }
 }
 
 const char* check_evict(const ws_paged_cache* c, const ws_evict_args* a) {
   if (const char* e = check_paged_cache(c)) return e;
   if (!a) return "null arguments";
-  if (a->n_req < 0) return "n_req must be >= 0";
+  if (a->n_req < 0 || a->n_req > 65535) return "n_req must be 0..65535";
+  if (a->max_kv > (1 << 30)) return "max_kv must be at most 2^30";
   if (a->max_kv < 1 || a->keep < 1 || a->keep > a->max_kv) return "keep must be 1..max_kv";
   if (a->sink < 0 || a->recent < 0 || (long long)a->sink + a->recent > a->keep)
     return "sink and recent must be >= 0 and sink + recent <= keep";
@@ -163,6 +324,49 @@ size_t evict_bytes(const ws_paged_cache* c, const ws_evict_args* a) {
   return (((size_t)a->n_req * 4 + 255) / 256 + ((size_t)a->n_req * c->n_kv_heads * a->keep * 4 + 255) / 256) * 256;
 }
 
+// CTAs per (request, head): enough to fill the machine, each with 1,024 keys
+// at least; the keys stay in shared memory where they fit.
+template <int NT>
+cudaError_t select(EvictP& p, cudaStream_t s) {
+  const long long units = (long long)p.a.n_req * p.c.n_kv_heads;
+  p.cs = 1;
+  while (p.cs < MAX_CS && units * p.cs < 304 && p.a.max_kv / (2 * p.cs) >= 1024) p.cs *= 2;
+  const int seg = (p.a.max_kv + p.cs - 1) / p.cs;
+  p.cached = seg <= 48 * 1024 ? seg : 0;
+  cudaError_t e = cudaFuncSetAttribute(evict_select<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(p.cs, p.c.n_kv_heads, p.a.n_req);
+  c.blockDim = dim3(NT);
+  c.dynamicSmemBytes = (size_t)p.cached * 4;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.cs; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, evict_select<NT>, (const EvictP)p);
+  if (e == cudaSuccess) ws_count_launches(1);
+  return e;
+}
+
+template <typename T>
+cudaError_t move(const EvictP& p, bool in_place, bool pdl, cudaStream_t s) {
+  constexpr int V = WS_DH * sizeof(T) / 16, ROWS = 8 * MV_NT / (2 * V);
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(in_place ? 2 * WS_DH * sizeof(T) / 32 : (p.a.keep + ROWS - 1) / ROWS, p.c.n_kv_heads, p.a.n_req);
+  c.blockDim = dim3(MV_NT);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = pdl ? 1 : 0;
+  const cudaError_t e = in_place ? cudaLaunchKernelEx(&c, evict_compact<T>, p) : cudaLaunchKernelEx(&c, evict_move<T>, p);
+  if (e == cudaSuccess) ws_count_launches(1);
+  return e;
+}
+
 }  // namespace
 
 extern "C" size_t ws_cache_evict_workspace(const ws_paged_cache* cache, const ws_evict_args* args) {
@@ -180,21 +384,21 @@ extern "C" int ws_cache_evict(const ws_paged_cache* cache, const ws_evict_args* 
     return paged_fail(WS_ENOSPACE, "workspace smaller than ws_cache_evict_workspace()");
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
-  EvictP p;
+  EvictP p = {};
   p.c = *cache;
   p.a = *args;
-  p.in_place = !args->page_table_out || args->page_table_out == cache->page_table;
-  p.tout = p.in_place ? cache->page_table : args->page_table_out;
-  p.tout_stride = p.in_place ? cache->table_stride : args->table_out_stride;
+  const bool in_place = !args->page_table_out || args->page_table_out == cache->page_table;
+  p.tout = in_place ? cache->page_table : args->page_table_out;
+  p.tout_stride = in_place ? cache->table_stride : args->table_out_stride;
   p.len = (int32_t*)workspace;
   p.idx = (int32_t*)((char*)workspace + ((size_t)args->n_req * 4 + 255) / 256 * 256);
-  cudaStream_t s = (cudaStream_t)stream;
-  const dim3 grid(args->n_req, cache->n_kv_heads);
-  evict_select<<<grid, NT, 0, s>>>(p);
-  if (cache->dtype == WS_BF16) evict_move<bf16><<<grid, NT, 0, s>>>(p);
-  else evict_move<float><<<grid, NT, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  p.ordered = args->mass_out == args->mass || (args->pos && args->pos_out == args->pos);
+  // programmatic dependent launch only on created streams, as elsewhere in the library
+  const bool pdl = stream != nullptr && (cudaStream_t)stream != cudaStreamLegacy && (cudaStream_t)stream != cudaStreamPerThread;
+  cudaError_t e = args->max_kv <= 4096 ? select<256>(p, (cudaStream_t)stream) : select<1024>(p, (cudaStream_t)stream);
+  if (e == cudaSuccess)
+    e = cache->dtype == WS_BF16 ? move<bf16>(p, in_place, pdl, (cudaStream_t)stream)
+                                : move<float>(p, in_place, pdl, (cudaStream_t)stream);
   if (e != cudaSuccess) return paged_fail(WS_ECUDA, std::string("cache eviction launch: ") + cudaGetErrorString(e));
-  ws_count_launches(2);
   return WS_OK;
 }

@@ -330,6 +330,35 @@ def test_evict_page_sizes_layouts_and_odd_masses(R, in_place, page, layout):
     _evict_case(R, [333, 200, 91], page, BF, 120, 3, 11, in_place=in_place, layout=layout, seed=page, odd=True)
 
 
+def test_evict_to_fresh_pages_with_masses_in_place(R):
+    """The rows go to other pages while the masses, labels and lengths are updated where they are."""
+    torch.manual_seed(3)
+    k = torch.randn(80, 2, 64, 64, device="cuda").to(BF)
+    table = torch.arange(40, dtype=torch.int32, device="cuda").reshape(2, 20).contiguous()
+    fresh = torch.arange(40, 80, dtype=torch.int32, device="cuda").reshape(2, 20).contiguous()
+    k0, mass = k.clone(), torch.rand(2, 2, 1280, device="cuda")
+    pos = torch.randint(0, 1 << 30, mass.shape, dtype=torch.int32, device="cuda")
+    m0, p0 = mass.clone(), pos.clone()
+    kv_len = torch.tensor([1280, 900], dtype=torch.int32, device="cuda")
+    R.PagedCache(k, k.clone(), table).evict(kv_len, mass, keep=850, max_kv=1280, recent=3, page_table_out=fresh, pos=pos)
+    torch.cuda.synchronize()
+    assert kv_len.tolist() == [850, 850]
+    for s in range(2):
+        for h in range(2):
+            kept = torch.tensor(evict_rule(m0[s, h].cpu(), (1280, 900)[s], 850, 0, 3), device="cuda")
+            assert torch.equal(mass[s, h, :850], m0[s, h, kept]) and torch.equal(pos[s, h, :850], p0[s, h, kept])
+            assert torch.equal(mass[s, h, 850:], m0[s, h, 850:])
+            rows = k[fresh[s].long(), h].reshape(-1, 64)[:850]
+            assert torch.equal(rows, k0[table[s].long(), h].reshape(-1, 64)[kept])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,hkv,page", [([9000], 1, 64), ([3000, 2999], 2, 16), ([30000, 12345, 500], 2, 100)])
+def test_evict_shared_by_a_cluster(R, in_place, lens, hkv, page):
+    """Few long caches: several CTAs select for one (request, head)."""
+    _evict_case(R, lens, page, BF, max(lens) // 3, 2, 7, hkv=hkv, in_place=in_place, seed=page, odd=True)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_long(R, in_place):
     _evict_case(R, [70001], 64, BF, 20000, 4, 100, hkv=1, in_place=in_place, seed=5)
