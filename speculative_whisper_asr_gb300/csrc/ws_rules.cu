@@ -2,28 +2,33 @@
 // block's rows, with the greedy choice and its log probability
 // (ws_logits_rules in include/ws.h gives the formulas).
 //
-// One pass over the logits: every element is read once, changed in
-// registers and written once (8 bytes per element: the HBM floor).  A row
-// belongs to one thread-block cluster whose CTAs take contiguous parts of
-// the vocabulary; each CTA issues all its logit loads first, then builds a
-// table of its part in shared memory while they are in flight,
+// One pass over the logits: every element is read once and written once (8
+// bytes per element: the HBM floor).  A row belongs to one CTA, or, where
+// there are few rows, to a thread-block cluster whose CTAs take contiguous
+// parts of the vocabulary.  Passes of 8,192 ids arrive in shared memory by
+// bulk copies, the next one under the current one's work.  Beside them a
+// table of the pass's ids is built,
 //   word[v] = first bias entry that lists v (high half) | occurrences of v
 //             in the row's token sequence (low half),
-// by integer atomics, whose result does not depend on their order.  Almost
-// every word is 0, so an element costs one shared load and a test.  The
-// CTAs' (largest value, lowest id, sum of exponentials) meet in the first
+// by integer atomics, whose result does not depend on their order.  The
+// penalties and biases are applied to the few listed ids alone, each claimed
+// by one thread, and the dense loop only masks, stores, compares and sums
+// exponentials: with the penalties inside it, unrolled over registers, the
+// code was fetched from memory once per launch and cost more than the data.
+// The CTAs' (largest value, lowest id, sum of exponentials) meet in the first
 // CTA's shared memory (distributed shared memory), so a call is one launch
 // without scratch.
 #include <string>
 
-#include "ws_internal.cuh"
+#include "ws_tc.cuh"
 
 namespace {
 
-constexpr int NT = 256;                    // threads per CTA
-constexpr int GPT = 8;                     // groups of 4 logits per thread and pass
-constexpr int SPAN = NT * GPT * 4;         // ids per pass of a CTA (a 32 KB table)
+constexpr int NT = 512;                    // threads per CTA
+constexpr int SPAN = 8192;                 // ids per pass
+constexpr int SMEM = 3 * SPAN * 4;         // two passes of logits and the table: two CTAs per SM
 constexpr int MAX_CL = 8;                  // portable cluster size
+constexpr int WORDS = SPAN / 32 + 1;       // grammar mask words of a pass
 
 struct RulesStat {
   unsigned long long key;                  // argmax_key of the largest value
@@ -34,14 +39,14 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   const uint32_t u = (uint32_t)(k >> 32);
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
-// exp(y - m) with y = m giving 1 also at infinities
+// exp(y - m), with y = m giving 1 also at infinities
 __device__ __forceinline__ float exp_to(float y, float m) { return y == m ? 1.0f : __expf(y - m); }
 
 __device__ __forceinline__ RulesStat merge(RulesStat a, RulesStat b) {
   const float ma = key_value(a.key), mb = key_value(b.key), m = fmaxf(ma, mb);
   RulesStat r;
   r.key = a.key > b.key ? a.key : b.key;
-  r.sum = a.sum * (a.sum > 0.f ? exp_to(ma, m) : 0.f) + b.sum * (b.sum > 0.f ? exp_to(mb, m) : 0.f);
+  r.sum = a.sum * exp_to(ma, m) + b.sum * exp_to(mb, m);
   return r;
 }
 
@@ -53,15 +58,23 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__global__ void __launch_bounds__(NT) rules_kernel(const ws_rules_args a, int cl, int part) {
-  __shared__ __align__(16) uint32_t tab[SPAN];
+__global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, int cl, int part) {
+  extern __shared__ __align__(128) float ysm[];      // [2][SPAN] logits, then the table
+  __shared__ uint32_t words[2][WORDS];
   __shared__ RulesStat wstat[NT / 32];
   __shared__ RulesStat cstat[MAX_CL];
+  __shared__ __align__(8) uint64_t bar[2];
+  uint32_t* tab = reinterpret_cast<uint32_t*>(ysm + 2 * SPAN);
   const int row = blockIdx.x / cl;
   const int i = row / a.H, j = row - i * a.H;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cl > 1 ? cluster_rank() : 0u;
+  // everything that depends on the row alone is asked for at once
   const int live = a.block_len ? a.block_len[i] : a.H;
+  const int hist_len = a.history ? a.hist_len[i] : 0, bias_len = a.bias_ids ? a.bias_len[i] : 0;
+  const int state = a.masks && a.mask_row ? a.mask_row[row] : -1;
+  const float theta = a.repetition ? a.repetition[i] : 1.f;
+  const float alpha = a.presence ? a.presence[i] : 0.f, freq = a.frequency ? a.frequency[i] : 0.f;
   if (j >= live) {                         // the whole cluster leaves
     if (rank == 0 && tid == 0) {
       if (a.target) a.target[row] = -1;
@@ -77,143 +90,161 @@ __global__ void __launch_bounds__(NT) rules_kernel(const ws_rules_args a, int cl
   // logits: u = v + ph, groups of u
   const int ph = (int)((reinterpret_cast<uintptr_t>(z) >> 2) & 3);
   const bool ovec = (int)((reinterpret_cast<uintptr_t>(o) >> 2) & 3) == ph;
-  const int u_end = V + ph;
-  const int lo = (int)rank * part, hi = min(lo + part, u_end);      // part is a multiple of 4
-  const float theta = a.repetition ? a.repetition[i] : 1.f;
-  const float alpha = a.presence ? a.presence[i] : 0.f, freq = a.frequency ? a.frequency[i] : 0.f;
-  const float* bvals = a.bias_vals ? a.bias_vals + (size_t)i * a.bias_stride : nullptr;
-  const uint32_t* mask = nullptr;
-  if (a.masks && a.mask_row) {
-    const int s = a.mask_row[row];
-    if (s >= 0 && s < a.n_masks) mask = a.masks + (size_t)s * ((V + 31) / 32);
+  const int lo = (int)rank * part, hi = min(lo + part, V + ph);     // part is a multiple of 4
+  // whole groups inside the row come by the bulk copy, up to three ids at
+  // either end of the row one by one
+  auto first_whole = [&](int base) { return base == 0 && ph ? 4 : base; };
+  auto end_whole = [&](int base) { return max(first_whole(base), min(base + SPAN, hi) & ~3); };
+  auto copy = [&](int base, int buf) {
+    const int b0 = first_whole(base), b1 = end_whole(base);
+    tc::mbar_expect_tx(&bar[buf], (uint32_t)(b1 - b0) * 4u);
+    if (b1 > b0) tc::bulk_g2s(ysm + buf * SPAN + (b0 - base), z + (b0 - ph), (uint32_t)(b1 - b0) * 4u, &bar[buf]);
+  };
+  if (tid == 0) {
+    tc::mbar_init(&bar[0], 1);
+    tc::mbar_init(&bar[1], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (lo < hi) copy(lo, 0);
   }
-  const int hl = a.history ? min(max(a.hist_len[i], 0), a.hist_stride) : 0;
+  const uint32_t* mask = state >= 0 && state < a.n_masks ? a.masks + (size_t)state * ((V + 31) / 32) : nullptr;
+  auto mask_word = [&](int base) -> uint32_t {     // this thread's word of the pass
+    const int w = (max(base - ph, 0) >> 5) + tid;
+    return mask && tid < WORDS && base < hi && w < (V + 31) / 32 ? __ldg(mask + w) : 0u;
+  };
+  const int hl = min(max(hist_len, 0), a.hist_stride);
   const int len = hl + (a.block ? j : 0);                           // tokens before this row
   const int from = a.window > 0 ? max(0, len - a.window) : 0;
-  const int nb = a.bias_ids ? min(max(a.bias_len[i], 0), a.bias_stride) : 0;
+  const int nb = min(max(bias_len, 0), a.bias_stride);
+  const int32_t* ids = a.bias_ids + (size_t)i * a.bias_stride;
+  auto token = [&](int p) {                // token p of the row's sequence
+    return p < hl ? a.history[(size_t)i * a.hist_stride + p] : a.block[(size_t)i * a.block_stride + (p - hl) + 1];
+  };
+  // this thread's first token and bias stay in registers for every pass
+  const int p0 = from + tid;
+  const int t0 = p0 < len ? token(p0) : -1, e0 = tid < nb ? ids[tid] : -1;
+  const float v0 = tid < nb ? a.bias_vals[(size_t)i * a.bias_stride + tid] : 0.f;
+  uint32_t word = mask_word(lo);
+  for (int x = tid; x < SPAN / 4; x += NT) reinterpret_cast<uint4*>(tab)[x] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
 
-  RulesStat best;
-  best.key = argmax_key(-INFINITY, 0);
-  best.sum = 0.f;
-  for (int base = lo; base < hi; base += SPAN) {
-    float y[GPT][4];
-#pragma unroll
-    for (int g = 0; g < GPT; ++g) {
-      const int u = base + (g * NT + tid) * 4, v = u - ph;
-      if (u < hi && v >= 0 && v + 3 < V) {
-        const float4 q = __ldcs(reinterpret_cast<const float4*>(z + v));
-        y[g][0] = q.x; y[g][1] = q.y; y[g][2] = q.z; y[g][3] = q.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[g][e] = (u < hi && v + e >= 0 && v + e < V) ? z[v + e] : -INFINITY;
-      }
+  float m = -INFINITY, sum = 0.f;          // this thread's largest value, its id and its sum
+  int mid = 0;
+  bool dead = false;
+  for (int base = lo, pass = 0; base < hi; base += SPAN, ++pass) {
+    const int buf = pass & 1, n = min(base + SPAN, hi) - base;
+    float* ys = ysm + buf * SPAN;
+    if (base + SPAN < hi && tid == 0) copy(base + SPAN, buf ^ 1);
+    if (tid < WORDS) words[buf][tid] = word;
+    word = mask_word(base + SPAN);
+    if (tid < 8) {
+      const int b0 = first_whole(base), b1 = end_whole(base);
+      const int u = tid < 4 ? base + tid : b1 + tid - 4, v = u - ph;
+      if (u >= base && u < base + SPAN && (u < b0 || u >= b1)) ys[u - base] = v >= 0 && v < V && u < base + n ? z[v] : -INFINITY;
     }
-    // ---- the table of ids base - ph .. + SPAN - 1
-#pragma unroll
-    for (int g = 0; g < GPT; ++g) reinterpret_cast<uint4*>(tab)[g * NT + tid] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    const int end = min(base + SPAN, hi);
+    const int shift = ph - base;
+    auto here = [&](int id) { return id >= 0 && id < V && id + shift >= 0 && id + shift < n; };
     if (nb > 0) {
-      const int32_t* ids = a.bias_ids + (size_t)i * a.bias_stride;
       for (int e = tid; e < nb; e += NT) {
-        const int u = ids[e] + ph;
-        if (ids[e] >= 0 && ids[e] < V && u >= base && u < end) atomicMax(&tab[u - base], (uint32_t)(0xFFFF - e) << 16);
+        const int id = e == tid ? e0 : ids[e];
+        if (here(id)) atomicMax(&tab[id + shift], (uint32_t)(0xFFFF - e) << 16);
       }
       __syncthreads();
     }
-    for (int p = from + tid; p < len; p += NT) {
-      const int t = p < hl ? a.history[(size_t)i * a.hist_stride + p] : a.block[(size_t)i * a.block_stride + (p - hl) + 1];
-      const int u = t + ph;
-      if (t >= 0 && t < V && u >= base && u < end) atomicAdd(&tab[u - base], 1u);
+    for (int p = p0; p < len; p += NT) {
+      const int id = p == p0 ? t0 : token(p);
+      if (here(id)) atomicAdd(&tab[id + shift], 1u);
     }
     __syncthreads();
-    // ---- the new logits
-    float m = -INFINITY;
-    int id = 0;
-#pragma unroll
-    for (int g = 0; g < GPT; ++g) {
-      const int u = base + (g * NT + tid) * 4, v = u - ph;
-      if (u >= hi) break;
-      const uint4 w4 = reinterpret_cast<const uint4*>(tab)[g * NT + tid];
-      if (w4.x | w4.y | w4.z | w4.w) {
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t c = w[e] & 0xFFFFu, b = w[e] >> 16;
-          float x = y[g][e];
-          if (c) {
-            x = x > 0.f ? __fdiv_rn(x, theta) : __fmul_rn(x, theta);
-            x = __fsub_rn(x, __fadd_rn(__fmul_rn(freq, (float)c), alpha));
-          }
-          if (b) x = __fadd_rn(x, bvals[0xFFFFu - b]);
-          y[g][e] = x;
+    if (!tc::mbar_wait(&bar[buf], (uint32_t)((pass >> 1) & 1))) {   // ran out: say so, and see the copy land
+      dead = true;
+      tc::mbar_wait(&bar[buf], (uint32_t)((pass >> 1) & 1));
+    }
+    // ---- penalties: the thread that takes an id's count away applies it
+    for (int p = p0; p < len; p += NT) {
+      const int id = p == p0 ? t0 : token(p);
+      if (!here(id)) continue;
+      const uint32_t c = atomicAnd(&tab[id + shift], 0xFFFF0000u) & 0xFFFFu;
+      if (c) {
+        float x = ys[id + shift];
+        x = x > 0.f ? __fdiv_rn(x, theta) : __fmul_rn(x, theta);
+        ys[id + shift] = __fsub_rn(x, __fadd_rn(__fmul_rn(freq, (float)c), alpha));
+      }
+    }
+    __syncthreads();
+    if (nb > 0) {
+      for (int e = tid; e < nb; e += NT) {
+        const int id = e == tid ? e0 : ids[e];
+        if (here(id) && tab[id + shift] >> 16 == (uint32_t)(0xFFFF - e)) {
+          ys[id + shift] = __fadd_rn(ys[id + shift], e == tid ? v0 : a.bias_vals[(size_t)i * a.bias_stride + e]);
+          tab[id + shift] = 0u;            // the entry that won leaves the word clear for the next pass
         }
       }
+      __syncthreads();
+    }
+    // ---- mask, store, compare, sum
+    const int w0 = max(base - ph, 0) >> 5;
+#pragma unroll 2
+    for (int x = tid; x < (n + 3) / 4; x += NT) {
+      float4 y = reinterpret_cast<const float4*>(ys)[x];
+      const int v = base + 4 * x - ph;
       const bool whole = v >= 0 && v + 3 < V;
       if (mask) {
-        uint32_t bits;
-        if (whole) {
-          const int sh = v & 31;
-          uint32_t w0 = __ldg(mask + (v >> 5)), w1 = sh > 28 ? __ldg(mask + (v >> 5) + 1) : 0u;
-          bits = __funnelshift_r(w0, w1, sh);
-        } else {
-          bits = 0u;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (v + e >= 0 && v + e < V) bits |= ((__ldg(mask + ((v + e) >> 5)) >> ((v + e) & 31)) & 1u) << e;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[g][e] = (bits >> e) & 1u ? y[g][e] : -INFINITY;
+        // bits of ids below 0 or at V and above are of no consequence: those logits are -inf already
+        const int s = max(v, 0), w = (s >> 5) - w0;
+        const uint32_t bits = __funnelshift_r(words[buf][w], words[buf][min(w + 1, WORDS - 1)], s & 31) << (s - v);
+        y.x = bits & 1u ? y.x : -INFINITY;
+        y.y = bits & 2u ? y.y : -INFINITY;
+        y.z = bits & 4u ? y.z : -INFINITY;
+        y.w = bits & 8u ? y.w : -INFINITY;
       }
       if (whole && ovec) {
-        __stcs(reinterpret_cast<float4*>(o + v), make_float4(y[g][0], y[g][1], y[g][2], y[g][3]));
+        __stcs(reinterpret_cast<float4*>(o + v), y);
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (v + e >= 0 && v + e < V) o[v + e] = y[g][e];
+        if (v >= 0 && v < V) o[v] = y.x;
+        if (v + 1 >= 0 && v + 1 < V) o[v + 1] = y.y;
+        if (v + 2 >= 0 && v + 2 < V) o[v + 2] = y.z;
+        if (v + 3 >= 0 && v + 3 < V) o[v + 3] = y.w;
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (v + e < 0 || v + e >= V) { y[g][e] = -INFINITY; continue; }
-        if (y[g][e] > m) { m = y[g][e]; id = v + e; }
+      const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+      if (top > m) {
+        sum *= __expf(m - top);
+        m = top;
+        mid = y.x == top ? v : y.y == top ? v + 1 : y.z == top ? v + 2 : v + 3;
+      }
+      if (fabsf(m) < INFINITY) {
+        sum += (__expf(y.x - m) + __expf(y.y - m)) + (__expf(y.z - m) + __expf(y.w - m));
+      } else {                             // nothing above -inf yet (a NaN still counts), or a row with +inf
+        sum += (exp_to(y.x, m) + exp_to(y.y, m)) + (exp_to(y.z, m) + exp_to(y.w, m));
+        if (m < 0.f && sum == sum) sum = 0.f;
       }
     }
-    // ---- this pass's largest value and, relative to it, the sum
-    unsigned long long key = argmax_key(m, id);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, s);
-      key = other > key ? other : key;
+    if (base + SPAN < hi) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before a later copy over these logits
+      __syncthreads();
     }
-    const float wm = key_value(key);
-    float sum = 0.f;
-    if (a.logprob && wm > -INFINITY) {
+  }
+  // ---- the row's largest value (lowest id) and the sum relative to it
+  RulesStat best;
+  {
+    const uint32_t ord = (uint32_t)(argmax_key(m, 0) >> 32), wo = __reduce_max_sync(0xffffffffu, ord);
+    const uint32_t id = __reduce_min_sync(0xffffffffu, ord == wo ? (uint32_t)mid : 0xFFFFFFFFu);
+    best.key = ((unsigned long long)wo << 32) | (unsigned long long)(0xFFFFFFFFu - id);
+    sum *= exp_to(m, key_value(best.key));
 #pragma unroll
-      for (int g = 0; g < GPT; ++g) {
-        if (base + (g * NT + tid) * 4 >= hi) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += exp_to(y[g][e], wm);
-      }
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    }
-    RulesStat st;
-    st.key = key; st.sum = sum;
-    best = merge(best, st);
-    __syncthreads();                       // the table is rebuilt by the next pass
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    best.sum = __any_sync(0xffffffffu, dead) ? NAN : sum;
   }
   if (lane == 0) wstat[warp] = best;
   __syncthreads();
   if (warp == 0) {
     RulesStat st = wstat[lane & (NT / 32 - 1)];
+    const uint32_t hi_ = (uint32_t)(st.key >> 32), wo = __reduce_max_sync(0xffffffffu, hi_);
+    const uint32_t lo_ = __reduce_max_sync(0xffffffffu, hi_ == wo ? (uint32_t)st.key : 0u);
+    best.key = ((unsigned long long)wo << 32) | lo_;
+    float s = st.sum * exp_to(key_value(st.key), key_value(best.key));
 #pragma unroll
-    for (int s = 1; s < NT / 32; s <<= 1) {
-      RulesStat other;
-      other.key = __shfl_xor_sync(0xffffffffu, st.key, s);
-      other.sum = __shfl_xor_sync(0xffffffffu, st.sum, s);
-      st = (lane & s) ? merge(other, st) : merge(st, other);
-    }
-    best = st;
+    for (int x = NT / 64; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    best.sum = s;
   }
   if (cl > 1) {
     cluster_wait();                        // every CTA of the cluster runs
@@ -268,19 +299,24 @@ extern "C" int ws_logits_rules(const ws_rules_args* p, ws_stream stream) {
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return fail(WS_ECUDA, (std::string("a CUDA error was pending before this call: ") +
                            cudaGetErrorString(prior)).c_str());
-  // a CTA's loads fit one pass where the cluster limit allows it
-  const int cl = min(MAX_CL, (a.vocab + 3 + SPAN - 1) / SPAN);
+  // one CTA per row where that gives every SM its two; else the row is shared
+  const long long rows = (long long)a.n * a.H;
+  const int passes = (a.vocab + 3 + SPAN - 1) / SPAN;
+  const int cl = (int)max(1ll, min((long long)min(MAX_CL, passes), 304 / rows));
   const int part = ((a.vocab + 3 + cl - 1) / cl + 3) / 4 * 4;
+  cudaError_t e = cudaFuncSetAttribute(rules_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return fail(WS_ECUDA, (std::string("logits rules: ") + cudaGetErrorString(e)).c_str());
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(a.n * a.H * cl));
   c.blockDim = dim3(NT);
+  c.dynamicSmemBytes = SMEM;
   c.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)cl; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, rules_kernel, a, cl, part);
+  e = cudaLaunchKernelEx(&c, rules_kernel, a, cl, part);
   if (e != cudaSuccess) return fail(WS_ECUDA, (std::string("logits rules launch: ") + cudaGetErrorString(e)).c_str());
   ws_count_launches(1);
   return WS_OK;
