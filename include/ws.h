@@ -515,7 +515,7 @@ int ws_cache_evict(const ws_paged_cache* cache, const ws_evict_args* args, void*
 
 /* Arguments of ws_logits_rules (device pointers; sizes are host ints). */
 typedef struct {
-  int32_t n, H, vocab;         /* requests, block rows per request, vocabulary (1..2^24) */
+  int32_t n, H, vocab;         /* requests, block rows per request, vocabulary (1..262144) */
   const float* logits;         /* row (i, j) at (i * H + j) * ld */
   int64_t ld;                  /* >= vocab */
   float* out;                  /* row (i, j) at (i * H + j) * ld_out; may be logits with ld_out = ld */
@@ -523,7 +523,7 @@ typedef struct {
   const int32_t* block_len;    /* [n] rows in use, or NULL (= H) */
   const int32_t* history;      /* [n, hist_stride] tokens so far, the block's anchor included, or NULL (none) */
   const int32_t* hist_len;     /* [n] */
-  int32_t hist_stride;         /* 0..32768 */
+  int32_t hist_stride;         /* >= 0 */
   const int32_t* block;        /* [n, block_stride] the block (column 0 the anchor), or NULL */
   int32_t block_stride;        /* >= H */
   int32_t window;              /* only the last `window` tokens of a row's sequence count; 0: all */
@@ -533,7 +533,7 @@ typedef struct {
   const int32_t* bias_ids;     /* [n, bias_stride] tokens with a bias, or NULL (none) */
   const float* bias_vals;      /* [n, bias_stride] */
   const int32_t* bias_len;     /* [n] entries in use */
-  int32_t bias_stride;         /* 0..32768 */
+  int32_t bias_stride;         /* >= 0 */
   const uint32_t* masks;       /* [n_masks, ceil(vocab/32)] grammar states: bit set = token allowed, or NULL */
   int32_t n_masks;
   const int32_t* mask_row;     /* [n, H] the row's grammar state; outside [0, n_masks): no constraint */
@@ -555,7 +555,9 @@ typedef struct {
  *            block_len and where no token is left above -inf
  *   logprob  0 for rows >= block_len, -inf where target is -1
  * A NaN logit is never chosen (its row's logprob is NaN).  Rows >= block_len of `out` are left as they
- * were.  ws_accept takes target (GREEDY) or out (SAMPLE) as its own. */
+ * were.  ws_accept takes target (GREEDY) or out (SAMPLE) as its own.
+ * At most 4,096 tokens (hist_stride + H - 1, or window) and biases
+ * (bias_stride) per row: WS_EUNSUPPORTED beyond. */
 int ws_logits_rules(const ws_rules_args* args, ws_stream stream);
 
 /* Number of CUDA kernels this library has launched in the process so far

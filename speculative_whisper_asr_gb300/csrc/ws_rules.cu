@@ -5,30 +5,35 @@
 // One pass over the logits: every element is read once and written once (8
 // bytes per element: the HBM floor).  A row belongs to one CTA, or, where
 // there are few rows, to a thread-block cluster whose CTAs take contiguous
-// parts of the vocabulary.  Passes of 8,192 ids arrive in shared memory by
-// bulk copies, the next one under the current one's work.  Beside them a
-// table of the pass's ids is built,
-//   word[v] = first bias entry that lists v (high half) | occurrences of v
-//             in the row's token sequence (low half),
-// by integer atomics, whose result does not depend on their order.  The
-// penalties and biases are applied to the few listed ids alone, each claimed
-// by one thread, and the dense loop only masks, stores, compares and sums
-// exponentials: with the penalties inside it, unrolled over registers, the
-// code was fetched from memory once per launch and cost more than the data.
+// parts of the vocabulary.
+//   1. The ids that have a penalty or a bias (a few hundred of 50,000) go
+//      into a hash table in shared memory, with their occurrences counted and
+//      their first bias entry found by integer atomics, whose result does not
+//      depend on their order; a bitmap marks them.
+//   2. Their new logits are computed, one id per thread.
+//   3. All other ids stream through registers, the next 16 per thread in
+//      flight while 16 are masked, stored, compared and summed.  No barrier
+//      stands in that loop (with the listed ids handled inside it, pass by
+//      pass, barriers took half of its time).
+//   4. The listed ids' logits are stored over the stream's.
 // The CTAs' (largest value, lowest id, sum of exponentials) meet in the first
 // CTA's shared memory (distributed shared memory), so a call is one launch
 // without scratch.
 #include <string>
 
-#include "ws_tc.cuh"
+#include "ws_internal.cuh"
 
 namespace {
 
-constexpr int NT = 512;                    // threads per CTA
-constexpr int SPAN = 8192;                 // ids per pass
-constexpr int SMEM = 3 * SPAN * 4;         // two passes of logits and the table: two CTAs per SM
+constexpr int NT = 512;                    // threads per CTA, two CTAs per SM
+constexpr int Q = 4;                       // groups of 4 ids per thread and step
 constexpr int MAX_CL = 8;                  // portable cluster size
-constexpr int WORDS = SPAN / 32 + 1;       // grammar mask words of a pass
+constexpr uint32_t FREE = 0xFFFFFFFFu;     // hash table: no id here
+
+// Shared memory: table (ids, counts / new logits, first bias entries), then
+// the row's grammar mask and the bitmap of the listed ids, a word per 32 ids.
+struct Table { int slots, words; };
+inline size_t rules_smem(const Table& t) { return (size_t)t.slots * 12 + (size_t)t.words * 8; }
 
 struct RulesStat {
   unsigned long long key;                  // argmax_key of the largest value
@@ -39,8 +44,13 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   const uint32_t u = (uint32_t)(k >> 32);
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
+__device__ __forceinline__ float exp_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
 // exp(y - m), with y = m giving 1 also at infinities
-__device__ __forceinline__ float exp_to(float y, float m) { return y == m ? 1.0f : __expf(y - m); }
+__device__ __forceinline__ float exp_to(float y, float m) { return y == m ? 1.0f : exp_of(y - m); }
 
 __device__ __forceinline__ RulesStat merge(RulesStat a, RulesStat b) {
   const float ma = key_value(a.key), mb = key_value(b.key), m = fmaxf(ma, mb);
@@ -58,13 +68,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, int cl, int part) {
-  extern __shared__ __align__(128) float ysm[];      // [2][SPAN] logits, then the table
-  __shared__ uint32_t words[2][WORDS];
+__global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, const Table tb, int cl, int part) {
+  extern __shared__ __align__(16) uint32_t sm[];
   __shared__ RulesStat wstat[NT / 32];
   __shared__ RulesStat cstat[MAX_CL];
-  __shared__ __align__(8) uint64_t bar[2];
-  uint32_t* tab = reinterpret_cast<uint32_t*>(ysm + 2 * SPAN);
+  uint32_t *hid = sm, *hcount = sm + tb.slots, *hbias = hcount + tb.slots, *allow = hbias + tb.slots, *listed = allow + tb.words;
   const int row = blockIdx.x / cl;
   const int i = row / a.H, j = row - i * a.H;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -91,26 +99,15 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, int
   const int ph = (int)((reinterpret_cast<uintptr_t>(z) >> 2) & 3);
   const bool ovec = (int)((reinterpret_cast<uintptr_t>(o) >> 2) & 3) == ph;
   const int lo = (int)rank * part, hi = min(lo + part, V + ph);     // part is a multiple of 4
-  // whole groups inside the row come by the bulk copy, up to three ids at
-  // either end of the row one by one
-  auto first_whole = [&](int base) { return base == 0 && ph ? 4 : base; };
-  auto end_whole = [&](int base) { return max(first_whole(base), min(base + SPAN, hi) & ~3); };
-  auto copy = [&](int base, int buf) {
-    const int b0 = first_whole(base), b1 = end_whole(base);
-    tc::mbar_expect_tx(&bar[buf], (uint32_t)(b1 - b0) * 4u);
-    if (b1 > b0) tc::bulk_g2s(ysm + buf * SPAN + (b0 - base), z + (b0 - ph), (uint32_t)(b1 - b0) * 4u, &bar[buf]);
+  // groups wholly inside the row; at most one at either end is not
+  const int g0 = (lo == 0 && ph ? 4 : lo) >> 2, g1 = min((lo + part) >> 2, (V + ph) >> 2);
+  float4 next[Q];
+  auto fetch = [&](int g) {
+#pragma unroll
+    for (int k = 0; k < Q; ++k)
+      if (g + k * NT < g1) next[k] = __ldcs(reinterpret_cast<const float4*>(z + 4 * (g + k * NT) - ph));
   };
-  if (tid == 0) {
-    tc::mbar_init(&bar[0], 1);
-    tc::mbar_init(&bar[1], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (lo < hi) copy(lo, 0);
-  }
-  const uint32_t* mask = state >= 0 && state < a.n_masks ? a.masks + (size_t)state * ((V + 31) / 32) : nullptr;
-  auto mask_word = [&](int base) -> uint32_t {     // this thread's word of the pass
-    const int w = (max(base - ph, 0) >> 5) + tid;
-    return mask && tid < WORDS && base < hi && w < (V + 31) / 32 ? __ldg(mask + w) : 0u;
-  };
+  fetch(g0 + tid);
   const int hl = min(max(hist_len, 0), a.hist_stride);
   const int len = hl + (a.block ? j : 0);                           // tokens before this row
   const int from = a.window > 0 ? max(0, len - a.window) : 0;
@@ -119,110 +116,123 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, int
   auto token = [&](int p) {                // token p of the row's sequence
     return p < hl ? a.history[(size_t)i * a.hist_stride + p] : a.block[(size_t)i * a.block_stride + (p - hl) + 1];
   };
-  // this thread's first token and bias stay in registers for every pass
-  const int p0 = from + tid;
-  const int t0 = p0 < len ? token(p0) : -1, e0 = tid < nb ? ids[tid] : -1;
-  const float v0 = tid < nb ? a.bias_vals[(size_t)i * a.bias_stride + tid] : 0.f;
-  uint32_t word = mask_word(lo);
-  for (int x = tid; x < SPAN / 4; x += NT) reinterpret_cast<uint4*>(tab)[x] = make_uint4(0u, 0u, 0u, 0u);
+  const int t0 = from + tid < len ? token(from + tid) : -1, e0 = tid < nb ? ids[tid] : -1;
+  const bool masked = state >= 0 && state < a.n_masks;
+  const uint32_t* mask = a.masks + (masked ? (size_t)state * ((V + 31) / 32) : 0);
+  // this CTA's words of the two bitmaps
+  const int wb = max(lo - ph, 0) >> 5, we = min(tb.words, ((hi - ph + 31) >> 5) + 1);
+  for (int w = wb + tid; w < we; w += NT) {
+    allow[w] = masked && w < (V + 31) / 32 ? __ldg(mask + w) : FREE;
+    listed[w] = 0u;
+  }
+  for (int s = tid; s < tb.slots; s += NT) { hid[s] = FREE; hcount[s] = 0u; hbias[s] = FREE; }
   __syncthreads();
-
+  // ---- 1: the listed ids of this part
+  auto here = [&](int id) { return id >= 0 && id < V && id + ph >= lo && id + ph < hi; };
+  auto slot = [&](int id) {                // at most half of the slots are ever taken
+    uint32_t s = ((uint32_t)id * 2654435761u) >> 7 & (uint32_t)(tb.slots - 1);
+    for (;;) {
+      const uint32_t old = atomicCAS(&hid[s], FREE, (uint32_t)id);
+      if (old == FREE) atomicOr(&listed[id >> 5], 1u << (id & 31));
+      if (old == FREE || old == (uint32_t)id) return s;
+      s = (s + 1) & (uint32_t)(tb.slots - 1);
+    }
+  };
+  for (int p = from + tid; p < len; p += NT) {
+    const int id = p == from + tid ? t0 : token(p);
+    if (here(id)) atomicAdd(&hcount[slot(id)], 1u);
+  }
+  for (int e = tid; e < nb; e += NT) {
+    const int id = e == tid ? e0 : ids[e];
+    if (here(id)) atomicMin(&hbias[slot(id)], (uint32_t)e);
+  }
+  __syncthreads();
+  // ---- 2: their logits
   float m = -INFINITY, sum = 0.f;          // this thread's largest value, its id and its sum
   int mid = 0;
-  bool dead = false;
-  for (int base = lo, pass = 0; base < hi; base += SPAN, ++pass) {
-    const int buf = pass & 1, n = min(base + SPAN, hi) - base;
-    float* ys = ysm + buf * SPAN;
-    if (base + SPAN < hi && tid == 0) copy(base + SPAN, buf ^ 1);
-    if (tid < WORDS) words[buf][tid] = word;
-    word = mask_word(base + SPAN);
-    if (tid < 8) {
-      const int b0 = first_whole(base), b1 = end_whole(base);
-      const int u = tid < 4 ? base + tid : b1 + tid - 4, v = u - ph;
-      if (u >= base && u < base + SPAN && (u < b0 || u >= b1)) ys[u - base] = v >= 0 && v < V && u < base + n ? z[v] : -INFINITY;
+  auto add = [&](const float* y, int count, auto id_of) {
+    float top = -INFINITY;
+    for (int k = 0; k < count; ++k) top = fmaxf(top, y[k]);
+    if (top >= m && top > -INFINITY) {
+      int first = 0x7FFFFFFF;
+      for (int k = count - 1; k >= 0; --k)
+        if (y[k] == top) first = id_of(k);  // the lowest id that has it
+      if (top > m || first < mid) mid = first;
+      sum *= top > m ? exp_of(m - top) : 1.f;
+      m = top;
     }
-    const int shift = ph - base;
-    auto here = [&](int id) { return id >= 0 && id < V && id + shift >= 0 && id + shift < n; };
-    if (nb > 0) {
-      for (int e = tid; e < nb; e += NT) {
-        const int id = e == tid ? e0 : ids[e];
-        if (here(id)) atomicMax(&tab[id + shift], (uint32_t)(0xFFFF - e) << 16);
-      }
-      __syncthreads();
+    if (fabsf(m) < INFINITY) {
+      for (int k = 0; k < count; k += 4)
+        sum += count < 4 ? exp_of(y[k] - m) : (exp_of(y[k] - m) + exp_of(y[k + 1] - m)) + (exp_of(y[k + 2] - m) + exp_of(y[k + 3] - m));
+    } else {                               // nothing above -inf yet (a NaN still counts), or a row with +inf
+      for (int k = 0; k < count; ++k) sum += exp_to(y[k], m);
+      if (m < 0.f && sum == sum) sum = 0.f;
     }
-    for (int p = p0; p < len; p += NT) {
-      const int id = p == p0 ? t0 : token(p);
-      if (here(id)) atomicAdd(&tab[id + shift], 1u);
+  };
+  for (int s = tid; s < tb.slots; s += NT) {
+    if (hid[s] == FREE) continue;
+    const int id = (int)hid[s];
+    float x = z[id];
+    if (hcount[s]) {
+      x = x > 0.f ? __fdiv_rn(x, theta) : __fmul_rn(x, theta);
+      x = __fsub_rn(x, __fadd_rn(__fmul_rn(freq, (float)hcount[s]), alpha));
     }
-    __syncthreads();
-    if (!tc::mbar_wait(&bar[buf], (uint32_t)((pass >> 1) & 1))) {   // ran out: say so, and see the copy land
-      dead = true;
-      tc::mbar_wait(&bar[buf], (uint32_t)((pass >> 1) & 1));
-    }
-    // ---- penalties: the thread that takes an id's count away applies it
-    for (int p = p0; p < len; p += NT) {
-      const int id = p == p0 ? t0 : token(p);
-      if (!here(id)) continue;
-      const uint32_t c = atomicAnd(&tab[id + shift], 0xFFFF0000u) & 0xFFFFu;
-      if (c) {
-        float x = ys[id + shift];
-        x = x > 0.f ? __fdiv_rn(x, theta) : __fmul_rn(x, theta);
-        ys[id + shift] = __fsub_rn(x, __fadd_rn(__fmul_rn(freq, (float)c), alpha));
-      }
-    }
-    __syncthreads();
-    if (nb > 0) {
-      for (int e = tid; e < nb; e += NT) {
-        const int id = e == tid ? e0 : ids[e];
-        if (here(id) && tab[id + shift] >> 16 == (uint32_t)(0xFFFF - e)) {
-          ys[id + shift] = __fadd_rn(ys[id + shift], e == tid ? v0 : a.bias_vals[(size_t)i * a.bias_stride + e]);
-          tab[id + shift] = 0u;            // the entry that won leaves the word clear for the next pass
-        }
-      }
-      __syncthreads();
-    }
-    // ---- mask, store, compare, sum
-    const int w0 = max(base - ph, 0) >> 5;
-#pragma unroll 2
-    for (int x = tid; x < (n + 3) / 4; x += NT) {
-      float4 y = reinterpret_cast<const float4*>(ys)[x];
-      const int v = base + 4 * x - ph;
-      const bool whole = v >= 0 && v + 3 < V;
-      if (mask) {
-        // bits of ids below 0 or at V and above are of no consequence: those logits are -inf already
-        const int s = max(v, 0), w = (s >> 5) - w0;
-        const uint32_t bits = __funnelshift_r(words[buf][w], words[buf][min(w + 1, WORDS - 1)], s & 31) << (s - v);
-        y.x = bits & 1u ? y.x : -INFINITY;
-        y.y = bits & 2u ? y.y : -INFINITY;
-        y.z = bits & 4u ? y.z : -INFINITY;
-        y.w = bits & 8u ? y.w : -INFINITY;
-      }
-      if (whole && ovec) {
-        __stcs(reinterpret_cast<float4*>(o + v), y);
-      } else {
-        if (v >= 0 && v < V) o[v] = y.x;
-        if (v + 1 >= 0 && v + 1 < V) o[v + 1] = y.y;
-        if (v + 2 >= 0 && v + 2 < V) o[v + 2] = y.z;
-        if (v + 3 >= 0 && v + 3 < V) o[v + 3] = y.w;
-      }
-      const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-      if (top > m) {
-        sum *= __expf(m - top);
-        m = top;
-        mid = y.x == top ? v : y.y == top ? v + 1 : y.z == top ? v + 2 : v + 3;
-      }
-      if (fabsf(m) < INFINITY) {
-        sum += (__expf(y.x - m) + __expf(y.y - m)) + (__expf(y.z - m) + __expf(y.w - m));
-      } else {                             // nothing above -inf yet (a NaN still counts), or a row with +inf
-        sum += (exp_to(y.x, m) + exp_to(y.y, m)) + (exp_to(y.z, m) + exp_to(y.w, m));
-        if (m < 0.f && sum == sum) sum = 0.f;
-      }
-    }
-    if (base + SPAN < hi) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before a later copy over these logits
-      __syncthreads();
+    if (hbias[s] != FREE) x = __fadd_rn(x, a.bias_vals[(size_t)i * a.bias_stride + hbias[s]]);
+    if (!((allow[id >> 5] >> (id & 31)) & 1u)) x = -INFINITY;
+    hcount[s] = __float_as_uint(x);
+    add(&x, 1, [&](int) { return id; });
+  }
+  // up to three ids at either end of the row
+  if (tid < 8) {
+    const int u = tid < 4 ? lo + tid : 4 * g1 + tid - 4, v = u - ph;
+    const bool edge = tid < 4 ? u < 4 * g0 : u >= 4 * g0;
+    if (edge && v >= 0 && v < V && u < hi && !((listed[v >> 5] >> (v & 31)) & 1u)) {
+      const float x = (allow[v >> 5] >> (v & 31)) & 1u ? z[v] : -INFINITY;
+      o[v] = x;
+      add(&x, 1, [&](int) { return v; });
     }
   }
+  __syncthreads();                         // in place, the listed ids are read before the stream stores over them
+  // ---- 3: the stream
+  for (int g = g0 + tid; g < g1; g += Q * NT) {
+    float y[4 * Q];
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      const bool on = g + k * NT < g1;
+      y[4 * k] = on ? next[k].x : -INFINITY;
+      y[4 * k + 1] = on ? next[k].y : -INFINITY;
+      y[4 * k + 2] = on ? next[k].z : -INFINITY;
+      y[4 * k + 3] = on ? next[k].w : -INFINITY;
+    }
+    fetch(g + Q * NT);
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      if (g + k * NT >= g1) continue;
+      const int v = 4 * (g + k * NT) - ph, w = v >> 5, sh = v & 31, w2 = min(w + 1, tb.words - 1);
+      if (masked) {
+        const uint32_t bits = __funnelshift_r(allow[w], allow[w2], sh);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!((bits >> e) & 1u)) y[4 * k + e] = -INFINITY;
+      }
+      if (ovec) {
+        __stcs(reinterpret_cast<float4*>(o + v), make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[v + e] = y[4 * k + e];
+      }
+      const uint32_t mine = __funnelshift_r(listed[w], listed[w2], sh) & 15u;
+      if (mine)                            // taken care of in step 2
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((mine >> e) & 1u) y[4 * k + e] = -INFINITY;
+    }
+    add(y, 4 * Q, [&](int k) { return 4 * (g + (k >> 2) * NT) - ph + (k & 3); });
+  }
+  __syncthreads();
+  // ---- 4: the listed ids over the stream's
+  for (int s = tid; s < tb.slots; s += NT)
+    if (hid[s] != FREE) o[hid[s]] = __uint_as_float(hcount[s]);
   // ---- the row's largest value (lowest id) and the sum relative to it
   RulesStat best;
   {
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, int
     sum *= exp_to(m, key_value(best.key));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    best.sum = __any_sync(0xffffffffu, dead) ? NAN : sum;
+    best.sum = sum;
   }
   if (lane == 0) wstat[warp] = best;
   __syncthreads();
@@ -280,43 +290,53 @@ extern "C" int ws_logits_rules(const ws_rules_args* p, ws_stream stream) {
   if (!p) return fail(WS_EINVAL, "null arguments");
   const ws_rules_args& a = *p;
   if (a.n < 0 || a.H < 0 || a.H > 16384) return fail(WS_EINVAL, "n must be >= 0 and H 0..16384");
-  if (a.vocab < 1 || a.vocab > (1 << 24)) return fail(WS_EINVAL, "vocab must be 1..2^24");
+  if (a.vocab < 1 || a.vocab > (1 << 18)) return fail(WS_EINVAL, "vocab must be 1..262144");
   if (a.n == 0 || a.H == 0) return WS_OK;
   if (!a.logits || !a.out) return fail(WS_EINVAL, "null logits or out");
   if ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.out)) & 3)
     return fail(WS_EINVAL, "logits and out must be 4-byte aligned");
   if (a.ld < a.vocab || a.ld_out < a.vocab) return fail(WS_EINVAL, "ld and ld_out must be >= vocab");
   if (a.logits == a.out && a.ld != a.ld_out) return fail(WS_EINVAL, "in place, ld_out must equal ld");
-  if (a.hist_stride < 0 || a.hist_stride > 32768) return fail(WS_EINVAL, "hist_stride must be 0..32768");
+  if (a.hist_stride < 0 || a.bias_stride < 0) return fail(WS_EINVAL, "hist_stride and bias_stride must be >= 0");
   if (a.history && !a.hist_len) return fail(WS_EINVAL, "history without hist_len");
   if (a.block && a.block_stride < a.H) return fail(WS_EINVAL, "block_stride must be >= H");
   if (a.window < 0) return fail(WS_EINVAL, "window must be >= 0");
-  if (a.bias_stride < 0 || a.bias_stride > 32768) return fail(WS_EINVAL, "bias_stride must be 0..32768");
   if (a.bias_ids && (!a.bias_vals || !a.bias_len)) return fail(WS_EINVAL, "bias_ids without bias_vals or bias_len");
   if (a.masks && a.n_masks < 1) return fail(WS_EINVAL, "masks need n_masks >= 1");
   if (a.masks && !a.mask_row) return fail(WS_EINVAL, "masks without mask_row");
   if ((long long)a.n * a.H > 2147483647ll / MAX_CL) return fail(WS_EINVAL, "too many rows");
+  // listed ids of a row at most: the tokens that count and the biases
+  long long tokens = a.history ? a.hist_stride : 0;
+  if (a.block) tokens += a.H - 1;
+  if (a.window > 0) tokens = min(tokens, (long long)a.window);
+  const long long most = tokens + (a.bias_ids ? a.bias_stride : 0);
+  if (most > 4096) return fail(WS_EUNSUPPORTED, "more than 4096 tokens and biases per row (window limits the tokens)");
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return fail(WS_ECUDA, (std::string("a CUDA error was pending before this call: ") +
                            cudaGetErrorString(prior)).c_str());
+  Table tb;
+  tb.slots = 64;
+  while (tb.slots < 2 * most) tb.slots *= 2;
+  tb.words = (a.vocab + 31) / 32 + 1;
+  const size_t smem = rules_smem(tb);
   // one CTA per row where that gives every SM its two; else the row is shared
   const long long rows = (long long)a.n * a.H;
-  const int passes = (a.vocab + 3 + SPAN - 1) / SPAN;
-  const int cl = (int)max(1ll, min((long long)min(MAX_CL, passes), 304 / rows));
+  const int steps = (a.vocab + 3 + 4 * Q * NT - 1) / (4 * Q * NT);
+  const int cl = (int)max(1ll, min((long long)min(MAX_CL, steps), 304 / rows));
   const int part = ((a.vocab + 3 + cl - 1) / cl + 3) / 4 * 4;
-  cudaError_t e = cudaFuncSetAttribute(rules_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  cudaError_t e = cudaFuncSetAttribute(rules_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 192 * 1024);
   if (e != cudaSuccess) return fail(WS_ECUDA, (std::string("logits rules: ") + cudaGetErrorString(e)).c_str());
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(a.n * a.H * cl));
   c.blockDim = dim3(NT);
-  c.dynamicSmemBytes = SMEM;
+  c.dynamicSmemBytes = smem;
   c.stream = (cudaStream_t)stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)cl; at[0].val.clusterDim.y = 1; at[0].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  e = cudaLaunchKernelEx(&c, rules_kernel, a, cl, part);
+  e = cudaLaunchKernelEx(&c, rules_kernel, a, tb, cl, part);
   if (e != cudaSuccess) return fail(WS_ECUDA, (std::string("logits rules launch: ") + cudaGetErrorString(e)).c_str());
   ws_count_launches(1);
   return WS_OK;

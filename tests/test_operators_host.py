@@ -101,16 +101,22 @@ def test_workspaces_checked(B):
     _refused(B, lambda: B.ws_paged_attention(_cache(B), a, 0, need, 0), B.WS_EINVAL)
 
 
-@pytest.mark.parametrize("bad", [dict(n=-1), dict(H=-1), dict(H=16385), dict(vocab=0), dict(vocab=(1 << 24) + 1, ld=1 << 25, ld_out=1 << 25),
+@pytest.mark.parametrize("bad", [dict(n=-1), dict(H=-1), dict(H=16385), dict(vocab=0), dict(vocab=(1 << 18) + 1, ld=1 << 25, ld_out=1 << 25),
                                  dict(logits=0), dict(out=0), dict(logits=4097), dict(out=4098), dict(ld=999),
                                  dict(ld_out=999), dict(out=4096, ld_out=1001), dict(history=4096, hist_stride=8),
-                                 dict(hist_stride=32769), dict(hist_stride=-1), dict(block=4096, block_stride=2),
+                                 dict(hist_stride=-1), dict(block=4096, block_stride=2),
                                  dict(window=-1), dict(bias_ids=4096, bias_stride=4),
-                                 dict(bias_ids=4096, bias_vals=4096, bias_stride=4), dict(bias_stride=32769),
+                                 dict(bias_ids=4096, bias_vals=4096, bias_stride=4), dict(bias_stride=-1),
                                  dict(masks=4096, n_masks=0, mask_row=4096), dict(masks=4096, n_masks=2),
                                  dict(n=1 << 30, H=4)])
 def test_bad_rules_refused(B, bad):
     _refused(B, lambda: B.ws_logits_rules(_rules(B, **bad), 0), B.WS_EINVAL)
+
+
+def test_rules_too_many_listed_tokens_refused(B):
+    _refused(B, lambda: B.ws_logits_rules(_rules(B, history=4096, hist_len=4096, hist_stride=4097), 0), B.WS_EUNSUPPORTED)
+    _refused(B, lambda: B.ws_logits_rules(_rules(B, history=4096, hist_len=4096, hist_stride=4000, window=3000, bias_ids=4096,
+                                                 bias_vals=4096, bias_len=4096, bias_stride=1097), 0), B.WS_EUNSUPPORTED)
 
 
 def test_null_structs_refused(B):
