@@ -455,26 +455,21 @@ class Encoder:
 
 
 # ---------------------------------------------------------------------- operators on the caller's tensors
-def _check_tensor(name, t, dtype, ndim, device, dense=True):
-    """A device tensor of the given type; dense: its last dimension is contiguous."""
-    if t.dtype is not dtype or t.dim() != ndim or t.device != device:
-        raise ValueError(f"{name}: a {ndim}-d {dtype} tensor on {device} is needed")
-    if dense and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+_I32, _F32 = torch.int32, torch.float32
 
 
-def _rows(name, t, dtype, shape, device):
-    """A contiguous device tensor of exactly this type and shape."""
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is needed")
+def _rows(name, t, dtype, shape, dev):
+    """Pointer of a contiguous tensor of exactly this type and shape on CUDA device number `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev} is needed")
     return t.data_ptr()
 
 
-def _on(device):
-    """The handle of the current stream; `device` has to be the current device."""
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"the tensors are on {device}, the current device is {torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _on(dev):
+    """The handle of the current stream; device number `dev` has to be the current device."""
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 class PagedCache:
@@ -492,17 +487,18 @@ class PagedCache:
             raise ValueError("v must have the type, shape, strides and device of k")
         if k.stride(3) != 1:
             raise ValueError("the head dimension must be contiguous")
-        _check_tensor("page_table", page_table, torch.int32, 2, k.device)
+        if (page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.device != k.device
+                or page_table.shape[1] > 1 and page_table.stride(1) != 1
+                or page_table.shape[0] > 1 and page_table.stride(0) < page_table.shape[1]):
+            raise ValueError("page_table: an int32 tensor [slots, pages] with contiguous rows on k's device is needed")
         self.k, self.v, self.page_table = k, v, page_table
-        self.dev, self.dtype = k.device, k.dtype
+        self.dev, self.dtype = k.get_device(), k.dtype
         self.pages, self.heads, self.page_size, _ = k.shape
         self.slots = page_table.shape[0]
         self.desc = B.PagedCacheDesc(
             B.WS_BF16 if k.dtype is torch.bfloat16 else B.WS_F32, self.heads, self.page_size, self.pages, k.data_ptr(),
             v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(), self.slots,
             page_table.stride(0) if self.slots > 1 else page_table.shape[1])
-        if self.slots > 1 and page_table.stride(0) < page_table.shape[1]:
-            raise ValueError("page_table rows must not overlap")
         self._attn, self._evict = B.AttentionArgs(), B.EvictArgs()
         self._ws, self._kept = {}, []
 
@@ -515,39 +511,44 @@ class PagedCache:
             if ws is not None:
                 self._kept.append(ws)
                 nbytes = max(nbytes, 2 * ws.numel())
-            ws = self._ws[stream] = torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
+            ws = self._ws[stream] = torch.empty(nbytes, dtype=torch.uint8, device=self.k.device)
         return ws.data_ptr()
-
-    def _slots(self, req_ids, n):
-        return 0 if req_ids is None else _rows("req_ids", req_ids, torch.int32, (n,), self.dev)
 
     def attend(self, q, kv_len, cu_q, max_q: int, max_kv: int, causal: bool = True, scale: float = 0.125, out=None,
                lse=None, mass=None, req_ids=None):
         """Attention of the chunks q [total_q, heads, 64] over the cache (ws_paged_attention).  kv_len [slots] int32
         counts the chunk's own positions; cu_q [requests + 1] int32.  lse [total_q, heads] fp32 receives the
         log-sum-exp; mass [slots, KV heads, >= max_kv] fp32 is added to.  Returns out."""
-        _check_tensor("q", q, self.dtype, 3, self.dev)
         if out is None:
             out = torch.zeros_like(q, memory_format=torch.contiguous_format)
-        _check_tensor("out", out, self.dtype, 3, self.dev)
-        if out.shape != q.shape or q.shape[2] != 64 or (q.shape[1] > 1 and (q.stride(1) != 64 or out.stride(1) != 64)):
-            raise ValueError("q and out: [rows, heads, 64] with contiguous heads are needed")
-        a = self._attn
+        dev = self.dev
+        if q.dim() != 3 or out.shape != q.shape or q.shape[2] != 64:
+            raise ValueError("q and out: [rows, heads, 64] are needed")
         rows, heads, _ = q.shape
+        a = self._attn
+        for name, t in (("q", q), ("out", out)):
+            s0, s1, s2 = t.stride()
+            if t.dtype is not self.dtype or t.get_device() != dev or s2 != 1 or (heads > 1 and s1 != 64):
+                raise ValueError(f"{name}: a {self.dtype} tensor with contiguous heads on cuda:{dev} is needed")
+            if rows < 2:
+                s0 = heads * 64
+            if name == "q":
+                a.q, a.q_stride = t.data_ptr(), s0
+            else:
+                a.out, a.out_stride = t.data_ptr(), s0
         n = cu_q.shape[0] - 1
-        a.n_req, a.req_ids = n, self._slots(req_ids, n)
-        a.kv_len = _rows("kv_len", kv_len, torch.int32, (self.slots,), self.dev)
-        a.cu_q = _rows("cu_q", cu_q, torch.int32, (n + 1,), self.dev)
-        a.total_q, a.max_q, a.max_kv, a.n_heads = rows, max_q, max_kv, heads
-        a.causal, a.scale = int(causal), scale
-        a.q, a.q_stride = q.data_ptr(), q.stride(0) if rows > 1 else heads * 64
-        a.out, a.out_stride = out.data_ptr(), out.stride(0) if rows > 1 else heads * 64
-        a.lse = 0 if lse is None else _rows("lse", lse, torch.float32, (rows, heads), self.dev)
-        a.mass = 0
-        if mass is not None:
-            a.mass_stride = mass.shape[2] if mass.dim() == 3 else 0
-            a.mass = _rows("mass", mass, torch.float32, (self.slots, self.heads, a.mass_stride), self.dev)
-        s = _on(self.dev)
+        a.n_req = n
+        a.req_ids = 0 if req_ids is None else _rows("req_ids", req_ids, _I32, (n,), dev)
+        a.kv_len = _rows("kv_len", kv_len, _I32, (self.slots,), dev)
+        a.cu_q = _rows("cu_q", cu_q, _I32, (n + 1,), dev)
+        a.total_q, a.max_q, a.max_kv, a.n_heads, a.causal, a.scale = rows, max_q, max_kv, heads, int(causal), scale
+        a.lse = 0 if lse is None else _rows("lse", lse, _F32, (rows, heads), dev)
+        if mass is None:
+            a.mass = 0
+        else:
+            a.mass_stride = width = mass.shape[-1]
+            a.mass = _rows("mass", mass, _F32, (self.slots, self.heads, width), dev)
+        s = _on(dev)
         need = B.ws_paged_attention_workspace(self.desc, a)
         B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
         return out
@@ -557,28 +558,36 @@ class PagedCache:
         """Keep min(kv_len, keep) positions per slot and head (ws_cache_evict): the first `sink`, the last `recent`,
         then those of the largest mass.  Without page_table_out the cache, and without kv_len_out / mass_out / pos_out
         the lengths, masses and labels, are compacted in place."""
-        a = self._evict
-        n = self.slots if req_ids is None else req_ids.shape[0]
-        a.n_req, a.req_ids = n, self._slots(req_ids, n)
-        a.kv_len = _rows("kv_len", kv_len, torch.int32, (self.slots,), self.dev)
-        a.kv_len_out = a.kv_len if kv_len_out is None else _rows("kv_len_out", kv_len_out, torch.int32, (self.slots,),
-                                                                 self.dev)
+        a, dev, slots, heads = self._evict, self.dev, self.slots, self.heads
+        n = slots if req_ids is None else req_ids.shape[0]
+        a.n_req = n
+        a.req_ids = 0 if req_ids is None else _rows("req_ids", req_ids, _I32, (n,), dev)
+        length = _rows("kv_len", kv_len, _I32, (slots,), dev)
+        a.kv_len = length
+        a.kv_len_out = length if kv_len_out is None else _rows("kv_len_out", kv_len_out, _I32, (slots,), dev)
         a.max_kv, a.keep, a.sink, a.recent = max_kv, keep, sink, recent
-
-        def per_position(name, t, dtype):
-            return _rows(name, t, dtype, (self.slots, self.heads, t.shape[-1]), self.dev), t.shape[-1]
-        a.mass, a.mass_stride = per_position("mass", mass, torch.float32)
-        a.mass_out, a.mass_out_stride = ((a.mass, a.mass_stride) if mass_out is None
-                                         else per_position("mass_out", mass_out, torch.float32))
-        a.pos, a.pos_stride = (0, 0) if pos is None else per_position("pos", pos, torch.int32)
-        a.pos_out, a.pos_out_stride = ((a.pos, a.pos_stride) if pos_out is None
-                                       else per_position("pos_out", pos_out, torch.int32))
-        a.page_table_out = 0
-        if page_table_out is not None:
-            a.table_out_stride = page_table_out.shape[1]
-            a.page_table_out = _rows("page_table_out", page_table_out, torch.int32, (self.slots, a.table_out_stride),
-                                     self.dev)
-        s = _on(self.dev)
+        width = mass.shape[-1]
+        ptr = _rows("mass", mass, _F32, (slots, heads, width), dev)
+        a.mass, a.mass_stride = ptr, width
+        if mass_out is not None:
+            width = mass_out.shape[-1]
+            ptr = _rows("mass_out", mass_out, _F32, (slots, heads, width), dev)
+        a.mass_out, a.mass_out_stride = ptr, width
+        ptr = width = 0
+        if pos is not None:
+            width = pos.shape[-1]
+            ptr = _rows("pos", pos, _I32, (slots, heads, width), dev)
+        a.pos, a.pos_stride = ptr, width
+        if pos_out is not None:
+            width = pos_out.shape[-1]
+            ptr = _rows("pos_out", pos_out, _I32, (slots, heads, width), dev)
+        a.pos_out, a.pos_out_stride = ptr, width
+        if page_table_out is None:
+            a.page_table_out = 0
+        else:
+            a.table_out_stride = width = page_table_out.shape[1]
+            a.page_table_out = _rows("page_table_out", page_table_out, _I32, (slots, width), dev)
+        s = _on(dev)
         need = B.ws_cache_evict_workspace(self.desc, a)
         B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
 
@@ -588,61 +597,70 @@ class LogitsRules:
     (ws_logits_rules).  repetition / presence / frequency: [n] fp32; bias_ids
     [n, entries] int32 with bias_vals and bias_len [n]; masks [states,
     ceil(vocab / 32)] int32 words, bit set = token allowed; window: how many
-    of the latest tokens count (0: all)."""
+    of the latest tokens count (0: all).  The tensors stay the object's; their
+    contents may change between calls."""
 
     def __init__(self, repetition=None, presence=None, frequency=None, window: int = 0, bias_ids=None, bias_vals=None,
                  bias_len=None, masks=None):
-        self.repetition, self.presence, self.frequency, self.window = repetition, presence, frequency, window
-        self.bias_ids, self.bias_vals, self.bias_len, self.masks = bias_ids, bias_vals, bias_len, masks
+        self._own = (repetition, presence, frequency, bias_ids, bias_vals, bias_len, masks)
         self._args = B.RulesArgs()
+        self._args.window = window
+        self._shape = None                 # (n, vocab, device) that the object's tensors were checked for
+
+    def _bind(self, n, V, dev):
+        a = self._args
+        rep, pres, freq, ids, vals, lens, masks = self._own
+        for name, t in (("repetition", rep), ("presence", pres), ("frequency", freq)):
+            setattr(a, name, 0 if t is None else _rows(name, t, _F32, (n,), dev))
+        a.bias_ids = a.bias_vals = a.bias_len = a.bias_stride = a.masks = a.n_masks = 0
+        if ids is not None:
+            width = a.bias_stride = ids.shape[1]
+            a.bias_ids = _rows("bias_ids", ids, _I32, (n, width), dev)
+            a.bias_vals = _rows("bias_vals", vals, _F32, (n, width), dev)
+            a.bias_len = _rows("bias_len", lens, _I32, (n,), dev)
+        if masks is not None:
+            a.n_masks = masks.shape[0]
+            a.masks = _rows("masks", masks, _I32, (a.n_masks, (V + 31) // 32), dev)
+        self._shape = (n, V, dev)
 
     def apply(self, logits, history=None, hist_len=None, block=None, block_len=None, mask_row=None, out=None,
               target=None, logprob=None):
         """New logits of rows [n, H, vocab] fp32 into out (default: in place).  history [n, tokens] with hist_len [n]:
         the tokens so far, the anchor included; block [n, >= H]: the block, whose columns 1..j precede row j;
-        mask_row [n, H]: each row's grammar state.  target [n, H] int32 and logprob [n, H] fp32 receive the greedy
-        choice.  Returns out."""
-        dev = logits.device
+        mask_row [n, H]: each row's grammar state (needed when the object has masks).  target [n, H] int32 and
+        logprob [n, H] fp32 receive the greedy choice.  Returns out."""
         out = logits if out is None else out
-        _check_tensor("logits", logits, torch.float32, 3, dev)
-        _check_tensor("out", out, torch.float32, 3, dev)
+        dev = logits.get_device()
         n, H, V = logits.shape
-        for t in (logits, out):
-            if t.shape != logits.shape or (n > 1 and t.stride(0) != H * t.stride(1)):
-                raise ValueError("logits and out: [n, H, vocab] with evenly spaced rows are needed")
         a = self._args
+        for t in (logits, out):
+            if t.dtype is not _F32 or t.get_device() != dev or dev < 0 or t.shape != logits.shape:
+                raise ValueError("logits and out: fp32 CUDA tensors [n, H, vocab] are needed")
+            s0, s1, s2 = t.stride()
+            ld = s1 if H > 1 else s0 if n > 1 else V
+            if (V > 1 and s2 != 1) or (n > 1 and s0 != H * ld):
+                raise ValueError("logits and out: evenly spaced contiguous rows are needed")
+            if t is logits:
+                a.logits, a.ld = t.data_ptr(), ld
+            if t is out:
+                a.out, a.ld_out = t.data_ptr(), ld
+        if self._shape != (n, V, dev):
+            self._bind(n, V, dev)
         a.n, a.H, a.vocab = n, H, V
-        a.logits, a.ld = logits.data_ptr(), logits.stride(1) if H > 1 else logits.stride(0) if n > 1 else V
-        a.out, a.ld_out = out.data_ptr(), out.stride(1) if H > 1 else out.stride(0) if n > 1 else V
-
-        def per_request(name, t, dtype):
-            return 0 if t is None else _rows(name, t, dtype, (n,), dev)
-        a.block_len = per_request("block_len", block_len, torch.int32)
-        a.history = a.hist_len = a.hist_stride = 0
-        if history is not None:
-            a.hist_stride = history.shape[1]
-            a.history = _rows("history", history, torch.int32, (n, a.hist_stride), dev)
-            a.hist_len = per_request("hist_len", hist_len, torch.int32)
-        a.block = a.block_stride = 0
-        if block is not None:
-            a.block_stride = block.shape[1]
-            a.block = _rows("block", block, torch.int32, (n, a.block_stride), dev)
-        a.window = self.window
-        a.repetition = per_request("repetition", self.repetition, torch.float32)
-        a.presence = per_request("presence", self.presence, torch.float32)
-        a.frequency = per_request("frequency", self.frequency, torch.float32)
-        a.bias_ids = a.bias_vals = a.bias_len = a.bias_stride = 0
-        if self.bias_ids is not None:
-            a.bias_stride = self.bias_ids.shape[1]
-            a.bias_ids = _rows("bias_ids", self.bias_ids, torch.int32, (n, a.bias_stride), dev)
-            a.bias_vals = _rows("bias_vals", self.bias_vals, torch.float32, (n, a.bias_stride), dev)
-            a.bias_len = per_request("bias_len", self.bias_len, torch.int32)
-        a.masks = a.n_masks = a.mask_row = 0
-        if self.masks is not None and mask_row is not None:
-            a.n_masks = self.masks.shape[0]
-            a.masks = _rows("masks", self.masks, torch.int32, (a.n_masks, (V + 31) // 32), dev)
-            a.mask_row = _rows("mask_row", mask_row, torch.int32, (n, H), dev)
-        a.target = 0 if target is None else _rows("target", target, torch.int32, (n, H), dev)
-        a.logprob = 0 if logprob is None else _rows("logprob", logprob, torch.float32, (n, H), dev)
+        a.block_len = 0 if block_len is None else _rows("block_len", block_len, _I32, (n,), dev)
+        if history is None:
+            a.history = 0
+        else:
+            a.hist_stride = width = history.shape[1]
+            a.history = _rows("history", history, _I32, (n, width), dev)
+            a.hist_len = _rows("hist_len", hist_len, _I32, (n,), dev)
+        if block is None:
+            a.block = 0
+        else:
+            a.block_stride = width = block.shape[1]
+            a.block = _rows("block", block, _I32, (n, width), dev)
+        a.mask_row = 0 if mask_row is None else _rows("mask_row", mask_row, _I32, (n, H), dev)
+        a.target = 0 if target is None else _rows("target", target, _I32, (n, H), dev)
+        a.logprob = 0 if logprob is None else _rows("logprob", logprob, _F32, (n, H), dev)
         B.ws_logits_rules(a, _on(dev))
         return out
