@@ -501,6 +501,7 @@ class PagedCache:
             page_table.stride(0) if self.slots > 1 else page_table.shape[1])
         self._attn, self._evict = B.AttentionArgs(), B.EvictArgs()
         self._ws, self._kept = {}, []
+        self._need = {}                    # workspace bytes by the sizes they depend on
 
     def _workspace(self, nbytes, stream):
         """Scratch of this stream.  Outgrown scratch is kept: work in flight or a captured graph may still use it."""
@@ -549,7 +550,10 @@ class PagedCache:
             a.mass_stride = width = mass.shape[-1]
             a.mass = _rows("mass", mass, _F32, (self.slots, self.heads, width), dev)
         s = _on(dev)
-        need = B.ws_paged_attention_workspace(self.desc, a)
+        sizes = (n, rows, heads, max_q, max_kv, scale, lse is None, mass is None)
+        need = self._need.get(sizes)
+        if need is None:
+            need = self._need[sizes] = B.ws_paged_attention_workspace(self.desc, a)
         B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
         return out
 
@@ -588,7 +592,9 @@ class PagedCache:
             a.table_out_stride = width = page_table_out.shape[1]
             a.page_table_out = _rows("page_table_out", page_table_out, _I32, (slots, width), dev)
         s = _on(dev)
-        need = B.ws_cache_evict_workspace(self.desc, a)
+        need = self._need.get((n, keep))
+        if need is None:
+            need = self._need[n, keep] = B.ws_cache_evict_workspace(self.desc, a)
         B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
 
 
