@@ -307,6 +307,32 @@ int ws_readout(ws_ctx* ctx, int n_req, const int32_t* req_ids, const int32_t* ro
  * (-1: none yet). */
 int ws_get_centers(ws_ctx* ctx, int n_req, const int32_t* req_ids, int32_t* out, ws_stream stream);
 
+/* Accumulated attention weight of the acoustic frames.  While a buffer is
+ * set, ws_verify adds, for every target layer and head, each block row's
+ * cross-attention weights (rows < block_len, rejected proposals included) to
+ *   mass  [n_layers, max_batch, n_heads, max_frames] float (device), by
+ *         slot; the caller clears it (a slot's part when the slot gets new
+ *         acoustic keys) and keeps it alive; NULL switches it off (default)
+ * The cross-attention then runs in the kernels of ws_paged_attention: rows
+ * agree with the usual path within the model's tolerance, not bit for bit,
+ * and the kernel-per-operation verify is used.  Host-only; no device work. */
+int ws_set_frame_mass(ws_ctx* ctx, float* mass);
+
+/* Cut the listed requests' acoustic caches: every target layer and head keeps
+ * the `keep` frames of the largest accumulated weight (ws_cache_evict with no
+ * protected positions), in order, and drops the others; requests of at most
+ * `keep` valid frames keep all.  Batch verification reads these caches once
+ * per layer and round, so its cross-attention then takes keep / F of its time.
+ * The result is approximate: the target attends to the kept frames alone from
+ * here on.  The drafter's caches keep every frame.  ws_cross_kv gives a slot
+ * its full caches back.
+ *   mass  laid out as for ws_set_frame_mass; it is not changed, and after
+ *         the call its positions are no longer the caches'
+ * A context whose caches were cut has no readout by frame: WS_EUNSUPPORTED
+ * here while a readout layer is set, and from ws_set_readout afterwards. */
+int ws_evict_frames(ws_ctx* ctx, int n_req, const int32_t* req_ids, const float* mass, int keep,
+                    ws_stream stream);
+
 /* Sample rows of given logits with the drafter's sampler: out[i, r] ~
  * softmax(logits[i, r, :] / T) using Philox counter (slot, round, r+1, 0).
  *   logits [n, rows, V] float; out [n, rows] int32 (row stride `rows`). */

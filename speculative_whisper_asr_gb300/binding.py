@@ -28,7 +28,7 @@ EXPORTS = ("ws_query_workspace", "ws_load_weights", "ws_reset", "ws_cross_kv", "
            "ws_encoder_free", "ws_encoder_attention",
            "ws_fused_layernorm",
            "ws_paged_attention_workspace", "ws_paged_attention", "ws_cache_evict_workspace", "ws_cache_evict",
-           "ws_logits_rules")
+           "ws_logits_rules", "ws_set_frame_mass", "ws_evict_frames")
 
 
 class WSError(RuntimeError):
@@ -136,6 +136,8 @@ def _load():
         "ws_cache_evict_workspace": (C.c_size_t, [P, P]),
         "ws_cache_evict": (I, [P, P, P, C.c_size_t, S]),
         "ws_logits_rules": (I, [P, S]),
+        "ws_set_frame_mass": (I, [P, P]),
+        "ws_evict_frames": (I, [P, I, P, P, I, S]),
         "ws_encoder_workspace": (C.c_size_t, [C.POINTER(EncoderDesc)]),
         "ws_encoder_load": (I, [C.POINTER(P), C.POINTER(EncoderDesc), P, C.c_size_t, P, S]),
         "ws_encode": (I, [P, I, P, P, S]),
@@ -379,3 +381,11 @@ def ws_cache_evict(cache: PagedCacheDesc, args: EvictArgs, workspace, nbytes, st
 
 def ws_logits_rules(args: RulesArgs, stream):
     return _check(None, lib.ws_logits_rules(C.addressof(args), stream))
+
+
+def ws_set_frame_mass(ctx, mass):
+    return _check(ctx, lib.ws_set_frame_mass(ctx, mass or None))
+
+
+def ws_evict_frames(ctx, n, req, mass, keep, stream):
+    return _check(ctx, lib.ws_evict_frames(ctx, n, req, mass, keep, stream))

@@ -43,6 +43,10 @@ struct ws_ctx {
   int32_t* ptab = nullptr;
   float* rope = nullptr;
   int32_t *L = nullptr, *Fc = nullptr, *Fv = nullptr, *pend_start = nullptr, *pend_n = nullptr, *status = nullptr;
+  int32_t* Fcut = nullptr;      // scratch of ws_evict_frames: the frames left
+  int32_t* Fd = nullptr;        // frames of the drafter's caches (Fv: the target's, fewer after ws_evict_frames)
+  float* frame_mass = nullptr;  // caller's [n_layers][max_batch][heads][max_frames], or null (ws_set_frame_mass)
+  bool evicted = false;         // a slot's frames were cut: positions in the target's caches are no longer frames
   int32_t* xcenter = nullptr;   // per slot: centre frame of the drafter's cross-attention window (-1: none)
   // verification-attention readout (ws_set_readout)
   int readout_layer = -1, half_width = 0, read_H = 0;
@@ -212,7 +216,7 @@ Plan make_plan(const ws_model_desc& d) {
   p.xkv = lay.take((size_t)d.max_batch * p.n_xl * 2 * D * d.max_frames * es);
   p.ptab = lay.take((size_t)p.n_pages * 4);
   p.rope = lay.take((size_t)d.max_pos * WS_DH * 4);
-  p.state = lay.take((size_t)d.max_batch * 6 * 4 + 256);
+  p.state = lay.take((size_t)d.max_batch * 8 * 4 + 256);
   p.x = lay.take(M * D * 4);
   p.h = lay.take(M * D * es);
   p.q = lay.take(M * D * es);
@@ -223,7 +227,8 @@ Plan make_plan(const ws_model_desc& d) {
   const int nh = d.drafter_layers > 0 ? d.n_hist : 0;
   p.hist = lay.take((size_t)d.max_batch * d.max_block * nh * D * 4);
   p.amax = lay.take(M * 8);
-  p.part = lay.take(M * d.n_heads * p.max_split * (WS_DH + 2) * 4);
+  // the attention that accumulates frame weights also keeps log-sum-exps, in padded regions
+  p.part = lay.take(M * d.n_heads * (p.max_split * (WS_DH + 2) + 1) * 4 + 1024);
   p.acnt = lay.take((size_t)d.max_batch * d.n_heads * 4);
   p.feat = lay.take(M * nh * D * es);
   p.hpre = lay.take(M * D * 4);
@@ -460,13 +465,55 @@ int flow_verify(ws_ctx* c, const int32_t* req, int H, const int32_t* block, cons
   return WS_OK;
 }
 
+// --------------------------------------------------------------------------- acoustic caches as described caches
+// A target layer's acoustic keys and values: one page of max_frames frames per
+// slot.  The self cache's page table holds 0, 1, 2, ..., so its first
+// max_batch entries map every slot to its page.
+ws_paged_cache frame_cache(const ws_ctx* c, int layer) {
+  ws_paged_cache x = {};
+  x.dtype = c->d.dtype;
+  x.n_kv_heads = c->heads;
+  x.page_size = c->d.max_frames;
+  x.n_pages = x.n_slots = c->d.max_batch;
+  x.k = (char*)c->xkv + (size_t)layer * c->x_layer_elems * c->es;
+  x.v = (char*)x.k + (size_t)c->heads * c->d.max_frames * WS_DH * c->es;
+  x.page_stride = (int64_t)c->x_slot_elems;
+  x.head_stride = (int64_t)c->d.max_frames * WS_DH;
+  x.token_stride = WS_DH;
+  x.page_table = c->ptab;
+  x.table_stride = 1;
+  return x;
+}
+
+// A target layer's cross-attention that also adds every row's weights to the
+// caller's frame masses.
+cudaError_t cross_attn_with_mass(ws_ctx* c, int n, int H, const int32_t* req, const int32_t* blen, int layer,
+                                 cudaStream_t s) {
+  ws_attention_args a = {};
+  a.n_req = n;
+  a.req_ids = req;
+  a.kv_len = c->Fv;
+  a.total_q = n * H;
+  a.max_q = H;
+  a.max_kv = c->max_fc;
+  a.n_heads = c->heads;
+  a.scale = 0.125f;                        // 1/sqrt(64)
+  a.q = c->q;
+  a.q_stride = a.out_stride = c->d.d_model;
+  a.out = c->ao;
+  a.mass_stride = c->d.max_frames;
+  a.mass = c->frame_mass + (size_t)layer * c->d.max_batch * c->heads * c->d.max_frames;
+  return launch_block_attention(frame_cache(c, layer), a, H, blen, c->part, s);
+}
+
 // --------------------------------------------------------------------------- verify
 template <typename T>
 int verify_impl(ws_ctx* c, int n, const int32_t* req, int H, const int32_t* block, const int32_t* blen,
                 int32_t* target, float* logits, cudaStream_t s, const TreeMask* tree = nullptr) {
   const ws_model_desc& d = c->d;
   const int D = d.d_model, M = n * H;
-  if (sizeof(T) == 2 && c->flow_ok && c->flow_on && c->readout_layer < 0 && !tree && n == 1 && H <= FLOW_MAX_ROWS)
+  if (sizeof(T) == 2 && c->flow_ok && c->flow_on && c->readout_layer < 0 && !c->frame_mass && !tree && n == 1 &&
+      H <= FLOW_MAX_ROWS)
     return flow_verify(c, req, H, block, blen, target, logits, s);
   const TreeMask tm = tree ? *tree : linear_tree();
   c->read_H = H;
@@ -489,8 +536,11 @@ int verify_impl(ws_ctx* c, int n, const int32_t* req, int H, const int32_t* bloc
     e.bias = w.b_qc; e.out = c->q; e.ldo = D;
     CK(ln_gemm<T>(c, M, c->x, w.ln2_g, w.ln2_b, w.w_qc, e, s));
     if (l == c->readout_layer) CK(cudaMemcpyAsync(c->qread, c->q, (size_t)M * D * c->es, cudaMemcpyDeviceToDevice, s));
-    CK(launch_cross_attn<T>(n, H, req, c->Fv, (const T*)c->q, xkv_of(c), l, (T*)c->ao, c->heads, c->max_fc, c->as,
-                            s, pdl));
+    if (c->frame_mass)
+      CK(cross_attn_with_mass(c, n, H, req, blen, l, s));
+    else
+      CK(launch_cross_attn<T>(n, H, req, c->Fv, (const T*)c->q, xkv_of(c), l, (T*)c->ao, c->heads, c->max_fc, c->as,
+                              s, pdl));
     e = epi0(c, EPI_RESID);
     e.bias = w.b_oc; e.resid = c->x; e.ldr = D;
     CK(gemm<T>(c, c->ao, c->mrows, w.w_oc, M, e, s));
@@ -561,10 +611,10 @@ int draft_impl(ws_ctx* c, int n, const int32_t* req, int32_t* block, float temp,
     e.bias = w.b_qc; e.out = c->q; e.ldo = D;
     CK(ln_gemm<T>(c, M, c->x, w.ln2_g, w.ln2_b, w.w_qc, e, s));
     if (c->half_width > 0)
-      CK(launch_window_attn<T>(n, K1, req, c->Fv, c->xcenter, c->half_width, (const T*)c->q, D, xkv_of(c),
+      CK(launch_window_attn<T>(n, K1, req, c->Fd, c->xcenter, c->half_width, (const T*)c->q, D, xkv_of(c),
                                d.n_layers + l, (T*)c->ao, s, pdl));
     else
-      CK(launch_cross_attn<T>(n, K1, req, c->Fv, (const T*)c->q, xkv_of(c), d.n_layers + l, (T*)c->ao, c->heads,
+      CK(launch_cross_attn<T>(n, K1, req, c->Fd, (const T*)c->q, xkv_of(c), d.n_layers + l, (T*)c->ao, c->heads,
                               c->max_fc, c->as, s, pdl));
     e = epi0(c, EPI_RESID);
     e.bias = w.b_oc; e.resid = c->x; e.ldr = D;
@@ -598,7 +648,7 @@ template <typename T>
 int cross_kv_impl(ws_ctx* c, int n, const int32_t* req, const void* enc, const int32_t* cu, const int32_t* valid,
                   int maxF, int total_frames, cudaStream_t s) {
   const ws_model_desc& d = c->d;
-  CK(launch_set_frames(n, req, cu, valid, d.max_frames, c->Fc, c->Fv, c->status, s));
+  CK(launch_set_frames(n, req, cu, valid, d.max_frames, c->Fc, c->Fv, c->Fd, c->status, s));
   for (int l = 0; l < c->n_xl; ++l) {
     const LayerW& w = l < d.n_layers ? c->tl[l] : c->dl[l - d.n_layers];
     Epi e = epi0(c, EPI_CROSSKV);
@@ -692,6 +742,8 @@ int ws_load_weights(ws_ctx** out, const ws_model_desc* desc, void* workspace, si
   c->pend_start = st + 3 * desc->max_batch; c->pend_n = st + 4 * desc->max_batch;
   c->status = st + 5 * desc->max_batch;
   c->xcenter = st + 5 * desc->max_batch + 64;     // after the status word (its 256-byte pad)
+  c->Fd = c->xcenter + desc->max_batch;
+  c->Fcut = c->Fd + desc->max_batch;
   c->x = (float*)(b + p.x); c->h = b + p.h; c->q = b + p.q; c->ao = b + p.ao; c->ffn = b + p.ffn;
   c->kb = b + p.kb; c->vb = b + p.vb; c->hist = (float*)(b + p.hist);
   c->amax = (unsigned long long*)(b + p.amax); c->part = (float*)(b + p.part);
@@ -735,6 +787,7 @@ int ws_load_weights(ws_ctx** out, const ws_model_desc* desc, void* workspace, si
   e = cudaMemcpyAsync(c->ptab, pt.data(), pt.size() * 4, cudaMemcpyHostToDevice, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(st, 0, (size_t)desc->max_batch * 5 * 4 + 256, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(c->xcenter, 0xFF, (size_t)desc->max_batch * 4, s);   // -1: no centre
+  if (e == cudaSuccess) e = cudaMemsetAsync(c->Fd, 0, (size_t)desc->max_batch * 2 * 4, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(c->hist, 0, (size_t)desc->max_batch * desc->max_block *
                                                         (desc->drafter_layers ? desc->n_hist : 0) * D * 4, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(c->as.counters, 0, (size_t)desc->max_batch * desc->n_heads * 4, s);
@@ -936,8 +989,42 @@ int ws_tree_tokens(ws_ctx* c, int n, const int32_t* req, const int32_t* block, i
   return WS_OK;
 }
 
+int ws_set_frame_mass(ws_ctx* c, float* mass) {
+  if (!c) return fail(nullptr, WS_EINVAL, "null context");
+  if (reinterpret_cast<uintptr_t>(mass) & 3) return fail(c, WS_EINVAL, "mass must be 4-byte aligned");
+  c->frame_mass = mass;
+  return WS_OK;
+}
+
+int ws_evict_frames(ws_ctx* c, int n, const int32_t* req, const float* mass, int keep, ws_stream stream) {
+  if (int r = check_common(c, n, req, stream)) return r;
+  if (n == 0) return WS_OK;
+  if (!mass) return fail(c, WS_EINVAL, "null mass");
+  if (keep < 1 || keep > c->d.max_frames) return fail(c, WS_EINVAL, "keep %d outside 1..max_frames (%d)", keep, c->d.max_frames);
+  if (c->readout_layer >= 0)
+    return fail(c, WS_EUNSUPPORTED, "the readout layer's keys are read by frame: switch the readout off first");
+  if (c->max_fc < 1) return fail(c, WS_EINVAL, "no acoustic keys yet (ws_cross_kv)");
+  if (keep >= c->max_fc) return WS_OK;     // every request already fits
+  ws_evict_args a = {};
+  a.n_req = n;
+  a.req_ids = req;
+  a.kv_len = c->Fv;
+  a.max_kv = c->max_fc;
+  a.keep = keep;
+  a.mass_stride = c->d.max_frames;
+  c->evicted = true;
+  for (int l = 0; l < c->d.n_layers; ++l) {
+    a.kv_len_out = l + 1 < c->d.n_layers ? c->Fcut : c->Fv;        // every layer starts from the same count
+    a.mass = mass + (size_t)l * c->d.max_batch * c->heads * c->d.max_frames;
+    CK(launch_cache_evict(frame_cache(c, l), a, c->part, (cudaStream_t)stream));
+  }
+  return WS_OK;
+}
+
 int ws_set_readout(ws_ctx* c, int layer, int half_width) {
   if (!c) return fail(nullptr, WS_EINVAL, "null context");
+  if (layer >= 0 && c->evicted)
+    return fail(c, WS_EUNSUPPORTED, "ws_evict_frames has cut acoustic caches of this context: no readout by frame");
   if (layer < -1 || layer >= c->d.n_layers) return fail(c, WS_EINVAL, "readout layer %d outside -1..n_layers-1", layer);
   if (half_width < 0) return fail(c, WS_EINVAL, "half_width must be >= 0");
   if (half_width > 0 && c->d.drafter_layers == 0) return fail(c, WS_EUNSUPPORTED, "context has no drafter");

@@ -385,6 +385,25 @@ cudaError_t move(const EvictP& p, bool in_place, bool pdl, cudaStream_t s) {
 
 }  // namespace
 
+size_t cache_evict_workspace(const ws_paged_cache& cache, const ws_evict_args& args) { return evict_bytes(&cache, &args); }
+
+cudaError_t launch_cache_evict(const ws_paged_cache& cache, const ws_evict_args& args, void* workspace, cudaStream_t s) {
+  EvictP p = {};
+  p.c = cache;
+  p.a = args;
+  const bool in_place = !args.page_table_out || args.page_table_out == cache.page_table;
+  p.tout = in_place ? cache.page_table : args.page_table_out;
+  p.tout_stride = in_place ? cache.table_stride : args.table_out_stride;
+  p.len = (int32_t*)workspace;
+  p.idx = (int32_t*)((char*)workspace + ((size_t)args.n_req * 4 + 255) / 256 * 256);
+  p.ordered = args.mass_out == args.mass || (args.pos && args.pos_out == args.pos);
+  // programmatic dependent launch only on created streams, as elsewhere in the library
+  const bool pdl = s != nullptr && s != cudaStreamLegacy && s != cudaStreamPerThread;
+  cudaError_t e = args.max_kv <= 4096 ? select<256>(p, s) : select<512>(p, s);
+  if (e != cudaSuccess) return e;
+  return cache.dtype == WS_BF16 ? move<bf16>(p, in_place, pdl, s) : move<float>(p, in_place, pdl, s);
+}
+
 extern "C" size_t ws_cache_evict_workspace(const ws_paged_cache* cache, const ws_evict_args* args) {
   if (check_evict(cache, args) || args->n_req == 0) return 0;
   return evict_bytes(cache, args);
@@ -400,21 +419,7 @@ extern "C" int ws_cache_evict(const ws_paged_cache* cache, const ws_evict_args* 
     return paged_fail(WS_ENOSPACE, "workspace smaller than ws_cache_evict_workspace()");
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
-  EvictP p = {};
-  p.c = *cache;
-  p.a = *args;
-  const bool in_place = !args->page_table_out || args->page_table_out == cache->page_table;
-  p.tout = in_place ? cache->page_table : args->page_table_out;
-  p.tout_stride = in_place ? cache->table_stride : args->table_out_stride;
-  p.len = (int32_t*)workspace;
-  p.idx = (int32_t*)((char*)workspace + ((size_t)args->n_req * 4 + 255) / 256 * 256);
-  p.ordered = args->mass_out == args->mass || (args->pos && args->pos_out == args->pos);
-  // programmatic dependent launch only on created streams, as elsewhere in the library
-  const bool pdl = stream != nullptr && (cudaStream_t)stream != cudaStreamLegacy && (cudaStream_t)stream != cudaStreamPerThread;
-  cudaError_t e = args->max_kv <= 4096 ? select<256>(p, (cudaStream_t)stream) : select<512>(p, (cudaStream_t)stream);
-  if (e == cudaSuccess)
-    e = cache->dtype == WS_BF16 ? move<bf16>(p, in_place, pdl, (cudaStream_t)stream)
-                                : move<float>(p, in_place, pdl, (cudaStream_t)stream);
+  const cudaError_t e = launch_cache_evict(*cache, *args, workspace, (cudaStream_t)stream);
   if (e != cudaSuccess) return paged_fail(WS_ECUDA, std::string("cache eviction launch: ") + cudaGetErrorString(e));
   return WS_OK;
 }

@@ -432,7 +432,7 @@ template <typename T>
 cudaError_t attn_init_attributes();
 cudaError_t launch_rope_table(float* tab, int max_pos, cudaStream_t s);
 cudaError_t launch_set_frames(int n, const int32_t* req_ids, const int32_t* cu, const int32_t* valid,
-                              int max_frames, int32_t* Fc, int32_t* Fv, int32_t* status, cudaStream_t s);
+                              int max_frames, int32_t* Fc, int32_t* Fv, int32_t* Fd, int32_t* status, cudaStream_t s);
 cudaError_t launch_reset(int n, const int32_t* req_ids, int32_t* L, int32_t* pend_n, int32_t* xcenter,
                          cudaStream_t s);
 template <typename T>
@@ -459,6 +459,14 @@ struct AcceptParams {
   unsigned long long parent4;  // tree: parent row of row j in bits 4j .. 4j + 3
   int32_t* tpath;              // tree: per request [L before, a, path rows 0..a] (WS_TREE_REC ints)
 };
+// Operators on a described cache (ws_pattn.cu, ws_evict.cu) for the context's
+// own: attention of the rows [n * H] of a block (block_len[i] of them in use;
+// cu_q is not read), and eviction.  Arguments are not checked again.
+size_t block_attention_workspace(const ws_paged_cache& cache, const ws_attention_args& args);
+cudaError_t launch_block_attention(const ws_paged_cache& cache, const ws_attention_args& args, int H,
+                                   const int32_t* block_len, void* workspace, cudaStream_t s);
+size_t cache_evict_workspace(const ws_paged_cache& cache, const ws_evict_args& args);
+cudaError_t launch_cache_evict(const ws_paged_cache& cache, const ws_evict_args& args, void* workspace, cudaStream_t s);
 #define WS_TREE_REC 18
 // Move the accepted root path's self keys / values (every target layer),
 // history rows and readout queries from their tree rows to block rows 0..a.

@@ -243,7 +243,7 @@ __global__ void rope_table_kernel(float* tab, int max_pos) {
 
 // ------------------------------------------------------------------ request state
 __global__ void set_frames_kernel(int n, const int32_t* req_ids, const int32_t* cu, const int32_t* valid,
-                                  int max_frames, int32_t* Fc, int32_t* Fv, int32_t* status) {
+                                  int max_frames, int32_t* Fc, int32_t* Fv, int32_t* Fd, int32_t* status) {
   int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n) return;
   int F = cu[i + 1] - cu[i];
@@ -255,6 +255,7 @@ __global__ void set_frames_kernel(int n, const int32_t* req_ids, const int32_t* 
   }
   Fc[req_ids[i]] = F;
   Fv[req_ids[i]] = v;
+  Fd[req_ids[i]] = v;
 }
 
 __global__ void reset_kernel(int n, const int32_t* req_ids, int32_t* L, int32_t* pend_n, int32_t* xcenter) {
@@ -1077,9 +1078,9 @@ cudaError_t launch_rope_table(float* tab, int max_pos, cudaStream_t s) {
   return cudaGetLastError();
 }
 cudaError_t launch_set_frames(int n, const int32_t* req_ids, const int32_t* cu, const int32_t* valid,
-                              int max_frames, int32_t* Fc, int32_t* Fv, int32_t* status, cudaStream_t s) {
+                              int max_frames, int32_t* Fc, int32_t* Fv, int32_t* Fd, int32_t* status, cudaStream_t s) {
   ws_count_launches(1);
-  set_frames_kernel<<<(n + 127) / 128, 128, 0, s>>>(n, req_ids, cu, valid, max_frames, Fc, Fv, status);
+  set_frames_kernel<<<(n + 127) / 128, 128, 0, s>>>(n, req_ids, cu, valid, max_frames, Fc, Fv, Fd, status);
   return cudaGetLastError();
 }
 cudaError_t launch_reset(int n, const int32_t* req_ids, int32_t* L, int32_t* pend_n, int32_t* xcenter,

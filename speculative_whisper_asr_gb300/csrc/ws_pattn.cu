@@ -653,7 +653,34 @@ cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
   return launch_f32_mass(p, q.wide, s);
 }
 
+cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int pad_H, const int32_t* chunk_len,
+                const Plan& q, char* ws, cudaStream_t s) {
+  AttnP p = {};
+  p.c = cache;
+  p.a = args;
+  p.pad_H = pad_H;
+  p.chunk_len = chunk_len;
+  p.G = args.n_heads / cache.n_kv_heads;
+  p.sl = args.scale == 0.f ? 1.f : fabsf(args.scale) * LOG2E;
+  p.q_and = args.scale == 0.f ? 0u : 0xffffffffu;
+  p.q_xor = args.scale < 0.f ? 0x80008000u : 0u;
+  p.nsplit = q.nsplit; p.tps = q.tps; p.geo = q.geo;
+  p.lse = args.lse ? args.lse : args.mass && !q.fa ? (float*)(ws + q.lse) : nullptr;
+  p.row_tiles = q.row_tiles;
+  if (q.fa && args.mass) p.nl = (float*)(ws + q.nl);
+  if (q.nsplit > 1) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
+  return cache.dtype == WS_BF16 ? run_bf16(p, q, s) : run_f32(p, q, s);
+}
+
 }  // namespace
+
+size_t block_attention_workspace(const ws_paged_cache& cache, const ws_attention_args& args) {
+  return make_plan(cache, args).bytes;
+}
+cudaError_t launch_block_attention(const ws_paged_cache& cache, const ws_attention_args& args, int H,
+                                   const int32_t* block_len, void* workspace, cudaStream_t s) {
+  return run(cache, args, H, block_len, make_plan(cache, args), (char*)workspace, s);
+}
 
 extern "C" size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attention_args* args) {
   if (check_attn(cache, args) || args->n_req == 0 || args->total_q == 0 || args->max_q == 0) return 0;
@@ -670,20 +697,7 @@ extern "C" int ws_paged_attention(const ws_paged_cache* cache, const ws_attentio
   if (q.bytes > workspace_bytes) return paged_fail(WS_ENOSPACE, "workspace smaller than ws_paged_attention_workspace()");
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
-  AttnP p = {};
-  p.c = *cache;
-  p.a = *args;
-  p.G = args->n_heads / cache->n_kv_heads;
-  p.sl = args->scale == 0.f ? 1.f : fabsf(args->scale) * LOG2E;
-  p.q_and = args->scale == 0.f ? 0u : 0xffffffffu;
-  p.q_xor = args->scale < 0.f ? 0x80008000u : 0u;
-  p.nsplit = q.nsplit; p.tps = q.tps; p.geo = q.geo;
-  char* ws = (char*)workspace;
-  p.lse = args->lse ? args->lse : args->mass && !q.fa ? (float*)(ws + q.lse) : nullptr;
-  p.row_tiles = q.row_tiles;
-  if (q.fa && args->mass) p.nl = (float*)(ws + q.nl);
-  if (q.nsplit > 1) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
-  const cudaError_t e = cache->dtype == WS_BF16 ? run_bf16(p, q, (cudaStream_t)stream) : run_f32(p, q, (cudaStream_t)stream);
+  const cudaError_t e = run(*cache, *args, 0, nullptr, q, (char*)workspace, (cudaStream_t)stream);
   if (e != cudaSuccess) return paged_fail(WS_ECUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
   return WS_OK;
 }

@@ -34,6 +34,8 @@ __host__ __device__ __forceinline__ int tile_count(const TileGeo& g, int page_si
 struct AttnP {
   ws_paged_cache c;
   ws_attention_args a;
+  int pad_H;                               // > 0: request i has rows i * pad_H .., chunk_len[i] of them in use (cu_q is not read)
+  const int32_t* chunk_len;
   int G;                                   // query heads per KV head
   float sl;                                // |scale| * log2(e): scores in log2 units (1 when scale is 0)
   uint32_t q_and, q_xor;                   // applied to bf16 query pairs: the sign of scale, or all zero
@@ -54,9 +56,14 @@ struct Req {
 __device__ __forceinline__ Req request(const AttnP& p, int i) {
   Req r;
   r.slot = p.a.req_ids ? p.a.req_ids[i] : i;
-  r.row0 = p.a.cu_q[i];
-  const int end = min(p.a.cu_q[i + 1], p.a.total_q);
-  r.c = r.row0 >= 0 ? min(max(end - r.row0, 0), p.a.max_q) : 0;
+  if (p.pad_H) {
+    r.row0 = i * p.pad_H;
+    r.c = min(max(p.chunk_len[i], 0), p.pad_H);
+  } else {
+    r.row0 = p.a.cu_q[i];
+    const int end = min(p.a.cu_q[i + 1], p.a.total_q);
+    r.c = r.row0 >= 0 ? min(max(end - r.row0, 0), p.a.max_q) : 0;
+  }
   r.L = 0;
   if (r.slot >= 0 && r.slot < p.c.n_slots)
     r.L = (int)min((long long)min(max(p.a.kv_len[r.slot], 0), p.a.max_kv), (long long)p.c.table_stride * p.c.page_size);

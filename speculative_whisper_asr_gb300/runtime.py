@@ -53,6 +53,8 @@ class Decoder:
         self.dtype = B.WS_BF16 if shape.dtype == "bf16" else B.WS_F32
         self.tdtype = torch.bfloat16 if shape.dtype == "bf16" else torch.float32
         self.readout = False
+        self.accumulating = False
+        self._mass = None
         self.tree = None
         dl = shape.drafter_layers if drafter is not None else 0
         self.max_block = max_block or max(shape.K + 1, len(shape.prompt))
@@ -143,19 +145,38 @@ class Decoder:
         B.ws_get_centers(self.ctx, req.numel(), req.data_ptr(), out.data_ptr(), _stream())
         return out.cpu().numpy()
 
+    def frame_mass(self) -> torch.Tensor:
+        """The decoder's accumulated frame weights [layers, slots, heads, frames] (allocated, zero, on first use)."""
+        if self._mass is None:
+            self._mass = torch.zeros(self.s.n_layers, self.max_batch, self.s.n_heads, self.max_frames, device=self.dev)
+        return self._mass
+
+    def accumulate_frames(self, on: bool):
+        """Whether verification adds the rows' cross-attention weights to frame_mass() (ws_set_frame_mass)."""
+        B.ws_set_frame_mass(self.ctx, self.frame_mass().data_ptr() if on else 0)
+        self.accumulating = on
+
+    def evict_frames(self, req, keep: int):
+        """Cut the requests' acoustic caches to the `keep` frames of the largest weight per layer and head
+        (ws_evict_frames) and clear their masses, whose positions are the caches' no more."""
+        mass = self.frame_mass()
+        B.ws_evict_frames(self.ctx, req.numel(), req.data_ptr(), mass.data_ptr(), keep, _stream())
+        mass[:, req.long()] = 0
+
     # ------------------------------------------------------------------ batch state
     def new_batch(self, req, budgets, tcap: int | None = None, sampling: bool = False,
-                  draft_logits: bool = False) -> "Batch":
+                  draft_logits: bool = False, rules: "LogitsRules | None" = None) -> "Batch":
         """draft_logits: keep the drafter's logits also for greedy decoding
-        (needed by a confidence threshold)."""
-        return Batch(self, req, budgets, tcap or self.s.max_pos, sampling, draft_logits)
+        (needed by a confidence threshold).  rules: penalties, biases and
+        grammar masks applied to the target's logits of every round."""
+        return Batch(self, req, budgets, tcap or self.s.max_pos, sampling, draft_logits, rules)
 
 
 class Batch:
     """Device arrays of one decoding batch (request slots `req`)."""
 
     def __init__(self, dec: Decoder, req: torch.Tensor, budgets, tcap: int, sampling: bool,
-                 draft_logits: bool = False):
+                 draft_logits: bool = False, rules: "LogitsRules | None" = None):
         self.dec = dec
         self.req = req
         n = req.numel()
@@ -181,8 +202,12 @@ class Batch:
         self.acc_sum = torch.zeros(n, dtype=torch.int64, device=dev)
         self.prop_sum = torch.zeros(n, dtype=torch.int64, device=dev)
         self.p_logits = self.q_logits = self.p_logits1 = None
-        if sampling:
-            self.p_logits = torch.empty(n, K + 1, dec.V, dtype=torch.float32, device=dev)
+        self.rules = rules
+        self._states = {}
+        if sampling or rules is not None:
+            rows = max(K + 1, len(dec.s.prompt)) if rules is not None else K + 1
+            self._p_store = torch.empty(n * rows * dec.V, dtype=torch.float32, device=dev)
+            self.p_logits = self._p_store[: n * (K + 1) * dec.V].view(n, K + 1, dec.V)
         if sampling or draft_logits or dec.tree is not None:
             self.q_logits = torch.empty(n, K, dec.V, dtype=torch.float32, device=dev)
         self.vblock = torch.zeros(n, K + 1, **i32)      # the block as verified (truncated proposals)
@@ -209,6 +234,25 @@ class Batch:
             self.graphs[key] = g
         B.ws_graph_launch(g, s)
 
+    def _logits(self, H):
+        """The target logits of an H-row verify, [n, H, vocab]."""
+        return self._p_store[: self.n * H * self.dec.V].view(self.n, H, self.dec.V)
+
+    def states(self, H: int) -> torch.Tensor:
+        """Grammar states [n, H] int32 of the rows of H-row blocks (a prompt, a single token, a verified block: row j
+        follows the block's first j proposals), read by every round of that height; -1, the start: no constraint."""
+        if H not in self._states:
+            self._states[H] = torch.full((self.n, H), -1, dtype=torch.int32, device=self.dec.dev)
+        return self._states[H]
+
+    def _apply_rules(self, H, block, blen, target, prompt=False):
+        """The rules on an H-row verify's logits, in place, and the greedy choice under them into target.  The rows
+        of a prompt follow no proposals."""
+        self.rules.apply(self._logits(H), history=self.transcript, hist_len=self.out_len,
+                         block=None if prompt else block, block_len=blen,
+                         mask_row=self.states(H) if self.rules.has_masks else None,
+                         target=target.view(-1)[: self.n * H].view(self.n, H))
+
     def _args(self, mode, H, block, blen, target, next_block, next_len, p_logits=None, q_logits=None,
               temperature=0.0, seed=0, rnd=0) -> B.AcceptArgs:
         a = B.AcceptArgs()
@@ -228,7 +272,11 @@ class Batch:
         d = self.dec
         d.reset(self.req)
         sampled = temperature > 0.0 and self.p_logits is not None
-        d.verify(self.req, self.prompt, self.plen, self.ptarget, self.p_logits if sampled else None)
+        P = self.prompt.shape[1]
+        d.verify(self.req, self.prompt, self.plen, self.ptarget,
+                 self._logits(P) if self.rules is not None else self.p_logits if sampled else None)
+        if self.rules is not None:
+            self._apply_rules(P, self.prompt, self.plen, self.ptarget, prompt=True)
         nb = self.block1 if ar else self.block
         a = self._args(B.WS_ACCEPT_FORCED, self.prompt.shape[1], self.prompt, self.plen, self.ptarget, nb,
                        self.blen, self.p_logits if sampled else None, None, temperature if sampled else 0.0,
@@ -241,18 +289,25 @@ class Batch:
         d = self.dec
 
         def calls():
-            d.verify(self.req, self.block1, self.blen, self.target1)
+            d.verify(self.req, self.block1, self.blen, self.target1,
+                     self._logits(1) if self.rules is not None else None)
+            if self.rules is not None:
+                self._apply_rules(1, self.block1, self.blen, self.target1)
             a = self._args(B.WS_ACCEPT_GREEDY, 1, self.block1, self.blen, self.target1, self.block1, self.blen)
             B.ws_accept(d.ctx, self.n, self.req.data_ptr(), a, _stream())
+        self.states(1)                     # allocated outside the capture
         if graph:
-            self.replay(("ar",), calls)
+            self.replay(("ar", d.accumulating), calls)
         else:
             calls()
 
     def ar_sample_step(self, rnd: int, temperature: float, seed: int):
         """Autoregressive sampling round: verify the anchor, draw from softmax(z/T)."""
         d = self.dec
-        d.verify(self.req, self.block1, self.blen, self.target1, self.p_logits)
+        d.verify(self.req, self.block1, self.blen, self.target1,
+                 self._logits(1) if self.rules is not None else self.p_logits)
+        if self.rules is not None:
+            self._apply_rules(1, self.block1, self.blen, self.target1)
         a = self._args(B.WS_ACCEPT_SAMPLE, 1, self.block1, self.blen, self.target1, self.block1, self.blen,
                        self.p_logits, self.q_logits, temperature, seed, rnd)
         B.ws_accept(d.ctx, self.n, self.req.data_ptr(), a, _stream())
@@ -267,15 +322,19 @@ class Batch:
         on the round.  tree: the drafter's ranked tokens fill the decoder's
         candidate tree (set_tree), verified in one pass and accepted along
         the longest matching root path (greedy only)."""
+        self.states(self.dec.K + 1 if k_verify is None else k_verify + 1)     # allocated outside a capture
+        self.states(self.dec.K + 1)
         if tree:
             if temperature > 0.0 or synthetic is not None or not run_drafter or self.dec.tree is None:
                 raise ValueError("tree rounds need set_tree, the drafter and greedy decoding")
+            if self.rules is not None:
+                raise ValueError("logits rules follow linear blocks: not in tree rounds")
             if graph:
-                self.replay(("tree", self.dec.tree), self._tree_calls)
+                self.replay(("tree", self.dec.tree, self.dec.accumulating), self._tree_calls)
             else:
                 self._tree_calls()
         elif graph and temperature <= 0.0:
-            self.replay(("spec", synthetic is not None, run_drafter, k_verify, threshold),
+            self.replay(("spec", synthetic is not None, run_drafter, k_verify, threshold, self.dec.accumulating),
                         lambda: self._spec_calls(0, synthetic, 0.0, 0, run_drafter, k_verify, threshold))
         else:
             self._spec_calls(rnd, synthetic, temperature, seed, run_drafter, k_verify, threshold)
@@ -313,7 +372,11 @@ class Batch:
                              _ptr(self.q_logits) if threshold > 0.0 else 0, k_verify, threshold, temperature,
                              vb.data_ptr(), H, self.blen.data_ptr(), _stream())
         B.ws_verify(d.ctx, self.n, self.req.data_ptr(), H, vb.data_ptr(), self.blen.data_ptr(),
-                    self.target.data_ptr(), _ptr(self.p_logits) if sampling else 0, _stream())
+                    self.target.data_ptr(),
+                    self._logits(H).data_ptr() if self.rules is not None else _ptr(self.p_logits) if sampling else 0,
+                    _stream())
+        if self.rules is not None:
+            self._apply_rules(H, vb.view(-1)[: self.n * H].view(self.n, H), self.blen, self.target)
         mode = B.WS_ACCEPT_SAMPLE if sampling else B.WS_ACCEPT_GREEDY
         a = self._args(mode, H, vb, self.blen, self.target, self.block, self.blen,
                        self.p_logits, self.q_logits, temperature, seed, rnd)
@@ -332,23 +395,51 @@ class Batch:
         return [list(map(int, t[i, :n[i]])) for i in range(self.n)]
 
 
-def run_ar(dec: Decoder, batch: Batch, max_rounds: int = 100000) -> int:
+def _frames_round(dec: Decoder, batch: Batch, rounds: int, keep_frames, evict_after: int):
+    """Before round `rounds` (0: the prompt): frame weights are accumulated up to round `evict_after`, after which
+    the caches are cut to keep_frames."""
+    if keep_frames is None or rounds > evict_after:
+        return
+    if rounds == 0:
+        dec.frame_mass()[:, batch.req.long()] = 0
+        dec.accumulate_frames(True)
+    if rounds == evict_after:
+        dec.accumulate_frames(False)
+        dec.evict_frames(batch.req, keep_frames)
+
+
+def run_ar(dec: Decoder, batch: Batch, max_rounds: int = 100000, keep_frames: int | None = None,
+           evict_after: int = 8) -> int:
+    """keep_frames: after `evict_after` rounds keep only that many acoustic frames per layer and head, those with the
+    most attention so far (approximate)."""
+    _frames_round(dec, batch, 0, keep_frames, max(1, evict_after))
     batch.prefill(ar=True)
     rounds = 0
     while batch.poll_done() < batch.n and rounds < max_rounds:
+        if rounds:
+            _frames_round(dec, batch, rounds, keep_frames, max(1, evict_after))
         batch.ar_step()
         rounds += 1
+    if dec.accumulating and keep_frames is not None:
+        dec.accumulate_frames(False)
     return rounds
 
 
 def run_spec(dec: Decoder, batch: Batch, synthetic=None, temperature=0.0, seed=0, max_rounds=100000,
-             run_drafter=True, graph=True, k_verify=None, threshold=0.0, tree=False) -> int:
+             run_drafter=True, graph=True, k_verify=None, threshold=0.0, tree=False, keep_frames: int | None = None,
+             evict_after: int = 8) -> int:
+    """keep_frames, evict_after: as for run_ar."""
+    _frames_round(dec, batch, 0, keep_frames, max(1, evict_after))
     batch.prefill(temperature=temperature, seed=seed)
     rounds = 0
     while batch.poll_done() < batch.n and rounds < max_rounds:
+        if rounds:
+            _frames_round(dec, batch, rounds, keep_frames, max(1, evict_after))
         batch.spec_step(rounds + 1, synthetic, temperature, seed, run_drafter, graph=graph, k_verify=k_verify,
                         threshold=threshold, tree=tree)
         rounds += 1
+    if dec.accumulating and keep_frames is not None:
+        dec.accumulate_frames(False)
     return rounds
 
 
@@ -609,6 +700,7 @@ class LogitsRules:
     def __init__(self, repetition=None, presence=None, frequency=None, window: int = 0, bias_ids=None, bias_vals=None,
                  bias_len=None, masks=None):
         self._own = (repetition, presence, frequency, bias_ids, bias_vals, bias_len, masks)
+        self.has_masks = masks is not None
         self._args = B.RulesArgs()
         self._args.window = window
         self._shape = None                 # (n, vocab, device) that the object's tensors were checked for
