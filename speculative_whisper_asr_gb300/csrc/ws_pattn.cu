@@ -552,7 +552,7 @@ struct Plan {
   int row_tiles = 1, nsplit = 1, tps = 1;
   bool stash = false;                      // the streaming kernel adds the mass itself
   TileGeo geo;
-  size_t lse = 0, ml = 0, o = 0, nl = 0, bytes = 0;
+  size_t lse = 0, ml = 0, o = 0, nl = 0, next = 0, bytes = 0;
 };
 constexpr int SMS = 152, SLOTS = 2 * SMS;  // two streaming CTAs on each of 152 SMs
 
@@ -591,7 +591,10 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
     q.tps = (tiles + want - 1) / want;
     q.nsplit = (tiles + q.tps - 1) / q.tps;
     partials(R);
-    if (a.mass) q.nl = take((size_t)a.n_req * c.n_kv_heads * q.row_tiles * FA_ROWS * 4);
+    if (a.mass) {
+      q.nl = take((size_t)a.n_req * c.n_kv_heads * q.row_tiles * FA_ROWS * 4);
+      q.next = take(8);
+    }
     return q;
   }
   if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
@@ -667,7 +670,7 @@ cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int 
   p.nsplit = q.nsplit; p.tps = q.tps; p.geo = q.geo;
   p.lse = args.lse ? args.lse : args.mass && !q.fa ? (float*)(ws + q.lse) : nullptr;
   p.row_tiles = q.row_tiles;
-  if (q.fa && args.mass) p.nl = (float*)(ws + q.nl);
+  if (q.fa && args.mass) { p.nl = (float*)(ws + q.nl); p.next_item = (unsigned long long*)(ws + q.next); }
   if (q.nsplit > 1) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
   return cache.dtype == WS_BF16 ? run_bf16(p, q, s) : run_f32(p, q, s);
 }

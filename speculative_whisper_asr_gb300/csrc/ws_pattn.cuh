@@ -48,6 +48,7 @@ struct AttnP {
   int row_tiles;                           // row tiles per (request, KV head)
   float* nl;                               // tcgen05 path with mass: -lse * log2(e) of every row tile's rows
                                            // [n_req][Hkv][row_tiles][128], 16-byte aligned; else null
+  unsigned long long* next_item;           // with nl: counter of the weight pass's work items, cleared by fa_kernel
 };
 
 struct Req {

@@ -12,8 +12,8 @@
 //   warps 2..5  softmax of A, warps 6..9 of B: one thread per row
 // Tensor memory (512 columns): S, P and O of each tile have columns of their
 // own, so the next S is computed as soon as the softmax has S in registers.
-// The row's reference maximum moves only when a score passes it by more than
-// 2^8; then O is rescaled in tensor memory.  With head width 64 a score costs
+// The row's reference is the maximum of its first tile; it moves, and O is
+// rescaled in tensor memory, only when a tile's weights pass 2^60.  With head width 64 a score costs
 // 256 FLOP and one exponential, so the exponentials bound the kernel as much
 // as the tensor core does; scaling and sums are packed pairs (f32x2).
 //
@@ -32,7 +32,7 @@ constexpr int FA_SMEM = 2 * TILE + NST * 2 * TILE + 1024;
 constexpr uint32_t TM_S = 0, TM_P = 256, TM_O = 384;   // + 128 w, + 64 w, + 64 w
 constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
 constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, 64) | (1u << 16);   // B (V) is N-major
-constexpr float HOLD = 8.0f;
+constexpr float MOST = 1152921504606846976.0f;     // 2^60: largest sum of a tile's weights before a row's reference moves
 
 struct Meta { uint32_t valid[4]; int base; int full; };
 
@@ -163,6 +163,25 @@ __device__ __forceinline__ TileInfo tile_info(const AttnP& p, int t, int page, i
   return f;
 }
 
+// The request whose visible length has rank z among the call's, the longest
+// first (its own index where there are more than 128 requests): CTAs start in
+// order, so the short ones end up filling the last round.  All threads call.
+__device__ __forceinline__ int longest_first(const AttnP& p, int z) {
+  __shared__ int len[128];
+  __shared__ int s_req;
+  const int n = p.a.n_req, x = threadIdx.x;
+  if (n > 128 || n == 1) return z;
+  if (x < n) len[x] = request(p, x).L;
+  __syncthreads();
+  if (x < n) {
+    int rank = 0;
+    for (int y = 0; y < n; ++y) rank += len[y] > len[x] || (len[y] == len[x] && y < x);
+    if (rank == z) s_req = x;
+  }
+  __syncthreads();
+  return s_req;
+}
+
 struct Bars {
   uint64_t q_full[2], full[NST], empty[NST], raw, s_full[2], s_free[2], p_full[2], pv_done[2];
 };
@@ -176,9 +195,10 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  if (p.next_item && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next_item = 0ull;
   const int pairs = (p.row_tiles + 1) / 2;
   const int pair = pairs - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
-  const int h = blockIdx.y, i = blockIdx.z;
+  const int h = blockIdx.y, i = longest_first(p, blockIdx.z);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Req r = request(p, i);
   const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
@@ -347,7 +367,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     const bool on = x < TR && rho < R;
     const int t = on ? rho / p.G : 0;
     const int lim = on ? row_limit(p, r, t) : 0, lim_all = first < R ? row_limit(p, r, first / p.G) : 0;
-    const float sl = p.sl, hold = fminf(HOLD / sl, 1e30f);
+    const float sl = p.sl;
     const float2 sl2 = make_float2(sl, sl);
     float m = -INFINITY, msl = 0.f, l = 0.f;
     bool ok = true;
@@ -375,17 +395,40 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
             if (!((see >> e) & 1u)) sv[32 * q + e] = -INFINITY;
         }
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < FA_KEYS; e += 8)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
-      const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
       // P and O are free once the previous product has finished
       if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
-      const bool grow = top > m + hold;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float mn = grow ? top : m;
+      float2 sum2[2];
+      auto weigh = [&]() {
+        const float2 nm2 = make_float2(-msl, -msl);
+        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 y = __ffma2_rn(make_float2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), sl2, nm2);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum2[e & 1] = __fadd2_rn(sum2[e & 1], y);
+            u[e] = pack_bf(y.x, y.y);
+          }
+          tm_st16(tP + 16 * q, u);
+        }
+        return (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+      };
+      // The weights go by the reference at hand.  A floating sum does not mind
+      // large weights, so the maximum is looked for only where a row has no
+      // reference yet or its sum grew past 2^60 (the scores are still in
+      // registers then).
+      float tile = 0.f;
+      if (j > 0) tile = weigh();
+      if (__any_sync(0xffffffffu, m == -INFINITY || !(tile < MOST))) {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < FA_KEYS; e += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
+        const float mn = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]));
         const float f = m > -INFINITY ? ex2((m - mn) * sl) : (mn > -INFINITY ? 0.f : 1.f);
         m = mn;
         msl = mn > -INFINITY ? mn * sl : 0.f;
@@ -403,23 +446,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
             tm_st16(tO + 16 * d, v);
           }
         }
+        tile = weigh();
       }
-      const float2 nm2 = make_float2(-msl, -msl);
-      float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t u[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 y = __ffma2_rn(make_float2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), sl2, nm2);
-          y.x = ex2(y.x);
-          y.y = ex2(y.y);
-          sum2[e & 1] = __fadd2_rn(sum2[e & 1], y);
-          u[e] = pack_bf(y.x, y.y);
-        }
-        tm_st16(tP + 16 * q, u);
-      }
-      l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+      l += tile;
       st_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -471,13 +500,16 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
 }
 
 // ------------------------------------------------------------------ accumulated weights
-// Work items are key tiles of (request, KV head); a CTA takes every
-// gridDim-th, two CTAs per SM (256 tensor memory columns each: S twice).  The
+// Work items are key tiles of (request, KV head), drawn from a counter (a
+// fixed share per CTA left the last one 25% behind); two CTAs per SM (256
+// tensor memory columns each: S twice).  The
 // producer runs up to MST row tiles ahead, across items, so that the next
 // item's lengths, pages and keys arrive under the current one's sums: a CTA
-// per item spent a third of its time on its first tile.
+// per item spent a third of its time on its first tile.  Two groups of four
+// warps take alternate row tiles, one S buffer each: a scheduler then has four
+// warps to choose from while exponentials are under way.
 constexpr int MST = 4;                             // row tile stages
-constexpr int MTHREADS = 192;                      // producer, MMA, four summing warps
+constexpr int MTHREADS = 320;                      // producer, MMA, two groups of four summing warps
 constexpr int MASS_SMEM = 2 * TILE + MST * TILE + 1024;
 
 struct MassItem {
@@ -486,7 +518,7 @@ struct MassItem {
   int q_lo, R, c, L;                               // first row tile; rows, chunk length, cache length
   float* mass;
 };
-struct MassBars { uint64_t k_full[2], k_empty[2], q_full[MST], empty[MST], s_full[2], s_free[2]; };
+struct MassBars { uint64_t k_full[2], k_empty[2], q_full[MST], empty[MST], s_full[2], s_free[2], t_full[2]; };
 
 __global__ void __launch_bounds__(MTHREADS, 2)
 fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant__ CUtensorMap mq,
@@ -495,6 +527,7 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   __shared__ __align__(8) MassBars B;
   __shared__ MassItem item[2];
   __shared__ __align__(16) float nlse[MST][FA_ROWS];   // -lse * log2(e) of a tile's rows
+  __shared__ float half[2][FA_KEYS];                   // the second group's sums of an item
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
@@ -506,6 +539,7 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&B.k_full[b], 1); tc::mbar_init(&B.k_empty[b], 4);
       tc::mbar_init(&B.s_full[b], 1); tc::mbar_init(&B.s_free[b], 4);
+      tc::mbar_init(&B.t_full[b], 4);
     }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -521,6 +555,11 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   if (warp == 0) {
     // ---- producer: key tiles, and row tiles with their log-sum-exps
     int n = 0, g = 0;                              // items and row tiles handed over
+    auto draw = [&]() {                            // the next item nobody has
+      long long x = 0;
+      if (lane == 0) x = (long long)atomicAdd(p.next_item, 1ull) + gridDim.x;
+      return __shfl_sync(0xffffffffu, x, 0);
+    };
     long long it = blockIdx.x;
     auto where = [&](long long x, int& kt, int& h, int& i) {
       const long long u = x / tiles;
@@ -532,7 +571,7 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
     if (it < items) { where(it, kt, h, i); r = request(p, i); }
     while (it < items && ok) {
       // the next item's lengths are asked for now
-      const long long it2 = it + gridDim.x;
+      const long long it2 = draw();
       int kt2 = 0, h2 = 0, i2 = 0;
       Req r2 = {};
       if (it2 < items) { where(it2, kt2, h2, i2); r2 = request(p, i2); }
@@ -582,7 +621,7 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   } else if (warp == 1) {
     const uint32_t lead = elect_one();
     const uint64_t kd0 = tc::sdesc_sw128(tc::smem_u32(sK(0))), qd0 = tc::sdesc_sw128(tc::smem_u32(sQ(0)));
-    int g = 0;
+    int g = 0, used[2] = {0, 0};                   // row tiles so far, and of each S buffer
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int kb = n & 1;
@@ -590,10 +629,11 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
       const int nt = item[kb].nt;
       if (nt < 0) break;
       for (int j = 0; j < nt; ++j) {
-        const int s = g % MST, b = g & 1;
+        const int s = g % MST, b = j & 1;          // an item's even tiles go to the first group, odd ones to the second
         ok = wait(&B.q_full[s], (uint32_t)((g / MST) & 1), abort) &&
-             (g < 2 || wait(&B.s_free[b], (uint32_t)((g / 2 - 1) & 1), abort));
+             (used[b] == 0 || wait(&B.s_free[b], (uint32_t)((used[b] - 1) & 1), abort));
         if (!ok) break;
+        ++used[b];
         tc::tc_fence_after();
         if (lead) {
           const uint64_t kd = kd0 + (uint64_t)(kb * (TILE >> 4)), qd = qd0 + (uint64_t)(s * (TILE >> 4));
@@ -607,15 +647,16 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
       }
     }
     if (*abort && lane == 0)
-      for (int x = max(0, g - 2); x < g; ++x) tc::mbar_wait(&B.s_full[x & 1], (uint32_t)((x / 2) & 1));
+      for (int b = 0; b < 2; ++b)
+        if (used[b] > 0) tc::mbar_wait(&B.s_full[b], (uint32_t)((used[b] - 1) & 1));
     __syncwarp();
   } else {
     // ---- sums: thread = key
-    const int quarter = warp & 3;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int quarter = warp & 3, group = warp >= 6 ? 1 : 0;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + 128u * group;
     const float2 sl2 = make_float2(p.sl, p.sl);
     bool ok = true;
-    int g = 0;
+    int g = 0, used = 0;
     for (int n = 0; ok; ++n) {
       const int kb = n & 1;
       if (!wait_warp(&B.k_full[kb], (uint32_t)((n / 2) & 1), abort)) break;
@@ -626,49 +667,63 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
       const int first = p.a.causal ? max(0, pos - (m.L - m.c)) * p.G : 0;      // first row that sees this key
       float* mass = m.mass + pos;
       const bool on = (m.valid[quarter] >> lane) & 1u;
-      float total = 0.f;
+      float2 total = make_float2(0.f, 0.f);
       for (int j = 0; j < nt; ++j, ++g) {
-        const int s = g % MST, b = g & 1, rho = (q_lo + j) * TR;
-        if (!wait_warp(&B.s_full[b], (uint32_t)((g / 2) & 1), abort)) { ok = false; break; }
+        if ((j & 1) != group) continue;
+        const int s = g % MST, rho = (q_lo + j) * TR;
+        if (!wait_warp(&B.s_full[group], (uint32_t)(used & 1), abort)) { ok = false; break; }
+        ++used;
         tc::tc_fence_after();
-        float sv[FA_ROWS];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tm_ld32(tl + 128u * b + 32 * q, sv + 32 * q);
-        ld_wait();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(&B.s_free[b]);
         const int cmin = first - rho, cmax = min(TR, R - rho);                 // columns that see this key
-        const float4* nl = reinterpret_cast<const float4*>(nlse[s]);
-        if (__all_sync(0xffffffffu, cmin <= 0 && cmax == FA_ROWS)) {
-          float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const bool whole = __all_sync(0xffffffffu, cmin <= 0 && cmax == FA_ROWS);
+        float buf[2][32];
+        tm_ld32(tl, buf[0]);
 #pragma unroll
-          for (int e = 0; e < FA_ROWS / 4; ++e) {
-            const float4 n4 = nl[e];
-            float2 a = __ffma2_rn(make_float2(sv[4 * e], sv[4 * e + 1]), sl2, make_float2(n4.x, n4.y));
-            float2 c = __ffma2_rn(make_float2(sv[4 * e + 2], sv[4 * e + 3]), sl2, make_float2(n4.z, n4.w));
-            a.x = ex2(a.x); a.y = ex2(a.y);
-            c.x = ex2(c.x); c.y = ex2(c.y);
-            sum2[0] = __fadd2_rn(sum2[0], a);
-            sum2[1] = __fadd2_rn(sum2[1], c);
+        for (int q = 0; q < 4; ++q) {
+          float* sv = buf[q & 1];
+          ld_wait();
+          if (q < 3) {
+            tm_ld32(tl + 32 * (q + 1), buf[(q + 1) & 1]);
+          } else {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&B.s_free[group]);
           }
-          total += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-        } else {
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          const float4* nl = reinterpret_cast<const float4*>(nlse[s] + 32 * q);
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < FA_ROWS; ++e) {
-            const float y = ex2(fmaf(sv[e], p.sl, nlse[s][e]));
-            if (e >= cmin && e < cmax && nlse[s][e] > -INFINITY) part[e & 3] += y;
+            for (int e = 0; e < 8; ++e) {
+              const float4 n4 = nl[e];
+              float2 a = __ffma2_rn(make_float2(sv[4 * e], sv[4 * e + 1]), sl2, make_float2(n4.x, n4.y));
+              float2 c = __ffma2_rn(make_float2(sv[4 * e + 2], sv[4 * e + 3]), sl2, make_float2(n4.z, n4.w));
+              a.x = ex2(a.x); a.y = ex2(a.y);
+              c.x = ex2(c.x); c.y = ex2(c.y);
+              total = __fadd2_rn(total, __fadd2_rn(a, c));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = nlse[s][32 * q + e], y = ex2(fmaf(sv[e], p.sl, x));
+              if (32 * q + e >= cmin && 32 * q + e < cmax && x > -INFINITY) total.x += y;
+            }
           }
-          total += (part[0] + part[1]) + (part[2] + part[3]);
         }
         __syncwarp();
         if (lane == 0) arrive(&B.empty[s]);        // the tile's S is computed and its log-sum-exps are read
       }
-      __syncwarp();
-      if (lane == 0) arrive(&B.k_empty[kb]);       // the item's keys and description are read
-      // the position is this thread's alone: the atomic has nothing to race with
-      if (on) atomicAdd(mass, ok ? total : NAN);
+      // the second group's part of the sum, then the first's on top
+      const float part = ok ? total.x + total.y : NAN;
+      if (group == 1) {
+        half[kb][quarter * 32 + lane] = part;
+        __syncwarp();
+        if (lane == 0) arrive(&B.t_full[kb]);
+      } else {
+        if (!wait_warp(&B.t_full[kb], (uint32_t)((n / 2) & 1), abort)) break;
+        // the position is this thread's alone: the atomic has nothing to race with
+        if (on) atomicAdd(mass, part + half[kb][quarter * 32 + lane]);
+        __syncwarp();
+        if (lane == 0) arrive(&B.k_empty[kb]);     // the item's keys, description and sums are read
+      }
     }
     tc::tc_fence_before();
   }
