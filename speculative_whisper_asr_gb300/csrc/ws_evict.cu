@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 2) evict_select(const Evic
   __shared__ int counts[2];                // keys of this CTA above the threshold, and equal to it
   __shared__ int wgt[NT / 32], weq[NT / 32];
   __shared__ int s_bin, s_left;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   const int i = blockIdx.z, h = blockIdx.y, H = p.c.n_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cs = p.cs;
   const uint32_t rank = cs > 1 ? cluster_rank() : 0u;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(MV_NT) evict_move(const EvictP p) {
   __shared__ Move mv[ROWS];
   const int h = blockIdx.y, i = blockIdx.z, H = p.c.n_kv_heads, j0 = blockIdx.x * ROWS;
   const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   if (slot < 0 || slot >= p.c.n_slots) return;
   const int keep = min(p.len[i], p.a.keep), n = min(ROWS, keep - j0);
   if (h == 0 && j0 == 0 && threadIdx.x == 0) p.a.kv_len_out[slot] = keep;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(MV_NT) evict_compact(const EvictP p) {
   const int h = blockIdx.y, i = blockIdx.z, H = p.c.n_kv_heads;
   const int col = blockIdx.x % COLS, which = blockIdx.x / COLS;
   const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   if (slot < 0 || slot >= p.c.n_slots) return;
   const int keep = min(p.len[i], p.a.keep);
   if (h == 0 && blockIdx.x == 0 && threadIdx.x == 0) p.a.kv_len_out[slot] = keep;
@@ -367,20 +367,11 @@ cudaError_t select(EvictP& p, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t move(const EvictP& p, bool in_place, bool pdl, cudaStream_t s) {
+cudaError_t move(const EvictP& p, bool in_place, cudaStream_t s) {
   constexpr int V = WS_DH * sizeof(T) / 16, ROWS = 8 * MV_NT / (2 * V);
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(in_place ? 2 * WS_DH * sizeof(T) / 32 : (p.a.keep + ROWS - 1) / ROWS, p.c.n_kv_heads, p.a.n_req);
-  c.blockDim = dim3(MV_NT);
-  c.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = pdl ? 1 : 0;
-  const cudaError_t e = in_place ? cudaLaunchKernelEx(&c, evict_compact<T>, p) : cudaLaunchKernelEx(&c, evict_move<T>, p);
-  if (e == cudaSuccess) ws_count_launches(1);
-  return e;
+  if (in_place)
+    return launch_after(evict_compact<T>, dim3(2 * WS_DH * sizeof(T) / 32, p.c.n_kv_heads, p.a.n_req), MV_NT, 0, s, p);
+  return launch_after(evict_move<T>, dim3((p.a.keep + ROWS - 1) / ROWS, p.c.n_kv_heads, p.a.n_req), MV_NT, 0, s, p);
 }
 
 }  // namespace
@@ -397,11 +388,9 @@ cudaError_t launch_cache_evict(const ws_paged_cache& cache, const ws_evict_args&
   p.len = (int32_t*)workspace;
   p.idx = (int32_t*)((char*)workspace + ((size_t)args.n_req * 4 + 255) / 256 * 256);
   p.ordered = args.mass_out == args.mass || (args.pos && args.pos_out == args.pos);
-  // programmatic dependent launch only on created streams, as elsewhere in the library
-  const bool pdl = s != nullptr && s != cudaStreamLegacy && s != cudaStreamPerThread;
   cudaError_t e = args.max_kv <= 4096 ? select<256>(p, s) : select<512>(p, s);
   if (e != cudaSuccess) return e;
-  return cache.dtype == WS_BF16 ? move<bf16>(p, in_place, pdl, s) : move<float>(p, in_place, pdl, s);
+  return cache.dtype == WS_BF16 ? move<bf16>(p, in_place, s) : move<float>(p, in_place, s);
 }
 
 extern "C" size_t ws_cache_evict_workspace(const ws_paged_cache* cache, const ws_evict_args* args) {

@@ -40,6 +40,26 @@ inline int paged_fail(int code, const std::string& msg) {
   return code;
 }
 
+// Launch of a kernel that begins with pdl_wait(): on created streams it may
+// start while the kernel before it (which calls pdl_trigger()) still runs, as
+// elsewhere in the library.
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = s != nullptr && s != cudaStreamLegacy && s != cudaStreamPerThread ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+  if (e == cudaSuccess) ws_count_launches(1);
+  return e;
+}
+
 // Page of position j of a slot, or -1 where it may not be read.
 __device__ __forceinline__ int paged_page(const ws_paged_cache& c, const int32_t* table, int stride, int slot, int j) {
   const int p = j / c.page_size;

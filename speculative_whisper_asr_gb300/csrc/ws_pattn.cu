@@ -125,6 +125,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rt = blockIdx.x / p.nsplit, split = blockIdx.x - rt * p.nsplit, h = blockIdx.y, i = blockIdx.z;
+  pdl_trigger();
   // the first tiles' pages are asked for together with the lengths: the
   // entries exist whatever the lengths turn out to be
   const int slot0 = p.a.req_ids ? p.a.req_ids[i] : i;
@@ -403,7 +404,9 @@ template <typename T>
 __global__ void __launch_bounds__(128) combine_kernel(const AttnP p) {
   const int lane = threadIdx.x & 31, h = blockIdx.y, i = blockIdx.z;
   const int rho = blockIdx.x * 4 + (threadIdx.x >> 5);
+  pdl_trigger();
   const Req r = request(p, i);
+  pdl_wait();
   if (rho >= r.c * p.G) return;
   const size_t at = (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit;
   float M = -INFINITY;
@@ -468,6 +471,7 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnP p) {
       }
     }
   const int R = r.c * p.G;
+  pdl_wait();                              // the log-sum-exps
   float sum[2][2] = {};
   // rows before the first that sees position k0 add nothing
   const int first = p.a.causal ? max(0, k0 - (r.L - r.c)) * p.G : 0;
@@ -631,28 +635,24 @@ cudaError_t run_streaming(const AttnP& p, const Plan& q, cudaStream_t s) {
   return q.stash ? run_split<4, true>(p, q, mk, mv, s) : run_split<4, false>(p, q, mk, mv, s);
 }
 
+template <typename T>
+cudaError_t combine(const AttnP& p, cudaStream_t s) {
+  return launch_after(combine_kernel<T>, dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128,
+                      0, s, p);
+}
+
 cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
-  const cudaError_t e = q.fa ? launch_fa(p, s) : run_streaming(p, q, s);
-  if (e != cudaSuccess) return e;
-  if (q.nsplit > 1) {
-    combine_kernel<bf16><<<dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
-    ws_count_launches(1);
-  }
-  if (!p.a.mass || p.a.max_kv == 0 || q.stash) return cudaGetLastError();
+  cudaError_t e = q.fa ? launch_fa(p, s) : run_streaming(p, q, s);
+  if (e == cudaSuccess && q.nsplit > 1) e = combine<bf16>(p, s);
+  if (e != cudaSuccess || !p.a.mass || p.a.max_kv == 0 || q.stash) return e;
   if (q.fa) return launch_fa_mass(p, s);
-  mass_kernel<<<dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
-  ws_count_launches(1);
-  return cudaGetLastError();
+  return launch_after(mass_kernel, dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s, p);
 }
 
 cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
-  const cudaError_t e = launch_f32(p, q.wide, s);
-  if (e != cudaSuccess) return e;
-  if (q.nsplit > 1) {
-    combine_kernel<float><<<dim3((unsigned)(((long long)p.a.max_q * p.G + 3) / 4), p.c.n_kv_heads, p.a.n_req), 128, 0, s>>>(p);
-    ws_count_launches(1);
-  }
-  if (!p.a.mass || p.a.max_kv == 0) return cudaGetLastError();
+  cudaError_t e = launch_f32(p, q.wide, s);
+  if (e == cudaSuccess && q.nsplit > 1) e = combine<float>(p, s);
+  if (e != cudaSuccess || !p.a.mass || p.a.max_kv == 0) return e;
   return launch_f32_mass(p, q.wide, s);
 }
 

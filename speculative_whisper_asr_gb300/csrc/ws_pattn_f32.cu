@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(NT, 2) f32_kernel(const AttnP p) {
   extern __shared__ __align__(16) float fsm[];
   __shared__ uint32_t s_valid[2][2];
   const int rt = blockIdx.x / p.nsplit, split = blockIdx.x - rt * p.nsplit, h = blockIdx.y, i = blockIdx.z;
+  pdl_trigger();
   const Req r = request(p, i);
   constexpr int TQ = 16 * RPT;
   const int R = r.c * p.G, r0 = rt * TQ;
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(NT, 2) f32_mass_kernel(const AttnP p) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, R = r.c * p.G;
   const bool valid = load_keys(p, r, h, j0, r.L, sk, nullptr);
   cp_commit();
+  pdl_wait();                                      // the log-sum-exps
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   // rows before the first that sees position j0 add nothing
   for (int r0 = p.a.causal ? max(0, j0 - (r.L - r.c)) * p.G : 0; r0 < R; r0 += TQ) {
@@ -258,9 +260,8 @@ cudaError_t run_f32(const AttnP& p, cudaStream_t s) {
 }
 template <int RPT>
 cudaError_t run_mass(const AttnP& p, cudaStream_t s) {
-  f32_mass_kernel<RPT><<<dim3((p.a.max_kv + TK - 1) / TK, p.c.n_kv_heads, p.a.n_req), NT, mass_smem<RPT>(), s>>>(p);
-  ws_count_launches(1);
-  return cudaGetLastError();
+  return launch_after(f32_mass_kernel<RPT>, dim3((p.a.max_kv + TK - 1) / TK, p.c.n_kv_heads, p.a.n_req), NT,
+                      mass_smem<RPT>(), s, p);
 }
 
 }  // namespace

@@ -195,6 +195,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  pdl_trigger();
   if (p.next_item && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next_item = 0ull;
   const int pairs = (p.row_tiles + 1) / 2;
   const int pair = pairs - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
@@ -548,6 +549,7 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  pdl_wait();                                      // the log-sum-exps and the counter
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   auto sK = [&](int b) { return sm + b * TILE; };
   auto sQ = [&](int b) { return sm + 2 * TILE + b * TILE; };
@@ -760,8 +762,6 @@ cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s) {
   const int tiles = tile_count(p.geo, p.c.page_size, FA_KEYS, p.a.max_kv);
   const long long items = (long long)tiles * p.c.n_kv_heads * p.a.n_req;
   if (items == 0) return cudaSuccess;
-  fa_mass_kernel<<<(unsigned)(items < 2 * 152 ? items : 2 * 152), MTHREADS, MASS_SMEM, s>>>(
-      p, tiles, items, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk));
-  ws_count_launches(1);
-  return cudaGetLastError();
+  return launch_after(fa_mass_kernel, dim3((unsigned)(items < 2 * 152 ? items : 2 * 152)), MTHREADS, MASS_SMEM, s, p, tiles,
+                      items, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk));
 }
