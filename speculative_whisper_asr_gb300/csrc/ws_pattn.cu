@@ -550,12 +550,14 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
 
 // The launch shape and the workspace of a call: a function of the host sizes.
 struct Plan {
+  F32Rows rows = {};                       // fp32, up to 16 rows
   bool wide = false;                       // fp32: row tiles of 64 rows, not 16
   bool fa = false;                         // tcgen05 row tiles instead of streaming ones
   int nt = 1;                              // streaming row tile: 8 * nt rows
   int row_tiles = 1, nsplit = 1, tps = 1;
   bool stash = false;                      // the streaming kernel adds the mass itself
   TileGeo geo;
+  bool parts = false;                      // the first kernel leaves partials to be joined
   size_t lse = 0, ml = 0, o = 0, nl = 0, next = 0, bytes = 0;
 };
 constexpr int SMS = 152, SLOTS = 2 * SMS;  // two streaming CTAs on each of 152 SMs
@@ -565,22 +567,30 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   const long long R = (long long)a.max_q * (a.n_heads / c.n_kv_heads);
   auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += (n + 255) / 256 * 256; return at; };
   auto partials = [&](long long R_) {
-    if (q.nsplit <= 1) return;
+    if (q.nsplit <= 1 && c.dtype == WS_BF16) return;
+    q.parts = true;
     const size_t rows = (size_t)a.n_req * c.n_kv_heads * R_ * q.nsplit;
     q.ml = take(rows * 8);
     q.o = take(rows * WS_DH * 4);
   };
   if (c.dtype != WS_BF16) {
-    if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
+    q.geo = tile_geo(c.page_size, F32_KEYS);
     q.wide = R > 16;
-    q.row_tiles = (int)((R + (q.wide ? 63 : 15)) / (q.wide ? 64 : 16));
+    if (!q.wide) {
+      q.rows = f32_rows_plan((long long)a.n_req * c.n_kv_heads, a.max_kv, a.mass != nullptr);
+      if (q.rows.join) return q;
+      q.nsplit = q.rows.ctas;
+    }
+    if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
+    if (!q.wide) { partials(R); return q; }
+    q.row_tiles = (int)((R + 63) / 64);
     const int tiles = max(1, (a.max_kv + F32_KEYS - 1) / F32_KEYS);
     const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
     // enough CTAs for two rounds of two per SM
     const int want = (int)min((2ll * SLOTS + units - 1) / units, (long long)tiles);
     q.tps = (tiles + want - 1) / want;
     q.nsplit = (tiles + q.tps - 1) / q.tps;
-    partials(R);
+    if (q.nsplit > 1) partials(R);
     return q;
   }
   const int G = a.n_heads / c.n_kv_heads;
@@ -643,16 +653,16 @@ cudaError_t combine(const AttnP& p, cudaStream_t s) {
 
 cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
   cudaError_t e = q.fa ? launch_fa(p, s) : run_streaming(p, q, s);
-  if (e == cudaSuccess && q.nsplit > 1) e = combine<bf16>(p, s);
+  if (e == cudaSuccess && q.parts) e = combine<bf16>(p, s);
   if (e != cudaSuccess || !p.a.mass || p.a.max_kv == 0 || q.stash) return e;
   if (q.fa) return launch_fa_mass(p, s);
   return launch_after(mass_kernel, dim3((p.a.max_kv + 127) / 128, p.c.n_kv_heads, p.a.n_req), 128, 0, s, p);
 }
 
 cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
-  cudaError_t e = launch_f32(p, q.wide, s);
-  if (e == cudaSuccess && q.nsplit > 1) e = combine<float>(p, s);
-  if (e != cudaSuccess || !p.a.mass || p.a.max_kv == 0) return e;
+  cudaError_t e = q.wide ? launch_f32(p, s) : launch_f32_rows(p, q.rows, s);
+  if (e == cudaSuccess && q.parts) e = combine<float>(p, s);
+  if (e != cudaSuccess || !p.a.mass || p.a.max_kv == 0 || q.rows.join) return e;
   return launch_f32_mass(p, q.wide, s);
 }
 
@@ -668,10 +678,10 @@ cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int 
   p.q_and = args.scale == 0.f ? 0u : 0xffffffffu;
   p.q_xor = args.scale < 0.f ? 0x80008000u : 0u;
   p.nsplit = q.nsplit; p.tps = q.tps; p.geo = q.geo;
-  p.lse = args.lse ? args.lse : args.mass && !q.fa ? (float*)(ws + q.lse) : nullptr;
+  p.lse = args.lse ? args.lse : args.mass && !q.fa && !q.rows.join ? (float*)(ws + q.lse) : nullptr;
   p.row_tiles = q.row_tiles;
   if (q.fa && args.mass) { p.nl = (float*)(ws + q.nl); p.next_item = (unsigned long long*)(ws + q.next); }
-  if (q.nsplit > 1) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
+  if (q.parts) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
   return cache.dtype == WS_BF16 ? run_bf16(p, q, s) : run_f32(p, q, s);
 }
 
