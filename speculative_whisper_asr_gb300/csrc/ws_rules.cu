@@ -31,7 +31,8 @@ constexpr int MAX_CL = 8;                  // portable cluster size
 constexpr uint32_t FREE = 0xFFFFFFFFu;     // hash table: no id here
 
 // Shared memory: table (ids, counts / new logits, first bias entries), then
-// the row's grammar mask and the bitmap of the listed ids, a word per 32 ids.
+// the row's grammar mask and the bitmap of the listed ids, a word per 32 ids
+// counted from the row's 16-byte boundary.
 struct Table { int slots, words; };
 inline size_t rules_smem(const Table& t) { return (size_t)t.slots * 12 + (size_t)t.words * 8; }
 
@@ -44,11 +45,13 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   const uint32_t u = (uint32_t)(k >> 32);
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
-__device__ __forceinline__ float exp_of(float x) {
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float exp_of(float x) { return ex2(x * LOG2E); }
 // exp(y - m), with y = m giving 1 also at infinities
 __device__ __forceinline__ float exp_to(float y, float m) { return y == m ? 1.0f : exp_of(y - m); }
 
@@ -101,11 +104,12 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
   const int lo = (int)rank * part, hi = min(lo + part, V + ph);     // part is a multiple of 4
   // groups wholly inside the row; at most one at either end is not
   const int g0 = (lo == 0 && ph ? 4 : lo) >> 2, g1 = min((lo + part) >> 2, (V + ph) >> 2);
+  const float4* zp = reinterpret_cast<const float4*>(z + 4 * (g0 + tid) - ph);
   float4 next[Q];
   auto fetch = [&](int g) {
 #pragma unroll
     for (int k = 0; k < Q; ++k)
-      if (g + k * NT < g1) next[k] = __ldcs(reinterpret_cast<const float4*>(z + 4 * (g + k * NT) - ph));
+      if (g + k * NT < g1) next[k] = __ldcs(zp + k * NT);
   };
   fetch(g0 + tid);
   const int hl = min(max(hist_len, 0), a.hist_stride);
@@ -119,10 +123,11 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
   const int t0 = from + tid < len ? token(from + tid) : -1, e0 = tid < nb ? ids[tid] : -1;
   const bool masked = state >= 0 && state < a.n_masks;
   const uint32_t* mask = a.masks + (masked ? (size_t)state * ((V + 31) / 32) : 0);
-  // this CTA's words of the two bitmaps
-  const int wb = max(lo - ph, 0) >> 5, we = min(tb.words, ((hi - ph + 31) >> 5) + 1);
-  for (int w = wb + tid; w < we; w += NT) {
-    allow[w] = masked && w < (V + 31) / 32 ? __ldg(mask + w) : FREE;
+  // this CTA's words of the two bitmaps, in u: a group's four bits are in one word
+  for (int w = (lo >> 5) + tid; w < min(tb.words, (hi + 31) >> 5); w += NT) {
+    const int words = (V + 31) / 32;
+    const uint32_t a0 = masked && w < words ? __ldg(mask + w) : FREE, a1 = masked && ph && w > 0 ? __ldg(mask + w - 1) : FREE;
+    allow[w] = __funnelshift_l(a1, a0, ph);
     listed[w] = 0u;
   }
   for (int s = tid; s < tb.slots; s += NT) { hid[s] = FREE; hcount[s] = 0u; hbias[s] = FREE; }
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
     uint32_t s = ((uint32_t)id * 2654435761u) >> 7 & (uint32_t)(tb.slots - 1);
     for (;;) {
       const uint32_t old = atomicCAS(&hid[s], FREE, (uint32_t)id);
-      if (old == FREE) atomicOr(&listed[id >> 5], 1u << (id & 31));
+      if (old == FREE) atomicOr(&listed[(id + ph) >> 5], 1u << ((id + ph) & 31));
       if (old == FREE || old == (uint32_t)id) return s;
       s = (s + 1) & (uint32_t)(tb.slots - 1);
     }
@@ -161,12 +166,23 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
       sum *= top > m ? exp_of(m - top) : 1.f;
       m = top;
     }
-    if (fabsf(m) < INFINITY) {
-      for (int k = 0; k < count; k += 4)
-        sum += count < 4 ? exp_of(y[k] - m) : (exp_of(y[k] - m) + exp_of(y[k + 1] - m)) + (exp_of(y[k + 2] - m) + exp_of(y[k + 3] - m));
-    } else {                               // nothing above -inf yet (a NaN still counts), or a row with +inf
+    if (fabsf(m) < 1e37f) {                // the scaled reference stays finite
+      const float ref = m * LOG2E;
+      if (count == 1) {
+        sum += ex2(fmaf(y[0], LOG2E, -ref));
+      } else {
+        float2 s2 = make_float2(0.f, 0.f);
+        for (int k = 0; k + 1 < count; k += 2) {
+          float2 e = __ffma2_rn(make_float2(y[k], y[k + 1]), make_float2(LOG2E, LOG2E), make_float2(-ref, -ref));
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          s2 = __fadd2_rn(s2, e);
+        }
+        sum += s2.x + s2.y;
+      }
+    } else {                               // nothing above -inf yet (a NaN still counts), infinities, lowest values
       for (int k = 0; k < count; ++k) sum += exp_to(y[k], m);
-      if (m < 0.f && sum == sum) sum = 0.f;
+      if (m == -INFINITY && sum == sum) sum = 0.f;
     }
   };
   for (int s = tid; s < tb.slots; s += NT) {
@@ -178,7 +194,7 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
       x = __fsub_rn(x, __fadd_rn(__fmul_rn(freq, (float)hcount[s]), alpha));
     }
     if (hbias[s] != FREE) x = __fadd_rn(x, a.bias_vals[(size_t)i * a.bias_stride + hbias[s]]);
-    if (!((allow[id >> 5] >> (id & 31)) & 1u)) x = -INFINITY;
+    if (!((allow[(id + ph) >> 5] >> ((id + ph) & 31)) & 1u)) x = -INFINITY;
     hcount[s] = __float_as_uint(x);
     add(&x, 1, [&](int) { return id; });
   }
@@ -186,15 +202,16 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
   if (tid < 8) {
     const int u = tid < 4 ? lo + tid : 4 * g1 + tid - 4, v = u - ph;
     const bool edge = tid < 4 ? u < 4 * g0 : u >= 4 * g0;
-    if (edge && v >= 0 && v < V && u < hi && !((listed[v >> 5] >> (v & 31)) & 1u)) {
-      const float x = (allow[v >> 5] >> (v & 31)) & 1u ? z[v] : -INFINITY;
+    if (edge && v >= 0 && v < V && u < hi && !((listed[u >> 5] >> (u & 31)) & 1u)) {
+      const float x = (allow[u >> 5] >> (u & 31)) & 1u ? z[v] : -INFINITY;
       o[v] = x;
       add(&x, 1, [&](int) { return v; });
     }
   }
   __syncthreads();                         // in place, the listed ids are read before the stream stores over them
   // ---- 3: the stream
-  for (int g = g0 + tid; g < g1; g += Q * NT) {
+  float* op = o + 4 * (g0 + tid) - ph;
+  for (int g = g0 + tid; g < g1; g += Q * NT, op += 4 * Q * NT) {
     float y[4 * Q];
 #pragma unroll
     for (int k = 0; k < Q; ++k) {
@@ -204,28 +221,29 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
       y[4 * k + 2] = on ? next[k].z : -INFINITY;
       y[4 * k + 3] = on ? next[k].w : -INFINITY;
     }
+    zp += Q * NT;
     fetch(g + Q * NT);
 #pragma unroll
     for (int k = 0; k < Q; ++k) {
       if (g + k * NT >= g1) continue;
-      const int v = 4 * (g + k * NT) - ph, w = v >> 5, sh = v & 31, w2 = min(w + 1, tb.words - 1);
+      const int w = (g + k * NT) >> 3, sh = (4 * (g + k * NT)) & 31;
       if (masked) {
-        const uint32_t bits = __funnelshift_r(allow[w], allow[w2], sh);
+        const uint32_t bits = allow[w] >> sh;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (!((bits >> e) & 1u)) y[4 * k + e] = -INFINITY;
+          if (!(bits & (1u << e))) y[4 * k + e] = -INFINITY;
       }
       if (ovec) {
-        __stcs(reinterpret_cast<float4*>(o + v), make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
+        __stcs(reinterpret_cast<float4*>(op) + k * NT, make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[v + e] = y[4 * k + e];
+        for (int e = 0; e < 4; ++e) op[4 * k * NT + e] = y[4 * k + e];
       }
-      const uint32_t mine = __funnelshift_r(listed[w], listed[w2], sh) & 15u;
+      const uint32_t mine = listed[w] >> sh & 15u;
       if (mine)                            // taken care of in step 2
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if ((mine >> e) & 1u) y[4 * k + e] = -INFINITY;
+          if (mine & (1u << e)) y[4 * k + e] = -INFINITY;
     }
     add(y, 4 * Q, [&](int k) { return 4 * (g + (k >> 2) * NT) - ph + (k & 3); });
   }
@@ -317,7 +335,7 @@ extern "C" int ws_logits_rules(const ws_rules_args* p, ws_stream stream) {
   Table tb;
   tb.slots = 64;
   while (tb.slots < 2 * most) tb.slots *= 2;
-  tb.words = (a.vocab + 31) / 32 + 1;
+  tb.words = (a.vocab + 3 + 31) / 32;
   const size_t smem = rules_smem(tb);
   // one CTA per row where that gives every SM its two; else the row is shared
   const long long rows = (long long)a.n * a.H;

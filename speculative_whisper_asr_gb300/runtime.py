@@ -556,6 +556,15 @@ def _rows(name, t, dtype, shape, dev):
     return t.data_ptr()
 
 
+def _per_position(name, t, dtype, slots, heads, dev):
+    """Pointer and width of a contiguous [slots, heads, width] tensor."""
+    s = t.shape
+    if (t.dtype is not dtype or t.get_device() != dev or len(s) != 3 or s[0] != slots or s[1] != heads
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor [{slots}, {heads}, width] on cuda:{dev} is needed")
+    return t.data_ptr(), s[2]
+
+
 def _on(dev):
     """The handle of the current stream; device number `dev` has to be the current device."""
     if torch.cuda.current_device() != dev:
@@ -638,8 +647,7 @@ class PagedCache:
         if mass is None:
             a.mass = 0
         else:
-            a.mass_stride = width = mass.shape[-1]
-            a.mass = _rows("mass", mass, _F32, (self.slots, self.heads, width), dev)
+            a.mass, a.mass_stride = _per_position("mass", mass, _F32, self.slots, self.heads, dev)
         s = _on(dev)
         sizes = (n, rows, heads, max_q, max_kv, scale, lse is None, mass is None)
         need = self._need.get(sizes)
@@ -661,22 +669,13 @@ class PagedCache:
         a.kv_len = length
         a.kv_len_out = length if kv_len_out is None else _rows("kv_len_out", kv_len_out, _I32, (slots,), dev)
         a.max_kv, a.keep, a.sink, a.recent = max_kv, keep, sink, recent
-        width = mass.shape[-1]
-        ptr = _rows("mass", mass, _F32, (slots, heads, width), dev)
-        a.mass, a.mass_stride = ptr, width
-        if mass_out is not None:
-            width = mass_out.shape[-1]
-            ptr = _rows("mass_out", mass_out, _F32, (slots, heads, width), dev)
-        a.mass_out, a.mass_out_stride = ptr, width
-        ptr = width = 0
-        if pos is not None:
-            width = pos.shape[-1]
-            ptr = _rows("pos", pos, _I32, (slots, heads, width), dev)
-        a.pos, a.pos_stride = ptr, width
-        if pos_out is not None:
-            width = pos_out.shape[-1]
-            ptr = _rows("pos_out", pos_out, _I32, (slots, heads, width), dev)
-        a.pos_out, a.pos_out_stride = ptr, width
+        ptr = _per_position("mass", mass, _F32, slots, heads, dev)
+        a.mass, a.mass_stride = ptr
+        a.mass_out, a.mass_out_stride = (ptr if mass_out is None
+                                         else _per_position("mass_out", mass_out, _F32, slots, heads, dev))
+        ptr = (0, 0) if pos is None else _per_position("pos", pos, _I32, slots, heads, dev)
+        a.pos, a.pos_stride = ptr
+        a.pos_out, a.pos_out_stride = ptr if pos_out is None else _per_position("pos_out", pos_out, _I32, slots, heads, dev)
         if page_table_out is None:
             a.page_table_out = 0
         else:
