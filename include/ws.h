@@ -448,7 +448,7 @@ typedef struct {
   int32_t n_pages;             /* >= 1 */
   void* k;                     /* 16-byte aligned */
   void* v;                     /* 16-byte aligned */
-  int64_t page_stride, head_stride, token_stride;   /* elements, >= 0; multiples of 16 bytes */
+  int64_t page_stride, head_stride, token_stride;   /* elements, >= 64 (a dimension of one: any); multiples of 16 bytes */
   const int32_t* page_table;   /* [n_slots, table_stride] (device) */
   int32_t n_slots;             /* >= 1 */
   int32_t table_stride;        /* pages listed per slot, >= 1 */

@@ -25,7 +25,9 @@ inline const char* check_paged_cache(const ws_paged_cache* c) {
   // the copy engine's strides end at 2^40 bytes
   const int64_t most = (int64_t)1 << 37;
   if (c->page_stride >= most || c->head_stride >= most || c->token_stride >= most) return "cache strides too large";
-  if (c->page_size > 1 && c->token_stride < WS_DH) return "token_stride must be >= 64";
+  if ((c->page_size > 1 && c->token_stride < WS_DH) || (c->n_kv_heads > 1 && c->head_stride < WS_DH) ||
+      (c->n_pages > 1 && c->page_stride < WS_DH))
+    return "cache strides must be >= 64 elements";
   if (c->n_slots < 1 || c->table_stride < 1) return "n_slots and table_stride must be >= 1";
   return nullptr;
 }

@@ -125,7 +125,9 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rt = blockIdx.x / p.nsplit, split = blockIdx.x - rt * p.nsplit, h = blockIdx.y, i = blockIdx.z;
-  pdl_trigger();
+  // a dependent kernel may take tensor memory and then wait for this one: with
+  // STASH it may start only once every CTA here has its own
+  if (!STASH) pdl_trigger();
   // the first tiles' pages are asked for together with the lengths: the
   // entries exist whatever the lengths turn out to be
   const int slot0 = p.a.req_ids ? p.a.req_ids[i] : i;
@@ -201,6 +203,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    pdl_trigger();
     tmem = s_tmem + ((uint32_t)warp << 21);
   }
   bool dead = false;
@@ -543,6 +546,7 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
     return "rows of q and out must be 16-byte aligned";
   if (a->q_stride < (int64_t)a->n_heads * WS_DH || a->out_stride < (int64_t)a->n_heads * WS_DH)
     return "q_stride and out_stride must be >= 64 * n_heads";
+  if (a->q_stride >= (int64_t)1 << 37 || a->out_stride >= (int64_t)1 << 37) return "q_stride or out_stride too large";
   if (a->mass && a->mass_stride < a->max_kv) return "mass_stride must be >= max_kv";
   if (!a->req_ids && a->n_req > c->n_slots) return "more requests than slots";
   return nullptr;

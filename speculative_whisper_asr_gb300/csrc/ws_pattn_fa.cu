@@ -195,7 +195,6 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
-  pdl_trigger();
   if (p.next_item && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next_item = 0ull;
   const int pairs = (p.row_tiles + 1) / 2;
   const int pair = pairs - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
@@ -243,6 +242,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  pdl_trigger();                                   // only now: a dependent kernel takes tensor memory too
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
   if (warp < 4) {
@@ -257,7 +257,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           tma_load_3d(sQ + w * TILE, &mq, &B.q_full[w], 0, h * p.G, r.row0 + pair * 2 * RB + w * RB);
         }
     }
-    const int32_t* table = p.c.page_table + (size_t)max(r.slot, 0) * p.c.table_stride;
+    const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
     int page = tile_page(p, table, lo, lane), issued = 0, raws = 0;
     for (int j = 0; j < nmax; ++j) {
       const int s = j % NST;
@@ -545,11 +545,11 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  pdl_wait();                                      // the log-sum-exps and the counter; no tensor memory is held meanwhile
   if (warp == 1) tc::tmem_alloc(&s_tmem, 256);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  pdl_wait();                                      // the log-sum-exps and the counter
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   auto sK = [&](int b) { return sm + b * TILE; };
   auto sQ = [&](int b) { return sm + 2 * TILE + b * TILE; };

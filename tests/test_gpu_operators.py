@@ -75,6 +75,20 @@ def test_attention_head_layouts(R, dtype, hq, hkv, chunks):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("chunks,lens", [([1, 1], [150, 97]), ([3, 2], [70, 33])])
+def test_attention_many_heads_share_one(R, dtype, chunks, lens):
+    """More query heads per KV head than a row tile holds."""
+    _check(R, AttnCase(chunks, lens, hq=140, hkv=1, dtype=dtype, seed=140))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("c", [1, 2, 3, 8, 9, 16, 17, 32, 33])
+@pytest.mark.parametrize("kv", [63, 64, 65, 1025])
+def test_attention_around_the_row_tiles(R, dtype, c, kv):
+    _check(R, AttnCase([c], [kv], hq=2, hkv=2, dtype=dtype, seed=c + kv))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("chunks", [[2, 1, 3], [64, 40, 33]])
 def test_attention_slots_and_bad_ids(R, dtype, chunks):
     c = AttnCase(chunks, [70, 90, 11], dtype=dtype, req_ids=[4, -1, 1], slots=6, seed=3)

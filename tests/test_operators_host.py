@@ -50,7 +50,7 @@ def _refused(B, fn, code):
 
 BAD_CACHE = [dict(dtype=2), dict(n_kv_heads=0), dict(n_kv_heads=65536), dict(page_size=0), dict(n_pages=0), dict(k=0),
              dict(v=0), dict(k=4104), dict(v=4098), dict(page_stride=-8), dict(page_stride=100), dict(head_stride=4),
-             dict(token_stride=68), dict(token_stride=56), dict(token_stride=0), dict(page_table=0), dict(n_slots=0),
+             dict(head_stride=0), dict(page_stride=0), dict(token_stride=68), dict(token_stride=56), dict(token_stride=0), dict(page_table=0), dict(n_slots=0),
              dict(table_stride=0), dict(page_stride=1 << 37)]
 
 
