@@ -20,8 +20,10 @@ namespace {
 // and one exponential.  The reference m of a row moves only when a score
 // exceeds it by more than 2^8 (p <= 256), which a vote detects, so the
 // common tile needs no reduction across lanes.  Statistics and sums are
-// fp32; the weights are rounded to bf16 for the value product alone (2^-8
-// relative at most, the output's own step).
+// fp32.  Up to 8 rows the weights enter the value product as bf16 hi + lo
+// (2^-16 relative), which the copy rate hides; with more rows as one bf16
+// value (2^-8 relative at most, the output's own step: hi + lo costs 7% at 9
+// rows, 94 -> 101 us for 96 requests x 20 heads).
 //
 // With STASH the raw scores stay in tensor memory, which this kernel has no
 // other use for: each of the four warps owns a lane quarter and parks a
@@ -116,6 +118,7 @@ template <int NT, bool STASH>
 __global__ void __launch_bounds__(SP_W * 32, NT == 4 ? 1 : 2)
 split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   constexpr int MT = SP_TK / 16;           // key steps of 16
+  constexpr bool HILO = NT == 1;
   constexpr uint32_t ALL = 0xffffffffu;
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t full[SP_W][SP_NS];
@@ -281,7 +284,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
           for (int d = 0; d < 4; ++d) { o[d][nt][e] *= f; o[d][nt][2 + e] *= f; }
         }
     }
-    uint32_t pf[MT][NT][2];
+    uint32_t pf[MT][NT][2], pg[MT][NT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -292,7 +295,10 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
           const float p1 = ex2(fmaf(sc[mt][nt][2 * e2 + 1], sl, -msl[nt][1]));
           l[nt][0] += p0;
           l[nt][1] += p1;
-          pf[mt][nt][e2] = movm(pack_bf16(p0, p1));
+          const uint32_t hi = pack_bf16(p0, p1);
+          const float2 hf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi));
+          pf[mt][nt][e2] = movm(hi);
+          if (HILO) pg[mt][nt][e2] = movm(pack_bf16(p0 - hf.x, p1 - hf.y));
         }
 #pragma unroll
     for (int ks = 0; ks < MT; ++ks)
@@ -302,7 +308,10 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
         const int mtx = lane >> 3, key = 16 * ks + ((mtx >> 1) << 3) + (lane & 7);
         ldsm_x4_t(vb + kv_off<true>(key, 2 * d + (mtx & 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[d][nt], a, pf[ks][nt][0], pf[ks][nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_bf16_16816(o[d][nt], a, pf[ks][nt][0], pf[ks][nt][1]);
+          if (HILO) mma_bf16_16816(o[d][nt], a, pg[ks][nt][0], pg[ks][nt][1]);
+        }
       }
     __syncwarp();                           // every lane has read the slot
     if (more) { issue(slot, page_next); w.next(p.geo); }
