@@ -678,21 +678,21 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
         tc::tc_fence_after();
         const int cmin = first - rho, cmax = min(TR, R - rho);                 // columns that see this key
         const bool whole = __all_sync(0xffffffffu, cmin <= 0 && cmax == FA_ROWS);
-        float buf[2][32];
-        tm_ld32(tl, buf[0]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          float* sv = buf[q & 1];
+          float sv[32];
+          tm_ld32(tl + 32 * q, sv);
           ld_wait();
-          if (q < 3) {
-            tm_ld32(tl + 32 * (q + 1), buf[(q + 1) & 1]);
-          } else {
+          if (q == 3) {
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(&B.s_free[group]);
           }
           const float4* nl = reinterpret_cast<const float4*>(nlse[s] + 32 * q);
-          if (whole) {
+          // in a tile that is not whole, the 32 columns may still be, or may be out of every lane's range
+          const bool all = whole || __all_sync(0xffffffffu, cmin <= 32 * q && cmax >= 32 * q + 32);
+          if (!all && __all_sync(0xffffffffu, cmin >= 32 * q + 32 || cmax <= 32 * q)) continue;
+          if (all) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float4 n4 = nl[e];
