@@ -4,8 +4,8 @@
 // and key range; rows are chunk rows x the query heads that share the KV
 // head, so a box of the query map is a row tile.  The two row tiles A and B
 // share every key tile of 128 keys:
-//   warp 0      producer: Q once, then K and V tiles (page by page) through
-//               four stages; zeroes value rows that do not count
+//   warps 0, 2  producers: Q once and the K tiles; the V tiles (page by page,
+//               through four stages), clearing value rows that do not count
 //   warp 1      MMA issuer: S = Q K^T (128 x 128, both from shared memory),
 //               O += P V with P from tensor memory and V as it lies in the
 //               pages (the "N-major" operand form: no transpose)
@@ -220,7 +220,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int b = 0; b < NST; ++b) {
-      tc::mbar_init(&B.full[b], 1);
+      tc::mbar_init(&B.full[b], 2);
       tc::mbar_init(&B.empty[b], 1);
     }
     tc::mbar_init(&B.raw, 1);
@@ -247,9 +247,11 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0) {
-    // ---- producer
-    if (lane == 0) {
+  if (warp == 0 || warp == 2) {
+    // ---- producers: Q and K, and V.  Two warps, because small pages make
+    // many copies of a tile and one warp's copies are issued one by one.
+    const bool values = warp == 2;
+    if (!values && lane == 0) {
 #pragma unroll
       for (int w = 0; w < 2; ++w)
         if (n[w]) {
@@ -265,23 +267,22 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (j + 1 < nmax) page = tile_page(p, table, lo + j + 1, lane);
       if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
       const bool go = f.page >= 0;
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 256u;
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 128u;
       const bool whole = (f.valid[0] & f.valid[1] & f.valid[2] & f.valid[3]) == 0xffffffffu;
-      uint64_t* bar = whole ? &B.full[s] : &B.raw;
+      uint64_t* bar = values && !whole ? &B.raw : &B.full[s];
       if (lane == 0) {
+        if (!values) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) meta[s].valid[q] = f.valid[q];
-        meta[s].base = f.base;
-        meta[s].full = whole;
+          for (int q = 0; q < 4; ++q) meta[s].valid[q] = f.valid[q];
+          meta[s].base = f.base;
+          meta[s].full = whole;
+        }
         tc::mbar_expect_tx(bar, bytes);
       }
       __syncwarp();
-      if (go) {
-        tma_load_4d(sK(s) + f.dst, &mk, bar, 0, f.tok, h, f.page);
-        tma_load_4d(sV(s) + f.dst, &mv, bar, 0, f.tok, h, f.page);
-      }
+      if (go) tma_load_4d((values ? sV(s) : sK(s)) + f.dst, values ? &mv : &mk, bar, 0, f.tok, h, f.page);
       ++issued;
-      if (!whole) {
+      if (values && !whole) {
         // value rows behind the cache's length, or of skipped pages, may hold
         // anything (0 * inf would reach the sums): cleared before the tile is
         // handed over
