@@ -380,26 +380,35 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
     // adds key 8 c + g.  The position is this thread's alone, so the atomic
     // (which does not wait for the old value) has nothing to race with.
     w.start(p.geo, tb + warp, SP_W);
-    for (int it = 0; it < n_my; ++it) {
-      float sv[MT][NT][4];
-      tm_ld<8 * NT>(tmem + (uint32_t)(it * 8 * NT), &sv[0][0][0]);
+    constexpr int U = NT == 4 ? 1 : 2;      // tiles at once: one's latencies under the other's
+    for (int it = 0; it < n_my; it += U) {
+      float sv[U][MT][NT][4];
+#pragma unroll
+      for (int k = 0; k < U; ++k) tm_ld<8 * NT>(tmem + (uint32_t)(min(it + k, n_my - 1) * 8 * NT), &sv[k][0][0][0]);
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-      float part[4];
+      float part[U][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {         // keys 8 q + g
-        float s = 0.f;
+      for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int q = 0; q < 4; ++q) {       // keys 8 q + g
+          float s = 0.f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) s += ex2(fmaf(sv[q >> 1][nt][2 * (q & 1) + e], sl, -nl[nt][e]));
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        part[q] = s;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s += ex2(fmaf(sv[k][q >> 1][nt][2 * (q & 1) + e], sl, -nl[nt][e]));
+          part[k][q] = s;
+        }
+      // a quad's four lanes hold parts of four keys: two exchanges leave each
+      // lane with the whole sum of one
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float a0 = (c & 2 ? part[k][2] : part[k][0]) + __shfl_xor_sync(0xffffffffu, c & 2 ? part[k][0] : part[k][2], 2);
+        const float a1 = (c & 2 ? part[k][3] : part[k][1]) + __shfl_xor_sync(0xffffffffu, c & 2 ? part[k][1] : part[k][3], 2);
+        const float sum = (c & 1 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);
+        const int j = 8 * c + g, pos = w.base(p.geo, p.c.page_size, SP_TK) + j;
+        if (it + k < n_my && j < w.room(p.geo, p.c.page_size, SP_TK) && pos < Lmax) atomicAdd(mass + pos, sum);
+        w.next(p.geo);
       }
-      const int j = 8 * c + g, pos = w.base(p.geo, p.c.page_size, SP_TK) + j;
-      if (j < w.room(p.geo, p.c.page_size, SP_TK) && pos < Lmax)
-        atomicAdd(mass + pos, c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : part[3]);
-      w.next(p.geo);
     }
     tc::tc_fence_before();
     __syncthreads();
