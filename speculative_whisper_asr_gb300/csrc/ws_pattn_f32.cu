@@ -114,6 +114,11 @@ __device__ __forceinline__ uint32_t remote(const void* local, uint32_t rank) {
   return a;
 }
 
+// Weight of a part with maximum x (log2 units) beside one of M.  Parts that
+// saw nothing are multiplied by 0, not left out: their sum is 0, or NaN where
+// every score was, and a NaN has to reach the result.
+__device__ __forceinline__ float weight_of(float x, float M) { return x == -INFINITY ? 0.f : ex2(x - M); }
+
 // grid (cs, heads, requests), cluster (cs, 1, 1) where the CTAs join their
 // parts themselves (JOIN), else the CTAs write split partials.
 constexpr int CL_MAX = 8, CL_KEYS = 1024;           // CTAs per cluster, positions per CTA whose scores are kept
@@ -291,8 +296,7 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
       for (int k = 0; k < KW; ++k) M = fmaxf(M, wstat[k][row].x);
       float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f), a1 = a0;
       for (int k = 0; k < KW; ++k) {
-        if (wstat[k][row].x == -INFINITY) continue;
-        const float f = ex2(wstat[k][row].x - M);
+        const float f = weight_of(wstat[k][row].x, M);
         sum = fmaf(f, wstat[k][row].y, sum);
         const float4 b0 = *reinterpret_cast<const float4*>(so + (k * 16 + row) * PITCH + d);
         const float4 b1 = *reinterpret_cast<const float4*>(so + (k * 16 + row) * PITCH + d + 4);
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
     const int row = x >> 4, d = (x & 15) * 4;
     float M = -INFINITY, sum = 0.f;
     for (int k = 0; k < cs; ++k) M = fmaxf(M, all[k][row].x);
-    for (int k = 0; k < cs; ++k) sum += all[k][row].x == -INFINITY ? 0.f : all[k][row].y * ex2(all[k][row].x - M);
+    for (int k = 0; k < cs; ++k) sum = fmaf(weight_of(all[k][row].x, M), all[k][row].y, sum);
     if (d == 0) row_lse[row] = sum == 0.f ? INFINITY : M + lg2(sum);
     if (row % cs != rank) continue;
     float4 part[CL_MAX];
@@ -350,8 +354,8 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < CL_MAX; ++k)
-      if (k < cs && all[k][row].x != -INFINITY) {
-        const float f = ex2(all[k][row].x - M);
+      if (k < cs) {
+        const float f = weight_of(all[k][row].x, M);
         a.x = fmaf(f, part[k].x, a.x); a.y = fmaf(f, part[k].y, a.y);
         a.z = fmaf(f, part[k].z, a.z); a.w = fmaf(f, part[k].w, a.w);
       }

@@ -27,7 +27,7 @@ namespace {
 
 constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
 constexpr int NST = 4;                             // key stages
-constexpr int THREADS = 384;                        // producer, MMA, two idle | softmax A | softmax B
+constexpr int THREADS = 384;                        // K producer, MMA, V producer, idle | softmax A | softmax B
 constexpr int FA_SMEM = 2 * TILE + NST * 2 * TILE + 1024;
 constexpr uint32_t TM_S = 0, TM_P = 256, TM_O = 384;   // + 128 w, + 64 w, + 64 w
 constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
@@ -436,6 +436,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         msl = mn > -INFINITY ? mn * sl : 0.f;
         l *= f;
         if (j > 0) {
+          st_wait();                               // the first weights are stored before the second ones are
           tc::tc_fence_after();
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
@@ -707,7 +708,7 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float x = nlse[s][32 * q + e], y = ex2(fmaf(sv[e], p.sl, x));
-              if (32 * q + e >= cmin && 32 * q + e < cmax && x > -INFINITY) total.x += y;
+              if (32 * q + e >= cmin && 32 * q + e < cmax && x != -INFINITY) total.x += y;
             }
           }
         }
