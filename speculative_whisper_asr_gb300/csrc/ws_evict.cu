@@ -388,6 +388,9 @@ cudaError_t launch_cache_evict(const ws_paged_cache& cache, const ws_evict_args&
   p.len = (int32_t*)workspace;
   p.idx = (int32_t*)((char*)workspace + ((size_t)args.n_req * 4 + 255) / 256 * 256);
   p.ordered = args.mass_out == args.mass || (args.pos && args.pos_out == args.pos);
+  // threads of a selecting CTA, 256 against 512 (whole eviction, 20 heads): 64
+  // requests x 4096 positions 101 and 115 us, 32 x 8192 80 and 75 us, 8 x 8192
+  // 42 and 37 us
   cudaError_t e = args.max_kv <= 4096 ? select<256>(p, s) : select<512>(p, s);
   if (e != cudaSuccess) return e;
   return cache.dtype == WS_BF16 ? move<bf16>(p, in_place, s) : move<float>(p, in_place, s);

@@ -616,7 +616,13 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
     return q;
   }
   const int G = a.n_heads / c.n_kv_heads;
-  if (R > 32 && G <= FA_ROWS && a.scale > 0.f) {
+  // Row tiles of 128 rows on tcgen05 or of 32 that stream the cache: 96
+  // requests x 20 heads over 375-1500 positions take 182 us on tcgen05 at any
+  // number of rows up to 128 and 104 / 111 / 119 / 146 / 164 / 185 us
+  // streaming at 17 / 32 / 33 / 40 / 48 / 64 rows (with the weights 325
+  // against 179 / 188 / 259 / 302 / 335 / 387); 4 requests over 4-16 thousand
+  // positions 84 against 76 / 78 / 81 / 87 / 99 / 104 us.
+  if (R > 40 && G <= FA_ROWS && a.scale > 0.f) {
     q.fa = true;
     q.row_tiles = (a.max_q + FA_ROWS / G - 1) / (FA_ROWS / G);
     q.geo = tile_geo(c.page_size, FA_KEYS);
