@@ -551,7 +551,7 @@ _I32, _F32 = torch.int32, torch.float32
 
 def _rows(name, t, dtype, shape, dev):
     """Pointer of a contiguous tensor of exactly this type and shape on CUDA device number `dev`."""
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev} is needed")
     return t.data_ptr()
 
@@ -578,7 +578,7 @@ class PagedCache:
     of 16 bytes (the same for both), page_table [slots, pages per slot] int32.
     The object keeps scratch for each stream that called it; graphs captured
     on one stream share it, so those that may replay at the same time need a
-    PagedCache each."""
+    PagedCache each.  One thread at a time calls it."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
         if k.dtype not in (torch.bfloat16, torch.float32) or k.dim() != 4 or k.shape[3] != 64 or not k.is_cuda:
@@ -588,17 +588,15 @@ class PagedCache:
         if k.stride(3) != 1:
             raise ValueError("the head dimension must be contiguous")
         if (page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.device != k.device
-                or page_table.shape[1] > 1 and page_table.stride(1) != 1
-                or page_table.shape[0] > 1 and page_table.stride(0) < page_table.shape[1]):
-            raise ValueError("page_table: an int32 tensor [slots, pages] with contiguous rows on k's device is needed")
+                or not page_table.is_contiguous()):
+            raise ValueError("page_table: a contiguous int32 tensor [slots, pages] on k's device is needed")
         self.k, self.v, self.page_table = k, v, page_table
         self.dev, self.dtype = k.get_device(), k.dtype
         self.pages, self.heads, self.page_size, _ = k.shape
         self.slots = page_table.shape[0]
         self.desc = B.PagedCacheDesc(
             B.WS_BF16 if k.dtype is torch.bfloat16 else B.WS_F32, self.heads, self.page_size, self.pages, k.data_ptr(),
-            v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(), self.slots,
-            page_table.stride(0) if self.slots > 1 else page_table.shape[1])
+            v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(), self.slots, page_table.shape[1])
         self._attn, self._evict = B.AttentionArgs(), B.EvictArgs()
         self._ws, self._kept = {}, []
         self._need = {}                    # workspace bytes by the sizes they depend on
@@ -650,10 +648,13 @@ class PagedCache:
             a.mass, a.mass_stride = _per_position("mass", mass, _F32, self.slots, self.heads, dev)
         s = _on(dev)
         sizes = (n, rows, heads, max_q, max_kv, scale, lse is None, mass is None)
-        need = self._need.get(sizes)
-        if need is None:
-            need = self._need[sizes] = B.ws_paged_attention_workspace(self.desc, a)
-        B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
+        need = self._need.get(sizes, -1)
+        if need < 0:
+            need = B.ws_paged_attention_workspace(self.desc, a)
+            B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
+            self._need[sizes] = need       # of a call that was not refused
+        else:
+            B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
         return out
 
     def evict(self, kv_len, mass, keep: int, max_kv: int, sink: int = 0, recent: int = 0, page_table_out=None,
@@ -682,10 +683,13 @@ class PagedCache:
             a.table_out_stride = width = page_table_out.shape[1]
             a.page_table_out = _rows("page_table_out", page_table_out, _I32, (slots, width), dev)
         s = _on(dev)
-        need = self._need.get((n, keep))
-        if need is None:
-            need = self._need[n, keep] = B.ws_cache_evict_workspace(self.desc, a)
-        B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
+        need = self._need.get((n, keep), -1)
+        if need < 0:
+            need = B.ws_cache_evict_workspace(self.desc, a)
+            B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
+            self._need[n, keep] = need     # of a call that was not refused
+        else:
+            B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
 
 
 class LogitsRules:

@@ -271,6 +271,57 @@ def test_wrong_tensors_raise(R):
         R.PagedCache(c.k, c.v, c.table.long())
 
 
+@pytest.mark.parametrize("c,G", [(33, 1), (40, 1), (41, 1), (48, 1), (10, 4), (11, 4), (5, 8), (6, 7)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_between_streaming_and_wide_row_tiles(R, c, G, causal):
+    """33 to 48 rows per KV head: two streaming row tiles, or one of 128 rows."""
+    _check(R, AttnCase([c, 3, c], [600, 64, 37], hq=2 * G, hkv=2, causal=causal, seed=c * G))
+    _check(R, AttnCase([c], [1700], hq=2 * G, hkv=2, causal=causal, seed=c + G))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("c", [1, 6, 30, 90])
+def test_attention_nan_row_stays_alone(R, dtype, c):
+    """A NaN in one query row makes that row NaN and no other."""
+    x = AttnCase([c, c], [300, 130], dtype=dtype, hq=4, hkv=2, seed=c)
+    want, tol = x.reference()
+    x.q[c - 1, 2, 5] = math.nan
+    out, lse, _ = _attend(R, x, mass=False)
+    assert bool(out[c - 1, 2].isnan().all()) and bool(lse[c - 1, 2].isnan())
+    for got, w, t in ((out, want[0], tol[0]), (lse, want[1], tol[1])):
+        got = got[: 2 * c].double().cpu()
+        got[c - 1, 2] = w[c - 1, 2]
+        close("rows beside a NaN row", got, w, t)
+
+
+def test_a_refused_call_leaves_the_next_one_alone(R):
+    """Sizes of a refused call are not remembered: the same sizes with sound arguments go through."""
+    c = AttnCase([90], [300], seed=4)
+    cache = R.PagedCache(c.k, c.v, c.table)
+    with pytest.raises(R.B.WSError):
+        cache.attend(c.q, c.kv_len, c.cu, max_q=c.max_q, max_kv=c.max_kv, causal=c.causal, scale=c.scale,
+                     mass=c.mass0[:, :, :5].contiguous())
+    out, lse, mass = _attend(R, c, lse=False, cache=cache)
+    want, tol = c.reference()
+    close("out", out[: c.rows], want[0], tol[0])
+    close("mass", mass, want[2], tol[2])
+    m, n = mass.clone(), int(c.kv_len[0])
+    with pytest.raises(R.B.WSError):
+        cache.evict(c.kv_len, m, keep=100, max_kv=n, mass_out=m[:, :, :20].contiguous())
+    kept = evict_rule(mass[0, 0].cpu().numpy(), n, 100, 0, 0)
+    cache.evict(c.kv_len, m, keep=100, max_kv=n)
+    torch.cuda.synchronize()
+    assert int(c.kv_len[0]) == 100 and torch.equal(m[0, 0, :100], mass[0, 0, kept])
+
+
+def test_strided_page_table_is_refused(R):
+    """Rows of a wider table: the entries behind the last row's may not exist."""
+    c = AttnCase([2], [200], seed=1)
+    wide = torch.zeros(3, 9, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        R.PagedCache(c.k, c.v, wide[:, 4:])
+
+
 # ------------------------------------------------------------------ eviction
 def _evict_case(R, lens, page, dtype, keep, sink, recent, hkv=3, layout="head", in_place=False, seed=0, odd=False):
     g = torch.Generator(device="cpu").manual_seed(seed)
