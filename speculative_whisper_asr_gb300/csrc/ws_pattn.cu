@@ -617,19 +617,25 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   }
   const int G = a.n_heads / c.n_kv_heads;
   // Row tiles of 128 rows on tcgen05 or of 32 that stream the cache: 96
-  // requests x 20 heads over 375-1500 positions take 182 us on tcgen05 at any
-  // number of rows up to 128 and 104 / 111 / 119 / 146 / 164 / 185 us
-  // streaming at 17 / 32 / 33 / 40 / 48 / 64 rows (with the weights 325
-  // against 179 / 188 / 259 / 302 / 335 / 387); 4 requests over 4-16 thousand
-  // positions 84 against 76 / 78 / 81 / 87 / 99 / 104 us.
+  // requests x 20 heads over 375-1500 positions take 152 us on tcgen05 at 48
+  // rows (156 at 128) and 104 / 111 / 119 / 146 / 164 / 185 us streaming at
+  // 17 / 32 / 33 / 40 / 48 / 64 rows (with the weights 300 against 179 / 188
+  // / 259 / 302 / 335 / 387); 4 requests over 4-16 thousand positions 84
+  // against 76 / 78 / 81 / 87 / 99 / 104 us.
   if (R > 40 && G <= FA_ROWS && a.scale > 0.f) {
     q.fa = true;
     q.row_tiles = (a.max_q + FA_ROWS / G - 1) / (FA_ROWS / G);
     q.geo = tile_geo(c.page_size, FA_KEYS);
     const int tiles = max(1, tile_count(q.geo, c.page_size, FA_KEYS, a.max_kv));
     const long long units = (long long)a.n_req * c.n_kv_heads * ((q.row_tiles + 1) / 2);
-    // about two CTAs per SM, none shorter than four key tiles
-    const int want = (int)min((2ll * SMS + units - 1) / units, (long long)max(1, tiles / 4));
+    // One round of CTAs (two per SM with one row tile each, else one), none
+    // shorter than four key tiles: a single request fills the round (a CTA
+    // more than the round costs another: 64 rows over 65,536 positions 140 us
+    // with 16 splits of 20 heads, 97 with 15), several requests' lengths
+    // differ and leave CTAs without keys, so one split more (4 requests over
+    // 4-16 thousand positions 101 us without it, 83 with it).
+    const long long round = (q.row_tiles == 1 ? 2ll : 1ll) * SMS / units + (a.n_req > 1 ? 1 : 0);
+    const int want = (int)max(1ll, min(round, (long long)(tiles / 4)));
     q.tps = (tiles + want - 1) / want;
     q.nsplit = (tiles + q.tps - 1) / q.tps;
     partials(R);

@@ -1,35 +1,49 @@
 // ws_paged_attention for long chunks of the bf16 model, on tcgen05.
 //
-// fa_kernel.  One CTA per (request, KV head, two row tiles of up to 128 rows)
-// and key range; rows are chunk rows x the query heads that share the KV
-// head, so a box of the query map is a row tile.  The two row tiles A and B
-// share every key tile of 128 keys:
-//   warps 0, 2  producers: Q once and the K tiles; the V tiles (page by page,
-//               through four stages), clearing value rows that do not count
-//   warp 1      MMA issuer: S = Q K^T (128 x 128, both from shared memory),
-//               O += P V with P from tensor memory and V as it lies in the
-//               pages (the "N-major" operand form: no transpose)
-//   warps 2..5  softmax of A, warps 6..9 of B: one thread per row
-// Tensor memory (512 columns): S, P and O of each tile have columns of their
+// fa_kernel.  One CTA per (request, KV head, W row tiles of up to 128 rows)
+// and key range.  Rows are chunk rows x the query heads that share the KV
+// head, so a box of the query map is a row tile.  W = 2, or, where a request
+// has one row tile, W = 1 with half of the CTA's means, so that two CTAs
+// share an SM and one's first copies and last rows lie under the other's
+// tiles (96 requests x 20 heads x 128 rows over 375-1500 positions: 187 ->
+// 156 us; with more row tiles W = 2 copies the keys half as often: 219 us
+// against 306 for 4 x 2048 rows).  Row tiles A and B share every key tile of
+// 128 keys:
+//   warps 0, 2   producers: Q once and the K tiles; the V tiles (page by
+//                page), clearing value rows that do not count
+//   warp 1       MMA issuer: S = Q K^T (128 x 128, both from shared memory),
+//                O += P V with P from tensor memory and V as it lies in the
+//                pages (the "N-major" operand form: no transpose)
+//   warps 4..7   softmax of A, warps 8..11 of B: one thread per row
+// Tensor memory (256 columns per row tile): S, P and O have columns of their
 // own, so the next S is computed as soon as the softmax has S in registers.
 // The row's reference is the maximum of its first tile; it moves, and O is
-// rescaled in tensor memory, only when a tile's weights pass 2^60.  With head width 64 a score costs
-// 256 FLOP and one exponential, so the exponentials bound the kernel as much
-// as the tensor core does; scaling and sums are packed pairs (f32x2).
+// rescaled in tensor memory, only when a tile's weights pass 2^60.  With head
+// width 64 a score costs 256 FLOP and one exponential, so the exponentials
+// bound the kernel as much as the tensor core does; scaling and sums are
+// packed pairs (f32x2).  P V (64 columns wide) takes the tensor core as long
+// as Q K^T (128 wide).  4 requests x 20 heads x 2048 rows over up to 8192
+// positions (198 GFLOP): 207 us, 0.96 PFLOP/s of the measured 1.92; tensor
+// pipe 52% busy, exponential pipe 45%.
 //
 // fa_mass_kernel.  The weights summed per key, once every row's log-sum-exp
 // is known: S^T = K Q^T puts a key into each thread, which adds
-// 2^(s * sl - lse * log2 e) over the rows of a tile in order; no reduction
-// across threads, no atomics.
+// 2^(s * sl - lse * log2 e) over the rows of a tile in order, without a
+// reduction across threads.  A second pass over the scores (99 GFLOP more)
+// and as many exponentials again: 160 us for the call above, exponential
+// pipe 55% busy.
 #include "ws_pattn.cuh"
 
 namespace {
 
 constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
-constexpr int NST = 4;                             // key stages
-constexpr int THREADS = 384;                        // K producer, MMA, V producer, idle | softmax A | softmax B
-constexpr int FA_SMEM = 2 * TILE + NST * 2 * TILE + 1024;
-constexpr uint32_t TM_S = 0, TM_P = 256, TM_O = 384;   // + 128 w, + 64 w, + 64 w
+template <int W>
+struct FaShape {                                   // a CTA with W row tiles; 3 - W run on an SM
+  static constexpr int STAGES = 2 * W;             // key stages
+  static constexpr int THREADS = 128 + 128 * W;    // K producer, MMA, V producer, idle | softmax A | softmax B
+  static constexpr int SMEM = W * TILE + STAGES * 2 * TILE + 1024;
+  static constexpr uint32_t COLS = 256 * W;        // tensor memory
+};
 constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
 constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, 64) | (1u << 16);   // B (V) is N-major
 constexpr float MOST = 1152921504606846976.0f;     // 2^60: largest sum of a tile's weights before a row's reference moves
@@ -182,41 +196,45 @@ __device__ __forceinline__ int longest_first(const AttnP& p, int z) {
   return s_req;
 }
 
+template <int W>
 struct Bars {
-  uint64_t q_full[2], full[NST], empty[NST], raw, s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t q_full[W], full[FaShape<W>::STAGES], empty[FaShape<W>::STAGES], raw, s_full[W], s_free[W], p_full[W], pv_done[W];
 };
 
-__global__ void __launch_bounds__(THREADS, 1)
+template <int W>
+__global__ void __launch_bounds__(FaShape<W>::THREADS, 3 - W)
 fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
+  constexpr int NST = FaShape<W>::STAGES, THREADS = FaShape<W>::THREADS;
+  constexpr uint32_t TM_S = 0, TM_P = 128 * W, TM_O = 192 * W;   // + 128 w, + 64 w, + 64 w
   extern __shared__ uint8_t dsm[];
-  __shared__ __align__(8) Bars B;
+  __shared__ __align__(8) Bars<W> B;
   __shared__ Meta meta[NST];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   if (p.next_item && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next_item = 0ull;
-  const int pairs = (p.row_tiles + 1) / 2;
-  const int pair = pairs - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
+  const int groups = (p.row_tiles + W - 1) / W;
+  const int pair = groups - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
   const int h = blockIdx.y, i = longest_first(p, blockIdx.z);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Req r = request(p, i);
   const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
-  const int rho0 = pair * 2 * TR;
+  const int rho0 = pair * W * TR;
   if (rho0 >= R) return;
   // key tiles of each row tile within this split
-  int n[2], lo;
+  int n[W], lo;
   {
     const int ps = p.c.page_size;
     lo = split * p.tps;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < W; ++w) {
       const int first = rho0 + w * TR, last = min(R, first + TR) - 1;
       const int nt = last >= first ? tile_count(p.geo, ps, FA_KEYS, row_limit(p, r, last / p.G)) : 0;
       n[w] = max(0, min(nt, lo + p.tps) - lo);
     }
   }
-  const int nmax = max(n[0], n[1]);
+  const int nmax = max(n[0], n[W - 1]);
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int b = 0; b < NST; ++b) {
@@ -224,17 +242,17 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       tc::mbar_init(&B.empty[b], 1);
     }
     tc::mbar_init(&B.raw, 1);
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < W; ++w) {
       tc::mbar_init(&B.q_full[w], 1); tc::mbar_init(&B.s_full[w], 1); tc::mbar_init(&B.s_free[w], 4);
       tc::mbar_init(&B.p_full[w], 4); tc::mbar_init(&B.pv_done[w], 1);
     }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tc::tmem_alloc(&s_tmem, 512);
+  if (warp == 1) tc::tmem_alloc(&s_tmem, FaShape<W>::COLS);
   uint8_t* sQ = sm;
-  auto sK = [&](int b) { return sm + 2 * TILE + b * 2 * TILE; };
-  auto sV = [&](int b) { return sm + 3 * TILE + b * 2 * TILE; };
+  auto sK = [&](int b) { return sm + W * TILE + b * 2 * TILE; };
+  auto sV = [&](int b) { return sm + (W + 1) * TILE + b * 2 * TILE; };
   if (p.geo.tpp && p.geo.box < FA_KEYS)            // value rows that no copy writes
     for (int x = threadIdx.x; x < NST * TILE / 16; x += THREADS)
       reinterpret_cast<uint4*>(sV(x / (TILE / 16)))[x % (TILE / 16)] = make_uint4(0u, 0u, 0u, 0u);
@@ -253,10 +271,10 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     const bool values = warp == 2;
     if (!values && lane == 0) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int w = 0; w < W; ++w)
         if (n[w]) {
           tc::mbar_expect_tx(&B.q_full[w], (uint32_t)TR * 128u);
-          tma_load_3d(sQ + w * TILE, &mq, &B.q_full[w], 0, h * p.G, r.row0 + pair * 2 * RB + w * RB);
+          tma_load_3d(sQ + w * TILE, &mq, &B.q_full[w], 0, h * p.G, r.row0 + pair * W * RB + w * RB);
         }
     }
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
@@ -335,24 +353,24 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), IDESC_PV,
                   (j | kk) ? 1u : 0u);
         tc::umma_commit(&B.pv_done[w]);
-        if (w == 1 || j >= n[1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
+        if (w == W - 1 || j >= n[W - 1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
       }
       __syncwarp();
       return true;
     };
     bool ok = true;
-    int sc[2] = {0, 0}, pc[2] = {0, 0};
+    int sc[W] = {}, pc[W] = {};
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int w = 0; w < W; ++w)
       if (ok && n[w]) { ok = wait(&B.q_full[w], 0, abort) && qk(w, 0); sc[w] = ok; }
     for (int j = 0; j < nmax && ok; ++j)
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < W; ++w) {
         if (ok && j + 1 < n[w]) { ok = qk(w, j + 1); sc[w] += ok; }
         if (ok && j < n[w]) { ok = pv(w, j); pc[w] += ok; }
       }
     if (*abort && lane == 0)                       // nothing may be in flight when the CTA ends
-      for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < W; ++w) {
         if (n[w]) tc::mbar_wait(&B.q_full[w], 0);
         if (sc[w]) tc::mbar_wait(&B.s_full[w], (uint32_t)((sc[w] - 1) & 1));
         if (pc[w]) tc::mbar_wait(&B.pv_done[w], (uint32_t)((pc[w] - 1) & 1));
@@ -361,7 +379,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   }
   } else {
     // ---- softmax: thread = row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");     // 168 a thread at launch
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");            // 128
     const int w = (warp >> 2) - 1, quarter = warp & 3, x = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tS = tl + TM_S + 128u * w, tP = tl + TM_P + 64u * w, tO = tl + TM_O + 64u * w;
@@ -490,7 +509,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         }
       }
       if (on && p.nl)
-        p.nl[(((size_t)i * p.c.n_kv_heads + h) * p.row_tiles + pair * 2 + w) * FA_ROWS + x] =
+        p.nl[(((size_t)i * p.c.n_kv_heads + h) * p.row_tiles + pair * W + w) * FA_ROWS + x] =
             !ok ? NAN : l == 0.f ? -INFINITY : -(msl + lg2(l));
       if (on && p.lse)
         p.lse[(size_t)(r.row0 + t) * p.a.n_heads + u_] = !ok ? NAN : l == 0.f ? -INFINITY : (msl + lg2(l)) * LN2;
@@ -499,7 +518,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   }
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (warp == 1) tc::tmem_dealloc(tmem, FaShape<W>::COLS);
 }
 
 // ------------------------------------------------------------------ accumulated weights
@@ -736,6 +755,17 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   if (warp == 1) tc::tmem_dealloc(tmem, 256);
 }
 
+template <int W>
+cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(fa_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, FaShape<W>::SMEM);
+  if (e != cudaSuccess) return e;
+  fa_kernel<W><<<dim3((p.row_tiles + W - 1) / W * p.nsplit, p.c.n_kv_heads, p.a.n_req), FaShape<W>::THREADS, FaShape<W>::SMEM, s>>>(
+      p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
+      reinterpret_cast<const CUtensorMap&>(mv));
+  ws_count_launches(1);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
@@ -744,13 +774,7 @@ cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
                        (uint32_t)(FA_ROWS / p.G)) ||
       !tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(fa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FA_SMEM);
-  if (e != cudaSuccess) return e;
-  fa_kernel<<<dim3((p.row_tiles + 1) / 2 * p.nsplit, p.c.n_kv_heads, p.a.n_req), THREADS, FA_SMEM, s>>>(
-      p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
-      reinterpret_cast<const CUtensorMap&>(mv));
-  ws_count_launches(1);
-  return cudaGetLastError();
+  return p.row_tiles == 1 ? run_fa<1>(p, mq, mk, mv, s) : run_fa<2>(p, mq, mk, mv, s);
 }
 
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s) {
