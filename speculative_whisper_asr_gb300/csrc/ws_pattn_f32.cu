@@ -23,6 +23,8 @@
 // f32_mass_kernel.  The weights of a tile of 64 keys: the keys stay in shared
 // memory, the rows pass by, each thread sums its rows of 4 keys, and the 16
 // row groups are added in order at the end.
+#include <algorithm>
+
 #include "ws_pattn.cuh"
 
 namespace {
@@ -583,14 +585,16 @@ cudaError_t launch_f32_rows(const AttnP& p, const F32Rows& f, cudaStream_t s) {
 }
 
 F32Rows f32_rows_plan(long long units, int max_kv, bool mass) {
-  // about three rounds of three CTAs per SM, none shorter than 64 positions
-  long long want = (1368 + units - 1) / units;
-  const long long most = max_kv > 64 ? max_kv / 64 : 1;
-  if (want > most) want = most;
+  // About three rounds of three CTAs per SM; none shorter than 64 positions,
+  // and none shorter than 256 beyond the first round.
+  constexpr long long ROUND = 3 * 152;
+  long long want = (3 * ROUND + units - 1) / units;
+  want = std::min(want, std::max({ROUND / units, max_kv / 256ll, 1ll}));
+  want = std::min(want, std::max(max_kv / 64ll, 1ll));
   F32Rows f;
   // one launch where a cluster's CTAs are enough, and keep their scores
   const bool fits = !mass || max_kv <= CL_MAX * CL_KEYS;
-  f.join = fits && (want <= CL_MAX || max_kv <= CL_MAX * 512);
+  f.join = fits && (mass || units * want <= ROUND) && (want <= CL_MAX || max_kv <= CL_MAX * 512);
   if (f.join && want > CL_MAX) want = CL_MAX;
   if (f.join && mass && want * CL_KEYS < max_kv) want = (max_kv + CL_KEYS - 1) / CL_KEYS;
   f.keys = (int)(((max_kv > 0 ? max_kv : 1) + want - 1) / want);
