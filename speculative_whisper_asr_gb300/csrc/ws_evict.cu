@@ -13,6 +13,11 @@
 // place, a destination is never behind its source, so a CTA goes through the
 // rows in order, a batch read before the batch is written; the parallelism
 // comes from cutting the rows into 32-byte columns, which never mix.
+//
+// 96 requests x 20 heads, up to 1500 positions cut to 512 (514 MB): selection
+// 19 us, move 82 us (6.1 TB/s); 8 requests x 8 heads, up to 65,536 cut to
+// 16,384 (560 MB): 25 and 89 us.  Selecting inside the moving kernel took 136
+// and 250 us: a CTA's histogram passes leave the memory idle.
 #include "ws_paged.cuh"
 
 namespace {
@@ -341,7 +346,9 @@ size_t evict_bytes(const ws_paged_cache* c, const ws_evict_args* a) {
 }
 
 // CTAs per (request, head): as many as run at once (two per SM), each with
-// 1,024 keys at least; the keys stay in shared memory where they fit.
+// 1,024 keys at least (whole eviction, 8 heads x 65,536 positions: 2 requests
+// 171 us with one CTA each, 60 so; 8 requests 237 and 134); the keys stay in
+// shared memory where they fit.
 template <int NT>
 cudaError_t select(EvictP& p, cudaStream_t s) {
   const long long units = (long long)p.a.n_req * p.c.n_kv_heads;

@@ -32,8 +32,12 @@ namespace {
 // (the CTA has the whole cache: no splits) each warp reads its fragments
 // back and adds its positions' weights, so the mass costs neither a second
 // read of the keys nor shared memory that the rings need.  Measured at 96
-// requests x 20 heads x 9 rows over 375-1500 positions: a second pass over
-// the keys 176 us, scores in shared memory 126 us.
+// requests x 20 heads x 9 rows over 375-1500 positions (480 MB): a second
+// pass over the keys 176 us, scores in shared memory 126 us, so 90 us (5.3
+// TB/s; 77 us, 6.2 TB/s, without weights).  One row of 32 heads on 8 over 16
+// caches of up to 65,536 positions (1.36 GB): 202 us, 6.7 TB/s, the rate of a
+// plain copy.  One row of one request, 20 heads x 448 positions: 7 us, the
+// latency of the chain of loads.
 constexpr int SP_TK = 32;                  // keys per tile
 constexpr int SP_W = 4;                    // warps
 constexpr int SP_NS = 3;                   // ring slots per warp
@@ -597,7 +601,7 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   };
   if (c.dtype != WS_BF16) {
     q.geo = tile_geo(c.page_size, F32_KEYS);
-    q.wide = R > 16;
+    q.wide = R > 16;                       // 96 requests x 6 heads x 16 rows over 112-448 positions: 178 us in wide tiles, half as rows
     if (!q.wide) {
       q.rows = f32_rows_plan((long long)a.n_req * c.n_kv_heads, a.max_kv, a.mass != nullptr);
       if (q.rows.join) return q;
@@ -646,6 +650,8 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
     return q;
   }
   if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
+  // the smallest row tile that holds all rows (16 rows of 96 requests: 90 us,
+  // 103 in a tile of 32; 8 rows 88 in either)
   q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
   q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
   const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;

@@ -158,7 +158,11 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
   __syncthreads();
   // warps take row groups in turn and, within one, every KW-th step of four keys
   const int RG = (R + NR - 1) / NR, KW = RG >= RW ? 1 : RW / RG, kw = warp / RG;
-  const int kb = min(r.L, rank * keys), ke = min(r.L, kb + keys);
+  // a cluster shares what the request has (64 requests x 6 heads x 16 rows
+  // over 512-2048 positions with weights: 246 us with fixed ranges, 193 so);
+  // split CTAs take fixed ranges and leave at once where there is nothing
+  const int mine = JOIN ? min(keys, ((r.L + cs - 1) / cs + 3) & ~3) : keys;
+  const int kb = min(r.L, rank * mine), ke = min(r.L, kb + mine);
   const bool works = kw < KW;
   for (int rg = warp % RG; works && rg < RG; rg += RW) {
     const int row = rg * NR + (NR == 8 ? c : c & 1);   // the row whose score this lane ends up with
@@ -578,6 +582,7 @@ static cudaError_t run_rows(const AttnP& p, int cs, int keys, cudaStream_t s) {
 }
 
 cudaError_t launch_f32_rows(const AttnP& p, const F32Rows& f, cudaStream_t s) {
+  // one or two rows: 8 requests x 6 heads x 448 positions 20 us, 24 with groups of eight rows
   const bool one = (long long)p.a.max_q * p.G <= 2, mass = p.a.mass != nullptr;
   if (!f.join) return one ? run_rows<2, false, false>(p, f.ctas, f.keys, s) : run_rows<8, false, false>(p, f.ctas, f.keys, s);
   if (mass) return one ? run_rows<2, true, true>(p, f.ctas, f.keys, s) : run_rows<8, true, true>(p, f.ctas, f.keys, s);
@@ -586,13 +591,18 @@ cudaError_t launch_f32_rows(const AttnP& p, const F32Rows& f, cudaStream_t s) {
 
 F32Rows f32_rows_plan(long long units, int max_kv, bool mass) {
   // About three rounds of three CTAs per SM; none shorter than 64 positions,
-  // and none shorter than 256 beyond the first round.
+  // and none shorter than 256 beyond the first round (64 requests x 6 heads x
+  // 16 rows over 112-448 positions: seven CTAs each 87 us, one each 62).
   constexpr long long ROUND = 3 * 152;
   long long want = (3 * ROUND + units - 1) / units;
   want = std::min(want, std::max({ROUND / units, max_kv / 256ll, 1ll}));
   want = std::min(want, std::max(max_kv / 64ll, 1ll));
   F32Rows f;
-  // one launch where a cluster's CTAs are enough, and keep their scores
+  // One launch where a cluster's CTAs are enough, and keep their scores.
+  // Without weights and beyond one round a second kernel joins faster, because
+  // nothing waits for the cluster's last CTA (16 rows over 512-2048 positions:
+  // 24 requests 80 us against 97, 64 requests 168 against 179; 8 requests, one
+  // round, 448 positions: 27 against 30).
   const bool fits = !mass || max_kv <= CL_MAX * CL_KEYS;
   f.join = fits && (mass || units * want <= ROUND) && (want <= CL_MAX || max_kv <= CL_MAX * 512);
   if (f.join && want > CL_MAX) want = CL_MAX;
