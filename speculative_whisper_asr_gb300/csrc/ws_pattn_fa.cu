@@ -141,6 +141,7 @@ struct TileInfo {
   int page;                                        // this lane's page to copy, or -1
   int tok, base, dst;                              // first token in it, the tile's first position, byte offset of the copy
   uint32_t valid[4];
+  bool clean;                                      // every row that the copies write counts, or is a zero behind a page's end
 };
 __device__ __forceinline__ int tile_entry(const AttnP& p, int t, int lane) {
   return p.geo.tpp ? t / p.geo.tpp : (t << p.geo.ppt_log) + lane;
@@ -161,6 +162,7 @@ __device__ __forceinline__ TileInfo tile_info(const AttnP& p, int t, int page, i
     for (int q = 0; q < 4; ++q)
       f.valid[q] = __ballot_sync(0xffffffffu, ok && 32 * q + lane < room && f.base + 32 * q + lane < limit);
     f.page = lane == 0 && ok && f.base < limit ? page : -1;
+    f.clean = ok && f.base + room <= limit;        // one page: the same in every lane
   } else {
     const int ps = 1 << p.geo.page_log;
     f.tok = 0;
@@ -173,6 +175,7 @@ __device__ __forceinline__ TileInfo tile_info(const AttnP& p, int t, int page, i
       f.valid[q] = __ballot_sync(0xffffffffu, ((okm >> (j >> p.geo.page_log)) & 1u) && f.base + j < limit);
     }
     f.page = (okm >> lane) & 1u ? page : -1;
+    f.clean = (f.valid[0] & f.valid[1] & f.valid[2] & f.valid[3]) == 0xffffffffu;
   }
   return f;
 }
@@ -286,21 +289,20 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
       const bool go = f.page >= 0;
       const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 128u;
-      const bool whole = (f.valid[0] & f.valid[1] & f.valid[2] & f.valid[3]) == 0xffffffffu;
-      uint64_t* bar = values && !whole ? &B.raw : &B.full[s];
+      uint64_t* bar = values && !f.clean ? &B.raw : &B.full[s];
       if (lane == 0) {
         if (!values) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) meta[s].valid[q] = f.valid[q];
           meta[s].base = f.base;
-          meta[s].full = whole;
+          meta[s].full = (f.valid[0] & f.valid[1] & f.valid[2] & f.valid[3]) == 0xffffffffu;
         }
         tc::mbar_expect_tx(bar, bytes);
       }
       __syncwarp();
       if (go) tma_load_4d((values ? sV(s) : sK(s)) + f.dst, values ? &mv : &mk, bar, 0, f.tok, h, f.page);
       ++issued;
-      if (values && !whole) {
+      if (values && !f.clean) {
         // value rows behind the cache's length, or of skipped pages, may hold
         // anything (0 * inf would reach the sums): cleared before the tile is
         // handed over
@@ -409,6 +411,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (!dense) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          if (mt.valid[q] == 0xffffffffu && base + 32 * q + 32 <= lim_all) continue;
           const int room = lim - base - 32 * q;    // columns of this word below the row's limit
           const uint32_t see = mt.valid[q] & (room >= 32 ? 0xffffffffu : room <= 0 ? 0u : (1u << room) - 1u);
 #pragma unroll
