@@ -9,15 +9,18 @@
 // are integers, so their order does not matter.
 //
 // evict_move copies the kept rows.  Its floor is HBM: every kept key and value
-// is read and written once.  To fresh pages, all rows move at once.  In
-// place, a destination is never behind its source, so a CTA goes through the
-// rows in order, a batch read before the batch is written; the parallelism
-// comes from cutting the rows into 32-byte columns, which never mix.
+// is read and written once.  To fresh pages, all rows move at once.
+//
+// evict_compact moves them in place.  A destination is never behind its
+// source, so a CTA goes through the rows in order, a batch read before the
+// batch is written; the parallelism comes from cutting the rows into parts,
+// which never mix.
 //
 // 96 requests x 20 heads, up to 1500 positions cut to 512 (514 MB): selection
-// 19 us, move 82 us (6.1 TB/s); 8 requests x 8 heads, up to 65,536 cut to
-// 16,384 (560 MB): 25 and 89 us.  Selecting inside the moving kernel took 136
-// and 250 us: a CTA's histogram passes leave the memory idle.
+// 19 us, move 82 us (6.1 TB/s), in place 95; 8 requests x 8 heads, up to
+// 65,536 cut to 16,384 (560 MB): 25 and 89 us, in place 120.  Selecting inside
+// the moving kernel took 136 and 250 us: a CTA's histogram passes leave the
+// memory idle.
 #include "ws_paged.cuh"
 
 namespace {
@@ -264,57 +267,73 @@ __global__ void __launch_bounds__(MV_NT) evict_move(const EvictP p) {
   }
 }
 
-// In place: one CTA per (request, head, keys or values, 32-byte column).  For
-// the calls measured above 167 and 213 us (fresh pages: 106 and 119); with
-// columns of 64 bytes 153 and 344, of 128 bytes 151 and 610.
-template <typename T>
-__global__ void __launch_bounds__(MV_NT) evict_compact(const EvictP p) {
-  constexpr int COLS = WS_DH * sizeof(T) / 32, U = 4, STEP = MV_NT / 2 * U;
+// In place: one CTA per (request, head, keys or values, part of the row: P
+// pieces of 16 bytes).  A batch of rows is read before any of it is written;
+// the next batch's places are looked up while the loads are in flight.
+constexpr int CP_NT = 512;
+template <typename T, int P>
+__global__ void __launch_bounds__(CP_NT) evict_compact(const EvictP p) {
+  constexpr int PARTS = WS_DH * sizeof(T) / (16 * P), U = 4, STEP = CP_NT / P * U, M = (STEP + CP_NT - 1) / CP_NT;
+  __shared__ Move mv[2][STEP];
   const int h = blockIdx.y, i = blockIdx.z, H = p.c.n_kv_heads;
-  const int col = blockIdx.x % COLS, which = blockIdx.x / COLS;
+  const int col = blockIdx.x % PARTS, which = blockIdx.x / PARTS, tid = threadIdx.x;
   const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
   pdl_wait();
   if (slot < 0 || slot >= p.c.n_slots) return;
   const int keep = min(p.len[i], p.a.keep);
-  if (h == 0 && blockIdx.x == 0 && threadIdx.x == 0) p.a.kv_len_out[slot] = keep;
+  if (h == 0 && blockIdx.x == 0 && tid == 0) p.a.kv_len_out[slot] = keep;
   const int32_t* idx = p.idx + ((size_t)i * H + h) * p.a.keep;
   const size_t unit = (size_t)slot * H + h;
-  uint4* base = (uint4*)(which ? p.c.v : p.c.k) + 2 * col + (threadIdx.x & 1);
-  const int r = threadIdx.x >> 1;
-  const bool marks = blockIdx.x == 0 && (threadIdx.x & 1) == 0;     // this thread also moves the masses and labels
-  for (int j0 = 0; j0 < keep; j0 += STEP) {
+  uint4* base = (uint4*)(which ? p.c.v : p.c.k) + P * col + tid % P;
+  const bool marks = blockIdx.x == 0;           // this CTA also moves the masses and labels
+  int from[M];                                  // sources of the rows this thread looks up
+  auto look_up = [&](int j0, Move* m) {
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+      const int x = q * CP_NT + tid, j = j0 + x;
+      if (x >= STEP) continue;
+      from[q] = j < keep ? idx[j] : -1;
+      Move w;
+      w.src = w.dst = -1;
+      if (j < keep && from[q] != j) w = move_of<T>(p, slot, h, from[q], j);
+      m[x] = w;
+    }
+  };
+  look_up(0, mv[0]);
+  __syncthreads();
+  for (int j0 = 0, buf = 0; j0 < keep; j0 += STEP, buf ^= 1) {
     uint4 reg[U];
     long long dst[U];
-    float ms[U];
-    int ps[U];
+    float ms[M];
+    int ps[M];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * (MV_NT / 2) + r;
-      dst[u] = -1;
-      if (j < keep) {
-        const int src = idx[j];
-        if (src != j) {
-          const Move m = move_of<T>(p, slot, h, src, j);
-          if (m.src >= 0) { reg[u] = base[m.src]; dst[u] = m.dst; }
-        }
-        if (marks) {
-          ms[u] = p.a.mass[unit * p.a.mass_stride + src];
-          ps[u] = p.a.pos ? p.a.pos[unit * p.a.pos_stride + src] : src;
-        }
-      }
+      const Move m = mv[buf][u * (CP_NT / P) + tid / P];
+      dst[u] = m.src >= 0 ? m.dst : -1;
+      if (m.src >= 0) reg[u] = base[m.src];
     }
+    bool on[M];
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+      on[q] = marks && q * CP_NT + tid < STEP && from[q] >= 0;
+      if (!on[q]) continue;
+      ms[q] = p.a.mass[unit * p.a.mass_stride + from[q]];
+      ps[q] = p.a.pos ? p.a.pos[unit * p.a.pos_stride + from[q]] : from[q];
+    }
+    look_up(j0 + STEP, mv[buf ^ 1]);
     __syncthreads();                            // the batch is read before any of it is written
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * (MV_NT / 2) + r;
+    for (int u = 0; u < U; ++u)
       if (dst[u] >= 0) base[dst[u]] = reg[u];
-      if (marks && j < keep) {
-        if (p.a.mass_out) p.a.mass_out[unit * p.a.mass_out_stride + j] = ms[u];
-        if (p.a.pos_out) p.a.pos_out[unit * p.a.pos_out_stride + j] = ps[u];
-      }
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+      if (!on[q]) continue;
+      const int j = j0 + q * CP_NT + tid;
+      if (p.a.mass_out) p.a.mass_out[unit * p.a.mass_out_stride + j] = ms[q];
+      if (p.a.pos_out) p.a.pos_out[unit * p.a.pos_out_stride + j] = ps[q];
     }
     // a later batch reads positions behind all of this one's destinations,
-    // and rows are read and written by the same columns' CTA alone
+    // and a part of the rows is read and written by this CTA alone
   }
 }
 
@@ -375,11 +394,18 @@ cudaError_t select(EvictP& p, cudaStream_t s) {
   return e;
 }
 
+template <typename T, int P>
+cudaError_t compact(const EvictP& p, cudaStream_t s) {
+  return launch_after(evict_compact<T, P>, dim3(2 * WS_DH * sizeof(T) / (16 * P), p.c.n_kv_heads, p.a.n_req), CP_NT, 0, s, p);
+}
+
 template <typename T>
 cudaError_t move(const EvictP& p, bool in_place, cudaStream_t s) {
   constexpr int V = WS_DH * sizeof(T) / 16, ROWS = 8 * MV_NT / (2 * V);
-  if (in_place)
-    return launch_after(evict_compact<T>, dim3(2 * WS_DH * sizeof(T) / 32, p.c.n_kv_heads, p.a.n_req), MV_NT, 0, s, p);
+  // 128 bytes of a row per CTA, or 64 where that gives too few CTAs (96 x 20
+  // heads cut from 1500 to 512 115 and 127 us; 8 x 8 heads from 65,536 to
+  // 16,384 183 and 147, with 32 bytes 193 and 200)
+  if (in_place) return 2ll * p.a.n_req * p.c.n_kv_heads >= 4 * 152 ? compact<T, 8>(p, s) : compact<T, 4>(p, s);
   return launch_after(evict_move<T>, dim3((p.a.keep + ROWS - 1) / ROWS, p.c.n_kv_heads, p.a.n_req), MV_NT, 0, s, p);
 }
 

@@ -161,7 +161,7 @@ class Decoder:
         (ws_evict_frames) and clear their masses, whose positions are the caches' no more."""
         mass = self.frame_mass()
         B.ws_evict_frames(self.ctx, req.numel(), req.data_ptr(), mass.data_ptr(), keep, _stream())
-        mass[:, req.long()] = 0
+        mass.index_fill_(1, req.long(), 0.0)
 
     # ------------------------------------------------------------------ batch state
     def new_batch(self, req, budgets, tcap: int | None = None, sampling: bool = False,
@@ -401,7 +401,7 @@ def _frames_round(dec: Decoder, batch: Batch, rounds: int, keep_frames, evict_af
     if keep_frames is None or rounds > evict_after:
         return
     if rounds == 0:
-        dec.frame_mass()[:, batch.req.long()] = 0
+        dec.frame_mass().index_fill_(1, batch.req.long(), 0.0)
         dec.accumulate_frames(True)
     if rounds == evict_after:
         dec.accumulate_frames(False)
