@@ -577,7 +577,7 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
 // The launch shape and the workspace of a call: a function of the host sizes.
 struct Plan {
   F32Rows rows = {};                       // fp32, up to 16 rows
-  bool wide = false;                       // fp32: row tiles of 64 rows, not 16
+  int rpt = 0;                             // fp32: row tiles of 16 * rpt rows (0: up to 16 rows, f32_rows_kernel)
   bool fa = false;                         // tcgen05 row tiles instead of streaming ones
   int nt = 1;                              // streaming row tile: 8 * nt rows
   int row_tiles = 1, nsplit = 1, tps = 1;
@@ -601,15 +601,17 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   };
   if (c.dtype != WS_BF16) {
     q.geo = tile_geo(c.page_size, F32_KEYS);
-    q.wide = R > 16;                       // 96 requests x 6 heads x 16 rows over 112-448 positions: 178 us in wide tiles, half as rows
-    if (!q.wide) {
+    // 64 requests x 6 heads over 112-448 positions: 16 rows 62 us as rows, 17
+    // rows 73 us in tiles of 32 and 87 in tiles of 64, 48 rows 106 and 90
+    q.rpt = R <= 16 ? 0 : R <= 32 ? 2 : 4;
+    if (!q.rpt) {
       q.rows = f32_rows_plan((long long)a.n_req * c.n_kv_heads, a.max_kv, a.mass != nullptr);
       if (q.rows.join) return q;
       q.nsplit = q.rows.ctas;
     }
     if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
-    if (!q.wide) { partials(R); return q; }
-    q.row_tiles = (int)((R + 63) / 64);
+    if (!q.rpt) { partials(R); return q; }
+    q.row_tiles = (int)((R + 16 * q.rpt - 1) / (16 * q.rpt));
     const int tiles = max(1, (a.max_kv + F32_KEYS - 1) / F32_KEYS);
     const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
     // enough CTAs for two rounds of two per SM
@@ -700,10 +702,10 @@ cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
 }
 
 cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
-  cudaError_t e = q.wide ? launch_f32(p, s) : launch_f32_rows(p, q.rows, s);
+  cudaError_t e = q.rpt ? launch_f32(p, q.rpt, s) : launch_f32_rows(p, q.rows, s);
   if (e == cudaSuccess && q.parts) e = combine<float>(p, s);
   if (e != cudaSuccess || !p.a.mass || p.a.max_kv == 0 || q.rows.join) return e;
-  return launch_f32_mass(p, q.wide, s);
+  return launch_f32_mass(p, q.rpt, s);
 }
 
 cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int pad_H, const int32_t* chunk_len,

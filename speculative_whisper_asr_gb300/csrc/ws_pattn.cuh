@@ -102,11 +102,11 @@ inline int fa_rows(int G) { return G * (FA_ROWS / G); }                        /
 cudaError_t launch_fa(const AttnP& p, cudaStream_t s);
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s);
 
-// The fp32 model (ws_pattn_f32.cu): row tiles of 64 rows and key tiles of
+// The fp32 model (ws_pattn_f32.cu): row tiles of 32 or 64 rows and key tiles of
 // F32_KEYS positions; up to 16 rows per KV head in f32_rows_kernel.
 constexpr int F32_KEYS = 64;
-cudaError_t launch_f32(const AttnP& p, cudaStream_t s);
+cudaError_t launch_f32(const AttnP& p, int rpt, cudaStream_t s);
 struct F32Rows { int ctas, keys; bool join; };   // CTAs per (request, KV head), positions each, joined by a cluster
 F32Rows f32_rows_plan(long long units, int max_kv, bool mass);
 cudaError_t launch_f32_rows(const AttnP& p, const F32Rows& f, cudaStream_t s);
-cudaError_t launch_f32_mass(const AttnP& p, bool wide, cudaStream_t s);
+cudaError_t launch_f32_mass(const AttnP& p, int rpt, cudaStream_t s);

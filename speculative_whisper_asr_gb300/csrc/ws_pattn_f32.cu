@@ -6,8 +6,9 @@
 // asynchronous copies.  A thread owns RPT rows x 4 keys of S and RPT rows x 4
 // dims of O; operands are read as 16-byte vectors along the summed dimension
 // (row pitch 68 floats, so neighbouring rows start in different banks), which
-// gives 16 RPT multiply-adds for RPT + 4 shared loads (RPT = 4: bound by the
-// FMA pipe).
+// gives 16 RPT multiply-adds for RPT + 4 shared loads.  RPT = 2 up to 32 rows,
+// else 4; 4 requests x 8 heads x 1000 rows over 512-2048 positions 313 us (26
+// TFLOP/s; 430 with RPT = 2).
 //
 // f32_rows_kernel.  Blocks and single tokens (up to 16 rows per KV head):
 // the cache is read once, straight into registers.  Eight lanes share a key,
@@ -18,7 +19,9 @@
 // by a cluster of up to 8 CTAs, whose statistics and values meet through
 // distributed shared memory; the scores wait in shared memory until the rows'
 // log-sum-exp is known, so that each CTA adds its own positions' weights: one
-// launch.  Longer ranges are split and joined by a second kernel.
+// launch (8 requests x 6 heads x 16 rows over 112-448 positions with weights
+// 16.4 us, a chain of latencies).  Longer ranges are split and joined by a
+// second kernel.
 //
 // f32_mass_kernel.  The weights of a tile of 64 keys: the keys stay in shared
 // memory, the rows pass by, each thread sums its rows of 4 keys, and the 16
@@ -613,5 +616,7 @@ F32Rows f32_rows_plan(long long units, int max_kv, bool mass) {
   return f;
 }
 
-cudaError_t launch_f32(const AttnP& p, cudaStream_t s) { return run_f32<4>(p, s); }
-cudaError_t launch_f32_mass(const AttnP& p, bool wide, cudaStream_t s) { return wide ? run_mass<4>(p, s) : run_mass<1>(p, s); }
+cudaError_t launch_f32(const AttnP& p, int rpt, cudaStream_t s) { return rpt == 2 ? run_f32<2>(p, s) : run_f32<4>(p, s); }
+cudaError_t launch_f32_mass(const AttnP& p, int rpt, cudaStream_t s) {
+  return rpt == 0 ? run_mass<1>(p, s) : rpt == 2 ? run_mass<2>(p, s) : run_mass<4>(p, s);
+}

@@ -279,6 +279,14 @@ def test_attention_between_streaming_and_wide_row_tiles(R, c, G, causal):
     _check(R, AttnCase([c], [1700], hq=2 * G, hkv=2, causal=causal, seed=c + G))
 
 
+@pytest.mark.parametrize("c", [15, 16, 17, 31, 32, 33, 47])
+@pytest.mark.parametrize("n", [2, 40])
+def test_fp32_row_tiles(R, c, n):
+    """Around the fp32 row tiles of 16, 32 and 64 rows, with few requests (joined key ranges) and many."""
+    lens = [max(c, 30 + 53 * (i % 7)) for i in range(n)]
+    _check(R, AttnCase([c if i % 3 else max(1, c - 9) for i in range(n)], lens, dtype=F32, seed=c + n))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("c", [1, 6, 30, 90])
 def test_attention_nan_row_stays_alone(R, dtype, c):
