@@ -657,13 +657,19 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
   q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
   const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
-  // enough CTAs for about four rounds of the machine, none shorter than 512 keys
-  const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
   q.geo = tile_geo(c.page_size, SP_TK);
   const int tiles = max(1, tile_count(q.geo, c.page_size, SP_TK, a.max_kv));
+  // Enough CTAs for about four rounds of the machine, none shorter than 512
+  // keys.  With weights, one CTA keeps all scores where they fit, unless that
+  // leaves most SMs idle: 20 heads x 9 rows x 2048 positions of 1 / 4 / 16
+  // requests 32 / 33 / 60 us in one CTA each, 27 / 43 / 92 us split and with
+  // the second pass over the keys.
+  const bool fits = a.mass && q.row_tiles == 1 && tiles <= SP_W * sp_stash_tiles(q.nt);
+  const int want = fits && units >= SMS / 2 ? 1
+                                            : (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
   q.tps = (tiles + want - 1) / want;
   q.nsplit = (tiles + q.tps - 1) / q.tps;
-  q.stash = a.mass && q.nsplit == 1 && q.row_tiles == 1 && tiles <= SP_W * sp_stash_tiles(q.nt);
+  q.stash = fits && q.nsplit == 1;
   partials(R);
   return q;
 }

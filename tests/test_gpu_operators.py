@@ -279,6 +279,13 @@ def test_attention_between_streaming_and_wide_row_tiles(R, c, G, causal):
     _check(R, AttnCase([c], [1700], hq=2 * G, hkv=2, causal=causal, seed=c + G))
 
 
+@pytest.mark.parametrize("c,kv", [(1, 4096), (1, 4097), (8, 4096), (9, 2048), (9, 2049), (16, 2048), (32, 2048), (32, 2049)])
+@pytest.mark.parametrize("page", [64, 100])
+def test_attention_scores_that_just_fit(R, c, kv, page):
+    """Weights with the longest caches whose scores one CTA keeps, and one position more."""
+    _check(R, AttnCase([c] * 10, [kv, 1, 700] + [40] * 7, hq=8, hkv=8, page=page, causal=c < 32, seed=c + kv))
+
+
 @pytest.mark.parametrize("c", [15, 16, 17, 31, 32, 33, 47])
 @pytest.mark.parametrize("n", [2, 40])
 def test_fp32_row_tiles(R, c, n):
