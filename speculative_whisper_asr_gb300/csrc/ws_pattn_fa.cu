@@ -443,10 +443,12 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       // The weights go by the reference at hand.  A floating sum does not mind
       // large weights, so the maximum is looked for only where a row has no
       // reference yet or its sum grew past 2^60 (the scores are still in
-      // registers then).
+      // registers then).  Lanes without a row have no say: theirs are other
+      // requests' rows, rows behind the last chunk, or shared memory that no
+      // copy writes (rows TR .. 127), and a row's bits may not depend on them.
       float tile = 0.f;
       if (j > 0) tile = weigh();
-      if (__any_sync(0xffffffffu, m == -INFINITY || !(tile < MOST))) {
+      if (j == 0 || __any_sync(0xffffffffu, on && (m == -INFINITY || !(tile < MOST)))) {
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < FA_KEYS; e += 8)
