@@ -201,8 +201,11 @@ typedef struct {
  *   queries then move from their tree rows to block rows 1..a, so the cache
  *   holds the accepted tokens at positions L+1..L+a as after a linear
  *   acceptance.
+ * A row that would emit a token but has none left (GREEDY, FORCED: target < 0;
+ *   SAMPLE: no logit above -inf, as when a grammar excludes every token)
+ *   emits nothing and ends the request; bit 8 of the status word is set.
  * Then L <- L + 1 + a (the old anchor plus the accepted candidates), R -= n_emit,
- * done when EOS was emitted or R == 0. */
+ * done when EOS was emitted, R == 0 or no token was left. */
 int ws_accept(ws_ctx* ctx, int n_req, const int32_t* req_ids,
               const ws_accept_args* args, ws_stream stream);
 
@@ -349,7 +352,10 @@ int ws_set_suppress(ws_ctx* ctx, const uint32_t* mask);
 int ws_get_lengths(ws_ctx* ctx, int n_req, const int32_t* req_ids, int32_t* out,
                    ws_stream stream);
 
-/* Synchronise `stream`, return and clear the device status word (0 = ok). */
+/* Synchronise `stream`, return and clear the device status word: 0 = ok, else
+ * the sum of 1 (a position at or beyond max_pos), 2 (a token id outside the
+ * vocabulary), 4 (frame counts that do not fit max_frames) and 8 (a request
+ * ended at a row that no token was left for). */
 int ws_status(ws_ctx* ctx, ws_stream stream, int32_t* host_status);
 
 /* Name of the GEMM engine in use ("simt" or "tcgen05"). */
@@ -581,7 +587,8 @@ typedef struct {
  *            block_len and where no token is left above -inf
  *   logprob  0 for rows >= block_len, -inf where target is -1
  * A NaN logit is never chosen (its row's logprob is NaN).  Rows >= block_len of `out` are left as they
- * were.  ws_accept takes target (GREEDY) or out (SAMPLE) as its own.
+ * were.  ws_accept takes target (GREEDY) or out (SAMPLE) as its own, and ends
+ * a request at a row that no token is left for.
  * At most 4,096 tokens (hist_stride + H - 1, or window) and biases
  * (bias_stride) per row: WS_EUNSUPPORTED beyond. */
 int ws_logits_rules(const ws_rules_args* args, ws_stream stream);

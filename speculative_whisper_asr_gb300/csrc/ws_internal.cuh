@@ -18,6 +18,7 @@ typedef __nv_bfloat16 bf16;
 #define WS_ST_POS 1       // a position at or beyond max_pos was requested
 #define WS_ST_TOKEN 2     // a token id outside [0, V) was seen
 #define WS_ST_FRAMES 4    // frame counts inconsistent with max_frames
+#define WS_ST_EMPTY 8     // a request ended at a row that no token was left for
 
 // ------------------------------------------------------------------ conversions
 template <typename T> __device__ __forceinline__ float to_f(T v);

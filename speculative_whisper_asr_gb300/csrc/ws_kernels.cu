@@ -270,6 +270,7 @@ __global__ void get_lengths_kernel(int n, const int32_t* req_ids, const int32_t*
 
 // ------------------------------------------------------------------ sampling helpers
 constexpr int SNT = 256;   // threads of the sampling / acceptance CTAs
+constexpr int ROW_EMPTY = 3;   // acceptance stopped at a row without a token
 
 __device__ __forceinline__ bool suppressed(const uint32_t* sup, int v) {
   return sup && ((sup[v >> 5] >> (v & 31)) & 1u);
@@ -724,7 +725,9 @@ __global__ void __launch_bounds__(128) window_attn_kernel(int H, const int32_t* 
 }
 
 // ------------------------------------------------------------------ acceptance
-// One CTA per request.  Whisper-Flash §3.1 / Appendix A.1 / A.4.
+// One CTA per request.  Whisper-Flash §3.1 / Appendix A.1 / A.4.  A row that
+// would emit but has no token left (target < 0, or no logit above -inf: a
+// grammar excluded all) ends its request with what it has.
 __global__ void __launch_bounds__(SNT) accept_kernel(AcceptParams P) {
   __shared__ double cdf_scratch[(SNT / 32) * CDF_SROWS];
   __shared__ float sh[SNT + 8];
@@ -796,13 +799,17 @@ __global__ void __launch_bounds__(SNT) accept_kernel(AcceptParams P) {
         last_row = cur;
       } else {
         for (int j = 1; j <= n_prop; ++j) {
-          if (blk[j] != g[j - 1]) break;
+          if (blk[j] != g[j - 1] || g[j - 1] < 0) break;
           ++a;
           s_emit[ne++] = blk[j];
           if (blk[j] == P.eos) { eos_hit = true; break; }
         }
       }
-      if (!eos_hit) s_emit[ne++] = g[last_row < 0 ? a : last_row];
+      if (!eos_hit) {
+        const int tok = g[last_row < 0 ? a : last_row];
+        if (tok >= 0) s_emit[ne++] = tok;
+        else s_stop = ROW_EMPTY;
+      }
       s_a = a;
       s_ne = ne;
     }
@@ -819,6 +826,11 @@ __global__ void __launch_bounds__(SNT) accept_kernel(AcceptParams P) {
       RowStat sp, sq;
       sp.m = ps.x; sp.S = ps.y;
       sq.m = qs.x; sq.S = qs.y;
+      if (sp.m == -INFINITY) {                     // the same in every thread
+        if (threadIdx.x == 0) s_stop = ROW_EMPTY;
+        __syncthreads();
+        break;
+      }
       const bool yok = y >= 0 && y < P.V;
       const float py = yok ? expf(scaled(zp, y, T, P.suppress) - sp.m) / sp.S : 0.0f;
       const float qy = yok ? expf(scaled(zq, y, T, P.suppress) - sq.m) / sq.S : 0.0f;
@@ -871,10 +883,14 @@ __global__ void __launch_bounds__(SNT) accept_kernel(AcceptParams P) {
       const float2 ps = P.pstat[(size_t)i * A.H + n_prop];
       RowStat sp;
       sp.m = ps.x; sp.S = ps.y;
-      const float u2 = ws_uniform(A.seed, (uint32_t)slot, A.round, (uint32_t)(n_prop + 1), 2u);
-      int tok = block_inverse_cdf([&](int v) { return expf(scaled(zp, v, T, P.suppress) - sp.m) / sp.S; }, P.V, u2,
-                                  cdf_scratch);
-      if (threadIdx.x == 0) s_emit[s_ne++] = tok;
+      if (sp.m == -INFINITY) {
+        if (threadIdx.x == 0) s_stop = ROW_EMPTY;
+      } else {
+        const float u2 = ws_uniform(A.seed, (uint32_t)slot, A.round, (uint32_t)(n_prop + 1), 2u);
+        int tok = block_inverse_cdf([&](int v) { return expf(scaled(zp, v, T, P.suppress) - sp.m) / sp.S; }, P.V, u2,
+                                    cdf_scratch);
+        if (threadIdx.x == 0) s_emit[s_ne++] = tok;
+      }
     }
     __syncthreads();
   }
@@ -883,8 +899,10 @@ __global__ void __launch_bounds__(SNT) accept_kernel(AcceptParams P) {
     const int a = s_a, ne = s_ne;
     P.L[slot] += 1 + a;                 // rollback by length: keep the anchor + a candidates
     R -= ne;
-    const int last = s_emit[ne - 1];
-    const bool done = (last == P.eos) || R <= 0;
+    const bool empty = s_stop == ROW_EMPTY;
+    if (empty) atomicOr(P.status, WS_ST_EMPTY);
+    const int last = ne > 0 ? s_emit[ne - 1] : blk[0];
+    const bool done = empty || last == P.eos || R <= 0;
     A.budget[i] = R;
     A.n_acc[i] = a;
     A.n_emit[i] = ne;

@@ -77,3 +77,66 @@ def test_a_request_does_not_change_with_the_next_one(R):
     for k in (0, 1):
         assert torch.equal(a[k][:70], b[k][:70])
     assert torch.equal(a[2][0], b[2][0])
+
+
+# ------------------------------------------------------------------ a grammar that leaves no token
+def _allow_all_or_nothing(R, s):
+    words = (s.vocab + 31) // 32
+    m = np.zeros((2, words), np.uint32)
+    m[0] = 0xFFFFFFFF                                         # state 0: every token, state 1: none
+    return R.LogitsRules(masks=torch.as_tensor(m.view(np.int32)).cuda())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mode", ["ar", "spec", "sample-ar", "sample-spec"])
+@pytest.mark.parametrize("where", ["prompt", "first", "later"])
+def test_a_state_without_tokens_ends_the_request(R, dtype, mode, where):
+    """Request 0 reaches a grammar state that excludes every token: it ends there, with what it had, and the status
+    word says so.  Request 1 goes on as if alone."""
+    n, budget = 2, 12
+    s, dec, req, _ = _decoder(R, dtype, n)
+    sampling, spec = mode.startswith("sample"), mode.endswith("spec")
+    if where == "later" and not spec:
+        pytest.skip("rows behind the first exist in speculative rounds")
+
+    def run(dead):
+        b = dec.new_batch(req, [budget] * n, sampling=sampling, rules=_allow_all_or_nothing(R, s))
+        P = len(s.prompt)
+        for H in (1, P, s.K + 1):
+            b.states(H).fill_(0)
+        if dead and where == "prompt":
+            b.states(P)[0] = 1
+        elif dead and where == "first":
+            b.states(1)[0] = 1
+            b.states(s.K + 1)[0] = 1
+        elif dead:
+            b.states(s.K + 1)[0, 2:] = 1                      # the third row and those after it
+        if spec:
+            rounds = R.run_spec(dec, b, temperature=0.9 if sampling else 0.0, seed=3, max_rounds=200)
+        elif sampling:
+            rounds = R.run_ar_sampling(dec, b, 0.9, 3, max_rounds=200)
+        else:
+            rounds = R.run_ar(dec, b, max_rounds=200)
+        assert rounds < 200
+        return b
+
+    full = run(False)
+    assert dec.status() == 0
+    want = full.transcripts()
+    b = run(True)
+    got = b.transcripts()
+    assert got[1] == want[1]
+    assert all(0 <= t < s.vocab for t in got[0])
+    assert got[0] == want[0][: len(got[0])]
+    if where == "prompt":
+        assert got[0] == []
+    elif where == "first":
+        assert len(got[0]) == 1
+    assert b.done.tolist() == [1, 1] and b.blen.tolist() == [0, 0]
+    ended_early = len(got[0]) < len(want[0])
+    assert ended_early or where == "later"
+    assert dec.status() == (8 if ended_early else 0)
+    assert b.budget[0].item() == budget - len(got[0])
+    # the slots decode on afterwards
+    again = run(False)
+    assert again.transcripts() == want and dec.status() == 0
