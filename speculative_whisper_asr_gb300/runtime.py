@@ -165,18 +165,28 @@ class Decoder:
 
     # ------------------------------------------------------------------ batch state
     def new_batch(self, req, budgets, tcap: int | None = None, sampling: bool = False,
-                  draft_logits: bool = False, rules: "LogitsRules | None" = None) -> "Batch":
+                  draft_logits: bool = False, rules: "LogitsRules | None" = None, next_states=None) -> "Batch":
         """draft_logits: keep the drafter's logits also for greedy decoding
         (needed by a confidence threshold).  rules: penalties, biases and
-        grammar masks applied to the target's logits of every round."""
-        return Batch(self, req, budgets, tcap or self.s.max_pos, sampling, draft_logits, rules)
+        grammar masks applied to the target's logits of every round.
+        next_states(batch, block, block_len, states): called in every round
+        once the block is known and before the rules read the grammar states;
+        it enqueues on the current stream what sets states [n, H].  Column j of
+        block [n, H] is the token before row j (column 0 the anchor, the last
+        of batch.transcript); for the prompt block is None and the transcript
+        empty.  A grammar whose state depends on the tokens needs it, because
+        the proposals do not exist before the round; its rounds are not
+        replayed from a graph."""
+        return Batch(self, req, budgets, tcap or self.s.max_pos, sampling, draft_logits, rules, next_states)
 
 
 class Batch:
     """Device arrays of one decoding batch (request slots `req`)."""
 
     def __init__(self, dec: Decoder, req: torch.Tensor, budgets, tcap: int, sampling: bool,
-                 draft_logits: bool = False, rules: "LogitsRules | None" = None):
+                 draft_logits: bool = False, rules: "LogitsRules | None" = None, next_states=None):
+        if next_states is not None and (rules is None or not rules.has_masks):
+            raise ValueError("next_states sets grammar states: rules with masks are needed")
         self.dec = dec
         self.req = req
         n = req.numel()
@@ -203,6 +213,7 @@ class Batch:
         self.prop_sum = torch.zeros(n, dtype=torch.int64, device=dev)
         self.p_logits = self.q_logits = self.p_logits1 = None
         self.rules = rules
+        self.next_states = next_states
         self._states = {}
         if sampling or rules is not None:
             rows = max(K + 1, len(dec.s.prompt)) if rules is not None else K + 1
@@ -240,7 +251,9 @@ class Batch:
 
     def states(self, H: int) -> torch.Tensor:
         """Grammar states [n, H] int32 of the rows of H-row blocks (a prompt, a single token, a verified block: row j
-        follows the block's first j proposals), read by every round of that height; -1, the start: no constraint."""
+        follows the block's first j proposals), read by every round of that height; -1, the start: no constraint.
+        They stay as the caller sets them, for grammars with one state per request, unless the batch has
+        next_states."""
         if H not in self._states:
             self._states[H] = torch.full((self.n, H), -1, dtype=torch.int32, device=self.dec.dev)
         return self._states[H]
@@ -248,6 +261,8 @@ class Batch:
     def _apply_rules(self, H, block, blen, target, prompt=False):
         """The rules on an H-row verify's logits, in place, and the greedy choice under them into target.  The rows
         of a prompt follow no proposals."""
+        if self.next_states is not None:
+            self.next_states(self, None if prompt else block, blen, self.states(H))
         self.rules.apply(self._logits(H), history=self.transcript, hist_len=self.out_len,
                          block=None if prompt else block, block_len=blen,
                          mask_row=self.states(H) if self.rules.has_masks else None,
@@ -296,7 +311,7 @@ class Batch:
             a = self._args(B.WS_ACCEPT_GREEDY, 1, self.block1, self.blen, self.target1, self.block1, self.blen)
             B.ws_accept(d.ctx, self.n, self.req.data_ptr(), a, _stream())
         self.states(1)                     # allocated outside the capture
-        if graph:
+        if graph and self.next_states is None:
             self.replay(("ar", d.accumulating), calls)
         else:
             calls()
@@ -333,7 +348,7 @@ class Batch:
                 self.replay(("tree", self.dec.tree, self.dec.accumulating), self._tree_calls)
             else:
                 self._tree_calls()
-        elif graph and temperature <= 0.0:
+        elif graph and temperature <= 0.0 and self.next_states is None:
             self.replay(("spec", synthetic is not None, run_drafter, k_verify, threshold, self.dec.accumulating),
                         lambda: self._spec_calls(0, synthetic, 0.0, 0, run_drafter, k_verify, threshold))
         else:

@@ -140,3 +140,59 @@ def test_a_state_without_tokens_ends_the_request(R, dtype, mode, where):
     # the slots decode on afterwards
     again = run(False)
     assert again.transcripts() == want and dec.status() == 0
+
+
+# ------------------------------------------------------------------ a grammar that depends on the tokens
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sampling", [False, True])
+def test_grammar_states_follow_the_proposals(R, dtype, sampling):
+    """The state of a row is given by the token before it: speculative decoding obeys the grammar at every token, and
+    greedy decoding gives the autoregressive transcript."""
+    n, budget = 2, 40
+    s, dec, req, _ = _decoder(R, dtype, n)
+    g = np.random.default_rng(5)
+    words = (s.vocab + 31) // 32
+    m = g.integers(0, 1 << 32, (4, words), dtype=np.uint64).astype(np.uint32)     # half of the tokens after each
+    rules = R.LogitsRules(masks=torch.as_tensor(m.view(np.int32)).cuda())
+    seen = []
+
+    def next_states(batch, block, block_len, states):
+        seen.append(tuple(states.shape))
+        if block is None:                                     # the prompt: the transcript is empty
+            states.fill_(3)
+        else:                                                 # column j is the token before row j
+            assert block.shape == states.shape and block_len.shape == (n,)
+            states.copy_(block % 3)
+
+    def run(spec, **kw):
+        b = dec.new_batch(req, [budget] * n, sampling=sampling, rules=rules, next_states=next_states)
+        if spec:
+            R.run_spec(dec, b, temperature=0.8 if sampling else 0.0, seed=2, **kw)
+        elif sampling:
+            R.run_ar_sampling(dec, b, 0.8, 2)
+        else:
+            R.run_ar(dec, b)
+        tr = b.transcripts()
+        for t in tr:
+            assert len(t) == budget or t[-1] == s.eos_id
+            for j, tok in enumerate(t):
+                state = 3 if j == 0 else t[j - 1] % 3
+                assert (int(m[state, tok // 32]) >> (tok % 32)) & 1, (j, tok)
+        return tr
+
+    ar = run(False)
+    assert (n, len(s.prompt)) in seen and (n, 1) in seen
+    for kw in (dict(), dict(k_verify=3), dict(graph=False)):
+        sp = run(True, **kw)
+        if not sampling:
+            assert sp == ar
+    assert (n, s.K + 1) in seen and (n, 4) in seen
+    assert dec.status() == 0
+
+
+def test_next_states_needs_masks(R):
+    s, dec, req, _ = _decoder(R, "f32", 1)
+    with pytest.raises(ValueError):
+        dec.new_batch(req, [4], next_states=lambda *a: None)
+    with pytest.raises(ValueError):
+        dec.new_batch(req, [4], rules=R.LogitsRules(), next_states=lambda *a: None)
