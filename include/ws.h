@@ -203,7 +203,7 @@ typedef struct {
  *   acceptance.
  * A row that would emit a token but has none left (GREEDY, FORCED: target < 0;
  *   SAMPLE: no logit above -inf, as when a grammar excludes every token)
- *   emits nothing and ends the request; bit 8 of the status word is set.
+ *   emits nothing and ends the request; 16 is added to the status word.
  * Then L <- L + 1 + a (the old anchor plus the accepted candidates), R -= n_emit,
  * done when EOS was emitted, R == 0 or no token was left. */
 int ws_accept(ws_ctx* ctx, int n_req, const int32_t* req_ids,
@@ -354,8 +354,9 @@ int ws_get_lengths(ws_ctx* ctx, int n_req, const int32_t* req_ids, int32_t* out,
 
 /* Synchronise `stream`, return and clear the device status word: 0 = ok, else
  * the sum of 1 (a position at or beyond max_pos), 2 (a token id outside the
- * vocabulary), 4 (frame counts that do not fit max_frames) and 8 (a request
- * ended at a row that no token was left for). */
+ * vocabulary), 4 (frame counts that do not fit max_frames), 8 (a bounded wait
+ * inside a kernel ran out) and 16 (a request ended at a row that no token was
+ * left for). */
 int ws_status(ws_ctx* ctx, ws_stream stream, int32_t* host_status);
 
 /* Name of the GEMM engine in use ("simt" or "tcgen05"). */

@@ -18,7 +18,8 @@ typedef __nv_bfloat16 bf16;
 #define WS_ST_POS 1       // a position at or beyond max_pos was requested
 #define WS_ST_TOKEN 2     // a token id outside [0, V) was seen
 #define WS_ST_FRAMES 4    // frame counts inconsistent with max_frames
-#define WS_ST_EMPTY 8     // a request ended at a row that no token was left for
+#define WS_ST_TIMEOUT 8   // a bounded wait inside a kernel ran out
+#define WS_ST_EMPTY 16    // a request ended at a row that no token was left for
 
 // ------------------------------------------------------------------ conversions
 template <typename T> __device__ __forceinline__ float to_f(T v);
@@ -398,7 +399,6 @@ cudaError_t launch_gemm_tc(const GemmShape& g, const Epi& e, const TcMap& mw, co
                            bool pdl);
 cudaError_t tc_init_attributes();
 int tc_bn_index(int bn);   // 16,32,64,128,256 -> 0..4
-#define WS_ST_TIMEOUT 8   // a bounded wait inside a kernel ran out
 
 template <typename T>
 cudaError_t launch_layernorm(int M, int d, const float* x, int ldx, const T* g, const T* b, T* y, int ldy,
