@@ -725,6 +725,7 @@ class LogitsRules:
 
     def _bind(self, n, V, dev):
         a = self._args
+        self._shape = None                 # a refusal below leaves the arguments half set
         rep, pres, freq, ids, vals, lens, masks = self._own
         for name, t in (("repetition", rep), ("presence", pres), ("frequency", freq)):
             setattr(a, name, 0 if t is None else _rows(name, t, _F32, (n,), dev))

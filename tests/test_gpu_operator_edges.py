@@ -196,3 +196,27 @@ def test_next_states_needs_masks(R):
         dec.new_batch(req, [4], next_states=lambda *a: None)
     with pytest.raises(ValueError):
         dec.new_batch(req, [4], rules=R.LogitsRules(), next_states=lambda *a: None)
+
+
+# ------------------------------------------------------------------ refused calls between sound ones
+def test_rules_after_a_refused_batch_size(R):
+    """A batch of another size is refused; the next sound call still has its biases, penalties and masks."""
+    V = 500
+    z = torch.randn(2, 1, V, device="cuda")
+    ids = torch.tensor([[3], [4]], dtype=torch.int32, device="cuda")
+    vals = torch.full((2, 1), 50.0, device="cuda")
+    lens = torch.ones(2, dtype=torch.int32, device="cuda")
+    masks = torch.full((1, (V + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    masks[0, 0] = ~(1 << 7)
+    row = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    for kw in (dict(bias_ids=ids, bias_vals=vals, bias_len=lens), dict(bias_ids=ids, bias_vals=vals, bias_len=lens, masks=masks)):
+        rules = R.LogitsRules(**kw)
+        state = row if "masks" in kw else None
+        a = rules.apply(z, mask_row=state, out=torch.empty_like(z))
+        with pytest.raises(ValueError):
+            rules.apply(torch.randn(3, 1, V, device="cuda"))
+        with pytest.raises(ValueError):                       # another vocabulary: the masks do not fit
+            rules.apply(torch.randn(3, 1, 2 * V, device="cuda"))
+        b = rules.apply(z, mask_row=state, out=torch.empty_like(z))
+        torch.cuda.synchronize()
+        assert a[0, 0, 3] == z[0, 0, 3] + 50.0 and torch.equal(a, b)
