@@ -318,7 +318,10 @@ int ws_get_centers(ws_ctx* ctx, int n_req, const int32_t* req_ids, int32_t* out,
  *         acoustic keys) and keeps it alive; NULL switches it off (default)
  * The cross-attention then runs in the kernels of ws_paged_attention: rows
  * agree with the usual path within the model's tolerance, not bit for bit,
- * and the kernel-per-operation verify is used.  Host-only; no device work. */
+ * and the kernel-per-operation verify is used.  As on the usual path a row's
+ * bits depend neither on the block's height nor on the other requests, so
+ * speculative greedy output still equals autoregressive greedy output.
+ * Host-only; no device work. */
 int ws_set_frame_mass(ws_ctx* ctx, float* mass);
 
 /* Cut the listed requests' acoustic caches: every target layer and head keeps

@@ -495,7 +495,7 @@ cudaError_t cross_attn_with_mass(ws_ctx* c, int n, int H, const int32_t* req, co
   a.kv_len = c->Fv;
   a.total_q = n * H;
   a.max_q = H;
-  a.max_kv = c->max_fc;
+  a.max_kv = c->d.max_frames;              // not what the requests happen to hold: it cuts the keys into parts
   a.n_heads = c->heads;
   a.scale = 0.125f;                        // 1/sqrt(64)
   a.q = c->q;

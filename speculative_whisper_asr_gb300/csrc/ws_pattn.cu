@@ -19,11 +19,14 @@ namespace {
 // product's operand.  Scores stay raw; p = 2^(s * sl - m * sl) with one FMA
 // and one exponential.  The reference m of a row moves only when a score
 // exceeds it by more than 2^8 (p <= 256), which a vote detects, so the
-// common tile needs no reduction across lanes.  Statistics and sums are
-// fp32.  Up to 8 rows the weights enter the value product as bf16 hi + lo
-// (2^-16 relative), which the copy rate hides; with more rows as one bf16
-// value (2^-8 relative at most, the output's own step: hi + lo costs 7% at 9
-// rows, 94 -> 101 us for 96 requests x 20 heads).
+// common tile needs no reduction across lanes; rows that did not exceed it
+// keep their reference, so a row's bits do not depend on the tile's other
+// rows.  Statistics and sums are fp32.  Up to 8 rows the weights enter the
+// value product as bf16 hi + lo (2^-16 relative), which the copy rate hides;
+// with more rows as one bf16 value (2^-8 relative at most, the output's own
+// step: hi + lo costs 7% at 9 rows, 94 -> 101 us for 96 requests x 20 heads),
+// except for a context's blocks (HILO), whose rows have to come out the same
+// bits in a block of any height.
 //
 // With STASH the raw scores stay in tensor memory, which this kernel has no
 // other use for: each of the four warps owns a lane quarter and parks a
@@ -118,11 +121,10 @@ __device__ __forceinline__ void tm_ld(uint32_t addr, float* v) {
   }
 }
 
-template <int NT, bool STASH>
+template <int NT, bool STASH, bool HILO>
 __global__ void __launch_bounds__(SP_W * 32, NT == 4 ? 1 : 2)
 split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   constexpr int MT = SP_TK / 16;           // key steps of 16
-  constexpr bool HILO = NT == 1;
   constexpr uint32_t ALL = 0xffffffffu;
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t full[SP_W][SP_NS];
@@ -279,7 +281,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
           t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 4));
           t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 8));
           t4 = fmaxf(t4, __shfl_xor_sync(0xffffffffu, t4, 16));
-          const float mn = fmaxf(m[nt][e], t4);
+          const float mn = t4 > m[nt][e] + hold ? t4 : m[nt][e];
           const float f = m[nt][e] > -INFINITY ? ex2((m[nt][e] - mn) * sl) : 0.f;
           m[nt][e] = mn;
           msl[nt][e] = mn > -INFINITY ? mn * sl : 0.f;
@@ -588,7 +590,13 @@ struct Plan {
 };
 constexpr int SMS = 152, SLOTS = 2 * SMS;  // two streaming CTAs on each of 152 SMs
 
-Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
+// `block`: the rows of a context's verify blocks (at most 16 per KV head).  A
+// row has to come out the same bits in blocks of any height and beside any
+// number of requests, so its keys are cut by the host bound max_kv alone (the
+// context passes its max_frames): into one part (bf16), or the parts of one
+// cluster (fp32).
+constexpr int BLOCK_ROWS = 16;
+Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block = false) {
   Plan q;
   const long long R = (long long)a.max_q * (a.n_heads / c.n_kv_heads);
   auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += (n + 255) / 256 * 256; return at; };
@@ -605,7 +613,8 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
     // rows 73 us in tiles of 32 and 87 in tiles of 64, 48 rows 106 and 90
     q.rpt = R <= 16 ? 0 : R <= 32 ? 2 : 4;
     if (!q.rpt) {
-      q.rows = f32_rows_plan((long long)a.n_req * c.n_kv_heads, a.max_kv, a.mass != nullptr);
+      q.rows = block ? f32_block_plan(a.max_kv)
+                     : f32_rows_plan((long long)a.n_req * c.n_kv_heads, a.max_kv, a.mass != nullptr);
       if (q.rows.join) return q;
       q.nsplit = q.rows.ctas;
     }
@@ -665,8 +674,9 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   // requests 32 / 33 / 60 us in one CTA each, 27 / 43 / 92 us split and with
   // the second pass over the keys.
   const bool fits = a.mass && q.row_tiles == 1 && tiles <= SP_W * sp_stash_tiles(q.nt);
-  const int want = fits && units >= SMS / 2 ? 1
-                                            : (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
+  const int want = block || (fits && units >= SMS / 2)
+                       ? 1
+                       : (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
   q.tps = (tiles + want - 1) / want;
   q.nsplit = (tiles + q.tps - 1) / q.tps;
   q.stash = fits && q.nsplit == 1;
@@ -674,11 +684,11 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a) {
   return q;
 }
 
-template <int NT, bool STASH>
+template <int NT, bool STASH, bool HILO = NT == 1>
 cudaError_t run_split(const AttnP& p, const Plan& q, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<NT, STASH>, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM);
+  cudaError_t e = cudaFuncSetAttribute(split_kernel<NT, STASH, HILO>, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM);
   if (e != cudaSuccess) return e;
-  split_kernel<NT, STASH><<<dim3(q.row_tiles * q.nsplit, p.c.n_kv_heads, p.a.n_req), SP_W * 32, SP_SMEM, s>>>(
+  split_kernel<NT, STASH, HILO><<<dim3(q.row_tiles * q.nsplit, p.c.n_kv_heads, p.a.n_req), SP_W * 32, SP_SMEM, s>>>(
       p, reinterpret_cast<const CUtensorMap&>(mk), reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
   return cudaGetLastError();
@@ -689,6 +699,7 @@ cudaError_t run_streaming(const AttnP& p, const Plan& q, cudaStream_t s) {
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)q.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)q.geo.box))
     return cudaErrorInvalidValue;
   if (q.nt == 1) return q.stash ? run_split<1, true>(p, q, mk, mv, s) : run_split<1, false>(p, q, mk, mv, s);
+  if (q.nt == 2 && p.pad_H) return q.stash ? run_split<2, true, true>(p, q, mk, mv, s) : run_split<2, false, true>(p, q, mk, mv, s);
   if (q.nt == 2) return q.stash ? run_split<2, true>(p, q, mk, mv, s) : run_split<2, false>(p, q, mk, mv, s);
   return q.stash ? run_split<4, true>(p, q, mk, mv, s) : run_split<4, false>(p, q, mk, mv, s);
 }
@@ -736,11 +747,12 @@ cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int 
 }  // namespace
 
 size_t block_attention_workspace(const ws_paged_cache& cache, const ws_attention_args& args) {
-  return make_plan(cache, args).bytes;
+  return make_plan(cache, args, true).bytes;
 }
 cudaError_t launch_block_attention(const ws_paged_cache& cache, const ws_attention_args& args, int H,
                                    const int32_t* block_len, void* workspace, cudaStream_t s) {
-  return run(cache, args, H, block_len, make_plan(cache, args), (char*)workspace, s);
+  if ((long long)args.max_q * (args.n_heads / cache.n_kv_heads) > BLOCK_ROWS) return cudaErrorInvalidValue;
+  return run(cache, args, H, block_len, make_plan(cache, args, true), (char*)workspace, s);
 }
 
 extern "C" size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attention_args* args) {

@@ -108,5 +108,6 @@ constexpr int F32_KEYS = 64;
 cudaError_t launch_f32(const AttnP& p, int rpt, cudaStream_t s);
 struct F32Rows { int ctas, keys; bool join; };   // CTAs per (request, KV head), positions each, joined by a cluster
 F32Rows f32_rows_plan(long long units, int max_kv, bool mass);
+F32Rows f32_block_plan(int max_kv);                // a context's block: by max_kv (at most 8,192) alone
 cudaError_t launch_f32_rows(const AttnP& p, const F32Rows& f, cudaStream_t s);
 cudaError_t launch_f32_mass(const AttnP& p, int rpt, cudaStream_t s);

@@ -159,8 +159,10 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
     *reinterpret_cast<float4*>(sq + row * PITCH + 4 * d) = v;
   }
   __syncthreads();
-  // warps take row groups in turn and, within one, every KW-th step of four keys
-  const int RG = (R + NR - 1) / NR, KW = RG >= RW ? 1 : RW / RG, kw = warp / RG;
+  // warps take row groups in turn and, within one, every KW-th step of four
+  // keys; two warps for a group of a context's block, whose rows have to come
+  // out the same bits in a block of any height
+  const int RG = (R + NR - 1) / NR, KW = p.pad_H ? 2 : RG >= RW ? 1 : RW / RG, kw = warp / RG;
   // a cluster shares what the request has (64 requests x 6 heads x 16 rows
   // over 512-2048 positions with weights: 246 us with fixed ranges, 193 so);
   // split CTAs take fixed ranges and leave at once where there is nothing
@@ -586,7 +588,8 @@ static cudaError_t run_rows(const AttnP& p, int cs, int keys, cudaStream_t s) {
 
 cudaError_t launch_f32_rows(const AttnP& p, const F32Rows& f, cudaStream_t s) {
   // one or two rows: 8 requests x 6 heads x 448 positions 20 us, 24 with groups of eight rows
-  const bool one = (long long)p.a.max_q * p.G <= 2, mass = p.a.mass != nullptr;
+  // (a context's block keeps the larger groups: their sums run in another order)
+  const bool one = (long long)p.a.max_q * p.G <= 2 && !p.pad_H, mass = p.a.mass != nullptr;
   if (!f.join) return one ? run_rows<2, false, false>(p, f.ctas, f.keys, s) : run_rows<8, false, false>(p, f.ctas, f.keys, s);
   if (mass) return one ? run_rows<2, true, true>(p, f.ctas, f.keys, s) : run_rows<8, true, true>(p, f.ctas, f.keys, s);
   return one ? run_rows<2, false, true>(p, f.ctas, f.keys, s) : run_rows<8, false, true>(p, f.ctas, f.keys, s);
@@ -613,6 +616,15 @@ F32Rows f32_rows_plan(long long units, int max_kv, bool mass) {
   f.keys = (int)(((max_kv > 0 ? max_kv : 1) + want - 1) / want);
   f.keys = (f.keys + 3) / 4 * 4;
   f.ctas = ((max_kv > 0 ? max_kv : 1) + f.keys - 1) / f.keys;
+  return f;
+}
+
+F32Rows f32_block_plan(int max_kv) {
+  F32Rows f;
+  f.join = true;
+  const int want = std::max(1, std::min(CL_MAX, max_kv / 256));
+  f.keys = ((std::max(max_kv, 1) + want - 1) / want + 3) / 4 * 4;
+  f.ctas = (std::max(max_kv, 1) + f.keys - 1) / f.keys;
   return f;
 }
 

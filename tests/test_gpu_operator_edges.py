@@ -220,3 +220,52 @@ def test_rules_after_a_refused_batch_size(R):
         b = rules.apply(z, mask_row=state, out=torch.empty_like(z))
         torch.cuda.synchronize()
         assert a[0, 0, 3] == z[0, 0, 3] + 50.0 and torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ accumulated frame weights in the decoder
+def _rows(dec, s, req, block, one_by_one):
+    """Target logits of the block's rows: in one verify, or row by row with a forced accept after each."""
+    import speculative_whisper_asr_gb300.binding as B
+    stream = torch.cuda.current_stream().cuda_stream
+    n, H = block.shape
+    dec.reset(req)
+    b = dec.new_batch(req, [10 ** 6] * n)
+    out = []
+    for part in ([block[:, j: j + 1].contiguous() for j in range(H)] if one_by_one else [block]):
+        h = part.shape[1]
+        t, lg = torch.zeros(n, h, dtype=torch.int32, device="cuda"), torch.zeros(n, h, s.vocab, device="cuda")
+        bl = dev_i32([h] * n)
+        dec.verify(req, part, bl, t, lg)
+        a = b._args(B.WS_ACCEPT_FORCED, h, part, bl, t, b.block1, b.blen)
+        B.ws_accept(dec.ctx, n, req.data_ptr(), a, stream)
+        out.append(lg)
+    torch.cuda.synchronize()
+    return torch.cat(out, 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("frames", [(140, 90, 33), (1500, 700, 1), (2600, 300, 40)])
+def test_rows_do_not_depend_on_the_call(R, dtype, accumulate, frames):
+    """A row's logits are the same bits in a block and alone, with other requests and without, also while the frames'
+    weights are accumulated."""
+    s, dec, req, _ = _decoder(R, dtype, 3, frames, drafter=False)
+    block = torch.as_tensor(np.random.default_rng(7).integers(0, s.vocab, (3, 9)), dtype=torch.int32, device="cuda")
+    dec.accumulate_frames(accumulate)
+    whole = _rows(dec, s, req, block, False)
+    assert torch.equal(_rows(dec, s, req, block, True), whole)
+    for i in range(3):
+        one = dec.slots([i])
+        assert torch.equal(_rows(dec, s, one, block[i: i + 1], False)[0], whole[i])
+    for H in (2, 8):
+        assert torch.equal(_rows(dec, s, req, block[:, :H].contiguous(), False), whole[:, :H])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_speculative_equals_autoregressive_while_accumulating(R, dtype):
+    s, dec, req, _ = _decoder(R, dtype, 2, (1400, 900), max_pos=448)
+    dec.accumulate_frames(True)
+    a, b = dec.new_batch(req, [150, 150]), dec.new_batch(req, [150, 150])
+    R.run_ar(dec, a)
+    R.run_spec(dec, b)
+    assert a.transcripts() == b.transcripts()
