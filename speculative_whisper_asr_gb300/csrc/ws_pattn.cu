@@ -1,5 +1,7 @@
 // Attention of a chunk of new tokens over a paged cache
 // (ws_paged_attention in include/ws.h gives the formulas).
+#include <type_traits>
+
 #include "ws_attn_mma.cuh"
 #include "ws_pattn.cuh"
 
@@ -381,41 +383,54 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) nl[nt][e] = r0 + 8 * nt + 2 * c + e < R ? row_lse[8 * nt + 2 * c + e] : INFINITY;
+    // a row whose log-sum-exp is NaN adds NaN where it sees, and nothing elsewhere
+    bool nan = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) nan |= nl[nt][0] != nl[nt][0] || nl[nt][1] != nl[nt][1];
+    nan = __any_sync(ALL, nan);
     float* mass = p.a.mass + ((size_t)r.slot * p.c.n_kv_heads + h) * p.a.mass_stride;
     // a quad ends up with the sums of four keys per step of 32; its lane c
     // adds key 8 c + g.  The position is this thread's alone, so the atomic
     // (which does not wait for the old value) has nothing to race with.
     w.start(p.geo, tb + warp, SP_W);
     constexpr int U = NT == 4 ? 1 : 2;      // tiles at once: one's latencies under the other's
-    for (int it = 0; it < n_my; it += U) {
-      float sv[U][MT][NT][4];
+    auto add_weights = [&](auto nan_row) {
+      constexpr bool NAN_ROW = decltype(nan_row)::value;
+      for (int it = 0; it < n_my; it += U) {
+        float sv[U][MT][NT][4];
 #pragma unroll
-      for (int k = 0; k < U; ++k) tm_ld<8 * NT>(tmem + (uint32_t)(min(it + k, n_my - 1) * 8 * NT), &sv[k][0][0][0]);
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-      float part[U][4];
+        for (int k = 0; k < U; ++k) tm_ld<8 * NT>(tmem + (uint32_t)(min(it + k, n_my - 1) * 8 * NT), &sv[k][0][0][0]);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        float part[U][4];
 #pragma unroll
-      for (int k = 0; k < U; ++k)
+        for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {       // keys 8 q + g
-          float s = 0.f;
+          for (int q = 0; q < 4; ++q) {       // keys 8 q + g
+            float s = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) s += ex2(fmaf(sv[k][q >> 1][nt][2 * (q & 1) + e], sl, -nl[nt][e]));
-          part[k][q] = s;
+              for (int e = 0; e < 2; ++e) {
+                const float x = sv[k][q >> 1][nt][2 * (q & 1) + e], y = ex2(fmaf(x, sl, -nl[nt][e]));
+                s += NAN_ROW && x == -INFINITY ? 0.f : y;
+              }
+            part[k][q] = s;
+          }
+        // a quad's four lanes hold parts of four keys: two exchanges leave each
+        // lane with the whole sum of one
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float a0 = (c & 2 ? part[k][2] : part[k][0]) + __shfl_xor_sync(0xffffffffu, c & 2 ? part[k][0] : part[k][2], 2);
+          const float a1 = (c & 2 ? part[k][3] : part[k][1]) + __shfl_xor_sync(0xffffffffu, c & 2 ? part[k][1] : part[k][3], 2);
+          const float sum = (c & 1 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);
+          const int j = 8 * c + g, pos = w.base(p.geo, p.c.page_size, SP_TK) + j;
+          if (it + k < n_my && j < w.room(p.geo, p.c.page_size, SP_TK) && pos < Lmax) atomicAdd(mass + pos, sum);
+          w.next(p.geo);
         }
-      // a quad's four lanes hold parts of four keys: two exchanges leave each
-      // lane with the whole sum of one
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const float a0 = (c & 2 ? part[k][2] : part[k][0]) + __shfl_xor_sync(0xffffffffu, c & 2 ? part[k][0] : part[k][2], 2);
-        const float a1 = (c & 2 ? part[k][3] : part[k][1]) + __shfl_xor_sync(0xffffffffu, c & 2 ? part[k][1] : part[k][3], 2);
-        const float sum = (c & 1 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);
-        const int j = 8 * c + g, pos = w.base(p.geo, p.c.page_size, SP_TK) + j;
-        if (it + k < n_my && j < w.room(p.geo, p.c.page_size, SP_TK) && pos < Lmax) atomicAdd(mass + pos, sum);
-        w.next(p.geo);
       }
-    }
+    };
+    if (nan) add_weights(std::true_type());
+    else add_weights(std::false_type());
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();

@@ -383,7 +383,10 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
       const int pos = kb + x;
       if (paged_page(p.c, p.c.page_table, p.c.table_stride, r.slot, pos) < 0) continue;
       float w = 0.f;
-      for (int row = 0; row < R; ++row) w += ex2(fmaf(stash[row * pitch + x], p.sl, -row_lse[row]));
+      for (int row = 0; row < R; ++row) {           // a NaN log-sum-exp adds NaN where its row sees, and nothing elsewhere
+        const float y = stash[row * pitch + x];
+        if (y != -INFINITY) w += ex2(fmaf(y, p.sl, -row_lse[row]));
+      }
       atomicAdd(mass + pos, w);                     // this thread's position alone
     }
   }

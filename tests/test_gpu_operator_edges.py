@@ -269,3 +269,34 @@ def test_speculative_equals_autoregressive_while_accumulating(R, dtype):
     R.run_ar(dec, a)
     R.run_spec(dec, b)
     assert a.transcripts() == b.transcripts()
+
+
+# ------------------------------------------------------------------ NaN beside sound values
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("c,lens", [(1, (300, 130)), (6, (300, 130)), (16, (70, 33)), (30, (300, 130)), (90, (300, 130)),
+                                    (9, (2500, 64)), (5, (5000, 64))])
+def test_a_nan_row_adds_its_weights_only_where_it_sees(R, dtype, c, lens):
+    """The NaN of one query row reaches the masses of the positions that row sees, of its KV head and request, and no
+    other position."""
+    x = AttnCase([c, c], lens, dtype=dtype, hq=4, hkv=2, page=16, seed=c)
+    t = c // 2
+    sound = AttnCase([c, c], lens, dtype=dtype, hq=4, hkv=2, page=16, seed=c)
+    x.table[0, 1] = -1                                        # positions 16..31 of the first cache have no page
+    sound.table[0, 1] = -1
+    tol = sound.reference(bad_pages=(1,))[1][2]               # of request 0 alone: the other has its second page
+    clean = _attend(R, sound)[2]
+    x.q[t, 2, 5] = math.nan                                   # row t of request 0, KV head 1
+    mass = _attend(R, x)[2]
+    L = lens[0]
+    sees = torch.zeros(mass.shape, dtype=torch.bool, device="cuda")
+    sees[0, 1, : L - c + t + 1] = True
+    sees[0, 1, 16:32] = False
+    assert bool(mass[sees].isnan().all())
+    assert not bool(mass[~sees].isnan().any())
+    assert torch.equal(mass[0, :, 16:32], x.mass0[0, :, 16:32])
+    other = torch.ones_like(sees)
+    other[0, 1] = False
+    assert torch.equal(mass[other], clean[other])             # other heads and requests: untouched
+    behind = ~sees
+    behind &= ~other
+    close("positions that the row does not see", mass[behind], clean[behind].double().cpu(), 2 * tol[behind.cpu()])
