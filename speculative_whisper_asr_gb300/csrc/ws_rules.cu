@@ -171,14 +171,17 @@ __global__ void __launch_bounds__(NT, 2) rules_kernel(const ws_rules_args a, con
       sum *= top > m ? exp_of(m - top) : 1.f;
       m = top;
     }
-    if (fabsf(m) < 1e37f) {                // the scaled reference stays finite
-      const float ref = m * LOG2E;
+    // The difference comes first: scaled to log2 units beforehand, the
+    // reference's rounding would stand in every term, the largest included
+    // (4e-5 of the log probability at logits near 1000), and the largest term
+    // has to be 1.
+    if (fabsf(m) < 1e37f) {
       if (count == 1) {
-        sum += ex2(fmaf(y[0], LOG2E, -ref));
+        sum += exp_of(y[0] - m);
       } else {
         float2 s2 = make_float2(0.f, 0.f);
         for (int k = 0; k + 1 < count; k += 2) {
-          float2 e = __ffma2_rn(make_float2(y[k], y[k + 1]), make_float2(LOG2E, LOG2E), make_float2(-ref, -ref));
+          float2 e = __fmul2_rn(__fadd2_rn(make_float2(y[k], y[k + 1]), make_float2(-m, -m)), make_float2(LOG2E, LOG2E));
           e.x = ex2(e.x);
           e.y = ex2(e.y);
           s2 = __fadd2_rn(s2, e);

@@ -300,3 +300,29 @@ def test_a_nan_row_adds_its_weights_only_where_it_sees(R, dtype, c, lens):
     behind = ~sees
     behind &= ~other
     close("positions that the row does not see", mass[behind], clean[behind].double().cpu(), 2 * tol[behind.cpu()])
+
+
+# ------------------------------------------------------------------ log probabilities of large logits
+@pytest.mark.parametrize("size", [30.0, 100.0, 1e3, 1e4, 1e6, -1e3, -1e4])
+@pytest.mark.parametrize("n,V", [(2, 1000), (3, 51866), (200, 5001)])
+def test_log_probabilities_far_from_zero(R, size, n, V):
+    """Every logit shifted: the log probability of the largest does not lose what the shift's size rounds away."""
+    g = np.random.default_rng(int(abs(size)) + V)
+    z = (g.standard_normal((n, 1, V)) + size).astype(np.float32)
+    forced = g.integers(0, V, n)
+    bias = np.where(np.arange(n) % 2 == 0, 3.0, abs(size)).astype(np.float32)      # odd rows: a certain token
+    rules = R.LogitsRules(bias_ids=dev_i32(forced[:, None]), bias_vals=torch.as_tensor(bias[:, None]).cuda(),
+                          bias_len=dev_i32(np.ones(n)))
+    lp, out = torch.zeros(n, 1, device="cuda"), torch.empty(n, 1, V, device="cuda")
+    rules.apply(torch.as_tensor(z).cuda(), out=out, target=torch.zeros(n, 1, dtype=torch.int32, device="cuda"), logprob=lp)
+    torch.cuda.synchronize()
+    y = out[:, 0].double().cpu()
+    want = y.max(1).values - torch.logsumexp(y, 1)
+    got = lp[:, 0].double().cpu()
+    assert bool((got <= 0).all())
+    # differences of logits are exact to half a step, their product with log2(e) to two, an exponential to 2^-20; a
+    # thread's sum has at most V / 512 terms and the joins 16 more
+    d = (y.max(1).values[:, None] - y).clamp(max=100.0)
+    w = torch.softmax(y, 1)
+    tol = (w * d).sum(1) * 4 * E32 + 2.0 ** -20 + (V // 512 + 32) * E32 + want.abs() * 4 * E32
+    assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol).max())
