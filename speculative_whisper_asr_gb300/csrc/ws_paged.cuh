@@ -42,9 +42,11 @@ inline int paged_fail(int code, const std::string& msg) {
   return code;
 }
 
-// Launch of a kernel that begins with pdl_wait(): on created streams it may
-// start while the kernel before it (which calls pdl_trigger()) still runs, as
-// elsewhere in the library.
+// Launch of a kernel whose every thread calls pdl_wait() before it returns: on
+// created streams it may start while the kernel before it (which calls
+// pdl_trigger()) still runs, as elsewhere in the library.  If all its CTAs left
+// without the wait, its end, which the next node of a graph depends on, could
+// come before the end of the kernel before it.
 template <class... P, class... A>
 inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t c = {};

@@ -496,7 +496,10 @@ __global__ void __launch_bounds__(128) mass_kernel(const AttnP p) {
   const int h = blockIdx.y, i = blockIdx.z;
   const Req r = request(p, i);
   const int k0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 32;
-  if (k0 >= r.L || r.c == 0) return;
+  if (k0 >= r.L || r.c == 0) {             // waits all the same: this grid's end has to follow the rows' kernels'
+    pdl_wait();
+    return;
+  }
   uint32_t ka[2][2][8];                    // [16-key step][key g or g + 8][2 * step of 16 dims + half]
   uint32_t valid = 0;
 #pragma unroll

@@ -515,7 +515,10 @@ __global__ void __launch_bounds__(NT, 2) f32_mass_kernel(const AttnP p) {
   constexpr int TQ = 16 * RPT;
   const int h = blockIdx.y, i = blockIdx.z, j0 = blockIdx.x * TK;
   const Req r = request(p, i);
-  if (j0 >= r.L || r.c == 0) return;
+  if (j0 >= r.L || r.c == 0) {                     // waits all the same: this grid's end has to follow the rows' kernels'
+    pdl_wait();
+    return;
+  }
   float *sq = fsm, *sk = sq + TQ * PITCH;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, R = r.c * p.G;
   const bool valid = load_keys(p, r, h, j0, r.L, sk, nullptr);

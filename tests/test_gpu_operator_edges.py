@@ -326,3 +326,31 @@ def test_log_probabilities_far_from_zero(R, size, n, V):
     w = torch.softmax(y, 1)
     tol = (w * d).sum(1) * 4 * E32 + 2.0 ** -20 + (V // 512 + 32) * E32 + want.abs() * 4 * E32
     assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol).max())
+
+
+# ------------------------------------------------------------------ calls with nothing to see
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("chunks,lens", [([1], [4000]), ([1, 1], [9000, 9000]), ([9, 9], [3000, 3000]), ([50, 20], [700, 513])])
+def test_empty_caches_then_the_next_kernel(R, dtype, chunks, lens):
+    """Every cache empty: the rows are zero for whatever is enqueued next, in a captured graph too, and no mass moves."""
+    x = AttnCase(chunks, lens, dtype=dtype, hq=4, hkv=2, seed=3)
+    x.kv_len.zero_()
+    cache = R.PagedCache(x.k, x.v, x.table)
+    out, seen, mass = torch.empty_like(x.q), torch.empty_like(x.q), x.mass0.clone()
+    lse = torch.empty(x.q.shape[:2], device="cuda")
+
+    def calls():
+        out.fill_(7.0)
+        cache.attend(x.q, x.kv_len, x.cu, max_q=x.max_q, max_kv=x.max_kv, out=out, lse=lse, mass=mass)
+        seen.copy_(out)
+        out.fill_(9.0)
+
+    calls()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for _ in range(50):
+        g.replay()
+    torch.cuda.synchronize()
+    assert bool((seen[: x.rows] == 0).all()) and bool((seen[x.rows:] == 7.0).all()) and bool((out == 9.0).all())
+    assert bool((lse[: x.rows] == -math.inf).all()) and torch.equal(mass, x.mass0)
