@@ -478,7 +478,8 @@ typedef struct {
   float scale;                 /* multiplies q . k (1/8 for the usual 1/sqrt(64)); finite */
   const void* q;               /* row r, head u at r * q_stride + u * 64 elements; 16-byte aligned rows */
   int64_t q_stride;
-  void* out;                   /* row r, head u at r * out_stride + u * 64; 16-byte aligned rows */
+  void* out;                   /* row r, head u at r * out_stride + u * 64; 16-byte aligned rows; shares none with q
+                                  (beside q in rows of the same stride is fine) */
   int64_t out_stride;
   float* lse;                  /* [total_q, n_heads] out: log sum exp of the row's scores, or NULL */
   float* mass;                 /* [n_slots, n_kv_heads, mass_stride] in/out, or NULL */

@@ -786,6 +786,11 @@ extern "C" int ws_paged_attention(const ws_paged_cache* cache, const ws_attentio
   if (q.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return paged_fail(WS_EINVAL, "workspace must be 16-byte aligned and not null");
   if (q.bytes > workspace_bytes) return paged_fail(WS_ENOSPACE, "workspace smaller than ws_paged_attention_workspace()");
+  // key splits, row tiles and the weight passes read q after the first rows are stored
+  const int64_t es = cache->dtype == WS_BF16 ? 2 : 4;
+  if (rows_overlap(args->q, args->q_stride * es, args->out, args->out_stride * es, args->total_q,
+                   (int64_t)args->n_heads * WS_DH * es))
+    return paged_fail(WS_EINVAL, "out must not share elements with q");
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
   const cudaError_t e = run(*cache, *args, 0, nullptr, q, (char*)workspace, (cudaStream_t)stream);

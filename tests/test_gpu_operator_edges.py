@@ -354,3 +354,32 @@ def test_empty_caches_then_the_next_kernel(R, dtype, chunks, lens):
     torch.cuda.synchronize()
     assert bool((seen[: x.rows] == 0).all()) and bool((seen[x.rows:] == 7.0).all()) and bool((out == 9.0).all())
     assert bool((lse[: x.rows] == -math.inf).all()) and torch.equal(mass, x.mass0)
+
+
+# ------------------------------------------------------------------ outputs beside and over inputs
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("c", [3, 30, 100])
+def test_out_beside_q_in_the_same_rows(R, dtype, c):
+    """q and out as columns of one buffer; out over q is refused."""
+    x = AttnCase([c], [140], hq=4, hkv=4, dtype=dtype, seed=9)
+    wide = torch.zeros(c, 12, 64, device="cuda", dtype=dtype)
+    wide[:, 4:8] = x.q[:c]
+    want, tol = x.reference()
+    cache = R.PagedCache(x.k, x.v, x.table)
+    args = dict(kv_len=x.kv_len, cu_q=x.cu, max_q=c, max_kv=140)
+    cache.attend(wide[:, 4:8], out=wide[:, 8:12], **args)
+    torch.cuda.synchronize()
+    close("out", wide[:, 8:12], want[0], tol[0])
+    assert torch.equal(wide[:, 4:8], x.q[:c])
+    for out in (wide[:, 4:8], wide[:, 5:9], wide[:, 2:6]):
+        with pytest.raises(R.B.WSError) as e:
+            cache.attend(wide[:, 4:8], out=out, **args)
+        assert e.value.code == R.B.WS_EINVAL
+    both = torch.zeros(2 * c + 2, 4, 64, device="cuda", dtype=dtype)       # q directly before and behind out
+    for at in (0, c):
+        both[at: at + c] = x.q[:c]
+        cache.attend(both[at: at + c], out=both[c - at: 2 * c - at], **args)
+        torch.cuda.synchronize()
+        close("out", both[c - at: 2 * c - at], want[0], tol[0])
+    with pytest.raises(R.B.WSError):
+        cache.attend(both[:c], out=both[c - 1: 2 * c - 1], **args)

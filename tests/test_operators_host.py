@@ -133,3 +133,20 @@ def test_empty_calls_do_nothing(B):
     B.ws_cache_evict(_cache(B), _evict(B, n_req=0), 0, 0, 0)
     B.ws_logits_rules(_rules(B, n=0), 0)
     B.ws_logits_rules(_rules(B, H=0), 0)
+
+
+@pytest.mark.parametrize("q,qs,out,os_", [
+    (4096, 512, 4096, 512),                              # in place
+    (4096, 512, 4096 + 512, 512),                        # half a row behind
+    (4096 + 1024 * 7, 512, 4096, 512),                   # out ends in q's first row
+    (4096, 1024, 4096 + 1024 + 16, 1024),                # interleaved rows of one buffer that reach into the next
+    (4096, 1024, 4096 + 1024 - 16, 1024),
+    (4096 + 2048 * 3 + 16, 1024, 4096 + 1024, 1024),
+    (4096 + 4096, 1024, 4096, 512),                      # other strides, ranges that meet
+])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_out_over_q_refused(B, q, qs, out, os_, dtype):
+    """8 rows of 8 heads (1,024 bytes in bf16; strides in elements) that share elements with q."""
+    f = 2 if dtype == B.WS_F32 else 1                    # fp32: the same picture with every distance doubled
+    a = _attn(B, q=q * f, q_stride=qs, out=out * f, out_stride=os_)
+    _refused(B, lambda: B.ws_paged_attention(_cache(B, dtype=dtype), a, 4096, 1 << 40, 0), B.WS_EINVAL)
