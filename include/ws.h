@@ -555,7 +555,7 @@ typedef struct {
   int32_t n, H, vocab;         /* requests, block rows per request, vocabulary (1..262144) */
   const float* logits;         /* row (i, j) at (i * H + j) * ld */
   int64_t ld;                  /* >= vocab */
-  float* out;                  /* row (i, j) at (i * H + j) * ld_out; may be logits with ld_out = ld */
+  float* out;                  /* row (i, j) at (i * H + j) * ld_out; logits with ld_out = ld, or disjoint from them */
   int64_t ld_out;
   const int32_t* block_len;    /* [n] rows in use, or NULL (= H) */
   const int32_t* history;      /* [n, hist_stride] tokens so far, the block's anchor included, or NULL (none) */

@@ -460,6 +460,16 @@ struct AcceptParams {
   unsigned long long parent4;  // tree: parent row of row j in bits 4j .. 4j + 3
   int32_t* tpath;              // tree: per request [L before, a, path rows 0..a] (WS_TREE_REC ints)
 };
+// Whether two arrays of `rows` rows of `width` bytes share a byte.  Rows of one
+// stride may lie beside each other in the same buffer; of two strides only
+// whole ranges are told apart.
+inline bool rows_overlap(const void* a, int64_t stride_a, const void* b, int64_t stride_b, int64_t rows, int64_t width) {
+  const char *x = (const char*)a, *y = (const char*)b;
+  if (x >= y + (rows - 1) * stride_b + width || y >= x + (rows - 1) * stride_a + width) return false;
+  if (stride_a != stride_b || rows == 1) return true;
+  const int64_t d = (x < y ? y - x : x - y) % stride_a;    // from a row of one to the next row of the other
+  return d < width || d > stride_a - width;
+}
 // Operators on a described cache (ws_pattn.cu, ws_evict.cu) for the context's
 // own: attention of the rows [n * H] of a block (block_len[i] of them in use;
 // cu_q is not read), and eviction.  Arguments are not checked again.

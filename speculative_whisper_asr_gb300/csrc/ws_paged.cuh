@@ -32,17 +32,6 @@ inline const char* check_paged_cache(const ws_paged_cache* c) {
   return nullptr;
 }
 
-// Whether two arrays of `rows` rows of `width` bytes share a byte.  Rows of one
-// stride may lie beside each other in the same buffer; of two strides only
-// whole ranges are told apart.
-inline bool rows_overlap(const void* a, int64_t stride_a, const void* b, int64_t stride_b, int64_t rows, int64_t width) {
-  const char *x = (const char*)a, *y = (const char*)b;
-  if (x >= y + (rows - 1) * stride_b + width || y >= x + (rows - 1) * stride_a + width) return false;
-  if (stride_a != stride_b || rows == 1) return true;
-  const int64_t d = (x < y ? y - x : x - y) % stride_a;    // from a row of one to the next row of the other
-  return d < width || d > stride_a - width;
-}
-
 inline int paged_fail(int code, const std::string& msg) {
   ws_set_thread_error(msg.c_str());
   return code;

@@ -337,6 +337,8 @@ extern "C" int ws_logits_rules(const ws_rules_args* p, ws_stream stream) {
   if (a.window > 0) tokens = min(tokens, (long long)a.window);
   const long long most = tokens + (a.bias_ids ? a.bias_stride : 0);
   if (most > 4096) return fail(WS_EUNSUPPORTED, "more than 4096 tokens and biases per row (window limits the tokens)");
+  if (a.logits != a.out && rows_overlap(a.logits, a.ld * 4, a.out, a.ld_out * 4, (long long)a.n * a.H, (int64_t)a.vocab * 4))
+    return fail(WS_EINVAL, "out must be logits or share no elements with them");
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return fail(WS_ECUDA, (std::string("a CUDA error was pending before this call: ") +
                            cudaGetErrorString(prior)).c_str());

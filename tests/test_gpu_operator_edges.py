@@ -383,3 +383,15 @@ def test_out_beside_q_in_the_same_rows(R, dtype, c):
         close("out", both[c - at: 2 * c - at], want[0], tol[0])
     with pytest.raises(R.B.WSError):
         cache.attend(both[:c], out=both[c - 1: 2 * c - 1], **args)
+
+
+def test_rules_out_beside_logits(R):
+    """New logits in the other half of the rows' buffer."""
+    both = torch.randn(2, 3, 2000, device="cuda")
+    z, out = both[:, :, :1000], both[:, :, 1000:]
+    want = z.clone()
+    R.LogitsRules().apply(z, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(z, want)
+    with pytest.raises(R.B.WSError):
+        R.LogitsRules().apply(z, out=both[:, :, 999:1999])

@@ -150,3 +150,10 @@ def test_out_over_q_refused(B, q, qs, out, os_, dtype):
     f = 2 if dtype == B.WS_F32 else 1                    # fp32: the same picture with every distance doubled
     a = _attn(B, q=q * f, q_stride=qs, out=out * f, out_stride=os_)
     _refused(B, lambda: B.ws_paged_attention(_cache(B, dtype=dtype), a, 4096, 1 << 40, 0), B.WS_EINVAL)
+
+
+@pytest.mark.parametrize("ld,out,ld_out", [(1000, 4096 + 4, 1000), (1000, 4096 + 4000, 1000), (1000, 4096 + 4000 * 6 - 4, 1000),
+                                           (2000, 4096 + 4000 - 4, 2000), (2000, 4096 + 4000 + 4, 2000), (2000, 4096 + 4000, 1000)])
+def test_rules_out_partly_over_logits_refused(B, ld, out, ld_out):
+    """6 rows of 1,000 logits (4,000 bytes)."""
+    _refused(B, lambda: B.ws_logits_rules(_rules(B, ld=ld, out=out, ld_out=ld_out), 0), B.WS_EINVAL)
