@@ -196,6 +196,53 @@ bool flow_shape_ok(const ws_model_desc& d) {
          d.max_pos <= 576;
 }
 
+// --------------------------------------------------------------------------- acoustic caches as described caches
+// A target layer's acoustic keys and values: one page of max_frames frames per
+// slot.
+ws_paged_cache frame_cache_shape(const ws_model_desc& d) {
+  ws_paged_cache x = {};
+  x.dtype = d.dtype;
+  x.n_kv_heads = d.n_heads;
+  x.page_size = d.max_frames;
+  x.n_pages = x.n_slots = d.max_batch;
+  x.head_stride = (int64_t)d.max_frames * WS_DH;
+  x.token_stride = WS_DH;
+  x.table_stride = 1;
+  return x;
+}
+// Cross-attention of n blocks of H rows that adds the rows' weights to `mass`.
+// The keys are cut by max_frames, not by what the requests happen to hold.
+ws_attention_args frame_attention(const ws_model_desc& d, int n, int H, float* mass) {
+  ws_attention_args a = {};
+  a.n_req = n;
+  a.total_q = n * H;
+  a.max_q = H;
+  a.max_kv = d.max_frames;
+  a.n_heads = d.n_heads;
+  a.scale = 0.125f;                        // 1/sqrt(64)
+  a.q_stride = a.out_stride = d.d_model;
+  a.mass = mass;
+  a.mass_stride = d.max_frames;
+  return a;
+}
+ws_evict_args frame_eviction(const ws_model_desc& d, int n, int max_kv, int keep) {
+  ws_evict_args a = {};
+  a.n_req = n;
+  a.max_kv = max_kv;
+  a.keep = keep;
+  a.mass_stride = d.max_frames;
+  return a;
+}
+// Scratch that any of these calls takes at most.
+size_t frame_scratch(const ws_model_desc& d) {
+  const ws_paged_cache x = frame_cache_shape(d);
+  float some = 0.f;                        // any buffer: sizes alone count
+  size_t most = cache_evict_workspace(x, frame_eviction(d, d.max_batch, d.max_frames, d.max_frames));
+  for (int H = 1; H <= d.max_block; ++H)
+    most = std::max(most, block_attention_workspace(x, frame_attention(d, d.max_batch, H, &some)));
+  return most;
+}
+
 Plan make_plan(const ws_model_desc& d) {
   Plan p;
   Layout lay;
@@ -227,8 +274,7 @@ Plan make_plan(const ws_model_desc& d) {
   const int nh = d.drafter_layers > 0 ? d.n_hist : 0;
   p.hist = lay.take((size_t)d.max_batch * d.max_block * nh * D * 4);
   p.amax = lay.take(M * 8);
-  // the attention that accumulates frame weights also keeps log-sum-exps, in padded regions
-  p.part = lay.take(M * d.n_heads * (p.max_split * (WS_DH + 2) + 1) * 4 + 1024);
+  p.part = lay.take(std::max(M * d.n_heads * p.max_split * (WS_DH + 2) * 4, frame_scratch(d)));
   p.acnt = lay.take((size_t)d.max_batch * d.n_heads * 4);
   p.feat = lay.take(M * nh * D * es);
   p.hpre = lay.take(M * D * 4);
@@ -465,23 +511,14 @@ int flow_verify(ws_ctx* c, const int32_t* req, int H, const int32_t* block, cons
   return WS_OK;
 }
 
-// --------------------------------------------------------------------------- acoustic caches as described caches
-// A target layer's acoustic keys and values: one page of max_frames frames per
-// slot.  The self cache's page table holds 0, 1, 2, ..., so its first
-// max_batch entries map every slot to its page.
+// The self cache's page table holds 0, 1, 2, ..., so its first max_batch
+// entries map every slot to its page.
 ws_paged_cache frame_cache(const ws_ctx* c, int layer) {
-  ws_paged_cache x = {};
-  x.dtype = c->d.dtype;
-  x.n_kv_heads = c->heads;
-  x.page_size = c->d.max_frames;
-  x.n_pages = x.n_slots = c->d.max_batch;
+  ws_paged_cache x = frame_cache_shape(c->d);
   x.k = (char*)c->xkv + (size_t)layer * c->x_layer_elems * c->es;
   x.v = (char*)x.k + (size_t)c->heads * c->d.max_frames * WS_DH * c->es;
   x.page_stride = (int64_t)c->x_slot_elems;
-  x.head_stride = (int64_t)c->d.max_frames * WS_DH;
-  x.token_stride = WS_DH;
   x.page_table = c->ptab;
-  x.table_stride = 1;
   return x;
 }
 
@@ -489,20 +526,12 @@ ws_paged_cache frame_cache(const ws_ctx* c, int layer) {
 // caller's frame masses.
 cudaError_t cross_attn_with_mass(ws_ctx* c, int n, int H, const int32_t* req, const int32_t* blen, int layer,
                                  cudaStream_t s) {
-  ws_attention_args a = {};
-  a.n_req = n;
+  ws_attention_args a =
+      frame_attention(c->d, n, H, c->frame_mass + (size_t)layer * c->d.max_batch * c->heads * c->d.max_frames);
   a.req_ids = req;
   a.kv_len = c->Fv;
-  a.total_q = n * H;
-  a.max_q = H;
-  a.max_kv = c->d.max_frames;              // not what the requests happen to hold: it cuts the keys into parts
-  a.n_heads = c->heads;
-  a.scale = 0.125f;                        // 1/sqrt(64)
   a.q = c->q;
-  a.q_stride = a.out_stride = c->d.d_model;
   a.out = c->ao;
-  a.mass_stride = c->d.max_frames;
-  a.mass = c->frame_mass + (size_t)layer * c->d.max_batch * c->heads * c->d.max_frames;
   return launch_block_attention(frame_cache(c, layer), a, H, blen, c->part, s);
 }
 
@@ -1005,13 +1034,9 @@ int ws_evict_frames(ws_ctx* c, int n, const int32_t* req, const float* mass, int
     return fail(c, WS_EUNSUPPORTED, "the readout layer's keys are read by frame: switch the readout off first");
   if (c->max_fc < 1) return fail(c, WS_EINVAL, "no acoustic keys yet (ws_cross_kv)");
   if (keep >= c->max_fc) return WS_OK;     // every request already fits
-  ws_evict_args a = {};
-  a.n_req = n;
+  ws_evict_args a = frame_eviction(c->d, n, c->max_fc, keep);
   a.req_ids = req;
   a.kv_len = c->Fv;
-  a.max_kv = c->max_fc;
-  a.keep = keep;
-  a.mass_stride = c->d.max_frames;
   c->evicted = true;
   for (int l = 0; l < c->d.n_layers; ++l) {
     a.kv_len_out = l + 1 < c->d.n_layers ? c->Fcut : c->Fv;        // every layer starts from the same count

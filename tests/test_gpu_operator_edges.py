@@ -395,3 +395,32 @@ def test_rules_out_beside_logits(R):
     assert torch.equal(out, want) and torch.equal(z, want)
     with pytest.raises(R.B.WSError):
         R.LogitsRules().apply(z, out=both[:, :, 999:1999])
+
+
+# ------------------------------------------------------------------ a context's scratch
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,frames,n", [(1, 4096, 2), (1, 2100, 3), (12, 4096, 2), (15, 1, 2), (1, 64, 70)])
+def test_the_smallest_and_largest_contexts_hold_their_scratch(R, dtype, K, frames, n):
+    """Frame weights and the largest cut in contexts whose blocks are short and caches long, and the other way round."""
+    s = small_shape(dtype, n_layers=1, K=K, prompt=(990,) * min(2, K + 1), hist_layers=(0,))
+    dec = R.Decoder(s, synth.target_weights(s, 3), None, max_batch=n, max_frames=frames, max_block=K + 1)
+    req = dec.slots(list(range(n)))
+    A = synth.encoder_states(s, 3, 0, frames=frames)
+    dec.cross_kv(req, torch.cat([dec.enc_tensor(A)] * n), [frames] * n)
+    block = torch.full((n, K + 1), 5, dtype=torch.int32, device="cuda")
+    t, bl = torch.zeros_like(block), dev_i32([K + 1] * n)
+    lg = torch.zeros(n, K + 1, s.vocab, device="cuda")
+    dec.accumulate_frames(True)
+    dec.verify(req, block, bl, t, lg)
+    torch.cuda.synchronize()
+    total = dec.frame_mass().double().sum(-1)
+    assert bool((total - (K + 1)).abs().max() < (K + 1) * (2.0 ** -19 + 4096 * 2.0 ** -24))
+    assert torch.equal(lg, lg[:1].expand_as(lg))              # the same request n times
+    if frames > 1:
+        dec.evict_frames(req, frames - 1)
+    again = torch.zeros_like(lg)
+    dec.reset(req)
+    dec.verify(req, block, bl, t, again)
+    torch.cuda.synchronize()
+    assert torch.equal(again, again[:1].expand_as(lg)) and bool(torch.isfinite(again).all())
+    assert dec.status() == 0
