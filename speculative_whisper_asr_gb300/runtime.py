@@ -592,8 +592,9 @@ class PagedCache:
     k, v [pages, KV heads, page_size, 64] with any strides that are multiples
     of 16 bytes (the same for both), page_table [slots, pages per slot] int32.
     The object keeps scratch for each stream that called it; graphs captured
-    on one stream share it, so those that may replay at the same time need a
-    PagedCache each.  One thread at a time calls it."""
+    on one stream share it with each other and with calls on that stream, so
+    what may run at the same time needs a PagedCache each.  One thread at a
+    time calls it."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
         if k.dtype not in (torch.bfloat16, torch.float32) or k.dim() != 4 or k.shape[3] != 64 or not k.is_cuda:
@@ -613,20 +614,25 @@ class PagedCache:
             B.WS_BF16 if k.dtype is torch.bfloat16 else B.WS_F32, self.heads, self.page_size, self.pages, k.data_ptr(),
             v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(), self.slots, page_table.shape[1])
         self._attn, self._evict = B.AttentionArgs(), B.EvictArgs()
-        self._ws, self._kept = {}, []
-        self._need = {}                    # workspace bytes by the sizes they depend on
+        self._ws, self._kept = {}, []      # (pointer, bytes) by stream; the tensors behind them
 
-    def _workspace(self, nbytes, stream):
-        """Scratch of this stream.  Outgrown scratch is kept: work in flight or a captured graph may still use it."""
-        if nbytes == 0:
-            return 0
-        ws = self._ws.get(stream)
-        if ws is None or ws.numel() < nbytes:
-            if ws is not None:
-                self._kept.append(ws)
-                nbytes = max(nbytes, 2 * ws.numel())
-            ws = self._ws[stream] = torch.empty(nbytes, dtype=torch.uint8, device=self.k.device)
-        return ws.data_ptr()
+    def _run(self, call, size, args, stream):
+        """The call with this stream's scratch, which grows when the call finds it too small.  Outgrown scratch is kept:
+        work in flight or a captured graph may still use it."""
+        ptr, nbytes = self._ws.get(stream, (0, 0))
+        if nbytes:
+            try:
+                return call(self.desc, args, ptr, nbytes, stream)
+            except B.WSError as e:
+                if e.code != B.WS_ENOSPACE:
+                    raise
+        need = size(self.desc, args)
+        if need:
+            nbytes = max(need, 2 * nbytes)
+            self._kept.append(torch.empty(nbytes, dtype=torch.uint8, device=self.k.device))
+            ptr = self._kept[-1].data_ptr()
+            self._ws[stream] = ptr, nbytes
+        return call(self.desc, args, ptr, nbytes, stream)
 
     def attend(self, q, kv_len, cu_q, max_q: int, max_kv: int, causal: bool = True, scale: float = 0.125, out=None,
                lse=None, mass=None, req_ids=None):
@@ -661,15 +667,7 @@ class PagedCache:
             a.mass = 0
         else:
             a.mass, a.mass_stride = _per_position("mass", mass, _F32, self.slots, self.heads, dev)
-        s = _on(dev)
-        sizes = (n, rows, heads, max_q, max_kv, scale, lse is None, mass is None)
-        need = self._need.get(sizes, -1)
-        if need < 0:
-            need = B.ws_paged_attention_workspace(self.desc, a)
-            B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
-            self._need[sizes] = need       # of a call that was not refused
-        else:
-            B.ws_paged_attention(self.desc, a, self._workspace(need, s), need, s)
+        self._run(B.ws_paged_attention, B.ws_paged_attention_workspace, a, _on(dev))
         return out
 
     def evict(self, kv_len, mass, keep: int, max_kv: int, sink: int = 0, recent: int = 0, page_table_out=None,
@@ -697,14 +695,7 @@ class PagedCache:
         else:
             a.table_out_stride = width = page_table_out.shape[1]
             a.page_table_out = _rows("page_table_out", page_table_out, _I32, (slots, width), dev)
-        s = _on(dev)
-        need = self._need.get((n, keep), -1)
-        if need < 0:
-            need = B.ws_cache_evict_workspace(self.desc, a)
-            B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
-            self._need[n, keep] = need     # of a call that was not refused
-        else:
-            B.ws_cache_evict(self.desc, a, self._workspace(need, s), need, s)
+        self._run(B.ws_cache_evict, B.ws_cache_evict_workspace, a, _on(dev))
 
 
 class LogitsRules:

@@ -424,3 +424,26 @@ def test_the_smallest_and_largest_contexts_hold_their_scratch(R, dtype, K, frame
     torch.cuda.synchronize()
     assert torch.equal(again, again[:1].expand_as(lg)) and bool(torch.isfinite(again).all())
     assert dec.status() == 0
+
+
+# ------------------------------------------------------------------ what a cache object holds
+def test_a_growing_loop_holds_nothing_per_step(R):
+    """A decoding loop whose length grows by one: the object keeps no entry per step, and its scratch fits every call."""
+    x = AttnCase([1], [400], hq=4, hkv=2, seed=3)
+    cache = R.PagedCache(x.k, x.v, x.table)
+    mass = torch.zeros_like(x.mass0)
+
+    def held():
+        return sum(len(v) for v in vars(cache).values() if isinstance(v, (dict, list)))
+
+    sizes = []
+    for L in range(1, 400):
+        x.kv_len.fill_(L)
+        out = cache.attend(x.q[:1], x.kv_len, x.cu, max_q=1, max_kv=L, mass=mass)
+        sizes.append(held())
+    torch.cuda.synchronize()
+    assert sizes[-1] <= sizes[20] + 6                         # scratch that was outgrown, at doubling sizes
+    want, tol = x.reference()
+    x.kv_len.fill_(400)
+    out = cache.attend(x.q[:1], x.kv_len, x.cu, max_q=1, max_kv=400)
+    close("out", out, want[0], tol[0])
