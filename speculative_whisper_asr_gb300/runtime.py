@@ -427,16 +427,18 @@ def run_ar(dec: Decoder, batch: Batch, max_rounds: int = 100000, keep_frames: in
            evict_after: int = 8) -> int:
     """keep_frames: after `evict_after` rounds keep only that many acoustic frames per layer and head, those with the
     most attention so far (approximate)."""
-    _frames_round(dec, batch, 0, keep_frames, max(1, evict_after))
-    batch.prefill(ar=True)
     rounds = 0
-    while batch.poll_done() < batch.n and rounds < max_rounds:
-        if rounds:
-            _frames_round(dec, batch, rounds, keep_frames, max(1, evict_after))
-        batch.ar_step()
-        rounds += 1
-    if dec.accumulating and keep_frames is not None:
-        dec.accumulate_frames(False)
+    try:
+        _frames_round(dec, batch, 0, keep_frames, max(1, evict_after))
+        batch.prefill(ar=True)
+        while batch.poll_done() < batch.n and rounds < max_rounds:
+            if rounds:
+                _frames_round(dec, batch, rounds, keep_frames, max(1, evict_after))
+            batch.ar_step()
+            rounds += 1
+    finally:
+        if dec.accumulating and keep_frames is not None:
+            dec.accumulate_frames(False)
     return rounds
 
 
@@ -444,17 +446,19 @@ def run_spec(dec: Decoder, batch: Batch, synthetic=None, temperature=0.0, seed=0
              run_drafter=True, graph=True, k_verify=None, threshold=0.0, tree=False, keep_frames: int | None = None,
              evict_after: int = 8) -> int:
     """keep_frames, evict_after: as for run_ar."""
-    _frames_round(dec, batch, 0, keep_frames, max(1, evict_after))
-    batch.prefill(temperature=temperature, seed=seed)
     rounds = 0
-    while batch.poll_done() < batch.n and rounds < max_rounds:
-        if rounds:
-            _frames_round(dec, batch, rounds, keep_frames, max(1, evict_after))
-        batch.spec_step(rounds + 1, synthetic, temperature, seed, run_drafter, graph=graph, k_verify=k_verify,
-                        threshold=threshold, tree=tree)
-        rounds += 1
-    if dec.accumulating and keep_frames is not None:
-        dec.accumulate_frames(False)
+    try:
+        _frames_round(dec, batch, 0, keep_frames, max(1, evict_after))
+        batch.prefill(temperature=temperature, seed=seed)
+        while batch.poll_done() < batch.n and rounds < max_rounds:
+            if rounds:
+                _frames_round(dec, batch, rounds, keep_frames, max(1, evict_after))
+            batch.spec_step(rounds + 1, synthetic, temperature, seed, run_drafter, graph=graph, k_verify=k_verify,
+                            threshold=threshold, tree=tree)
+            rounds += 1
+    finally:
+        if dec.accumulating and keep_frames is not None:
+            dec.accumulate_frames(False)
     return rounds
 
 
