@@ -15,7 +15,9 @@
  *     caller allocates every buffer (workspace, weights, inputs, outputs)
  *     and keeps it alive while work that uses it is in flight.  The library
  *     never allocates device memory and never synchronises the stream
- *     (except ws_load_weights, which finishes its copies before returning).
+ *     (except ws_load_weights, which finishes its copies before returning,
+ *     the calls that return a status word, and ws_set_readout where caches
+ *     were cut).
  *   - All work is enqueued asynchronously on `stream` (a cudaStream_t; NULL
  *     is the legacy default stream).  Launch sequences are CUDA-graph
  *     capturable once the context exists.
@@ -294,7 +296,8 @@ int ws_verify_tree(ws_ctx* ctx, int n_req, const int32_t* req_ids, int H,
  *               (every frame until its first readout); 0: unrestricted
  * With a readout layer set, ws_verify keeps that layer's cross-attention
  * queries of its block rows (the kernel-per-operation path is used).
- * Host-only; no device work.  Acceptance is unchanged, so greedy output
+ * Host-only; no device work, except in a context whose caches
+ * ws_evict_frames has cut.  Acceptance is unchanged, so greedy output
  * stays equal to autoregressive greedy output. */
 int ws_set_readout(ws_ctx* ctx, int layer, int half_width);
 
@@ -334,8 +337,9 @@ int ws_set_frame_mass(ws_ctx* ctx, float* mass);
  * its full caches back.
  *   mass  laid out as for ws_set_frame_mass; it is not changed, and after
  *         the call its positions are no longer the caches'
- * A context whose caches were cut has no readout by frame: WS_EUNSUPPORTED
- * here while a readout layer is set, and from ws_set_readout afterwards. */
+ * Cut caches have no readout by frame: WS_EUNSUPPORTED here while a readout
+ * layer is set, and from ws_set_readout (which then waits for the device to
+ * see; not during a capture) while any slot's are cut. */
 int ws_evict_frames(ws_ctx* ctx, int n_req, const int32_t* req_ids, const float* mass, int keep,
                     ws_stream stream);
 

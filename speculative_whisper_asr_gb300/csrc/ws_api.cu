@@ -4,6 +4,8 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
+#include <new>
 #include <string>
 #include <algorithm>
 #include <vector>
@@ -46,7 +48,7 @@ struct ws_ctx {
   int32_t* Fcut = nullptr;      // scratch of ws_evict_frames: the frames left
   int32_t* Fd = nullptr;        // frames of the drafter's caches (Fv: the target's, fewer after ws_evict_frames)
   float* frame_mass = nullptr;  // caller's [n_layers][max_batch][heads][max_frames], or null (ws_set_frame_mass)
-  bool evicted = false;         // a slot's frames were cut: positions in the target's caches are no longer frames
+  bool evicted = false;         // frames may have been cut: where Fv < Fd, positions in the target's caches are no longer frames
   int32_t* xcenter = nullptr;   // per slot: centre frame of the drafter's cross-attention window (-1: none)
   // verification-attention readout (ws_set_readout)
   int readout_layer = -1, half_width = 0, read_H = 0;
@@ -1048,11 +1050,21 @@ int ws_evict_frames(ws_ctx* c, int n, const int32_t* req, const float* mass, int
 
 int ws_set_readout(ws_ctx* c, int layer, int half_width) {
   if (!c) return fail(nullptr, WS_EINVAL, "null context");
-  if (layer >= 0 && c->evicted)
-    return fail(c, WS_EUNSUPPORTED, "ws_evict_frames has cut acoustic caches of this context: no readout by frame");
   if (layer < -1 || layer >= c->d.n_layers) return fail(c, WS_EINVAL, "readout layer %d outside -1..n_layers-1", layer);
   if (half_width < 0) return fail(c, WS_EINVAL, "half_width must be >= 0");
   if (half_width > 0 && c->d.drafter_layers == 0) return fail(c, WS_EUNSUPPORTED, "context has no drafter");
+  if (layer >= 0 && c->evicted) {
+    // which slots are cut (fewer frames than the drafter's caches) stands on the device
+    const int mb = c->d.max_batch;
+    std::unique_ptr<int32_t[]> f(new (std::nothrow) int32_t[2 * (size_t)mb]);
+    if (!f) return fail(c, WS_EINVAL, "out of host memory");
+    CK(cudaDeviceSynchronize());
+    CK(cudaMemcpy(f.get(), c->Fv, (size_t)mb * 4, cudaMemcpyDeviceToHost));
+    CK(cudaMemcpy(f.get() + mb, c->Fd, (size_t)mb * 4, cudaMemcpyDeviceToHost));
+    for (int i = 0; i < mb; ++i)
+      if (f[i] < f[mb + i])
+        return fail(c, WS_EUNSUPPORTED, "slot %d's acoustic caches are cut (ws_evict_frames): no readout by frame", i);
+  }
   c->readout_layer = layer;
   c->half_width = half_width;
   return WS_OK;

@@ -447,3 +447,31 @@ def test_a_growing_loop_holds_nothing_per_step(R):
     x.kv_len.fill_(400)
     out = cache.attend(x.q[:1], x.kv_len, x.cu, max_q=1, max_kv=400)
     close("out", out, want[0], tol[0])
+
+
+# ------------------------------------------------------------------ readout after a cut
+def test_readout_returns_with_the_full_caches(R):
+    """While a slot's acoustic cache is cut there is no readout; once every cut slot has new acoustic keys there is."""
+    s, dec, req, A = _decoder(R, "bf16", 2, (140, 90))
+    dec.frame_mass().uniform_()
+    dec.evict_frames(req, 50)
+
+    def refused():
+        with pytest.raises(R.B.WSError) as e:
+            dec.set_readout(1, 10)
+        return e.value.code == R.B.WS_EUNSUPPORTED
+
+    assert refused()
+    dec.cross_kv(dec.slots([1]), dec.enc_tensor(A[1]), [90])
+    assert refused()                                          # slot 0 is still cut
+    dec.cross_kv(dec.slots([0]), dec.enc_tensor(A[0]), [140])
+    dec.set_readout(1, 10)
+    b = dec.new_batch(req, [20, 20])
+    R.run_spec(dec, b)
+    dec.set_readout(-1, 0)
+    plain = dec.new_batch(req, [20, 20])
+    R.run_ar(dec, plain)
+    assert b.transcripts() == plain.transcripts()
+    dec.frame_mass().uniform_()
+    dec.evict_frames(req, 139)                                # cuts slot 0 alone
+    assert refused()
