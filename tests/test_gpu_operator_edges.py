@@ -9,8 +9,8 @@ import pytest
 import torch
 
 import synth
-from gpu_common import dev_i32, small_shape
-from operator_common import E32, AttnCase, close, evict_rule
+from gpu_common import dev_i32, small_shape, teacher_forced_logits
+from operator_common import E32, AttnCase, close
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -475,3 +475,55 @@ def test_readout_returns_with_the_full_caches(R):
     dec.frame_mass().uniform_()
     dec.evict_frames(req, 139)                                # cuts slot 0 alone
     assert refused()
+
+
+# ------------------------------------------------------------------ one-request contexts
+def test_frames_in_a_one_request_context(R):
+    """A bf16 context of one slot verifies in its dataflow kernel: weights are accumulated all the same, and over cut
+    caches it gives what the kernel-per-operation path gives."""
+    s = small_shape("bf16")
+    tw = synth.target_weights(s, 3)
+    dw = synth.drafter_weights(s, 3, tw)
+    A = synth.encoder_states(s, 3, 0, frames=200)
+    decs = [R.Decoder(s, tw, dw, max_batch=mb, max_frames=200) for mb in (1, 2)]
+    got = []
+    for dec in decs:
+        req = dec.slots([0])
+        dec.cross_kv(req, dec.enc_tensor(A), [200])
+        tr = []
+        for keep in (None, 60):
+            b, c = dec.new_batch(req, [40]), dec.new_batch(req, [40])
+            R.run_spec(dec, b, keep_frames=keep, evict_after=2)
+            R.run_ar(dec, c)                                  # over the caches as they now are
+            tr += [b.transcripts(), c.transcripts()]
+            if keep is None:
+                assert tr[0] == tr[1]
+        d = dec.new_batch(req, [40])
+        R.run_spec(dec, d)
+        assert d.transcripts() == tr[3]
+        assert dec.status() == 0
+        got.append(tr)
+    assert got[0][0] == got[1][0]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("spec", [False, True])
+def test_keeping_every_frame_changes_nothing_beyond_the_tolerance(R, dtype, spec):
+    """keep_frames as large as the caches: nothing is cut; a token differs from plain decoding only where the rounds
+    that accumulated weights met logits closer than the model's tolerance."""
+    s, dec, req, _ = _decoder(R, dtype, 2, (140, 90))
+    run = R.run_spec if spec else R.run_ar
+    plain, kept = dec.new_batch(req, [30, 30]), dec.new_batch(req, [30, 30])
+    run(dec, plain)
+    run(dec, kept, keep_frames=140, evict_after=3)
+    rel = 1e-4 if dtype == "f32" else 2e-2
+    for i, (a, b) in enumerate(zip(plain.transcripts(), kept.transcripts())):
+        j = next((k for k in range(min(len(a), len(b))) if a[k] != b[k]), None)
+        if j is None:
+            assert a == b
+            continue
+        row = teacher_forced_logits(dec, dec.slots([i]), s, a[:j])[len(s.prompt) - 1 + j]
+        assert row.max() - row[b[j]] <= 2 * rel * max(1.0, np.abs(row).max())
+    again = dec.new_batch(req, [30, 30])
+    run(dec, again)
+    assert again.transcripts() == plain.transcripts()         # the caches are what they were
