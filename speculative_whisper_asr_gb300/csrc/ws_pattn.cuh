@@ -94,11 +94,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Long chunks on tcgen05 (ws_pattn_fa.cu): tiles of fa_rows(G) rows (whole
+// Long chunks on tcgen05 (ws_pattn_fa.cu): tiles of G * (128 / G) rows (whole
 // chunk rows) against tiles of FA_KEYS keys.  Rows of unsplit calls go to
 // out / lse, those of split calls to the partials.
 constexpr int FA_ROWS = 128, FA_KEYS = 128;
-inline int fa_rows(int G) { return G * (FA_ROWS / G); }                        // G <= 128
 cudaError_t launch_fa(const AttnP& p, cudaStream_t s);
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s);
 
