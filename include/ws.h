@@ -509,7 +509,8 @@ size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attent
  * the same bits.
  * A row that sees no position gets out = 0 and lse = -inf and adds no mass.
  * Rows of requests with kv_len <= 0, or with an id outside [0, n_slots), see
- * nothing.  Cached values behind kv_len are not read into any result.  Rows
+ * nothing.  Cached values behind kv_len are not read into any result, and what
+ * a row does not see does not reach it, infinite or NaN included.  Rows
  * outside every chunk and mass behind kv_len are left as they were. */
 int ws_paged_attention(const ws_paged_cache* cache, const ws_attention_args* args, void* workspace,
                        size_t workspace_bytes, ws_stream stream);

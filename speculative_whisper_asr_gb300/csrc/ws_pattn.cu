@@ -123,7 +123,10 @@ __device__ __forceinline__ void tm_ld(uint32_t addr, float* v) {
   }
 }
 
-template <int NT, bool STASH, bool HILO>
+// MIX: causal chunks of more than one row, where values that are not finite
+// are kept from the rows that do not see them (the look at the last tiles and
+// its registers cost the other calls 2%: 92 against 90 us).
+template <int NT, bool STASH, bool HILO, bool MIX>
 __global__ void __launch_bounds__(SP_W * 32, NT == 4 ? 1 : 2)
 split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   constexpr int MT = SP_TK / 16;           // key steps of 16
@@ -131,6 +134,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t full[SP_W][SP_NS];
   __shared__ SpMeta meta[SP_W][SP_NS];
+  __shared__ Odd odd[MIX ? SP_W : 1];      // each warp's own
   __shared__ float row_lse[8 * NT];
   __shared__ uint32_t s_tmem;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
@@ -208,6 +212,12 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
   }
+  const bool mixed = MIX && Lmin < Lmax;    // some row does not see all of the tile's positions
+  if (mixed) {
+    for (int x = lane; x < 3 * WS_DH; x += 32) odd[warp].first[0][x] = 0x7FFFFFFF;
+    if (lane == 0) odd[warp].any = 0;
+    __syncwarp();
+  }
   const float sl = p.sl, hold = fminf(SP_HOLD / sl, 1e30f);
   uint32_t tmem = 0;                        // this warp's columns
   if (STASH) {
@@ -232,6 +242,10 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
 #pragma unroll
         for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(Vt + lane * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next copy
+      __syncwarp();
+    }
+    if (mixed && mt_.base + SP_TK > Lmin && take_out_odd<SP_TK>(odd[warp], Vt, mt_.base, lane)) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next copy
       __syncwarp();
     }
@@ -362,6 +376,16 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       sum = fmaf(f, sml[(k * 8 * NT + row) * 2 + 1], sum);
       a0 = fmaf(f, v.x, a0); a1 = fmaf(f, v.y, a1); a2 = fmaf(f, v.z, a2); a3 = fmaf(f, v.w, a3);
     }
+    if (mixed)
+#pragma unroll
+      for (int k = 0; k < SP_W; ++k)
+        if (odd[k].any) {
+          const int limit = row_limit(p, r, rho / p.G), d = 4 * d4;
+          a0 = with_odd(odd[k], a0, limit, d);
+          a1 = with_odd(odd[k], a1, limit, d + 1);
+          a2 = with_odd(odd[k], a2, limit, d + 2);
+          a3 = with_odd(odd[k], a3, limit, d + 3);
+        }
     if (p.nsplit > 1) {
       const size_t at = (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split;
       *reinterpret_cast<float4*>(p.part_o + at * WS_DH + 4 * d4) = make_float4(a0, a1, a2, a3);
@@ -702,24 +726,32 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
   return q;
 }
 
-template <int NT, bool STASH, bool HILO = NT == 1>
+template <int NT, bool STASH, bool HILO = NT == 1, bool MIX = false>
 cudaError_t run_split(const AttnP& p, const Plan& q, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<NT, STASH, HILO>, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM);
+  cudaError_t e = cudaFuncSetAttribute(split_kernel<NT, STASH, HILO, MIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM);
   if (e != cudaSuccess) return e;
-  split_kernel<NT, STASH, HILO><<<dim3(q.row_tiles * q.nsplit, p.c.n_kv_heads, p.a.n_req), SP_W * 32, SP_SMEM, s>>>(
+  split_kernel<NT, STASH, HILO, MIX><<<dim3(q.row_tiles * q.nsplit, p.c.n_kv_heads, p.a.n_req), SP_W * 32, SP_SMEM, s>>>(
       p, reinterpret_cast<const CUtensorMap&>(mk), reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
   return cudaGetLastError();
+}
+
+template <bool MIX>
+cudaError_t run_tiles(const AttnP& p, const Plan& q, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
+  if (q.nt == 1) return q.stash ? run_split<1, true, true, MIX>(p, q, mk, mv, s) : run_split<1, false, true, MIX>(p, q, mk, mv, s);
+  if (q.nt == 2) return q.stash ? run_split<2, true, false, MIX>(p, q, mk, mv, s) : run_split<2, false, false, MIX>(p, q, mk, mv, s);
+  return q.stash ? run_split<4, true, false, MIX>(p, q, mk, mv, s) : run_split<4, false, false, MIX>(p, q, mk, mv, s);
 }
 
 cudaError_t run_streaming(const AttnP& p, const Plan& q, cudaStream_t s) {
   TcMap mk, mv;
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)q.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)q.geo.box))
     return cudaErrorInvalidValue;
-  if (q.nt == 1) return q.stash ? run_split<1, true>(p, q, mk, mv, s) : run_split<1, false>(p, q, mk, mv, s);
-  if (q.nt == 2 && p.pad_H) return q.stash ? run_split<2, true, true>(p, q, mk, mv, s) : run_split<2, false, true>(p, q, mk, mv, s);
-  if (q.nt == 2) return q.stash ? run_split<2, true>(p, q, mk, mv, s) : run_split<2, false>(p, q, mk, mv, s);
-  return q.stash ? run_split<4, true>(p, q, mk, mv, s) : run_split<4, false>(p, q, mk, mv, s);
+  if (p.pad_H) {                           // a context's block: all rows see all
+    if (q.nt == 1) return q.stash ? run_split<1, true>(p, q, mk, mv, s) : run_split<1, false>(p, q, mk, mv, s);
+    return q.stash ? run_split<2, true, true>(p, q, mk, mv, s) : run_split<2, false, true>(p, q, mk, mv, s);
+  }
+  return p.a.causal && p.a.max_q > 1 ? run_tiles<true>(p, q, mk, mv, s) : run_tiles<false>(p, q, mk, mv, s);
 }
 
 template <typename T>

@@ -85,6 +85,48 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Values that are not finite where some row of the CTA does not see them: the
+// row's weight is 0 there, but 0 * inf is not.  They are taken out of the tile
+// and noted as the first position of a +inf, a -inf and a NaN in each element;
+// the rows that see it get it back at the end (their weight is above 0).
+struct Odd { int first[3][WS_DH]; int any; };
+__device__ __forceinline__ float with_odd(const Odd& odd, float o, int limit, int d) {
+  if (limit > odd.first[2][d]) o = NAN;
+  if (limit > odd.first[0][d]) o += INFINITY;
+  if (limit > odd.first[1][d]) o -= INFINITY;
+  return o;
+}
+// A warp looks through the ROWS rows (ROWS / 4 pieces of 16 bytes per lane) of
+// a value tile of 128-byte rows, 128-byte swizzle, first position `base`.
+template <int ROWS>
+__device__ __forceinline__ bool take_out_odd(Odd& odd, uint8_t* tile, int base, int lane) {
+  constexpr int N = ROWS / 4, STEP = 8;
+  uint4* at = reinterpret_cast<uint4*>(tile) + lane;
+  uint32_t found = 0;                      // bit 31 or 15 of a pair's exponent + 1: all ones
+#pragma unroll
+  for (int q = 0; q < N; q += STEP) {
+    uint4 v[STEP];
+#pragma unroll
+    for (int k = 0; k < STEP; ++k) v[k] = at[32 * (q + k)];
+#pragma unroll
+    for (int k = 0; k < STEP; ++k)
+      found |= ((v[k].x & 0x7FFF7FFFu) + 0x00800080u) | ((v[k].y & 0x7FFF7FFFu) + 0x00800080u) |
+               ((v[k].z & 0x7FFF7FFFu) + 0x00800080u) | ((v[k].w & 0x7FFF7FFFu) + 0x00800080u);
+  }
+  if (!__any_sync(0xffffffffu, (found & 0x80008000u) != 0u)) return false;
+  for (int q = 0; q < N; ++q) {
+    const int x = 32 * q + lane, row = x >> 3, d = ((x & 7) ^ (row & 7)) * 8;
+    unsigned short* e = reinterpret_cast<unsigned short*>(at + 32 * q);
+    for (int k = 0; k < 8; ++k) {
+      const unsigned short b = e[k];
+      if ((b & 0x7F80u) != 0x7F80u) continue;
+      atomicMin(&odd.first[b & 0x7Fu ? 2 : b >> 15][d + k], base + row);
+      e[k] = 0;
+    }
+  }
+  if (lane == 0) odd.any = 1;
+  return true;
+}
 constexpr float LN2 = 0.69314718055994531f, LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int t, int h, int p) {

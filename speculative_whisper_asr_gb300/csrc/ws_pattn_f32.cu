@@ -27,6 +27,7 @@
 // memory, the rows pass by, each thread sums its rows of 4 keys, and the 16
 // row groups are added in order at the end.
 #include <algorithm>
+#include <type_traits>
 
 #include "ws_pattn.cuh"
 
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
   // split CTAs take fixed ranges and leave at once where there is nothing
   const int mine = JOIN ? min(keys, ((r.L + cs - 1) / cs + 3) & ~3) : keys;
   const int kb = min(r.L, rank * mine), ke = min(r.L, kb + mine);
+  const int all_see = row_limit(p, r, 0);           // positions that every row sees
   const bool works = kw < KW;
   for (int rg = warp % RG; works && rg < RG; rg += RW) {
     const int row = rg * NR + (NR == 8 ? c : c & 1);   // the row whose score this lane ends up with
@@ -262,20 +264,27 @@ __global__ void __launch_bounds__(RNT, NR == 8 ? 3 : 4) f32_rows_kernel(const At
           for (int d = 0; d < 4; ++d) { o[a][d].x *= fa; o[a][d].y *= fa; }
         }
       }
+      // where some row does not see all of the keys, a weight of zero takes no
+      // value: 0 * inf would reach the rows before an infinite one
+      auto add_values = [&](auto mixed) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float e = ex2(fmaf(x[u], p.sl, -msl));
-        l += e;
+        for (int u = 0; u < U; ++u) {
+          const float e = ex2(fmaf(x[u], p.sl, -msl));
+          l += e;
 #pragma unroll
-        for (int a = 0; a < NR; ++a) {
-          const float w = __shfl_sync(0xffffffffu, e, a, 8);
-          const float2 w2 = make_float2(w, w);
-          o[a][0] = __ffma2_rn(w2, make_float2(v[u][0].x, v[u][0].y), o[a][0]);
-          o[a][1] = __ffma2_rn(w2, make_float2(v[u][0].z, v[u][0].w), o[a][1]);
-          o[a][2] = __ffma2_rn(w2, make_float2(v[u][1].x, v[u][1].y), o[a][2]);
-          o[a][3] = __ffma2_rn(w2, make_float2(v[u][1].z, v[u][1].w), o[a][3]);
+          for (int a = 0; a < NR; ++a) {
+            const float w = __shfl_sync(0xffffffffu, e, a, 8);
+            if (decltype(mixed)::value && w == 0.f) continue;
+            const float2 w2 = make_float2(w, w);
+            o[a][0] = __ffma2_rn(w2, make_float2(v[u][0].x, v[u][0].y), o[a][0]);
+            o[a][1] = __ffma2_rn(w2, make_float2(v[u][0].z, v[u][0].w), o[a][1]);
+            o[a][2] = __ffma2_rn(w2, make_float2(v[u][1].x, v[u][1].y), o[a][2]);
+            o[a][3] = __ffma2_rn(w2, make_float2(v[u][1].z, v[u][1].w), o[a][3]);
+          }
         }
-      }
+      };
+      if (all_see < ke && j0 - grp + (U - 1) * KW * 4 + 4 > all_see) add_values(std::true_type());
+      else add_values(std::false_type());
     }
     // ---- the warp's four groups
     float M = m;
@@ -465,24 +474,31 @@ __global__ void __launch_bounds__(NT, 2) f32_kernel(const AttnP p) {
       }
     }
     __syncwarp();                                  // a row of P is written and read by one half-warp
+    // where some row does not see all of the keys, a weight of zero takes no
+    // value: 0 * inf would reach the rows before an infinite one
+    auto add_values = [&](auto mixed) {
 #pragma unroll 4
-    for (int j = 0; j < TK; j += 4) {
-      float4 w[RPT], x[4];
+      for (int j = 0; j < TK; j += 4) {
+        float4 w[RPT], x[4];
 #pragma unroll
-      for (int a = 0; a < RPT; ++a) w[a] = *reinterpret_cast<const float4*>(sp + (ty + 16 * a) * PITCH + j);
+        for (int a = 0; a < RPT; ++a) w[a] = *reinterpret_cast<const float4*>(sp + (ty + 16 * a) * PITCH + j);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) x[b] = *reinterpret_cast<const float4*>(v + (j + b) * PITCH + 4 * tx);
+        for (int b = 0; b < 4; ++b) x[b] = *reinterpret_cast<const float4*>(v + (j + b) * PITCH + 4 * tx);
 #pragma unroll
-      for (int a = 0; a < RPT; ++a) {
-        const float ws[4] = {w[a].x, w[a].y, w[a].z, w[a].w};
+        for (int a = 0; a < RPT; ++a) {
+          const float ws[4] = {w[a].x, w[a].y, w[a].z, w[a].w};
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float2 w2 = make_float2(ws[b], ws[b]);
-          o[a][0] = __ffma2_rn(w2, make_float2(x[b].x, x[b].y), o[a][0]);
-          o[a][1] = __ffma2_rn(w2, make_float2(x[b].z, x[b].w), o[a][1]);
+          for (int b = 0; b < 4; ++b) {
+            if (decltype(mixed)::value && ws[b] == 0.f) continue;
+            const float2 w2 = make_float2(ws[b], ws[b]);
+            o[a][0] = __ffma2_rn(w2, make_float2(x[b].x, x[b].y), o[a][0]);
+            o[a][1] = __ffma2_rn(w2, make_float2(x[b].z, x[b].w), o[a][1]);
+          }
         }
       }
-    }
+    };
+    if (Lmin < Lmax && (t + 1) * TK > Lmin) add_values(std::true_type());
+    else add_values(std::false_type());
     __syncthreads();                               // the stage and P are free
   }
 #pragma unroll

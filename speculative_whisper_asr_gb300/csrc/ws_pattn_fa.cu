@@ -9,8 +9,9 @@
 // 156 us; with more row tiles W = 2 copies the keys half as often: 219 us
 // against 306 for 4 x 2048 rows).  Row tiles A and B share every key tile of
 // 128 keys:
-//   warps 0, 2   producers: Q once and the K tiles; the V tiles (page by
-//                page), clearing value rows that do not count
+//   warps 0, 2   producers: Q once and the K tiles; the V tiles (page by page)
+//   warp 3       clears value rows that do not count, and values that are not
+//                finite where some row does not see them
 //   warp 1       MMA issuer: S = Q K^T (128 x 128, both from shared memory),
 //                O += P V with P from tensor memory and V as it lies in the
 //                pages (the "N-major" operand form: no transpose)
@@ -40,7 +41,7 @@ constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
 template <int W>
 struct FaShape {                                   // a CTA with W row tiles; 3 - W run on an SM
   static constexpr int STAGES = 2 * W;             // key stages
-  static constexpr int THREADS = 128 + 128 * W;    // K producer, MMA, V producer, idle | softmax A | softmax B
+  static constexpr int THREADS = 128 + 128 * W;    // K producer, MMA, V producer, V cleaner | softmax A | softmax B
   static constexpr int SMEM = W * TILE + STAGES * 2 * TILE + 1024;
   static constexpr uint32_t COLS = 256 * W;        // tensor memory
 };
@@ -201,7 +202,8 @@ __device__ __forceinline__ int longest_first(const AttnP& p, int z) {
 
 template <int W>
 struct Bars {
-  uint64_t q_full[W], full[FaShape<W>::STAGES], empty[FaShape<W>::STAGES], raw, s_full[W], s_free[W], p_full[W], pv_done[W];
+  uint64_t q_full[W], full[FaShape<W>::STAGES], empty[FaShape<W>::STAGES], raw[FaShape<W>::STAGES], s_full[W], s_free[W],
+      p_full[W], pv_done[W];
 };
 
 template <int W>
@@ -213,6 +215,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) Bars<W> B;
   __shared__ Meta meta[NST];
+  __shared__ Odd odd;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
@@ -243,8 +246,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     for (int b = 0; b < NST; ++b) {
       tc::mbar_init(&B.full[b], 2);
       tc::mbar_init(&B.empty[b], 1);
+      tc::mbar_init(&B.raw[b], 1);
     }
-    tc::mbar_init(&B.raw, 1);
+    odd.any = 0;
     for (int w = 0; w < W; ++w) {
       tc::mbar_init(&B.q_full[w], 1); tc::mbar_init(&B.s_full[w], 1); tc::mbar_init(&B.s_free[w], 4);
       tc::mbar_init(&B.p_full[w], 4); tc::mbar_init(&B.pv_done[w], 1);
@@ -253,6 +257,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tc::tmem_alloc(&s_tmem, FaShape<W>::COLS);
+  for (int x = threadIdx.x; x < 3 * WS_DH; x += THREADS) odd.first[0][x] = 0x7FFFFFFF;
   uint8_t* sQ = sm;
   auto sK = [&](int b) { return sm + W * TILE + b * 2 * TILE; };
   auto sV = [&](int b) { return sm + (W + 1) * TILE + b * 2 * TILE; };
@@ -266,6 +271,14 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   pdl_trigger();                                   // only now: a dependent kernel takes tensor memory too
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
+  // Value tiles that go straight to the MMA: all rows that the copies write
+  // count, and every row of the CTA sees them all.  The others are cleaned
+  // first: values behind the cache's length or of skipped pages may hold
+  // anything, and of those that only later rows see, elements that are not
+  // finite are taken out (0 * inf would reach the rows before) and come back
+  // in the epilogue for the rows that see them.
+  const int all_see = row_limit(p, r, rho0 / p.G);
+  auto direct = [&](const TileInfo& f) { return f.clean && (all_see >= r.L || f.base + FA_KEYS <= all_see); };
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0 || warp == 2) {
@@ -281,7 +294,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         }
     }
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
-    int page = tile_page(p, table, lo, lane), issued = 0, raws = 0;
+    int page = tile_page(p, table, lo, lane), issued = 0;
+    uint32_t raw = 0, phase = 0;                   // by stage: the last tile went to the cleaner; its barrier's parity
     for (int j = 0; j < nmax; ++j) {
       const int s = j % NST;
       const TileInfo f = tile_info(p, lo + j, page, r.L, lane);
@@ -289,7 +303,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
       const bool go = f.page >= 0;
       const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 128u;
-      uint64_t* bar = values && !f.clean ? &B.raw : &B.full[s];
+      const bool dirty = values && !direct(f);
+      uint64_t* bar = dirty ? &B.raw[s] : &B.full[s];
       if (lane == 0) {
         if (!values) {
 #pragma unroll
@@ -302,26 +317,41 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       __syncwarp();
       if (go) tma_load_4d((values ? sV(s) : sK(s)) + f.dst, values ? &mv : &mk, bar, 0, f.tok, h, f.page);
       ++issued;
-      if (values && !f.clean) {
-        // value rows behind the cache's length, or of skipped pages, may hold
-        // anything (0 * inf would reach the sums): cleared before the tile is
-        // handed over
-        ++raws;
-        if (!wait_warp(&B.raw, (uint32_t)((raws - 1) & 1), abort)) break;
+      raw = dirty ? raw | 1u << s : raw & ~(1u << s);
+      if (dirty) phase ^= 1u << s;
+    }
+    if (*abort && lane == 0)                       // see the copies in flight land
+      for (int j = max(0, issued - NST); j < issued; ++j) {
+        const int s = j % NST;
+        if ((raw >> s) & 1u) tc::mbar_wait(&B.raw[s], ~(phase >> s) & 1u);
+        else tc::mbar_wait(&B.full[s], (uint32_t)((j / NST) & 1));
+      }
+  } else if (warp == 3) {
+    // ---- cleaner
+    const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
+    int page = tile_page(p, table, lo, lane);
+    uint32_t phase = 0;
+    for (int j = 0; j < nmax; ++j) {
+      const int s = j % NST;
+      const TileInfo f = tile_info(p, lo + j, page, r.L, lane);
+      if (j + 1 < nmax) page = tile_page(p, table, lo + j + 1, lane);
+      if (direct(f)) continue;
+      if (!wait_warp(&B.raw[s], (phase >> s) & 1u, abort)) break;
+      tc::mbar_try_wait(&B.raw[s], (phase >> s) & 1u);         // every lane sees the copy, not lane 0 alone
+      phase ^= 1u << s;
+      if (!f.clean) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (!((f.valid[q] >> lane) & 1u))
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               *reinterpret_cast<uint4*>(sV(s) + (32 * q + lane) * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive(&B.full[s]);
       }
-    }
-    if (*abort && lane == 0) {                     // see the copies in flight land
-      for (int j = max(0, issued - NST); j < issued; ++j) tc::mbar_wait(&B.full[j % NST], (uint32_t)((j / NST) & 1));
-      if (raws) tc::mbar_wait(&B.raw, (uint32_t)((raws - 1) & 1));
+      if (all_see < r.L && f.base + FA_KEYS > all_see) take_out_odd<FA_KEYS>(odd, sV(s), f.base, lane);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(&B.full[s]);
     }
   } else if (warp == 1) {
     // ---- MMA issuer: the whole warp walks along, so that descriptors stay
@@ -483,12 +513,16 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     if (ok && nw > 0) ok = wait_warp(&B.pv_done[w], (uint32_t)((nw - 1) & 1), abort);
     tc::tc_fence_after();
+    const bool any_odd = nw > 0 && *(volatile int*)&odd.any != 0;
     if (p.nsplit > 1) {
       const size_t at = on ? (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split : 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float o[16];
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
+        if (any_odd)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
         if (on)
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
@@ -504,6 +538,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int q = 0; q < 4; ++q) {
         float o[16];
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
+        if (any_odd)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
         uint32_t u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e] = nw > 0 ? pack_bf(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;

@@ -527,3 +527,57 @@ def test_keeping_every_frame_changes_nothing_beyond_the_tolerance(R, dtype, spec
     again = dec.new_batch(req, [30, 30])
     run(dec, again)
     assert again.transcripts() == plain.transcripts()         # the caches are what they were
+
+
+# ------------------------------------------------------------------ values that are not finite, where a row does not see
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("chunks,lens,hq,hkv,page", [
+    ((5, 3), (300, 130), 4, 2, 64), ((16, 9), (70, 40), 2, 2, 16), ((30, 33), (300, 64), 2, 2, 64), ((40, 40), (200, 1025), 4, 4, 100),
+    ((90, 70), (300, 130), 4, 2, 16), ((300, 128), (700, 500), 3, 3, 64), ((70, 1), (230, 90), 10, 2, 100),
+    ((3, 2), (400, 300), 130, 1, 64), ((2, 3), (900, 300), 100, 1, 16), ((700,), (1500,), 5, 1, 128), ((60,), (5000,), 2, 1, 64),
+    ((9,), (4000,), 1, 1, 64), ((100, 37), (100, 37), 2, 1, 7)])
+def test_what_a_row_does_not_see_does_not_reach_it(R, dtype, chunks, lens, hq, hkv, page):
+    """Values and keys of the chunk's own later positions that are not finite: rows before them are as with finite
+    ones; rows that see an infinite or NaN value have it in that element alone."""
+    x = AttnCase(chunks, lens, hq=hq, hkv=hkv, page=page, dtype=dtype, seed=sum(lens))
+    clean = AttnCase(chunks, lens, hq=hq, hkv=hkv, page=page, dtype=dtype, seed=sum(lens))
+    g = np.random.default_rng(sum(lens))
+    inf = math.inf
+    special = []                                              # (request, position, KV head, element, value)
+    for i, (c, L) in enumerate(zip(chunks, lens)):
+        first = max(0, L - c) + 1                             # the first position that some row does not see
+        for pos in sorted(set(g.integers(first, L, 4).tolist() + [L - 1])) if first < L else []:
+            h = int(g.integers(0, hkv))
+            for e, v in zip(g.choice(64, 3, replace=False).tolist(), (inf, -inf, math.nan)):
+                special.append((i, pos, h, e, v))
+    for i, pos, h, e, v in special:
+        p = int(x.table[i, pos // page])
+        x.v[p, h, pos % page, e] = v
+        clean.v[p, h, pos % page, e] = 0.0
+    want, tol = clean.reference()
+    out, lse, mass = _attend(R, x)
+    ref = want[0].clone()
+    row0 = np.concatenate([[0], np.cumsum(chunks)])
+    G = hq // hkv
+    for i, pos, h, e, v in special:
+        first = pos - (lens[i] - chunks[i])                   # the first row of the chunk that sees pos
+        rows = slice(row0[i] + max(0, first), row0[i + 1])
+        ref[rows, h * G: (h + 1) * G, e] += v
+    got = out[: x.rows].double().cpu()
+    assert torch.equal(got.isnan(), ref.isnan())
+    close("out", torch.nan_to_num(got, nan=0.0, posinf=inf, neginf=-inf), torch.nan_to_num(ref, nan=0.0, posinf=inf, neginf=-inf), tol[0])
+    close("lse", lse[: x.rows], want[1], tol[1])
+    close("mass", mass, want[2], tol[2])
+    # a key
+    y = AttnCase(chunks, lens, hq=hq, hkv=hkv, page=page, dtype=dtype, seed=sum(lens))
+    want, tol = y.reference()
+    i = len(chunks) - 1 if chunks[-1] > 1 else 0
+    pos = lens[i] - 1 - (chunks[i] - 1) // 2
+    y.k[int(y.table[i, pos // page]), 0, pos % page, 3] = math.nan
+    out, lse, _ = _attend(R, y, mass=False)
+    sees = slice(row0[i] + pos - (lens[i] - chunks[i]), row0[i + 1])
+    assert bool(out[sees, :G].isnan().all()) and bool(lse[sees, :G].isnan().all())
+    for a, w, t in ((out, want[0], tol[0]), (lse, want[1], tol[1])):
+        a = a[: y.rows].double().cpu()
+        a[sees, :G] = w[sees, :G]
+        close("rows that do not see the key", a, w, t)
