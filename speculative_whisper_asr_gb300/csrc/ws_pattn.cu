@@ -123,9 +123,22 @@ __device__ __forceinline__ void tm_ld(uint32_t addr, float* v) {
   }
 }
 
+// The values that the warps took out, back into their partials of the rows that see them.
+template <int ROWS>
+__device__ __noinline__ void give_back_odd(const AttnP& p, const Req& r, const Odd* odd, float* so, int r0, int R) {
+  for (int x = threadIdx.x; x < SP_W * ROWS * WS_DH; x += SP_W * 32) {
+    const int k = x / (ROWS * WS_DH), row = x / WS_DH % ROWS, d = x % WS_DH;
+    if (r0 + row >= R || !odd[k].any) continue;
+    float* o = so + (k * ROWS + row) * SP_OP + d;
+    *o = with_odd(odd[k], *o, row_limit(p, r, (r0 + row) / p.G), d);
+  }
+  __syncthreads();
+}
+
 // MIX: causal chunks of more than one row, where values that are not finite
-// are kept from the rows that do not see them (the look at the last tiles and
-// its registers cost the other calls 2%: 92 against 90 us).
+// are kept from the rows that do not see them.  The look at the last tiles
+// costs 5% (96 requests x 20 heads: 32 rows over 375-1500 positions 112 -> 118
+// us, 9 rows over 112-448 54 -> 57), which the other calls need not pay.
 template <int NT, bool STASH, bool HILO, bool MIX>
 __global__ void __launch_bounds__(SP_W * 32, NT == 4 ? 1 : 2)
 split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -213,11 +226,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
   }
   const bool mixed = MIX && Lmin < Lmax;    // some row does not see all of the tile's positions
-  if (mixed) {
-    for (int x = lane; x < 3 * WS_DH; x += 32) odd[warp].first[0][x] = 0x7FFFFFFF;
-    if (lane == 0) odd[warp].any = 0;
-    __syncwarp();
-  }
+  if (MIX && lane == 0) odd[warp].any = 0;
   const float sl = p.sl, hold = fminf(SP_HOLD / sl, 1e30f);
   uint32_t tmem = 0;                        // this warp's columns
   if (STASH) {
@@ -228,11 +237,14 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
     tmem = s_tmem + ((uint32_t)warp << 21);
   }
   bool dead = false;
-  for (int it = 0; it < n_my; ++it) {
+  // One tile.  The last ones, which some row does not see all of, have a copy
+  // of the code to themselves (96 x 32 causal rows 118 us; 120 with their look
+  // at the values inside the usual loop).
+  auto tile = [&](int it, auto last_tiles) -> bool {
     const int slot = it % SP_NS;
     const bool more = it + SP_NS < n_my;
     const int page_next = more ? page_of() : -1;      // in flight while this tile is computed
-    if (!tc::mbar_wait(&full[warp][slot], (uint32_t)((it / SP_NS) & 1))) { dead = true; break; }
+    if (!tc::mbar_wait(&full[warp][slot], (uint32_t)((it / SP_NS) & 1))) { dead = true; return false; }
     const SpMeta mt_ = meta[warp][slot];
     uint8_t* Kt = ring + slot * (2 * SP_KB);
     uint8_t* Vt = Kt + SP_KB;
@@ -245,7 +257,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next copy
       __syncwarp();
     }
-    if (mixed && mt_.base + SP_TK > Lmin && take_out_odd<SP_TK>(odd[warp], Vt, mt_.base, lane)) {
+    if (decltype(last_tiles)::value && take_out_odd<SP_TK, 2>(odd[warp], Vt, mt_.base, lane)) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next copy
       __syncwarp();
     }
@@ -337,6 +349,17 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       }
     __syncwarp();                           // every lane has read the slot
     if (more) { issue(slot, page_next); w.next(p.geo); }
+    return true;
+  };
+  int it = 0;
+  if (MIX) {
+    // this warp's tiles that end at or before Lmin
+    const int whole = mixed ? tile_whole(p.geo, p.c.page_size, SP_TK, Lmin) : n_my * SP_W;
+    const int n_whole = min(n_my, max(0, (whole - tb - warp + SP_W - 1) / SP_W));
+    while (it < n_whole && tile(it, std::false_type())) ++it;
+    while (!dead && it < n_my && tile(it, std::true_type())) ++it;
+  } else {
+    while (it < n_my && tile(it, std::false_type())) ++it;
   }
   // ---- the four warps' partials meet in shared memory
   __syncthreads();
@@ -361,6 +384,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       }
     }
   __syncthreads();
+  if (MIX && (odd[0].any | odd[1].any | odd[2].any | odd[3].any)) give_back_odd<8 * NT>(p, r, odd, so, r0, R);
   for (int x = threadIdx.x; x < 8 * NT * 16; x += SP_W * 32) {
     const int row = x >> 4, d4 = x & 15, rho = r0 + row;
     if (rho >= R) continue;
@@ -376,16 +400,6 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       sum = fmaf(f, sml[(k * 8 * NT + row) * 2 + 1], sum);
       a0 = fmaf(f, v.x, a0); a1 = fmaf(f, v.y, a1); a2 = fmaf(f, v.z, a2); a3 = fmaf(f, v.w, a3);
     }
-    if (mixed)
-#pragma unroll
-      for (int k = 0; k < SP_W; ++k)
-        if (odd[k].any) {
-          const int limit = row_limit(p, r, rho / p.G), d = 4 * d4;
-          a0 = with_odd(odd[k], a0, limit, d);
-          a1 = with_odd(odd[k], a1, limit, d + 1);
-          a2 = with_odd(odd[k], a2, limit, d + 2);
-          a3 = with_odd(odd[k], a3, limit, d + 3);
-        }
     if (p.nsplit > 1) {
       const size_t at = (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split;
       *reinterpret_cast<float4*>(p.part_o + at * WS_DH + 4 * d4) = make_float4(a0, a1, a2, a3);

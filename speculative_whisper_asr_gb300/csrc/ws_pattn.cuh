@@ -30,6 +30,12 @@ __host__ __device__ __forceinline__ int tile_count(const TileGeo& g, int page_si
   if (g.tpp == 0) return (L + tk - 1) / tk;
   return L / page_size * g.tpp + (L % page_size + tk - 1) / tk;
 }
+// Tiles that end at or before position L.
+__device__ __forceinline__ int tile_whole(const TileGeo& g, int page_size, int tk, int L) {
+  if (g.tpp == 0) return L / tk;
+  const int rest = L % page_size;
+  return L / page_size * g.tpp + rest / tk;
+}
 
 struct AttnP {
   ws_paged_cache c;
@@ -89,7 +95,7 @@ __device__ __forceinline__ float lg2(float x) {
 // row's weight is 0 there, but 0 * inf is not.  They are taken out of the tile
 // and noted as the first position of a +inf, a -inf and a NaN in each element;
 // the rows that see it get it back at the end (their weight is above 0).
-struct Odd { int first[3][WS_DH]; int any; };
+struct Odd { int first[3][WS_DH]; int any; };      // `any` starts at 0, the rest with the first find
 __device__ __forceinline__ float with_odd(const Odd& odd, float o, int limit, int d) {
   if (limit > odd.first[2][d]) o = NAN;
   if (limit > odd.first[0][d]) o += INFINITY;
@@ -99,9 +105,29 @@ __device__ __forceinline__ float with_odd(const Odd& odd, float o, int limit, in
 // A warp looks through the ROWS rows (ROWS / 4 pieces of 16 bytes per lane) of
 // a value tile of 128-byte rows, 128-byte swizzle, first position `base`.
 template <int ROWS>
-__device__ __forceinline__ bool take_out_odd(Odd& odd, uint8_t* tile, int base, int lane) {
-  constexpr int N = ROWS / 4, STEP = 8;
+__device__ __noinline__ void note_odd(Odd& odd, uint8_t* tile, int base, int lane) {
+  if (!odd.any) {
+    for (int x = lane; x < 3 * WS_DH; x += 32) odd.first[0][x] = 0x7FFFFFFF;
+    __syncwarp();
+  }
   uint4* at = reinterpret_cast<uint4*>(tile) + lane;
+  for (int q = 0; q < ROWS / 4; ++q) {
+    const int x = 32 * q + lane, row = x >> 3, d = ((x & 7) ^ (row & 7)) * 8;
+    unsigned short* e = reinterpret_cast<unsigned short*>(at + 32 * q);
+    for (int k = 0; k < 8; ++k) {
+      const unsigned short b = e[k];
+      if ((b & 0x7F80u) != 0x7F80u) continue;
+      atomicMin(&odd.first[b & 0x7Fu ? 2 : b >> 15][d + k], base + row);
+      e[k] = 0;
+    }
+  }
+  __syncwarp();
+  if (lane == 0) odd.any = 1;
+}
+template <int ROWS, int STEP>
+__device__ __forceinline__ bool take_out_odd(Odd& odd, uint8_t* tile, int base, int lane) {
+  constexpr int N = ROWS / 4;              // STEP of them in flight
+  const uint4* at = reinterpret_cast<const uint4*>(tile) + lane;
   uint32_t found = 0;                      // bit 31 or 15 of a pair's exponent + 1: all ones
 #pragma unroll
   for (int q = 0; q < N; q += STEP) {
@@ -114,17 +140,7 @@ __device__ __forceinline__ bool take_out_odd(Odd& odd, uint8_t* tile, int base, 
                ((v[k].z & 0x7FFF7FFFu) + 0x00800080u) | ((v[k].w & 0x7FFF7FFFu) + 0x00800080u);
   }
   if (!__any_sync(0xffffffffu, (found & 0x80008000u) != 0u)) return false;
-  for (int q = 0; q < N; ++q) {
-    const int x = 32 * q + lane, row = x >> 3, d = ((x & 7) ^ (row & 7)) * 8;
-    unsigned short* e = reinterpret_cast<unsigned short*>(at + 32 * q);
-    for (int k = 0; k < 8; ++k) {
-      const unsigned short b = e[k];
-      if ((b & 0x7F80u) != 0x7F80u) continue;
-      atomicMin(&odd.first[b & 0x7Fu ? 2 : b >> 15][d + k], base + row);
-      e[k] = 0;
-    }
-  }
-  if (lane == 0) odd.any = 1;
+  note_odd<ROWS>(odd, tile, base, lane);
   return true;
 }
 constexpr float LN2 = 0.69314718055994531f, LOG2E = 1.4426950408889634f;

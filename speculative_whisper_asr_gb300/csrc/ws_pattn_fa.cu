@@ -257,7 +257,6 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tc::tmem_alloc(&s_tmem, FaShape<W>::COLS);
-  for (int x = threadIdx.x; x < 3 * WS_DH; x += THREADS) odd.first[0][x] = 0x7FFFFFFF;
   uint8_t* sQ = sm;
   auto sK = [&](int b) { return sm + W * TILE + b * 2 * TILE; };
   auto sV = [&](int b) { return sm + (W + 1) * TILE + b * 2 * TILE; };
@@ -348,7 +347,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
               *reinterpret_cast<uint4*>(sV(s) + (32 * q + lane) * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
       }
-      if (all_see < r.L && f.base + FA_KEYS > all_see) take_out_odd<FA_KEYS>(odd, sV(s), f.base, lane);
+      if (all_see < r.L && f.base + FA_KEYS > all_see) take_out_odd<FA_KEYS, 8>(odd, sV(s), f.base, lane);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(&B.full[s]);
