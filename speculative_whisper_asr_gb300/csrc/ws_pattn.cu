@@ -257,7 +257,7 @@ split_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next copy
       __syncwarp();
     }
-    if (decltype(last_tiles)::value && take_out_odd<SP_TK, 2>(odd[warp], Vt, mt_.base, lane)) {
+    if (decltype(last_tiles)::value && take_out_odd<SP_TK, 2, true>(odd[warp], Vt, mt_.base, lane)) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot's next copy
       __syncwarp();
     }

@@ -105,7 +105,7 @@ __device__ __forceinline__ float with_odd(const Odd& odd, float o, int limit, in
 // A warp looks through the ROWS rows (ROWS / 4 pieces of 16 bytes per lane) of
 // a value tile of 128-byte rows, 128-byte swizzle, first position `base`.
 template <int ROWS>
-__device__ __noinline__ void note_odd(Odd& odd, uint8_t* tile, int base, int lane) {
+__device__ __forceinline__ void note_odd(Odd& odd, uint8_t* tile, int base, int lane) {
   if (!odd.any) {
     for (int x = lane; x < 3 * WS_DH; x += 32) odd.first[0][x] = 0x7FFFFFFF;
     __syncwarp();
@@ -124,7 +124,13 @@ __device__ __noinline__ void note_odd(Odd& odd, uint8_t* tile, int base, int lan
   __syncwarp();
   if (lane == 0) odd.any = 1;
 }
-template <int ROWS, int STEP>
+template <int ROWS>
+__device__ __noinline__ void call_note_odd(Odd& odd, uint8_t* tile, int base, int lane) {
+  note_odd<ROWS>(odd, tile, base, lane);
+}
+// CALL: the rare part outside the caller's code (not where setmaxnreg has
+// limited the warp's registers: a called function does not know the limit).
+template <int ROWS, int STEP, bool CALL>
 __device__ __forceinline__ bool take_out_odd(Odd& odd, uint8_t* tile, int base, int lane) {
   constexpr int N = ROWS / 4;              // STEP of them in flight
   const uint4* at = reinterpret_cast<const uint4*>(tile) + lane;
@@ -140,7 +146,8 @@ __device__ __forceinline__ bool take_out_odd(Odd& odd, uint8_t* tile, int base, 
                ((v[k].z & 0x7FFF7FFFu) + 0x00800080u) | ((v[k].w & 0x7FFF7FFFu) + 0x00800080u);
   }
   if (!__any_sync(0xffffffffu, (found & 0x80008000u) != 0u)) return false;
-  note_odd<ROWS>(odd, tile, base, lane);
+  if (CALL) call_note_odd<ROWS>(odd, tile, base, lane);
+  else note_odd<ROWS>(odd, tile, base, lane);
   return true;
 }
 constexpr float LN2 = 0.69314718055994531f, LOG2E = 1.4426950408889634f;

@@ -24,8 +24,8 @@
 // bound the kernel as much as the tensor core does; scaling and sums are
 // packed pairs (f32x2).  P V (64 columns wide) takes the tensor core as long
 // as Q K^T (128 wide).  4 requests x 20 heads x 2048 rows over up to 8192
-// positions (198 GFLOP): 207 us, 0.96 PFLOP/s of the measured 1.92; tensor
-// pipe 52% busy, exponential pipe 45%.
+// positions (198 GFLOP): 209 us, 0.95 PFLOP/s of the measured 1.92; tensor
+// pipe 52% busy, exponential pipe 44%.
 //
 // fa_mass_kernel.  The weights summed per key, once every row's log-sum-exp
 // is known: S^T = K Q^T puts a key into each thread, which adds
@@ -347,7 +347,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
               *reinterpret_cast<uint4*>(sV(s) + (32 * q + lane) * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
       }
-      if (all_see < r.L && f.base + FA_KEYS > all_see) take_out_odd<FA_KEYS, 8>(odd, sV(s), f.base, lane);
+      if (all_see < r.L && f.base + FA_KEYS > all_see) take_out_odd<FA_KEYS, 8, false>(odd, sV(s), f.base, lane);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(&B.full[s]);
