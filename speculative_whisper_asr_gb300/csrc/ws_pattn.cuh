@@ -102,8 +102,7 @@ __device__ __forceinline__ float with_odd(const Odd& odd, float o, int limit, in
   if (limit > odd.first[1][d]) o -= INFINITY;
   return o;
 }
-// A warp looks through the ROWS rows (ROWS / 4 pieces of 16 bytes per lane) of
-// a value tile of 128-byte rows, 128-byte swizzle, first position `base`.
+// Notes and clears such values of a tile.
 template <int ROWS>
 __device__ __forceinline__ void note_odd(Odd& odd, uint8_t* tile, int base, int lane) {
   if (!odd.any) {
@@ -128,8 +127,11 @@ template <int ROWS>
 __device__ __noinline__ void call_note_odd(Odd& odd, uint8_t* tile, int base, int lane) {
   note_odd<ROWS>(odd, tile, base, lane);
 }
-// CALL: the rare part outside the caller's code (not where setmaxnreg has
-// limited the warp's registers: a called function does not know the limit).
+// A warp looks through the ROWS rows (ROWS / 4 pieces of 16 bytes per lane) of
+// a value tile of 128-byte rows, 128-byte swizzle, first position `base`; true
+// if something was cleared.  CALL: the rare part outside the caller's code (not
+// where setmaxnreg has limited the warp's registers: a called function does not
+// know the limit).
 template <int ROWS, int STEP, bool CALL>
 __device__ __forceinline__ bool take_out_odd(Odd& odd, uint8_t* tile, int base, int lane) {
   constexpr int N = ROWS / 4;              // STEP of them in flight

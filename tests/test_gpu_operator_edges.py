@@ -88,16 +88,14 @@ def _allow_all_or_nothing(R, s):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("mode", ["ar", "spec", "sample-ar", "sample-spec"])
-@pytest.mark.parametrize("where", ["prompt", "first", "later"])
+@pytest.mark.parametrize("mode,where", [(m, w) for m in ("ar", "spec", "sample-ar", "sample-spec") for w in ("prompt", "first")]
+                         + [("spec", "later"), ("sample-spec", "later")])    # rows behind the first: speculative rounds alone
 def test_a_state_without_tokens_ends_the_request(R, dtype, mode, where):
     """Request 0 reaches a grammar state that excludes every token: it ends there, with what it had, and the status
     word says so.  Request 1 goes on as if alone."""
     n, budget = 2, 12
     s, dec, req, _ = _decoder(R, dtype, n)
     sampling, spec = mode.startswith("sample"), mode.endswith("spec")
-    if where == "later" and not spec:
-        pytest.skip("rows behind the first exist in speculative rounds")
 
     def run(dead):
         b = dec.new_batch(req, [budget] * n, sampling=sampling, rules=_allow_all_or_nothing(R, s))
