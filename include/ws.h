@@ -57,7 +57,8 @@ enum {
   WS_EUNSUPPORTED = -6   /* shape or option the library does not implement */
 };
 
-enum { WS_F32 = 0, WS_BF16 = 1 };
+enum { WS_F32 = 0, WS_BF16 = 1,
+       WS_E4M3 = 2 };    /* ws_paged_cache only: 8-bit floats (e4m3) with scales */
 
 /* GEMM engine: both compute every output element with a K order that does
  * not depend on the number of rows, so block verification and one-token
@@ -445,7 +446,9 @@ int ws_argmax_rows_noalloc(const float* logits, int rows, int vocab, const uint3
  * the GPU (two streams, two graphs) need a workspace each.
  * ------------------------------------------------------------------------ */
 
-/* A paged key/value cache with head width 64.  Element x (0..63) of token t
+/* A paged key/value cache with head width 64, in the model dtype or in 8 bits
+ * (WS_E4M3: one byte per element, strides in bytes, queries and outputs in
+ * bfloat16).  Element x (0..63) of token t
  * of head h on page p is at
  *   p * page_stride + h * head_stride + t * token_stride + x
  * elements from k (keys) and from v (values), so the contexts' own pools
@@ -454,9 +457,18 @@ int ws_argmax_rows_noalloc(const float* logits, int rows, int vocab, const uint3
  * Position j of a slot is token j % page_size of page
  * page_table[slot * table_stride + j / page_size].  A page id outside
  * [0, n_pages) is never read: its positions take no part in attention, and
- * ws_cache_evict moves nothing from or to it. */
+ * ws_cache_evict moves nothing from or to it.
+ *
+ * In a cache in 8 bits the tokens b * scale_block .. of a page are block b, and
+ * the keys of a block and head have one scale 2^(s - 127), s the byte at
+ *   p * scale_page_stride + h * scale_head_stride + b
+ * from k_scale; the values likewise from v_scale (255 is not a scale).  The
+ * element stands for its e4m3 value times the scale; the codes 0x7f and 0xff
+ * for NaN.  Powers of two keep the products exact, and a block whose scale
+ * grows is moved to it without loss, but for its values below 2^-6 of the new
+ * scale, which are rounded again. */
 typedef struct {
-  int32_t dtype;               /* WS_F32 or WS_BF16 (keys, values, queries, outputs) */
+  int32_t dtype;               /* WS_F32 or WS_BF16 (keys, values, queries, outputs), or WS_E4M3 */
   int32_t n_kv_heads;          /* >= 1 */
   int32_t page_size;           /* tokens per page, >= 1 (a divisor of 64 that is >= 8, or >= 64, is fastest) */
   int32_t n_pages;             /* >= 1 */
@@ -466,6 +478,11 @@ typedef struct {
   const int32_t* page_table;   /* [n_slots, table_stride] (device) */
   int32_t n_slots;             /* >= 1 */
   int32_t table_stride;        /* pages listed per slot, >= 1 */
+  /* WS_E4M3 only, not read otherwise: */
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t scale_page_stride, scale_head_stride;     /* bytes, >= page_size / scale_block (a dimension of one: any) */
+  int32_t scale_block;         /* tokens per scale, a divisor of page_size (>= 16 is fastest) */
 } ws_paged_cache;
 
 /* Arguments of ws_paged_attention (device pointers; sizes are host ints). */
@@ -486,7 +503,7 @@ typedef struct {
                                   (beside q in rows of the same stride is fine) */
   int64_t out_stride;
   float* lse;                  /* [total_q, n_heads] out: log sum exp of the row's scores, or NULL */
-  float* mass;                 /* [n_slots, n_kv_heads, mass_stride] in/out, or NULL */
+  float* mass;                 /* [n_slots, n_kv_heads, mass_stride] in/out, or NULL (WS_E4M3: NULL) */
   int64_t mass_stride;         /* >= max_kv */
 } ws_attention_args;
 
@@ -511,7 +528,10 @@ size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attent
  * Rows of requests with kv_len <= 0, or with an id outside [0, n_slots), see
  * nothing.  Cached values behind kv_len are not read into any result, and what
  * a row does not see does not reach it, infinite or NaN included.  Rows
- * outside every chunk and mass behind kv_len are left as they were. */
+ * outside every chunk and mass behind kv_len are left as they were.
+ * A cache in 8 bits is read as the values it stands for (queries and outputs
+ * bfloat16, the same sums); its weights are not accumulated: mass is
+ * WS_EUNSUPPORTED. */
 int ws_paged_attention(const ws_paged_cache* cache, const ws_attention_args* args, void* workspace,
                        size_t workspace_bytes, ws_stream stream);
 
@@ -551,7 +571,9 @@ size_t ws_cache_evict_workspace(const ws_paged_cache* cache, const ws_evict_args
  * cache's page_table and the move is in place; mass_out = mass and
  * pos_out = pos are in place with equal strides, and otherwise the arrays
  * are disjoint.  Slots must not share pages that the call writes.  Contents
- * behind the new length, and slots not listed, are left as they were. */
+ * behind the new length, and slots not listed, are left as they were.
+ * Caches in 8 bits, whose positions cannot leave their block's scale, are
+ * WS_EUNSUPPORTED. */
 int ws_cache_evict(const ws_paged_cache* cache, const ws_evict_args* args, void* workspace,
                    size_t workspace_bytes, ws_stream stream);
 
@@ -602,6 +624,117 @@ typedef struct {
  * At most 4,096 tokens (hist_stride + H - 1, or window) and biases
  * (bias_stride) per row: WS_EUNSUPPORTED beyond. */
 int ws_logits_rules(const ws_rules_args* args, ws_stream stream);
+
+/* Arguments of ws_cache_append (device pointers; sizes are host ints). */
+typedef struct {
+  int32_t n_req;               /* >= 0 */
+  const int32_t* req_ids;      /* [n_req] slots, distinct, or NULL (= 0..n_req-1) */
+  const int32_t* kv_len;       /* [n_slots] positions in the cache, the chunk's own included */
+  const int32_t* cu_q;         /* [n_req + 1] prefix sums of the chunk lengths (cu_q[0] = 0) */
+  int32_t total_q;             /* cu_q[n_req]: rows of k, v, q and q_out (bounds every access to them) */
+  int32_t max_q;               /* >= every chunk length; longer chunks are cut off at it */
+  const void* k;               /* row r, KV head h at r * k_stride + h * 64 elements of the cache's type (WS_E4M3: */
+  int64_t k_stride;            /*   bfloat16); 16-byte aligned rows */
+  const void* v;
+  int64_t v_stride;
+  int32_t n_heads;             /* query heads of q */
+  const void* q;               /* row r, head u at r * q_stride + u * 64, or NULL (no queries) */
+  int64_t q_stride;
+  void* q_out;                 /* the queries, turned; q itself with the same stride, or apart from q, k and v */
+  int64_t q_out_stride;
+  const uint64_t* turns;       /* [rot_dims / 2] turns per position, as fractions of 2^64, or NULL (no rotation) */
+  int32_t rot_dims;            /* leading elements of a head that turn: a multiple of 8, 8..64 */
+  int32_t rot_halves;          /* 1: pairs of elements (i, i + rot_dims / 2); 0: (2 i, 2 i + 1) */
+  const int32_t* pos;          /* [total_q] position that a row turns by, or NULL (its place in the cache) */
+} ws_append_args;
+
+/* Appends the keys and values of new tokens to a paged cache, the step
+ * between a layer's projections and ws_paged_attention.  Row r of a chunk of c
+ * rows goes to position kv_len - c + r of its slot.  With `turns`, keys and
+ * queries are turned on the way (rotary positions, as in the drafter,
+ * Whisper-Flash App. A.2): pair i of a row at position m becomes
+ *   (x cos a - y sin a, x sin a + y cos a),  a = 2 pi m turns[i] / 2^64,
+ * m and turns[i] multiplied modulo 2^64: the angle of any 32-bit position is
+ * exact to 2^-32 of a turn.  Values are stored as they are.
+ * A cache in 8 bits: with m the largest finite |x| of the rows that a block
+ * and head receives, after the turn, and s the smallest power of two (2^-127
+ * at least) with m <= 448 s, a block that begins with this call takes the
+ * scale s, and any other the larger of s and its own; where that grows, the
+ * block's earlier tokens are moved to it.  Elements are rounded to nearest
+ * even; those that are not finite become NaN.  Appending again what a call
+ * appended gives the same values.
+ * Positions before 0, behind the page table, or on a page id outside
+ * [0, n_pages) are not stored; rows of a slot outside [0, n_slots) and rows
+ * before position 0 are left out altogether, their queries too.  Pages that
+ * the call writes belong to one slot each.  Rows outside every chunk, and the
+ * cache elsewhere, are left as they were. */
+int ws_cache_append(const ws_paged_cache* cache, const ws_append_args* args, ws_stream stream);
+
+/* Arguments of ws_cache_reorder (device pointers; sizes are host ints). */
+typedef struct {
+  int32_t n_req;               /* >= 0 */
+  int32_t beams;               /* 1..16 */
+  const int32_t* req_ids;      /* [n_req, beams] slots, distinct, or NULL (= i * beams + b) */
+  const int32_t* kv_len;       /* [n_slots] positions in the cache, the same for the beams of a request */
+  const int32_t* parent;       /* [n_req, beams] the beam that each new beam continues; outside [0, beams): itself */
+  int32_t* page_table;         /* the cache's own page table, whose rows are reordered, or NULL (contents alone) */
+} ws_reorder_args;
+
+/* Reorders the caches of beams after a step of beam search: beam b of a
+ * request goes on from what its beam parent[b] held.  A page that is full is
+ * not copied: the new beam's page table lists the parent's page, and beams
+ * come to share it.  Of the page that the next position falls into, each beam
+ * has one of its own, which stays its own, and the parent's tokens (and, in a
+ * cache in 8 bits, scales) are copied into it.  Entries of the page table
+ * behind the full pages are neither moved nor read, but for that one.
+ * So n_slots * table_stride pages suffice for any number of steps: each slot
+ * starts with pages of its own, listed once, and full pages are only read.
+ * Caches that share a page table (a model's layers) take one call each, one
+ * of them, in any order, with page_table.  All is done in place, and nothing
+ * is allocated. */
+int ws_cache_reorder(const ws_paged_cache* cache, const ws_reorder_args* args, ws_stream stream);
+
+/* Arguments of ws_beam_select (device pointers; sizes are host ints). */
+typedef struct {
+  int32_t n, beams, vocab;     /* requests, beams (1..16), vocabulary (1..262144) */
+  const float* logits;         /* row (i, b) at (i * beams + b) * ld */
+  int64_t ld;                  /* >= vocab */
+  int32_t eos_id;              /* end of transcript, or -1 (no token ends a beam) */
+  const float* score;          /* [n, beams] log probability of each beam; a beam that is not finite is none */
+  float* score_out;            /* [n, beams]; score itself, or apart */
+  int32_t* parent;             /* [n, beams] out: the beam that the new one continues */
+  int32_t* token;              /* [n, beams] out: with this token */
+  const int32_t* tokens;       /* [n, beams, capacity] transcripts, or NULL */
+  int32_t* tokens_out;         /* tokens itself, or apart */
+  const int32_t* length;       /* [n] tokens per transcript (with tokens) */
+  int32_t* length_out;         /* length itself, or apart */
+  int32_t capacity;
+  int32_t max_done;            /* finished transcripts kept per request, >= 0 */
+  const int32_t* n_done;       /* [n] finished so far, or NULL (beams that end are dropped) */
+  int32_t* n_done_out;         /* n_done itself, or apart */
+  float* done_score;           /* [n, max_done] log probability, the end included */
+  int32_t* done_length;        /* [n, max_done], or NULL (with tokens) */
+  int32_t* done_tokens;        /* [n, max_done, capacity], or NULL (with tokens) */
+} ws_beam_args;
+
+/* One step of beam search on the logits that ws_verify or ws_logits_rules
+ * left (the search that Whisper's decoder offers beside greedy decoding).
+ * Every token v of every beam b is a candidate with
+ *   score[b] + logits[b, v] - log sum_u exp(logits[b, u])
+ * (equal: the lower beam, then the lower token); the sums of exponentials are
+ * fp32 sums, the rest is in double.  In that order, candidates that are
+ * eos_id join the finished transcripts (while there is room) and the others
+ * become beams 0, 1, ..., until there are `beams` of them.  A transcript is
+ * the parent's and the token; a finished one the parent's alone.
+ * Candidates that are not finite (a banned token; a beam whose score, or a
+ * row whose sum of exponentials, is not) do not count.  Beams that no
+ * candidate is left for get score -inf, token -1 and themselves as parent.
+ * A request with max_done finished transcripts, or a full one (length >=
+ * capacity), is idle: parent itself, token -1, all else as it was.
+ * tokens_out behind the new length is left as it was.  The same call gives
+ * the same bits, and equal rows give equal sums wherever they lie. */
+int ws_beam_select(const ws_beam_args* args, void* workspace, size_t workspace_bytes, ws_stream stream);
+size_t ws_beam_select_workspace(const ws_beam_args* args);
 
 /* Number of CUDA kernels this library has launched in the process so far
  * (all contexts; host-side counter, for instrumentation). */

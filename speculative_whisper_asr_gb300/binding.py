@@ -15,7 +15,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libws.so")
 
 WS_OK, WS_EINVAL, WS_ENOSPACE, WS_EPOS, WS_ECUDA, WS_EDEVICE, WS_EUNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
-WS_F32, WS_BF16 = 0, 1
+WS_F32, WS_BF16, WS_E4M3 = 0, 1, 2
 WS_GEMM_AUTO, WS_GEMM_SIMT, WS_GEMM_TC = 0, 1, 2
 WS_ACCEPT_GREEDY, WS_ACCEPT_SAMPLE, WS_ACCEPT_FORCED, WS_ACCEPT_TREE = 0, 1, 2, 3
 
@@ -28,7 +28,8 @@ EXPORTS = ("ws_query_workspace", "ws_load_weights", "ws_reset", "ws_cross_kv", "
            "ws_encoder_free", "ws_encoder_attention",
            "ws_fused_layernorm",
            "ws_paged_attention_workspace", "ws_paged_attention", "ws_cache_evict_workspace", "ws_cache_evict",
-           "ws_logits_rules", "ws_set_frame_mass", "ws_evict_frames")
+           "ws_logits_rules", "ws_set_frame_mass", "ws_evict_frames",
+           "ws_cache_append", "ws_cache_reorder", "ws_beam_select_workspace", "ws_beam_select")
 
 
 class WSError(RuntimeError):
@@ -59,7 +60,8 @@ class PagedCacheDesc(C.Structure):
     _fields_ = [("dtype", C.c_int32), ("n_kv_heads", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
                 ("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64), ("head_stride", C.c_int64),
                 ("token_stride", C.c_int64), ("page_table", C.c_void_p), ("n_slots", C.c_int32),
-                ("table_stride", C.c_int32)]
+                ("table_stride", C.c_int32), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("scale_page_stride", C.c_int64), ("scale_head_stride", C.c_int64), ("scale_block", C.c_int32)]
 
 
 class AttentionArgs(C.Structure):
@@ -88,6 +90,28 @@ class RulesArgs(C.Structure):
                 ("bias_vals", C.c_void_p), ("bias_len", C.c_void_p), ("bias_stride", C.c_int32),
                 ("masks", C.c_void_p), ("n_masks", C.c_int32), ("mask_row", C.c_void_p), ("target", C.c_void_p),
                 ("logprob", C.c_void_p)]
+
+
+class AppendArgs(C.Structure):
+    _fields_ = [("n_req", C.c_int32), ("req_ids", C.c_void_p), ("kv_len", C.c_void_p), ("cu_q", C.c_void_p),
+                ("total_q", C.c_int32), ("max_q", C.c_int32), ("k", C.c_void_p), ("k_stride", C.c_int64),
+                ("v", C.c_void_p), ("v_stride", C.c_int64), ("n_heads", C.c_int32), ("q", C.c_void_p),
+                ("q_stride", C.c_int64), ("q_out", C.c_void_p), ("q_out_stride", C.c_int64), ("turns", C.c_void_p),
+                ("rot_dims", C.c_int32), ("rot_halves", C.c_int32), ("pos", C.c_void_p)]
+
+
+class ReorderArgs(C.Structure):
+    _fields_ = [("n_req", C.c_int32), ("beams", C.c_int32), ("req_ids", C.c_void_p), ("kv_len", C.c_void_p),
+                ("parent", C.c_void_p), ("page_table", C.c_void_p)]
+
+
+class BeamArgs(C.Structure):
+    _fields_ = [("n", C.c_int32), ("beams", C.c_int32), ("vocab", C.c_int32), ("logits", C.c_void_p), ("ld", C.c_int64),
+                ("eos_id", C.c_int32), ("score", C.c_void_p), ("score_out", C.c_void_p), ("parent", C.c_void_p),
+                ("token", C.c_void_p), ("tokens", C.c_void_p), ("tokens_out", C.c_void_p), ("length", C.c_void_p),
+                ("length_out", C.c_void_p), ("capacity", C.c_int32), ("max_done", C.c_int32), ("n_done", C.c_void_p),
+                ("n_done_out", C.c_void_p), ("done_score", C.c_void_p), ("done_length", C.c_void_p),
+                ("done_tokens", C.c_void_p)]
 
 
 class EncoderDesc(C.Structure):
@@ -136,6 +160,10 @@ def _load():
         "ws_cache_evict_workspace": (C.c_size_t, [P, P]),
         "ws_cache_evict": (I, [P, P, P, C.c_size_t, S]),
         "ws_logits_rules": (I, [P, S]),
+        "ws_cache_append": (I, [P, P, S]),
+        "ws_cache_reorder": (I, [P, P, S]),
+        "ws_beam_select_workspace": (C.c_size_t, [P]),
+        "ws_beam_select": (I, [P, P, C.c_size_t, S]),
         "ws_set_frame_mass": (I, [P, P]),
         "ws_evict_frames": (I, [P, I, P, P, I, S]),
         "ws_encoder_workspace": (C.c_size_t, [C.POINTER(EncoderDesc)]),
@@ -381,6 +409,22 @@ def ws_cache_evict(cache: PagedCacheDesc, args: EvictArgs, workspace, nbytes, st
 
 def ws_logits_rules(args: RulesArgs, stream):
     return _check(None, lib.ws_logits_rules(C.addressof(args), stream))
+
+
+def ws_cache_append(cache: PagedCacheDesc, args: AppendArgs, stream):
+    return _check(None, lib.ws_cache_append(C.addressof(cache), C.addressof(args), stream))
+
+
+def ws_cache_reorder(cache: PagedCacheDesc, args: ReorderArgs, stream):
+    return _check(None, lib.ws_cache_reorder(C.addressof(cache), C.addressof(args), stream))
+
+
+def ws_beam_select_workspace(args: BeamArgs) -> int:
+    return lib.ws_beam_select_workspace(C.addressof(args))
+
+
+def ws_beam_select(args: BeamArgs, workspace, nbytes, stream):
+    return _check(None, lib.ws_beam_select(C.addressof(args), workspace or None, nbytes, stream))
 
 
 def ws_set_frame_mass(ctx, mass):

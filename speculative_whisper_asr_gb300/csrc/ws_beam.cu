@@ -1,0 +1,349 @@
+// One step of beam search over beams and vocabulary (ws_beam_select in
+// include/ws.h gives the rule).
+//
+// scan_kernel.  A CTA reads a part of one beam's logits once: a running
+// maximum with the sum of exponentials below it, and each thread's largest
+// logit.  A thread's logits depend on the tokens alone, not on the row's
+// alignment, so equal rows get equal sums and equal candidates stay equal.
+// The K = beams + 1 best candidates of a part (no beam can need more: `beams`
+// that go on and the end) are found after the stream, without a barrier or a
+// list in it: T, the K-th best of the threads' best in the order (larger
+// logit, lower token), has K logits at or before it, so each of the K best is
+// in a thread whose best is not behind T, and exactly K threads are such.
+// Their logits (K of the 256th parts, from L2) are read again, those not
+// behind T kept, and ranked by counting.
+//
+// merge_kernel.  One CTA per request: log-sum-exps of the beams (in double:
+// what differs by less than fp32's step from another beam is still told
+// apart), the parts' candidates ranked within their beams, the beams' against
+// each other by whole numbers that order like the doubles, and the walk over
+// the 2 * beams best: candidates that end go to the finished transcripts.
+// Then each thread moves a column of the transcripts for all beams, so the
+// move may be in place.
+#include <string>
+
+#include "ws_paged.cuh"
+
+namespace {
+
+constexpr int BM_NT = 256;
+constexpr int BM_BEAMS = 16;
+constexpr int BM_K = BM_BEAMS + 1;
+constexpr int BM_PART = 16384;             // logits per part, at most
+constexpr int BM_PARTS = 32;               // parts per row, at most
+constexpr float LOG2E = 1.4426950408889634f;
+
+struct BeamP {
+  ws_beam_args a;
+  int parts, part;                         // per row; logits per part
+  unsigned long long* cand;                // [rows][parts][K] argmax keys, 0: none
+  float2* stat;                            // [rows][parts] (largest logit, sum of exp below it)
+};
+
+// The difference comes first: log2(e) times each of the two, one of them
+// rounded, would put an error of the logits' own size into every term.
+__device__ __forceinline__ float exp_of(float difference) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(difference * LOG2E));
+  return y;
+}
+__device__ __forceinline__ float key_value(unsigned long long k) {
+  const uint32_t u = (uint32_t)(k >> 32);
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+__device__ __forceinline__ bool idle(const ws_beam_args& a, int i) {
+  return (a.n_done && a.n_done[i] >= a.max_done) || (a.tokens && a.length[i] >= a.capacity);
+}
+
+__global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
+  __shared__ unsigned long long s_key[8 * BM_K];
+  __shared__ int s_thread[BM_K];
+  __shared__ unsigned long long s_t;
+  __shared__ unsigned long long s_list[BM_K * (BM_PART / BM_NT)];
+  __shared__ int s_n;
+  __shared__ float s_m[8], s_s[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.y, V = p.a.vocab, K = p.a.beams + 1;
+  pdl_trigger();
+  if (idle(p.a, row / p.a.beams)) return;
+  const float* z = p.a.logits + (size_t)row * (size_t)p.a.ld;
+  const int v0 = blockIdx.x * p.part, v1 = min(V, v0 + p.part);
+  // ---- the stream: U logits of a thread in flight
+  float m = -INFINITY, ref = 0.f, s = 0.f; // largest so far (ref: 0 until there is one); sum of exp(. - ref)
+  int at = -1;                             // its token
+  constexpr int U = 16;
+  for (int v = v0 + tid; v < v1; v += U * BM_NT) {
+    float f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) f[u] = v + u * BM_NT < v1 ? __ldg(z + v + u * BM_NT) : -INFINITY;
+    float t = f[0];
+#pragma unroll
+    for (int u = 1; u < U; ++u) t = fmaxf(t, f[u]);
+    if (t > m) {
+#pragma unroll
+      for (int u = U - 1; u >= 0; --u)
+        if (f[u] == t) at = v + u * BM_NT;
+      s *= exp_of(m - t);                  // m = -inf: 0
+      m = ref = t;
+    }
+#pragma unroll
+    for (int u = 0; u < U; u += 2) s += exp_of(f[u] - ref) + exp_of(f[u + 1] - ref);
+  }
+  // ---- the K best of the warp's threads, then of the CTA's
+  const unsigned long long key = at >= 0 ? argmax_key(m, at) : 0ull;
+  uint32_t left = (uint32_t)(key >> 32);
+  for (int r = 0; r < K; ++r) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, left);
+    const uint32_t low = __reduce_max_sync(0xffffffffu, left == best ? (uint32_t)key : 0u);
+    if (lane == 0) s_key[warp * K + r] = best ? (unsigned long long)best << 32 | low : 0ull;
+    if (left == best && (uint32_t)key == low) left = 0u;
+  }
+  {
+    const float wm = warp_max(m);
+    const float ws = warp_sum(m > -INFINITY ? s * exp_of(m - wm) : s);
+    if (lane == 0) { s_m[warp] = wm; s_s[warp] = ws; }
+  }
+  if (tid == 0) { s_n = 0; s_t = 1ull; }
+  if (tid < K) s_thread[tid] = -1;
+  __syncthreads();
+  if (tid < 8 * K) {
+    const unsigned long long mine = s_key[tid];
+    if (mine) {
+      int rank = 0;
+      for (int j = 0; j < 8 * K; ++j) rank += s_key[j] > mine;
+      if (rank < K) s_thread[rank] = (argmax_key_id(mine) - v0) % BM_NT;
+      if (rank == K - 1) s_t = mine;       // else fewer than K threads have any: all that is above -inf
+    }
+  }
+  if (tid == 0) {
+    float M = s_m[0];
+    for (int w = 1; w < 8; ++w) M = fmaxf(M, s_m[w]);
+    float S = 0.f;
+    for (int w = 0; w < 8; ++w) S += s_m[w] > -INFINITY ? s_s[w] * exp_of(s_m[w] - M) : s_s[w];
+    p.stat[(size_t)row * p.parts + blockIdx.x] = make_float2(M, S);
+  }
+  __syncthreads();
+  // ---- the logits of those threads, again
+  const unsigned long long T = s_t;
+  const int steps = (v1 - v0 + BM_NT - 1) / BM_NT;
+  for (int y = tid; y < K * steps; y += BM_NT) {
+    const int th = s_thread[y / steps], v = v0 + (y - y / steps * steps) * BM_NT + th;
+    if (th < 0 || v >= v1) continue;
+    const float f = __ldg(z + v);
+    if (!(f > -INFINITY)) continue;
+    const unsigned long long mine = argmax_key(f, v);
+    if (mine >= T) s_list[atomicAdd(&s_n, 1)] = mine;
+  }
+  __syncthreads();
+  const int n = s_n;
+  unsigned long long* out = p.cand + ((size_t)row * p.parts + blockIdx.x) * K;
+  for (int y = tid; y < n; y += BM_NT) {
+    const unsigned long long mine = s_list[y];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += s_list[j] > mine;
+    if (rank < K) out[rank] = mine;
+  }
+  if (tid >= n && tid < K) out[tid] = 0ull;
+}
+
+// Whole numbers that order like doubles (NaN does not occur).
+__device__ __forceinline__ unsigned long long f64_order(double d) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(d == 0.0 ? 0.0 : d);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double order_f64(unsigned long long u) {
+  return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
+}
+
+__global__ void __launch_bounds__(BM_NT) merge_kernel(const BeamP p) {
+  extern __shared__ unsigned long long sm[];               // the parts' candidates [beams][parts * K]
+  __shared__ unsigned long long s_c[BM_BEAMS * BM_K];      // a beam's K best: order of the score, 0: none
+  __shared__ int s_v[BM_BEAMS * BM_K];                     // and their tokens
+  __shared__ double s_lse[BM_BEAMS];
+  __shared__ int s_top[2 * BM_BEAMS];                      // the best of all: places in s_c
+  __shared__ int s_par[BM_BEAMS], s_tok[BM_BEAMS], s_dpar[BM_BEAMS], s_dplace[BM_BEAMS], s_ends;
+  const ws_beam_args& a = p.a;
+  const int tid = threadIdx.x, i = blockIdx.x, B = a.beams, K = B + 1, each = p.parts * K;
+  const bool rest = idle(a, i);
+  const int L = a.tokens ? max(a.length[i], 0) : 0, had = a.n_done ? max(a.n_done[i], 0) : 0;
+  float was = 0.f;
+  if (tid < B) was = a.score[(size_t)i * B + tid];
+  pdl_wait();
+  if (tid < 2 * BM_BEAMS) s_top[tid] = -1;
+  if (tid < BM_BEAMS) { s_par[tid] = tid; s_tok[tid] = -1; }
+  if (tid == 0) s_ends = 0;
+  if (!rest) {
+    for (int x = tid; x < B * each; x += BM_NT) sm[x] = p.cand[(size_t)i * B * each + x];
+    for (int x = tid; x < B * K; x += BM_NT) s_c[x] = 0ull;
+    if (tid < B) {
+      const float2* st = p.stat + ((size_t)i * B + tid) * p.parts;
+      float M = -INFINITY;
+      for (int q = 0; q < p.parts; ++q) M = fmaxf(M, st[q].x);
+      double S = 0.0;
+      for (int q = 0; q < p.parts; ++q)
+        S += (double)(st[q].x > -INFINITY ? st[q].y * exp_of(st[q].x - M) : st[q].y);
+      const double lse = M > -INFINITY ? (double)M + log(S) : NAN;
+      s_lse[tid] = fabsf(was) < INFINITY && fabs(lse) < INFINITY ? (double)was - lse : NAN;
+    }
+    __syncthreads();
+    for (int x = tid; x < B * each; x += BM_NT) {
+      const unsigned long long mine = sm[x];
+      const int b = x / each;
+      const double off = s_lse[b];
+      if (!mine || off != off) continue;
+      int rank = 0;
+      for (int j = b * each; j < (b + 1) * each; ++j) rank += sm[j] > mine;
+      if (rank >= K) continue;
+      // score + (z - lse) is off + z but for a rounding of 2^-53
+      s_c[b * K + rank] = f64_order(off + (double)key_value(mine));
+      s_v[b * K + rank] = argmax_key_id(mine);
+    }
+    __syncthreads();
+    for (int x = tid; x < B * K; x += BM_NT) {
+      const unsigned long long mine = s_c[x];
+      if (!mine) continue;
+      // equal scores: the lower beam, then the lower token (logits apart may come out equal)
+      int rank = 0;
+      for (int j = 0; j < B * K; ++j) {
+        const unsigned long long o = s_c[j];
+        rank += o > mine || (o == mine && (j / K < x / K || (j / K == x / K && s_v[j] < s_v[x])));
+      }
+      if (rank < 2 * B) s_top[rank] = x;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int live = 0, ends = 0;
+      for (int r = 0; r < 2 * B && live < B && s_top[r] >= 0; ++r) {
+        const int x = s_top[r];
+        if (a.eos_id >= 0 && s_v[x] == a.eos_id) {
+          if (a.n_done && had + ends < a.max_done) {
+            s_dpar[ends] = x / K;
+            s_dplace[ends] = had + ends;
+            a.done_score[(size_t)i * a.max_done + had + ends] = (float)order_f64(s_c[x]);
+            if (a.done_length) a.done_length[(size_t)i * a.max_done + had + ends] = L;
+            ++ends;
+          }
+          continue;
+        }
+        s_par[live] = x / K;
+        s_tok[live] = s_v[x];
+        a.score_out[(size_t)i * B + live] = (float)order_f64(s_c[x]);
+        ++live;
+      }
+      for (int b = live; b < B; ++b) a.score_out[(size_t)i * B + b] = -INFINITY;
+      s_ends = ends;
+    }
+  } else if (tid < B) {
+    a.score_out[(size_t)i * B + tid] = was;
+  }
+  __syncthreads();
+  if (tid < B) {
+    a.parent[(size_t)i * B + tid] = s_par[tid];
+    a.token[(size_t)i * B + tid] = s_tok[tid];
+  }
+  const int ends = s_ends;
+  if (tid == 0) {
+    if (a.n_done) a.n_done_out[i] = rest ? a.n_done[i] : had + ends;
+    if (a.tokens) a.length_out[i] = rest ? a.length[i] : L + 1;
+  }
+  if (!a.tokens || (rest && a.tokens == a.tokens_out)) return;
+  // ---- transcripts, a column of all beams per thread
+  const size_t cap = (size_t)a.capacity;
+  const int32_t* src = a.tokens + (size_t)i * B * cap;
+  int32_t* dst = a.tokens_out + (size_t)i * B * cap;
+  const int cols = min(L, a.capacity);
+  for (int t = tid; t < cols; t += BM_NT) {
+    int32_t r[BM_BEAMS];
+#pragma unroll
+    for (int b = 0; b < BM_BEAMS; ++b)
+      if (b < B) r[b] = src[(size_t)s_par[b] * cap + t];
+    if (a.done_tokens)
+      for (int d = 0; d < ends; ++d)
+        a.done_tokens[((size_t)i * a.max_done + s_dplace[d]) * cap + t] = src[(size_t)s_dpar[d] * cap + t];
+#pragma unroll
+    for (int b = 0; b < BM_BEAMS; ++b)
+      if (b < B) dst[(size_t)b * cap + t] = r[b];
+  }
+  if (!rest && tid < B) dst[(size_t)tid * cap + L] = s_tok[tid];
+}
+
+int fail(int code, const char* msg) {
+  ws_set_thread_error(msg);
+  return code;
+}
+
+const char* check_beam(const ws_beam_args* a) {
+  if (!a) return "null arguments";
+  if (a->n < 0) return "n must be >= 0";
+  if (a->beams < 1 || a->beams > BM_BEAMS) return "beams must be 1..16";
+  if (a->vocab < 1 || a->vocab > (1 << 18)) return "vocab must be 1..262144";
+  if ((long long)a->n * a->beams > 65535) return "n * beams must be at most 65535";
+  if (a->eos_id < -1 || a->eos_id >= a->vocab) return "eos_id must be -1..vocab - 1";
+  if (a->max_done < 0) return "max_done must be >= 0";
+  if (a->n == 0) return nullptr;
+  if (!a->logits || !a->score || !a->score_out || !a->parent || !a->token) return "null logits, score, score_out, parent or token";
+  if (reinterpret_cast<uintptr_t>(a->logits) & 3) return "logits must be 4-byte aligned";
+  if (a->ld < a->vocab) return "ld must be >= vocab";
+  if (a->tokens) {
+    if (!a->tokens_out || !a->length || !a->length_out) return "tokens without tokens_out, length or length_out";
+    if (a->capacity < 1) return "capacity must be >= 1";
+  } else if (a->tokens_out || a->length || a->length_out || a->done_tokens || a->done_length) {
+    return "lengths and transcripts need tokens";
+  }
+  if (a->n_done) {
+    if (!a->n_done_out) return "n_done without n_done_out";
+    if (a->max_done > 0 && !a->done_score) return "n_done without done_score";
+  } else if (a->n_done_out || a->done_score || a->done_length || a->done_tokens) {
+    return "finished transcripts need n_done";
+  }
+  return nullptr;
+}
+
+struct Plan { int parts, part; size_t stat, bytes; };
+// Parts enough for four CTAs per SM (a row is read once whatever they are),
+// none longer than the list of its candidates is made for, and none shorter
+// than four logits per thread.
+Plan make_plan(const ws_beam_args& a) {
+  Plan q = {};
+  const long long rows = (long long)a.n * a.beams;
+  const int least = (a.vocab + BM_PART - 1) / BM_PART, most = min(BM_PARTS, (a.vocab + 4 * BM_NT - 1) / (4 * BM_NT));
+  const int want = max(least, min(most, (int)((4ll * 152 + rows - 1) / rows)));
+  q.part = ((a.vocab + want - 1) / want + BM_NT - 1) / BM_NT * BM_NT;
+  q.parts = (a.vocab + q.part - 1) / q.part;
+  q.stat = (size_t)rows * q.parts * (a.beams + 1) * 8;
+  q.bytes = (q.stat + (size_t)rows * q.parts * 8 + 255) / 256 * 256;
+  return q;
+}
+
+}  // namespace
+
+extern "C" size_t ws_beam_select_workspace(const ws_beam_args* args) {
+  return check_beam(args) || args->n == 0 ? 0 : make_plan(*args).bytes;
+}
+
+extern "C" int ws_beam_select(const ws_beam_args* args, void* workspace, size_t workspace_bytes, ws_stream stream) {
+  if (const char* e = check_beam(args)) return fail(WS_EINVAL, e);
+  if (args->n == 0) return WS_OK;
+  const Plan q = make_plan(*args);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)) return fail(WS_EINVAL, "workspace must be 16-byte aligned and not null");
+  if (q.bytes > workspace_bytes) return fail(WS_ENOSPACE, "workspace smaller than ws_beam_select_workspace()");
+  if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
+    return fail(WS_ECUDA, (std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior)).c_str());
+  BeamP p = {};
+  p.a = *args;
+  p.parts = q.parts;
+  p.part = q.part;
+  p.cand = (unsigned long long*)workspace;
+  p.stat = (float2*)((char*)workspace + q.stat);
+  const cudaStream_t s = (cudaStream_t)stream;
+  scan_kernel<<<dim3((unsigned)q.parts, (unsigned)(args->n * args->beams)), BM_NT, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    ws_count_launches(1);
+    const size_t smem = (size_t)args->beams * q.parts * (args->beams + 1) * 8;
+    e = cudaFuncSetAttribute(merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BM_BEAMS * BM_PARTS * BM_K * 8);
+    if (e == cudaSuccess) e = launch_after(merge_kernel, dim3((unsigned)args->n), BM_NT, smem, s, p);
+  }
+  if (e != cudaSuccess) return fail(WS_ECUDA, (std::string("beam selection launch: ") + cudaGetErrorString(e)).c_str());
+  return WS_OK;
+}

@@ -432,13 +432,14 @@ cudaError_t launch_cache_evict(const ws_paged_cache& cache, const ws_evict_args&
 }
 
 extern "C" size_t ws_cache_evict_workspace(const ws_paged_cache* cache, const ws_evict_args* args) {
-  if (check_evict(cache, args) || args->n_req == 0) return 0;
+  if (check_evict(cache, args) || args->n_req == 0 || cache->dtype == WS_E4M3) return 0;
   return evict_bytes(cache, args);
 }
 
 extern "C" int ws_cache_evict(const ws_paged_cache* cache, const ws_evict_args* args, void* workspace,
                               size_t workspace_bytes, ws_stream stream) {
   if (const char* e = check_evict(cache, args)) return paged_fail(WS_EINVAL, e);
+  if (cache->dtype == WS_E4M3) return paged_fail(WS_EUNSUPPORTED, "positions of a cache in 8 bits cannot leave their block's scale");
   if (args->n_req == 0) return WS_OK;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))
     return paged_fail(WS_EINVAL, "workspace must be 16-byte aligned and not null");

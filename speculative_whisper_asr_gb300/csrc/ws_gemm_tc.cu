@@ -721,19 +721,21 @@ bool tc_encode_map(TcMap* m, const void* base, uint64_t rows, uint64_t cols, uin
 
 // Keys or values of a paged cache as a 4-D map {64 dims, tokens, heads,
 // pages} with boxes of box_rows tokens of one head and page, 128-byte
-// swizzle.  Tokens behind the page's end and pages outside the pool read as 0.
+// swizzle (bf16) or 64-byte (8 bits: a row is 64 bytes).  Tokens behind the
+// page's end and pages outside the pool read as 0.
 bool tc_encode_paged(TcMap* m, const void* base, const ws_paged_cache& c, uint32_t box_rows) {
   if (!tc_engine_available()) return false;
   cuuint64_t dims[4] = {WS_DH, (cuuint64_t)c.page_size, (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
+  const bool q8 = c.dtype == WS_E4M3;
   // a dimension of one entry is never stepped through: any valid stride does
-  auto bytes = [](int64_t stride, int64_t n) { return (cuuint64_t)(n > 1 || stride > 0 ? stride * 2 : WS_DH * 2); };
+  auto bytes = [q8](int64_t stride, int64_t n) { return (cuuint64_t)((n > 1 || stride > 0 ? stride : WS_DH) * (q8 ? 1 : 2)); };
   cuuint64_t strides[3] = {bytes(c.token_stride, c.page_size), bytes(c.head_stride, c.n_kv_heads),
                            bytes(c.page_stride, c.n_pages)};
   cuuint32_t box[4] = {WS_DH, box_rows, 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
-  CUresult r = g_encode(reinterpret_cast<CUtensorMap*>(m), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                        const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  CUresult r = g_encode(reinterpret_cast<CUtensorMap*>(m), q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        q8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

@@ -8,17 +8,21 @@
 
 #include "ws_internal.cuh"
 
+// Bytes per element of a cache, and of the rows that go into and come out of it.
+inline int cache_es(const ws_paged_cache& c) { return c.dtype == WS_F32 ? 4 : c.dtype == WS_BF16 ? 2 : 1; }
+inline int row_es(const ws_paged_cache& c) { return c.dtype == WS_F32 ? 4 : 2; }
+
 // Message of a bad cache description, or null.
 inline const char* check_paged_cache(const ws_paged_cache* c) {
   if (!c) return "null cache";
-  if (c->dtype != WS_F32 && c->dtype != WS_BF16) return "dtype must be WS_F32 or WS_BF16";
+  if (c->dtype != WS_F32 && c->dtype != WS_BF16 && c->dtype != WS_E4M3) return "dtype must be WS_F32, WS_BF16 or WS_E4M3";
   if (c->n_kv_heads < 1 || c->n_kv_heads > 65535) return "n_kv_heads must be 1..65535";
   if (c->page_size < 1) return "page_size must be >= 1";
   if (c->n_pages < 1) return "n_pages must be >= 1";
   if (!c->k || !c->v || !c->page_table) return "null keys, values or page table";
   if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15)
     return "keys and values must be 16-byte aligned";
-  const int64_t unit = c->dtype == WS_BF16 ? 8 : 4;
+  const int64_t unit = 16 / cache_es(*c);
   if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->page_stride % unit ||
       c->head_stride % unit || c->token_stride % unit)
     return "cache strides must be multiples of 16 bytes and not negative";
@@ -29,6 +33,14 @@ inline const char* check_paged_cache(const ws_paged_cache* c) {
       (c->n_pages > 1 && c->page_stride < WS_DH))
     return "cache strides must be >= 64 elements";
   if (c->n_slots < 1 || c->table_stride < 1) return "n_slots and table_stride must be >= 1";
+  if (c->dtype == WS_E4M3) {
+    if (!c->k_scale || !c->v_scale) return "null scales";
+    if (c->scale_block < 1 || c->page_size % c->scale_block) return "scale_block must be a divisor of page_size";
+    const int64_t blocks = c->page_size / c->scale_block;
+    if ((c->n_kv_heads > 1 && c->scale_head_stride < blocks) || (c->n_pages > 1 && c->scale_page_stride < blocks) ||
+        c->scale_head_stride < 0 || c->scale_page_stride < 0 || c->scale_head_stride >= most || c->scale_page_stride >= most)
+      return "scale strides must be >= page_size / scale_block";
+  }
   return nullptr;
 }
 
@@ -71,3 +83,10 @@ __device__ __forceinline__ size_t paged_off(const ws_paged_cache& c, int page, i
   return (size_t)page * (size_t)c.page_stride + (size_t)head * (size_t)c.head_stride +
          (size_t)(j % c.page_size) * (size_t)c.token_stride;
 }
+
+// Caches in 8 bits: offset of a block's scale, and the scale that a byte stands for.
+__device__ __forceinline__ size_t scale_off(const ws_paged_cache& c, int page, int head, int j) {
+  return (size_t)page * (size_t)c.scale_page_stride + (size_t)head * (size_t)c.scale_head_stride +
+         (size_t)(j % c.page_size / c.scale_block);
+}
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }

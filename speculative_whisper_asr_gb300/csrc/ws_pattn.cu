@@ -54,30 +54,6 @@ constexpr int sp_cols(int nt) { return nt == 4 ? 512 : 256; }                  /
 constexpr int sp_stash_tiles(int nt) { return sp_cols(nt) / (8 * nt); }        // tiles per warp
 constexpr float SP_HOLD = 8.0f;
 
-__device__ __forceinline__ uint32_t movm(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-// A warp's walk over every step-th tile from t0 on: position of the tile and
-// the page(s) of its keys.
-struct TileWalk {
-  int t, pi, sub, step;
-  __device__ __forceinline__ void start(const TileGeo& g, int t0, int st) {
-    t = t0; step = st;
-    if (g.tpp) { pi = t0 / g.tpp; sub = t0 - pi * g.tpp; }
-  }
-  __device__ __forceinline__ void next(const TileGeo& g) {
-    t += step;
-    if (g.tpp) { sub += step; while (sub >= g.tpp) { sub -= g.tpp; ++pi; } }
-  }
-  // first position of the tile, keys it may hold, and for key j its table entry
-  __device__ __forceinline__ int base(const TileGeo& g, int ps, int tk) const { return g.tpp ? pi * ps + sub * tk : t * tk; }
-  __device__ __forceinline__ int room(const TileGeo& g, int ps, int tk) const { return g.tpp ? min(tk, ps - sub * tk) : tk; }
-  __device__ __forceinline__ int entry(const TileGeo& g, int j) const { return g.tpp ? pi : (t << g.ppt_log) + (j >> g.page_log); }
-};
-
 struct SpMeta { uint32_t valid; int base; };   // keys of a tile that count; its first position
 
 // Query fragments of 8 * NT rows (B operand): rows r0 + 8 nt + lane / 4.
@@ -620,7 +596,7 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
   if (!isfinite(a->scale)) return "scale must be finite";
   if (a->n_req == 0 || a->total_q == 0) return nullptr;
   if (!a->kv_len || !a->cu_q || !a->q || !a->out) return "null kv_len, cu_q, q or out";
-  const int64_t unit = c->dtype == WS_BF16 ? 8 : 4;
+  const int64_t unit = 16 / row_es(*c);
   if ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out)) & 15 || a->q_stride % unit ||
       a->out_stride % unit)
     return "rows of q and out must be 16-byte aligned";
@@ -657,13 +633,25 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
   const long long R = (long long)a.max_q * (a.n_heads / c.n_kv_heads);
   auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += (n + 255) / 256 * 256; return at; };
   auto partials = [&](long long R_) {
-    if (q.nsplit <= 1 && c.dtype == WS_BF16) return;
+    if (q.nsplit <= 1 && c.dtype != WS_F32) return;
     q.parts = true;
     const size_t rows = (size_t)a.n_req * c.n_kv_heads * R_ * q.nsplit;
     q.ml = take(rows * 8);
     q.o = take(rows * WS_DH * 4);
   };
-  if (c.dtype != WS_BF16) {
+  if (c.dtype == WS_E4M3) {
+    q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+    q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
+    const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
+    q.geo = tile_geo(c.page_size, Q8_TK);
+    const int tiles = max(1, tile_count(q.geo, c.page_size, Q8_TK, a.max_kv));
+    const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
+    q.tps = (tiles + want - 1) / want;
+    q.nsplit = (tiles + q.tps - 1) / q.tps;
+    partials(R);
+    return q;
+  }
+  if (c.dtype == WS_F32) {
     q.geo = tile_geo(c.page_size, F32_KEYS);
     // 64 requests x 6 heads over 112-448 positions: 16 rows 62 us as rows, 17
     // rows 73 us in tiles of 32 and 87 in tiles of 64, 48 rows 106 and 90
@@ -789,6 +777,11 @@ cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
   return launch_f32_mass(p, q.rpt, s);
 }
 
+cudaError_t run_8bit(const AttnP& p, const Plan& q, cudaStream_t s) {
+  const cudaError_t e = launch_q8(p, q.nt, s);
+  return e == cudaSuccess && q.parts ? combine<bf16>(p, s) : e;
+}
+
 cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int pad_H, const int32_t* chunk_len,
                 const Plan& q, char* ws, cudaStream_t s) {
   AttnP p = {};
@@ -805,7 +798,7 @@ cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int 
   p.row_tiles = q.row_tiles;
   if (q.fa && args.mass) { p.nl = (float*)(ws + q.nl); p.next_item = (unsigned long long*)(ws + q.next); }
   if (q.parts) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
-  return cache.dtype == WS_BF16 ? run_bf16(p, q, s) : run_f32(p, q, s);
+  return cache.dtype == WS_BF16 ? run_bf16(p, q, s) : cache.dtype == WS_E4M3 ? run_8bit(p, q, s) : run_f32(p, q, s);
 }
 
 }  // namespace
@@ -821,19 +814,22 @@ cudaError_t launch_block_attention(const ws_paged_cache& cache, const ws_attenti
 
 extern "C" size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attention_args* args) {
   if (check_attn(cache, args) || args->n_req == 0 || args->total_q == 0 || args->max_q == 0) return 0;
+  if (cache->dtype == WS_E4M3 && args->mass) return 0;
   return make_plan(*cache, *args).bytes;
 }
 
 extern "C" int ws_paged_attention(const ws_paged_cache* cache, const ws_attention_args* args, void* workspace,
                                   size_t workspace_bytes, ws_stream stream) {
   if (const char* e = check_attn(cache, args)) return paged_fail(WS_EINVAL, e);
+  if (cache->dtype == WS_E4M3 && args->mass)
+    return paged_fail(WS_EUNSUPPORTED, "the weights over a cache in 8 bits are not accumulated: mass must be null");
   if (args->n_req == 0 || args->total_q == 0 || args->max_q == 0) return WS_OK;
   const Plan q = make_plan(*cache, *args);
   if (q.bytes && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)))
     return paged_fail(WS_EINVAL, "workspace must be 16-byte aligned and not null");
   if (q.bytes > workspace_bytes) return paged_fail(WS_ENOSPACE, "workspace smaller than ws_paged_attention_workspace()");
   // key splits, row tiles and the weight passes read q after the first rows are stored
-  const int64_t es = cache->dtype == WS_BF16 ? 2 : 4;
+  const int64_t es = row_es(*cache);
   if (rows_overlap(args->q, args->q_stride * es, args->out, args->out_stride * es, args->total_q,
                    (int64_t)args->n_heads * WS_DH * es))
     return paged_fail(WS_EINVAL, "out must not share elements with q");

@@ -37,6 +37,30 @@ __device__ __forceinline__ int tile_whole(const TileGeo& g, int page_size, int t
   return L / page_size * g.tpp + rest / tk;
 }
 
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// A warp's walk over every step-th tile from t0 on: position of the tile and
+// the page(s) of its keys.
+struct TileWalk {
+  int t, pi, sub, step;
+  __device__ __forceinline__ void start(const TileGeo& g, int t0, int st) {
+    t = t0; step = st;
+    if (g.tpp) { pi = t0 / g.tpp; sub = t0 - pi * g.tpp; }
+  }
+  __device__ __forceinline__ void next(const TileGeo& g) {
+    t += step;
+    if (g.tpp) { sub += step; while (sub >= g.tpp) { sub -= g.tpp; ++pi; } }
+  }
+  // first position of the tile, keys it may hold, and for key j its table entry
+  __device__ __forceinline__ int base(const TileGeo& g, int ps, int tk) const { return g.tpp ? pi * ps + sub * tk : t * tk; }
+  __device__ __forceinline__ int room(const TileGeo& g, int ps, int tk) const { return g.tpp ? min(tk, ps - sub * tk) : tk; }
+  __device__ __forceinline__ int entry(const TileGeo& g, int j) const { return g.tpp ? pi : (t << g.ppt_log) + (j >> g.page_log); }
+};
+
 struct AttnP {
   ws_paged_cache c;
   ws_attention_args a;
@@ -177,3 +201,7 @@ F32Rows f32_rows_plan(long long units, int max_kv, bool mass);
 F32Rows f32_block_plan(int max_kv);                // a context's block: by max_kv (at most 8,192) alone
 cudaError_t launch_f32_rows(const AttnP& p, const F32Rows& f, cudaStream_t s);
 cudaError_t launch_f32_mass(const AttnP& p, int rpt, cudaStream_t s);
+
+// Caches in 8 bits (ws_pattn_q8.cu): row tiles of 8 * nt rows that stream the cache.
+constexpr int Q8_TK = 32;                          // keys per tile
+cudaError_t launch_q8(const AttnP& p, int nt, cudaStream_t s);

@@ -1,0 +1,131 @@
+// Reordering the paged caches of beams by their parents (ws_cache_reorder in
+// include/ws.h).  Full pages change hands in the page table; of the page that
+// is being filled, the parent's tokens are copied.  Parents form no order (two
+// beams may exchange places), and the copy is in place: a thread owns 16
+// bytes of one token for all beams of a request, reads what each beam
+// receives and then writes, so nothing needs a buffer or a second launch.
+#include <string>
+
+#include "ws_paged.cuh"
+
+namespace {
+
+constexpr int RO_NT = 256;
+constexpr int RO_BEAMS = 16;
+
+struct ReorderP {
+  ws_paged_cache c;
+  ws_reorder_args a;
+  int ppr_log;                             // log2 of the 16-byte pieces of a token's keys or values
+};
+
+// NB: beams at most.
+template <int NB>
+__global__ void __launch_bounds__(RO_NT) reorder_kernel(const ReorderP p) {
+  __shared__ int s_page[RO_BEAMS], s_slot[RO_BEAMS], s_par[RO_BEAMS], s_any;
+  const int tid = threadIdx.x, i = blockIdx.z, B = p.a.beams;
+  if (tid == 0) s_any = 0;
+  __syncthreads();
+  // the request's length is its first beam's; a beam of a bad slot stays out of it
+  const int slot0 = p.a.req_ids ? p.a.req_ids[(size_t)i * B] : i * B;
+  const int L = slot0 >= 0 && slot0 < p.c.n_slots ? max(p.a.kv_len[slot0], 0) : 0;
+  const int full = min(L / p.c.page_size, p.c.table_stride), rest = full < p.c.table_stride ? L % p.c.page_size : 0;
+  if (tid < B) {
+    const int slot = p.a.req_ids ? p.a.req_ids[(size_t)i * B + tid] : i * B + tid;
+    const bool ok = slot >= 0 && slot < p.c.n_slots;
+    int par = p.a.parent[(size_t)i * B + tid];
+    if (par < 0 || par >= B) par = tid;
+    s_slot[tid] = ok ? slot : -1;
+    s_page[tid] = ok && rest ? paged_page(p.c, p.c.page_table, p.c.table_stride, slot, full * p.c.page_size) : -1;
+    s_par[tid] = par;
+    if (par != tid) s_any = 1;
+  }
+  __syncthreads();
+  if (!s_any) return;
+  const int rows = 2 * p.c.n_kv_heads;
+  if ((int)blockIdx.y < rows) {
+    const bool v = (int)blockIdx.y >= p.c.n_kv_heads;
+    const int h = v ? blockIdx.y - p.c.n_kv_heads : blockIdx.y;
+    char* base = (char*)(v ? p.c.v : p.c.k);
+    const int es = p.c.dtype == WS_F32 ? 4 : p.c.dtype == WS_BF16 ? 2 : 1;
+    auto moves = [&](int b) { return b < B && s_par[b] != b && s_page[b] >= 0 && s_page[s_par[b]] >= 0; };
+    for (int x = blockIdx.x * RO_NT + tid; x < rest << p.ppr_log; x += gridDim.x * RO_NT) {
+      const size_t in = ((size_t)h * (size_t)p.c.head_stride + (size_t)(x >> p.ppr_log) * (size_t)p.c.token_stride) * es +
+                        (size_t)(x & ((1 << p.ppr_log) - 1)) * 16;
+      uint4 r[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (moves(b)) r[b] = *reinterpret_cast<const uint4*>(base + (size_t)s_page[s_par[b]] * (size_t)p.c.page_stride * es + in);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (moves(b)) *reinterpret_cast<uint4*>(base + (size_t)s_page[b] * (size_t)p.c.page_stride * es + in) = r[b];
+    }
+    if (p.c.dtype != WS_E4M3) return;
+    uint8_t* sc = (v ? p.c.v_scale : p.c.k_scale) + (size_t)h * (size_t)p.c.scale_head_stride;
+    const int blocks = (rest + p.c.scale_block - 1) / p.c.scale_block;
+    for (int x = blockIdx.x * RO_NT + tid; x < blocks; x += gridDim.x * RO_NT) {
+      uint8_t r[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (moves(b)) r[b] = sc[(size_t)s_page[s_par[b]] * (size_t)p.c.scale_page_stride + x];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (moves(b)) sc[(size_t)s_page[b] * (size_t)p.c.scale_page_stride + x] = r[b];
+    }
+    return;
+  }
+  // ---- the page table's rows, as far as pages are full
+  for (int x = blockIdx.x * RO_NT + tid; x < full; x += gridDim.x * RO_NT) {
+    int r[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (b < B && s_slot[s_par[b]] >= 0) r[b] = p.a.page_table[(size_t)s_slot[s_par[b]] * p.c.table_stride + x];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (b < B && s_par[b] != b && s_slot[b] >= 0 && s_slot[s_par[b]] >= 0)
+        p.a.page_table[(size_t)s_slot[b] * p.c.table_stride + x] = r[b];
+  }
+}
+
+const char* check_reorder(const ws_paged_cache* c, const ws_reorder_args* a) {
+  if (const char* e = check_paged_cache(c)) return e;
+  if (!a) return "null arguments";
+  if (a->n_req < 0 || a->n_req > 65535) return "n_req must be 0..65535";
+  if (a->beams < 1 || a->beams > RO_BEAMS) return "beams must be 1..16";
+  if (c->n_kv_heads > 32767) return "n_kv_heads must be at most 32767";
+  if (c->page_size > 1 << 26) return "page_size must be at most 2^26";
+  if (a->n_req == 0) return nullptr;
+  if (!a->kv_len || !a->parent) return "null kv_len or parent";
+  if (a->page_table && a->page_table != c->page_table) return "page_table must be the cache's own, or null";
+  if (!a->req_ids && (long long)a->n_req * a->beams > c->n_slots) return "more beams than slots";
+  return nullptr;
+}
+
+template <int NB>
+void launch(const ReorderP& p, dim3 grid, cudaStream_t s) {
+  reorder_kernel<NB><<<grid, RO_NT, 0, s>>>(p);
+  ws_count_launches(1);
+}
+
+}  // namespace
+
+extern "C" int ws_cache_reorder(const ws_paged_cache* cache, const ws_reorder_args* args, ws_stream stream) {
+  if (const char* e = check_reorder(cache, args)) return paged_fail(WS_EINVAL, e);
+  if (args->n_req == 0 || args->beams == 1) return WS_OK;
+  if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
+    return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
+  ReorderP p = {};
+  p.c = *cache;
+  p.a = *args;
+  p.ppr_log = cache->dtype == WS_F32 ? 4 : cache->dtype == WS_BF16 ? 3 : 2;
+  const long long pieces = (long long)cache->page_size << p.ppr_log;
+  const dim3 grid((unsigned)min(1024ll, (pieces + RO_NT - 1) / RO_NT),
+                  2u * (unsigned)cache->n_kv_heads + (args->page_table ? 1u : 0u), (unsigned)args->n_req);
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (args->beams <= 4) launch<4>(p, grid, s);
+  else if (args->beams <= 8) launch<8>(p, grid, s);
+  else launch<16>(p, grid, s);
+  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess)
+    return paged_fail(WS_ECUDA, std::string("cache reorder launch: ") + cudaGetErrorString(e));
+  return WS_OK;
+}

@@ -591,18 +591,78 @@ def _on(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _head_rows(name, t, dtype, rows, heads, dev):
+    """Pointer and row stride of a tensor [rows, heads, 64] whose heads lie side by side."""
+    s = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(s) != 3 or s[0] != rows or s[1] != heads or s[2] != 64:
+        raise ValueError(f"{name}: a {dtype} tensor [{rows}, {heads}, 64] on cuda:{dev} is needed")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != 64):
+        raise ValueError(f"{name}: heads have to lie side by side")
+    return t.data_ptr(), s0 if rows > 1 else heads * 64
+
+
+class _Scratch:
+    """An operator's scratch on a device, for each stream that calls it.  It grows when a call finds it too small;
+    outgrown scratch is kept: work in flight or a captured graph may still use it."""
+
+    def __init__(self, device):
+        self.device = device
+        self._ws, self._kept = {}, []      # (pointer, bytes) by stream; the tensors behind them
+
+    def run(self, call, size, args, stream):
+        ptr, nbytes = self._ws.get(stream, (0, 0))
+        if nbytes:
+            try:
+                return call(*args, ptr, nbytes, stream)
+            except B.WSError as e:
+                if e.code != B.WS_ENOSPACE:
+                    raise
+        need = size(*args)
+        if need:
+            nbytes = max(need, 2 * nbytes)
+            self._kept.append(torch.empty(nbytes, dtype=torch.uint8, device=self.device))
+            ptr = self._kept[-1].data_ptr()
+            self._ws[stream] = ptr, nbytes
+        return call(*args, ptr, nbytes, stream)
+
+
+class Rotation:
+    """The position rotation of a model: the first `dims` (8 .. 64, a multiple of 8) elements of a head turn in pairs,
+    pair i by base^(-2 i / dims) per position, or by inv_freq[i] (float64 values) where given.  Pairs are adjacent
+    elements (2 i, 2 i + 1), as in the drafter, or, with adjacent=False, (i, i + dims / 2)."""
+
+    def __init__(self, dims: int = 64, base: float = 10000.0, adjacent: bool = True, inv_freq=None, device=None):
+        if dims % 8 or not 8 <= dims <= 64:
+            raise ValueError("dims: a multiple of 8, 8 .. 64, is needed")
+        if inv_freq is None:
+            inv_freq = [base ** (-2.0 * i / dims) for i in range(dims // 2)]
+        inv_freq = [float(f) for f in inv_freq]
+        if len(inv_freq) != dims // 2 or not all(np.isfinite(inv_freq)):
+            raise ValueError(f"inv_freq: {dims // 2} finite values are needed")
+        # turns per position as fractions of 2^64: whole turns do not count
+        turns = [round(f / (2.0 * np.pi) * 2.0 ** 64) % 2 ** 64 for f in inv_freq]
+        self.dims, self.adjacent = dims, adjacent
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        self.turns = torch.as_tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=dev)
+
+
 class PagedCache:
     """A paged key/value cache in the caller's tensors (ws_paged_cache):
     k, v [pages, KV heads, page_size, 64] with any strides that are multiples
     of 16 bytes (the same for both), page_table [slots, pages per slot] int32.
+    A cache in 8 bits (k, v in float8_e4m3fn) has k_scale and v_scale [pages,
+    KV heads, blocks], uint8 or float8_e8m0fnu, blocks dividing page_size; its
+    rows of queries, keys, values and outputs are bf16.
     The object keeps scratch for each stream that called it; graphs captured
     on one stream share it with each other and with calls on that stream, so
     what may run at the same time needs a PagedCache each.  One thread at a
     time calls it."""
 
-    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
-        if k.dtype not in (torch.bfloat16, torch.float32) or k.dim() != 4 or k.shape[3] != 64 or not k.is_cuda:
-            raise ValueError("k: a CUDA tensor [pages, heads, page_size, 64] in bf16 or fp32 is needed")
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, k_scale=None, v_scale=None):
+        if (k.dtype not in (torch.bfloat16, torch.float32, torch.float8_e4m3fn) or k.dim() != 4 or k.shape[3] != 64
+                or not k.is_cuda):
+            raise ValueError("k: a CUDA tensor [pages, heads, page_size, 64] in bf16, fp32 or float8_e4m3fn is needed")
         if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
             raise ValueError("v must have the type, shape, strides and device of k")
         if k.stride(3) != 1:
@@ -610,33 +670,81 @@ class PagedCache:
         if (page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.device != k.device
                 or not page_table.is_contiguous()):
             raise ValueError("page_table: a contiguous int32 tensor [slots, pages] on k's device is needed")
-        self.k, self.v, self.page_table = k, v, page_table
-        self.dev, self.dtype = k.get_device(), k.dtype
+        scales = (0, 0, 0, 0, 0)
+        q8 = k.dtype is torch.float8_e4m3fn
+        if q8 != (k_scale is not None) or q8 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to a cache in float8_e4m3fn, both of them")
+        if q8:
+            for t in (k_scale, v_scale):
+                if (t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or t.device != k.device or t.dim() != 3
+                        or t.shape[:2] != k.shape[:2] or t.shape[2] < 1 or k.shape[2] % t.shape[2]
+                        or (t.shape[2] > 1 and t.stride(2) != 1)):
+                    raise ValueError("k_scale and v_scale: uint8 or float8_e8m0fnu tensors [pages, heads, blocks] on k's "
+                                     "device are needed, contiguous blocks, their number a divisor of page_size")
+            if v_scale.shape != k_scale.shape or v_scale.stride() != k_scale.stride():
+                raise ValueError("v_scale must have the shape and strides of k_scale")
+            scales = (k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(0), k_scale.stride(1),
+                      k.shape[2] // k_scale.shape[2])
+        self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
+        self.dev, self.dtype = k.get_device(), torch.bfloat16 if q8 else k.dtype
         self.pages, self.heads, self.page_size, _ = k.shape
         self.slots = page_table.shape[0]
         self.desc = B.PagedCacheDesc(
-            B.WS_BF16 if k.dtype is torch.bfloat16 else B.WS_F32, self.heads, self.page_size, self.pages, k.data_ptr(),
-            v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(), self.slots, page_table.shape[1])
-        self._attn, self._evict = B.AttentionArgs(), B.EvictArgs()
-        self._ws, self._kept = {}, []      # (pointer, bytes) by stream; the tensors behind them
+            B.WS_E4M3 if q8 else B.WS_BF16 if k.dtype is torch.bfloat16 else B.WS_F32, self.heads, self.page_size,
+            self.pages, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(),
+            self.slots, page_table.shape[1], *scales)
+        self._attn, self._evict, self._append, self._reorder = B.AttentionArgs(), B.EvictArgs(), B.AppendArgs(), B.ReorderArgs()
+        self._scratch = _Scratch(k.device)
 
     def _run(self, call, size, args, stream):
-        """The call with this stream's scratch, which grows when the call finds it too small.  Outgrown scratch is kept:
-        work in flight or a captured graph may still use it."""
-        ptr, nbytes = self._ws.get(stream, (0, 0))
-        if nbytes:
-            try:
-                return call(self.desc, args, ptr, nbytes, stream)
-            except B.WSError as e:
-                if e.code != B.WS_ENOSPACE:
-                    raise
-        need = size(self.desc, args)
-        if need:
-            nbytes = max(need, 2 * nbytes)
-            self._kept.append(torch.empty(nbytes, dtype=torch.uint8, device=self.k.device))
-            ptr = self._kept[-1].data_ptr()
-            self._ws[stream] = ptr, nbytes
-        return call(self.desc, args, ptr, nbytes, stream)
+        return self._scratch.run(call, size, (self.desc, args), stream)
+
+    def append(self, k, v, kv_len, cu_q, max_q: int, rotation: Rotation | None = None, pos=None, q=None, q_out=None,
+               req_ids=None):
+        """Append the rows k, v [total_q, KV heads, 64] of chunks to the cache (ws_cache_append): kv_len [slots] int32
+        counts them already; cu_q [requests + 1] int32.  With a rotation, keys and the queries q [total_q, heads, 64]
+        are turned by their place in the cache, or by pos [total_q] int32.  Returns q_out (default: q, in place)."""
+        a, dev = self._append, self.dev
+        rows = k.shape[0]
+        a.k, a.k_stride = _head_rows("k", k, self.dtype, rows, self.heads, dev)
+        a.v, a.v_stride = _head_rows("v", v, self.dtype, rows, self.heads, dev)
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+            a.q = a.q_out = 0
+        else:
+            q_out = q if q_out is None else q_out
+            a.n_heads = heads = q.shape[1]
+            a.q, a.q_stride = _head_rows("q", q, self.dtype, rows, heads, dev)
+            a.q_out, a.q_out_stride = _head_rows("q_out", q_out, self.dtype, rows, heads, dev)
+        n = cu_q.shape[0] - 1
+        a.n_req = n
+        a.req_ids = 0 if req_ids is None else _rows("req_ids", req_ids, _I32, (n,), dev)
+        a.kv_len = _rows("kv_len", kv_len, _I32, (self.slots,), dev)
+        a.cu_q = _rows("cu_q", cu_q, _I32, (n + 1,), dev)
+        a.total_q, a.max_q = rows, max_q
+        if rotation is None:
+            a.turns = 0
+        else:
+            a.rot_dims, a.rot_halves = rotation.dims, 0 if rotation.adjacent else 1
+            a.turns = _rows("rotation", rotation.turns, torch.int64, (rotation.dims // 2,), dev)
+        a.pos = 0 if pos is None else _rows("pos", pos, _I32, (rows,), dev)
+        B.ws_cache_append(self.desc, a, _on(dev))
+        return q_out
+
+    def reorder(self, parent, kv_len, table: bool = True, req_ids=None):
+        """Let each beam go on from its parent's cache (ws_cache_reorder): parent [requests, beams] int32; slots are
+        request * beams + beam, or req_ids [requests, beams] int32; kv_len [slots] int32.  Full pages change hands in
+        page_table, the tokens of the page being filled are copied.  Caches that share a page table take one call
+        each, all but one of them with table=False."""
+        a, dev = self._reorder, self.dev
+        n, beams = parent.shape
+        a.n_req, a.beams = n, beams
+        a.parent = _rows("parent", parent, _I32, (n, beams), dev)
+        a.req_ids = 0 if req_ids is None else _rows("req_ids", req_ids, _I32, (n, beams), dev)
+        a.kv_len = _rows("kv_len", kv_len, _I32, (self.slots,), dev)
+        a.page_table = self.desc.page_table if table else 0
+        B.ws_cache_reorder(self.desc, a, _on(dev))
 
     def attend(self, q, kv_len, cu_q, max_q: int, max_kv: int, causal: bool = True, scale: float = 0.125, out=None,
                lse=None, mass=None, req_ids=None):
@@ -776,3 +884,64 @@ class LogitsRules:
         a.logprob = 0 if logprob is None else _rows("logprob", logprob, _F32, (n, H), dev)
         B.ws_logits_rules(a, _on(dev))
         return out
+
+
+class BeamSearch:
+    """The steps of beam search of a model whose transcripts end with eos_id (-1: none ends) (ws_beam_select).  The
+    object keeps scratch for each stream that called it; graphs captured on one stream share it with each other and
+    with calls on that stream, so what may run at the same time needs a BeamSearch each.  One thread at a time calls
+    it."""
+
+    def __init__(self, eos_id: int = -1):
+        self._args = B.BeamArgs()
+        self._args.eos_id = eos_id
+        self._scratch = {}                 # by device
+
+    def select(self, logits, score, parent, token, score_out=None, tokens=None, length=None, tokens_out=None,
+               length_out=None, n_done=None, n_done_out=None, done_score=None, done_length=None, done_tokens=None):
+        """The next beams from logits [n, beams, vocab] fp32 and score [n, beams] fp32 (a beam at -inf is none):
+        parent, token [n, beams] int32, and the new scores in score_out.  tokens [n, beams, capacity] int32 with
+        length [n] int32: transcripts, reordered and extended into tokens_out and length_out.  n_done [n] int32 with
+        done_score [n, room] fp32, done_length [n, room] and done_tokens [n, room, capacity] int32 (both optional,
+        with tokens): the finished transcripts, counted in n_done_out.  The outs default to in place."""
+        dev = logits.get_device()
+        n, beams, V = logits.shape
+        a = self._args
+        s0, s1, s2 = logits.stride()
+        ld = s1 if beams > 1 else s0 if n > 1 else V
+        if logits.dtype is not _F32 or dev < 0 or (V > 1 and s2 != 1) or (n > 1 and s0 != beams * ld):
+            raise ValueError("logits: an fp32 CUDA tensor [n, beams, vocab] of evenly spaced contiguous rows is needed")
+        a.n, a.beams, a.vocab, a.logits, a.ld = n, beams, V, logits.data_ptr(), ld
+        a.score = _rows("score", score, _F32, (n, beams), dev)
+        a.score_out = a.score if score_out is None else _rows("score_out", score_out, _F32, (n, beams), dev)
+        a.parent = _rows("parent", parent, _I32, (n, beams), dev)
+        a.token = _rows("token", token, _I32, (n, beams), dev)
+        if tokens is None:
+            if not (length is tokens_out is length_out is done_length is done_tokens is None):
+                raise ValueError("lengths and transcripts need tokens")
+            a.tokens = a.tokens_out = a.length = a.length_out = 0
+        else:
+            cap = a.capacity = tokens.shape[2]
+            a.tokens = _rows("tokens", tokens, _I32, (n, beams, cap), dev)
+            a.tokens_out = a.tokens if tokens_out is None else _rows("tokens_out", tokens_out, _I32, (n, beams, cap), dev)
+            a.length = _rows("length", length, _I32, (n,), dev)
+            a.length_out = a.length if length_out is None else _rows("length_out", length_out, _I32, (n,), dev)
+        a.done_length = a.done_tokens = 0
+        if n_done is None:
+            if not (n_done_out is done_score is done_length is done_tokens is None):
+                raise ValueError("finished transcripts need n_done")
+            a.n_done = a.n_done_out = a.done_score = a.max_done = 0
+        else:
+            room = a.max_done = done_score.shape[1]
+            a.n_done = _rows("n_done", n_done, _I32, (n,), dev)
+            a.n_done_out = a.n_done if n_done_out is None else _rows("n_done_out", n_done_out, _I32, (n,), dev)
+            a.done_score = _rows("done_score", done_score, _F32, (n, room), dev)
+            if done_length is not None:
+                a.done_length = _rows("done_length", done_length, _I32, (n, room), dev)
+            if done_tokens is not None:
+                a.done_tokens = _rows("done_tokens", done_tokens, _I32, (n, room, cap), dev)
+        stream = _on(dev)
+        scratch = self._scratch.get(dev)
+        if scratch is None:
+            scratch = self._scratch[dev] = _Scratch(logits.device)
+        scratch.run(B.ws_beam_select, B.ws_beam_select_workspace, (a,), stream)

@@ -1,0 +1,637 @@
+"""The beam-search serving operators on the GPU against their definitions in
+float64: appending to paged caches, attention over caches in 8 bits, beam
+selection, reordering, and a beam search made of them."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from beam_common import (D, E32, Pool, Q8Case, append_rule, beam_rule, check_appended, e4m3_round, needed_exponent,
+                         turned)
+from operator_common import close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def R():
+    import __graft_entry__ as g
+    g.build()
+    from speculative_whisper_asr_gb300 import runtime
+    return runtime
+
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32, "e4m3": torch.float8_e4m3fn}
+
+
+def i32(v):
+    return torch.as_tensor(np.asarray(v, dtype=np.int32), device="cuda")
+
+
+# ------------------------------------------------------------------ append
+def run_append(R, pool, chunks, lens, hq, rotate, dims=64, pos=None, ids=None, slots_len=None, with_q=True,
+               in_place=False, side_by_side=True, seed=0, max_q=None, values=None):
+    """One append checked against the rule."""
+    g = torch.Generator().manual_seed(seed + 7)
+    hkv, rows = pool.hkv, sum(chunks) + 2
+    dt = torch.float32 if pool.dtype is torch.float32 else torch.bfloat16
+    x = torch.randn(rows, hq + 2 * hkv, D, generator=g) * torch.exp2(torch.randint(-3, 4, (rows, 1, 1), generator=g).float())
+    if values is not None:
+        x = values(x)
+    x = x.to(dt).to("cuda")
+    parts = x.split([hq, hkv, hkv], 1)
+    if not side_by_side:
+        parts = [t.contiguous() for t in parts]
+    q, k, v = parts
+    cu = np.concatenate([[0], np.cumsum(chunks)])
+    kv_len = np.asarray(lens if slots_len is None else slots_len)
+    rot = None if rotate == "none" else R.Rotation(dims=dims, adjacent=rotate == "adjacent")
+    inv = None if rotate == "none" else 10000.0 ** (-np.arange(0, dims, 2) / dims)
+    contents, ex, table = pool.read()
+    qd, kd, vd = (t.double().cpu().numpy() for t in (q, k, v))
+    mq = max(chunks) if max_q is None else max_q
+    want, wex, tol, wq, seen = append_rule((contents, ex), table, pool.page, pool.block, kd, vd, kv_len, cu, mq, ids, inv,
+                                           dims, rotate != "halves", pos, qd if with_q else None)
+    q_out = None if not with_q or in_place else torch.full_like(q, 7.0, memory_format=torch.contiguous_format)
+    res = pool.cache(R).append(k, v, i32(kv_len), i32(cu), max_q=mq, rotation=rot, pos=None if pos is None else i32(pos),
+                               q=q if with_q else None, q_out=q_out, req_ids=None if ids is None else i32(ids))
+    torch.cuda.synchronize()
+    got, gex, gtable = pool.read()
+    assert np.array_equal(gtable, table)
+    if ex is not None:
+        assert np.array_equal(gex, wex), f"{int((gex != wex).sum())} scales"
+        check_appended("cache", got, want, tol, True)
+    else:
+        half = 2.0 ** -8 if pool.dtype is torch.bfloat16 else E32
+        same = tol == 0
+        assert np.array_equal(got[same], want[same])
+        assert (np.abs(got - want)[~same] <= (tol + half * np.abs(want))[~same]).all()
+    if with_q:
+        gq = res.double().cpu().numpy()
+        half = 2.0 ** -8 if dt is torch.bfloat16 else E32
+        lim = half * np.abs(wq) + np.abs(qd).max(-1, keepdims=True) * 2.0 ** -21
+        assert (np.abs(gq - wq)[seen] <= lim[seen]).all()
+        untouched = qd if in_place else np.full_like(qd, 7.0)
+        assert np.array_equal(gq[~seen], untouched[~seen])
+    else:
+        assert res is None
+
+
+@pytest.mark.parametrize("dtype,page,block", [("bf16", 64, 0), ("f32", 16, 0), ("bf16", 5, 0), ("e4m3", 64, 16),
+                                              ("e4m3", 64, 64), ("e4m3", 48, 48), ("e4m3", 32, 8), ("e4m3", 7, 7),
+                                              ("e4m3", 12, 4), ("e4m3", 10, 1)])
+@pytest.mark.parametrize("rotate,dims", [("none", 64), ("adjacent", 64), ("halves", 64), ("adjacent", 24), ("halves", 40)])
+@pytest.mark.parametrize("chunks,lens", [([1], [1]), ([1, 1, 1], [64, 33, 100]), ([3, 0, 17, 9], [3, 20, 130, 48])])
+def test_append(R, dtype, page, block, rotate, dims, chunks, lens):
+    pool = Pool(len(chunks), -(-max(lens) // page) + 1, 2, page, DT[dtype], block, seed=page + block)
+    run_append(R, pool, chunks, lens, 4, rotate, dims)
+
+
+@pytest.mark.parametrize("dtype,block", [("bf16", 0), ("f32", 0), ("e4m3", 16)])
+@pytest.mark.parametrize("layout", ["token", "pair"])
+def test_append_layouts(R, dtype, block, layout):
+    pool = Pool(3, 5, 3, 32, DT[dtype], block, layout=layout, seed=3)
+    run_append(R, pool, [5, 40, 1], [70, 99, 128], 6, "halves", in_place=True)
+    run_append(R, pool, [5, 40, 1], [75, 139, 129], 6, "adjacent", with_q=False, side_by_side=False)
+
+
+@pytest.mark.parametrize("block", [80, 130, 192])
+def test_append_blocks_longer_than_a_visit(R, block):
+    pool = Pool(2, 3, 2, block, DT["e4m3"], block, seed=block)
+    run_append(R, pool, [150, block], [200, block], 3, "adjacent")
+    run_append(R, pool, [5, 70], [205, block + 70], 3, "halves")
+
+
+def test_append_many_heads_with_long_blocks(R):
+    pool = Pool(1, 2, 140, 96, DT["e4m3"], 96, seed=4)
+    run_append(R, pool, [100], [150], 140, "adjacent")
+
+
+@pytest.mark.parametrize("dtype,block", [("bf16", 0), ("e4m3", 16)])
+def test_append_positions_of_their_own(R, dtype, block):
+    pool = Pool(2, 4, 2, 32, DT[dtype], block, seed=5)
+    pos = np.array([2 ** 31 - 1 - 5 * j if j % 3 else -j * 1000003 for j in range(5 + 33 + 2)])
+    run_append(R, pool, [5, 33], [17, 90], 4, "adjacent", pos=pos)
+
+
+@pytest.mark.parametrize("dtype,block", [("bf16", 0), ("f32", 0), ("e4m3", 16), ("e4m3", 32)])
+def test_append_slots_and_bounds(R, dtype, block):
+    """Request ids out of order and out of range, chunks cut at max_q, rows before position 0, positions behind the
+    page table, pages that are none."""
+    pool = Pool(4, 3, 2, 32, DT[dtype], block, seed=6)
+    run_append(R, pool, [4, 3, 5, 2], None, 4, "adjacent", ids=[2, -1, 0, 9], slots_len=[40, 50, 60, 70])
+    run_append(R, pool, [9, 9], None, 4, "halves", ids=[3, 1], slots_len=[40, 50, 60, 70], max_q=6)
+    run_append(R, pool, [9, 20], None, 4, "none", ids=[3, 1], slots_len=[1, 13, 1, 4])
+    run_append(R, pool, [50], None, 4, "adjacent", ids=[1], slots_len=[1, 110, 1, 4])
+    pool.table[1, 1] = -1
+    pool.table[2, 0] = pool.k.shape[0]
+    run_append(R, pool, [64, 30], None, 4, "adjacent", ids=[1, 2], slots_len=[1, 90, 40, 4])
+    run_append(R, pool, [3, 3], None, 4, "adjacent", ids=[1, 2], slots_len=[0, 0, -5, 0])
+
+
+def test_append_values_that_are_hard(R):
+    """Zeros, numbers at the border of a scale, tiny and huge numbers, infinities and NaN."""
+    def values(x):
+        x = x.clone()
+        x[0] = 0.0
+        x[1, :, ::3] = 448.0
+        x[2, :, 5] = 448.0 * 1.0078125
+        x[3] *= 2.0 ** -126
+        x[4] *= 2.0 ** 110
+        x[5, :, 9] = math.inf
+        x[6, :, 11] = math.nan
+        x[7] = -math.inf
+        x[8, :, 1::2] = -0.0
+        return x
+    for first in range(0, 9):
+        pool = Pool(1, 4, 2, 16, DT["e4m3"], 8, seed=first)
+        run_append(R, pool, [9], [first + 9], 2, "none", with_q=False, values=values)
+        pool = Pool(1, 18, 2, 1, DT["e4m3"], 1, seed=first)
+        run_append(R, pool, [9], [first + 9], 2, "none", with_q=False, values=values)
+
+
+def test_append_again_and_in_steps(R):
+    """The same call twice leaves the same cache; token by token gives the same scales, and the same values but for
+    those that were rounded twice, below 2^-6 of the last scale."""
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(40, 3, D, generator=g).mul(torch.exp2(torch.arange(40.0) / 5)[:, None, None]).bfloat16().cuda() for _ in range(2))
+    pool, one = (Pool(1, 3, 3, 32, DT["e4m3"], 16, seed=2) for _ in range(2))
+    c = pool.cache(R)
+    c.append(k, v, i32([45]), i32([0, 40]), max_q=40)
+    first = pool.bits()
+    c.append(k, v, i32([45]), i32([0, 40]), max_q=40)
+    assert all(torch.equal(a, b) for a, b in zip(first, pool.bits()))
+    s = one.cache(R)
+    for t in range(40):
+        s.append(k[t: t + 1], v[t: t + 1], i32([6 + t]), i32([0, 1]), max_q=1)
+    (a, ea, _), (b, eb, _) = pool.read(), one.read()
+    assert np.array_equal(ea, eb)
+    differ = np.nan_to_num(a) != np.nan_to_num(b)
+    assert (np.maximum(np.abs(a), np.abs(b))[differ] <= 2.0 ** -6).all()
+    assert (np.abs(a - b)[differ] <= 2.0 ** -9).all()
+
+
+# ------------------------------------------------------------------ attention over 8 bits
+def check_q8(R, cs):
+    (o, l, _), (to, tl, _) = cs.reference()
+    out = torch.full_like(cs.q, 3.0)
+    lse = torch.full(cs.q.shape[:2], 3.0, device="cuda")
+    cs.cache(R).attend(cs.q, cs.kv_len, cs.cu, max_q=cs.max_q, max_kv=cs.max_kv, causal=cs.causal, scale=cs.scale,
+                       out=out, lse=lse, req_ids=cs.req)
+    torch.cuda.synchronize()
+    close("out", out[: cs.rows], o, to)
+    close("lse", lse[: cs.rows], l, tl)
+    assert bool((out[cs.rows:] == 3.0).all()) and bool((lse[cs.rows:] == 3.0).all())
+    return out, lse
+
+
+@pytest.mark.parametrize("page,block", [(64, 64), (64, 16), (16, 16), (8, 8), (48, 48), (128, 32), (100, 25), (7, 7), (40, 1)])
+@pytest.mark.parametrize("chunks,lens,hq,hkv", [([1, 1, 1], [1, 65, 200], 4, 4), ([1, 1], [33, 700], 8, 2),
+                                                ([9, 3, 0, 9], [9, 130, 77, 300], 4, 2), ([20, 33], [20, 97], 2, 1),
+                                                ([130], [260], 2, 2), ([300, 40], [700, 500], 4, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_8bit(R, page, block, chunks, lens, hq, hkv, causal):
+    check_q8(R, Q8Case(chunks, lens, hq, hkv, page, block=block, causal=causal, seed=page + len(chunks)))
+
+
+@pytest.mark.parametrize("chunks", [[1, 1, 1], [9, 4, 9], [50, 70, 3]])
+def test_attend_8bit_layout_ids_scale(R, chunks):
+    check_q8(R, Q8Case(chunks, [90, 10, 200], 6, 3, 32, block=16, layout="token", seed=1, scale=0.3))
+    check_q8(R, Q8Case(chunks, [90, 10, 200], 6, 3, 32, block=16, seed=2, scale=-0.2, req_ids=[4, 7, 0], slots=5))
+    check_q8(R, Q8Case(chunks, [0, 100, 1], 6, 3, 32, block=16, seed=3, scale=0.0, causal=False))
+
+
+@pytest.mark.parametrize("chunks", [[1], [9], [64]])
+def test_attend_8bit_scales_far_apart(R, chunks):
+    """Blocks whose scales differ by up to 2^24, in any order, and queries of very different sizes."""
+    check_q8(R, Q8Case(chunks, [500], 2, 2, 16, block=8, spread=12, seed=9, amp=0.05))
+    cs = Q8Case(chunks, [500], 2, 2, 16, block=8, spread=0, seed=10)
+    cs.q_all[:, :, 3] *= 2.0 ** -60
+    cs.q_all[:, 1] *= 2.0 ** -100
+    check_q8(R, cs)
+
+
+def test_attend_8bit_long(R):
+    """More than 2^31 elements in the pool: the last pages."""
+    pages, hkv, page = 2 ** 31 // (8 * 64 * 64) + 40, 8, 64
+    k, v = (torch.zeros(pages, hkv, page, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    sc = torch.full((2, pages, hkv, 4), 127, dtype=torch.uint8, device="cuda")
+    small = Pool(1, 20, hkv, page, DT["e4m3"], 16, seed=3)
+    last = torch.arange(pages - 20, pages, device="cuda")
+    own = small.table[0].long()
+    k.view(torch.uint8)[last] = small.k.view(torch.uint8)[own]
+    v.view(torch.uint8)[last] = small.v.view(torch.uint8)[own]
+    sc[:, last] = small.scales[:, own]
+    big = R.PagedCache(k, v, last[None].to(torch.int32).contiguous(), k_scale=sc[0], v_scale=sc[1])
+    for rows in (3, 90):
+        q = torch.randn(rows, 16, D, device="cuda").bfloat16() * 0.01
+        a, b = (c.attend(q, i32([1250]), i32([0, rows]), max_q=rows, max_kv=1250) for c in (big, small.cache(R)))
+        assert torch.equal(a, b)
+    rows = torch.randn(40, hkv, D, device="cuda").bfloat16()
+    for c in (big, small.cache(R)):
+        c.append(rows, rows, i32([1260]), i32([0, 40]), max_q=40)
+    torch.cuda.synchronize()
+    assert torch.equal(k.view(torch.uint8)[last], small.k.view(torch.uint8)[own])
+
+
+@pytest.mark.parametrize("c", [1, 5, 40, 100, 300])
+def test_attend_8bit_nan_stays_where_it_is_seen(R, c):
+    """NaN codes of keys and values: the rows that see them, and no others, are NaN."""
+    lens = [c + 70]
+    for which in ("k", "v"):
+        cs = Q8Case([c], lens, 4, 2, 16, block=16, seed=c)
+        clean, _ = check_q8(R, cs)
+        bad = lens[0] - max(1, c // 2)
+        page, t = int(cs.table[0, bad // 16]), bad % 16
+        (cs.k8 if which == "k" else cs.v8).view(torch.uint8)[page, 1, t, 7] = 0xFF
+        out = cs.cache(R).attend(cs.q, cs.kv_len, cs.cu, max_q=c, max_kv=lens[0], causal=True)
+        torch.cuda.synchronize()
+        sees = torch.arange(c, device="cuda") + lens[0] - c >= bad
+        got, was = out[: cs.rows], clean[: cs.rows]
+        if which == "k":
+            assert bool(torch.isnan(got[sees][:, 2:]).all())
+        else:
+            assert bool(torch.isnan(got[sees][:, 2:, 7]).all())
+            rest = [d for d in range(D) if d != 7]
+            assert bool(torch.isfinite(got[sees][:, 2:, rest]).all())
+        assert torch.equal(got[~sees], was[~sees])
+        assert torch.equal(got[sees][:, :2], was[sees][:, :2])
+
+
+def test_attend_8bit_pages_that_are_none(R):
+    cs = Q8Case([1, 9, 60], [90, 100, 120], 4, 2, 16, block=16, seed=5, causal=False)
+    for s in range(3):
+        cs.table[s, 2] = [-1, cs.k.shape[0], -7][s]
+    (o, l, _), (to, tl, _) = cs.reference(bad_pages=(2,))
+    lse = torch.zeros(cs.q.shape[:2], device="cuda")
+    out = cs.cache(R).attend(cs.q, cs.kv_len, cs.cu, max_q=60, max_kv=120, causal=False, lse=lse)
+    torch.cuda.synchronize()
+    close("out", out[: cs.rows], o, to)
+    close("lse", lse[: cs.rows], l, tl)
+
+
+# ------------------------------------------------------------------ beam selection
+def make_beam(n, B, V, cap, room, seed, spread=2.0, ties=False):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn(n, B, V, generator=g) * spread
+    if ties:
+        z = torch.round(z * 2) / 2
+    return dict(logits=z, score=-10 * torch.rand(n, B, generator=g).sort(1)[0],
+                tokens=torch.randint(0, V, (n, B, cap), generator=g, dtype=torch.int32),
+                length=torch.randint(0, cap, (n,), generator=g, dtype=torch.int32),
+                n_done=torch.randint(0, room + 1, (n,), generator=g, dtype=torch.int32))
+
+
+def run_beam(R, x, eos, room, in_place=False, search=None, logits=None):
+    n, B, V = x["logits"].shape
+    cap = x["tokens"].shape[2]
+    want = beam_rule(x["logits"].numpy(), x["score"].numpy(), eos, x["tokens"].numpy(), x["length"].numpy(),
+                     x["n_done"].numpy(), room)
+    d = {k: t.clone().cuda() for k, t in x.items()}
+    z = d["logits"] if logits is None else logits
+    parent, token = (torch.full((n, B), 77, dtype=torch.int32, device="cuda") for _ in range(2))
+    done = dict(done_score=torch.full((n, room), 5.0, device="cuda"), done_length=torch.full((n, room), 5, dtype=torch.int32, device="cuda"),
+                done_tokens=torch.full((n, room, cap), -9, dtype=torch.int32, device="cuda"))
+    outs = {} if in_place else dict(score_out=torch.zeros_like(d["score"]), tokens_out=torch.full_like(d["tokens"], -8),
+                                    length_out=torch.zeros_like(d["length"]), n_done_out=torch.zeros_like(d["n_done"]))
+    before = d["tokens"].cpu().clone() if in_place else torch.full_like(x["tokens"], -8)
+    (search or R.BeamSearch(eos_id=eos)).select(z, d["score"], parent, token, tokens=d["tokens"], length=d["length"],
+                                                n_done=d["n_done"], **outs, **done)
+    torch.cuda.synchronize()
+    got = {k: outs.get(k + "_out", d[k]).cpu().numpy() for k in ("score", "tokens", "length", "n_done")}
+    assert np.array_equal(parent.cpu().numpy(), want["parent"])
+    assert np.array_equal(token.cpu().numpy(), want["token"])
+    # a log-sum-exp: terms good to 2^-21, sums of V terms in a tree; the score's own rounding
+    fin = np.isfinite(want["score"])
+    gs, ws = got["score"], want["score"]
+    assert np.array_equal(fin, np.isfinite(gs)) and np.array_equal(gs[~fin], ws[~fin], equal_nan=True)
+    assert (np.abs(gs[fin] - ws[fin]) <= 2.0 ** -20 + 2 * E32 * np.abs(ws[fin])).all()
+    ds, dl, dtk = (done[k].cpu().numpy() for k in ("done_score", "done_length", "done_tokens"))
+    for i in range(n):
+        L = int(x["length"][i])
+        wide = L if want["idle"][i] else L + 1
+        assert got["length"][i] == wide
+        for b in range(B):
+            assert list(got["tokens"][i, b, :wide]) == want["tokens"][i][b]
+            assert np.array_equal(got["tokens"][i, b, wide:], before[i, b, wide:].numpy())
+        had = int(x["n_done"][i])
+        assert got["n_done"][i] == had + len(want["done"][i])
+        for j in range(room):
+            if had <= j < had + len(want["done"][i]):
+                c, t = want["done"][i][j - had]
+                assert abs(ds[i, j] - c) <= 2.0 ** -20 + 2 * E32 * abs(c) and dl[i, j] == L and list(dtk[i, j, :L]) == t
+                assert (dtk[i, j, L:] == -9).all()
+            else:
+                assert ds[i, j] == 5.0 and dl[i, j] == 5 and (dtk[i, j] == -9).all()
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 100, 1023, 1025, 5000, 51866])
+@pytest.mark.parametrize("B", [1, 2, 5, 16])
+def test_beam(R, V, B):
+    x = make_beam(3, B, V, 12, 4, V + B)
+    run_beam(R, x, min(V - 1, 3), 4)
+    run_beam(R, x, -1, 4, in_place=True)
+
+
+@pytest.mark.parametrize("B", [1, 5, 12])
+def test_beam_ties(R, B):
+    """Logits of few different values, beams that are equal, and rows that are all alike: the lower beam, then the
+    lower token."""
+    x = make_beam(4, B, 3001, 6, 3, B, ties=True)
+    x["logits"][1] = 0.5
+    x["logits"][2] = x["logits"][2, :1]
+    x["score"][1:3] = -1.0
+    x["logits"][3] = -0.0
+    x["logits"][3, :, 1500:] = 0.0
+    x["n_done"][:] = 0
+    x["length"][:] = 2
+    run_beam(R, x, 0, 3)
+    run_beam(R, x, 2900, 3, in_place=True)
+
+
+@pytest.mark.parametrize("order", ["up", "down", "stride"])
+def test_beam_orders(R, order):
+    """Largest logits side by side, at the end, or all in one thread's reach."""
+    x = make_beam(2, 12, 40000, 6, 3, 1)
+    z = torch.linspace(-9, 9, 40000).expand(2, 12, 40000).clone()
+    if order == "down":
+        z = z.flip(2)
+    if order == "stride":
+        z[:] = -5.0
+        z[:, :, 5::256] = torch.linspace(1, 6, z[:, :, 5::256].shape[2])
+    x["logits"] = z
+    x["n_done"][:] = 0
+    run_beam(R, x, 17, 3)
+
+
+def test_beam_banned_and_broken_rows(R):
+    """Tokens at -inf, beams that are none, rows with NaN, +inf or nothing: they offer no candidates."""
+    x = make_beam(8, 4, 500, 6, 3, 2)
+    z, inf = x["logits"], math.inf
+    z[0, :, 3:] = -inf
+    z[1, 1:, :] = -inf
+    z[2, 0, 17] = math.nan
+    z[3, 2, 400] = inf
+    z[4] = -inf
+    x["score"][5, 1:] = -inf
+    x["score"][6, 0], x["score"][6, 1] = math.nan, inf
+    z[7, :, 1:] = -inf
+    x["n_done"][:] = 0
+    x["length"][:] = 3
+    run_beam(R, x, 1, 3)
+    run_beam(R, x, 0, 3, in_place=True)
+
+
+def test_beam_ends(R):
+    """The end of transcript best in every beam: finished transcripts in order, until there is no room; idle requests."""
+    x = make_beam(6, 5, 900, 6, 3, 3)
+    x["logits"][:, :, 44] = 30.0
+    x["n_done"] = torch.tensor([0, 1, 2, 3, 0, 4], dtype=torch.int32)
+    x["length"] = torch.tensor([0, 5, 3, 3, 6, 2], dtype=torch.int32)
+    run_beam(R, x, 44, 3)
+    run_beam(R, x, 44, 3, in_place=True)
+
+
+def test_beam_views_and_reuse(R):
+    """Logits inside wider rows, not on a 16-byte boundary; one object for calls of several sizes."""
+    s = R.BeamSearch(eos_id=5)
+    for V, off in ((1000, 1), (4097, 2), (777, 3)):
+        x = make_beam(3, 4, V, 8, 3, V)
+        wide = torch.full((3, 4, V + 9), 99.0, device="cuda")
+        wide[:, :, off: off + V] = x["logits"].cuda()
+        run_beam(R, x, 5, 3, search=s, logits=wide[:, :, off: off + V])
+
+
+def test_beam_without_transcripts(R):
+    x = make_beam(3, 4, 1000, 4, 2, 8)
+    want = beam_rule(x["logits"].numpy(), x["score"].numpy(), 7)
+    parent, token = (torch.zeros(3, 4, dtype=torch.int32, device="cuda") for _ in range(2))
+    sc = x["score"].cuda()
+    R.BeamSearch(eos_id=7).select(x["logits"].cuda(), sc, parent, token)
+    torch.cuda.synchronize()
+    assert np.array_equal(parent.cpu().numpy(), want["parent"]) and np.array_equal(token.cpu().numpy(), want["token"])
+    assert np.allclose(sc.cpu().numpy(), want["score"], atol=2.0 ** -20, rtol=2 * E32)
+
+
+# ------------------------------------------------------------------ reorder
+def reorder_rule(pool, parent, kv_len, ids, table=True):
+    x = [t.numpy().copy() for t in pool.bits()]
+    tab = x[-1]
+    for i in range(parent.shape[0]):
+        B = parent.shape[1]
+        slot = [i * B + b if ids is None else ids[i][b] for b in range(B)]
+        ok = [0 <= s < pool.slots for s in slot]
+        L = max(0, kv_len[slot[0]]) if ok[0] else 0
+        full, rest = L // pool.page, L % pool.page
+        par = [p if 0 <= p < B else b for b, p in enumerate(parent[i])]
+        if full >= pool.width:
+            full, rest = pool.width, 0
+        old = [t.copy() for t in x]
+        for b in range(B):
+            if not ok[b] or not ok[par[b]]:
+                continue
+            if rest:
+                to, frm = tab[slot[b], full], old[-1][slot[par[b]], full]
+                if 0 <= to < pool.k.shape[0] and 0 <= frm < pool.k.shape[0]:
+                    for w in (0, 1):
+                        x[w][to, :, :rest] = old[w][frm, :, :rest]
+                        if pool.scales is not None:
+                            nb = -(-rest // pool.block)
+                            x[2][w, to, :, :nb] = old[2][w, frm, :, :nb]
+            if table:
+                tab[slot[b], :full] = old[-1][slot[par[b]], :full]
+    return x
+
+
+@pytest.mark.parametrize("dtype,page,block,layout", [("bf16", 64, 0, "pair"), ("f32", 16, 0, "head"), ("e4m3", 32, 8, "head"),
+                                                     ("e4m3", 64, 64, "token"), ("bf16", 5, 0, "token")])
+@pytest.mark.parametrize("B", [1, 2, 5, 16])
+def test_reorder(R, dtype, page, block, layout, B):
+    g = np.random.default_rng(B)
+    pool = Pool(3 * B, 4, 3, page, DT[dtype], block, layout=layout, seed=B)
+    cache = pool.cache(R)
+    for lens in ([0, 1, page], [page - 1, 2 * page + 1, 3 * page + page // 2], [4 * page, 4 * page + 9, 3 * page]):
+        parent = g.integers(0, B, (3, B))
+        parent[0] = np.roll(np.arange(B), 1)
+        parent[2, 0] = [-1, B, 0][lens[0] % 3]
+        kv = np.repeat(lens, B)
+        for table in (False, True):
+            want = reorder_rule(pool, parent, kv, None, table)
+            cache.reorder(i32(parent), i32(kv), table=table)
+            torch.cuda.synchronize()
+            for a, b in zip(pool.bits(), want):
+                assert np.array_equal(a.numpy(), b)
+
+
+def test_reorder_ids_and_bad_pages(R):
+    pool = Pool(8, 3, 2, 16, DT["e4m3"], 16, seed=1)
+    cache = pool.cache(R)
+    pool.table[6, 1], pool.table[2, 1] = -1, pool.k.shape[0]
+    ids = [[6, 1, 0], [4, 9, 2], [-1, 3, 5]]
+    parent = np.array([[1, 2, 1], [2, 0, 0], [1, 2, 0]])
+    kv = np.array([20, 20, 25, 30, 25, 30, 20, 3])
+    want = reorder_rule(pool, parent, kv, ids)
+    cache.reorder(i32(parent), i32(kv), req_ids=i32(ids))
+    torch.cuda.synchronize()
+    for a, b in zip(pool.bits(), want):
+        assert np.array_equal(a.numpy(), b)
+
+
+# ------------------------------------------------------------------ a search made of them
+class Toy:
+    """A one-layer attention model over random weights, in float64 on the host and on the GPU through the operators."""
+
+    def __init__(self, V, hq, hkv, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.V, self.hq, self.hkv = V, hq, hkv
+        self.emb = torch.randn(V, (hq + 2 * hkv) * D, generator=g).bfloat16()
+        self.w = (torch.randn(hq * D, V, generator=g) * 0.25).bfloat16()
+        self.inv = 10000.0 ** (-np.arange(0, D, 2) / D)
+
+
+class HostCache:
+    """A beam's cache in 8 bits as lists: codes' values by position, exponents by block, of keys and of values."""
+
+    def __init__(self, hkv, block):
+        self.hkv, self.block = hkv, block
+        self.x, self.e = [[], []], [[], []]
+
+    def copy(self):
+        c = HostCache(self.hkv, self.block)
+        c.x, c.e = [[r.copy() for r in s] for s in self.x], [[r.copy() for r in s] for s in self.e]
+        return c
+
+    def add(self, k, v):
+        for s, row in enumerate((k, v)):
+            t = len(self.x[s])
+            now = np.array([needed_exponent(np.abs(row[h]).max()) for h in range(self.hkv)])
+            if t % self.block == 0:
+                self.e[s].append(now)
+            else:
+                was = self.e[s][-1]
+                now = np.maximum(was, now)
+                for r in self.x[s][t // self.block * self.block:]:
+                    for h in np.flatnonzero(now > was):
+                        r[h] = e4m3_round(r[h] * 2.0 ** int(was[h] - now[h]))
+                self.e[s][-1] = now
+            self.x[s].append(np.stack([e4m3_round(row[h] * 2.0 ** -int(now[h])) for h in range(self.hkv)]))
+
+    def dense(self, s, h):
+        return np.stack([r[h] * 2.0 ** int(self.e[s][j // self.block][h]) for j, r in enumerate(self.x[s])])
+
+
+def host_logits(toy, cache, tok):
+    """Logits of the token after `tok`, whose keys and values join the cache, and how far they may be off."""
+    hq, hkv, t = toy.hq, toy.hkv, len(cache.x[0])
+    row = toy.emb[tok].double().numpy().reshape(hq + 2 * hkv, D)[None]
+    q = turned(row[:, :hq], [t], toy.inv, D, True)[0]
+    cache.add(turned(row[:, hq: hq + hkv], [t], toy.inv, D, True)[0], row[0, hq + hkv:])
+    q = torch.from_numpy(q).bfloat16().double().numpy()
+    o, size = [], []
+    for u in range(hq):
+        kk, vv = cache.dense(0, u * hkv // hq), cache.dense(1, u * hkv // hq)
+        z = kk @ q[u] / 8.0
+        p = np.exp(z - z.max())
+        p /= p.sum()
+        o.append(p @ vv)
+        # the output's rounding; weights off by 2^-11 and by what a turned query at another bf16 value (2^-8 of it)
+        # moves the scores
+        ds = 2.0 ** -8 * (np.abs(kk) @ np.abs(q[u])).max() / 8.0
+        size.append(2.0 ** -8 * np.abs(o[-1]) + (2.0 ** -10 + 2 * ds) * (p @ np.abs(vv)))
+    w = toy.w.double().numpy()
+    return np.concatenate(o) @ w, np.concatenate(size) @ np.abs(w)
+
+
+class Search:
+    """The search on the GPU: one step is append, attend, logits, select, reorder."""
+
+    def __init__(self, R, toy, start, B, steps, page, block, eos, room):
+        n, hq, hkv, V = len(start), toy.hq, toy.hkv, toy.V
+        width = -(-(steps + 1) // page)
+        self.pool = Pool(n * B, width, hkv, page, DT["e4m3"], block, seed=12)
+        cache, search, rot = self.pool.cache(R), R.BeamSearch(eos_id=eos), R.Rotation()
+        emb, w = toy.emb.cuda(), toy.w.cuda().float()
+        cap = steps + 1
+        self.tokens = torch.zeros(n, B, cap, dtype=torch.int32, device="cuda")
+        self.tokens[:, :, 0] = i32(start)[:, None]
+        self.last = self.tokens[:, :, 0].contiguous()
+        self.length = torch.ones(n, dtype=torch.int32, device="cuda")
+        self.kv_len = torch.zeros(n * B, dtype=torch.int32, device="cuda")
+        cu = torch.arange(n * B + 1, dtype=torch.int32, device="cuda")
+        self.score = torch.full((n, B), -math.inf, device="cuda")
+        self.score[:, 0] = 0.0
+        self.parent, self.token = (torch.zeros(n, B, dtype=torch.int32, device="cuda") for _ in range(2))
+        self.n_done = torch.zeros(n, dtype=torch.int32, device="cuda")
+        self.done = dict(done_score=torch.zeros(n, room, device="cuda"),
+                         done_length=torch.zeros(n, room, dtype=torch.int32, device="cuda"),
+                         done_tokens=torch.zeros(n, room, cap, dtype=torch.int32, device="cuda"))
+        self.z = torch.zeros(n, B, V, device="cuda")
+
+        def step():
+            self.kv_len.add_(1)
+            qkv = emb[self.last.reshape(-1).clamp(min=0)].reshape(n * B, hq + 2 * hkv, D)
+            q, k, v = qkv.split([hq, hkv, hkv], 1)
+            cache.append(k, v, self.kv_len, cu, max_q=1, rotation=rot, q=q)
+            o = cache.attend(q, self.kv_len, cu, max_q=1, max_kv=width * page)
+            self.z.copy_((o.reshape(n * B, -1, 1).float() * w).sum(1).view(n, B, V))
+            search.select(self.z, self.score, self.parent, self.token, tokens=self.tokens, length=self.length,
+                          n_done=self.n_done, **self.done)
+            cache.reorder(self.parent, self.kv_len)
+            self.last.copy_(self.token)
+        self.step = step
+
+    def state(self):
+        return [self.tokens, self.last, self.length, self.kv_len, self.score, self.n_done, self.parent, self.token, self.z,
+                *self.done.values(), self.pool.k.view(torch.uint8), self.pool.v.view(torch.uint8), self.pool.scales,
+                self.pool.table]
+
+
+@pytest.mark.parametrize("B,page,block,hq,hkv", [(3, 8, 4, 4, 2), (5, 16, 16, 2, 2)])
+def test_search(R, B, page, block, hq, hkv):
+    """Every step's logits against the caches as the host reorders them, and its choice against the rule."""
+    toy = Toy(60, hq, hkv, B)
+    start, steps, eos, room = [3, 7, 11], 21, 5, 3
+    gpu = Search(R, toy, start, B, steps, page, block, eos, room)
+    caches = [[HostCache(hkv, block) for _ in range(B)] for _ in start]
+    reordered = 0
+    for _ in range(steps):
+        last, score, tokens, length, n_done = [t.clone().cpu().numpy() for t in (gpu.last, gpu.score, gpu.tokens, gpu.length, gpu.n_done)]
+        gpu.step()
+        torch.cuda.synchronize()
+        z, parent = gpu.z.cpu().numpy(), gpu.parent.cpu().numpy()
+        for i in range(len(start)):
+            for b in range(B):
+                want, tol = host_logits(toy, caches[i][b], max(0, last[i, b]))
+                assert (np.abs(z[i, b] - want) <= tol + 1e-4).all()
+        rule = beam_rule(z, score, eos, tokens, length, n_done, room)
+        assert np.array_equal(parent, rule["parent"]) and np.array_equal(gpu.token.cpu().numpy(), rule["token"])
+        for i in range(len(start)):
+            assert [list(t[: len(rule["tokens"][i][0])]) for t in gpu.tokens[i].cpu().numpy()] == rule["tokens"][i]
+            caches[i] = [caches[i][p].copy() for p in parent[i]]
+        reordered += int((parent != np.arange(B)).sum())
+    assert reordered > 0
+
+
+def test_search_replayed(R):
+    """The step captured into a graph and replayed leaves the same bits as calls."""
+    toy = Toy(60, 4, 2, 3)
+    a, b = (Search(R, toy, [3, 7, 11], 4, 21, 8, 8, 5, 3) for _ in range(2))
+    for _ in range(21):
+        a.step()
+    saved = [t.clone() for t in b.state()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b.step()                                           # scratch comes to be outside the capture
+        for t, x in zip(b.state(), saved):
+            t.copy_(x)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            b.step()
+        for _ in range(21):
+            g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(a.state(), b.state()):
+        assert torch.equal(x, y)
