@@ -10,14 +10,14 @@
 // list in it: T, the K-th best of the threads' best in the order (larger
 // logit, lower token), has K logits at or before it, so each of the K best is
 // in a thread whose best is not behind T, and exactly K threads are such.
-// Their logits (K of the 256th parts, from L2) are read again, those not
+// Their logits (K of the 128th parts, from L2) are read again, those not
 // behind T kept, and ranked by counting.
 //
 // merge_kernel.  One CTA per request: log-sum-exps of the beams (in double:
 // what differs by less than fp32's step from another beam is still told
 // apart), the parts' candidates ranked within their beams, the beams' against
-// each other by whole numbers that order like the doubles, and the walk over
-// the 2 * beams best: candidates that end go to the finished transcripts.
+// each other by whole numbers that order like the doubles, and the 2 * beams
+// best dealt out: candidates that end go to the finished transcripts.
 // Then each thread moves a column of the transcripts for all beams, so the
 // move may be in place.
 #include <string>
@@ -26,11 +26,13 @@
 
 namespace {
 
-constexpr int BM_NT = 256;
+constexpr int BM_NT = 128;                  // threads per part ...
+constexpr int BM_MT = 256;                  // ... and per request
 constexpr int BM_BEAMS = 16;
 constexpr int BM_K = BM_BEAMS + 1;
-constexpr int BM_PART = 16384;             // logits per part, at most
-constexpr int BM_PARTS = 32;               // parts per row, at most
+constexpr int BM_W = BM_NT / 32;
+constexpr int BM_PART = 32768;             // logits per part, at most
+constexpr int BM_PARTS = 32;               // parts per row, at most (a lane each in the merge)
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct BeamP {
@@ -56,12 +58,12 @@ __device__ __forceinline__ bool idle(const ws_beam_args& a, int i) {
 }
 
 __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
-  __shared__ unsigned long long s_key[8 * BM_K];
+  extern __shared__ unsigned long long s_list[];           // [K][steps]
+  __shared__ unsigned long long s_key[BM_W * BM_K];
   __shared__ int s_thread[BM_K];
   __shared__ unsigned long long s_t;
-  __shared__ unsigned long long s_list[BM_K * (BM_PART / BM_NT)];
   __shared__ int s_n;
-  __shared__ float s_m[8], s_s[8];
+  __shared__ float s_m[BM_W], s_s[BM_W];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.y, V = p.a.vocab, K = p.a.beams + 1;
   pdl_trigger();
@@ -106,20 +108,20 @@ __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
   if (tid == 0) { s_n = 0; s_t = 1ull; }
   if (tid < K) s_thread[tid] = -1;
   __syncthreads();
-  if (tid < 8 * K) {
+  if (tid < BM_W * K) {
     const unsigned long long mine = s_key[tid];
     if (mine) {
       int rank = 0;
-      for (int j = 0; j < 8 * K; ++j) rank += s_key[j] > mine;
+      for (int j = 0; j < BM_W * K; ++j) rank += s_key[j] > mine;
       if (rank < K) s_thread[rank] = (argmax_key_id(mine) - v0) % BM_NT;
       if (rank == K - 1) s_t = mine;       // else fewer than K threads have any: all that is above -inf
     }
   }
   if (tid == 0) {
     float M = s_m[0];
-    for (int w = 1; w < 8; ++w) M = fmaxf(M, s_m[w]);
+    for (int w = 1; w < BM_W; ++w) M = fmaxf(M, s_m[w]);
     float S = 0.f;
-    for (int w = 0; w < 8; ++w) S += s_m[w] > -INFINITY ? s_s[w] * exp_of(s_m[w] - M) : s_s[w];
+    for (int w = 0; w < BM_W; ++w) S += s_m[w] > -INFINITY ? s_s[w] * exp_of(s_m[w] - M) : s_s[w];
     p.stat[(size_t)row * p.parts + blockIdx.x] = make_float2(M, S);
   }
   __syncthreads();
@@ -155,51 +157,53 @@ __device__ __forceinline__ double order_f64(unsigned long long u) {
   return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
 }
 
-__global__ void __launch_bounds__(BM_NT) merge_kernel(const BeamP p) {
+__global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
   extern __shared__ unsigned long long sm[];               // the parts' candidates [beams][parts * K]
   __shared__ unsigned long long s_c[BM_BEAMS * BM_K];      // a beam's K best: order of the score, 0: none
   __shared__ int s_v[BM_BEAMS * BM_K];                     // and their tokens
-  __shared__ double s_lse[BM_BEAMS];
   __shared__ int s_top[2 * BM_BEAMS];                      // the best of all: places in s_c
   __shared__ int s_par[BM_BEAMS], s_tok[BM_BEAMS], s_dpar[BM_BEAMS], s_dplace[BM_BEAMS], s_ends;
+  constexpr uint32_t ALL = 0xffffffffu;
   const ws_beam_args& a = p.a;
-  const int tid = threadIdx.x, i = blockIdx.x, B = a.beams, K = B + 1, each = p.parts * K;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i = blockIdx.x, B = a.beams, K = B + 1, each = p.parts * K;
   const bool rest = idle(a, i);
   const int L = a.tokens ? max(a.length[i], 0) : 0, had = a.n_done ? max(a.n_done[i], 0) : 0;
-  float was = 0.f;
-  if (tid < B) was = a.score[(size_t)i * B + tid];
-  pdl_wait();
   if (tid < 2 * BM_BEAMS) s_top[tid] = -1;
   if (tid < BM_BEAMS) { s_par[tid] = tid; s_tok[tid] = -1; }
   if (tid == 0) s_ends = 0;
+  pdl_wait();
+  float kept = 0.f;
+  if (rest && tid < B) kept = a.score[(size_t)i * B + tid];
   if (!rest) {
-    for (int x = tid; x < B * each; x += BM_NT) sm[x] = p.cand[(size_t)i * B * each + x];
-    for (int x = tid; x < B * K; x += BM_NT) s_c[x] = 0ull;
-    if (tid < B) {
-      const float2* st = p.stat + ((size_t)i * B + tid) * p.parts;
-      float M = -INFINITY;
-      for (int q = 0; q < p.parts; ++q) M = fmaxf(M, st[q].x);
-      double S = 0.0;
-      for (int q = 0; q < p.parts; ++q)
-        S += (double)(st[q].x > -INFINITY ? st[q].y * exp_of(st[q].x - M) : st[q].y);
-      const double lse = M > -INFINITY ? (double)M + log(S) : NAN;
-      s_lse[tid] = fabsf(was) < INFINITY && fabs(lse) < INFINITY ? (double)was - lse : NAN;
+    for (int b = warp; b < B; b += BM_MT / 32) {           // a warp per beam, a lane per part
+      unsigned long long* list = sm + b * each;
+      for (int x = lane; x < each; x += 32) list[x] = p.cand[((size_t)i * B + b) * each + x];
+      const float was = a.score[(size_t)i * B + b];
+      const float2 st = lane < p.parts ? p.stat[((size_t)i * B + b) * p.parts + lane] : make_float2(-INFINITY, 0.f);
+      const float M = warp_max(st.x);
+      const float S = warp_sum(st.x > -INFINITY ? st.y * exp_of(st.x - M) : st.y);
+      const double lse = M > -INFINITY ? (double)M + log((double)S) : NAN;
+      const bool live = fabsf(was) < INFINITY && fabs(lse) < INFINITY;
+      __syncwarp();
+      // the parts' lists are in order: their heads are compared K times
+      unsigned long long head = lane < p.parts ? list[lane * K] : 0ull, mine = 0ull;
+      int at = 0;
+      for (int r = 0; r < K; ++r) {
+        const uint32_t hi = __reduce_max_sync(ALL, (uint32_t)(head >> 32));
+        const uint32_t lo = __reduce_max_sync(ALL, (uint32_t)(head >> 32) == hi ? (uint32_t)head : 0u);
+        const unsigned long long best = (unsigned long long)hi << 32 | lo;
+        if (lane == r) mine = best;
+        if (best && head == best) { ++at; head = at < K ? list[lane * K + at] : 0ull; }
+      }
+      if (lane < K) {
+        // score + (z - lse) is (score - lse) + z but for a rounding of 2^-53
+        s_c[b * K + lane] = live && mine ? f64_order(((double)was - lse) + (double)key_value(mine)) : 0ull;
+        s_v[b * K + lane] = argmax_key_id(mine);
+      }
     }
     __syncthreads();
-    for (int x = tid; x < B * each; x += BM_NT) {
-      const unsigned long long mine = sm[x];
-      const int b = x / each;
-      const double off = s_lse[b];
-      if (!mine || off != off) continue;
-      int rank = 0;
-      for (int j = b * each; j < (b + 1) * each; ++j) rank += sm[j] > mine;
-      if (rank >= K) continue;
-      // score + (z - lse) is off + z but for a rounding of 2^-53
-      s_c[b * K + rank] = f64_order(off + (double)key_value(mine));
-      s_v[b * K + rank] = argmax_key_id(mine);
-    }
-    __syncthreads();
-    for (int x = tid; x < B * K; x += BM_NT) {
+    for (int x = tid; x < B * K; x += BM_MT) {
       const unsigned long long mine = s_c[x];
       if (!mine) continue;
       // equal scores: the lower beam, then the lower token (logits apart may come out equal)
@@ -211,30 +215,30 @@ __global__ void __launch_bounds__(BM_NT) merge_kernel(const BeamP p) {
       if (rank < 2 * B) s_top[rank] = x;
     }
     __syncthreads();
-    if (tid == 0) {
-      int live = 0, ends = 0;
-      for (int r = 0; r < 2 * B && live < B && s_top[r] >= 0; ++r) {
-        const int x = s_top[r];
-        if (a.eos_id >= 0 && s_v[x] == a.eos_id) {
-          if (a.n_done && had + ends < a.max_done) {
-            s_dpar[ends] = x / K;
-            s_dplace[ends] = had + ends;
-            a.done_score[(size_t)i * a.max_done + had + ends] = (float)order_f64(s_c[x]);
-            if (a.done_length) a.done_length[(size_t)i * a.max_done + had + ends] = L;
-            ++ends;
-          }
-          continue;
-        }
-        s_par[live] = x / K;
-        s_tok[live] = s_v[x];
-        a.score_out[(size_t)i * B + live] = (float)order_f64(s_c[x]);
-        ++live;
+    if (warp == 0) {                                       // lane = rank: which go on, which end
+      const int x = lane < 2 * B ? s_top[lane] : -1;
+      const bool end = x >= 0 && a.eos_id >= 0 && s_v[x] == a.eos_id;
+      const uint32_t lives = __ballot_sync(ALL, x >= 0 && !end), below = (1u << lane) - 1u;
+      const int before = __popc(lives & below);            // beams found before this candidate
+      const uint32_t endings = __ballot_sync(ALL, end && before < B && a.n_done);
+      const int place = had + __popc(endings & below);
+      const float score = x >= 0 ? (float)order_f64(s_c[x]) : -INFINITY;
+      if (x >= 0 && !end && before < B) {
+        s_par[before] = x / K;
+        s_tok[before] = s_v[x];
+        a.score_out[(size_t)i * B + before] = score;
       }
-      for (int b = live; b < B; ++b) a.score_out[(size_t)i * B + b] = -INFINITY;
-      s_ends = ends;
+      if (((endings >> lane) & 1u) && place < a.max_done) {
+        s_dpar[place - had] = x / K;
+        s_dplace[place - had] = place;
+        a.done_score[(size_t)i * a.max_done + place] = score;
+        if (a.done_length) a.done_length[(size_t)i * a.max_done + place] = L;
+      }
+      if (lane < B && lane >= __popc(lives)) a.score_out[(size_t)i * B + lane] = -INFINITY;
+      if (lane == 0) s_ends = min(__popc(endings), a.n_done ? a.max_done - had : 0);
     }
   } else if (tid < B) {
-    a.score_out[(size_t)i * B + tid] = was;
+    a.score_out[(size_t)i * B + tid] = kept;
   }
   __syncthreads();
   if (tid < B) {
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(BM_NT) merge_kernel(const BeamP p) {
   const int32_t* src = a.tokens + (size_t)i * B * cap;
   int32_t* dst = a.tokens_out + (size_t)i * B * cap;
   const int cols = min(L, a.capacity);
-  for (int t = tid; t < cols; t += BM_NT) {
+  for (int t = tid; t < cols; t += BM_MT) {
     int32_t r[BM_BEAMS];
 #pragma unroll
     for (int b = 0; b < BM_BEAMS; ++b)
@@ -300,14 +304,14 @@ const char* check_beam(const ws_beam_args* a) {
 }
 
 struct Plan { int parts, part; size_t stat, bytes; };
-// Parts enough for four CTAs per SM (a row is read once whatever they are),
-// none longer than the list of its candidates is made for, and none shorter
-// than four logits per thread.
+// Twelve CTAs of 128 threads run on an SM: as many parts as fill that round
+// (a row is read once whatever they are), none longer than 256 logits per
+// thread, and none shorter than four.
 Plan make_plan(const ws_beam_args& a) {
   Plan q = {};
   const long long rows = (long long)a.n * a.beams;
   const int least = (a.vocab + BM_PART - 1) / BM_PART, most = min(BM_PARTS, (a.vocab + 4 * BM_NT - 1) / (4 * BM_NT));
-  const int want = max(least, min(most, (int)((4ll * 152 + rows - 1) / rows)));
+  const int want = max(least, (int)min((long long)most, 12ll * 152 / rows));
   q.part = ((a.vocab + want - 1) / want + BM_NT - 1) / BM_NT * BM_NT;
   q.parts = (a.vocab + q.part - 1) / q.part;
   q.stat = (size_t)rows * q.parts * (a.beams + 1) * 8;
@@ -336,13 +340,14 @@ extern "C" int ws_beam_select(const ws_beam_args* args, void* workspace, size_t 
   p.cand = (unsigned long long*)workspace;
   p.stat = (float2*)((char*)workspace + q.stat);
   const cudaStream_t s = (cudaStream_t)stream;
-  scan_kernel<<<dim3((unsigned)q.parts, (unsigned)(args->n * args->beams)), BM_NT, 0, s>>>(p);
+  const size_t list = (size_t)(args->beams + 1) * (q.part / BM_NT) * 8;      // at most 34 KB
+  scan_kernel<<<dim3((unsigned)q.parts, (unsigned)(args->n * args->beams)), BM_NT, list, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) {
     ws_count_launches(1);
     const size_t smem = (size_t)args->beams * q.parts * (args->beams + 1) * 8;
     e = cudaFuncSetAttribute(merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BM_BEAMS * BM_PARTS * BM_K * 8);
-    if (e == cudaSuccess) e = launch_after(merge_kernel, dim3((unsigned)args->n), BM_NT, smem, s, p);
+    if (e == cudaSuccess) e = launch_after(merge_kernel, dim3((unsigned)args->n), BM_MT, smem, s, p);
   }
   if (e != cudaSuccess) return fail(WS_ECUDA, (std::string("beam selection launch: ") + cudaGetErrorString(e)).c_str());
   return WS_OK;

@@ -639,18 +639,6 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
     q.ml = take(rows * 8);
     q.o = take(rows * WS_DH * 4);
   };
-  if (c.dtype == WS_E4M3) {
-    q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
-    q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
-    const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
-    q.geo = tile_geo(c.page_size, Q8_TK);
-    const int tiles = max(1, tile_count(q.geo, c.page_size, Q8_TK, a.max_kv));
-    const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
-    q.tps = (tiles + want - 1) / want;
-    q.nsplit = (tiles + q.tps - 1) / q.tps;
-    partials(R);
-    return q;
-  }
   if (c.dtype == WS_F32) {
     q.geo = tile_geo(c.page_size, F32_KEYS);
     // 64 requests x 6 heads over 112-448 positions: 16 rows 62 us as rows, 17
@@ -684,7 +672,7 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
   if (R > 40 && G <= FA_ROWS && a.scale > 0.f) {
     q.fa = true;
     q.row_tiles = (a.max_q + FA_ROWS / G - 1) / (FA_ROWS / G);
-    q.geo = tile_geo(c.page_size, FA_KEYS);
+    if (c.dtype != WS_E4M3) q.geo = tile_geo(c.page_size, FA_KEYS);       // 8 bits: any 128 positions
     const int tiles = max(1, tile_count(q.geo, c.page_size, FA_KEYS, a.max_kv));
     const long long units = (long long)a.n_req * c.n_kv_heads * ((q.row_tiles + 1) / 2);
     // One round of CTAs (two per SM with one row tile each, else one), none
@@ -702,6 +690,18 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
       q.nl = take((size_t)a.n_req * c.n_kv_heads * q.row_tiles * FA_ROWS * 4);
       q.next = take(8);
     }
+    return q;
+  }
+  if (c.dtype == WS_E4M3) {
+    q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+    q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
+    const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
+    q.geo = tile_geo(c.page_size, Q8_TK);
+    const int tiles = max(1, tile_count(q.geo, c.page_size, Q8_TK, a.max_kv));
+    const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
+    q.tps = (tiles + want - 1) / want;
+    q.nsplit = (tiles + q.tps - 1) / q.tps;
+    partials(R);
     return q;
   }
   if (a.mass && !a.lse) q.lse = take((size_t)a.total_q * a.n_heads * 4);
@@ -778,7 +778,7 @@ cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
 }
 
 cudaError_t run_8bit(const AttnP& p, const Plan& q, cudaStream_t s) {
-  const cudaError_t e = launch_q8(p, q.nt, s);
+  const cudaError_t e = q.fa ? launch_fa(p, s) : launch_q8(p, q.nt, s);
   return e == cudaSuccess && q.parts ? combine<bf16>(p, s) : e;
 }
 

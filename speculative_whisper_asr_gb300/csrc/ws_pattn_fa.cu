@@ -38,10 +38,13 @@
 namespace {
 
 constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
-template <int W>
+template <int W, bool Q8 = false>
 struct FaShape {                                   // a CTA with W row tiles; 3 - W run on an SM
   static constexpr int STAGES = 2 * W;             // key stages
-  static constexpr int THREADS = 128 + 128 * W;    // K producer, MMA, V producer, V cleaner | softmax A | softmax B
+  static constexpr bool OWN = Q8 && W == 2;        // the converters are warps 4..7 (else 0, 2 and 3)
+  static constexpr int CONV = OWN ? 4 : 3;         // converter warps
+  // K producer, MMA, V producer, V cleaner | converters | softmax A | softmax B
+  static constexpr int THREADS = 128 + 128 * W + (OWN ? 128 : 0);
   static constexpr int SMEM = W * TILE + STAGES * 2 * TILE + 1024;
   static constexpr uint32_t COLS = 256 * W;        // tensor memory
 };
@@ -206,11 +209,61 @@ struct Bars {
       p_full[W], pv_done[W];
 };
 
-template <int W>
-__global__ void __launch_bounds__(FaShape<W>::THREADS, 3 - W)
+// A divisor's quotients: exact for 0 <= x < 2^31.
+struct Div {
+  uint32_t d, m;
+  __device__ __forceinline__ explicit Div(int by) : d((uint32_t)by), m(0xFFFFFFFFu / (uint32_t)by + 1u) {}
+  __device__ __forceinline__ int of(int x) const {
+    if (d == 1u) return x;
+    const uint32_t q = __umulhi((uint32_t)x, m);   // at most one too large
+    return (int)(q * d > (uint32_t)x ? q - 1u : q);
+  }
+};
+
+// Four e4m3 codes times 2^k as bf16 (exact), f = 2^(120 + k) twice: sign, exponent and
+// mantissa are shifted to where bf16 has them, which leaves the value 2^-120
+// times too small (also where the exponent is 0), and multiplied.
+__device__ __forceinline__ uint32_t widen_pair(uint32_t w, uint32_t sel, __nv_bfloat162 f) {
+  const uint32_t x = __byte_perm(w, 0u, sel);      // a code in the high byte of each half
+  const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ __nv_bfloat162 pow2_pair(int k) {       // 2^k, -126 <= k <= 127
+  const uint32_t u = (uint32_t)(k + 127) << 7;
+  const uint32_t two = u | u << 16;
+  return *reinterpret_cast<const __nv_bfloat162*>(&two);
+}
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }   // bit 7 of a byte: NaN
+// 16 codes, with the scale of byte s, into two 16-byte chunks.
+__device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, uint4& hi) {
+  const int k = (int)s - 127;
+  const __nv_bfloat162 f = pow2_pair(120 + min(k, 7));
+  lo = make_uint4(widen_pair(w.x, 0x1404, f), widen_pair(w.x, 0x3424, f), widen_pair(w.y, 0x1404, f), widen_pair(w.y, 0x3424, f));
+  hi = make_uint4(widen_pair(w.z, 0x1404, f), widen_pair(w.z, 0x3424, f), widen_pair(w.w, 0x1404, f), widen_pair(w.w, 0x3424, f));
+  if (k > 7) {                                     // 2^(120 + k) is no bf16 number: in two factors
+    const __nv_bfloat162 g = pow2_pair(k - 7);
+    uint32_t* u[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(u[q]), g);
+      *u[q] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+}
+
+// Q8: a cache in 8 bits.  In place of the copies, converter warps read the
+// codes into registers, a tile ahead, and write bf16 values, scaled, into the
+// stages, rows that do not count as zeros; NaN values that not every row sees
+// are noted and left out at once, so there is nothing to clean.  For W = 2 the
+// converters are a warpgroup of their own, for W = 1 the warps whose copies
+// and cleaning they replace.
+template <int W, bool Q8>
+__global__ void __launch_bounds__(FaShape<W, Q8>::THREADS, 3 - W)
 fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
-  constexpr int NST = FaShape<W>::STAGES, THREADS = FaShape<W>::THREADS;
+  using Shape = FaShape<W, Q8>;
+  constexpr int NST = Shape::STAGES, THREADS = Shape::THREADS;
   constexpr uint32_t TM_S = 0, TM_P = 128 * W, TM_O = 192 * W;   // + 128 w, + 64 w, + 64 w
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) Bars<W> B;
@@ -244,7 +297,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int b = 0; b < NST; ++b) {
-      tc::mbar_init(&B.full[b], 2);
+      tc::mbar_init(&B.full[b], Q8 ? Shape::CONV : 2);
       tc::mbar_init(&B.empty[b], 1);
       tc::mbar_init(&B.raw[b], 1);
     }
@@ -256,11 +309,13 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tc::tmem_alloc(&s_tmem, FaShape<W>::COLS);
+  if (Q8)
+    for (int x = threadIdx.x; x < 3 * WS_DH; x += THREADS) odd.first[0][x] = 0x7FFFFFFF;
+  if (warp == 1) tc::tmem_alloc(&s_tmem, Shape::COLS);
   uint8_t* sQ = sm;
   auto sK = [&](int b) { return sm + W * TILE + b * 2 * TILE; };
   auto sV = [&](int b) { return sm + (W + 1) * TILE + b * 2 * TILE; };
-  if (p.geo.tpp && p.geo.box < FA_KEYS)            // value rows that no copy writes
+  if (!Q8 && p.geo.tpp && p.geo.box < FA_KEYS)     // value rows that no copy writes
     for (int x = threadIdx.x; x < NST * TILE / 16; x += THREADS)
       reinterpret_cast<uint4*>(sV(x / (TILE / 16)))[x % (TILE / 16)] = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -278,9 +333,112 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   // in the epilogue for the rows that see them.
   const int all_see = row_limit(p, r, rho0 / p.G);
   auto direct = [&](const TileInfo& f) { return f.clean && (all_see >= r.L || f.base + FA_KEYS <= all_see); };
+  // Q8: converter number, or -1
+  const int ci = !Q8 ? -1 : Shape::OWN ? (warp >= 4 && warp < 8 ? warp - 4 : -1) : warp == 0 ? 0 : warp == 2 || warp == 3 ? warp - 1 : -1;
+  auto convert = [&]() {
+    constexpr int NC = Shape::CONV, NG = (16 + NC - 1) / NC;       // groups of eight rows; of a warp
+    const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
+    const uint8_t* kp = (const uint8_t*)p.c.k + (size_t)h * (size_t)p.c.head_stride + (lane & 3) * 16;
+    const uint8_t* vp = (const uint8_t*)p.c.v + (size_t)h * (size_t)p.c.head_stride + (lane & 3) * 16;
+    const uint8_t* ksp = p.c.k_scale + (size_t)h * (size_t)p.c.scale_head_stride;
+    const uint8_t* vsp = p.c.v_scale + (size_t)h * (size_t)p.c.scale_head_stride;
+    const Div by_page(p.c.page_size), by_block(p.c.scale_block);
+    uint4 kw[NG], vw[NG];
+    uint32_t ks[NG], vs[NG], have = 0;             // scale bytes; bit q: the row counts
+    int page[NG];
+    auto row = [&](int q) { return 8 * (ci + NC * q) + (lane >> 2); };
+    auto look_up = [&](int j) {                    // the pages of tile j's rows
+#pragma unroll
+      for (int q = 0; q < NG; ++q) {
+        const int pos = (lo + j) * FA_KEYS + row(q);
+        const int e = by_page.of(pos);
+        page[q] = ci + NC * q < 16 && pos < r.L && e < p.c.table_stride ? __ldg(table + e) : -1;
+      }
+    };
+    auto fetch = [&](int j, int q) {
+      const int pos = (lo + j) * FA_KEYS + row(q), tok = pos - by_page.of(pos) * p.c.page_size;
+      kw[q] = vw[q] = make_uint4(0u, 0u, 0u, 0u);
+      ks[q] = vs[q] = 0u;
+      have &= ~(1u << q);
+      if (page[q] >= 0 && page[q] < p.c.n_pages) {
+        const size_t at = (size_t)page[q] * (size_t)p.c.page_stride + (size_t)tok * (size_t)p.c.token_stride;
+        const size_t as = (size_t)page[q] * (size_t)p.c.scale_page_stride + (size_t)by_block.of(tok);
+        kw[q] = __ldg(reinterpret_cast<const uint4*>(kp + at));
+        vw[q] = __ldg(reinterpret_cast<const uint4*>(vp + at));
+        ks[q] = __ldg(ksp + as);
+        vs[q] = __ldg(vsp + as);
+        have |= 1u << q;
+      }
+    };
+    look_up(0);
+#pragma unroll
+    for (int q = 0; q < NG; ++q) fetch(0, q);
+    look_up(1);
+    for (int j = 0; j < nmax; ++j) {
+      const int s = j % NST;
+      if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
+      const int base = (lo + j) * FA_KEYS;
+#pragma unroll
+      for (int q = 0; q < NG; ++q) {
+        if (ci + NC * q >= 16) continue;           // the same in all lanes
+        const int x = row(q);
+        // a bit per row of the group
+        uint32_t m = __ballot_sync(0xffffffffu, (have >> q) & 1u) & 0x11111111u;
+        m = (m | m >> 3) & 0x03030303u;
+        m = (m | m >> 6) & 0x000F000Fu;
+        if (lane == 0) reinterpret_cast<uint8_t*>(meta[s].valid)[ci + NC * q] = (uint8_t)(m | m >> 12);
+        uint4 klo, khi, vlo, vhi;
+        widen16(kw[q], ks[q], klo, khi);
+        widen16(vw[q], vs[q], vlo, vhi);
+        const uint32_t odds = (nan_codes(kw[q].x) | nan_codes(kw[q].y) | nan_codes(kw[q].z) | nan_codes(kw[q].w) |
+                               nan_codes(vw[q].x) | nan_codes(vw[q].y) | nan_codes(vw[q].z) | nan_codes(vw[q].w)) & 0x80808080u;
+        const uint32_t at = (uint32_t)(x * 128 + (((2 * (lane & 3)) ^ (x & 7)) << 4)), at2 = at ^ 16u;
+        *reinterpret_cast<uint4*>(sK(s) + at) = klo;
+        *reinterpret_cast<uint4*>(sK(s) + at2) = khi;
+        *reinterpret_cast<uint4*>(sV(s) + at) = vlo;
+        *reinterpret_cast<uint4*>(sV(s) + at2) = vhi;
+        if (odds) {
+          const bool all = base + x < all_see;     // every row sees it
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t to = (e < 8 ? at : at2) + 2u * (e & 7);
+            const int sh = 8 * (e & 3);
+            const uint32_t kc = (e < 4 ? kw[q].x : e < 8 ? kw[q].y : e < 12 ? kw[q].z : kw[q].w) >> sh;
+            const uint32_t vc = (e < 4 ? vw[q].x : e < 8 ? vw[q].y : e < 12 ? vw[q].z : vw[q].w) >> sh;
+            if ((kc & 0x7Fu) == 0x7Fu) *reinterpret_cast<uint16_t*>(sK(s) + to) = 0x7FFFu;
+            if ((vc & 0x7Fu) == 0x7Fu) {
+              *reinterpret_cast<uint16_t*>(sV(s) + to) = all ? 0x7FFFu : 0u;
+              if (!all) {
+                atomicMin(&odd.first[2][16 * (lane & 3) + e], base + x);
+                odd.any = 1;
+              }
+            }
+          }
+        }
+        if (j + 1 < nmax) fetch(j + 1, q);
+      }
+      if (j + 2 < nmax) look_up(j + 2);
+      if (ci == 0 && lane == 0) meta[s].base = base;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(&B.full[s]);
+    }
+  };
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0 || warp == 2) {
+    if (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else if (Shape::OWN) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (Q8 && warp != 1) {
+    if (warp == 0 && lane == 0) {
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (n[w]) {
+          tc::mbar_expect_tx(&B.q_full[w], (uint32_t)TR * 128u);
+          tma_load_3d(sQ + w * TILE, &mq, &B.q_full[w], 0, h * p.G, r.row0 + pair * W * RB + w * RB);
+        }
+    }
+    __syncwarp();
+    if (!Shape::OWN) convert();
+  } else if (!Q8 && (warp == 0 || warp == 2)) {
     // ---- producers: Q and K, and V.  Two warps, because small pages make
     // many copies of a tile and one warp's copies are issued one by one.
     const bool values = warp == 2;
@@ -325,7 +483,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         if ((raw >> s) & 1u) tc::mbar_wait(&B.raw[s], ~(phase >> s) & 1u);
         else tc::mbar_wait(&B.full[s], (uint32_t)((j / NST) & 1));
       }
-  } else if (warp == 3) {
+  } else if (!Q8 && warp == 3) {
     // ---- cleaner
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
     int page = tile_page(p, table, lo, lane);
@@ -408,11 +566,17 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       }
     __syncwarp();
   }
+  } else if (Shape::OWN && warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    convert();
   } else {
     // ---- softmax: thread = row
-    if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");     // 168 a thread at launch
+    if (Q8) {                                      // 128 a thread at launch: 4 * 128 = 56 + 88 + 2 * 184, or 2 * 128 = 88 + 168
+      if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    } else if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");     // 168 a thread at launch
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");            // 128
-    const int w = (warp >> 2) - 1, quarter = warp & 3, x = quarter * 32 + lane;
+    const int w = (warp >> 2) - (Shape::OWN ? 2 : 1), quarter = warp & 3, x = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tS = tl + TM_S + 128u * w, tP = tl + TM_P + 64u * w, tO = tl + TM_O + 64u * w;
     const int first = rho0 + w * TR, rho = first + x;
@@ -432,7 +596,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int q = 0; q < 8; ++q) tm_ld16(tS + 16 * q, sv + 16 * q);
       const Meta& mt = meta[j % NST];
       const int base = mt.base;
-      const bool dense = mt.full && base + FA_KEYS <= lim_all;
+      const bool all = Q8 ? (mt.valid[0] & mt.valid[1] & mt.valid[2] & mt.valid[3]) == 0xffffffffu : mt.full != 0;
+      const bool dense = all && base + FA_KEYS <= lim_all;
       ld_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -559,7 +724,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   }
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == 1) tc::tmem_dealloc(tmem, FaShape<W>::COLS);
+  if (warp == 1) tc::tmem_dealloc(tmem, Shape::COLS);
 }
 
 // ------------------------------------------------------------------ accumulated weights
@@ -796,11 +961,12 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   if (warp == 1) tc::tmem_dealloc(tmem, 256);
 }
 
-template <int W>
+template <int W, bool Q8>
 cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(fa_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, FaShape<W>::SMEM);
+  using Shape = FaShape<W, Q8>;
+  cudaError_t e = cudaFuncSetAttribute(fa_kernel<W, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::SMEM);
   if (e != cudaSuccess) return e;
-  fa_kernel<W><<<dim3((p.row_tiles + W - 1) / W * p.nsplit, p.c.n_kv_heads, p.a.n_req), FaShape<W>::THREADS, FaShape<W>::SMEM, s>>>(
+  fa_kernel<W, Q8><<<dim3((p.row_tiles + W - 1) / W * p.nsplit, p.c.n_kv_heads, p.a.n_req), Shape::THREADS, Shape::SMEM, s>>>(
       p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
       reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
@@ -811,11 +977,14 @@ cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap
 
 cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
   TcMap mq, mk, mv;
+  const bool q8 = p.c.dtype == WS_E4M3;            // whose keys and values are not copied by map
   if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
-                       (uint32_t)(FA_ROWS / p.G)) ||
-      !tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
+                       (uint32_t)(FA_ROWS / p.G)))
     return cudaErrorInvalidValue;
-  return p.row_tiles == 1 ? run_fa<1>(p, mq, mk, mv, s) : run_fa<2>(p, mq, mk, mv, s);
+  if (q8) return p.row_tiles == 1 ? run_fa<1, true>(p, mq, mq, mq, s) : run_fa<2, true>(p, mq, mq, mq, s);
+  if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
+    return cudaErrorInvalidValue;
+  return p.row_tiles == 1 ? run_fa<1, false>(p, mq, mk, mv, s) : run_fa<2, false>(p, mq, mk, mv, s);
 }
 
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s) {

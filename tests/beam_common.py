@@ -191,7 +191,7 @@ class Q8Case(AttnCase):
     """The bf16 case with its live contents rounded to e4m3 with a scale per block, and the cache in 8 bits that
     stands for the same values; codes that are not live are NaN and scales of blocks without live positions 255."""
 
-    def __init__(self, *a, block=16, spread=3, seed=0, **kw):
+    def __init__(self, *a, block=16, spread=3, tails=0, seed=0, **kw):
         super().__init__(*a, dtype=torch.bfloat16, seed=seed, **kw)
         g = torch.Generator().manual_seed(seed + 1)
         self.block = block
@@ -200,6 +200,8 @@ class Q8Case(AttnCase):
         for w, x in enumerate((self.k, self.v)):
             y = x.float().cpu().reshape(pages, hkv, page // block, block, D)
             y = y * torch.exp2(torch.randint(-spread, spread + 1, y.shape[:3], generator=g).float())[..., None, None]
+            if tails:                      # every exponent and the numbers below the normal ones occur
+                y = y * torch.exp2(-torch.randint(0, tails + 1, y.shape, generator=g).float())
             live = ~torch.isnan(y[..., 0])
             m = torch.nan_to_num(y).abs().amax((3, 4))
             e = torch.tensor([needed_exponent(float(t)) for t in m.reshape(-1)]).reshape(m.shape)

@@ -202,6 +202,27 @@ def test_attend_8bit_layout_ids_scale(R, chunks):
     check_q8(R, Q8Case(chunks, [0, 100, 1], 6, 3, 32, block=16, seed=3, scale=0.0, causal=False))
 
 
+@pytest.mark.parametrize("chunks", [[1], [9], [64], [300]])
+def test_attend_8bit_all_codes(R, chunks):
+    cs = Q8Case(chunks, [500], 2, 2, 32, block=16, tails=16, seed=8)
+    seen = torch.unique(torch.cat([c.view(torch.uint8).reshape(-1) for c in (cs.k8, cs.v8)]))
+    assert len(seen) >= 250
+    check_q8(R, cs)
+
+
+@pytest.mark.parametrize("chunks", [[1], [9], [64], [300]])
+@pytest.mark.parametrize("e", [-40, 9, 30])
+def test_attend_8bit_small_and_large_scales(R, chunks, e):
+    """Values with scales of 2^e and keys with 2^-e."""
+    cs = Q8Case(chunks, [500], 2, 2, 32, block=16, seed=11, amp=1e-3 if e < 0 else 1.5)
+    cs.scales[1] += np.uint8(e % 256)
+    cs.v.mul_(2.0 ** e)
+    if e > 0:
+        cs.scales[0] -= e
+        cs.k.mul_(2.0 ** -e)
+    check_q8(R, cs)
+
+
 @pytest.mark.parametrize("chunks", [[1], [9], [64]])
 def test_attend_8bit_scales_far_apart(R, chunks):
     """Blocks whose scales differ by up to 2^24, in any order, and queries of very different sizes."""
