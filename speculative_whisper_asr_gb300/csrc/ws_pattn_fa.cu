@@ -38,10 +38,13 @@
 namespace {
 
 constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
-template <int W, bool Q8 = false>
+// What the cache holds: bf16; 8 bits whose scales hold for whole groups of 16
+// positions; or 8 bits with other blocks.
+enum { MODE_BF16 = 0, MODE_GROUPS = 1, MODE_ANY = 2 };
+template <int W, int MODE = MODE_BF16>
 struct FaShape {                                   // a CTA with W row tiles; 3 - W run on an SM
   static constexpr int STAGES = 2 * W;             // key stages
-  static constexpr bool OWN = Q8 && W == 2;        // the converters are warps 4..7 (else 0, 2 and 3)
+  static constexpr bool OWN = MODE != MODE_BF16 && W == 2;        // the converters are warps 4..7 (else 0, 2 and 3)
   static constexpr int CONV = OWN ? 4 : 3;         // converter warps
   // K producer, MMA, V producer, V cleaner | converters | softmax A | softmax B
   static constexpr int THREADS = 128 + 128 * W + (OWN ? 128 : 0);
@@ -50,9 +53,15 @@ struct FaShape {                                   // a CTA with W row tiles; 3 
 };
 constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
 constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, 64) | (1u << 16);   // B (V) is N-major
+constexpr uint32_t F16_FOR_BF16 = ~((1u << 7) | (1u << 10));          // descriptors' types of A and B
 constexpr float MOST = 1152921504606846976.0f;     // 2^60: largest sum of a tile's weights before a row's reference moves
+// Weights as fp16 are stored 2^5 times larger, and a tile's sum is at most
+// 2^10, so that they reach from 2^15 down to 2^-24: 2^-29 of the reference's.
+constexpr int RAISE = 5;
+constexpr float MOST_F16 = 1024.0f;
+constexpr int FAINT = -60;                         // log2 of a value scale to the largest, below which fp16 weights are 0
 
-struct Meta { uint32_t valid[4]; int base; int full; };
+struct Meta { uint32_t valid[4]; int base; int full; uint32_t ks[2], vs[2]; };   // ks, vs: scale bytes of the groups of 16
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
@@ -235,7 +244,23 @@ __device__ __forceinline__ __nv_bfloat162 pow2_pair(int k) {       // 2^k, -126 
   return *reinterpret_cast<const __nv_bfloat162*>(&two);
 }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }   // bit 7 of a byte: NaN
-// 16 codes, with the scale of byte s, into two 16-byte chunks.
+// 16 codes as fp16, in two 16-byte chunks.
+__device__ __forceinline__ void halves16(const uint4& w, uint4& lo, uint4& hi) {
+  auto four = [](uint32_t c, uint32_t& a, uint32_t& b) {
+    asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
+        : "=r"(a), "=r"(b) : "r"(c));
+  };
+  four(w.x, lo.x, lo.y);
+  four(w.y, lo.z, lo.w);
+  four(w.z, hi.x, hi.y);
+  four(w.w, hi.z, hi.w);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 16 codes as bf16, with the scale of byte s, in two 16-byte chunks.
 __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, uint4& hi) {
   const int k = (int)s - 127;
   const __nv_bfloat162 f = pow2_pair(120 + min(k, 7));
@@ -252,17 +277,27 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, u
   }
 }
 
-// Q8: a cache in 8 bits.  In place of the copies, converter warps read the
-// codes into registers, a tile ahead, and write bf16 values, scaled, into the
-// stages, rows that do not count as zeros; NaN values that not every row sees
-// are noted and left out at once, so there is nothing to clean.  For W = 2 the
-// converters are a warpgroup of their own, for W = 1 the warps whose copies
-// and cleaning they replace.
-template <int W, bool Q8>
-__global__ void __launch_bounds__(FaShape<W, Q8>::THREADS, 3 - W)
+// A cache in 8 bits: in place of the copies, converter warps read the codes
+// into registers, a tile ahead, and write the stages, rows that do not count
+// as zeros; NaN values that not every row sees are noted and left out at once,
+// so there is nothing to clean.  For W = 2 the converters are a warpgroup of
+// their own, for W = 1 the warps whose copies and cleaning they replace.
+//
+// MODE_GROUPS: the codes become fp16 (one conversion for two) and the scales
+// are left to the softmax, to which a group of 16 keys with one scale costs a
+// few instructions: the keys' is a factor of the scores' scale, the values'
+// an addend of the exponent, 2^(v - E) relative to the largest so far, that
+// the row's sum takes out again.  So weights are fp16, and the reference moves
+// at a tile's sum of 2^10.  Queries become fp16 too, each row with a power of two of its own
+// (ws_pattn_q8.cu).  MODE_ANY: bf16 values with their scales, ten instructions
+// for four codes, which the converters are bound by.
+template <int W, int MODE>
+__global__ void __launch_bounds__(FaShape<W, MODE>::THREADS, 3 - W)
 fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
-  using Shape = FaShape<W, Q8>;
+  using Shape = FaShape<W, MODE>;
+  constexpr bool Q8 = MODE != MODE_BF16, GROUPS = MODE == MODE_GROUPS;
+  constexpr uint32_t ID_S = GROUPS ? IDESC_S & F16_FOR_BF16 : IDESC_S, ID_PV = GROUPS ? IDESC_PV & F16_FOR_BF16 : IDESC_PV;
   constexpr int NST = Shape::STAGES, THREADS = Shape::THREADS;
   constexpr uint32_t TM_S = 0, TM_P = 128 * W, TM_O = 192 * W;   // + 128 w, + 64 w, + 64 w
   extern __shared__ uint8_t dsm[];
@@ -303,7 +338,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     odd.any = 0;
     for (int w = 0; w < W; ++w) {
-      tc::mbar_init(&B.q_full[w], 1); tc::mbar_init(&B.s_full[w], 1); tc::mbar_init(&B.s_free[w], 4);
+      tc::mbar_init(&B.q_full[w], GROUPS ? 4 : 1); tc::mbar_init(&B.s_full[w], 1); tc::mbar_init(&B.s_free[w], 4);
       tc::mbar_init(&B.p_full[w], 4); tc::mbar_init(&B.pv_done[w], 1);
     }
     s_abort = 0;
@@ -388,10 +423,23 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         m = (m | m >> 6) & 0x000F000Fu;
         if (lane == 0) reinterpret_cast<uint8_t*>(meta[s].valid)[ci + NC * q] = (uint8_t)(m | m >> 12);
         uint4 klo, khi, vlo, vhi;
-        widen16(kw[q], ks[q], klo, khi);
-        widen16(vw[q], vs[q], vlo, vhi);
-        const uint32_t odds = (nan_codes(kw[q].x) | nan_codes(kw[q].y) | nan_codes(kw[q].z) | nan_codes(kw[q].w) |
-                               nan_codes(vw[q].x) | nan_codes(vw[q].y) | nan_codes(vw[q].z) | nan_codes(vw[q].w)) & 0x80808080u;
+        uint32_t odds = 0u;                        // NaN that the conversion does not see to
+        if (GROUPS) {
+          if (lane == 0 && ((ci + NC * q) & 1) == 0) {
+            const bool on = (have >> q) & 1u;
+            reinterpret_cast<uint8_t*>(meta[s].ks)[(ci + NC * q) >> 1] = (uint8_t)(on ? ks[q] : 127u);
+            reinterpret_cast<uint8_t*>(meta[s].vs)[(ci + NC * q) >> 1] = (uint8_t)vs[q];
+          }
+          halves16(kw[q], klo, khi);
+          halves16(vw[q], vlo, vhi);
+          if (base + FA_KEYS > all_see)
+            odds = (nan_codes(vw[q].x) | nan_codes(vw[q].y) | nan_codes(vw[q].z) | nan_codes(vw[q].w)) & 0x80808080u;
+        } else {
+          widen16(kw[q], ks[q], klo, khi);
+          widen16(vw[q], vs[q], vlo, vhi);
+          odds = (nan_codes(kw[q].x) | nan_codes(kw[q].y) | nan_codes(kw[q].z) | nan_codes(kw[q].w) |
+                  nan_codes(vw[q].x) | nan_codes(vw[q].y) | nan_codes(vw[q].z) | nan_codes(vw[q].w)) & 0x80808080u;
+        }
         const uint32_t at = (uint32_t)(x * 128 + (((2 * (lane & 3)) ^ (x & 7)) << 4)), at2 = at ^ 16u;
         *reinterpret_cast<uint4*>(sK(s) + at) = klo;
         *reinterpret_cast<uint4*>(sK(s) + at2) = khi;
@@ -428,7 +476,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     else if (Shape::OWN) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (Q8 && warp != 1) {
-    if (warp == 0 && lane == 0) {
+    if (!GROUPS && warp == 0 && lane == 0) {
 #pragma unroll
       for (int w = 0; w < W; ++w)
         if (n[w]) {
@@ -525,7 +573,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         const uint64_t qd = qd0 + (uint64_t)(w * (TILE >> 4)), kd = kd0 + (uint64_t)(s * (2 * TILE >> 4));
 #pragma unroll
         for (int kk = 0; kk < WS_DH / 16; ++kk)
-          tc::umma_bf16(tmem + TM_S + 128u * w, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), IDESC_S, kk ? 1u : 0u);
+          tc::umma_bf16(tmem + TM_S + 128u * w, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), ID_S, kk ? 1u : 0u);
         tc::umma_commit(&B.s_full[w]);
       }
       __syncwarp();
@@ -539,7 +587,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         const uint64_t vd = vd0 + (uint64_t)(s * (2 * TILE >> 4));
 #pragma unroll
         for (int kk = 0; kk < FA_KEYS / 16; ++kk)
-          umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), IDESC_PV,
+          umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), ID_PV,
                   (j | kk) ? 1u : 0u);
         tc::umma_commit(&B.pv_done[w]);
         if (w == W - 1 || j >= n[W - 1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
@@ -583,11 +631,38 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     const bool on = x < TR && rho < R;
     const int t = on ? rho / p.G : 0;
     const int lim = on ? row_limit(p, r, t) : 0, lim_all = first < R ? row_limit(p, r, first / p.G) : 0;
-    const float sl = p.sl;
+    const int nw = n[w];
+    float sl = p.sl;
+    if (GROUPS && nw > 0) {                        // this row's query as fp16, its largest element in 1 .. 2
+      const bf16* q = (const bf16*)p.a.q + (size_t)(r.row0 + t) * p.a.q_stride + (size_t)(h * p.G + (on ? rho - t * p.G : 0)) * WS_DH;
+      uint4 v[8];
+      float most = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        v[c] = on ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          most = fmaxf(most, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
+      }
+      const int e2 = most >= 1.17549435e-38f && most < INFINITY ? min((int)(__float_as_uint(most) >> 23) - 127, 126) : 0;
+      const float f = __uint_as_float((uint32_t)(127 - e2) << 23);
+      sl = fmaxf(sl * __uint_as_float((uint32_t)(127 + e2) << 23), 1e-37f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = pack_f16(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f);
+        *reinterpret_cast<uint4*>(sQ + w * TILE + x * 128 + ((c ^ (x & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(&B.q_full[w]);
+    }
     const float2 sl2 = make_float2(sl, sl);
     float m = -INFINITY, msl = 0.f, l = 0.f;
+    int E = 0;                                     // GROUPS: byte of the largest value scale so far
     bool ok = true;
-    const int nw = n[w];
     for (int j = 0; j < nw; ++j) {
       if (!wait_warp(&B.s_full[w], (uint32_t)(j & 1), abort)) { ok = false; break; }
       tc::tc_fence_after();
@@ -615,8 +690,46 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       }
       // P and O are free once the previous product has finished
       if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
+      // GROUPS: the groups' scale bytes, and the factor of O where a value scale is larger than before
+      const uint32_t gk[2] = {mt.ks[0], mt.ks[1]}, gv[2] = {mt.vs[0], mt.vs[1]};
+      float of = 1.f;
+      if (GROUPS) {
+        const uint32_t m4 = __vmaxu4(gv[0], gv[1]), m2 = __vmaxu4(m4, m4 >> 16);
+        const int now = max(E, (int)max(m2 & 0xFFu, (m2 >> 8) & 0xFFu));
+        of = E - now < -126 ? 0.f : __uint_as_float((uint32_t)(E - now + 127) << 23);
+        E = now;
+      }
+      auto key_scale = [&](int g) { return scale_of((gk[g >> 2] >> (8 * (g & 3))) & 0xFFu); };
       float2 sum2[2];
+      auto weigh_groups = [&]() {
+        float tile = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int g = 2 * q + e;
+            const float slk = fmaxf(sl * key_scale(g), 1.17549435e-38f);
+            const int dv = max((int)((gv[g >> 2] >> (8 * (g & 3))) & 0xFFu) - E, FAINT);
+            const float add = (float)(dv + RAISE) - msl;
+            float2 gs = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float2 y = __ffma2_rn(make_float2(sv[16 * g + 2 * k], sv[16 * g + 2 * k + 1]), make_float2(slk, slk),
+                                    make_float2(add, add));
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              gs = __fadd2_rn(gs, y);
+              u[8 * e + k] = pack_f16(y.x, y.y);
+            }
+            tile = fmaf(gs.x + gs.y, __uint_as_float((uint32_t)(127 - RAISE - dv) << 23), tile);
+          }
+          tm_st16(tP + 16 * q, u);
+        }
+        return tile;
+      };
       auto weigh = [&]() {
+        if (GROUPS) return weigh_groups();
         const float2 nm2 = make_float2(-msl, -msl);
         sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -642,12 +755,18 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       // copy writes (rows TR .. 127), and a row's bits may not depend on them.
       float tile = 0.f;
       if (j > 0) tile = weigh();
-      if (j == 0 || __any_sync(0xffffffffu, on && (m == -INFINITY || !(tile < MOST)))) {
+      constexpr float most = GROUPS ? MOST_F16 : MOST;
+      if (j == 0 || __any_sync(0xffffffffu, (GROUPS && of != 1.f) || (on && (m == -INFINITY || !(tile < most))))) {
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < FA_KEYS; e += 8)
+          if (GROUPS) {
+            const float top = max3(max3(sv[e], sv[e + 1], sv[e + 2]), max3(sv[e + 3], sv[e + 4], sv[e + 5]), fmaxf(sv[e + 6], sv[e + 7]));
+            mx[e / 8 & 3] = fmaxf(mx[e / 8 & 3], top * key_scale(e / 16));
+          } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
+          }
         const float mn = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]));
         const float f = m > -INFINITY ? ex2((m - mn) * sl) : (mn > -INFINITY ? 0.f : 1.f);
         m = mn;
@@ -663,7 +782,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
             tm_ld16(tO + 16 * d, o);
             ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * f);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * (GROUPS ? f * of : f));
             tm_st16(tO + 16 * d, v);
           }
         }
@@ -677,6 +796,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     if (ok && nw > 0) ok = wait_warp(&B.pv_done[w], (uint32_t)((nw - 1) & 1), abort);
     tc::tc_fence_after();
+    const float size = GROUPS ? scale_of((uint32_t)E) * (1.f / (1 << RAISE)) : 1.f;        // of O
     const bool any_odd = nw > 0 && *(volatile int*)&odd.any != 0;
     if (p.nsplit > 1) {
       const size_t at = on ? (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split : 0;
@@ -684,6 +804,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int q = 0; q < 4; ++q) {
         float o[16];
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
+        if (GROUPS)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= size;
         if (any_odd)
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
@@ -702,6 +825,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int q = 0; q < 4; ++q) {
         float o[16];
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
+        if (GROUPS)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= size;
         if (any_odd)
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
@@ -961,30 +1087,34 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   if (warp == 1) tc::tmem_dealloc(tmem, 256);
 }
 
-template <int W, bool Q8>
+template <int W, int MODE>
 cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  using Shape = FaShape<W, Q8>;
-  cudaError_t e = cudaFuncSetAttribute(fa_kernel<W, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::SMEM);
+  using Shape = FaShape<W, MODE>;
+  cudaError_t e = cudaFuncSetAttribute(fa_kernel<W, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::SMEM);
   if (e != cudaSuccess) return e;
-  fa_kernel<W, Q8><<<dim3((p.row_tiles + W - 1) / W * p.nsplit, p.c.n_kv_heads, p.a.n_req), Shape::THREADS, Shape::SMEM, s>>>(
+  fa_kernel<W, MODE><<<dim3((p.row_tiles + W - 1) / W * p.nsplit, p.c.n_kv_heads, p.a.n_req), Shape::THREADS, Shape::SMEM, s>>>(
       p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
       reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
   return cudaGetLastError();
+}
+template <int MODE>
+cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
+  return p.row_tiles == 1 ? run_fa<1, MODE>(p, mq, mk, mv, s) : run_fa<2, MODE>(p, mq, mk, mv, s);
 }
 
 }  // namespace
 
 cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
   TcMap mq, mk, mv;
-  const bool q8 = p.c.dtype == WS_E4M3;            // whose keys and values are not copied by map
   if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
                        (uint32_t)(FA_ROWS / p.G)))
     return cudaErrorInvalidValue;
-  if (q8) return p.row_tiles == 1 ? run_fa<1, true>(p, mq, mq, mq, s) : run_fa<2, true>(p, mq, mq, mq, s);
+  if (p.c.dtype == WS_E4M3)                        // whose keys and values are not copied by map
+    return p.c.scale_block % 16 == 0 ? run_fa<MODE_GROUPS>(p, mq, mq, mq, s) : run_fa<MODE_ANY>(p, mq, mq, mq, s);
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
     return cudaErrorInvalidValue;
-  return p.row_tiles == 1 ? run_fa<1, false>(p, mq, mk, mv, s) : run_fa<2, false>(p, mq, mk, mv, s);
+  return run_fa<MODE_BF16>(p, mq, mk, mv, s);
 }
 
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s) {

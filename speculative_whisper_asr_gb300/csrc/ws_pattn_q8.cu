@@ -19,9 +19,9 @@
 // Scales never touch an element: a key's multiplies its scores (fp32), a
 // value's its weight.  Weights enter the product as fp16, 2^-11 of each at
 // most, an eighth of the bf16 output's own step, relative to 2^E, the largest
-// value scale so far, so that they stay within fp16 whatever the scales are
-// (weights are at most 2^8 there; one that falls below 2^-14 is rounded to
-// fp16's steps below its normal numbers, 2^-24).  Queries, 8 bits each, are
+// value scale so far, so that they stay within fp16 whatever the scales are.
+// They are at most 2^8 and stored 2^7 times larger, so that fp16's last step is
+// 2^-31 of a row's largest weight times the largest value scale.  Queries, 8 bits each, are
 // exact in fp16 once a row's largest is brought to 1 .. 2 by a power of two,
 // which joins the row's scale; elements below 2^-17 of the largest round to
 // 2^-25 of it, the step of the fp32 sums.
@@ -37,6 +37,7 @@ constexpr int NS = 4;                      // ring slots per warp
 constexpr int TB = TK * WS_DH;             // bytes of a K or V tile
 constexpr int OP = WS_DH + 4;              // row pitch of the CTA's merge area, which reuses the rings
 constexpr float HOLD = 8.0f;               // log2 of the largest weight before a row's reference moves
+constexpr float RAISE = 128.0f;            // weights are stored this much larger
 constexpr int q8_smem(int nt) {
   const int ring = W * NS * 2 * TB, merge = W * 8 * nt * (OP + 2) * 4;
   return (ring > merge ? ring : merge) + 1024;
@@ -368,7 +369,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
-        const float f = down(vs[mt][e2] - E);
+        const float f = down(vs[mt][e2] - E) * RAISE;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float p0 = ex2(fmaf(sc[mt][nt][2 * e2], sl[nt][0], -msl[nt][0]));
@@ -415,7 +416,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
   __syncthreads();
   float* so = reinterpret_cast<float*>(sm);                // [warp][8 NT][OP]
   float* sml = so + W * 8 * NT * OP;                       // [warp][8 NT][2]: reference in log2 units, sum
-  const float size = scale_of((uint32_t)E);
+  const float size = scale_of((uint32_t)E) * (1.0f / RAISE);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
