@@ -672,7 +672,7 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
   if (R > 40 && G <= FA_ROWS && a.scale > 0.f) {
     q.fa = true;
     q.row_tiles = (a.max_q + FA_ROWS / G - 1) / (FA_ROWS / G);
-    if (c.dtype != WS_E4M3) q.geo = tile_geo(c.page_size, FA_KEYS);       // 8 bits: any 128 positions
+    q.geo = tile_geo(c.page_size, FA_KEYS);
     const int tiles = max(1, tile_count(q.geo, c.page_size, FA_KEYS, a.max_kv));
     const long long units = (long long)a.n_req * c.n_kv_heads * ((q.row_tiles + 1) / 2);
     // One round of CTAs (two per SM with one row tile each, else one), none

@@ -44,11 +44,12 @@ enum { MODE_BF16 = 0, MODE_GROUPS = 1, MODE_ANY = 2 };
 template <int W, int MODE = MODE_BF16>
 struct FaShape {                                   // a CTA with W row tiles; 3 - W run on an SM
   static constexpr int STAGES = 2 * W;             // key stages
-  static constexpr bool OWN = MODE != MODE_BF16 && W == 2;        // the converters are warps 4..7 (else 0, 2 and 3)
-  static constexpr int CONV = OWN ? 4 : 3;         // converter warps
+  static constexpr bool OWN = MODE != MODE_BF16 && W == 2;        // the converters are warps 4..7 (else 2 and 3)
+  static constexpr int CONV = OWN ? 4 : 2;         // converter warps
   // K producer, MMA, V producer, V cleaner | converters | softmax A | softmax B
   static constexpr int THREADS = 128 + 128 * W + (OWN ? 128 : 0);
-  static constexpr int SMEM = W * TILE + STAGES * 2 * TILE + 1024;
+  static constexpr int AHEAD = OWN ? 3 : 1;        // 8 bits: tiles of codes in shared memory, TILE bytes each
+  static constexpr int SMEM = W * TILE + STAGES * 2 * TILE + (MODE == MODE_BF16 ? 0 : AHEAD * TILE) + 1024;
   static constexpr uint32_t COLS = 256 * W;        // tensor memory
 };
 constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
@@ -214,19 +215,8 @@ __device__ __forceinline__ int longest_first(const AttnP& p, int z) {
 
 template <int W>
 struct Bars {
-  uint64_t q_full[W], full[FaShape<W>::STAGES], empty[FaShape<W>::STAGES], raw[FaShape<W>::STAGES], s_full[W], s_free[W],
+  uint64_t q_full[W], full[FaShape<W>::STAGES], empty[FaShape<W>::STAGES], raw[FaShape<W>::STAGES], raw_free[FaShape<W>::STAGES], s_full[W], s_free[W],
       p_full[W], pv_done[W];
-};
-
-// A divisor's quotients: exact for 0 <= x < 2^31.
-struct Div {
-  uint32_t d, m;
-  __device__ __forceinline__ explicit Div(int by) : d((uint32_t)by), m(0xFFFFFFFFu / (uint32_t)by + 1u) {}
-  __device__ __forceinline__ int of(int x) const {
-    if (d == 1u) return x;
-    const uint32_t q = __umulhi((uint32_t)x, m);   // at most one too large
-    return (int)(q * d > (uint32_t)x ? q - 1u : q);
-  }
 };
 
 // Four e4m3 codes times 2^k as bf16 (exact), f = 2^(120 + k) twice: sign, exponent and
@@ -277,11 +267,13 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, u
   }
 }
 
-// A cache in 8 bits: in place of the copies, converter warps read the codes
-// into registers, a tile ahead, and write the stages, rows that do not count
-// as zeros; NaN values that not every row sees are noted and left out at once,
-// so there is nothing to clean.  For W = 2 the converters are a warpgroup of
-// their own, for W = 1 the warps whose copies and cleaning they replace.
+// A cache in 8 bits: warp 0 copies codes and scales, AHEAD tiles at once, and
+// converter warps write the stages from them, rows that do not count as zeros;
+// NaN values that not every row sees are noted and left out at once, so there
+// is nothing to clean.  For W = 2 the converters are a warpgroup of their own.
+// (Codes loaded into the converters' registers, or by copies of their own, cost
+// a memory latency per tile: a warp's fence before its stores may be read
+// waits for whatever it has asked for; 4 x 2048 rows 368 and 590 us.)
 //
 // MODE_GROUPS: the codes become fp16 (one conversion for two) and the scales
 // are left to the softmax, to which a group of 16 keys with one scale costs a
@@ -306,6 +298,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   __shared__ Odd odd;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  constexpr int AHEAD = Shape::AHEAD;
+  __shared__ uint16_t s_scale[Q8 ? AHEAD : 1][GROUPS ? 8 : FA_KEYS];       // scale bytes of the rows (groups), key's and value's << 8
+  __shared__ Meta raw_meta[Q8 ? AHEAD : 1];        // of the codes
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   if (p.next_item && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next_item = 0ull;
   const int groups = (p.row_tiles + W - 1) / W;
@@ -334,7 +329,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     for (int b = 0; b < NST; ++b) {
       tc::mbar_init(&B.full[b], Q8 ? Shape::CONV : 2);
       tc::mbar_init(&B.empty[b], 1);
-      tc::mbar_init(&B.raw[b], 1);
+      tc::mbar_init(&B.raw[b], Q8 ? 2 : 1);
+      tc::mbar_init(&B.raw_free[b], Shape::CONV);
     }
     odd.any = 0;
     for (int w = 0; w < W; ++w) {
@@ -368,77 +364,98 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   // in the epilogue for the rows that see them.
   const int all_see = row_limit(p, r, rho0 / p.G);
   auto direct = [&](const TileInfo& f) { return f.clean && (all_see >= r.L || f.base + FA_KEYS <= all_see); };
-  // Q8: converter number, or -1
-  const int ci = !Q8 ? -1 : Shape::OWN ? (warp >= 4 && warp < 8 ? warp - 4 : -1) : warp == 0 ? 0 : warp == 2 || warp == 3 ? warp - 1 : -1;
-  auto convert = [&]() {
-    constexpr int NC = Shape::CONV, NG = (16 + NC - 1) / NC;       // groups of eight rows; of a warp
+  // ---- a cache in 8 bits: warp 0, and the converters
+  auto codes = [&](int slot) { return sm + (W + 2 * NST) * TILE + slot * TILE; };        // keys, and TILE / 2 on values
+  auto copy_codes = [&]() {
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
-    const uint8_t* kp = (const uint8_t*)p.c.k + (size_t)h * (size_t)p.c.head_stride + (lane & 3) * 16;
-    const uint8_t* vp = (const uint8_t*)p.c.v + (size_t)h * (size_t)p.c.head_stride + (lane & 3) * 16;
-    const uint8_t* ksp = p.c.k_scale + (size_t)h * (size_t)p.c.scale_head_stride;
-    const uint8_t* vsp = p.c.v_scale + (size_t)h * (size_t)p.c.scale_head_stride;
-    const Div by_page(p.c.page_size), by_block(p.c.scale_block);
-    uint4 kw[NG], vw[NG];
-    uint32_t ks[NG], vs[NG], have = 0;             // scale bytes; bit q: the row counts
-    int page[NG];
-    auto row = [&](int q) { return 8 * (ci + NC * q) + (lane >> 2); };
-    auto look_up = [&](int j) {                    // the pages of tile j's rows
+    int page = tile_page(p, table, lo, lane), issued = 0;
+    uint32_t kb[4], vb[4];                         // scale bytes of the tile asked for last
+    auto keep_scales = [&](int slot) {
 #pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        const int pos = (lo + j) * FA_KEYS + row(q);
-        const int e = by_page.of(pos);
-        page[q] = ci + NC * q < 16 && pos < r.L && e < p.c.table_stride ? __ldg(table + e) : -1;
-      }
+      for (int q = 0; q < (GROUPS ? 1 : 4); ++q)
+        if (!GROUPS || lane < 8) s_scale[slot][32 * q + lane] = (uint16_t)(kb[q] | vb[q] << 8);
+      __syncwarp();
+      if (lane == 0) arrive(&B.raw[slot]);
     };
-    auto fetch = [&](int j, int q) {
-      const int pos = (lo + j) * FA_KEYS + row(q), tok = pos - by_page.of(pos) * p.c.page_size;
-      kw[q] = vw[q] = make_uint4(0u, 0u, 0u, 0u);
-      ks[q] = vs[q] = 0u;
-      have &= ~(1u << q);
-      if (page[q] >= 0 && page[q] < p.c.n_pages) {
-        const size_t at = (size_t)page[q] * (size_t)p.c.page_stride + (size_t)tok * (size_t)p.c.token_stride;
-        const size_t as = (size_t)page[q] * (size_t)p.c.scale_page_stride + (size_t)by_block.of(tok);
-        kw[q] = __ldg(reinterpret_cast<const uint4*>(kp + at));
-        vw[q] = __ldg(reinterpret_cast<const uint4*>(vp + at));
-        ks[q] = __ldg(ksp + as);
-        vs[q] = __ldg(vsp + as);
-        have |= 1u << q;
-      }
-    };
-    look_up(0);
-#pragma unroll
-    for (int q = 0; q < NG; ++q) fetch(0, q);
-    look_up(1);
     for (int j = 0; j < nmax; ++j) {
-      const int s = j % NST;
+      const int slot = j % AHEAD;
+      const TileInfo f = tile_info(p, lo + j, page, r.L, lane);
+      if (j + 1 < nmax) page = tile_page(p, table, lo + j + 1, lane);
+      if (AHEAD == 1 && j > 0) keep_scales(0);
+      if (j >= AHEAD && !wait_warp(&B.raw_free[slot], (uint32_t)((j / AHEAD - 1) & 1), abort)) break;
+      const bool go = f.page >= 0;
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 128u;
+      if (lane == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) raw_meta[slot].valid[q] = f.valid[q];
+        raw_meta[slot].base = f.base;
+        tc::mbar_expect_tx(&B.raw[slot], bytes);
+      }
+      __syncwarp();
+      if (go) {
+        tma_load_4d(codes(slot) + f.dst / 2, &mk, &B.raw[slot], 0, f.tok, h, f.page);
+        tma_load_4d(codes(slot) + TILE / 2 + f.dst / 2, &mv, &B.raw[slot], 0, f.tok, h, f.page);
+      }
+      ++issued;
+      // the last tile's scales have arrived by now; this one's are stored with the next
+      if (AHEAD > 1 && j > 0) keep_scales((j - 1) % AHEAD);
+#pragma unroll
+      for (int q = 0; q < (GROUPS ? 1 : 4); ++q) {
+        const int x = GROUPS ? 16 * (lane & 7) : 32 * q + lane;    // the row whose scale it is
+        const int pg = __shfl_sync(0xffffffffu, f.page, p.geo.tpp ? 0 : x >> p.geo.page_log);
+        uint32_t valid = f.valid[GROUPS ? 0 : q];
+        if (GROUPS) valid = x < 32 ? f.valid[0] : x < 64 ? f.valid[1] : x < 96 ? f.valid[2] : f.valid[3];
+        kb[q] = GROUPS ? 127u : 0u;                // of keys that do not count, whose scores are -inf: any but 0
+        vb[q] = 0u;
+        if ((valid >> (x & 31)) & 1u) {
+          const int tok = p.geo.tpp ? f.tok + x : x & ((1 << p.geo.page_log) - 1);
+          const size_t at = (size_t)pg * (size_t)p.c.scale_page_stride + (size_t)h * (size_t)p.c.scale_head_stride +
+                            (size_t)(tok / p.c.scale_block);
+          kb[q] = __ldg(p.c.k_scale + at);
+          vb[q] = __ldg(p.c.v_scale + at);
+        }
+      }
+    }
+    if (issued) keep_scales((issued - 1) % AHEAD);
+    if (*abort && lane == 0)                       // see the copies in flight land
+      for (int j = max(0, issued - AHEAD); j < issued; ++j) tc::mbar_wait(&B.raw[j % AHEAD], (uint32_t)((j / AHEAD) & 1));
+  };
+  auto convert = [&](int ci) {
+    constexpr int NC = Shape::CONV, NG = 16 / NC;  // groups of eight rows of a warp
+    for (int j = 0; j < nmax; ++j) {
+      const int s = j % NST, slot = j % AHEAD;
       if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
-      const int base = (lo + j) * FA_KEYS;
+      if (!wait_warp(&B.raw[slot], (uint32_t)((j / AHEAD) & 1), abort)) break;
+      tc::mbar_try_wait(&B.raw[slot], (uint32_t)((j / AHEAD) & 1));        // every lane sees the copies, not lane 0 alone
+      const int base = raw_meta[slot].base;
+      const uint32_t v4[4] = {raw_meta[slot].valid[0], raw_meta[slot].valid[1], raw_meta[slot].valid[2], raw_meta[slot].valid[3]};
+      const bool all = (v4[0] & v4[1] & v4[2] & v4[3]) == 0xffffffffu, seen = base + FA_KEYS <= all_see;
+      if (ci == 0) {
+        if (lane < 4) meta[s].valid[lane] = raw_meta[slot].valid[lane];
+        if (lane == 0) { meta[s].base = base; meta[s].full = all; }
+        if (GROUPS && lane < 8) {
+          reinterpret_cast<uint8_t*>(meta[s].ks)[lane] = (uint8_t)s_scale[slot][lane];
+          reinterpret_cast<uint8_t*>(meta[s].vs)[lane] = (uint8_t)(s_scale[slot][lane] >> 8);
+        }
+      }
 #pragma unroll
       for (int q = 0; q < NG; ++q) {
-        if (ci + NC * q >= 16) continue;           // the same in all lanes
-        const int x = row(q);
-        // a bit per row of the group
-        uint32_t m = __ballot_sync(0xffffffffu, (have >> q) & 1u) & 0x11111111u;
-        m = (m | m >> 3) & 0x03030303u;
-        m = (m | m >> 6) & 0x000F000Fu;
-        if (lane == 0) reinterpret_cast<uint8_t*>(meta[s].valid)[ci + NC * q] = (uint8_t)(m | m >> 12);
+        const int x = 8 * (ci + NC * q) + (lane >> 2);             // this lane's row, and 16 bytes of it
+        const uint8_t* src = codes(slot) + x * WS_DH + (((lane & 3) ^ ((x >> 1) & 3)) << 4);
+        uint4 kw = *reinterpret_cast<const uint4*>(src), vw = *reinterpret_cast<const uint4*>(src + TILE / 2);
+        if (!all && !((v4[(ci + NC * q) >> 2] >> (x & 31)) & 1u)) kw = vw = make_uint4(0u, 0u, 0u, 0u);
         uint4 klo, khi, vlo, vhi;
         uint32_t odds = 0u;                        // NaN that the conversion does not see to
         if (GROUPS) {
-          if (lane == 0 && ((ci + NC * q) & 1) == 0) {
-            const bool on = (have >> q) & 1u;
-            reinterpret_cast<uint8_t*>(meta[s].ks)[(ci + NC * q) >> 1] = (uint8_t)(on ? ks[q] : 127u);
-            reinterpret_cast<uint8_t*>(meta[s].vs)[(ci + NC * q) >> 1] = (uint8_t)vs[q];
-          }
-          halves16(kw[q], klo, khi);
-          halves16(vw[q], vlo, vhi);
-          if (base + FA_KEYS > all_see)
-            odds = (nan_codes(vw[q].x) | nan_codes(vw[q].y) | nan_codes(vw[q].z) | nan_codes(vw[q].w)) & 0x80808080u;
+          halves16(kw, klo, khi);
+          halves16(vw, vlo, vhi);
+          if (!seen) odds = (nan_codes(vw.x) | nan_codes(vw.y) | nan_codes(vw.z) | nan_codes(vw.w)) & 0x80808080u;
         } else {
-          widen16(kw[q], ks[q], klo, khi);
-          widen16(vw[q], vs[q], vlo, vhi);
-          odds = (nan_codes(kw[q].x) | nan_codes(kw[q].y) | nan_codes(kw[q].z) | nan_codes(kw[q].w) |
-                  nan_codes(vw[q].x) | nan_codes(vw[q].y) | nan_codes(vw[q].z) | nan_codes(vw[q].w)) & 0x80808080u;
+          const uint32_t both = s_scale[slot][x];
+          widen16(kw, both & 0xFFu, klo, khi);
+          widen16(vw, both >> 8, vlo, vhi);
+          odds = (nan_codes(kw.x) | nan_codes(kw.y) | nan_codes(kw.z) | nan_codes(kw.w) |
+                  nan_codes(vw.x) | nan_codes(vw.y) | nan_codes(vw.z) | nan_codes(vw.w)) & 0x80808080u;
         }
         const uint32_t at = (uint32_t)(x * 128 + (((2 * (lane & 3)) ^ (x & 7)) << 4)), at2 = at ^ 16u;
         *reinterpret_cast<uint4*>(sK(s) + at) = klo;
@@ -446,29 +463,29 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         *reinterpret_cast<uint4*>(sV(s) + at) = vlo;
         *reinterpret_cast<uint4*>(sV(s) + at2) = vhi;
         if (odds) {
-          const bool all = base + x < all_see;     // every row sees it
+          const bool everywhere = base + x < all_see;              // every row sees it
           for (int e = 0; e < 16; ++e) {
             const uint32_t to = (e < 8 ? at : at2) + 2u * (e & 7);
             const int sh = 8 * (e & 3);
-            const uint32_t kc = (e < 4 ? kw[q].x : e < 8 ? kw[q].y : e < 12 ? kw[q].z : kw[q].w) >> sh;
-            const uint32_t vc = (e < 4 ? vw[q].x : e < 8 ? vw[q].y : e < 12 ? vw[q].z : vw[q].w) >> sh;
+            const uint32_t kc = (e < 4 ? kw.x : e < 8 ? kw.y : e < 12 ? kw.z : kw.w) >> sh;
+            const uint32_t vc = (e < 4 ? vw.x : e < 8 ? vw.y : e < 12 ? vw.z : vw.w) >> sh;
             if ((kc & 0x7Fu) == 0x7Fu) *reinterpret_cast<uint16_t*>(sK(s) + to) = 0x7FFFu;
             if ((vc & 0x7Fu) == 0x7Fu) {
-              *reinterpret_cast<uint16_t*>(sV(s) + to) = all ? 0x7FFFu : 0u;
-              if (!all) {
+              *reinterpret_cast<uint16_t*>(sV(s) + to) = everywhere ? 0x7FFFu : 0u;
+              if (!everywhere) {
                 atomicMin(&odd.first[2][16 * (lane & 3) + e], base + x);
                 odd.any = 1;
               }
             }
           }
         }
-        if (j + 1 < nmax) fetch(j + 1, q);
       }
-      if (j + 2 < nmax) look_up(j + 2);
-      if (ci == 0 && lane == 0) meta[s].base = base;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive(&B.full[s]);
+      if (lane == 0) {
+        arrive(&B.full[s]);
+        arrive(&B.raw_free[slot]);
+      }
     }
   };
   if (warp < 4) {
@@ -485,7 +502,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         }
     }
     __syncwarp();
-    if (!Shape::OWN) convert();
+    if (warp == 0) copy_codes();
+    else if (!Shape::OWN) convert(warp - 2);
   } else if (!Q8 && (warp == 0 || warp == 2)) {
     // ---- producers: Q and K, and V.  Two warps, because small pages make
     // many copies of a tile and one warp's copies are issued one by one.
@@ -616,7 +634,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   }
   } else if (Shape::OWN && warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    convert();
+    convert(warp - 4);
   } else {
     // ---- softmax: thread = row
     if (Q8) {                                      // 128 a thread at launch: 4 * 128 = 56 + 88 + 2 * 184, or 2 * 128 = 88 + 168
@@ -671,8 +689,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int q = 0; q < 8; ++q) tm_ld16(tS + 16 * q, sv + 16 * q);
       const Meta& mt = meta[j % NST];
       const int base = mt.base;
-      const bool all = Q8 ? (mt.valid[0] & mt.valid[1] & mt.valid[2] & mt.valid[3]) == 0xffffffffu : mt.full != 0;
-      const bool dense = all && base + FA_KEYS <= lim_all;
+      const bool dense = mt.full && base + FA_KEYS <= lim_all;
       ld_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -1110,10 +1127,10 @@ cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
   if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
                        (uint32_t)(FA_ROWS / p.G)))
     return cudaErrorInvalidValue;
-  if (p.c.dtype == WS_E4M3)                        // whose keys and values are not copied by map
-    return p.c.scale_block % 16 == 0 ? run_fa<MODE_GROUPS>(p, mq, mq, mq, s) : run_fa<MODE_ANY>(p, mq, mq, mq, s);
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
     return cudaErrorInvalidValue;
+  if (p.c.dtype == WS_E4M3)
+    return p.c.scale_block % 16 == 0 ? run_fa<MODE_GROUPS>(p, mq, mk, mv, s) : run_fa<MODE_ANY>(p, mq, mk, mv, s);
   return run_fa<MODE_BF16>(p, mq, mk, mv, s);
 }
 

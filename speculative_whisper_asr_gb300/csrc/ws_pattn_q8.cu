@@ -151,7 +151,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
   const int tb = min(nt_all, split * p.tps), te = min(nt_all, tb + p.tps);
   const int n_my = max(0, (te - tb - warp + W - 1) / W);
   uint8_t* ring = sm + warp * (NS * 2 * TB);
-  uint32_t scales;                         // of this lane's key in the tile asked for last: key's, value's << 8
+  uint32_t k_byte, v_byte;                 // scales of this lane's key in the tile asked for last
   auto issue = [&](int slot, int page) {
     const int base = w.base(p.geo, p.c.page_size, TK);
     const bool ok = page >= 0 && page < p.c.n_pages && lane < w.room(p.geo, p.c.page_size, TK) && base + lane < Lmax;
@@ -170,18 +170,19 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       tma_load_4d(dst, &mk, &full[warp][slot], 0, tok, h, page);
       tma_load_4d(dst + TB, &mv, &full[warp][slot], 0, tok, h, page);
     }
-    scales = 0;
+    k_byte = v_byte = 0;
     if (ok) {
       const int tok = p.geo.tpp ? w.sub * TK + lane : lane & (p.geo.box - 1);
       const size_t at = (size_t)page * (size_t)p.c.scale_page_stride + (size_t)h * (size_t)p.c.scale_head_stride +
                         (size_t)(tok / p.c.scale_block);
-      scales = (uint32_t)__ldg(p.c.k_scale + at) | (uint32_t)__ldg(p.c.v_scale + at) << 8;
+      k_byte = __ldg(p.c.k_scale + at);
+      v_byte = __ldg(p.c.v_scale + at);
     }
   };
   // A slot's scales are stored a tile after they were asked for.
   auto keep_scales = [&](int slot) {
-    slots[warp][slot].ks[lane] = (uint8_t)scales;
-    slots[warp][slot].vs[lane] = (uint8_t)(scales >> 8);
+    slots[warp][slot].ks[lane] = (uint8_t)k_byte;
+    slots[warp][slot].vs[lane] = (uint8_t)v_byte;
   };
   w.start(p.geo, split * p.tps + warp, W);
 #pragma unroll
