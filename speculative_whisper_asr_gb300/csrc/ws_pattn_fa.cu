@@ -56,13 +56,7 @@ constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
 constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, 64) | (1u << 16);   // B (V) is N-major
 constexpr uint32_t F16_FOR_BF16 = ~((1u << 7) | (1u << 10));          // descriptors' types of A and B
 constexpr float MOST = 1152921504606846976.0f;     // 2^60: largest sum of a tile's weights before a row's reference moves
-// Weights as fp16 are stored 2^5 times larger, and a tile's sum is at most
-// 2^10, so that they reach from 2^15 down to 2^-24: 2^-29 of the reference's.
-constexpr int RAISE = 5;
-constexpr float MOST_F16 = 1024.0f;
-constexpr int FAINT = -60;                         // log2 of a value scale to the largest, below which fp16 weights are 0
-
-struct Meta { uint32_t valid[4]; int base; int full; uint32_t ks[2], vs[2]; };   // ks, vs: scale bytes of the groups of 16
+struct Meta { uint32_t valid[4]; int base; int full; };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
@@ -219,18 +213,17 @@ struct Bars {
       p_full[W], pv_done[W];
 };
 
-// Four e4m3 codes times 2^k as bf16 (exact), f = 2^(120 + k) twice: sign, exponent and
-// mantissa are shifted to where bf16 has them, which leaves the value 2^-120
-// times too small (also where the exponent is 0), and multiplied.
-__device__ __forceinline__ uint32_t widen_pair(uint32_t w, uint32_t sel, __nv_bfloat162 f) {
-  const uint32_t x = __byte_perm(w, 0u, sel);      // a code in the high byte of each half
-  const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
-  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
+// Two e4m3 codes times f (a power of two, twice) as bf16: exact, NaN included.
+__device__ __forceinline__ uint32_t widen_pair(uint16_t two, __nv_bfloat162 f) {
+  uint32_t r;
+  asm("{.reg .b32 h;\n\t.reg .b16 a, b;\n\t.reg .f32 x, y;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %1;\n\tmov.b32 {a, b}, h;\n\tcvt.f32.f16 x, a;\n\tcvt.f32.f16 y, b;\n\t"
+      "cvt.rn.bf16x2.f32 %0, y, x;}" : "=r"(r) : "h"(two));
+  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), f);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ __nv_bfloat162 pow2_pair(int k) {       // 2^k, -126 <= k <= 127
-  const uint32_t u = (uint32_t)(k + 127) << 7;
-  const uint32_t two = u | u << 16;
+__device__ __forceinline__ __nv_bfloat162 scale_pair(uint32_t byte) {      // 2^(byte - 127)
+  const uint32_t u = byte ? byte << 7 : 0x0040u, two = u | u << 16;
   return *reinterpret_cast<const __nv_bfloat162*>(&two);
 }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }   // bit 7 of a byte: NaN
@@ -252,44 +245,39 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 // 16 codes as bf16, with the scale of byte s, in two 16-byte chunks.
 __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, uint4& hi) {
-  const int k = (int)s - 127;
-  const __nv_bfloat162 f = pow2_pair(120 + min(k, 7));
-  lo = make_uint4(widen_pair(w.x, 0x1404, f), widen_pair(w.x, 0x3424, f), widen_pair(w.y, 0x1404, f), widen_pair(w.y, 0x3424, f));
-  hi = make_uint4(widen_pair(w.z, 0x1404, f), widen_pair(w.z, 0x3424, f), widen_pair(w.w, 0x1404, f), widen_pair(w.w, 0x3424, f));
-  if (k > 7) {                                     // 2^(120 + k) is no bf16 number: in two factors
-    const __nv_bfloat162 g = pow2_pair(k - 7);
-    uint32_t* u[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(u[q]), g);
-      *u[q] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-  }
+  const __nv_bfloat162 f = scale_pair(s);
+  auto four = [f](uint32_t c, uint32_t& a, uint32_t& b) {
+    a = widen_pair((uint16_t)c, f);
+    b = widen_pair((uint16_t)(c >> 16), f);
+  };
+  four(w.x, lo.x, lo.y);
+  four(w.y, lo.z, lo.w);
+  four(w.z, hi.x, hi.y);
+  four(w.w, hi.z, hi.w);
 }
 
-// A cache in 8 bits: warp 0 copies codes and scales, AHEAD tiles at once, and
-// converter warps write the stages from them, rows that do not count as zeros;
+// A cache in 8 bits: warps 0 and 2 (W = 1: 0) copy codes and scales, AHEAD tiles
+// at once, and converter warps write the stages from them, rows that do not count as zeros;
 // NaN values that not every row sees are noted and left out at once, so there
 // is nothing to clean.  For W = 2 the converters are a warpgroup of their own.
 // (Codes loaded into the converters' registers, or by copies of their own, cost
 // a memory latency per tile: a warp's fence before its stores may be read
 // waits for whatever it has asked for; 4 x 2048 rows 368 and 590 us.)
 //
-// MODE_GROUPS: the codes become fp16 (one conversion for two) and the scales
-// are left to the softmax, to which a group of 16 keys with one scale costs a
-// few instructions: the keys' is a factor of the scores' scale, the values'
-// an addend of the exponent, 2^(v - E) relative to the largest so far, that
-// the row's sum takes out again.  So weights are fp16, and the reference moves
-// at a tile's sum of 2^10.  Queries become fp16 too, each row with a power of two of its own
-// (ws_pattn_q8.cu).  MODE_ANY: bf16 values with their scales, ten instructions
-// for four codes, which the converters are bound by.
+// MODE_GROUPS: keys become fp16 (one conversion for two codes), and so do the
+// queries, each row with a power of two of its own (ws_pattn_q8.cu); a group of
+// 16 keys with one scale costs the softmax a factor.  Values become bf16 with
+// their scales in them (ten instructions for four codes), because the weights
+// have to be bf16: in fp16 their reference moves at 2^15, which some row of a
+// warp does in most tiles (348 us against 2^60's).  MODE_ANY: keys like
+// values, which any blocks of scales allow.
 template <int W, int MODE>
 __global__ void __launch_bounds__(FaShape<W, MODE>::THREADS, 3 - W)
 fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
   using Shape = FaShape<W, MODE>;
   constexpr bool Q8 = MODE != MODE_BF16, GROUPS = MODE == MODE_GROUPS;
-  constexpr uint32_t ID_S = GROUPS ? IDESC_S & F16_FOR_BF16 : IDESC_S, ID_PV = GROUPS ? IDESC_PV & F16_FOR_BF16 : IDESC_PV;
+  constexpr uint32_t ID_S = GROUPS ? IDESC_S & F16_FOR_BF16 : IDESC_S;
   constexpr int NST = Shape::STAGES, THREADS = Shape::THREADS;
   constexpr uint32_t TM_S = 0, TM_P = 128 * W, TM_O = 192 * W;   // + 128 w, + 64 w, + 64 w
   extern __shared__ uint8_t dsm[];
@@ -299,7 +287,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   constexpr int AHEAD = Shape::AHEAD;
-  __shared__ uint16_t s_scale[Q8 ? AHEAD : 1][GROUPS ? 8 : FA_KEYS];       // scale bytes of the rows (groups), key's and value's << 8
+  __shared__ uint8_t s_scale[2][Q8 ? AHEAD : 1][GROUPS ? 8 : FA_KEYS];     // scale bytes of the rows' (groups') keys, and values
+  __shared__ __align__(16) float s_ks[GROUPS ? NST : 1][8];                // scales of the groups' keys
   __shared__ Meta raw_meta[Q8 ? AHEAD : 1];        // of the codes
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   if (p.next_item && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next_item = 0ull;
@@ -329,7 +318,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     for (int b = 0; b < NST; ++b) {
       tc::mbar_init(&B.full[b], Q8 ? Shape::CONV : 2);
       tc::mbar_init(&B.empty[b], 1);
-      tc::mbar_init(&B.raw[b], Q8 ? 2 : 1);
+      tc::mbar_init(&B.raw[b], !Q8 ? 1 : W == 1 ? 2 : 4);
       tc::mbar_init(&B.raw_free[b], Shape::CONV);
     }
     odd.any = 0;
@@ -366,14 +355,18 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   auto direct = [&](const TileInfo& f) { return f.clean && (all_see >= r.L || f.base + FA_KEYS <= all_see); };
   // ---- a cache in 8 bits: warp 0, and the converters
   auto codes = [&](int slot) { return sm + (W + 2 * NST) * TILE + slot * TILE; };        // keys, and TILE / 2 on values
-  auto copy_codes = [&]() {
+  // W = 2: keys by warp 0, values by warp 2, each with its scales; W = 1: both by warp 0
+  auto copy_codes = [&](bool keys, bool values) {
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
     int page = tile_page(p, table, lo, lane), issued = 0;
-    uint32_t kb[4], vb[4];                         // scale bytes of the tile asked for last
+    uint32_t kb[4] = {}, vb[4] = {};               // scale bytes of the tile asked for last
     auto keep_scales = [&](int slot) {
 #pragma unroll
       for (int q = 0; q < (GROUPS ? 1 : 4); ++q)
-        if (!GROUPS || lane < 8) s_scale[slot][32 * q + lane] = (uint16_t)(kb[q] | vb[q] << 8);
+        if (!GROUPS || lane < 8) {
+          if (keys) s_scale[0][slot][32 * q + lane] = (uint8_t)kb[q];
+          if (values) s_scale[1][slot][32 * q + lane] = (uint8_t)vb[q];
+        }
       __syncwarp();
       if (lane == 0) arrive(&B.raw[slot]);
     };
@@ -384,17 +377,19 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (AHEAD == 1 && j > 0) keep_scales(0);
       if (j >= AHEAD && !wait_warp(&B.raw_free[slot], (uint32_t)((j / AHEAD - 1) & 1), abort)) break;
       const bool go = f.page >= 0;
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 128u;
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * (keys && values ? 128u : 64u);
       if (lane == 0) {
+        if (keys) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) raw_meta[slot].valid[q] = f.valid[q];
-        raw_meta[slot].base = f.base;
+          for (int q = 0; q < 4; ++q) raw_meta[slot].valid[q] = f.valid[q];
+          raw_meta[slot].base = f.base;
+        }
         tc::mbar_expect_tx(&B.raw[slot], bytes);
       }
       __syncwarp();
       if (go) {
-        tma_load_4d(codes(slot) + f.dst / 2, &mk, &B.raw[slot], 0, f.tok, h, f.page);
-        tma_load_4d(codes(slot) + TILE / 2 + f.dst / 2, &mv, &B.raw[slot], 0, f.tok, h, f.page);
+        if (keys) tma_load_4d(codes(slot) + f.dst / 2, &mk, &B.raw[slot], 0, f.tok, h, f.page);
+        if (values) tma_load_4d(codes(slot) + TILE / 2 + f.dst / 2, &mv, &B.raw[slot], 0, f.tok, h, f.page);
       }
       ++issued;
       // the last tile's scales have arrived by now; this one's are stored with the next
@@ -411,8 +406,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           const int tok = p.geo.tpp ? f.tok + x : x & ((1 << p.geo.page_log) - 1);
           const size_t at = (size_t)pg * (size_t)p.c.scale_page_stride + (size_t)h * (size_t)p.c.scale_head_stride +
                             (size_t)(tok / p.c.scale_block);
-          kb[q] = __ldg(p.c.k_scale + at);
-          vb[q] = __ldg(p.c.v_scale + at);
+          if (keys) kb[q] = __ldg(p.c.k_scale + at);
+          if (values) vb[q] = __ldg(p.c.v_scale + at);
         }
       }
     }
@@ -428,55 +423,36 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (!wait_warp(&B.raw[slot], (uint32_t)((j / AHEAD) & 1), abort)) break;
       tc::mbar_try_wait(&B.raw[slot], (uint32_t)((j / AHEAD) & 1));        // every lane sees the copies, not lane 0 alone
       const int base = raw_meta[slot].base;
-      const uint32_t v4[4] = {raw_meta[slot].valid[0], raw_meta[slot].valid[1], raw_meta[slot].valid[2], raw_meta[slot].valid[3]};
-      const bool all = (v4[0] & v4[1] & v4[2] & v4[3]) == 0xffffffffu, seen = base + FA_KEYS <= all_see;
+      const uint32_t* valid = raw_meta[slot].valid;
+      const bool all = (valid[0] & valid[1] & valid[2] & valid[3]) == 0xffffffffu, seen = base + FA_KEYS <= all_see;
       if (ci == 0) {
         if (lane < 4) meta[s].valid[lane] = raw_meta[slot].valid[lane];
         if (lane == 0) { meta[s].base = base; meta[s].full = all; }
-        if (GROUPS && lane < 8) {
-          reinterpret_cast<uint8_t*>(meta[s].ks)[lane] = (uint8_t)s_scale[slot][lane];
-          reinterpret_cast<uint8_t*>(meta[s].vs)[lane] = (uint8_t)(s_scale[slot][lane] >> 8);
-        }
+        if (GROUPS && lane < 8) s_ks[s][lane] = scale_of(s_scale[0][slot][lane]);
       }
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < NG; ++q) {
         const int x = 8 * (ci + NC * q) + (lane >> 2);             // this lane's row, and 16 bytes of it
         const uint8_t* src = codes(slot) + x * WS_DH + (((lane & 3) ^ ((x >> 1) & 3)) << 4);
         uint4 kw = *reinterpret_cast<const uint4*>(src), vw = *reinterpret_cast<const uint4*>(src + TILE / 2);
-        if (!all && !((v4[(ci + NC * q) >> 2] >> (x & 31)) & 1u)) kw = vw = make_uint4(0u, 0u, 0u, 0u);
+        if (!all && !((valid[x >> 5] >> (x & 31)) & 1u)) kw = vw = make_uint4(0u, 0u, 0u, 0u);
         uint4 klo, khi, vlo, vhi;
-        uint32_t odds = 0u;                        // NaN that the conversion does not see to
-        if (GROUPS) {
-          halves16(kw, klo, khi);
-          halves16(vw, vlo, vhi);
-          if (!seen) odds = (nan_codes(vw.x) | nan_codes(vw.y) | nan_codes(vw.z) | nan_codes(vw.w)) & 0x80808080u;
-        } else {
-          const uint32_t both = s_scale[slot][x];
-          widen16(kw, both & 0xFFu, klo, khi);
-          widen16(vw, both >> 8, vlo, vhi);
-          odds = (nan_codes(kw.x) | nan_codes(kw.y) | nan_codes(kw.z) | nan_codes(kw.w) |
-                  nan_codes(vw.x) | nan_codes(vw.y) | nan_codes(vw.z) | nan_codes(vw.w)) & 0x80808080u;
-        }
+        widen16(vw, s_scale[1][slot][GROUPS ? x >> 4 : x], vlo, vhi);
+        if (GROUPS) halves16(kw, klo, khi);
+        else widen16(kw, s_scale[0][slot][x], klo, khi);
         const uint32_t at = (uint32_t)(x * 128 + (((2 * (lane & 3)) ^ (x & 7)) << 4)), at2 = at ^ 16u;
         *reinterpret_cast<uint4*>(sK(s) + at) = klo;
         *reinterpret_cast<uint4*>(sK(s) + at2) = khi;
         *reinterpret_cast<uint4*>(sV(s) + at) = vlo;
         *reinterpret_cast<uint4*>(sV(s) + at2) = vhi;
-        if (odds) {
-          const bool everywhere = base + x < all_see;              // every row sees it
+        // NaN values that not every row sees: noted, and zero to the product
+        if (!seen && ((nan_codes(vw.x) | nan_codes(vw.y) | nan_codes(vw.z) | nan_codes(vw.w)) & 0x80808080u)) {
+#pragma unroll 1
           for (int e = 0; e < 16; ++e) {
-            const uint32_t to = (e < 8 ? at : at2) + 2u * (e & 7);
-            const int sh = 8 * (e & 3);
-            const uint32_t kc = (e < 4 ? kw.x : e < 8 ? kw.y : e < 12 ? kw.z : kw.w) >> sh;
-            const uint32_t vc = (e < 4 ? vw.x : e < 8 ? vw.y : e < 12 ? vw.z : vw.w) >> sh;
-            if ((kc & 0x7Fu) == 0x7Fu) *reinterpret_cast<uint16_t*>(sK(s) + to) = 0x7FFFu;
-            if ((vc & 0x7Fu) == 0x7Fu) {
-              *reinterpret_cast<uint16_t*>(sV(s) + to) = everywhere ? 0x7FFFu : 0u;
-              if (!everywhere) {
-                atomicMin(&odd.first[2][16 * (lane & 3) + e], base + x);
-                odd.any = 1;
-              }
-            }
+            if ((src[TILE / 2 + e] & 0x7Fu) != 0x7Fu || base + x < all_see) continue;
+            *reinterpret_cast<uint16_t*>(sV(s) + (e < 8 ? at : at2) + 2u * (e & 7)) = 0u;
+            atomicMin(&odd.first[2][16 * (lane & 3) + e], base + x);
+            odd.any = 1;
           }
         }
       }
@@ -490,7 +466,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   };
   if (warp < 4) {
     if (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else if (Shape::OWN) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else if (Shape::OWN) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (Q8 && warp != 1) {
     if (!GROUPS && warp == 0 && lane == 0) {
@@ -502,7 +478,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         }
     }
     __syncwarp();
-    if (warp == 0) copy_codes();
+    if (warp == 0 || (W == 2 && warp == 2)) copy_codes(warp == 0, W == 1 || warp == 2);
     else if (!Shape::OWN) convert(warp - 2);
   } else if (!Q8 && (warp == 0 || warp == 2)) {
     // ---- producers: Q and K, and V.  Two warps, because small pages make
@@ -605,7 +581,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         const uint64_t vd = vd0 + (uint64_t)(s * (2 * TILE >> 4));
 #pragma unroll
         for (int kk = 0; kk < FA_KEYS / 16; ++kk)
-          umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), ID_PV,
+          umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), IDESC_PV,
                   (j | kk) ? 1u : 0u);
         tc::umma_commit(&B.pv_done[w]);
         if (w == W - 1 || j >= n[W - 1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
@@ -633,11 +609,11 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     __syncwarp();
   }
   } else if (Shape::OWN && warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     convert(warp - 4);
   } else {
     // ---- softmax: thread = row
-    if (Q8) {                                      // 128 a thread at launch: 4 * 128 = 56 + 88 + 2 * 184, or 2 * 128 = 88 + 168
+    if (Q8) {                                      // 128 a thread at launch: 4 * 128 = 2 * 72 + 2 * 184, or 2 * 128 = 88 + 168
       if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
       else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     } else if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");     // 168 a thread at launch
@@ -679,7 +655,6 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     const float2 sl2 = make_float2(sl, sl);
     float m = -INFINITY, msl = 0.f, l = 0.f;
-    int E = 0;                                     // GROUPS: byte of the largest value scale so far
     bool ok = true;
     for (int j = 0; j < nw; ++j) {
       if (!wait_warp(&B.s_full[w], (uint32_t)(j & 1), abort)) { ok = false; break; }
@@ -707,46 +682,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       }
       // P and O are free once the previous product has finished
       if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
-      // GROUPS: the groups' scale bytes, and the factor of O where a value scale is larger than before
-      const uint32_t gk[2] = {mt.ks[0], mt.ks[1]}, gv[2] = {mt.vs[0], mt.vs[1]};
-      float of = 1.f;
-      if (GROUPS) {
-        const uint32_t m4 = __vmaxu4(gv[0], gv[1]), m2 = __vmaxu4(m4, m4 >> 16);
-        const int now = max(E, (int)max(m2 & 0xFFu, (m2 >> 8) & 0xFFu));
-        of = E - now < -126 ? 0.f : __uint_as_float((uint32_t)(E - now + 127) << 23);
-        E = now;
-      }
-      auto key_scale = [&](int g) { return scale_of((gk[g >> 2] >> (8 * (g & 3))) & 0xFFu); };
+      const float* ks = s_ks[GROUPS ? j % NST : 0];
       float2 sum2[2];
-      auto weigh_groups = [&]() {
-        float tile = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t u[16];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int g = 2 * q + e;
-            const float slk = fmaxf(sl * key_scale(g), 1.17549435e-38f);
-            const int dv = max((int)((gv[g >> 2] >> (8 * (g & 3))) & 0xFFu) - E, FAINT);
-            const float add = (float)(dv + RAISE) - msl;
-            float2 gs = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float2 y = __ffma2_rn(make_float2(sv[16 * g + 2 * k], sv[16 * g + 2 * k + 1]), make_float2(slk, slk),
-                                    make_float2(add, add));
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              gs = __fadd2_rn(gs, y);
-              u[8 * e + k] = pack_f16(y.x, y.y);
-            }
-            tile = fmaf(gs.x + gs.y, __uint_as_float((uint32_t)(127 - RAISE - dv) << 23), tile);
-          }
-          tm_st16(tP + 16 * q, u);
-        }
-        return tile;
-      };
       auto weigh = [&]() {
-        if (GROUPS) return weigh_groups();
         const float2 nm2 = make_float2(-msl, -msl);
         sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -754,7 +692,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           uint32_t u[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float2 y = __ffma2_rn(make_float2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), sl2, nm2);
+            // not 0, which times -inf would be NaN
+            const float slk = GROUPS ? fmaxf(sl * ks[2 * q + (e >> 3)], 1.17549435e-38f) : sl;
+            float2 y = __ffma2_rn(make_float2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), GROUPS ? make_float2(slk, slk) : sl2, nm2);
             y.x = ex2(y.x);
             y.y = ex2(y.y);
             sum2[e & 1] = __fadd2_rn(sum2[e & 1], y);
@@ -771,15 +711,13 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       // requests' rows, rows behind the last chunk, or shared memory that no
       // copy writes (rows TR .. 127), and a row's bits may not depend on them.
       float tile = 0.f;
-      if (j > 0) tile = weigh();
-      constexpr float most = GROUPS ? MOST_F16 : MOST;
-      if (j == 0 || __any_sync(0xffffffffu, (GROUPS && of != 1.f) || (on && (m == -INFINITY || !(tile < most))))) {
+      auto look = [&]() {
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < FA_KEYS; e += 8)
           if (GROUPS) {
             const float top = max3(max3(sv[e], sv[e + 1], sv[e + 2]), max3(sv[e + 3], sv[e + 4], sv[e + 5]), fmaxf(sv[e + 6], sv[e + 7]));
-            mx[e / 8 & 3] = fmaxf(mx[e / 8 & 3], top * key_scale(e / 16));
+            mx[e / 8 & 3] = fmaxf(mx[e / 8 & 3], top * ks[e / 16]);
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
@@ -792,18 +730,34 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         if (j > 0) {
           st_wait();                               // the first weights are stored before the second ones are
           tc::tc_fence_after();
-#pragma unroll
+#pragma unroll(Q8 ? 1 : 4)
           for (int d = 0; d < 4; ++d) {
             float o[16];
             uint32_t v[16];
             tm_ld16(tO + 16 * d, o);
             ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * (GROUPS ? f * of : f));
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * f);
             tm_st16(tO + 16 * d, v);
           }
         }
-        tile = weigh();
+      };
+      auto passed = [&]() { return __any_sync(0xffffffffu, on && (m == -INFINITY || !(tile < MOST))) != 0; };
+      if (Q8) {
+        // in one place each: beside the converters' code, two of each overflow
+        // the instruction cache (4 x 2048 rows: 404 us, 309 in this form)
+#pragma unroll 1
+        for (bool first = j == 0;; first = true) {
+          if (first) look();
+          tile = weigh();
+          if (first || !passed()) break;
+        }
+      } else {
+        if (j > 0) tile = weigh();
+        if (j == 0 || passed()) {
+          look();
+          tile = weigh();
+        }
       }
       l += tile;
       st_wait();
@@ -813,7 +767,6 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     if (ok && nw > 0) ok = wait_warp(&B.pv_done[w], (uint32_t)((nw - 1) & 1), abort);
     tc::tc_fence_after();
-    const float size = GROUPS ? scale_of((uint32_t)E) * (1.f / (1 << RAISE)) : 1.f;        // of O
     const bool any_odd = nw > 0 && *(volatile int*)&odd.any != 0;
     if (p.nsplit > 1) {
       const size_t at = on ? (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split : 0;
@@ -821,9 +774,6 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int q = 0; q < 4; ++q) {
         float o[16];
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
-        if (GROUPS)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= size;
         if (any_odd)
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
@@ -842,9 +792,6 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int q = 0; q < 4; ++q) {
         float o[16];
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
-        if (GROUPS)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= size;
         if (any_odd)
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
