@@ -481,7 +481,7 @@ typedef struct {
   /* WS_E4M3 only, not read otherwise: */
   uint8_t* k_scale;
   uint8_t* v_scale;
-  int64_t scale_page_stride, scale_head_stride;     /* bytes, >= page_size / scale_block (a dimension of one: any) */
+  int64_t scale_page_stride, scale_head_stride;     /* bytes, page_size / scale_block .. 2^31 - 1 (a dimension of one: any) */
   int32_t scale_block;         /* tokens per scale, a divisor of page_size (>= 16 is fastest) */
 } ws_paged_cache;
 

@@ -38,8 +38,8 @@ inline const char* check_paged_cache(const ws_paged_cache* c) {
     if (c->scale_block < 1 || c->page_size % c->scale_block) return "scale_block must be a divisor of page_size";
     const int64_t blocks = c->page_size / c->scale_block;
     if ((c->n_kv_heads > 1 && c->scale_head_stride < blocks) || (c->n_pages > 1 && c->scale_page_stride < blocks) ||
-        c->scale_head_stride < 0 || c->scale_page_stride < 0 || c->scale_head_stride >= most || c->scale_page_stride >= most)
-      return "scale strides must be >= page_size / scale_block";
+        c->scale_head_stride < 0 || c->scale_page_stride < 0 || c->scale_head_stride > INT_MAX || c->scale_page_stride > INT_MAX)
+      return "scale strides must be >= page_size / scale_block and less than 2^31";
   }
   return nullptr;
 }

@@ -78,6 +78,7 @@ struct AttnP {
   int row_tiles;                           // row tiles per (request, KV head)
   float* nl;                               // tcgen05 path with mass: -lse * log2(e) of every row tile's rows
                                            // [n_req][Hkv][row_tiles][128], 16-byte aligned; else null
+  uint32_t block_mul;                      // 8 bits: 2^32 / scale_block, rounded up (0: scale_block is 1)
   unsigned long long* next_item;           // with nl: counter of the weight pass's work items, cleared by fa_kernel
 };
 
@@ -204,4 +205,4 @@ cudaError_t launch_f32_mass(const AttnP& p, int rpt, cudaStream_t s);
 
 // Caches in 8 bits (ws_pattn_q8.cu): row tiles of 8 * nt rows that stream the cache.
 constexpr int Q8_TK = 32;                          // keys per tile
-cudaError_t launch_q8(const AttnP& p, int nt, cudaStream_t s);
+cudaError_t launch_q8(AttnP p, int nt, cudaStream_t s);

@@ -46,7 +46,7 @@ constexpr int q8_smem(int nt) {
 struct Slot {                              // of a ring: keys that count, the first position, bytes of the keys' scales
   uint32_t valid;
   int base;
-  uint8_t ks[TK], vs[TK];
+  uint8_t ks[TK], vs[TK];                  // UNI: of all keys, in place 0
 };
 // Key of a 32-key tile that stands at place p of the products: bits 0 and 1 of
 // it change places, so that the keys of a quad's lanes (bits 1 and 2 of p)
@@ -110,8 +110,8 @@ __device__ __forceinline__ bool take_out_nan(Odd& odd, uint8_t* tile, int base, 
 }
 
 // MIX: causal chunks of more than one row, where NaN values are kept from the
-// rows that do not see them.
-template <int NT, bool MIX>
+// rows that do not see them.  UNI: scales hold for whole tiles.
+template <int NT, bool MIX, bool UNI>
 __global__ void __launch_bounds__(W * 32, NT == 4 ? 2 : 3)
 q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   constexpr int MT = TK / 16;              // key steps of 16
@@ -152,6 +152,8 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
   const int n_my = max(0, (te - tb - warp + W - 1) / W);
   uint8_t* ring = sm + warp * (NS * 2 * TB);
   uint32_t k_byte, v_byte;                 // scales of this lane's key in the tile asked for last
+  const uint8_t* k_scales = p.c.k_scale + (size_t)h * (size_t)p.c.scale_head_stride;
+  const uint8_t* v_scales = p.c.v_scale + (size_t)h * (size_t)p.c.scale_head_stride;
   auto issue = [&](int slot, int page) {
     const int base = w.base(p.geo, p.c.page_size, TK);
     const bool ok = page >= 0 && page < p.c.n_pages && lane < w.room(p.geo, p.c.page_size, TK) && base + lane < Lmax;
@@ -172,17 +174,26 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
     }
     k_byte = v_byte = 0;
     if (ok) {
-      const int tok = p.geo.tpp ? w.sub * TK + lane : lane & (p.geo.box - 1);
-      const size_t at = (size_t)page * (size_t)p.c.scale_page_stride + (size_t)h * (size_t)p.c.scale_head_stride +
-                        (size_t)(tok / p.c.scale_block);
-      k_byte = __ldg(p.c.k_scale + at);
-      v_byte = __ldg(p.c.v_scale + at);
+      const uint32_t tok = (uint32_t)(p.geo.tpp ? w.sub * TK + (UNI ? 0 : lane) : lane & (p.geo.box - 1));
+      uint32_t b = p.block_mul ? __umulhi(tok, p.block_mul) : tok;        // tok / scale_block, or one more
+      b -= b * (uint32_t)p.c.scale_block > tok;
+      const uint64_t at = (uint64_t)(uint32_t)page * (uint32_t)p.c.scale_page_stride + b;
+      k_byte = __ldg(k_scales + at);
+      v_byte = __ldg(v_scales + at);
     }
   };
   // A slot's scales are stored a tile after they were asked for.
   auto keep_scales = [&](int slot) {
-    slots[warp][slot].ks[lane] = (uint8_t)k_byte;
-    slots[warp][slot].vs[lane] = (uint8_t)v_byte;
+    if (UNI) {                             // of any key that counts: a tile of one scale is a tile of one page
+      const uint32_t kb = __reduce_max_sync(ALL, k_byte), vb = __reduce_max_sync(ALL, v_byte);
+      if (lane == 0) {
+        slots[warp][slot].ks[0] = (uint8_t)kb;
+        slots[warp][slot].vs[0] = (uint8_t)vb;
+      }
+    } else {
+      slots[warp][slot].ks[lane] = (uint8_t)k_byte;
+      slots[warp][slot].vs[lane] = (uint8_t)v_byte;
+    }
   };
   w.start(p.geo, split * p.tps + warp, W);
 #pragma unroll
@@ -195,7 +206,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
 
   // ---- queries: rows r0 + 8 nt + g, dims 16 c .. 16 c + 15 of this lane
   uint32_t qf[4][NT][2];
-  float sl[NT][2], hold[NT][2];            // of this lane's rows 8 nt + 2 c + e: score scale in log2 units, HOLD by it
+  float sl[NT][2];                         // of this lane's rows 8 nt + 2 c + e: score scale in log2 units
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int rho = r0 + 8 * nt + g;
@@ -228,8 +239,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       for (int k = 0; k < 2; ++k) qf[s][nt][k] = pack_f16(x[4 * s + 2 * k] * f, x[4 * s + 2 * k + 1] * f);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      sl[nt][k] = p.sl * __shfl_sync(ALL, back, 4 * (2 * c + k));
-      hold[nt][k] = fminf(HOLD / sl[nt][k], 1e30f);
+      sl[nt][k] = fmaxf(p.sl * __shfl_sync(ALL, back, 4 * (2 * c + k)), 1e-37f);
     }
   }
   int lim[NT][2];
@@ -237,11 +247,11 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) lim[nt][e] = row_limit(p, r, min(r0 + 8 * nt + 2 * c + e, R - 1) / p.G);
-  float o[4][NT][4], m[NT][2], msl[NT][2], l[NT][2];
+  float o[4][NT][4], m[NT][2], l[NT][2];   // m: the rows' references, in log2 units
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) { m[nt][e] = -INFINITY; msl[nt][e] = 0.f; l[nt][e] = 0.f; }
+    for (int e = 0; e < 2; ++e) { m[nt][e] = -INFINITY; l[nt][e] = 0.f; }
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -256,8 +266,6 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
     const int slot = it % NS;
     const bool more = it + NS < n_my;
     const int page_next = more ? page_of() : -1;           // in flight while this tile is computed
-    // the scales asked for at the end of the last tile, of the slot that it freed
-    if (it > 0 && it - 1 + NS < n_my) keep_scales((it - 1) % NS);
     if (!tc::mbar_wait(&full[warp][slot], (uint32_t)((it / NS) & 1))) { dead = true; return false; }
     __syncwarp();
     const Slot& sl_ = slots[warp][slot];
@@ -300,15 +308,17 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
 #pragma unroll
         for (int s = 0; s < 4; ++s) mma_f16(sc[mt][nt], a[s], qf[s][nt][0], qf[s][nt][1]);
       }
+      if (!UNI)
 #pragma unroll
-      for (int e2 = 0; e2 < 2; ++e2) {
-        const int key = 16 * mt + 8 * e2 + key_g;
-        const float ks = scale_of(sl_.ks[key]);
-        vs[mt][e2] = sl_.vs[key];
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const int key = 16 * mt + 8 * e2 + key_g;
+          const float ks = scale_of(sl_.ks[key]);
+          vs[mt][e2] = sl_.vs[key];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) { sc[mt][nt][2 * e2] *= ks; sc[mt][nt][2 * e2 + 1] *= ks; }
-      }
+          for (int nt = 0; nt < NT; ++nt) { sc[mt][nt][2 * e2] *= ks; sc[mt][nt][2 * e2 + 1] *= ks; }
+        }
     }
+    if (UNI) vs[0][0] = sl_.vs[0];
     if (valid != ALL || base + TK > Lmin) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -325,9 +335,9 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
     }
     // ---- a larger value scale than before?
     {
-      const int most = max(max(vs[0][0], vs[0][1]), max(vs[1][0], vs[1][1]));
+      const int most = UNI ? vs[0][0] : max(max(vs[0][0], vs[0][1]), max(vs[1][0], vs[1][1]));
       if (__any_sync(ALL, most > E)) {
-        const int now = __reduce_max_sync(ALL, max(most, E));
+        const int now = UNI ? most : __reduce_max_sync(ALL, max(most, E));
         const float f = down(E - now);
         E = now;
 #pragma unroll
@@ -339,42 +349,50 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       }
     }
     // ---- does a score pass its row's reference by more than 2^8?
+    const float ks = UNI ? scale_of(sl_.ks[0]) : 1.f;
     bool grow = false;
+    float slk[NT][2], top[NT][2];          // UNI: with the keys' scale (not 0, which times -inf would be NaN)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float t4 = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
-        grow |= t4 > m[nt][e] + hold[nt][e];
+        slk[nt][e] = UNI ? fmaxf(sl[nt][e] * ks, 1.17549435e-38f) : sl[nt][e];
+        top[nt][e] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e])) * slk[nt][e];
+        grow |= top[nt][e] > m[nt][e] + HOLD;
       }
     if (__any_sync(ALL, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t4 = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
+          float t4 = top[nt][e];
           t4 = fmaxf(t4, __shfl_xor_sync(ALL, t4, 4));
           t4 = fmaxf(t4, __shfl_xor_sync(ALL, t4, 8));
           t4 = fmaxf(t4, __shfl_xor_sync(ALL, t4, 16));
-          const float mn = t4 > m[nt][e] + hold[nt][e] ? t4 : m[nt][e];
-          const float f = m[nt][e] > -INFINITY ? ex2((m[nt][e] - mn) * sl[nt][e]) : 0.f;
+          const float mn = t4 > m[nt][e] + HOLD ? t4 : m[nt][e];
+          const float f = m[nt][e] > -INFINITY ? ex2(m[nt][e] - mn) : 0.f;
           m[nt][e] = mn;
-          msl[nt][e] = mn > -INFINITY ? mn * sl[nt][e] : 0.f;
           l[nt][e] *= f;
 #pragma unroll
           for (int d = 0; d < 4; ++d) { o[d][nt][e] *= f; o[d][nt][2 + e] *= f; }
         }
     }
+    float ref[NT][2];                      // 0 where a row has none yet
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[nt][e] = m[nt][e] > -INFINITY ? m[nt][e] : 0.f;
     uint32_t pf[MT][NT][2];
+    const float fu = UNI ? down(vs[0][0] - E) * RAISE : 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
-        const float f = down(vs[mt][e2] - E) * RAISE;
+        const float f = UNI ? fu : down(vs[mt][e2] - E) * RAISE;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float p0 = ex2(fmaf(sc[mt][nt][2 * e2], sl[nt][0], -msl[nt][0]));
-          const float p1 = ex2(fmaf(sc[mt][nt][2 * e2 + 1], sl[nt][1], -msl[nt][1]));
+          const float p0 = ex2(fmaf(sc[mt][nt][2 * e2], slk[nt][0], -ref[nt][0]));
+          const float p1 = ex2(fmaf(sc[mt][nt][2 * e2 + 1], slk[nt][1], -ref[nt][1]));
           l[nt][0] += p0;
           l[nt][1] += p1;
           pf[mt][nt][e2] = movm(pack_f16(p0 * f, p1 * f));
@@ -400,6 +418,8 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
         for (int nt = 0; nt < NT; ++nt) mma_f16(o[d][nt], a[d], pf[ks][nt][0], pf[ks][nt][1]);
     }
     __syncwarp();                          // every lane has read the slot
+    // the scales asked for at the end of the last tile, of the slot that it freed
+    if (it > 0 && it - 1 + NS < n_my) keep_scales((it - 1) % NS);
     if (more) { issue(slot, page_next); w.next(p.geo); }
     return true;
   };
@@ -432,7 +452,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       for (int d = 0; d < 4; ++d)
         *reinterpret_cast<float2*>(dst + 8 * g + 2 * d) = make_float2(o[d][nt][e] * size, o[d][nt][2 + e] * size);
       if (g == 0) {
-        sml[(warp * 8 * NT + row) * 2] = dead ? NAN : m[nt][e] > -INFINITY ? msl[nt][e] : m[nt][e];
+        sml[(warp * 8 * NT + row) * 2] = dead ? NAN : m[nt][e];
         sml[(warp * 8 * NT + row) * 2 + 1] = dead ? NAN : s;
       }
     }
@@ -478,24 +498,30 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
     for (int s = 0; s < NS; ++s) { tc::mbar_wait(&full[warp][s], 0); tc::mbar_wait(&full[warp][s], 1); }
 }
 
-template <int NT, bool MIX>
+template <int NT, bool MIX, bool UNI>
 cudaError_t run(const AttnP& p, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(q8_kernel<NT, MIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, q8_smem(NT));
+  cudaError_t e = cudaFuncSetAttribute(q8_kernel<NT, MIX, UNI>, cudaFuncAttributeMaxDynamicSharedMemorySize, q8_smem(NT));
   if (e != cudaSuccess) return e;
-  q8_kernel<NT, MIX><<<dim3(p.row_tiles * p.nsplit, p.c.n_kv_heads, p.a.n_req), W * 32, q8_smem(NT), s>>>(
+  q8_kernel<NT, MIX, UNI><<<dim3(p.row_tiles * p.nsplit, p.c.n_kv_heads, p.a.n_req), W * 32, q8_smem(NT), s>>>(
       p, reinterpret_cast<const CUtensorMap&>(mk), reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
   return cudaGetLastError();
 }
+template <bool MIX, bool UNI>
+cudaError_t run(const AttnP& p, int nt, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
+  if (nt == 1) return run<1, MIX, UNI>(p, mk, mv, s);
+  return nt == 2 ? run<2, MIX, UNI>(p, mk, mv, s) : run<4, MIX, UNI>(p, mk, mv, s);
+}
 
 }  // namespace
 
-cudaError_t launch_q8(const AttnP& p, int nt, cudaStream_t s) {
+cudaError_t launch_q8(AttnP p, int nt, cudaStream_t s) {
   TcMap mk, mv;
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
     return cudaErrorInvalidValue;
-  const bool mix = p.a.causal && p.a.max_q > 1;
-  if (nt == 1) return mix ? run<1, true>(p, mk, mv, s) : run<1, false>(p, mk, mv, s);
-  if (nt == 2) return mix ? run<2, true>(p, mk, mv, s) : run<2, false>(p, mk, mv, s);
-  return mix ? run<4, true>(p, mk, mv, s) : run<4, false>(p, mk, mv, s);
+  const int block = p.c.scale_block;
+  p.block_mul = block == 1 ? 0u : (uint32_t)(((1ull << 32) + block - 1) / block);
+  const bool mix = p.a.causal && p.a.max_q > 1, uni = block % TK == 0;
+  if (mix) return uni ? run<true, true>(p, nt, mk, mv, s) : run<true, false>(p, nt, mk, mv, s);
+  return uni ? run<false, true>(p, nt, mk, mv, s) : run<false, false>(p, nt, mk, mv, s);
 }
