@@ -203,6 +203,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       w.next(p.geo);
       keep_scales(s);
     }
+  int page_next = page_of();               // of the tile asked for next: looked up a tile ahead
 
   // ---- queries: rows r0 + 8 nt + g, dims 16 c .. 16 c + 15 of this lane
   uint32_t qf[4][NT][2];
@@ -264,8 +265,6 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
   bool dead = false;
   auto tile = [&](int it, auto last_tiles) -> bool {
     const int slot = it % NS;
-    const bool more = it + NS < n_my;
-    const int page_next = more ? page_of() : -1;           // in flight while this tile is computed
     if (!tc::mbar_wait(&full[warp][slot], (uint32_t)((it / NS) & 1))) { dead = true; return false; }
     __syncwarp();
     const Slot& sl_ = slots[warp][slot];
@@ -286,21 +285,46 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     }
+    // ---- the tile into registers, so that its slot takes the next copy at once:
+    // what is under way bounds the rate (slots held until the end: 141 us for 117)
     const uint32_t kb = tc::smem_u32(Kt), vb = tc::smem_u32(Vt);
+    uint4 kw[MT][2];                       // key 16 mt + 8 e2 + key_g, dims 16 c ..
+    uint2 vw[MT][2][2];                    // keys 16 mt + 8 e2 + key_c, + 2 (places 2 c, 2 c + 1), dims 8 g ..
+    int vs[MT][2];                         // scales of the former keys' values, and of them
+    float ksc[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        const int key = 16 * mt + 8 * e2 + key_g, k0 = 16 * mt + 8 * e2 + key_c;
+        kw[mt][e2] = lds128(kb + key * WS_DH + ((c ^ ((key >> 1) & 3)) << 4));
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          vw[mt][e2][e] = lds64(vb + (k0 + 2 * e) * WS_DH + (((g >> 1) ^ (((k0 + 2 * e) >> 1) & 3)) << 4) + ((g & 1) << 3));
+        if (!UNI || (mt == 0 && e2 == 0)) {
+          vs[mt][e2] = sl_.vs[UNI ? 0 : key];
+          ksc[mt][e2] = scale_of(sl_.ks[UNI ? 0 : key]);
+        }
+      }
+    __syncwarp();                          // every lane has read the slot
+    // the scales asked for at the end of the last tile, of the slot that it freed
+    if (it > 0 && it - 1 + NS < n_my) keep_scales((it - 1) % NS);
+    if (it + NS < n_my) {
+      issue(slot, page_next);
+      w.next(p.geo);
+      page_next = page_of();
+    }
     // ---- S^T: place 16 mt + 8 e2 + g of the products is key 16 mt + 8 e2 + key_g
     float sc[MT][NT][4];
-    int vs[MT][2];                         // value scales of those keys
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       uint32_t a[4][4];
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
-        const int key = 16 * mt + 8 * e2 + key_g;
-        const uint4 v = lds128(kb + key * WS_DH + ((c ^ ((key >> 1) & 3)) << 4));
-        widen(v.x, a[0][e2], a[0][2 + e2]);
-        widen(v.y, a[1][e2], a[1][2 + e2]);
-        widen(v.z, a[2][e2], a[2][2 + e2]);
-        widen(v.w, a[3][e2], a[3][2 + e2]);
+        widen(kw[mt][e2].x, a[0][e2], a[0][2 + e2]);
+        widen(kw[mt][e2].y, a[1][e2], a[1][2 + e2]);
+        widen(kw[mt][e2].z, a[2][e2], a[2][2 + e2]);
+        widen(kw[mt][e2].w, a[3][e2], a[3][2 + e2]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -310,15 +334,10 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       }
       if (!UNI)
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {
-          const int key = 16 * mt + 8 * e2 + key_g;
-          const float ks = scale_of(sl_.ks[key]);
-          vs[mt][e2] = sl_.vs[key];
+        for (int e2 = 0; e2 < 2; ++e2)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) { sc[mt][nt][2 * e2] *= ks; sc[mt][nt][2 * e2 + 1] *= ks; }
-        }
+          for (int nt = 0; nt < NT; ++nt) { sc[mt][nt][2 * e2] *= ksc[mt][e2]; sc[mt][nt][2 * e2 + 1] *= ksc[mt][e2]; }
     }
-    if (UNI) vs[0][0] = sl_.vs[0];
     if (valid != ALL || base + TK > Lmin) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -349,14 +368,13 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       }
     }
     // ---- does a score pass its row's reference by more than 2^8?
-    const float ks = UNI ? scale_of(sl_.ks[0]) : 1.f;
     bool grow = false;
     float slk[NT][2], top[NT][2];          // UNI: with the keys' scale (not 0, which times -inf would be NaN)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        slk[nt][e] = UNI ? fmaxf(sl[nt][e] * ks, 1.17549435e-38f) : sl[nt][e];
+        slk[nt][e] = UNI ? fmaxf(sl[nt][e] * ksc[0][0], 1.17549435e-38f) : sl[nt][e];
         top[nt][e] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e])) * slk[nt][e];
         grow |= top[nt][e] > m[nt][e] + HOLD;
       }
@@ -404,9 +422,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       uint32_t a[4][4];
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
-        const int k0 = 16 * ks + 8 * e2 + key_c, k1 = k0 + 2;          // places 2 c and 2 c + 1
-        const uint2 v0 = lds64(vb + k0 * WS_DH + (((g >> 1) ^ ((k0 >> 1) & 3)) << 4) + ((g & 1) << 3));
-        const uint2 v1 = lds64(vb + k1 * WS_DH + (((g >> 1) ^ ((k1 >> 1) & 3)) << 4) + ((g & 1) << 3));
+        const uint2 v0 = vw[ks][e2][0], v1 = vw[ks][e2][1];
         widen(__byte_perm(v0.x, v1.x, 0x5140), a[0][2 * e2], a[0][2 * e2 + 1]);
         widen(__byte_perm(v0.x, v1.x, 0x7362), a[1][2 * e2], a[1][2 * e2 + 1]);
         widen(__byte_perm(v0.y, v1.y, 0x5140), a[2][2 * e2], a[2][2 * e2 + 1]);
@@ -417,10 +433,6 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_f16(o[d][nt], a[d], pf[ks][nt][0], pf[ks][nt][1]);
     }
-    __syncwarp();                          // every lane has read the slot
-    // the scales asked for at the end of the last tile, of the slot that it freed
-    if (it > 0 && it - 1 + NS < n_my) keep_scales((it - 1) % NS);
-    if (more) { issue(slot, page_next); w.next(p.geo); }
     return true;
   };
   int it = 0;
