@@ -13,9 +13,9 @@
 // Their logits (K of the 128th parts, from L2) are read again, those not
 // behind T kept, and ranked by counting.
 //
-// merge_kernel.  One CTA per request: log-sum-exps of the beams (in double:
-// what differs by less than fp32's step from another beam is still told
-// apart), the parts' candidates ranked within their beams, the beams' against
+// merge_kernel.  One CTA per request: log-sum-exps of the beams (in double, as
+// are the candidates' scores: what differs from another beam's by less than
+// fp32's step is still told apart), the parts' candidates ranked within their beams, the beams' against
 // each other by whole numbers that order like the doubles, and the 2 * beams
 // best dealt out: candidates that end go to the finished transcripts.
 // Then each thread moves a column of the transcripts for all beams, so the
@@ -31,6 +31,7 @@ constexpr int BM_MT = 256;                  // ... and per request
 constexpr int BM_BEAMS = 16;
 constexpr int BM_K = BM_BEAMS + 1;
 constexpr int BM_W = BM_NT / 32;
+constexpr int BM_STEP = 2 * BM_NT;         // logits of a step of all threads
 constexpr int BM_PART = 32768;             // logits per part, at most
 constexpr int BM_PARTS = 32;               // parts per row, at most (a lane each in the merge)
 constexpr float LOG2E = 1.4426950408889634f;
@@ -53,12 +54,27 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   const uint32_t u = (uint32_t)(k >> 32);
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
+// log of a positive fp32 number to 2^-25: its exponent's part in double, that of its significand in 0.75 .. 1.5 in fp32
+// (a logarithm in double took the merge 10 us of 15).
+__device__ __forceinline__ double log_of(float x) {
+  const int e = (int)(__float_as_uint(x) - 0x3F400000u) >> 23;
+  return (double)e * 0.69314718055994530942 + (double)logf(__uint_as_float(__float_as_uint(x) - ((uint32_t)e << 23)));
+}
 __device__ __forceinline__ bool idle(const ws_beam_args& a, int i) {
   return (a.n_done && a.n_done[i] >= a.max_done) || (a.tokens && a.length[i] >= a.capacity);
 }
 
+// Tokens v and v + 1 of a row, -inf behind v1.  PAIR: every row is 8-byte aligned.
+template <bool PAIR>
+__device__ __forceinline__ float2 two_logits(const float* z, int v, int v1) {
+  if (PAIR && v + 1 < v1) return __ldg(reinterpret_cast<const float2*>(z + v));
+  return make_float2(v < v1 ? __ldg(z + v) : -INFINITY, v + 1 < v1 ? __ldg(z + v + 1) : -INFINITY);
+}
+
+// A thread's tokens are the same with and without PAIR: 2 tid, 2 tid + 1 and on by STEP.
+template <bool PAIR>
 __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
-  extern __shared__ unsigned long long s_list[];           // [K][steps]
+  extern __shared__ unsigned long long s_list[];           // [K][a thread's logits]
   __shared__ unsigned long long s_key[BM_W * BM_K];
   __shared__ int s_thread[BM_K];
   __shared__ unsigned long long s_t;
@@ -70,26 +86,28 @@ __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
   if (idle(p.a, row / p.a.beams)) return;
   const float* z = p.a.logits + (size_t)row * (size_t)p.a.ld;
   const int v0 = blockIdx.x * p.part, v1 = min(V, v0 + p.part);
-  // ---- the stream: U logits of a thread in flight
+  // ---- the stream: 2 U logits of a thread in flight
   float m = -INFINITY, ref = 0.f, s = 0.f; // largest so far (ref: 0 until there is one); sum of exp(. - ref)
   int at = -1;                             // its token
-  constexpr int U = 16;
-  for (int v = v0 + tid; v < v1; v += U * BM_NT) {
-    float f[U];
+  constexpr int U = 8;
+  for (int v = v0 + 2 * tid; v < v1; v += U * BM_STEP) {
+    float2 f[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) f[u] = v + u * BM_NT < v1 ? __ldg(z + v + u * BM_NT) : -INFINITY;
-    float t = f[0];
+    for (int u = 0; u < U; ++u) f[u] = two_logits<PAIR>(z, v + u * BM_STEP, v1);
+    float t = fmaxf(f[0].x, f[0].y);
 #pragma unroll
-    for (int u = 1; u < U; ++u) t = fmaxf(t, f[u]);
+    for (int u = 1; u < U; ++u) t = fmaxf(t, fmaxf(f[u].x, f[u].y));
     if (t > m) {
 #pragma unroll
-      for (int u = U - 1; u >= 0; --u)
-        if (f[u] == t) at = v + u * BM_NT;
+      for (int u = U - 1; u >= 0; --u) {
+        if (f[u].y == t) at = v + u * BM_STEP + 1;
+        if (f[u].x == t) at = v + u * BM_STEP;
+      }
       s *= exp_of(m - t);                  // m = -inf: 0
       m = ref = t;
     }
 #pragma unroll
-    for (int u = 0; u < U; u += 2) s += exp_of(f[u] - ref) + exp_of(f[u + 1] - ref);
+    for (int u = 0; u < U; ++u) s += exp_of(f[u].x - ref) + exp_of(f[u].y - ref);
   }
   // ---- the K best of the warp's threads, then of the CTA's
   const unsigned long long key = at >= 0 ? argmax_key(m, at) : 0ull;
@@ -113,7 +131,7 @@ __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
     if (mine) {
       int rank = 0;
       for (int j = 0; j < BM_W * K; ++j) rank += s_key[j] > mine;
-      if (rank < K) s_thread[rank] = (argmax_key_id(mine) - v0) % BM_NT;
+      if (rank < K) s_thread[rank] = (argmax_key_id(mine) - v0) % BM_STEP / 2;
       if (rank == K - 1) s_t = mine;       // else fewer than K threads have any: all that is above -inf
     }
   }
@@ -127,14 +145,27 @@ __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
   __syncthreads();
   // ---- the logits of those threads, again
   const unsigned long long T = s_t;
-  const int steps = (v1 - v0 + BM_NT - 1) / BM_NT;
-  for (int y = tid; y < K * steps; y += BM_NT) {
-    const int th = s_thread[y / steps], v = v0 + (y - y / steps * steps) * BM_NT + th;
-    if (th < 0 || v >= v1) continue;
-    const float f = __ldg(z + v);
-    if (!(f > -INFINITY)) continue;
-    const unsigned long long mine = argmax_key(f, v);
-    if (mine >= T) s_list[atomicAdd(&s_n, 1)] = mine;
+  const int steps = (v1 - v0 + BM_STEP - 1) / BM_STEP;
+  for (int y0 = tid; y0 < K * steps; y0 += 4 * BM_NT) {
+    float2 f[4];
+    int v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int y = y0 + q * BM_NT, r = y / steps, th = y < K * steps ? s_thread[r] : -1;
+      v[q] = th < 0 ? v1 : v0 + (y - r * steps) * BM_STEP + 2 * th;
+      f[q] = two_logits<PAIR>(z, v[q], v1);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (f[q].x > -INFINITY) {
+        const unsigned long long mine = argmax_key(f[q].x, v[q]);
+        if (mine >= T) s_list[atomicAdd(&s_n, 1)] = mine;
+      }
+      if (f[q].y > -INFINITY) {
+        const unsigned long long mine = argmax_key(f[q].y, v[q] + 1);
+        if (mine >= T) s_list[atomicAdd(&s_n, 1)] = mine;
+      }
+    }
   }
   __syncthreads();
   const int n = s_n;
@@ -160,7 +191,7 @@ __device__ __forceinline__ double order_f64(unsigned long long u) {
 __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
   extern __shared__ unsigned long long sm[];               // the parts' candidates [beams][parts * K]
   __shared__ unsigned long long s_c[BM_BEAMS * BM_K];      // a beam's K best: order of the score, 0: none
-  __shared__ int s_v[BM_BEAMS * BM_K];                     // and their tokens
+  __shared__ int s_v[BM_BEAMS * BM_K];                     // and their tokens, with the beam << 18
   __shared__ int s_top[2 * BM_BEAMS];                      // the best of all: places in s_c
   __shared__ int s_par[BM_BEAMS], s_tok[BM_BEAMS], s_dpar[BM_BEAMS], s_dplace[BM_BEAMS], s_ends;
   constexpr uint32_t ALL = 0xffffffffu;
@@ -183,7 +214,7 @@ __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
       const float2 st = lane < p.parts ? p.stat[((size_t)i * B + b) * p.parts + lane] : make_float2(-INFINITY, 0.f);
       const float M = warp_max(st.x);
       const float S = warp_sum(st.x > -INFINITY ? st.y * exp_of(st.x - M) : st.y);
-      const double lse = M > -INFINITY ? (double)M + log((double)S) : NAN;
+      const double lse = M > -INFINITY ? (double)M + log_of(S) : NAN;
       const bool live = fabsf(was) < INFINITY && fabs(lse) < INFINITY;
       __syncwarp();
       // the parts' lists are in order: their heads are compared K times
@@ -199,7 +230,7 @@ __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
       if (lane < K) {
         // score + (z - lse) is (score - lse) + z but for a rounding of 2^-53
         s_c[b * K + lane] = live && mine ? f64_order(((double)was - lse) + (double)key_value(mine)) : 0ull;
-        s_v[b * K + lane] = argmax_key_id(mine);
+        s_v[b * K + lane] = mine ? b << 18 | argmax_key_id(mine) : 0;
       }
     }
     __syncthreads();
@@ -207,29 +238,32 @@ __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
       const unsigned long long mine = s_c[x];
       if (!mine) continue;
       // equal scores: the lower beam, then the lower token (logits apart may come out equal)
+      const int tie = s_v[x];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < B * K; ++j) {
         const unsigned long long o = s_c[j];
-        rank += o > mine || (o == mine && (j / K < x / K || (j / K == x / K && s_v[j] < s_v[x])));
+        rank += (o > mine) | ((o == mine) & (s_v[j] < tie));
       }
       if (rank < 2 * B) s_top[rank] = x;
     }
     __syncthreads();
     if (warp == 0) {                                       // lane = rank: which go on, which end
       const int x = lane < 2 * B ? s_top[lane] : -1;
-      const bool end = x >= 0 && a.eos_id >= 0 && s_v[x] == a.eos_id;
+      const int beam = x >= 0 ? s_v[x] >> 18 : 0, v = x >= 0 ? s_v[x] & 0x3FFFF : -1;
+      const bool end = x >= 0 && v == a.eos_id;
       const uint32_t lives = __ballot_sync(ALL, x >= 0 && !end), below = (1u << lane) - 1u;
       const int before = __popc(lives & below);            // beams found before this candidate
       const uint32_t endings = __ballot_sync(ALL, end && before < B && a.n_done);
       const int place = had + __popc(endings & below);
       const float score = x >= 0 ? (float)order_f64(s_c[x]) : -INFINITY;
       if (x >= 0 && !end && before < B) {
-        s_par[before] = x / K;
-        s_tok[before] = s_v[x];
+        s_par[before] = beam;
+        s_tok[before] = v;
         a.score_out[(size_t)i * B + before] = score;
       }
       if (((endings >> lane) & 1u) && place < a.max_done) {
-        s_dpar[place - had] = x / K;
+        s_dpar[place - had] = beam;
         s_dplace[place - had] = place;
         a.done_score[(size_t)i * a.max_done + place] = score;
         if (a.done_length) a.done_length[(size_t)i * a.max_done + place] = L;
@@ -312,7 +346,7 @@ Plan make_plan(const ws_beam_args& a) {
   const long long rows = (long long)a.n * a.beams;
   const int least = (a.vocab + BM_PART - 1) / BM_PART, most = min(BM_PARTS, (a.vocab + 4 * BM_NT - 1) / (4 * BM_NT));
   const int want = max(least, (int)min((long long)most, 12ll * 152 / rows));
-  q.part = ((a.vocab + want - 1) / want + BM_NT - 1) / BM_NT * BM_NT;
+  q.part = ((a.vocab + want - 1) / want + BM_STEP - 1) / BM_STEP * BM_STEP;
   q.parts = (a.vocab + q.part - 1) / q.part;
   q.stat = (size_t)rows * q.parts * (a.beams + 1) * 8;
   q.bytes = (q.stat + (size_t)rows * q.parts * 8 + 255) / 256 * 256;
@@ -341,7 +375,9 @@ extern "C" int ws_beam_select(const ws_beam_args* args, void* workspace, size_t 
   p.stat = (float2*)((char*)workspace + q.stat);
   const cudaStream_t s = (cudaStream_t)stream;
   const size_t list = (size_t)(args->beams + 1) * (q.part / BM_NT) * 8;      // at most 34 KB
-  scan_kernel<<<dim3((unsigned)q.parts, (unsigned)(args->n * args->beams)), BM_NT, list, s>>>(p);
+  const dim3 grid((unsigned)q.parts, (unsigned)(args->n * args->beams));
+  if (((reinterpret_cast<uintptr_t>(args->logits) >> 2) | (uint64_t)args->ld) & 1) scan_kernel<false><<<grid, BM_NT, list, s>>>(p);
+  else scan_kernel<true><<<grid, BM_NT, list, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) {
     ws_count_launches(1);
