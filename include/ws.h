@@ -724,7 +724,8 @@ typedef struct {
  * Every token v of every beam b is a candidate with
  *   score[b] + logits[b, v] - log sum_u exp(logits[b, u])
  * (equal: the lower beam, then the lower token); the sums of exponentials are
- * fp32 sums, the rest is in double.  In that order, candidates that are
+ * fp32 sums, and the scores are compared as sums of two fp32 numbers each.  In
+ * that order, candidates that are
  * eos_id join the finished transcripts (while there is room) and the others
  * become beams 0, 1, ..., until there are `beams` of them.  A transcript is
  * the parent's and the token; a finished one the parent's alone.

@@ -13,12 +13,12 @@
 // Their logits (K of the 128th parts, from L2) are read again, those not
 // behind T kept, and ranked by counting.
 //
-// merge_kernel.  One CTA per request: log-sum-exps of the beams (in double, as
-// are the candidates' scores: what differs from another beam's by less than
-// fp32's step is still told apart), the parts' candidates ranked within their beams, the beams' against
-// each other by whole numbers that order like the doubles, and the 2 * beams
-// best dealt out: candidates that end go to the finished transcripts.
-// Then each thread moves a column of the transcripts for all beams, so the
+// merge_kernel.  One CTA per request: log-sum-exps of the beams, candidates'
+// scores as two fp32 numbers each (what differs from another beam's by less
+// than fp32's step is still told apart), the parts' candidates in order within
+// their beams, the beams' against each other by whole numbers that order like
+// the scores, and the 2 * beams best dealt out: those that end go to the
+// finished transcripts.  Then each thread moves a column of the transcripts for all beams, so the
 // move may be in place.
 #include <string>
 
@@ -54,14 +54,31 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   const uint32_t u = (uint32_t)(k >> 32);
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
-// log of a positive fp32 number to 2^-25: its exponent's part in double, that of its significand in 0.75 .. 1.5 in fp32
-// (a logarithm in double took the merge 10 us of 15).
-__device__ __forceinline__ double log_of(float x) {
-  const int e = (int)(__float_as_uint(x) - 0x3F400000u) >> 23;
-  return (double)e * 0.69314718055994530942 + (double)logf(__uint_as_float(__float_as_uint(x) - ((uint32_t)e << 23)));
+// Scores are sums of two fp32 numbers, hi the sum rounded and lo what is left
+// (double is 64 times slower here: 10 of the merge's 15 us were its sums).
+struct Two { float hi, lo; };
+__device__ __forceinline__ Two two_sum(float a, float b) {           // exact (Knuth)
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two plus(Two a, float b) {
+  const Two s = two_sum(a.hi, b);
+  const float lo = __fadd_rn(s.lo, a.lo), hi = __fadd_rn(s.hi, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+// x - log(y), y > 0: exponent and significand (0.75 .. 1.5) of y apart, with log 2 in a part whose multiples are exact
+// and the rest; good to 2^-24 of the significand's logarithm.
+__device__ __forceinline__ Two less_log(Two x, float y) {
+  const int e = (int)(__float_as_uint(y) - 0x3F400000u) >> 23;
+  const float f = __uint_as_float(__float_as_uint(y) - ((uint32_t)e << 23));
+  return plus(plus(x, -(float)e * 0.693115234375f), -fmaf((float)e, 3.1946184945e-05f, logf(f)));
+}
+__device__ __forceinline__ unsigned long long two_order(Two x) {     // larger score, larger number
+  return (unsigned long long)f32_order(x.hi == 0.f ? 0.f : x.hi) << 32 | f32_order(x.lo == 0.f ? 0.f : x.lo);
 }
 __device__ __forceinline__ bool idle(const ws_beam_args& a, int i) {
-  return (a.n_done && a.n_done[i] >= a.max_done) || (a.tokens && a.length[i] >= a.capacity);
+  const bool full = a.n_done && a.n_done[i] >= a.max_done;
+  return (a.tokens && a.length[i] >= a.capacity) || full;  // both asked for at once
 }
 
 // Tokens v and v + 1 of a row, -inf behind v1.  PAIR: every row is 8-byte aligned.
@@ -86,14 +103,20 @@ __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
   if (idle(p.a, row / p.a.beams)) return;
   const float* z = p.a.logits + (size_t)row * (size_t)p.a.ld;
   const int v0 = blockIdx.x * p.part, v1 = min(V, v0 + p.part);
-  // ---- the stream: 2 U logits of a thread in flight
+  // ---- the stream: 2 U logits of a thread under way while 2 U are summed
   float m = -INFINITY, ref = 0.f, s = 0.f; // largest so far (ref: 0 until there is one); sum of exp(. - ref)
   int at = -1;                             // its token
   constexpr int U = 8;
+  float2 next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) next[u] = two_logits<PAIR>(z, v0 + 2 * tid + u * BM_STEP, v1);
   for (int v = v0 + 2 * tid; v < v1; v += U * BM_STEP) {
     float2 f[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) f[u] = two_logits<PAIR>(z, v + u * BM_STEP, v1);
+    for (int u = 0; u < U; ++u) f[u] = next[u];
+    if (v + U * BM_STEP < v1)
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u] = two_logits<PAIR>(z, v + (U + u) * BM_STEP, v1);
     float t = fmaxf(f[0].x, f[0].y);
 #pragma unroll
     for (int u = 1; u < U; ++u) t = fmaxf(t, fmaxf(f[u].x, f[u].y));
@@ -179,15 +202,6 @@ __global__ void __launch_bounds__(BM_NT) scan_kernel(const BeamP p) {
   if (tid >= n && tid < K) out[tid] = 0ull;
 }
 
-// Whole numbers that order like doubles (NaN does not occur).
-__device__ __forceinline__ unsigned long long f64_order(double d) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(d == 0.0 ? 0.0 : d);
-  return u >> 63 ? ~u : u | 1ull << 63;
-}
-__device__ __forceinline__ double order_f64(unsigned long long u) {
-  return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
-}
-
 __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
   extern __shared__ unsigned long long sm[];               // the parts' candidates [beams][parts * K]
   __shared__ unsigned long long s_c[BM_BEAMS * BM_K];      // a beam's K best: order of the score, 0: none
@@ -214,8 +228,8 @@ __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
       const float2 st = lane < p.parts ? p.stat[((size_t)i * B + b) * p.parts + lane] : make_float2(-INFINITY, 0.f);
       const float M = warp_max(st.x);
       const float S = warp_sum(st.x > -INFINITY ? st.y * exp_of(st.x - M) : st.y);
-      const double lse = M > -INFINITY ? (double)M + log_of(S) : NAN;
-      const bool live = fabsf(was) < INFINITY && fabs(lse) < INFINITY;
+      const bool live = fabsf(was) < INFINITY && fabsf(M) < INFINITY && S < INFINITY;
+      const Two off = live ? less_log(two_sum(was, -M), S) : Two{0.f, 0.f};
       __syncwarp();
       // the parts' lists are in order: their heads are compared K times
       unsigned long long head = lane < p.parts ? list[lane * K] : 0ull, mine = 0ull;
@@ -228,8 +242,8 @@ __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
         if (best && head == best) { ++at; head = at < K ? list[lane * K + at] : 0ull; }
       }
       if (lane < K) {
-        // score + (z - lse) is (score - lse) + z but for a rounding of 2^-53
-        s_c[b * K + lane] = live && mine ? f64_order(((double)was - lse) + (double)key_value(mine)) : 0ull;
+        const Two c = plus(off, key_value(mine));
+        s_c[b * K + lane] = live && mine && fabsf(c.hi) < INFINITY ? two_order(c) : 0ull;
         s_v[b * K + lane] = mine ? b << 18 | argmax_key_id(mine) : 0;
       }
     }
@@ -256,7 +270,7 @@ __global__ void __launch_bounds__(BM_MT) merge_kernel(const BeamP p) {
       const int before = __popc(lives & below);            // beams found before this candidate
       const uint32_t endings = __ballot_sync(ALL, end && before < B && a.n_done);
       const int place = had + __popc(endings & below);
-      const float score = x >= 0 ? (float)order_f64(s_c[x]) : -INFINITY;
+      const float score = x >= 0 ? key_value(s_c[x]) : -INFINITY;
       if (x >= 0 && !end && before < B) {
         s_par[before] = beam;
         s_tok[before] = v;
