@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int RO_NT = 256;
+constexpr int RO_NT = 128;
 constexpr int RO_BEAMS = 16;
 
 struct ReorderP {
@@ -23,7 +23,7 @@ struct ReorderP {
 template <int NB>
 __global__ void __launch_bounds__(RO_NT) reorder_kernel(const ReorderP p) {
   __shared__ int s_page[RO_BEAMS], s_slot[RO_BEAMS], s_par[RO_BEAMS], s_any;
-  const int tid = threadIdx.x, i = blockIdx.z, B = p.a.beams;
+  const int tid = threadIdx.x, i = blockIdx.y, B = p.a.beams;
   if (tid == 0) s_any = 0;
   __syncthreads();
   // the request's length is its first beam's; a beam of a bad slot stays out of it
@@ -42,40 +42,43 @@ __global__ void __launch_bounds__(RO_NT) reorder_kernel(const ReorderP p) {
   }
   __syncthreads();
   if (!s_any) return;
-  const int rows = 2 * p.c.n_kv_heads;
-  if ((int)blockIdx.y < rows) {
-    const bool v = (int)blockIdx.y >= p.c.n_kv_heads;
-    const int h = v ? blockIdx.y - p.c.n_kv_heads : blockIdx.y;
-    char* base = (char*)(v ? p.c.v : p.c.k);
-    const int es = p.c.dtype == WS_F32 ? 4 : p.c.dtype == WS_BF16 ? 2 : 1;
-    auto moves = [&](int b) { return b < B && s_par[b] != b && s_page[b] >= 0 && s_page[s_par[b]] >= 0; };
-    for (int x = blockIdx.x * RO_NT + tid; x < rest << p.ppr_log; x += gridDim.x * RO_NT) {
-      const size_t in = ((size_t)h * (size_t)p.c.head_stride + (size_t)(x >> p.ppr_log) * (size_t)p.c.token_stride) * es +
-                        (size_t)(x & ((1 << p.ppr_log) - 1)) * 16;
-      uint4 r[NB];
+  const int heads = p.c.n_kv_heads, lane0 = blockIdx.x * RO_NT + tid, step = gridDim.x * RO_NT;
+  const int es = p.c.dtype == WS_F32 ? 4 : p.c.dtype == WS_BF16 ? 2 : 1;
+  auto moves = [&](int b) { return b < B && s_par[b] != b && s_page[b] >= 0 && s_page[s_par[b]] >= 0; };
+  // 16-byte pieces, head by head of keys and of values
+  const long long per = (long long)rest << p.ppr_log, all = 2 * heads * per;
+  for (long long x = lane0; x < all; x += step) {
+    const int row = per == (int)per && all < (1ll << 31) ? (int)((uint32_t)x / (uint32_t)per) : (int)(x / per), y = (int)(x - row * per);
+    const bool v = row >= heads;
+    char* base = (char*)(v ? p.c.v : p.c.k) + ((size_t)(v ? row - heads : row) * (size_t)p.c.head_stride +
+                                               (size_t)(y >> p.ppr_log) * (size_t)p.c.token_stride) * es +
+                 (size_t)(y & ((1 << p.ppr_log) - 1)) * 16;
+    uint4 r[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (moves(b)) r[b] = *reinterpret_cast<const uint4*>(base + (size_t)s_page[s_par[b]] * (size_t)p.c.page_stride * es + in);
+    for (int b = 0; b < NB; ++b)
+      if (moves(b)) r[b] = *reinterpret_cast<const uint4*>(base + (size_t)s_page[s_par[b]] * (size_t)p.c.page_stride * es);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (moves(b)) *reinterpret_cast<uint4*>(base + (size_t)s_page[b] * (size_t)p.c.page_stride * es + in) = r[b];
-    }
-    if (p.c.dtype != WS_E4M3) return;
-    uint8_t* sc = (v ? p.c.v_scale : p.c.k_scale) + (size_t)h * (size_t)p.c.scale_head_stride;
+    for (int b = 0; b < NB; ++b)
+      if (moves(b)) *reinterpret_cast<uint4*>(base + (size_t)s_page[b] * (size_t)p.c.page_stride * es) = r[b];
+  }
+  if (p.c.dtype == WS_E4M3) {
     const int blocks = (rest + p.c.scale_block - 1) / p.c.scale_block;
-    for (int x = blockIdx.x * RO_NT + tid; x < blocks; x += gridDim.x * RO_NT) {
+    for (long long x = lane0; x < 2ll * heads * blocks; x += step) {
+      const int row = (int)(x / blocks);
+      const bool v = row >= heads;
+      uint8_t* sc = (v ? p.c.v_scale : p.c.k_scale) + (size_t)(v ? row - heads : row) * (size_t)p.c.scale_head_stride + (x - (long long)row * blocks);
       uint8_t r[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        if (moves(b)) r[b] = sc[(size_t)s_page[s_par[b]] * (size_t)p.c.scale_page_stride + x];
+        if (moves(b)) r[b] = sc[(size_t)s_page[s_par[b]] * (size_t)p.c.scale_page_stride];
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        if (moves(b)) sc[(size_t)s_page[b] * (size_t)p.c.scale_page_stride + x] = r[b];
+        if (moves(b)) sc[(size_t)s_page[b] * (size_t)p.c.scale_page_stride] = r[b];
     }
-    return;
   }
+  if (!p.a.page_table) return;
   // ---- the page table's rows, as far as pages are full
-  for (int x = blockIdx.x * RO_NT + tid; x < full; x += gridDim.x * RO_NT) {
+  for (int x = lane0; x < full; x += step) {
     int r[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -92,7 +95,6 @@ const char* check_reorder(const ws_paged_cache* c, const ws_reorder_args* a) {
   if (!a) return "null arguments";
   if (a->n_req < 0 || a->n_req > 65535) return "n_req must be 0..65535";
   if (a->beams < 1 || a->beams > RO_BEAMS) return "beams must be 1..16";
-  if (c->n_kv_heads > 32767) return "n_kv_heads must be at most 32767";
   if (c->page_size > 1 << 26) return "page_size must be at most 2^26";
   if (a->n_req == 0) return nullptr;
   if (!a->kv_len || !a->parent) return "null kv_len or parent";
@@ -118,9 +120,11 @@ extern "C" int ws_cache_reorder(const ws_paged_cache* cache, const ws_reorder_ar
   p.c = *cache;
   p.a = *args;
   p.ppr_log = cache->dtype == WS_F32 ? 4 : cache->dtype == WS_BF16 ? 3 : 2;
-  const long long pieces = (long long)cache->page_size << p.ppr_log;
-  const dim3 grid((unsigned)min(1024ll, (pieces + RO_NT - 1) / RO_NT),
-                  2u * (unsigned)cache->n_kv_heads + (args->page_table ? 1u : 0u), (unsigned)args->n_req);
+  // two rounds of CTAs (16 per SM), each with as much of a request as comes
+  // out: a CTA's look at lengths, parents and pages is a chain of latencies
+  // (a CTA per head: 96 requests x 5 beams x 80 heads 93 us, in this form 45)
+  const long long pieces = ((long long)cache->page_size << p.ppr_log) * 2 * cache->n_kv_heads;
+  const dim3 grid((unsigned)min((pieces + RO_NT - 1) / RO_NT, max(1ll, 32ll * 152 / args->n_req)), (unsigned)args->n_req);
   const cudaStream_t s = (cudaStream_t)stream;
   if (args->beams <= 4) launch<4>(p, grid, s);
   else if (args->beams <= 8) launch<8>(p, grid, s);
