@@ -2,32 +2,36 @@
 // keys and queries on the way (ws_cache_append in include/ws.h gives the
 // formulas).
 //
-// A CTA takes a tile of consecutive tokens of one request (in a cache in 8
-// bits one block of one scale, or 64 tokens of a longer one) and some of the
-// heads; a warp takes a head of queries, keys or values at a time: lane l
-// holds elements of token l / 8 + 4 j, so a warp's access covers whole rows.
-// The cosines and sines are computed once per tile into shared memory and
-// serve all its heads.  An angle is the 64-bit product of the position and
-// the turns per position, whose overflow drops whole turns exactly; its top 32
-// bits, as a fraction of half a turn, go through sincospif.  The rows are
-// asked for as soon as the chunk's place in them is known, before the angles.
-// In 8 bits the lanes find the block's largest value first (the rows stay in
-// registers), which gives the scale's exponent from the bits of the maximum;
-// then the elements are multiplied by a power of two (exact) and rounded
-// once.  Only where an older block's scale grows are its earlier tokens read.
+// A CTA takes a tile of up to 64 consecutive tokens of one request (in a cache
+// in 8 bits the tokens of one scale) and some of the heads.  A thread holds the
+// same eight elements of the same token in every head, so the cosines and
+// sines of its pairs are computed once, into registers.  An angle is the
+// 64-bit product of the position and the turns per position, whose overflow
+// drops whole turns exactly; its top 32 bits, as a fraction of half a turn, go
+// through sincospif.  Heads are taken AP_H at a time, the next ones' rows under
+// way meanwhile.  In 8 bits the CTA agrees on a head's largest value (as bits,
+// so that what is not finite shows), which gives the scale's exponent; then
+// the elements, still in registers, are multiplied by a power of two (exact)
+// and rounded once.  A block of more than 64 tokens is gone through twice, for
+// its largest values and for its codes.
+// HBM bounds it: 4 chunks of up to 2048 rows, 32 query and 8 key/value heads
+// (77 MB in 8 bits): see launch below.
 #include <string>
+#include <type_traits>
 
 #include "ws_paged.cuh"
 
 namespace {
 
-constexpr int AP_W = 8;                    // warps
-constexpr int AP_T = 64;                   // tokens at a time, at most
+constexpr int AP_T = 64;                   // tokens at a time, at most: eight threads each
+constexpr int AP_H = 4;                    // heads at a time
+constexpr int AP_MAX = 256;                // heads of a CTA, at most
 
 struct AppendP {
   ws_paged_cache c;
   ws_append_args a;
   int items;                               // heads of queries, keys and values
+  int per;                                 // of them per CTA
   int tile;                                // tokens per CTA
 };
 
@@ -52,17 +56,26 @@ __device__ __forceinline__ float2 from_e4m3_pair(uint32_t two) {
   return f;
 }
 
-// Eight elements of a row: four from o1 on and four from o2 on.
-struct Piece { int o1, o2, pair; bool turns; };           // the pairs (o1 + 0, + 1), ... or (o1 + e, o2 + e) are pair, pair + 1, ...
+// Eight elements of a row: four from o1 on and four from o2 on, which lie
+// together unless pairs are halves of the head.
+struct Piece { int o1, o2; bool together, turns; };
 template <class T> struct Raw;
 template <> struct Raw<bf16> { uint2 a, b; };
 template <> struct Raw<float> { float4 a, b; };
 
-template <class T>
-__device__ __forceinline__ void load_piece(const T* row, const Piece& pc, Raw<T>& r) {
-  using V = decltype(r.a);
-  r.a = *reinterpret_cast<const V*>(row + pc.o1);
-  r.b = *reinterpret_cast<const V*>(row + pc.o2);
+__device__ __forceinline__ void load_piece(const bf16* row, const Piece& pc, Raw<bf16>& r) {
+  if (pc.together) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + pc.o1);
+    r.a = make_uint2(v.x, v.y);
+    r.b = make_uint2(v.z, v.w);
+  } else {
+    r.a = *reinterpret_cast<const uint2*>(row + pc.o1);
+    r.b = *reinterpret_cast<const uint2*>(row + pc.o2);
+  }
+}
+__device__ __forceinline__ void load_piece(const float* row, const Piece& pc, Raw<float>& r) {
+  r.a = *reinterpret_cast<const float4*>(row + pc.o1);
+  r.b = *reinterpret_cast<const float4*>(row + pc.o2);
 }
 __device__ __forceinline__ float2 two(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); }
 __device__ __forceinline__ void unpack(const Raw<bf16>& r, float* x) {
@@ -77,34 +90,38 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ void store_piece(bf16* row, const Piece& pc, const float* x) {
-  *reinterpret_cast<uint2*>(row + pc.o1) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
-  *reinterpret_cast<uint2*>(row + pc.o2) = make_uint2(pack2(x[4], x[5]), pack2(x[6], x[7]));
+  const uint2 a = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3])), b = make_uint2(pack2(x[4], x[5]), pack2(x[6], x[7]));
+  if (pc.together) {
+    *reinterpret_cast<uint4*>(row + pc.o1) = make_uint4(a.x, a.y, b.x, b.y);
+  } else {
+    *reinterpret_cast<uint2*>(row + pc.o1) = a;
+    *reinterpret_cast<uint2*>(row + pc.o2) = b;
+  }
 }
 __device__ __forceinline__ void store_piece(float* row, const Piece& pc, const float* x) {
   *reinterpret_cast<float4*>(row + pc.o1) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(row + pc.o2) = make_float4(x[4], x[5], x[6], x[7]);
 }
-// The rotation of a piece; cs: cosines of its four pairs, then (AP_T * 32 floats on) their sines.
-__device__ __forceinline__ void turn(float* x, const float* cs, bool halves) {
-  const float4 c4 = *reinterpret_cast<const float4*>(cs), s4 = *reinterpret_cast<const float4*>(cs + AP_T * 32);
-  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-  float y[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float p = halves ? x[e] : x[2 * e], q = halves ? x[4 + e] : x[2 * e + 1];
-    const float u = p * c[e] - q * s[e], v = p * s[e] + q * c[e];
-    if (halves) { y[e] = u; y[4 + e] = v; } else { y[2 * e] = u; y[2 * e + 1] = v; }
+__device__ __forceinline__ void store_codes(uint8_t* row, const Piece& pc, uint32_t a, uint32_t b) {
+  if (pc.together) {
+    *reinterpret_cast<uint2*>(row + pc.o1) = make_uint2(a, b);
+  } else {
+    *reinterpret_cast<uint32_t*>(row + pc.o1) = a;
+    *reinterpret_cast<uint32_t*>(row + pc.o2) = b;
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = y[e];
+}
+// Four codes times f1 f2.
+__device__ __forceinline__ uint32_t move_codes(uint32_t w, float f1, float f2) {
+  const float2 a = from_e4m3_pair(w & 0xFFFFu), b = from_e4m3_pair(w >> 16);
+  return e4m3_pair(a.x * f1 * f2, a.y * f1 * f2) | e4m3_pair(b.x * f1 * f2, b.y * f1 * f2) << 16;
 }
 
-// NP pieces per lane: tiles of up to 4 * NP tokens at a time.
-template <class T, bool Q8, int NP>
-__global__ void __launch_bounds__(AP_W * 32, 2) append_kernel(const AppendP p) {
-  __shared__ __align__(16) float cs[2 * AP_T * 32];        // cosines, sines [token][pair]
-  __shared__ int page_of[AP_T];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+template <class T, bool Q8>
+__global__ void __launch_bounds__(8 * AP_T) append_kernel(const AppendP p) {
+  __shared__ uint32_t s_max[Q8 ? AP_MAX : 1];              // bits of the heads' largest finite |x|
+  __shared__ uint8_t s_was[Q8 ? AP_MAX : 1];               // scale bytes of the block before the call
+  __shared__ int s_odd;                                    // something is not finite
+  const int tid = threadIdx.x, lane = tid & 31, tokens = blockDim.x >> 3;      // tokens at a time
   const int i = blockIdx.z;
   const int slot = p.a.req_ids ? p.a.req_ids[i] : i;
   const int row0 = p.a.cu_q[i];
@@ -121,155 +138,156 @@ __global__ void __launch_bounds__(AP_W * 32, 2) append_kernel(const AppendP p) {
   const bool halves = p.a.rot_halves != 0;
   const int nq = p.a.q ? p.a.n_heads : 0, nk = p.c.n_kv_heads;
   const int pairs = p.a.turns ? p.a.rot_dims / 2 : 0;
+  const int item0 = blockIdx.y * p.per, item1 = min(item0 + p.per, p.items);
   Piece pc;
   {
-    const int a = lane & 7;
+    const int a = tid & 7;
     pc.turns = 8 * a < 2 * pairs;
-    pc.pair = 4 * a;
-    pc.o1 = halves && pc.turns ? 4 * a : 8 * a;
-    pc.o2 = halves && pc.turns ? pairs + 4 * a : 8 * a + 4;
+    pc.together = !(halves && pc.turns);
+    pc.o1 = pc.together ? 8 * a : 4 * a;
+    pc.o2 = pc.together ? 8 * a + 4 : pairs + 4 * a;
   }
-  // a tile longer than AP_T tokens (a long block of one scale) is gone through
-  // twice: for its largest values, then for its codes
-  const bool whole = !Q8 || p.tile <= 4 * NP;
-  __shared__ float s_max[Q8 ? 2 * 128 : 1];                // by key / value head of this CTA (long blocks)
-  const int first_item = blockIdx.y * AP_W + warp, step = gridDim.y * AP_W;
-  for (int pass = whole ? 1 : 0; pass < 2; ++pass)
-    for (long long sub = Q8 ? (lo - t0) / (4 * NP) * (4 * NP) : 0; sub < p.tile && t0 + sub < hi; sub += 4 * NP) {
-      const int base = (int)(t0 + sub);                    // first token of the visit (may lie before position 0)
-      const int from = max(lo, base), to = (int)min((long long)hi, (long long)base + 4 * NP);
-      __syncthreads();                                     // the last visit's angles have been read
-      Raw<T> raw[NP];
-      auto load = [&](int item) {
-        const bool isq = item < nq, isk = !isq && item < nq + nk;
-        const T* src = isq ? (const T*)p.a.q + (size_t)item * WS_DH
-                           : isk ? (const T*)p.a.k + (size_t)(item - nq) * WS_DH : (const T*)p.a.v + (size_t)(item - nq - nk) * WS_DH;
-        const int64_t ld = isq ? p.a.q_stride : isk ? p.a.k_stride : p.a.v_stride;
+  const bool whole = !Q8 || p.tile <= tokens;
+  const bool begins = !Q8 || t0 >= begin;                  // the block, with this call
+  // 8 bits: a block lies in one page
+  const int bp = Q8 ? paged_page(p.c, p.c.page_table, p.c.table_stride, slot, (int)t0) : -1;
+  auto scale_at = [&](int item) {                          // of a head of keys or values
+    const int h = item - nq < nk ? item - nq : item - nq - nk;
+    return (item - nq < nk ? p.c.k_scale : p.c.v_scale) + scale_off(p.c, bp, h, (int)t0);
+  };
+  if (Q8) {
+    for (int x = tid; x < item1 - item0; x += blockDim.x) {
+      s_max[x] = 0u;
+      s_was[x] = begins || bp < 0 || item0 + x < nq ? 0 : *scale_at(item0 + x);
+    }
+    if (tid == 0) s_odd = 0;
+    __syncthreads();
+  }
+  for (int pass = whole ? 1 : 0; pass < 2; ++pass) {
+    if (Q8 && !whole && pass == 1) __syncthreads();        // all largest values are known
+    for (long long sub = pass == 0 ? (lo - t0) / tokens * tokens : 0; sub < p.tile && t0 + sub < hi; sub += tokens) {
+      const long long t = t0 + sub + (tid >> 3);           // this thread's token
+      const bool live = t >= lo && t < hi, older = Q8 && t < begin;
+      const size_t row = live ? (size_t)(row0 + (t - start)) : 0;
+      const int page = Q8 ? bp : live ? paged_page(p.c, p.c.page_table, p.c.table_stride, slot, (int)t) : -1;
+      float cs[4], sn[4];
+      bool angles = false;                                 // known
+      // Heads h .. h1 - 1 of queries (0), keys (1) or values (2), of which m0 is the first one's place in s_max.
+      auto heads = [&](auto kind, int h, int h1, int m0) {
+        constexpr int KIND = decltype(kind)::value;
+        if (h >= h1 || (KIND == 0 && pass == 0)) return;
+        const T* src = (const T*)(KIND == 0 ? p.a.q : KIND == 1 ? p.a.k : p.a.v) +
+                       row * (size_t)(KIND == 0 ? p.a.q_stride : KIND == 1 ? p.a.k_stride : p.a.v_stride) + (size_t)h * WS_DH;
+        Raw<T> raw[AP_H];
+        auto load = [&](int n) {
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const int t = base + 4 * j + (lane >> 3);
-          if (t >= from && t < to) load_piece(src + (size_t)(row0 + (t - start)) * ld, pc, raw[j]);
-          else raw[j] = Raw<T>{};
-        }
-      };
-      if (first_item < p.items) load(first_item);          // under the angles
-      for (int x = tid; x < (to - from) * pairs; x += AP_W * 32) {
-        const int t = x / pairs, f = x - t * pairs;
-        const int m = p.a.pos ? p.a.pos[row0 + (from + t - start)] : from + t;
-        const uint64_t phase = (uint64_t)(int64_t)m * p.a.turns[f];
-        float s_, c_;
-        sincospif((float)(int32_t)(uint32_t)(phase >> 32) * (1.f / 2147483648.f), &s_, &c_);
-        cs[(from - base + t) * 32 + f] = c_;
-        cs[AP_T * 32 + (from - base + t) * 32 + f] = s_;
-      }
-      for (int x = tid; x < to - from; x += AP_W * 32)
-        page_of[from - base + x] = paged_page(p.c, p.c.page_table, p.c.table_stride, slot, from + x);
-      __syncthreads();
-      for (int item = first_item, n = 0; item < p.items; item += step, ++n) {
-        if (n) load(item);
-        const bool isq = item < nq, isk = !isq && item < nq + nk;
-        const bool turned = pc.turns && (isq || isk);
-        auto values = [&](int j, float* x) {
-          unpack(raw[j], x);
-          if (turned) turn(x, cs + (4 * j + (lane >> 3)) * 32 + pc.pair, halves);
+          for (int u = 0; u < AP_H; ++u) {
+            raw[u] = Raw<T>{};
+            if (u < n && live) load_piece(src + u * WS_DH, pc, raw[u]);
+          }
+          src += AP_H * WS_DH;
         };
-        if (isq) {
-          if (pass == 0) continue;
+        load(h1 - h);                                      // under the angles
+        if (KIND < 2 && !angles && pc.turns && live) {
+          const int m = p.a.pos ? p.a.pos[row] : (int)t;
 #pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            const int t = base + 4 * j + (lane >> 3);
-            if (t < from || t >= to) continue;
-            float x[8];
-            values(j, x);
-            store_piece((T*)p.a.q_out + (size_t)(row0 + (t - start)) * p.a.q_out_stride + (size_t)item * WS_DH, pc, x);
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t phase = (uint64_t)(int64_t)m * p.a.turns[4 * (tid & 7) + e];
+            sincospif((float)(int32_t)(uint32_t)(phase >> 32) * (1.f / 2147483648.f), &sn[e], &cs[e]);
           }
-          continue;
         }
-        const int h = isk ? item - nq : item - nq - nk;
-        if (!Q8) {
-          T* dst = (T*)(isk ? p.c.k : p.c.v);
-#pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            const int t = base + 4 * j + (lane >> 3);
-            if (t < from || t >= to) continue;
-            const int page = page_of[t - base];
-            if (page < 0) continue;
-            float x[8];
-            values(j, x);
-            store_piece(dst + paged_off(p.c, page, h, t), pc, x);
-          }
-          continue;
+        if (KIND < 2) angles = true;
+        T* to = KIND == 0 ? (T*)p.a.q_out + row * (size_t)p.a.q_out_stride : (T*)(KIND == 1 ? p.c.k : p.c.v);
+        uint8_t* to8 = (uint8_t*)(KIND == 1 ? p.c.k : p.c.v);
+        if (KIND > 0 && page >= 0 && (live || older)) {
+          const size_t off = paged_off(p.c, page, 0, (int)t);
+          to += off;
+          to8 += off;
         }
-        // ---- 8 bits.  A block lies in one page.
-        const int page = page_of[from - base];
-        if (page < 0) continue;
-        uint8_t* dst = (uint8_t*)(isk ? p.c.k : p.c.v) + paged_off(p.c, page, h, (int)t0);
-        uint8_t* scale = (isk ? p.c.k_scale : p.c.v_scale) + scale_off(p.c, page, h, (int)t0);
-        const bool begins = t0 >= begin;                   // with this call
-        const int e_was = begins ? -127 : (int)*scale - 127;
-        float m = 0.f;
-        bool odd = false;
-        if (whole || pass == 0) {
+        const size_t step = KIND == 0 ? WS_DH : (size_t)p.c.head_stride;   // from a head to the next
+        to += (size_t)h * step;
+        to8 += (size_t)h * step;
+        for (; h < h1; h += AP_H, m0 += AP_H) {
+          float x[AP_H][8];
 #pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            float x[8];
-            values(j, x);                                  // rows that are not there are zero
+          for (int u = 0; u < AP_H; ++u) unpack(raw[u], x[u]);
+          if (h + AP_H < h1) load(h1 - h - AP_H);
+          if (KIND < 2 && pc.turns) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float y = fabsf(x[e]);
-              odd |= !(y < INFINITY);
-              m = fmaxf(m, y < INFINITY ? y : 0.f);
-            }
+            for (int u = 0; u < AP_H; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // (x[2 e], x[2 e + 1]) or (x[e], x[4 + e]): the places are the compiler's to know
+                const float a = halves ? x[u][e] : x[u][2 * e], b = halves ? x[u][4 + e] : x[u][2 * e + 1];
+                const float v = a * cs[e] - b * sn[e], w = a * sn[e] + b * cs[e];
+                if (halves) { x[u][e] = v; x[u][4 + e] = w; } else { x[u][2 * e] = v; x[u][2 * e + 1] = w; }
+              }
           }
+          if (KIND == 0 || !Q8) {
 #pragma unroll
-          for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-          odd = __any_sync(0xffffffffu, odd);
-          if (!whole) {
-            if (lane == 0) s_max[n * AP_W + warp] = from == lo ? m : fmaxf(s_max[n * AP_W + warp], m);
-            __syncwarp();
+            for (int u = 0; u < AP_H; ++u)
+              if (h + u < h1 && live && (KIND == 0 || page >= 0)) store_piece(to + u * step, pc, x[u]);
+            to += AP_H * step;
             continue;
           }
-        } else {
-          m = s_max[n * AP_W + warp];
-          odd = true;
-        }
-        const int e_now = max(e_was, scale_exponent(m));
-        const float f = pow2(-e_now);
+          if (whole || pass == 0) {
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const int t = base + 4 * j + (lane >> 3);
-          if (t < from || t >= to) continue;
-          float x[8];
-          values(j, x);
+            for (int u = 0; u < AP_H; ++u) {               // rows and heads that are not there are zero
+              uint32_t m = 0u;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float y = x[e] * f;
-            x[e] = odd && !(fabsf(x[e]) < INFINITY) ? NAN : y;
-          }
-          uint8_t* at = dst + (size_t)(t - (int)t0) * (size_t)p.c.token_stride;
-          *reinterpret_cast<uint32_t*>(at + pc.o1) = e4m3_pair(x[0], x[1]) | e4m3_pair(x[2], x[3]) << 16;
-          *reinterpret_cast<uint32_t*>(at + pc.o2) = e4m3_pair(x[4], x[5]) | e4m3_pair(x[6], x[7]) << 16;
-        }
-        if (from != lo) continue;                          // once per block and head
-        if (!begins && e_now > e_was) {                    // move the earlier tokens to the new scale
-          const int down = e_was - e_now, half = down / 2;
-          const float f1 = pow2(half), f2 = pow2(down - half);
-          for (int x = lane; x < (begin - (int)t0) * 4; x += 32) {
-            uint4* at = reinterpret_cast<uint4*>(dst + (size_t)(x >> 2) * (size_t)p.c.token_stride) + (x & 3);
-            uint4 v = *at;
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[u][e]) & 0x7FFFFFFFu);
+              m = __reduce_max_sync(0xffffffffu, live ? m : 0u);
+              if (m >= 0x7F800000u) {
+                s_odd = 1;
+                m = 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float2 a = from_e4m3_pair(w[e] & 0xFFFFu), b = from_e4m3_pair(w[e] >> 16);
-              w[e] = e4m3_pair(a.x * f1 * f2, a.y * f1 * f2) | e4m3_pair(b.x * f1 * f2, b.y * f1 * f2) << 16;
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t y = __float_as_uint(x[u][e]) & 0x7FFFFFFFu;
+                  if (live && y < 0x7F800000u) m = max(m, y);
+                }
+                m = __reduce_max_sync(0xffffffffu, m);
+              }
+              if (lane == 0 && h + u < h1) atomicMax(&s_max[m0 + u], m);
             }
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            if (pass == 0) continue;
+            __syncthreads();
           }
+          const bool odd = s_odd != 0;
+          if (page >= 0 && (live || older)) {
+#pragma unroll
+            for (int u = 0; u < AP_H; ++u) {
+              if (h + u >= h1) continue;
+              const int e_was = (int)s_was[m0 + u] - 127;
+              const int e_now = max(e_was, scale_exponent(__uint_as_float(s_max[m0 + u])));
+              uint8_t* at = to8 + u * step;
+              if (live) {
+                const float f = __uint_as_float((uint32_t)(127 - min(e_now, 126)) << 23);    // 2^-e_now
+                if (odd)
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) x[u][e] = fabsf(x[u][e]) < INFINITY ? x[u][e] : NAN;
+                store_codes(at, pc, e4m3_pair(x[u][0] * f, x[u][1] * f) | e4m3_pair(x[u][2] * f, x[u][3] * f) << 16,
+                            e4m3_pair(x[u][4] * f, x[u][5] * f) | e4m3_pair(x[u][6] * f, x[u][7] * f) << 16);
+              } else if (e_now > e_was) {                  // earlier tokens of the block: to the new scale
+                const int down = e_was - e_now, half = down / 2;
+                const float f1 = pow2(half), f2 = pow2(down - half);
+                const uint32_t a = *reinterpret_cast<const uint32_t*>(at + pc.o1), b = *reinterpret_cast<const uint32_t*>(at + pc.o2);
+                store_codes(at, pc, move_codes(a, f1, f2), move_codes(b, f1, f2));
+              }
+            }
+          }
+          to8 += AP_H * step;
         }
-        __syncwarp();                                      // every lane has read the old scale
-        if (lane == 0 && (begins || e_now > e_was)) *scale = (uint8_t)(e_now + 127);
-      }
+      };
+      heads(std::integral_constant<int, 0>(), item0, min(item1, nq), 0);
+      heads(std::integral_constant<int, 1>(), max(item0 - nq, 0), min(item1 - nq, nk), max(nq - item0, 0));
+      heads(std::integral_constant<int, 2>(), max(item0 - nq - nk, 0), item1 - nq - nk, max(nq + nk - item0, 0));
     }
+  }
+  if (!Q8 || bp < 0) return;
+  for (int x = tid; x < item1 - item0; x += blockDim.x) {  // the scales: their old ones have been read
+    const int e_was = (int)s_was[x] - 127, e_now = max(e_was, scale_exponent(__uint_as_float(s_max[x])));
+    if (item0 + x >= nq && (begins || e_now > e_was)) *scale_at(item0 + x) = (uint8_t)(e_now + 127);
+  }
 }
 
 const char* check_append(const ws_paged_cache* c, const ws_append_args* a) {
@@ -315,21 +333,11 @@ const char* check_append(const ws_paged_cache* c, const ws_append_args* a) {
   return nullptr;
 }
 
-template <class T, bool Q8, int NP>
-cudaError_t launch(const AppendP& p, dim3 grid, cudaStream_t s) {
-  append_kernel<T, Q8, NP><<<grid, AP_W * 32, 0, s>>>(p);
+template <class T, bool Q8>
+cudaError_t launch(const AppendP& p, dim3 grid, int tokens, cudaStream_t s) {
+  append_kernel<T, Q8><<<grid, 8 * tokens, 0, s>>>(p);
   ws_count_launches(1);
   return cudaGetLastError();
-}
-template <class T, bool Q8>
-cudaError_t launch_np(const AppendP& p, dim3 grid, cudaStream_t s) {
-  if (p.tile <= 4) return launch<T, Q8, 1>(p, grid, s);
-  if (p.tile <= 8) return launch<T, Q8, 2>(p, grid, s);
-  if constexpr (Q8) {
-    if (p.tile > 32) return launch<T, Q8, 16>(p, grid, s);
-    if (p.tile > 16) return launch<T, Q8, 8>(p, grid, s);
-  }
-  return launch<T, Q8, 4>(p, grid, s);
 }
 
 }  // namespace
@@ -344,19 +352,24 @@ extern "C" int ws_cache_append(const ws_paged_cache* cache, const ws_append_args
   p.a = *args;
   const bool q8 = cache->dtype == WS_E4M3;
   p.items = (args->q ? args->n_heads : 0) + 2 * cache->n_kv_heads;
-  p.tile = q8 ? cache->scale_block : args->max_q <= 4 ? 4 : args->max_q <= 8 ? 8 : 16;
+  // tokens at a time: 8, 16, 32 or 64 that hold the block, or some of the chunk
+  int tokens = 8;
+  const int want = q8 ? cache->scale_block : min(args->max_q, 32);
+  while (tokens < want && tokens < AP_T) tokens *= 2;
+  p.tile = q8 ? cache->scale_block : tokens;
   const long long tiles = q8 ? ((long long)args->max_q + p.tile - 2) / p.tile + 1 : (args->max_q + p.tile - 1) / p.tile;
-  // a warp takes one head where there are few tiles; else as many as leave four CTAs per SM
-  const int most = (p.items + AP_W - 1) / AP_W;
+  // heads split over CTAs until there are about eight CTAs' worth of 128 threads per SM
   const long long units = tiles * args->n_req;
-  int groups = (int)min((long long)most, max(1ll, (4ll * 152 + units - 1) / units));
-  // heads of a long block whose largest values a CTA keeps: 32 per warp
-  if (q8) groups = max(groups, (p.items + 32 * AP_W - 1) / (32 * AP_W));
+  const int most = (p.items + AP_H - 1) / AP_H, least = (p.items + AP_MAX - 1) / AP_MAX;
+  const long long wanted = (8ll * 152 * 16 / tokens + units - 1) / units;
+  int groups = (int)max((long long)least, min((long long)most, wanted));
+  p.per = ((p.items + groups - 1) / groups + AP_H - 1) / AP_H * AP_H;
+  groups = (p.items + p.per - 1) / p.per;
   if (tiles > 2147483647ll || groups > 65535) return paged_fail(WS_EINVAL, "too many tiles or heads");
   const dim3 grid((unsigned)tiles, (unsigned)groups, (unsigned)args->n_req);
-  const cudaError_t e = q8 ? launch_np<bf16, true>(p, grid, (cudaStream_t)stream)
-                           : cache->dtype == WS_BF16 ? launch_np<bf16, false>(p, grid, (cudaStream_t)stream)
-                                                     : launch_np<float, false>(p, grid, (cudaStream_t)stream);
+  const cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = q8 ? launch<bf16, true>(p, grid, tokens, s)
+                           : cache->dtype == WS_BF16 ? launch<bf16, false>(p, grid, tokens, s) : launch<float, false>(p, grid, tokens, s);
   if (e != cudaSuccess) return paged_fail(WS_ECUDA, std::string("cache append launch: ") + cudaGetErrorString(e));
   return WS_OK;
 }
