@@ -14,8 +14,9 @@
 // the elements, still in registers, are multiplied by a power of two (exact)
 // and rounded once.  A block of more than 64 tokens is gone through twice, for
 // its largest values and for its codes.
-// HBM bounds it: 4 chunks of up to 2048 rows, 32 query and 8 key/value heads
-// (77 MB in 8 bits): see launch below.
+// 4 chunks of up to 2048 rows, 32 query and 8 key/value heads in 8 bits (77 MB):
+// 24.6 us, 3.1 TB/s; the copy rate would take 11.  What is left is latency: a
+// tile's chain of lengths, page and rows, and the agreement on the scales.
 #include <string>
 #include <type_traits>
 
@@ -24,7 +25,7 @@
 namespace {
 
 constexpr int AP_T = 64;                   // tokens at a time, at most: eight threads each
-constexpr int AP_H = 4;                    // heads at a time
+constexpr int AP_H = 2;                    // heads at a time (4, one CTA of 512 threads per SM: 29 us for 24.6)
 constexpr int AP_MAX = 256;                // heads of a CTA, at most
 
 struct AppendP {
@@ -117,7 +118,7 @@ __device__ __forceinline__ uint32_t move_codes(uint32_t w, float f1, float f2) {
 }
 
 template <class T, bool Q8>
-__global__ void __launch_bounds__(8 * AP_T) append_kernel(const AppendP p) {
+__global__ void __launch_bounds__(8 * AP_T, 2) append_kernel(const AppendP p) {
   __shared__ uint32_t s_max[Q8 ? AP_MAX : 1];              // bits of the heads' largest finite |x|
   __shared__ uint8_t s_was[Q8 ? AP_MAX : 1];               // scale bytes of the block before the call
   __shared__ int s_odd;                                    // something is not finite
@@ -358,10 +359,12 @@ extern "C" int ws_cache_append(const ws_paged_cache* cache, const ws_append_args
   while (tokens < want && tokens < AP_T) tokens *= 2;
   p.tile = q8 ? cache->scale_block : tokens;
   const long long tiles = q8 ? ((long long)args->max_q + p.tile - 2) / p.tile + 1 : (args->max_q + p.tile - 1) / p.tile;
-  // heads split over CTAs until there are about eight CTAs' worth of 128 threads per SM
+  // Heads split over CTAs until there are eight times the threads an SM holds:
+  // more CTAs hide each other's chains of lengths, pages and rows, and compute
+  // more angles (chunks of up to 2048 rows, a quarter of that 24.6 us, twice 26.8)
   const long long units = tiles * args->n_req;
   const int most = (p.items + AP_H - 1) / AP_H, least = (p.items + AP_MAX - 1) / AP_MAX;
-  const long long wanted = (8ll * 152 * 16 / tokens + units - 1) / units;
+  const long long wanted = (16ll * 152 * 16 / tokens + units - 1) / units;
   int groups = (int)max((long long)least, min((long long)most, wanted));
   p.per = ((p.items + groups - 1) / groups + AP_H - 1) / AP_H * AP_H;
   groups = (p.items + p.per - 1) / p.per;

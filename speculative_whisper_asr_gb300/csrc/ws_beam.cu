@@ -324,6 +324,11 @@ int fail(int code, const char* msg) {
   return code;
 }
 
+bool apart(const void* a, const void* b, long long bytes_a, long long bytes_b) {
+  const char *x = (const char*)a, *y = (const char*)b;
+  return !x || !y || x + bytes_a <= y || y + bytes_b <= x;
+}
+
 const char* check_beam(const ws_beam_args* a) {
   if (!a) return "null arguments";
   if (a->n < 0) return "n must be >= 0";
@@ -348,6 +353,14 @@ const char* check_beam(const ws_beam_args* a) {
   } else if (a->n_done_out || a->done_score || a->done_length || a->done_tokens) {
     return "finished transcripts need n_done";
   }
+  const long long rows = 4ll * a->n * a->beams, reqs = 4ll * a->n, text = a->tokens ? rows * a->capacity : 0;
+  auto in_place = [](const void* in, const void* out, long long bytes) { return in == out || apart(in, out, bytes, bytes); };
+  if (!in_place(a->score, a->score_out, rows) || !in_place(a->tokens, a->tokens_out, text) ||
+      !in_place(a->length, a->length_out, reqs) || !in_place(a->n_done, a->n_done_out, reqs))
+    return "score_out, tokens_out, length_out and n_done_out must be score, tokens, length and n_done or share no elements with them";
+  const long long done = reqs * a->max_done * (a->tokens ? a->capacity : 0);
+  if (!apart(a->done_tokens, a->tokens, done, text) || !apart(a->done_tokens, a->tokens_out, done, text))
+    return "done_tokens must share no elements with tokens and tokens_out";
   return nullptr;
 }
 
