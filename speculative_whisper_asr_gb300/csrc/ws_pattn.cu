@@ -796,6 +796,8 @@ cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int 
   p.nsplit = q.nsplit; p.tps = q.tps; p.geo = q.geo;
   p.lse = args.lse ? args.lse : args.mass && !q.fa && !q.rows.join ? (float*)(ws + q.lse) : nullptr;
   p.row_tiles = q.row_tiles;
+  if (cache.dtype == WS_E4M3 && cache.scale_block > 1)
+    p.block_mul = (uint32_t)(((1ull << 32) + cache.scale_block - 1) / cache.scale_block);
   if (q.fa && args.mass) { p.nl = (float*)(ws + q.nl); p.next_item = (unsigned long long*)(ws + q.next); }
   if (q.parts) { p.part_ml = (float2*)(ws + q.ml); p.part_o = (float*)(ws + q.o); }
   return cache.dtype == WS_BF16 ? run_bf16(p, q, s) : cache.dtype == WS_E4M3 ? run_8bit(p, q, s) : run_f32(p, q, s);

@@ -205,4 +205,4 @@ cudaError_t launch_f32_mass(const AttnP& p, int rpt, cudaStream_t s);
 
 // Caches in 8 bits (ws_pattn_q8.cu): row tiles of 8 * nt rows that stream the cache.
 constexpr int Q8_TK = 32;                          // keys per tile
-cudaError_t launch_q8(AttnP p, int nt, cudaStream_t s);
+cudaError_t launch_q8(const AttnP& p, int nt, cudaStream_t s);

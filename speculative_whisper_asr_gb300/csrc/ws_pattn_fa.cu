@@ -358,6 +358,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   // W = 2: keys by warp 0, values by warp 2, each with its scales; W = 1: both by warp 0
   auto copy_codes = [&](bool keys, bool values) {
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
+    const uint8_t* k_scales = p.c.k_scale + (size_t)h * (size_t)p.c.scale_head_stride;
+    const uint8_t* v_scales = p.c.v_scale + (size_t)h * (size_t)p.c.scale_head_stride;
     int page = tile_page(p, table, lo, lane), issued = 0;
     uint32_t kb[4] = {}, vb[4] = {};               // scale bytes of the tile asked for last
     auto keep_scales = [&](int slot) {
@@ -403,11 +405,12 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         kb[q] = GROUPS ? 127u : 0u;                // of keys that do not count, whose scores are -inf: any but 0
         vb[q] = 0u;
         if ((valid >> (x & 31)) & 1u) {
-          const int tok = p.geo.tpp ? f.tok + x : x & ((1 << p.geo.page_log) - 1);
-          const size_t at = (size_t)pg * (size_t)p.c.scale_page_stride + (size_t)h * (size_t)p.c.scale_head_stride +
-                            (size_t)(tok / p.c.scale_block);
-          if (keys) kb[q] = __ldg(p.c.k_scale + at);
-          if (values) vb[q] = __ldg(p.c.v_scale + at);
+          const uint32_t tok = (uint32_t)(p.geo.tpp ? f.tok + x : x & ((1 << p.geo.page_log) - 1));
+          uint32_t b = p.block_mul ? __umulhi(tok, p.block_mul) : tok;     // tok / scale_block, or one more
+          b -= b * (uint32_t)p.c.scale_block > tok;
+          const uint64_t at = (uint64_t)(uint32_t)pg * (uint32_t)p.c.scale_page_stride + b;
+          if (keys) kb[q] = __ldg(k_scales + at);
+          if (values) vb[q] = __ldg(v_scales + at);
         }
       }
     }

@@ -527,13 +527,11 @@ cudaError_t run(const AttnP& p, int nt, const TcMap& mk, const TcMap& mv, cudaSt
 
 }  // namespace
 
-cudaError_t launch_q8(AttnP p, int nt, cudaStream_t s) {
+cudaError_t launch_q8(const AttnP& p, int nt, cudaStream_t s) {
   TcMap mk, mv;
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
     return cudaErrorInvalidValue;
-  const int block = p.c.scale_block;
-  p.block_mul = block == 1 ? 0u : (uint32_t)(((1ull << 32) + block - 1) / block);
-  const bool mix = p.a.causal && p.a.max_q > 1, uni = block % TK == 0;
+  const bool mix = p.a.causal && p.a.max_q > 1, uni = p.c.scale_block % TK == 0;
   if (mix) return uni ? run<true, true>(p, nt, mk, mv, s) : run<true, false>(p, nt, mk, mv, s);
   return uni ? run<false, true>(p, nt, mk, mv, s) : run<false, false>(p, nt, mk, mv, s);
 }
