@@ -433,7 +433,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         if (lane == 0) { meta[s].base = base; meta[s].full = all; }
         if (GROUPS && lane < 8) s_ks[s][lane] = scale_of(s_scale[0][slot][lane]);
       }
-#pragma unroll 1
+#pragma unroll 1                               // unrolled, it overflows the instruction cache (4 x 2048 rows: 404 us)
       for (int q = 0; q < NG; ++q) {
         const int x = 8 * (ci + NC * q) + (lane >> 2);             // this lane's row, and 16 bytes of it
         const uint8_t* src = codes(slot) + x * WS_DH + (((lane & 3) ^ ((x >> 1) & 3)) << 4);
@@ -687,6 +687,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
       const float* ks = s_ks[GROUPS ? j % NST : 0];
       float2 sum2[2];
+      float slk[8];                                // of the groups; not 0, which times -inf would be NaN
+#pragma unroll
+      for (int g = 0; g < 8; ++g) slk[g] = GROUPS ? fmaxf(sl * ks[g], 1.17549435e-38f) : sl;
       auto weigh = [&]() {
         const float2 nm2 = make_float2(-msl, -msl);
         sum2[0] = sum2[1] = make_float2(0.f, 0.f);
@@ -695,9 +698,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           uint32_t u[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            // not 0, which times -inf would be NaN
-            const float slk = GROUPS ? fmaxf(sl * ks[2 * q + (e >> 3)], 1.17549435e-38f) : sl;
-            float2 y = __ffma2_rn(make_float2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), GROUPS ? make_float2(slk, slk) : sl2, nm2);
+            const float s1 = slk[2 * q + (e >> 3)];
+            float2 y = __ffma2_rn(make_float2(sv[32 * q + 2 * e], sv[32 * q + 2 * e + 1]), GROUPS ? make_float2(s1, s1) : sl2, nm2);
             y.x = ex2(y.x);
             y.y = ex2(y.y);
             sum2[e & 1] = __fadd2_rn(sum2[e & 1], y);
@@ -746,21 +748,10 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         }
       };
       auto passed = [&]() { return __any_sync(0xffffffffu, on && (m == -INFINITY || !(tile < MOST))) != 0; };
-      if (Q8) {
-        // in one place each: beside the converters' code, two of each overflow
-        // the instruction cache (4 x 2048 rows: 404 us, 309 in this form)
-#pragma unroll 1
-        for (bool first = j == 0;; first = true) {
-          if (first) look();
-          tile = weigh();
-          if (first || !passed()) break;
-        }
-      } else {
-        if (j > 0) tile = weigh();
-        if (j == 0 || passed()) {
-          look();
-          tile = weigh();
-        }
+      if (j > 0) tile = weigh();
+      if (j == 0 || passed()) {
+        look();
+        tile = weigh();
       }
       l += tile;
       st_wait();

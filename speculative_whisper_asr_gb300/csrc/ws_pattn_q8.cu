@@ -196,11 +196,20 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
     }
   };
   w.start(p.geo, split * p.tps + warp, W);
+  uint32_t first_k[NS], first_v[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s)
     if (s < n_my) {
       issue(s, page0[s]);
       w.next(p.geo);
+      first_k[s] = k_byte;
+      first_v[s] = v_byte;
+    }
+#pragma unroll
+  for (int s = 0; s < NS; ++s)             // behind the last copy: they wait for the scales
+    if (s < n_my) {
+      k_byte = first_k[s];
+      v_byte = first_v[s];
       keep_scales(s);
     }
   int page_next = page_of();               // of the tile asked for next: looked up a tile ahead
