@@ -238,6 +238,104 @@ def test_attend_8bit_scales_far_apart(R, chunks):
     check_q8(R, cs)
 
 
+@pytest.mark.parametrize("page,block", [(64, 16), (40, 8)])
+@pytest.mark.parametrize("chunks,lens", [([1], [3000]), ([12], [2500]), ([50], [3000]), ([90, 70], [2900, 1500]), ([60], [4000])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_8bit_in_parts(R, page, block, chunks, lens, causal):
+    """Caches long enough that a row's positions are split over CTAs."""
+    check_q8(R, Q8Case(chunks, lens, 2, 1, page, block=block, causal=causal, seed=len(chunks) + page))
+
+
+def test_calls_on_other_streams(R):
+    """Calls on two streams, with an object each, between calls on the current one: the same bits."""
+    cs = Q8Case([5, 60], [700, 900], 4, 2, 32, block=16, seed=6)
+    x = make_beam(4, 5, 5000, 8, 3, 1)
+    z, sc = x["logits"].cuda(), x["score"].cuda()
+    par, tok = (torch.zeros(4, 5, dtype=torch.int32, device="cuda") for _ in range(2))
+    search = R.BeamSearch(eos_id=3)
+
+    def attend(c):
+        return c.attend(cs.q, cs.kv_len, cs.cu, max_q=60, max_kv=900)
+
+    def select(s):
+        out = sc.clone()
+        s.select(z, out, par, tok)
+        return out
+    first, pick = attend(cs.cache(R)), select(search)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+            with torch.cuda.stream(s):
+                got.append((attend(cs.cache(R)), select(R.BeamSearch(eos_id=3))))
+        attend(cs.cache(R))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[: cs.rows], first[: cs.rows]) and torch.equal(b, pick) for a, b in got)
+    for s in (torch.cuda.Stream(), torch.cuda.current_stream()):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            again = select(search)                         # one object, scratch of its own per stream
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        assert torch.equal(again, pick)
+
+
+def test_refusals_of_tensors(R):
+    """What the objects check themselves: types, shapes, devices and strides of tensors."""
+    pool = Pool(2, 3, 4, 32, DT["e4m3"], 16, seed=1)
+    k8, sc = pool.k, pool.scales
+    for bad in (dict(), dict(k_scale=sc[0]), dict(k_scale=sc[0], v_scale=sc[1].float()), dict(k_scale=sc[0], v_scale=sc[1, :, :, :1]),
+                dict(k_scale=sc[0, :2], v_scale=sc[1, :2]), dict(k_scale=sc[0].cpu(), v_scale=sc[1].cpu()),
+                dict(k_scale=sc[0, :, :, :0], v_scale=sc[1, :, :, :0])):
+        with pytest.raises(ValueError):
+            R.PagedCache(k8, pool.v, pool.table, **bad)
+    with pytest.raises(ValueError):
+        R.PagedCache(k8.view(torch.uint8), pool.v.view(torch.uint8), pool.table, k_scale=sc[0], v_scale=sc[1])
+    bf = Pool(2, 3, 4, 32, DT["bf16"], seed=1)
+    with pytest.raises(ValueError):
+        R.PagedCache(bf.k, bf.v, bf.table, k_scale=sc[0], v_scale=sc[1])
+    c = pool.cache(R)
+    k, q = torch.randn(5, 4, D, device="cuda").bfloat16(), torch.randn(5, 8, D, device="cuda").bfloat16()
+    cu, L = i32([0, 2, 5]), i32([7, 9])
+    good = dict(max_q=3, q=q, rotation=R.Rotation())
+    c.append(k, k, L, cu, **good)
+    for args, kw in (((k.float(), k, L, cu), good), ((k, k[:4], L, cu), good), ((k[:, :3], k, L, cu), good), ((k, k, L.long(), cu), good),
+                     ((k, k, L[:1], cu), good), ((k.cpu(), k, L, cu), good), ((k, k.transpose(0, 1), L, cu), good),
+                     ((k, k, L, cu), dict(good, q=q.float())), ((k, k, L, cu), dict(good, q=q[:4])), ((k, k, L, cu), dict(good, q_out=q[:, :4])),
+                     ((k, k, L, cu), dict(max_q=3, q_out=q)), ((k, k, L, cu), dict(good, pos=L)), ((k, k, L, cu), dict(good, req_ids=i32([0])))):
+        with pytest.raises(ValueError):
+            c.append(*args, **kw)
+    for kw in (dict(dims=0), dict(dims=12), dict(dims=72), dict(inv_freq=[1.0]), dict(inv_freq=[math.inf] * 32)):
+        with pytest.raises(ValueError):
+            R.Rotation(**kw)
+    with pytest.raises(R.B.WSError):
+        c.attend(q, L, cu, max_q=3, max_kv=9, mass=torch.zeros(2, 4, 9, device="cuda"))
+    with pytest.raises(R.B.WSError):
+        c.evict(L, torch.zeros(2, 4, 9, device="cuda"), keep=4, max_kv=9)
+    with pytest.raises(ValueError):
+        c.reorder(i32([[0, 1]]), i32([7]))
+    with pytest.raises(ValueError):
+        c.reorder(torch.zeros(1, 2, device="cuda"), L)
+    with pytest.raises(R.B.WSError):
+        c.reorder(i32([[0, 1, 2]]), L)                     # three beams, two slots
+    x = make_beam(2, 3, 50, 4, 2, 1)
+    d = {n: t.cuda() for n, t in x.items()}
+    par, tok = (torch.zeros(2, 3, dtype=torch.int32, device="cuda") for _ in range(2))
+    s = R.BeamSearch(eos_id=3)
+    for args, kw in (((d["logits"].half(), d["score"], par, tok), {}), ((x["logits"], d["score"], par, tok), {}),
+                     ((d["logits"].transpose(0, 1), d["score"], par, tok), {}), ((d["logits"], d["score"][:1], par, tok), {}),
+                     ((d["logits"], d["score"], par.float(), tok), {}), ((d["logits"], d["score"], par, tok), dict(length=d["length"])),
+                     ((d["logits"], d["score"], par, tok), dict(done_score=d["score"])),
+                     ((d["logits"], d["score"], par, tok), dict(tokens=d["tokens"])),
+                     ((d["logits"], d["score"], par, tok), dict(tokens=d["tokens"].long(), length=d["length"]))):
+        with pytest.raises((ValueError, AttributeError)):
+            s.select(*args, **kw)
+    with pytest.raises(R.B.WSError):
+        R.BeamSearch(eos_id=50).select(d["logits"], d["score"], par, tok)
+    s.select(d["logits"], d["score"], par, tok)            # a refusal leaves nothing behind
+    torch.cuda.synchronize()
+
+
 def test_attend_8bit_long(R):
     """More than 2^31 elements in the pool: the last pages."""
     pages, hkv, page = 2 ** 31 // (8 * 64 * 64) + 40, 8, 64
