@@ -668,20 +668,24 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
   // rows (156 at 128) and 104 / 111 / 119 / 146 / 164 / 185 us streaming at
   // 17 / 32 / 33 / 40 / 48 / 64 rows (with the weights 300 against 179 / 188
   // / 259 / 302 / 335 / 387); 4 requests over 4-16 thousand positions 84
-  // against 76 / 78 / 81 / 87 / 99 / 104 us.
-  if (R > 40 && G <= FA_ROWS && a.scale > 0.f) {
+  // against 76 / 78 / 81 / 87 / 99 / 104 us.  In 8 bits the conversion makes
+  // tcgen05 dearer and streaming takes tiles of 16 rows: 225 us on tcgen05
+  // against 159 / 174 / 223 / 252 streaming at 40 / 48 / 64 / 72 rows, and 91
+  // against 92 / 97 / 124 at 40 / 48 / 64.
+  if (R > (c.dtype == WS_E4M3 ? 48 : 40) && G <= FA_ROWS && a.scale > 0.f) {
     q.fa = true;
     q.row_tiles = (a.max_q + FA_ROWS / G - 1) / (FA_ROWS / G);
-    q.geo = tile_geo(c.page_size, FA_KEYS);
+    // in 8 bits pages of 48 positions in pieces of 16: 4 x 2048 rows 296 us, 853 in short tiles
+    q.geo = tile_geo(c.page_size, FA_KEYS, c.dtype == WS_E4M3);
     const int tiles = max(1, tile_count(q.geo, c.page_size, FA_KEYS, a.max_kv));
     const long long units = (long long)a.n_req * c.n_kv_heads * ((q.row_tiles + 1) / 2);
-    // One round of CTAs (two per SM with one row tile each, else one), none
+    // One round of CTAs (two per SM with one bf16 row tile each, else one), none
     // shorter than four key tiles: a single request fills the round (a CTA
     // more than the round costs another: 64 rows over 65,536 positions 140 us
     // with 16 splits of 20 heads, 97 with 15), several requests' lengths
     // differ and leave CTAs without keys, so one split more (4 requests over
     // 4-16 thousand positions 101 us without it, 83 with it).
-    const long long round = (q.row_tiles == 1 ? 2ll : 1ll) * SMS / units + (a.n_req > 1 ? 1 : 0);
+    const long long round = (q.row_tiles == 1 && c.dtype == WS_BF16 ? 2ll : 1ll) * SMS / units + (a.n_req > 1 ? 1 : 0);
     const int want = (int)max(1ll, min(round, (long long)(tiles / 4)));
     q.tps = (tiles + want - 1) / want;
     q.nsplit = (tiles + q.tps - 1) / q.tps;
@@ -693,7 +697,11 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
     return q;
   }
   if (c.dtype == WS_E4M3) {
-    q.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+    // Row tiles of 8 rows or of 16: 96 requests x 20 heads over 375-1500
+    // positions 61 / 73 / 102 / 112 us in eights and 71 / 72 / 75 / 85 in
+    // sixteens at 8 / 9 / 16 / 17 rows.  (Tiles of 32 leave room for fewer warps: 117 at
+    // 17 rows, 126 at 32 for 128, 227 at 64 for 223.)
+    q.nt = R <= 8 ? 1 : 2;
     q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
     const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
     q.geo = tile_geo(c.page_size, Q8_TK);

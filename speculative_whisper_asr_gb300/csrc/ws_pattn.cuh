@@ -12,9 +12,17 @@ struct TileGeo {
   int tpp;                                 // tiles per page (0: several pages per tile)
   int ppt_log;                             // log2 pages per tile, page_log: log2 page_size
   int page_log;
+  int pieces;                              // > 1: what is called a page here is one of so many pieces of a page
 };
-inline TileGeo tile_geo(int page_size, int tk) {
+// `split`: pages that neither divide a tile nor hold whole ones are taken in
+// pieces that do (their largest power of two), else a page's last tile is short.
+inline TileGeo tile_geo(int page_size, int tk, bool split = false) {
   TileGeo g = {};
+  if (split && page_size % tk && tk % page_size && page_size % 8 == 0) {
+    const int piece = page_size & -page_size;
+    g.pieces = page_size / piece;
+    page_size = piece;
+  }
   if (page_size < tk && tk % page_size == 0 && page_size >= 8) {
     g.box = page_size;
     while ((1 << g.page_log) < page_size) ++g.page_log;

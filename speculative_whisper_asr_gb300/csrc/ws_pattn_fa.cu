@@ -41,15 +41,15 @@ constexpr int TILE = FA_KEYS * WS_DH * 2;          // 16 KB: a Q, K or V tile
 // What the cache holds: bf16; 8 bits whose scales hold for whole groups of 16
 // positions; or 8 bits with other blocks.
 enum { MODE_BF16 = 0, MODE_GROUPS = 1, MODE_ANY = 2 };
+constexpr int CONV = 4;                            // 8 bits: converter warps
 template <int W, int MODE = MODE_BF16>
 struct FaShape {                                   // a CTA with W row tiles; 3 - W run on an SM
   static constexpr int STAGES = 2 * W;             // key stages
-  static constexpr bool OWN = MODE != MODE_BF16 && W == 2;        // the converters are warps 4..7 (else 2 and 3)
-  static constexpr int CONV = OWN ? 4 : 2;         // converter warps
+  static constexpr bool Q8 = MODE != MODE_BF16;
   // K producer, MMA, V producer, V cleaner | converters | softmax A | softmax B
-  static constexpr int THREADS = 128 + 128 * W + (OWN ? 128 : 0);
-  static constexpr int AHEAD = OWN ? 3 : 1;        // 8 bits: tiles of codes in shared memory, TILE bytes each
-  static constexpr int SMEM = W * TILE + STAGES * 2 * TILE + (MODE == MODE_BF16 ? 0 : AHEAD * TILE) + 1024;
+  static constexpr int THREADS = 128 + (Q8 ? 128 : 0) + 128 * W;
+  static constexpr int AHEAD = 3;                  // 8 bits: tiles of codes in shared memory, TILE bytes each
+  static constexpr int SMEM = W * TILE + STAGES * 2 * TILE + (Q8 ? AHEAD * TILE : 0) + 1024;
   static constexpr uint32_t COLS = 256 * W;        // tensor memory
 };
 constexpr uint32_t IDESC_S = tc::idesc_bf16(128, 128);
@@ -151,13 +151,18 @@ struct TileInfo {
   uint32_t valid[4];
   bool clean;                                      // every row that the copies write counts, or is a zero behind a page's end
 };
+// PIECES: pages may be taken in pieces.
+template <bool PIECES>
 __device__ __forceinline__ int tile_entry(const AttnP& p, int t, int lane) {
-  return p.geo.tpp ? t / p.geo.tpp : (t << p.geo.ppt_log) + lane;
+  const int e = p.geo.tpp ? t / p.geo.tpp : (t << p.geo.ppt_log) + lane;
+  return PIECES && p.geo.pieces > 1 ? e / p.geo.pieces : e;
 }
+template <bool PIECES = false>
 __device__ __forceinline__ int tile_page(const AttnP& p, const int32_t* table, int t, int lane) {
-  const int e = tile_entry(p, t, lane);
+  const int e = tile_entry<PIECES>(p, t, lane);
   return (p.geo.tpp || lane < (1 << p.geo.ppt_log)) && e < p.c.table_stride ? __ldg(table + e) : -1;
 }
+template <bool PIECES = false>
 __device__ __forceinline__ TileInfo tile_info(const AttnP& p, int t, int page, int limit, int lane) {
   TileInfo f;
   const bool ok = page >= 0 && page < p.c.n_pages;
@@ -173,7 +178,7 @@ __device__ __forceinline__ TileInfo tile_info(const AttnP& p, int t, int page, i
     f.clean = ok && f.base + room <= limit;        // one page: the same in every lane
   } else {
     const int ps = 1 << p.geo.page_log;
-    f.tok = 0;
+    f.tok = PIECES && p.geo.pieces > 1 ? ((t << p.geo.ppt_log) + lane) % p.geo.pieces * ps : 0;
     f.base = t * FA_KEYS;
     f.dst = lane * ps * 128;
     const uint32_t okm = __ballot_sync(0xffffffffu, ok && f.base + lane * ps < limit);
@@ -256,21 +261,28 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, u
   four(w.w, hi.z, hi.w);
 }
 
-// A cache in 8 bits: warps 0 and 2 (W = 1: 0) copy codes and scales, AHEAD tiles
-// at once, and converter warps write the stages from them, rows that do not count as zeros;
-// NaN values that not every row sees are noted and left out at once, so there
-// is nothing to clean.  For W = 2 the converters are a warpgroup of their own.
+// A cache in 8 bits: warps 0 and 2 copy codes and scales of keys and of values,
+// AHEAD tiles at once, and a warpgroup of converters (warps 4..7) writes the
+// stages from them, rows that do not count as zeros; NaN values that not every
+// row sees are noted and left out at once, so there is nothing to clean.
 // (Codes loaded into the converters' registers, or by copies of their own, cost
 // a memory latency per tile: a warp's fence before its stores may be read
-// waits for whatever it has asked for; 4 x 2048 rows 368 and 590 us.)
+// waits for whatever it has asked for; 4 x 2048 rows 368 and 590 us.)  W = 2
+// also for one row tile: two CTAs of W = 1 leave two warps each and room for
+// one tile of codes (96 requests x 20 heads x 128 rows 262 us for 225, 4 x 64
+// rows over 4-16 thousand positions 142 for 91).
 //
 // MODE_GROUPS: keys become fp16 (one conversion for two codes), and so do the
 // queries, each row with a power of two of its own (ws_pattn_q8.cu); a group of
 // 16 keys with one scale costs the softmax a factor.  Values become bf16 with
 // their scales in them (ten instructions for four codes), because the weights
 // have to be bf16: in fp16 their reference moves at 2^15, which some row of a
-// warp does in most tiles (348 us against 2^60's).  MODE_ANY: keys like
-// values, which any blocks of scales allow.
+// warp does in most tiles (348 us).  MODE_ANY: keys like values, which any
+// blocks of scales allow.
+// The call above in 8 bits, pages and blocks of 16: 282 us, 0.70 PFLOP/s;
+// blocks of 8 in pages of 64 277, in pages of 16 345.  Without the conversions'
+// arithmetic it would take 245: they share the schedulers' issue slots with
+// the softmax.
 template <int W, int MODE>
 __global__ void __launch_bounds__(FaShape<W, MODE>::THREADS, 3 - W)
 fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -316,10 +328,10 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int b = 0; b < NST; ++b) {
-      tc::mbar_init(&B.full[b], Q8 ? Shape::CONV : 2);
+      tc::mbar_init(&B.full[b], Q8 ? CONV : 2);
       tc::mbar_init(&B.empty[b], 1);
-      tc::mbar_init(&B.raw[b], !Q8 ? 1 : W == 1 ? 2 : 4);
-      tc::mbar_init(&B.raw_free[b], Shape::CONV);
+      tc::mbar_init(&B.raw[b], Q8 ? 4 : 1);
+      tc::mbar_init(&B.raw_free[b], CONV);
     }
     odd.any = 0;
     for (int w = 0; w < W; ++w) {
@@ -353,35 +365,29 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   // in the epilogue for the rows that see them.
   const int all_see = row_limit(p, r, rho0 / p.G);
   auto direct = [&](const TileInfo& f) { return f.clean && (all_see >= r.L || f.base + FA_KEYS <= all_see); };
-  // ---- a cache in 8 bits: warp 0, and the converters
+  // ---- a cache in 8 bits: warps 0 (keys) and 2 (values), and the converters
   auto codes = [&](int slot) { return sm + (W + 2 * NST) * TILE + slot * TILE; };        // keys, and TILE / 2 on values
-  // W = 2: keys by warp 0, values by warp 2, each with its scales; W = 1: both by warp 0
-  auto copy_codes = [&](bool keys, bool values) {
+  auto copy_codes = [&](bool values) {
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
-    const uint8_t* k_scales = p.c.k_scale + (size_t)h * (size_t)p.c.scale_head_stride;
-    const uint8_t* v_scales = p.c.v_scale + (size_t)h * (size_t)p.c.scale_head_stride;
-    int page = tile_page(p, table, lo, lane), issued = 0;
-    uint32_t kb[4] = {}, vb[4] = {};               // scale bytes of the tile asked for last
+    const uint8_t* scales = (values ? p.c.v_scale : p.c.k_scale) + (size_t)h * (size_t)p.c.scale_head_stride;
+    int page = tile_page<true>(p, table, lo, lane), issued = 0;
+    uint32_t sb[4] = {};                           // scale bytes of the tile asked for last
     auto keep_scales = [&](int slot) {
 #pragma unroll
       for (int q = 0; q < (GROUPS ? 1 : 4); ++q)
-        if (!GROUPS || lane < 8) {
-          if (keys) s_scale[0][slot][32 * q + lane] = (uint8_t)kb[q];
-          if (values) s_scale[1][slot][32 * q + lane] = (uint8_t)vb[q];
-        }
+        if (!GROUPS || lane < 8) s_scale[values][slot][32 * q + lane] = (uint8_t)sb[q];
       __syncwarp();
       if (lane == 0) arrive(&B.raw[slot]);
     };
     for (int j = 0; j < nmax; ++j) {
       const int slot = j % AHEAD;
-      const TileInfo f = tile_info(p, lo + j, page, r.L, lane);
-      if (j + 1 < nmax) page = tile_page(p, table, lo + j + 1, lane);
-      if (AHEAD == 1 && j > 0) keep_scales(0);
+      const TileInfo f = tile_info<true>(p, lo + j, page, r.L, lane);
+      if (j + 1 < nmax) page = tile_page<true>(p, table, lo + j + 1, lane);
       if (j >= AHEAD && !wait_warp(&B.raw_free[slot], (uint32_t)((j / AHEAD - 1) & 1), abort)) break;
       const bool go = f.page >= 0;
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * (keys && values ? 128u : 64u);
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 64u;
       if (lane == 0) {
-        if (keys) {
+        if (!values) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) raw_meta[slot].valid[q] = f.valid[q];
           raw_meta[slot].base = f.base;
@@ -389,28 +395,24 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         tc::mbar_expect_tx(&B.raw[slot], bytes);
       }
       __syncwarp();
-      if (go) {
-        if (keys) tma_load_4d(codes(slot) + f.dst / 2, &mk, &B.raw[slot], 0, f.tok, h, f.page);
-        if (values) tma_load_4d(codes(slot) + TILE / 2 + f.dst / 2, &mv, &B.raw[slot], 0, f.tok, h, f.page);
-      }
+      if (go)
+        tma_load_4d(codes(slot) + (values ? TILE / 2 : 0) + f.dst / 2, values ? &mv : &mk, &B.raw[slot], 0, f.tok, h, f.page);
       ++issued;
       // the last tile's scales have arrived by now; this one's are stored with the next
-      if (AHEAD > 1 && j > 0) keep_scales((j - 1) % AHEAD);
+      if (j > 0) keep_scales((j - 1) % AHEAD);
 #pragma unroll
       for (int q = 0; q < (GROUPS ? 1 : 4); ++q) {
         const int x = GROUPS ? 16 * (lane & 7) : 32 * q + lane;    // the row whose scale it is
-        const int pg = __shfl_sync(0xffffffffu, f.page, p.geo.tpp ? 0 : x >> p.geo.page_log);
+        const int from = p.geo.tpp ? 0 : x >> p.geo.page_log;      // the lane that copies it
+        const int pg = __shfl_sync(0xffffffffu, f.page, from), tok0 = __shfl_sync(0xffffffffu, f.tok, from);
         uint32_t valid = f.valid[GROUPS ? 0 : q];
         if (GROUPS) valid = x < 32 ? f.valid[0] : x < 64 ? f.valid[1] : x < 96 ? f.valid[2] : f.valid[3];
-        kb[q] = GROUPS ? 127u : 0u;                // of keys that do not count, whose scores are -inf: any but 0
-        vb[q] = 0u;
+        sb[q] = GROUPS && !values ? 127u : 0u;     // of keys that do not count, whose scores are -inf: any but 0
         if ((valid >> (x & 31)) & 1u) {
-          const uint32_t tok = (uint32_t)(p.geo.tpp ? f.tok + x : x & ((1 << p.geo.page_log) - 1));
+          const uint32_t tok = (uint32_t)(tok0 + (p.geo.tpp ? x : x & ((1 << p.geo.page_log) - 1)));
           uint32_t b = p.block_mul ? __umulhi(tok, p.block_mul) : tok;     // tok / scale_block, or one more
           b -= b * (uint32_t)p.c.scale_block > tok;
-          const uint64_t at = (uint64_t)(uint32_t)pg * (uint32_t)p.c.scale_page_stride + b;
-          if (keys) kb[q] = __ldg(k_scales + at);
-          if (values) vb[q] = __ldg(v_scales + at);
+          sb[q] = __ldg(scales + (uint64_t)(uint32_t)pg * (uint32_t)p.c.scale_page_stride + b);
         }
       }
     }
@@ -419,7 +421,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int j = max(0, issued - AHEAD); j < issued; ++j) tc::mbar_wait(&B.raw[j % AHEAD], (uint32_t)((j / AHEAD) & 1));
   };
   auto convert = [&](int ci) {
-    constexpr int NC = Shape::CONV, NG = 16 / NC;  // groups of eight rows of a warp
+    constexpr int NC = CONV, NG = 16 / NC;         // groups of eight rows of a warp
     for (int j = 0; j < nmax; ++j) {
       const int s = j % NST, slot = j % AHEAD;
       if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
@@ -468,9 +470,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
   };
   if (warp < 4) {
-    if (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else if (Shape::OWN) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (Q8 && warp != 1) {
     if (!GROUPS && warp == 0 && lane == 0) {
 #pragma unroll
@@ -481,8 +481,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         }
     }
     __syncwarp();
-    if (warp == 0 || (W == 2 && warp == 2)) copy_codes(warp == 0, W == 1 || warp == 2);
-    else if (!Shape::OWN) convert(warp - 2);
+    if (warp != 3) copy_codes(warp == 2);
   } else if (!Q8 && (warp == 0 || warp == 2)) {
     // ---- producers: Q and K, and V.  Two warps, because small pages make
     // many copies of a tile and one warp's copies are issued one by one.
@@ -611,17 +610,15 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       }
     __syncwarp();
   }
-  } else if (Shape::OWN && warp < 8) {
+  } else if (Q8 && warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     convert(warp - 4);
   } else {
     // ---- softmax: thread = row
-    if (Q8) {                                      // 128 a thread at launch: 4 * 128 = 2 * 72 + 2 * 184, or 2 * 128 = 88 + 168
-      if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-      else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    } else if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");     // 168 a thread at launch
+    if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");        // 128 a thread at launch: 4 * 128 = 2 * 72 + 2 * 184
+    else if (W == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");     // 168 a thread at launch
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");            // 128
-    const int w = (warp >> 2) - (Shape::OWN ? 2 : 1), quarter = warp & 3, x = quarter * 32 + lane;
+    const int w = (warp >> 2) - (Q8 ? 2 : 1), quarter = warp & 3, x = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tS = tl + TM_S + 128u * w, tP = tl + TM_P + 64u * w, tO = tl + TM_O + 64u * w;
     const int first = rho0 + w * TR, rho = first + x;
@@ -1058,7 +1055,9 @@ cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap
 }
 template <int MODE>
 cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  return p.row_tiles == 1 ? run_fa<1, MODE>(p, mq, mk, mv, s) : run_fa<2, MODE>(p, mq, mk, mv, s);
+  if constexpr (MODE == MODE_BF16)
+    if (p.row_tiles == 1) return run_fa<1, MODE>(p, mq, mk, mv, s);
+  return run_fa<2, MODE>(p, mq, mk, mv, s);
 }
 
 }  // namespace

@@ -112,7 +112,7 @@ __device__ __forceinline__ bool take_out_nan(Odd& odd, uint8_t* tile, int base, 
 // MIX: causal chunks of more than one row, where NaN values are kept from the
 // rows that do not see them.  UNI: scales hold for whole tiles.
 template <int NT, bool MIX, bool UNI>
-__global__ void __launch_bounds__(W * 32, NT == 4 ? 2 : 3)
+__global__ void __launch_bounds__(W * 32, 3)
 q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   constexpr int MT = TK / 16;              // key steps of 16
   constexpr uint32_t ALL = 0xffffffffu;
@@ -530,8 +530,7 @@ cudaError_t run(const AttnP& p, const TcMap& mk, const TcMap& mv, cudaStream_t s
 }
 template <bool MIX, bool UNI>
 cudaError_t run(const AttnP& p, int nt, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  if (nt == 1) return run<1, MIX, UNI>(p, mk, mv, s);
-  return nt == 2 ? run<2, MIX, UNI>(p, mk, mv, s) : run<4, MIX, UNI>(p, mk, mv, s);
+  return nt == 1 ? run<1, MIX, UNI>(p, mk, mv, s) : run<2, MIX, UNI>(p, mk, mv, s);
 }
 
 }  // namespace

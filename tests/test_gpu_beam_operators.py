@@ -246,6 +246,14 @@ def test_attend_8bit_in_parts(R, page, block, chunks, lens, causal):
     check_q8(R, Q8Case(chunks, lens, 2, 1, page, block=block, causal=causal, seed=len(chunks) + page))
 
 
+@pytest.mark.parametrize("page,block", [(24, 8), (48, 16), (48, 48), (56, 7), (80, 16), (192, 64), (320, 32)])
+@pytest.mark.parametrize("chunks,lens", [([49, 70], [250, 1301]), ([130, 300], [700, 310]), ([60], [3000])])
+@pytest.mark.parametrize("layout", ["pair", "head"])
+def test_attend_8bit_pages_in_pieces(R, page, block, chunks, lens, layout):
+    """Long chunks over pages that neither divide a tile nor hold whole ones."""
+    check_q8(R, Q8Case(chunks, lens, 2, 2, page, block=block, layout=layout, seed=page + len(chunks)))
+
+
 def test_calls_on_other_streams(R):
     """Calls on two streams, with an object each, between calls on the current one: the same bits."""
     cs = Q8Case([5, 60], [700, 900], 4, 2, 32, block=16, seed=6)
