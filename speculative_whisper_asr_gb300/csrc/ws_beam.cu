@@ -18,8 +18,11 @@
 // than fp32's step is still told apart), the parts' candidates in order within
 // their beams, the beams' against each other by whole numbers that order like
 // the scores, and the 2 * beams best dealt out: those that end go to the
-// finished transcripts.  Then each thread moves a column of the transcripts for all beams, so the
-// move may be in place.
+// finished transcripts.  Then each thread moves a column of the transcripts for
+// all beams, so the move may be in place.
+// 96 requests x 5 beams over 51,866 tokens (100 MB): 33 us, of which the scan,
+// one round of CTAs, takes 23 (4.4 TB/s) and the merge 8, a chain of latencies;
+// one request 14.
 #include <string>
 
 #include "ws_paged.cuh"
@@ -367,7 +370,7 @@ const char* check_beam(const ws_beam_args* a) {
 struct Plan { int parts, part; size_t stat, bytes; };
 // Twelve CTAs of 128 threads run on an SM: as many parts as fill that round
 // (a row is read once whatever they are), none longer than 256 logits per
-// thread, and none shorter than four.
+// thread, and none shorter than four.  480 rows of 51,866: 3 parts 33 us.
 Plan make_plan(const ws_beam_args& a) {
   Plan q = {};
   const long long rows = (long long)a.n * a.beams;

@@ -14,12 +14,15 @@ struct TileGeo {
   int page_log;
   int pieces;                              // > 1: what is called a page here is one of so many pieces of a page
 };
-// `split`: pages that neither divide a tile nor hold whole ones are taken in
-// pieces that do (their largest power of two), else a page's last tile is short.
+// `split`: pages that neither divide a tile nor hold whole ones may be taken in
+// pieces that do (their largest power of two), else a page's last tile is
+// short.  Many copies of eight keys cost a third, so those only where short
+// tiles would be less than three quarters full.
 inline TileGeo tile_geo(int page_size, int tk, bool split = false) {
   TileGeo g = {};
-  if (split && page_size % tk && tk % page_size && page_size % 8 == 0) {
-    const int piece = page_size & -page_size;
+  const int piece = page_size & -page_size;
+  if (split && page_size % tk && tk % page_size &&
+      (piece >= 16 || (piece == 8 && page_size < (page_size + tk - 1) / tk * (tk / 4 * 3)))) {
     g.pieces = page_size / piece;
     page_size = piece;
   }

@@ -246,7 +246,7 @@ def test_attend_8bit_in_parts(R, page, block, chunks, lens, causal):
     check_q8(R, Q8Case(chunks, lens, 2, 1, page, block=block, causal=causal, seed=len(chunks) + page))
 
 
-@pytest.mark.parametrize("page,block", [(24, 8), (48, 16), (48, 48), (56, 7), (80, 16), (192, 64), (320, 32)])
+@pytest.mark.parametrize("page,block", [(24, 8), (48, 16), (48, 48), (56, 7), (80, 16), (192, 64), (320, 32), (248, 8), (200, 8)])
 @pytest.mark.parametrize("chunks,lens", [([49, 70], [250, 1301]), ([130, 300], [700, 310]), ([60], [3000])])
 @pytest.mark.parametrize("layout", ["pair", "head"])
 def test_attend_8bit_pages_in_pieces(R, page, block, chunks, lens, layout):
