@@ -48,6 +48,9 @@ __device__ __forceinline__ int tile_whole(const TileGeo& g, int page_size, int t
   return L / page_size * g.tpp + rest / tk;
 }
 
+// A factor of scores, kept from 0 and infinity: times -inf or 0 they would be NaN.
+__device__ __forceinline__ float score_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 3e38f); }
+
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));

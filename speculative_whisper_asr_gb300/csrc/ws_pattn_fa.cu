@@ -641,7 +641,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       }
       const int e2 = most >= 1.17549435e-38f && most < INFINITY ? min((int)(__float_as_uint(most) >> 23) - 127, 126) : 0;
       const float f = __uint_as_float((uint32_t)(127 - e2) << 23);
-      sl = fmaxf(sl * __uint_as_float((uint32_t)(127 + e2) << 23), 1e-37f);
+      sl = score_factor(sl * __uint_as_float((uint32_t)(127 + e2) << 23));
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
@@ -684,9 +684,9 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
       const float* ks = s_ks[GROUPS ? j % NST : 0];
       float2 sum2[2];
-      float slk[8];                                // of the groups; not 0, which times -inf would be NaN
+      float slk[8];                                // of the groups
 #pragma unroll
-      for (int g = 0; g < 8; ++g) slk[g] = GROUPS ? fmaxf(sl * ks[g], 1.17549435e-38f) : sl;
+      for (int g = 0; g < 8; ++g) slk[g] = GROUPS ? score_factor(sl * ks[g]) : sl;
       auto weigh = [&]() {
         const float2 nm2 = make_float2(-msl, -msl);
         sum2[0] = sum2[1] = make_float2(0.f, 0.f);

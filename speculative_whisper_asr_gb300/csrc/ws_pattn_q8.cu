@@ -258,7 +258,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       for (int k = 0; k < 2; ++k) qf[s][nt][k] = pack_f16(x[4 * s + 2 * k] * f, x[4 * s + 2 * k + 1] * f);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      sl[nt][k] = fmaxf(p.sl * __shfl_sync(ALL, back, 4 * (2 * c + k)), 1e-37f);
+      sl[nt][k] = score_factor(p.sl * __shfl_sync(ALL, back, 4 * (2 * c + k)));
     }
   }
   int lim[NT][2];
@@ -387,12 +387,12 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
     }
     // ---- does a score pass its row's reference by more than 2^8?
     bool grow = false;
-    float slk[NT][2], top[NT][2];          // UNI: with the keys' scale (not 0, which times -inf would be NaN)
+    float slk[NT][2], top[NT][2];          // UNI: with the keys' scale
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        slk[nt][e] = UNI ? fmaxf(sl[nt][e] * ksc[0][0], 1.17549435e-38f) : sl[nt][e];
+        slk[nt][e] = UNI ? score_factor(sl[nt][e] * ksc[0][0]) : sl[nt][e];
         top[nt][e] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e])) * slk[nt][e];
         grow |= top[nt][e] > m[nt][e] + HOLD;
       }

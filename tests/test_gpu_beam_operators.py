@@ -238,6 +238,19 @@ def test_attend_8bit_scales_far_apart(R, chunks):
     check_q8(R, cs)
 
 
+@pytest.mark.parametrize("chunks", [[1], [9], [64], [300]])
+@pytest.mark.parametrize("block", [8, 16, 32])
+def test_attend_8bit_scores_that_are_nothing(R, chunks, block):
+    """Queries that meet zeros of keys whose scale, times theirs, passes fp32: scores are 0, not NaN."""
+    cs = Q8Case(chunks, [400], 2, 2, 64, block=block, causal=False, seed=block)
+    cs.q_all.zero_()
+    cs.q_all[..., 0] = 2.0 ** 12
+    cs.k8.view(torch.uint8)[..., 0] = 0
+    cs.scales[0] = 245
+    cs.k.mul_(0.0)                                         # what matters of the keys
+    check_q8(R, cs)
+
+
 @pytest.mark.parametrize("page,block", [(64, 16), (40, 8)])
 @pytest.mark.parametrize("chunks,lens", [([1], [3000]), ([12], [2500]), ([50], [3000]), ([90, 70], [2900, 1500]), ([60], [4000])])
 @pytest.mark.parametrize("causal", [True, False])
