@@ -708,7 +708,13 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
     const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
     q.geo = tile_geo(c.page_size, Q8_TK);
     const int tiles = max(1, tile_count(q.geo, c.page_size, Q8_TK, a.max_kv));
-    const int want = (int)min((4ll * SLOTS + units - 1) / units, (long long)max(1, a.max_kv / 512));
+    // Splits of at least 512 keys: for one request a round of CTAs, three per
+    // SM (20 heads over 65,536 positions 40 us with 22 splits, 52 with 31, 61
+    // with 61); several requests' lengths differ and leave CTAs without keys,
+    // so a third more (16 requests x 8 heads over up to 65,536 positions 131 us
+    // with 5 splits, 147 with 4, 190 with 3, 131 with 10).
+    const long long round = a.n_req == 1 ? 3ll * SMS / units : (4ll * SMS + units - 1) / units;
+    const int want = (int)max(1ll, min(round, (long long)(a.max_kv / 512)));
     q.tps = (tiles + want - 1) / want;
     q.nsplit = (tiles + q.tps - 1) / q.tps;
     partials(R);
