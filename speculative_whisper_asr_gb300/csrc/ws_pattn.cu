@@ -612,7 +612,8 @@ const char* check_attn(const ws_paged_cache* c, const ws_attention_args* a) {
 struct Plan {
   F32Rows rows = {};                       // fp32, up to 16 rows
   int rpt = 0;                             // fp32: row tiles of 16 * rpt rows (0: up to 16 rows, f32_rows_kernel)
-  bool fa = false;                         // tcgen05 row tiles instead of streaming ones
+  bool fa = false;                         // tcgen05 row tiles instead of streaming ones ...
+  bool two_heads = false;                  // ... of two heads per CTA
   int nt = 1;                              // streaming row tile: 8 * nt rows
   int row_tiles = 1, nsplit = 1, tps = 1;
   bool stash = false;                      // the streaming kernel adds the mass itself
@@ -669,7 +670,7 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
   // 17 / 32 / 33 / 40 / 48 / 64 rows (with the weights 300 against 179 / 188
   // / 259 / 302 / 335 / 387); 4 requests over 4-16 thousand positions 84
   // against 76 / 78 / 81 / 87 / 99 / 104 us.  In 8 bits the conversion makes
-  // tcgen05 dearer and streaming takes tiles of 16 rows: 225 us on tcgen05
+  // tcgen05 dearer and streaming takes tiles of 16 rows: 182 us on tcgen05
   // against 159 / 174 / 223 / 252 streaming at 40 / 48 / 64 / 72 rows, and 91
   // against 92 / 97 / 124 at 40 / 48 / 64.
   if (R > (c.dtype == WS_E4M3 ? 48 : 40) && G <= FA_ROWS && a.scale > 0.f) {
@@ -680,7 +681,12 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
     // eight for as much with 200, 398 for 1753 with 24, 379 for 309 with 248.
     q.geo = tile_geo(c.page_size, FA_KEYS, c.dtype == WS_E4M3);
     const int tiles = max(1, tile_count(q.geo, c.page_size, FA_KEYS, a.max_kv));
-    const long long units = (long long)a.n_req * c.n_kv_heads * ((q.row_tiles + 1) / 2);
+    // In 8 bits a CTA has an SM to itself: with one row tile each it takes two
+    // heads, unless that leaves SMs idle (96 requests x 20 heads x 128 rows 186
+    // us, 227 one by one; one request x 64 rows over 448 positions 20 and 15).
+    q.two_heads = c.dtype == WS_E4M3 && q.row_tiles == 1 && (long long)a.n_req * c.n_kv_heads > SMS;
+    const long long units =
+        (long long)a.n_req * (q.two_heads ? (c.n_kv_heads + 1) / 2 : c.n_kv_heads) * ((q.row_tiles + 1) / 2);
     // One round of CTAs (two per SM with one bf16 row tile each, else one), none
     // shorter than four key tiles: a single request fills the round (a CTA
     // more than the round costs another: 64 rows over 65,536 positions 140 us
@@ -779,7 +785,7 @@ cudaError_t combine(const AttnP& p, cudaStream_t s) {
 }
 
 cudaError_t run_bf16(const AttnP& p, const Plan& q, cudaStream_t s) {
-  cudaError_t e = q.fa ? launch_fa(p, s) : run_streaming(p, q, s);
+  cudaError_t e = q.fa ? launch_fa(p, false, s) : run_streaming(p, q, s);
   if (e == cudaSuccess && q.parts) e = combine<bf16>(p, s);
   if (e != cudaSuccess || !p.a.mass || p.a.max_kv == 0 || q.stash) return e;
   if (q.fa) return launch_fa_mass(p, s);
@@ -794,7 +800,7 @@ cudaError_t run_f32(const AttnP& p, const Plan& q, cudaStream_t s) {
 }
 
 cudaError_t run_8bit(const AttnP& p, const Plan& q, cudaStream_t s) {
-  const cudaError_t e = q.fa ? launch_fa(p, s) : launch_q8(p, q.nt, s);
+  const cudaError_t e = q.fa ? launch_fa(p, q.two_heads, s) : launch_q8(p, q.nt, s);
   return e == cudaSuccess && q.parts ? combine<bf16>(p, s) : e;
 }
 

@@ -204,7 +204,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // chunk rows) against tiles of FA_KEYS keys.  Rows of unsplit calls go to
 // out / lse, those of split calls to the partials.
 constexpr int FA_ROWS = 128, FA_KEYS = 128;
-cudaError_t launch_fa(const AttnP& p, cudaStream_t s);
+cudaError_t launch_fa(const AttnP& p, bool two_heads, cudaStream_t s);
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s);
 
 // The fp32 model (ws_pattn_f32.cu): row tiles of 32 or 64 rows and key tiles of

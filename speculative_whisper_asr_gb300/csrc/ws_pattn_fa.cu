@@ -269,8 +269,8 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, u
 // a memory latency per tile: a warp's fence before its stores may be read
 // waits for whatever it has asked for; 4 x 2048 rows 368 and 590 us.)  W = 2
 // also for one row tile: two CTAs of W = 1 leave two warps each and room for
-// one tile of codes (96 requests x 20 heads x 128 rows 262 us for 225, 4 x 64
-// rows over 4-16 thousand positions 142 for 91).
+// one tile of codes (96 requests x 20 heads x 128 rows 262 us, 4 x 64 rows over
+// 4-16 thousand positions 142 for 91).
 //
 // MODE_GROUPS: keys become fp16 (one conversion for two codes), and so do the
 // queries, each row with a power of two of its own (ws_pattn_q8.cu); a group of
@@ -283,7 +283,9 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, u
 // blocks of 8 in pages of 64 277, in pages of 16 345.  Without the conversions'
 // arithmetic it would take 245: they share the schedulers' issue slots with
 // the softmax.
-template <int W, int MODE>
+// HEADS: A and B are the only row tiles of two heads, whose key tiles take
+// turns in the stages (96 requests x 20 heads x 128 rows 186 us for 227).
+template <int W, int MODE, bool HEADS>
 __global__ void __launch_bounds__(FaShape<W, MODE>::THREADS, 3 - W)
 fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
@@ -295,7 +297,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) Bars<W> B;
   __shared__ Meta meta[NST];
-  __shared__ Odd odd;
+  __shared__ Odd odds[HEADS ? 2 : 1];
+  Odd& odd = odds[0];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   constexpr int AHEAD = Shape::AHEAD;
@@ -306,11 +309,12 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   if (p.next_item && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next_item = 0ull;
   const int groups = (p.row_tiles + W - 1) / W;
   const int pair = groups - 1 - blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;   // the longest rows first
-  const int h = blockIdx.y, i = longest_first(p, blockIdx.z);
+  const int h = HEADS ? 2 * blockIdx.y : blockIdx.y, i = longest_first(p, blockIdx.z);
+  const int two = HEADS && h + 1 < p.c.n_kv_heads;         // log2 of the heads
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Req r = request(p, i);
   const int R = r.c * p.G, RB = FA_ROWS / p.G, TR = RB * p.G;
-  const int rho0 = pair * W * TR;
+  const int rho0 = HEADS ? 0 : pair * W * TR;
   if (rho0 >= R) return;
   // key tiles of each row tile within this split
   int n[W], lo;
@@ -319,12 +323,13 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     lo = split * p.tps;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const int first = rho0 + w * TR, last = min(R, first + TR) - 1;
-      const int nt = last >= first ? tile_count(p.geo, ps, FA_KEYS, row_limit(p, r, last / p.G)) : 0;
+      const int first = rho0 + (HEADS ? 0 : w * TR), last = min(R, first + TR) - 1;
+      const int nt = last >= first && (!HEADS || w <= two) ? tile_count(p.geo, ps, FA_KEYS, row_limit(p, r, last / p.G)) : 0;
       n[w] = max(0, min(nt, lo + p.tps) - lo);
     }
   }
   const int nmax = max(n[0], n[W - 1]);
+  const int items = nmax << two;                   // key tiles of the CTA: tile j of A is item j << two, that of B the next
   volatile int* abort = &s_abort;
   if (threadIdx.x == 0) {
     for (int b = 0; b < NST; ++b) {
@@ -333,7 +338,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       tc::mbar_init(&B.raw[b], Q8 ? 4 : 1);
       tc::mbar_init(&B.raw_free[b], CONV);
     }
-    odd.any = 0;
+    for (Odd& o : odds) o.any = 0;
     for (int w = 0; w < W; ++w) {
       tc::mbar_init(&B.q_full[w], GROUPS ? 4 : 1); tc::mbar_init(&B.s_full[w], 1); tc::mbar_init(&B.s_free[w], 4);
       tc::mbar_init(&B.p_full[w], 4); tc::mbar_init(&B.pv_done[w], 1);
@@ -342,7 +347,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (Q8)
-    for (int x = threadIdx.x; x < 3 * WS_DH; x += THREADS) odd.first[0][x] = 0x7FFFFFFF;
+    for (Odd& o : odds)
+      for (int x = threadIdx.x; x < 3 * WS_DH; x += THREADS) o.first[0][x] = 0x7FFFFFFF;
   if (warp == 1) tc::tmem_alloc(&s_tmem, Shape::COLS);
   uint8_t* sQ = sm;
   auto sK = [&](int b) { return sm + W * TILE + b * 2 * TILE; };
@@ -369,7 +375,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   auto codes = [&](int slot) { return sm + (W + 2 * NST) * TILE + slot * TILE; };        // keys, and TILE / 2 on values
   auto copy_codes = [&](bool values) {
     const int32_t* table = p.c.page_table + (size_t)min(max(r.slot, 0), p.c.n_slots - 1) * p.c.table_stride;
-    const uint8_t* scales = (values ? p.c.v_scale : p.c.k_scale) + (size_t)h * (size_t)p.c.scale_head_stride;
+    const uint8_t* scales = values ? p.c.v_scale : p.c.k_scale;
     int page = tile_page<true>(p, table, lo, lane), issued = 0;
     uint32_t sb[4] = {};                           // scale bytes of the tile asked for last
     auto keep_scales = [&](int slot) {
@@ -379,10 +385,10 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       __syncwarp();
       if (lane == 0) arrive(&B.raw[slot]);
     };
-    for (int j = 0; j < nmax; ++j) {
-      const int slot = j % AHEAD;
-      const TileInfo f = tile_info<true>(p, lo + j, page, r.L, lane);
-      if (j + 1 < nmax) page = tile_page<true>(p, table, lo + j + 1, lane);
+    for (int j = 0; j < items; ++j) {
+      const int slot = j % AHEAD, hj = h + (j & two);
+      const TileInfo f = tile_info<true>(p, lo + (j >> two), page, r.L, lane);
+      if (j + 1 < items) page = tile_page<true>(p, table, lo + ((j + 1) >> two), lane);
       if (j >= AHEAD && !wait_warp(&B.raw_free[slot], (uint32_t)((j / AHEAD - 1) & 1), abort)) break;
       const bool go = f.page >= 0;
       const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)p.geo.box * 64u;
@@ -396,7 +402,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       }
       __syncwarp();
       if (go)
-        tma_load_4d(codes(slot) + (values ? TILE / 2 : 0) + f.dst / 2, values ? &mv : &mk, &B.raw[slot], 0, f.tok, h, f.page);
+        tma_load_4d(codes(slot) + (values ? TILE / 2 : 0) + f.dst / 2, values ? &mv : &mk, &B.raw[slot], 0, f.tok, hj, f.page);
       ++issued;
       // the last tile's scales have arrived by now; this one's are stored with the next
       if (j > 0) keep_scales((j - 1) % AHEAD);
@@ -412,7 +418,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           const uint32_t tok = (uint32_t)(tok0 + (p.geo.tpp ? x : x & ((1 << p.geo.page_log) - 1)));
           uint32_t b = p.block_mul ? __umulhi(tok, p.block_mul) : tok;     // tok / scale_block, or one more
           b -= b * (uint32_t)p.c.scale_block > tok;
-          sb[q] = __ldg(scales + (uint64_t)(uint32_t)pg * (uint32_t)p.c.scale_page_stride + b);
+          sb[q] = __ldg(scales + (size_t)hj * (size_t)p.c.scale_head_stride + (uint64_t)(uint32_t)pg * (uint32_t)p.c.scale_page_stride + b);
         }
       }
     }
@@ -422,7 +428,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
   };
   auto convert = [&](int ci) {
     constexpr int NC = CONV, NG = 16 / NC;         // groups of eight rows of a warp
-    for (int j = 0; j < nmax; ++j) {
+    for (int j = 0; j < items; ++j) {
       const int s = j % NST, slot = j % AHEAD;
       if (j >= NST && !wait_warp(&B.empty[s], (uint32_t)((j / NST - 1) & 1), abort)) break;
       if (!wait_warp(&B.raw[slot], (uint32_t)((j / AHEAD) & 1), abort)) break;
@@ -456,8 +462,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           for (int e = 0; e < 16; ++e) {
             if ((src[TILE / 2 + e] & 0x7Fu) != 0x7Fu || base + x < all_see) continue;
             *reinterpret_cast<uint16_t*>(sV(s) + (e < 8 ? at : at2) + 2u * (e & 7)) = 0u;
-            atomicMin(&odd.first[2][16 * (lane & 3) + e], base + x);
-            odd.any = 1;
+            atomicMin(&odds[j & two].first[2][16 * (lane & 3) + e], base + x);
+            odds[j & two].any = 1;
           }
         }
       }
@@ -477,7 +483,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int w = 0; w < W; ++w)
         if (n[w]) {
           tc::mbar_expect_tx(&B.q_full[w], (uint32_t)TR * 128u);
-          tma_load_3d(sQ + w * TILE, &mq, &B.q_full[w], 0, h * p.G, r.row0 + pair * W * RB + w * RB);
+          tma_load_3d(sQ + w * TILE, &mq, &B.q_full[w], 0, (HEADS ? h + w : h) * p.G, r.row0 + (HEADS ? 0 : pair * W * RB + w * RB));
         }
     }
     __syncwarp();
@@ -561,8 +567,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     const uint64_t qd0 = tc::sdesc_sw128(tc::smem_u32(sQ)), kd0 = tc::sdesc_sw128(tc::smem_u32(sK(0))),
                    vd0 = sdesc_nmajor(tc::smem_u32(sV(0)));
     auto qk = [&](int w, int j) -> bool {
-      const int s = j % NST;
-      if ((w == 0 || j >= n[0]) && !wait(&B.full[s], (uint32_t)((j / NST) & 1), abort)) return false;
+      const int it = HEADS ? (j << two) + w : j, s = it % NST;
+      if ((HEADS || w == 0 || j >= n[0]) && !wait(&B.full[s], (uint32_t)((it / NST) & 1), abort)) return false;
       if (j > 0 && !wait(&B.s_free[w], (uint32_t)((j - 1) & 1), abort)) return false;
       tc::tc_fence_after();
       if (lead) {
@@ -576,7 +582,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       return true;
     };
     auto pv = [&](int w, int j) -> bool {
-      const int s = j % NST;
+      const int s = (HEADS ? (j << two) + w : j) % NST;
       if (!wait(&B.p_full[w], (uint32_t)(j & 1), abort)) return false;
       tc::tc_fence_after();
       if (lead) {
@@ -586,7 +592,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
           umma_ts(tmem + TM_O + 64u * w, tmem + TM_P + 64u * w + 8u * kk, vd + (uint64_t)(kk * 128), IDESC_PV,
                   (j | kk) ? 1u : 0u);
         tc::umma_commit(&B.pv_done[w]);
-        if (w == W - 1 || j >= n[W - 1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
+        if (HEADS || w == W - 1 || j >= n[W - 1]) tc::umma_commit(&B.empty[s]);     // the stage's last reader
       }
       __syncwarp();
       return true;
@@ -621,14 +627,14 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     const int w = (warp >> 2) - (Q8 ? 2 : 1), quarter = warp & 3, x = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t tS = tl + TM_S + 128u * w, tP = tl + TM_P + 64u * w, tO = tl + TM_O + 64u * w;
-    const int first = rho0 + w * TR, rho = first + x;
-    const bool on = x < TR && rho < R;
+    const int first = rho0 + (HEADS ? 0 : w * TR), rho = first + x, hw = HEADS ? h + w : h;
+    const bool on = x < TR && rho < R && (!HEADS || w <= two);
     const int t = on ? rho / p.G : 0;
     const int lim = on ? row_limit(p, r, t) : 0, lim_all = first < R ? row_limit(p, r, first / p.G) : 0;
     const int nw = n[w];
     float sl = p.sl;
     if (GROUPS && nw > 0) {                        // this row's query as fp16, its largest element in 1 .. 2
-      const bf16* q = (const bf16*)p.a.q + (size_t)(r.row0 + t) * p.a.q_stride + (size_t)(h * p.G + (on ? rho - t * p.G : 0)) * WS_DH;
+      const bf16* q = (const bf16*)p.a.q + (size_t)(r.row0 + t) * p.a.q_stride + (size_t)(hw * p.G + (on ? rho - t * p.G : 0)) * WS_DH;
       uint4 v[8];
       float most = 0.f;
 #pragma unroll
@@ -662,7 +668,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       float sv[FA_KEYS];
 #pragma unroll
       for (int q = 0; q < 8; ++q) tm_ld16(tS + 16 * q, sv + 16 * q);
-      const Meta& mt = meta[j % NST];
+      const int stage = (HEADS ? (j << two) + w : j) % NST;
+      const Meta& mt = meta[stage];
       const int base = mt.base;
       const bool dense = mt.full && base + FA_KEYS <= lim_all;
       ld_wait();
@@ -682,7 +689,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       }
       // P and O are free once the previous product has finished
       if (j > 0 && !wait_warp(&B.pv_done[w], (uint32_t)((j - 1) & 1), abort)) { ok = false; break; }
-      const float* ks = s_ks[GROUPS ? j % NST : 0];
+      const float* ks = s_ks[GROUPS ? stage : 0];
       float2 sum2[2];
       float slk[8];                                // of the groups
 #pragma unroll
@@ -758,16 +765,16 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     if (ok && nw > 0) ok = wait_warp(&B.pv_done[w], (uint32_t)((nw - 1) & 1), abort);
     tc::tc_fence_after();
-    const bool any_odd = nw > 0 && *(volatile int*)&odd.any != 0;
+    const bool any_odd = nw > 0 && *(volatile int*)&odds[HEADS ? w : 0].any != 0;
     if (p.nsplit > 1) {
-      const size_t at = on ? (((size_t)i * p.c.n_kv_heads + h) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split : 0;
+      const size_t at = on ? (((size_t)i * p.c.n_kv_heads + hw) * ((size_t)p.a.max_q * p.G) + rho) * p.nsplit + split : 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float o[16];
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
         if (any_odd)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
+          for (int e = 0; e < 16; ++e) o[e] = with_odd(odds[HEADS ? w : 0], o[e], lim, 16 * q + e);
         if (on)
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
@@ -777,7 +784,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (on) p.part_ml[at] = make_float2(m == -INFINITY ? m : msl, ok ? l : NAN);
     } else {
       const float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / l;
-      const int u_ = h * p.G + (on ? rho - t * p.G : 0);
+      const int u_ = hw * p.G + (on ? rho - t * p.G : 0);
       bf16* out = (bf16*)p.a.out + (size_t)(r.row0 + t) * p.a.out_stride + (size_t)u_ * WS_DH;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -785,7 +792,7 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         if (nw > 0) { tm_ld16(tO + 16 * q, o); ld_wait(); }
         if (any_odd)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = with_odd(odd, o[e], lim, 16 * q + e);
+          for (int e = 0; e < 16; ++e) o[e] = with_odd(odds[HEADS ? w : 0], o[e], lim, 16 * q + e);
         uint32_t u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e] = nw > 0 ? pack_bf(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
@@ -1042,27 +1049,27 @@ fa_mass_kernel(const AttnP p, int tiles, long long items, const __grid_constant_
   if (warp == 1) tc::tmem_dealloc(tmem, 256);
 }
 
-template <int W, int MODE>
+template <int W, int MODE, bool HEADS = false>
 cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
   using Shape = FaShape<W, MODE>;
-  cudaError_t e = cudaFuncSetAttribute(fa_kernel<W, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::SMEM);
+  constexpr auto kernel = fa_kernel<W, MODE, HEADS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::SMEM);
   if (e != cudaSuccess) return e;
-  fa_kernel<W, MODE><<<dim3((p.row_tiles + W - 1) / W * p.nsplit, p.c.n_kv_heads, p.a.n_req), Shape::THREADS, Shape::SMEM, s>>>(
-      p, reinterpret_cast<const CUtensorMap&>(mq), reinterpret_cast<const CUtensorMap&>(mk),
-      reinterpret_cast<const CUtensorMap&>(mv));
+  const dim3 grid((p.row_tiles + W - 1) / W * p.nsplit, HEADS ? (p.c.n_kv_heads + 1) / 2 : p.c.n_kv_heads, p.a.n_req);
+  kernel<<<grid, Shape::THREADS, Shape::SMEM, s>>>(p, reinterpret_cast<const CUtensorMap&>(mq),
+                                                   reinterpret_cast<const CUtensorMap&>(mk),
+                                                   reinterpret_cast<const CUtensorMap&>(mv));
   ws_count_launches(1);
   return cudaGetLastError();
 }
 template <int MODE>
-cudaError_t run_fa(const AttnP& p, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
-  if constexpr (MODE == MODE_BF16)
-    if (p.row_tiles == 1) return run_fa<1, MODE>(p, mq, mk, mv, s);
-  return run_fa<2, MODE>(p, mq, mk, mv, s);
+cudaError_t run_q8(const AttnP& p, bool two_heads, const TcMap& mq, const TcMap& mk, const TcMap& mv, cudaStream_t s) {
+  return two_heads ? run_fa<2, MODE, true>(p, mq, mk, mv, s) : run_fa<2, MODE>(p, mq, mk, mv, s);
 }
 
 }  // namespace
 
-cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
+cudaError_t launch_fa(const AttnP& p, bool two_heads, cudaStream_t s) {
   TcMap mq, mk, mv;
   if (!tc_encode_heads(&mq, p.a.q, p.a.q_stride, (uint64_t)p.a.total_q, (uint32_t)p.a.n_heads, (uint32_t)p.G,
                        (uint32_t)(FA_ROWS / p.G)))
@@ -1070,8 +1077,8 @@ cudaError_t launch_fa(const AttnP& p, cudaStream_t s) {
   if (!tc_encode_paged(&mk, p.c.k, p.c, (uint32_t)p.geo.box) || !tc_encode_paged(&mv, p.c.v, p.c, (uint32_t)p.geo.box))
     return cudaErrorInvalidValue;
   if (p.c.dtype == WS_E4M3)
-    return p.c.scale_block % 16 == 0 ? run_fa<MODE_GROUPS>(p, mq, mk, mv, s) : run_fa<MODE_ANY>(p, mq, mk, mv, s);
-  return run_fa<MODE_BF16>(p, mq, mk, mv, s);
+    return p.c.scale_block % 16 == 0 ? run_q8<MODE_GROUPS>(p, two_heads, mq, mk, mv, s) : run_q8<MODE_ANY>(p, two_heads, mq, mk, mv, s);
+  return p.row_tiles == 1 ? run_fa<1, MODE_BF16>(p, mq, mk, mv, s) : run_fa<2, MODE_BF16>(p, mq, mk, mv, s);
 }
 
 cudaError_t launch_fa_mass(const AttnP& p, cudaStream_t s) {

@@ -267,6 +267,44 @@ def test_attend_8bit_pages_in_pieces(R, page, block, chunks, lens, layout):
     check_q8(R, Q8Case(chunks, lens, 2, 2, page, block=block, layout=layout, seed=page + len(chunks)))
 
 
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 2), (3, 3), (10, 5)])
+@pytest.mark.parametrize("page,block", [(64, 16), (16, 8), (48, 48)])
+@pytest.mark.parametrize("chunks,lens", [([60], [61]), ([64, 50, 3], [64, 1200, 700]), ([55, 0, 64], [4000, 5, 90])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_8bit_single_row_tiles(R, hq, hkv, page, block, chunks, lens, causal):
+    """Up to 128 rows per KV head: odd and even numbers of heads, in one part and in several."""
+    check_q8(R, Q8Case(chunks, lens, hq, hkv, page, block=block, causal=causal, seed=hkv + page))
+
+
+@pytest.mark.parametrize("n,hkv,page,block,causal", [(154, 1, 64, 16, True), (31, 5, 64, 16, False), (31, 5, 16, 8, True),
+                                                     (54, 3, 48, 16, True)])
+def test_attend_8bit_single_row_tiles_of_many(R, n, hkv, page, block, causal):
+    """More heads in all than the machine has SMs."""
+    chunks = [27 - (7 * i) % 12 if i % 9 else i % 2 for i in range(n)]
+    check_q8(R, Q8Case(chunks, [c + (37 * i) % 200 for i, c in enumerate(chunks)], 2 * hkv, hkv, page, block=block,
+                       causal=causal, seed=n))
+
+
+@pytest.mark.parametrize("heads", [[0], [1], [0, 2]])
+def test_attend_8bit_nan_of_a_head(R, heads):
+    """NaN values that later rows alone see, in some of the heads: those rows of those heads, and nothing else."""
+    for n in (1, 60):                                      # as few heads as are taken one by one, and more
+        cs = Q8Case([100] * n, [300] * n, 3, 3, 32, block=16, seed=3)
+        c = cs.cache(R)
+
+        def attend():
+            return c.attend(cs.q, cs.kv_len, cs.cu, max_q=100, max_kv=300)[: cs.rows].clone()
+        clean = attend()
+        page, at = int(cs.table[n - 1, 290 // 32]), 290 % 32
+        for h in heads:
+            cs.v8.view(torch.uint8)[page, h, at, 7] = 0x7F
+        got = attend()
+        torch.cuda.synchronize()
+        hit = torch.zeros_like(clean, dtype=torch.bool)
+        hit[100 * n - 10:, heads, 7] = True                # row r of the last chunk sees positions up to 200 + r
+        assert bool(torch.isnan(got)[hit].all()) and torch.equal(got[~hit], clean[~hit])
+
+
 def test_calls_on_other_streams(R):
     """Calls on two streams, with an object each, between calls on the current one: the same bits."""
     cs = Q8Case([5, 60], [700, 900], 4, 2, 32, block=16, seed=6)
