@@ -712,7 +712,10 @@ Plan make_plan(const ws_paged_cache& c, const ws_attention_args& a, bool block =
     q.nt = R <= 8 ? 1 : 2;
     q.row_tiles = (int)((R + 8 * q.nt - 1) / (8 * q.nt));
     const long long units = (long long)a.n_req * c.n_kv_heads * q.row_tiles;
-    q.geo = tile_geo(c.page_size, Q8_TK);
+    // 96 x 9 rows take 80 us in pieces of 16 positions for 95 in short tiles
+    // with pages of 48, 80 for 84 with 80, 85 in pieces of eight for 110 with
+    // 40 (72 with pages of 64)
+    q.geo = tile_geo(c.page_size, Q8_TK, true);
     const int tiles = max(1, tile_count(q.geo, c.page_size, Q8_TK, a.max_kv));
     // Splits of at least 512 keys: for one request a round of CTAs, three per
     // SM (20 heads over 65,536 positions 40 us with 22 splits, 52 with 31, 61

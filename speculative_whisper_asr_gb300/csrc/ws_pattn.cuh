@@ -16,8 +16,8 @@ struct TileGeo {
 };
 // `split`: pages that neither divide a tile nor hold whole ones may be taken in
 // pieces that do (their largest power of two), else a page's last tile is
-// short.  Many copies of eight keys cost a third, so those only where short
-// tiles would be less than three quarters full.
+// short.  Many copies of eight keys cost up to a third, so those only where
+// short tiles would be less than three quarters full.
 inline TileGeo tile_geo(int page_size, int tk, bool split = false) {
   TileGeo g = {};
   const int piece = page_size & -page_size;

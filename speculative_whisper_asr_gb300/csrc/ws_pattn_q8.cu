@@ -139,7 +139,8 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
   const int32_t* table = p.c.page_table + (size_t)min(max(slot0, 0), p.c.n_slots - 1) * p.c.table_stride;
   TileWalk w;
   auto page_of = [&]() -> int {            // table entry of this lane's key in the walk's tile, -1: none
-    const int e = w.entry(p.geo, lane);
+    int e = w.entry(p.geo, lane);
+    if (!UNI && p.geo.pieces > 1) e /= p.geo.pieces;
     return e < p.c.table_stride ? __ldg(table + e) : -1;
   };
   w.start(p.geo, split * p.tps + warp, W);
@@ -175,15 +176,17 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       tc::mbar_expect_tx(&full[warp][slot], (uint32_t)__popc(boxes) * 2u * (uint32_t)p.geo.box * (uint32_t)WS_DH);
     }
     __syncwarp();
+    // several pages: first token of this lane's copy
+    const int tok0 = !UNI && p.geo.pieces > 1 ? w.entry(p.geo, lane) % p.geo.pieces * p.geo.box : 0;
     if (go) {
       uint8_t* dst = ring + slot * (2 * TB) + (p.geo.tpp ? 0 : lane * WS_DH);
-      const int tok = p.geo.tpp ? w.sub * TK : 0;
+      const int tok = p.geo.tpp ? w.sub * TK : tok0;
       tma_load_4d(dst, &mk, &full[warp][slot], 0, tok, h, page);
       tma_load_4d(dst + TB, &mv, &full[warp][slot], 0, tok, h, page);
     }
     k_byte = v_byte = 0;
     if (ok) {
-      const uint32_t tok = (uint32_t)(p.geo.tpp ? w.sub * TK + (UNI ? 0 : lane) : lane & (p.geo.box - 1));
+      const uint32_t tok = (uint32_t)(p.geo.tpp ? w.sub * TK + (UNI ? 0 : lane) : tok0 + (lane & (p.geo.box - 1)));
       uint32_t b = p.block_mul ? __umulhi(tok, p.block_mul) : tok;        // tok / scale_block, or one more
       b -= b * (uint32_t)p.c.scale_block > tok;
       const uint64_t at = (uint64_t)(uint32_t)page * (uint32_t)p.c.scale_page_stride + b;
