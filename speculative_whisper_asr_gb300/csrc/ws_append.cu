@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(8 * AP_T, 2) append_kernel(const AppendP p) {
               const int e_now = max(e_was, scale_exponent(__uint_as_float(s_max[m0 + u])));
               uint8_t* at = to8 + u * step;
               if (live) {
-                const float f = __uint_as_float((uint32_t)(127 - min(e_now, 126)) << 23);    // 2^-e_now
+                const float f = pow2(-e_now);               // 2^-127 for byte 254 is below the normal numbers
                 if (odd)
 #pragma unroll
                   for (int e = 0; e < 8; ++e) x[u][e] = fabsf(x[u][e]) < INFINITY ? x[u][e] : NAN;
