@@ -532,7 +532,8 @@ size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attent
  * A cache in 8 bits is read as the values it stands for (queries and outputs
  * bfloat16, the same sums).  The weights enter the value product as fp16, and
  * besides its 2^-11 of itself a weight may be off by 2^-30 of the row's largest
- * weight times the largest value scale among the keys, over its value's own.
+ * weight times the largest value scale among the keys that the row sees, over
+ * its value's own.
  * The weights are not accumulated: mass is WS_EUNSUPPORTED. */
 int ws_paged_attention(const ws_paged_cache* cache, const ws_attention_args* args, void* workspace,
                        size_t workspace_bytes, ws_stream stream);

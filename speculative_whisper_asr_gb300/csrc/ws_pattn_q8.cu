@@ -19,8 +19,8 @@
 // Scales never touch an element: a key's multiplies its scores (fp32), a
 // value's its weight.  Weights enter the product as fp16, 2^-11 of each at
 // most, an eighth of the bf16 output's own step, relative to 2^E, the largest
-// value scale so far, so that they stay within fp16 whatever the scales are.
-// They are at most 2^8 and stored 2^7 times larger, so that fp16's last step is
+// value scale that the row has seen so far, so that they stay within fp16
+// whatever the scales are.  They are at most 2^8 and stored 2^7 times larger, so that fp16's last step is
 // 2^-31 of a row's largest weight times the largest value scale.  Queries, 8 bits each, are
 // exact in fp16 once a row's largest is brought to 1 .. 2 by a power of two,
 // which joins the row's scale; elements below 2^-17 of the largest round to
@@ -279,7 +279,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
   }
-  int E = 0;                               // byte of the largest value scale so far
+  int E[MIX ? NT : 1][MIX ? 2 : 1] = {};   // byte of the largest value scale that the rows have seen so far
   const bool mixed = MIX && Lmin < Lmax;   // some row does not see all of the tile's positions
   if (MIX && lane == 0) odd[warp].any = 0;
   const int key_g = KEY(g), key_c = KEY(2 * c);            // of places g and 2 c
@@ -373,20 +373,63 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
               if (!ok || base + j >= lim[nt][e]) sc[mt][nt][2 * e2 + e] = -INFINITY;
         }
     }
-    // ---- a larger value scale than before?
-    {
-      const int most = UNI ? vs[0][0] : max(max(vs[0][0], vs[0][1]), max(vs[1][0], vs[1][1]));
-      if (__any_sync(ALL, most > E)) {
-        const int now = UNI ? most : __reduce_max_sync(ALL, max(most, E));
-        const float f = down(E - now);
-        E = now;
+    // ---- a larger value scale than before?  The same for all rows as long as
+    // they see the same; then each row's own, of the keys that it sees: a scale
+    // that it does not see would take its weights' last bits, or all of them.
+    constexpr bool OWN = MIX && decltype(last_tiles)::value;
+    const int most = UNI ? vs[0][0] : max(max(vs[0][0], vs[0][1]), max(vs[1][0], vs[1][1]));
+    int least = E[0][0];                   // of this lane's rows
+    if (OWN)
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 2; ++e) least = min(least, E[MIX ? nt : 0][MIX ? e : 0]);
+    const bool larger = __any_sync(ALL, most > least);
+    if (OWN && larger) {
+      int now[NT][2];
+      bool more = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][nt][e] *= f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          now[nt][e] = E[MIX ? nt : 0][MIX ? e : 0];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              const int j = 16 * mt + 8 * e2 + key_g, s = UNI ? vs[0][0] : vs[mt][e2];
+              if (((valid >> j) & 1u) && base + j < lim[nt][e] && s > now[nt][e]) { now[nt][e] = s; more = true; }
+            }
+        }
+      if (__any_sync(ALL, more)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            int t = now[nt][e];
+            t = max(t, __shfl_xor_sync(ALL, t, 4));
+            t = max(t, __shfl_xor_sync(ALL, t, 8));
+            t = max(t, __shfl_xor_sync(ALL, t, 16));
+            int& was = E[MIX ? nt : 0][MIX ? e : 0];
+            const float f = down(was - t);
+            was = t;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) { o[d][nt][e] *= f; o[d][nt][2 + e] *= f; }
+          }
       }
+    } else if (larger) {
+      const int now = UNI ? most : __reduce_max_sync(ALL, max(most, least));
+      const float f = down(least - now);
+#pragma unroll
+      for (auto& row : E)
+#pragma unroll
+        for (int& x : row) x = now;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[d][nt][e] *= f;
     }
     // ---- does a score pass its row's reference by more than 2^8?
     bool grow = false;
@@ -422,19 +465,25 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
 #pragma unroll
       for (int e = 0; e < 2; ++e) ref[nt][e] = m[nt][e] > -INFINITY ? m[nt][e] : 0.f;
     uint32_t pf[MT][NT][2];
-    const float fu = UNI ? down(vs[0][0] - E) * RAISE : 0.f;
+    // a weight's factor; keys that a row does not see have weight 0, whatever their scale
+    auto factor = [&](int s, int nt, int e) { return down(OWN ? min(s - E[MIX ? nt : 0][MIX ? e : 0], 0) : s - E[0][0]) * RAISE; };
+    float fu[NT][2] = {};                  // UNI: of all keys
+    if (UNI)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) fu[nt][e] = factor(vs[0][0], nt, e);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int e2 = 0; e2 < 2; ++e2) {
-        const float f = UNI ? fu : down(vs[mt][e2] - E) * RAISE;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float p0 = ex2(fmaf(sc[mt][nt][2 * e2], slk[nt][0], -ref[nt][0]));
           const float p1 = ex2(fmaf(sc[mt][nt][2 * e2 + 1], slk[nt][1], -ref[nt][1]));
           l[nt][0] += p0;
           l[nt][1] += p1;
-          pf[mt][nt][e2] = movm(pack_f16(p0 * f, p1 * f));
+          pf[mt][nt][e2] = movm(pack_f16(p0 * (UNI ? fu[nt][0] : factor(vs[mt][e2], nt, 0)), p1 * (UNI ? fu[nt][1] : factor(vs[mt][e2], nt, 1))));
         }
       }
     // ---- O^T: dims 8 g + 2 d (rows 0 .. 7 of step d) and 8 g + 2 d + 1 (rows 8 .. 15)
@@ -470,7 +519,6 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
   __syncthreads();
   float* so = reinterpret_cast<float*>(sm);                // [warp][8 NT][OP]
   float* sml = so + W * 8 * NT * OP;                       // [warp][8 NT][2]: reference in log2 units, sum
-  const float size = scale_of((uint32_t)E) * (1.0f / RAISE);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -480,6 +528,7 @@ q8_kernel(const AttnP p, const __grid_constant__ CUtensorMap mk, const __grid_co
       s += __shfl_xor_sync(ALL, s, 8);
       s += __shfl_xor_sync(ALL, s, 16);
       const int row = 8 * nt + 2 * c + e;
+      const float size = scale_of((uint32_t)E[MIX ? nt : 0][MIX ? e : 0]) * (1.0f / RAISE);
       float* dst = so + (warp * 8 * NT + row) * OP;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
