@@ -263,8 +263,9 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, u
 
 // A cache in 8 bits: warps 0 and 2 copy codes and scales of keys and of values,
 // AHEAD tiles at once, and a warpgroup of converters (warps 4..7) writes the
-// stages from them, rows that do not count as zeros; NaN values that not every
-// row sees are noted and left out at once, so there is nothing to clean.
+// stages from them, rows that do not count as zeros; values that are not finite
+// and that not every row sees are noted and left out at once, so there is
+// nothing to clean.
 // (Codes loaded into the converters' registers, or by copies of their own, cost
 // a memory latency per tile: a warp's fence before its stores may be read
 // waits for whatever it has asked for; 4 x 2048 rows 368 and 590 us.)  W = 2
@@ -448,7 +449,8 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         uint4 kw = *reinterpret_cast<const uint4*>(src), vw = *reinterpret_cast<const uint4*>(src + TILE / 2);
         if (!all && !((valid[x >> 5] >> (x & 31)) & 1u)) kw = vw = make_uint4(0u, 0u, 0u, 0u);
         uint4 klo, khi, vlo, vhi;
-        widen16(vw, s_scale[1][slot][GROUPS ? x >> 4 : x], vlo, vhi);
+        const uint32_t v_byte = s_scale[1][slot][GROUPS ? x >> 4 : x];
+        widen16(vw, v_byte, vlo, vhi);
         if (GROUPS) halves16(kw, klo, khi);
         else widen16(kw, s_scale[0][slot][x], klo, khi);
         const uint32_t at = (uint32_t)(x * 128 + (((2 * (lane & 3)) ^ (x & 7)) << 4)), at2 = at ^ 16u;
@@ -456,13 +458,16 @@ fa_kernel(const AttnP p, const __grid_constant__ CUtensorMap mq, const __grid_co
         *reinterpret_cast<uint4*>(sK(s) + at2) = khi;
         *reinterpret_cast<uint4*>(sV(s) + at) = vlo;
         *reinterpret_cast<uint4*>(sV(s) + at2) = vhi;
-        // NaN values that not every row sees: noted, and zero to the product
-        if (!seen && ((nan_codes(vw.x) | nan_codes(vw.y) | nan_codes(vw.z) | nan_codes(vw.w)) & 0x80808080u)) {
+        // values that are not finite and that not every row sees: noted, and zero to the product.  NaN codes, and what
+        // passes fp32, 2^(code's exponent - 7 + byte - 127) of at least 2^128.
+        if (!seen && (v_byte >= 262u - 15u || ((nan_codes(vw.x) | nan_codes(vw.y) | nan_codes(vw.z) | nan_codes(vw.w)) & 0x80808080u))) {
 #pragma unroll 1
           for (int e = 0; e < 16; ++e) {
-            if ((src[TILE / 2 + e] & 0x7Fu) != 0x7Fu || base + x < all_see) continue;
+            const uint32_t code = src[TILE / 2 + e];
+            const bool nan = (code & 0x7Fu) == 0x7Fu;
+            if (!(nan || (code >> 3 & 15u) + v_byte >= 262u) || base + x < all_see) continue;
             *reinterpret_cast<uint16_t*>(sV(s) + (e < 8 ? at : at2) + 2u * (e & 7)) = 0u;
-            atomicMin(&odds[j & two].first[2][16 * (lane & 3) + e], base + x);
+            atomicMin(&odds[j & two].first[nan ? 2 : code >> 7][16 * (lane & 3) + e], base + x);
             odds[j & two].any = 1;
           }
         }

@@ -79,3 +79,50 @@ def test_attend_8bit_scales_that_grow_along_a_chunk(R):
         lim = L - c + t + 1
         floor = 2.0 ** -30 * lim * 2 * float(v[:lim].abs().max())
         assert bool(((got[t] - o[t]).abs() <= to[t] + floor).all()), t
+
+
+@pytest.mark.parametrize("n,hkv,c", [(1, 1, 60), (1, 2, 100), (2, 1, 300), (60, 3, 60)])
+@pytest.mark.parametrize("page,block", [(64, 16), (64, 8), (48, 48)])
+@pytest.mark.parametrize("code,scale", [(0x78, 247), (0xFE, 247), (0x7E, 254), (0xF1, 248)])
+def test_attend_8bit_infinite_values_stay_where_they_are_seen(R, n, hkv, c, page, block, code, scale):
+    """Elements whose value passes fp32 (256 * 2^120, as an append of finite rows may leave it) in a position that the
+    last row alone sees, in one head of one request: that row's element is infinite, and nothing else differs."""
+    L = 6 * 96 + 1                                         # a block of its own in every page size
+    cs = Q8Case([c] * n, [L] * n, hkv, hkv, page, block=block, seed=c)
+    at = int(cs.table[n - 1, (L - 1) // page]), hkv - 1, (L - 1) % page
+    codes = cs.v8.view(torch.uint8)
+    codes[at] = 0
+    cache = cs.cache(R)
+
+    def attend():
+        return cache.attend(cs.q, cs.kv_len, cs.cu, max_q=c, max_kv=L)[: cs.rows].clone()
+    want = attend()
+    codes[at[0], at[1], at[2], 7] = code
+    cs.scales[1][at[0], at[1], at[2] // block] = scale
+    got = attend()
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[n * c - 1, hkv - 1, 7] = True
+    assert torch.equal(got[~hit], want[~hit])
+    assert float(got[hit]) == (-math.inf if code & 0x80 else math.inf)
+
+
+def test_attend_8bit_infinite_values_of_both_signs(R):
+    """Rows that see none, one or both of them."""
+    c, L = 100, 401
+    cs = Q8Case([c], [L], 1, 1, 16, block=16, seed=1)
+    codes = cs.v8.view(torch.uint8)
+    cache = cs.cache(R)
+    for pos in (384, 400):
+        codes[int(cs.table[0, pos // 16]), 0, :] = 0
+    want = cache.attend(cs.q, cs.kv_len, cs.cu, max_q=c, max_kv=L)[:c].clone()
+    for pos, code in ((384, 0x7C), (400, 0xFC)):
+        page = int(cs.table[0, pos // 16])
+        codes[page, 0, 0, 3] = code
+        cs.scales[1][page] = 250
+    got = cache.attend(cs.q, cs.kv_len, cs.cu, max_q=c, max_kv=L)[:c]
+    torch.cuda.synchronize()
+    others = [d for d in range(D) if d != 3]
+    assert torch.equal(got[:, 0, others], want[:, 0, others])
+    assert torch.equal(got[:83], want[:83])                # row r sees 302 + r positions
+    assert bool((got[83:99, 0, 3] == math.inf).all()) and bool(torch.isnan(got[99, 0, 3]))
