@@ -349,7 +349,7 @@ extern "C" int ws_cache_append(const ws_paged_cache* cache, const ws_append_args
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
   AppendP p = {};
-  p.c = *cache;
+  p.c = paged_copy(*cache);
   p.a = *args;
   const bool q8 = cache->dtype == WS_E4M3;
   p.items = (args->q ? args->n_heads : 0) + 2 * cache->n_kv_heads;

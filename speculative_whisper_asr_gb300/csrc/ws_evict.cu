@@ -415,7 +415,7 @@ size_t cache_evict_workspace(const ws_paged_cache& cache, const ws_evict_args& a
 
 cudaError_t launch_cache_evict(const ws_paged_cache& cache, const ws_evict_args& args, void* workspace, cudaStream_t s) {
   EvictP p = {};
-  p.c = cache;
+  p.c = paged_copy(cache);
   p.a = args;
   const bool in_place = !args.page_table_out || args.page_table_out == cache.page_table;
   p.tout = in_place ? cache.page_table : args.page_table_out;

@@ -3,6 +3,8 @@
 #pragma once
 #include <limits.h>
 #include <math.h>
+#include <stddef.h>
+#include <string.h>
 
 #include <string>
 
@@ -42,6 +44,14 @@ inline const char* check_paged_cache(const ws_paged_cache* c) {
       return "scale strides must be >= page_size / scale_block and less than 2^31";
   }
   return nullptr;
+}
+
+// The description for a kernel.  What describes caches in 8 bits came last and
+// is read for those alone: a program built before has a shorter structure.
+inline ws_paged_cache paged_copy(const ws_paged_cache& c) {
+  ws_paged_cache r = {};
+  memcpy(&r, &c, c.dtype == WS_E4M3 ? sizeof r : offsetof(ws_paged_cache, k_scale));
+  return r;
 }
 
 inline int paged_fail(int code, const std::string& msg) {

@@ -810,7 +810,7 @@ cudaError_t run_8bit(const AttnP& p, const Plan& q, cudaStream_t s) {
 cudaError_t run(const ws_paged_cache& cache, const ws_attention_args& args, int pad_H, const int32_t* chunk_len,
                 const Plan& q, char* ws, cudaStream_t s) {
   AttnP p = {};
-  p.c = cache;
+  p.c = paged_copy(cache);
   p.a = args;
   p.pad_H = pad_H;
   p.chunk_len = chunk_len;

@@ -117,7 +117,7 @@ extern "C" int ws_cache_reorder(const ws_paged_cache* cache, const ws_reorder_ar
   if (cudaError_t prior = cudaPeekAtLastError(); prior != cudaSuccess)
     return paged_fail(WS_ECUDA, std::string("a CUDA error was pending before this call: ") + cudaGetErrorString(prior));
   ReorderP p = {};
-  p.c = *cache;
+  p.c = paged_copy(*cache);
   p.a = *args;
   p.ppr_log = cache->dtype == WS_F32 ? 4 : cache->dtype == WS_BF16 ? 3 : 2;
   // two rounds of CTAs (16 per SM), each with as much of a request as comes

@@ -2,6 +2,8 @@
 scale bytes at both ends of their range, values whose product with the scale
 passes fp32, and what rows that do not see such blocks must not feel."""
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -126,3 +128,61 @@ def test_attend_8bit_infinite_values_of_both_signs(R):
     assert torch.equal(got[:, 0, others], want[:, 0, others])
     assert torch.equal(got[:83], want[:83])                # row r sees 302 + r positions
     assert bool((got[83:99, 0, 3] == math.inf).all()) and bool(torch.isnan(got[99, 0, 3]))
+
+
+# ------------------------------------------------------------------ the description of a cache
+# One that is not in 8 bits, as long as it was before there were caches in 8 bits, at the very end of a mapping: what
+# the library reads behind it ends the process on the host.
+SHORT = """
+import ctypes as C, mmap, sys
+sys.path.insert(0, {root!r})
+import torch
+from speculative_whisper_asr_gb300 import binding as B, runtime as R
+libc = C.CDLL(None)
+libc.mmap.restype = C.c_void_p
+libc.mmap.argtypes = [C.c_void_p, C.c_size_t, C.c_int, C.c_int, C.c_int, C.c_long]
+libc.mprotect.argtypes = [C.c_void_p, C.c_size_t, C.c_int]
+size, page = B.PagedCacheDesc.k_scale.offset, mmap.PAGESIZE
+at = libc.mmap(None, 2 * page, mmap.PROT_READ | mmap.PROT_WRITE, mmap.MAP_PRIVATE | mmap.MAP_ANONYMOUS, -1, 0)
+assert at not in (None, C.c_void_p(-1).value) and libc.mprotect(at + page, page, 0) == 0
+class Short:
+    def __init__(self, desc):
+        C.memmove(at + page - size, C.addressof(desc), size)
+C_addressof = C.addressof
+B.C.addressof = lambda x: at + page - size if isinstance(x, Short) else C_addressof(x)
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+torch.manual_seed(0)
+state = []
+for short in (False, True):
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(6, 2, 16, 64, generator=g).to(torch.{dtype}).cuda() for _ in range(2))
+    rows = torch.randn(3, 8, 64, generator=g).to(torch.{dtype}).cuda()
+    cache = R.PagedCache(k, v, i32(0, 1, 2, 3, 4, 5).view(2, 3))
+    if short:
+        cache.desc = Short(cache.desc)
+    L, cu = i32(20, 20), i32(0, 2, 3)
+    mass = torch.rand(2, 2, 48, generator=g).cuda()
+    cache.append(rows[:, :2], rows[:, 2:4], L, cu, max_q=2)
+    out = cache.attend(rows[:, 4:].contiguous(), L, cu, max_q=2, max_kv=20, mass=mass)
+    if short:
+        a = cache._reorder
+        a.n_req, a.beams, a.req_ids, a.kv_len, a.page_table = 1, 2, 0, L.data_ptr(), 0
+        parent = i32(1, 1)
+        a.parent = parent.data_ptr()
+        B.ws_cache_reorder(cache.desc, a, torch.cuda.current_stream().cuda_stream)
+    else:
+        cache.reorder(i32(1, 1).view(1, 2), L, table=False)
+    cache.evict(L, mass, keep=10, max_kv=20)
+    torch.cuda.synchronize()
+    state.append([k, v, rows, out, mass, L])
+assert all(torch.equal(a, b) for a, b in zip(*state))
+print("done")
+"""
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_scales_of_other_caches_are_not_read(R, dtype):
+    import __graft_entry__ as g
+    r = subprocess.run([sys.executable, "-c", SHORT.format(root=g.ROOT, dtype=dtype)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, (r.returncode, r.stderr[-1500:])
