@@ -735,7 +735,9 @@ typedef struct {
  * candidate is left for get score -inf, token -1 and themselves as parent.
  * A request with max_done finished transcripts, or a full one (length >=
  * capacity), is idle: parent itself, token -1, all else as it was.
- * tokens_out behind the new length is left as it was.  The same call gives
+ * tokens_out behind the new length is left as it was.  Outputs share no
+ * elements with each other, nor with score, tokens, length and n_done but the
+ * one whose place they may take.  The same call gives
  * the same bits, and equal rows give equal sums wherever they lie. */
 int ws_beam_select(const ws_beam_args* args, void* workspace, size_t workspace_bytes, ws_stream stream);
 size_t ws_beam_select_workspace(const ws_beam_args* args);

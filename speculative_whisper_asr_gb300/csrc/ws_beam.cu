@@ -367,6 +367,22 @@ const char* check_beam(const ws_beam_args* a) {
   return nullptr;
 }
 
+// What one request's threads write must not be what others read or write.
+const char* check_beam_apart(const ws_beam_args* a) {
+  const long long rows = 4ll * a->n * a->beams, reqs = 4ll * a->n, text = a->tokens ? rows * a->capacity : 0;
+  const long long done = reqs * a->max_done;
+  struct Array { const void* p; long long bytes; const void* in; };          // in: what it may take the place of
+  const Array outs[] = {{a->score_out, rows, a->score}, {a->parent, rows, nullptr}, {a->token, rows, nullptr},
+                        {a->tokens_out, text, a->tokens}, {a->length_out, reqs, a->length}, {a->n_done_out, reqs, a->n_done},
+                        {a->done_score, done, nullptr}, {a->done_length, done, nullptr},
+                        {a->done_tokens, a->tokens ? done * a->capacity : 0, nullptr}};
+  for (const Array& x : outs)
+    for (const Array& y : outs)
+      if (&x != &y && (!apart(x.p, y.p, x.bytes, y.bytes) || !apart(x.p, y.in, x.bytes, y.bytes)))
+        return "outputs must share no elements with each other, nor with inputs other than their own";
+  return nullptr;
+}
+
 struct Plan { int parts, part; size_t stat, bytes; };
 // Twelve CTAs of 128 threads run on an SM: as many parts as fill that round
 // (a row is read once whatever they are), none longer than 256 logits per
@@ -392,6 +408,7 @@ extern "C" size_t ws_beam_select_workspace(const ws_beam_args* args) {
 extern "C" int ws_beam_select(const ws_beam_args* args, void* workspace, size_t workspace_bytes, ws_stream stream) {
   if (const char* e = check_beam(args)) return fail(WS_EINVAL, e);
   if (args->n == 0) return WS_OK;
+  if (const char* e = check_beam_apart(args)) return fail(WS_EINVAL, e);
   const Plan q = make_plan(*args);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15)) return fail(WS_EINVAL, "workspace must be 16-byte aligned and not null");
   if (q.bytes > workspace_bytes) return fail(WS_ENOSPACE, "workspace smaller than ws_beam_select_workspace()");
