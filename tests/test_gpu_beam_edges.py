@@ -186,3 +186,48 @@ def test_scales_of_other_caches_are_not_read(R, dtype):
     import __graft_entry__ as g
     r = subprocess.run([sys.executable, "-c", SHORT.format(root=g.ROOT, dtype=dtype)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, (r.returncode, r.stderr[-1500:])
+
+
+# ------------------------------------------------------------------ two heads per CTA, in parts
+@pytest.mark.parametrize("n,hkv,page,block,causal", [(31, 5, 64, 16, True), (31, 5, 16, 8, False), (77, 2, 64, 64, True),
+                                                     (52, 3, 48, 16, False), (52, 3, 64, 8, True)])
+def test_attend_8bit_single_row_tiles_of_many_in_parts(R, n, hkv, page, block, causal):
+    """More heads in all than SMs (odd numbers of them too) over caches long enough to be split: short, empty and full
+    requests beside each other."""
+    kv = 1550
+    chunks = [[64, 49, 3, 0, 1, 57][i % 6] if i < 12 else 1 + i % 2 for i in range(n)]
+    lens = [max(c, [kv, 1200, 0 if not c else 5, 700, kv - 1, 130][i % 6]) for i, c in enumerate(chunks)]
+    check_q8(R, Q8Case(chunks, lens, hkv, hkv, page, block=block, causal=causal, seed=n + hkv))
+
+
+@pytest.mark.parametrize("heads", [[0], [1], [4]])
+@pytest.mark.parametrize("block", [16, 8])
+def test_attend_8bit_values_that_are_not_finite_in_parts(R, heads, block):
+    """NaN and infinite values in the first and the last part, in some heads of a pair: those rows of those heads."""
+    n, hkv, c, L = 31, 5, 60, 1553
+    cs = Q8Case([c] * n, [L] * n, hkv, hkv, 16, block=block, seed=5)
+    codes = cs.v8.view(torch.uint8)
+    first, late = L - c + 9, L - 1                         # seen from row 9 on, and by the last row
+    for pos in (first, late):
+        codes[int(cs.table[n - 2, pos // 16]), :, pos % 16] = 0
+    cache = cs.cache(R)
+
+    def attend():
+        return cache.attend(cs.q, cs.kv_len, cs.cu, max_q=c, max_kv=L)[: cs.rows].clone()
+    want = attend()
+    for h in heads:
+        codes[int(cs.table[n - 2, first // 16]), h, first % 16, 7] = 0x7F
+        page = int(cs.table[n - 2, late // 16])
+        codes[page, h, late % 16, 9] = 0xFE
+        cs.scales[1][page, h, late % 16 // block] = 250
+    got = attend()
+    torch.cuda.synchronize()
+    row0 = (n - 2) * c
+    nan, inf = (torch.zeros_like(got, dtype=torch.bool) for _ in range(2))
+    nan[row0 + 9: row0 + c, heads, 7] = True
+    inf[row0 + c - 1, heads, 9] = True
+    # what else the last block holds has another scale now, which rows that see it feel
+    felt = torch.zeros_like(nan)
+    felt[row0 + c - 1 - (late % 16 % block): row0 + c, heads] = True
+    assert bool(torch.isnan(got)[nan].all()) and bool((got[inf] == -math.inf).all())
+    assert torch.equal(got[~nan & ~inf & ~felt], want[~nan & ~inf & ~felt])
