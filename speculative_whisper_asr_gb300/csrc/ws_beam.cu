@@ -384,14 +384,18 @@ const char* check_beam_apart(const ws_beam_args* a) {
 }
 
 struct Plan { int parts, part; size_t stat, bytes; };
-// Twelve CTAs of 128 threads run on an SM: as many parts as fill that round
-// (a row is read once whatever they are), none longer than 256 logits per
-// thread, and none shorter than four.  480 rows of 51,866: 3 parts 33 us.
+// Ten CTAs of 128 threads run on an SM (44 and 46 registers): as many parts as
+// fill that round (a row is read once whatever they are), none longer than 256
+// logits per thread, and none shorter than four.  480 rows of 51,866: 3 parts
+// 33 us.  Parts for twelve CTAs ran into a second round (5 beams over and over on
+// the same logits of 16 / 32 / 64 requests: 19.0 / 20.8 / 23.9 us, and 17.7 /
+// 18.7 / 22.1 in this form), and registers for twelve spill (18.5 / 20.5 / 24.2).
+constexpr int BM_RESIDENT = 10;
 Plan make_plan(const ws_beam_args& a) {
   Plan q = {};
   const long long rows = (long long)a.n * a.beams;
   const int least = (a.vocab + BM_PART - 1) / BM_PART, most = min(BM_PARTS, (a.vocab + 4 * BM_NT - 1) / (4 * BM_NT));
-  const int want = max(least, (int)min((long long)most, 12ll * 152 / rows));
+  const int want = max(least, (int)min((long long)most, (long long)BM_RESIDENT * 152 / rows));
   q.part = ((a.vocab + want - 1) / want + BM_STEP - 1) / BM_STEP * BM_STEP;
   q.parts = (a.vocab + q.part - 1) / q.part;
   q.stat = (size_t)rows * q.parts * (a.beams + 1) * 8;

@@ -1,4 +1,5 @@
-"""Refusals of the beam selection where arrays share elements (no GPU needed)."""
+"""Refusals of the beam selection where arrays share elements, and the parts that
+its rows are cut into (no GPU needed)."""
 import pytest
 
 from test_beam_operators_host import B, _beam, _refused  # noqa: F401  (B: the fixture)
@@ -38,3 +39,16 @@ def test_beam_outputs_beside_each_other_pass(B, ok):
             "assert rc == B.WS_ECUDA, (rc, B.ws_last_error())\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, env=dict(os.environ, CUDA_VISIBLE_DEVICES=""))
     assert r.returncode == 0, r.stderr[-800:]
+
+
+@pytest.mark.parametrize("n,beams", [(1, 1), (16, 5), (20, 5), (24, 5), (32, 5), (60, 5), (72, 5), (95, 5), (96, 5), (32, 12), (33, 4)])
+@pytest.mark.parametrize("vocab", [700, 20000, 51866])
+def test_beam_parts_run_at_once(B, n, beams, vocab):
+    """The parts of all rows, each a CTA, are no more than ten per SM, what the kernel's registers allow, unless a row
+    needs that many; the workspace has beams + 1 candidates and a pair of sums of each."""
+    bare = {k: 0 for k in ("tokens", "tokens_out", "length", "length_out", "n_done", "n_done_out", "done_score", "done_length", "done_tokens")}
+    need = B.ws_beam_select_workspace(_beam(B, n=n, beams=beams, vocab=vocab, ld=vocab, eos_id=-1, **bare))
+    rows = n * beams
+    parts = need // (rows * (beams + 2) * 8)
+    assert need == -(-rows * parts * (beams + 2) * 8 // 256) * 256
+    assert parts >= 1 and (rows * parts <= 10 * 152 or parts == -(-vocab // 32768))
