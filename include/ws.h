@@ -478,7 +478,7 @@ typedef struct {
   const int32_t* page_table;   /* [n_slots, table_stride] (device) */
   int32_t n_slots;             /* >= 1 */
   int32_t table_stride;        /* pages listed per slot, >= 1 */
-  /* WS_E4M3 only, not read otherwise: */
+  /* WS_E4M3 only, not read otherwise (a program built before they existed may pass the shorter structure): */
   uint8_t* k_scale;
   uint8_t* v_scale;
   int64_t scale_page_stride, scale_head_stride;     /* bytes, page_size / scale_block .. 2^31 - 1 (a dimension of one: any) */
@@ -528,13 +528,22 @@ size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attent
  * Rows of requests with kv_len <= 0, or with an id outside [0, n_slots), see
  * nothing.  Cached values behind kv_len are not read into any result, and what
  * a row does not see does not reach it, infinite or NaN included.  Rows
- * outside every chunk and mass behind kv_len are left as they were.
+ * outside every chunk and mass behind kv_len are left as they were.  In bf16
+ * and 8 bits the sums of chunks of more than 40 and 48 rows per KV head (chunk
+ * rows times the query heads that share it) are taken relative to a weight as
+ * small as 2^-60 of the row's largest: values of 2^45 and more may overflow
+ * fp32 there.
  * A cache in 8 bits is read as the values it stands for (queries and outputs
- * bfloat16, the same sums).  The weights enter the value product as fp16, and
- * besides its 2^-11 of itself a weight may be off by 2^-30 of the row's largest
- * weight times the largest value scale among the keys that the row sees, over
- * its value's own.
- * The weights are not accumulated: mass is WS_EUNSUPPORTED. */
+ * bfloat16, the same sums).  In chunks of up to 48 rows per KV head, or with
+ * scale <= 0 or more than 128 query heads per KV head, the weights enter the
+ * value product as fp16, and besides its 2^-11 of itself a weight may be off by
+ * 2^-30 of the row's largest weight times the largest value scale among the
+ * keys that the row sees, over its value's own.  In longer chunks they enter it
+ * as bf16, 2^-8 at most of each, and elements of 2^128 and more are infinite.
+ * Scores may pass fp32 on the way where a key's scale is above 2^111 (byte
+ * 238), and queries whose largest element is below 2^-126 may count as zeros.
+ * The weights are not accumulated, since eviction, which they serve, has no
+ * form for these caches: mass is WS_EUNSUPPORTED. */
 int ws_paged_attention(const ws_paged_cache* cache, const ws_attention_args* args, void* workspace,
                        size_t workspace_bytes, ws_stream stream);
 
@@ -657,8 +666,9 @@ typedef struct {
  * queries are turned on the way (rotary positions, as in the drafter,
  * Whisper-Flash App. A.2): pair i of a row at position m becomes
  *   (x cos a - y sin a, x sin a + y cos a),  a = 2 pi m turns[i] / 2^64,
- * m and turns[i] multiplied modulo 2^64: the angle of any 32-bit position is
- * exact to 2^-32 of a turn.  Values are stored as they are.
+ * m and turns[i] multiplied modulo 2^64, the product as an fp32 number of half
+ * turns: the angle of any 32-bit position is good to 2^-26 of a turn.  Values
+ * are stored as they are.
  * A cache in 8 bits: with m the largest finite |x| of the rows that a block
  * and head receives, after the turn, and s the smallest power of two (2^-127
  * at least) with m <= 448 s, a block that begins with this call takes the
@@ -669,8 +679,9 @@ typedef struct {
  * Positions before 0, behind the page table, or on a page id outside
  * [0, n_pages) are not stored; rows of a slot outside [0, n_slots) and rows
  * before position 0 are left out altogether, their queries too.  Pages that
- * the call writes belong to one slot each.  Rows outside every chunk, and the
- * cache elsewhere, are left as they were. */
+ * the call writes belong to one slot each, and share no elements with k, v, q
+ * and q_out.  Rows outside every chunk, and the cache elsewhere, are left as
+ * they were. */
 int ws_cache_append(const ws_paged_cache* cache, const ws_append_args* args, ws_stream stream);
 
 /* Arguments of ws_cache_reorder (device pointers; sizes are host ints). */
@@ -693,8 +704,10 @@ typedef struct {
  * So n_slots * table_stride pages suffice for any number of steps: each slot
  * starts with pages of its own, listed once, and full pages are only read.
  * Caches that share a page table (a model's layers) take one call each, one
- * of them, in any order, with page_table.  All is done in place, and nothing
- * is allocated. */
+ * of them, in any order, with page_table.  A request whose first beam's slot is
+ * outside [0, n_slots) is left as it is; of the others, beams of such a slot
+ * are left out, and beams whose parent has one keep their own.  All is done in
+ * place, and nothing is allocated. */
 int ws_cache_reorder(const ws_paged_cache* cache, const ws_reorder_args* args, ws_stream stream);
 
 /* Arguments of ws_beam_select (device pointers; sizes are host ints). */

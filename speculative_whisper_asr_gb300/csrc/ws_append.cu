@@ -16,7 +16,9 @@
 // its largest values and for its codes.
 // 4 chunks of up to 2048 rows, 32 query and 8 key/value heads in 8 bits (77 MB):
 // 24.6 us, 3.1 TB/s; the copy rate would take 11.  What is left is latency: a
-// tile's chain of lengths, page and rows, and the agreement on the scales.
+// tile's chain of lengths, page and rows, and the agreement on the scales.  (The
+// 8-bit form spills four bytes at the 64 registers that let two CTAs of 512
+// threads run on an SM.)
 #include <string>
 #include <type_traits>
 
@@ -359,12 +361,14 @@ extern "C" int ws_cache_append(const ws_paged_cache* cache, const ws_append_args
   while (tokens < want && tokens < AP_T) tokens *= 2;
   p.tile = q8 ? cache->scale_block : tokens;
   const long long tiles = q8 ? ((long long)args->max_q + p.tile - 2) / p.tile + 1 : (args->max_q + p.tile - 1) / p.tile;
-  // Heads split over CTAs until there are eight times the threads an SM holds:
-  // more CTAs hide each other's chains of lengths, pages and rows, and compute
-  // more angles (chunks of up to 2048 rows, a quarter of that 24.6 us, twice 26.8)
+  // Heads split over CTAs until there are 2048 threads per SM, two rounds at
+  // 61-64 registers: more CTAs hide each other's chains of lengths, pages and
+  // rows, and compute more angles (the same inputs again and again, in 8 bits
+  // chunks of up to 2048 rows 22.8 us, half as many CTAs 25.6, twice 25.5;
+  // 480 single tokens 25.4 / 24.1 / 29.5)
   const long long units = tiles * args->n_req;
   const int most = (p.items + AP_H - 1) / AP_H, least = (p.items + AP_MAX - 1) / AP_MAX;
-  const long long wanted = (16ll * 152 * 16 / tokens + units - 1) / units;
+  const long long wanted = (16ll * SMS * 16 / tokens + units - 1) / units;
   int groups = (int)max((long long)least, min((long long)most, wanted));
   p.per = ((p.items + groups - 1) / groups + AP_H - 1) / AP_H * AP_H;
   groups = (p.items + p.per - 1) / p.per;

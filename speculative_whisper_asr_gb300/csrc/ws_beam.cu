@@ -21,8 +21,8 @@
 // finished transcripts.  Then each thread moves a column of the transcripts for
 // all beams, so the move may be in place.
 // 96 requests x 5 beams over 51,866 tokens (100 MB): 33 us, of which the scan,
-// one round of CTAs, takes 23 (4.4 TB/s) and the merge 8, a chain of latencies;
-// one request 14.
+// one round of CTAs, takes 23 (4.4 TB/s) and the merge 8, a chain of latencies
+// (80 registers and four bytes spilled); one request 14.
 #include <string>
 
 #include "ws_paged.cuh"
@@ -70,7 +70,7 @@ __device__ __forceinline__ Two plus(Two a, float b) {
   return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
 }
 // x - log(y), y > 0: exponent and significand (0.75 .. 1.5) of y apart, with log 2 in a part whose multiples are exact
-// and the rest; good to 2^-24 of the significand's logarithm.
+// and the rest (Cody and Waite's reduction); good to 2^-24 of the significand's logarithm.
 __device__ __forceinline__ Two less_log(Two x, float y) {
   const int e = (int)(__float_as_uint(y) - 0x3F400000u) >> 23;
   const float f = __uint_as_float(__float_as_uint(y) - ((uint32_t)e << 23));
@@ -395,7 +395,7 @@ Plan make_plan(const ws_beam_args& a) {
   Plan q = {};
   const long long rows = (long long)a.n * a.beams;
   const int least = (a.vocab + BM_PART - 1) / BM_PART, most = min(BM_PARTS, (a.vocab + 4 * BM_NT - 1) / (4 * BM_NT));
-  const int want = max(least, (int)min((long long)most, (long long)BM_RESIDENT * 152 / rows));
+  const int want = max(least, (int)min((long long)most, (long long)BM_RESIDENT * SMS / rows));
   q.part = ((a.vocab + want - 1) / want + BM_STEP - 1) / BM_STEP * BM_STEP;
   q.parts = (a.vocab + q.part - 1) / q.part;
   q.stat = (size_t)rows * q.parts * (a.beams + 1) * 8;

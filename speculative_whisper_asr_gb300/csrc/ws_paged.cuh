@@ -10,6 +10,8 @@
 
 #include "ws_internal.cuh"
 
+constexpr int SMS = 152;                   // of the GPU that the grids are sized for
+
 // Bytes per element of a cache, and of the rows that go into and come out of it.
 inline int cache_es(const ws_paged_cache& c) { return c.dtype == WS_F32 ? 4 : c.dtype == WS_BF16 ? 2 : 1; }
 inline int row_es(const ws_paged_cache& c) { return c.dtype == WS_F32 ? 4 : 2; }

@@ -621,7 +621,7 @@ struct Plan {
   bool parts = false;                      // the first kernel leaves partials to be joined
   size_t lse = 0, ml = 0, o = 0, nl = 0, next = 0, bytes = 0;
 };
-constexpr int SMS = 152, SLOTS = 2 * SMS;  // two streaming CTAs on each of 152 SMs
+constexpr int SLOTS = 2 * SMS;             // two streaming CTAs on each SM
 
 // `block`: the rows of a context's verify blocks (at most 16 per KV head).  A
 // row has to come out the same bits in blocks of any height and beside any

@@ -280,7 +280,7 @@ __device__ __forceinline__ void widen16(const uint4& w, uint32_t s, uint4& lo, u
 // have to be bf16: in fp16 their reference moves at 2^15, which some row of a
 // warp does in most tiles (348 us).  MODE_ANY: keys like values, which any
 // blocks of scales allow.
-// The call above in 8 bits, pages and blocks of 16: 282-287 us, 0.70 PFLOP/s;
+// The call above in 8 bits, pages and blocks of 16: 285-289 us, 0.69 PFLOP/s;
 // blocks of 8 in pages of 64 277, in pages of 16 345.  Without the conversions'
 // arithmetic it would take 245: they share the schedulers' issue slots with
 // the softmax.

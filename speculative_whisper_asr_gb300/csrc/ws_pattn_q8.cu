@@ -20,14 +20,14 @@
 // value's its weight.  Weights enter the product as fp16, 2^-11 of each at
 // most, an eighth of the bf16 output's own step, relative to 2^E, the largest
 // value scale that the row has seen so far, so that they stay within fp16
-// whatever the scales are.  They are at most 2^8 and stored 2^7 times larger, so that fp16's last step is
-// 2^-31 of a row's largest weight times the largest value scale.  Queries, 8 bits each, are
-// exact in fp16 once a row's largest is brought to 1 .. 2 by a power of two,
-// which joins the row's scale; elements below 2^-17 of the largest round to
-// 2^-25 of it, the step of the fp32 sums.
+// whatever the scales are.  They are at most 2^8 and stored 2^7 times larger, so
+// that fp16's last step is 2^-31 of a row's largest weight times the largest
+// value scale.  Queries, 8 bits each, are exact in fp16 once a row's largest is
+// brought to 1 .. 2 by a power of two, which joins the row's scale; elements
+// below 2^-17 of the largest round to 2^-25 of it, the step of the fp32 sums.
 //
-// 16 requests x 1 row, 32 heads on 8, up to 65,536 positions (680 MB): 131 us,
-// 5.2 TB/s; the copies alone take 117.  96 x 9 rows, 20 heads, 375-1500
+// 16 requests x 1 row, 32 heads on 8, up to 65,536 positions (680 MB): 132 us,
+// 5.1 TB/s; the copies alone take 117.  96 x 9 rows, 20 heads, 375-1500
 // positions (234 MB): 71 us, 3.3 TB/s; the copies alone take 54, because a
 // CTA has a dozen microseconds of work between its rings' first fill and the
 // join of its warps.  Two CTAs per SM with 6 slots per warp 90 and 162 us, 8

@@ -120,11 +120,14 @@ extern "C" int ws_cache_reorder(const ws_paged_cache* cache, const ws_reorder_ar
   p.c = paged_copy(*cache);
   p.a = *args;
   p.ppr_log = cache->dtype == WS_F32 ? 4 : cache->dtype == WS_BF16 ? 3 : 2;
-  // two rounds of CTAs (16 per SM), each with as much of a request as comes
-  // out: a CTA's look at lengths, parents and pages is a chain of latencies
-  // (a CTA per head: 96 requests x 5 beams x 80 heads 93 us, in this form 45)
+  // 32 CTAs per SM in all, each with as much of a request as comes out: a CTA's
+  // look at lengths, parents and pages is a chain of latencies (a CTA per head:
+  // 96 requests x 5 beams x 80 heads 93 us, in this form 45).  At 46 / 65 / 131
+  // registers (4 / 8 / 16 beams) 10 / 7 / 3 of them run on an SM at a time; two
+  // rounds of those take 46 us for the 45, 59 for 57 (40 x 12 beams x 80 heads)
+  // and 35 for 38 (96 x 12 x 20 heads), 64 per SM 48, 67 and 46.
   const long long pieces = ((long long)cache->page_size << p.ppr_log) * 2 * cache->n_kv_heads;
-  const dim3 grid((unsigned)min((pieces + RO_NT - 1) / RO_NT, max(1ll, 32ll * 152 / args->n_req)), (unsigned)args->n_req);
+  const dim3 grid((unsigned)min((pieces + RO_NT - 1) / RO_NT, max(1ll, 32ll * SMS / args->n_req)), (unsigned)args->n_req);
   const cudaStream_t s = (cudaStream_t)stream;
   if (args->beams <= 4) launch<4>(p, grid, s);
   else if (args->beams <= 8) launch<8>(p, grid, s);
