@@ -329,7 +329,7 @@ int fail(int code, const char* msg) {
 
 bool apart(const void* a, const void* b, long long bytes_a, long long bytes_b) {
   const char *x = (const char*)a, *y = (const char*)b;
-  return !x || !y || x + bytes_a <= y || y + bytes_b <= x;
+  return !x || !y || bytes_a <= 0 || bytes_b <= 0 || x + bytes_a <= y || y + bytes_b <= x;
 }
 
 const char* check_beam(const ws_beam_args* a) {

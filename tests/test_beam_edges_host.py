@@ -22,7 +22,7 @@ def test_beam_outputs_that_share_elements_refused(B, bad):
 
 @pytest.mark.parametrize("ok", [dict(), dict(score_out=M, tokens_out=3 * M, length_out=5 * M, n_done_out=7 * M), dict(token=4096 + 60),
                                 dict(parent=2 * M - 60), dict(done_score=9 * M, done_length=9 * M + 60, done_tokens=9 * M + 120),
-                                dict(parent=2 * M + 60, token=2 * M + 120)])
+                                dict(parent=2 * M + 60, token=2 * M + 120), dict(max_done=0, done_score=2 * M + 8, done_length=4096)])
 def test_beam_outputs_beside_each_other_pass(B, ok):
     """What passes the checks ends at the missing GPU, in a process of its own."""
     import os
