@@ -529,10 +529,10 @@ size_t ws_paged_attention_workspace(const ws_paged_cache* cache, const ws_attent
  * nothing.  Cached values behind kv_len are not read into any result, and what
  * a row does not see does not reach it, infinite or NaN included.  Rows
  * outside every chunk and mass behind kv_len are left as they were.  In bf16
- * and 8 bits the sums of chunks of more than 40 and 48 rows per KV head (chunk
- * rows times the query heads that share it) are taken relative to a weight as
- * small as 2^-60 of the row's largest: values of 2^45 and more may overflow
- * fp32 there.
+ * and 8 bits the sums are taken relative to a weight as small as 2^-8 of the
+ * row's largest, in chunks of more than 40 and 48 rows per KV head (chunk rows
+ * times the query heads that share it) 2^-60: they may overflow where 2^8 or
+ * 2^60 times the largest value times the positions passes fp32.
  * A cache in 8 bits is read as the values it stands for (queries and outputs
  * bfloat16, the same sums).  In chunks of up to 48 rows per KV head, or with
  * scale <= 0 or more than 128 query heads per KV head, the weights enter the

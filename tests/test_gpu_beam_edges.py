@@ -36,7 +36,7 @@ def test_append_to_blocks_of_any_scale(R, byte, block):
 # ------------------------------------------------------------------ what a row does not see
 @pytest.mark.parametrize("c,hq", [(2, 1), (9, 1), (16, 2), (5, 6)])
 @pytest.mark.parametrize("block,L", [(8, 265), (8, 281), (16, 273), (32, 257), (64, 1665)])
-@pytest.mark.parametrize("gap", [24, 60, 140])
+@pytest.mark.parametrize("gap", [24, 60, 140, 200])
 def test_attend_8bit_scale_that_a_row_does_not_see(R, c, hq, block, L, gap):
     """A block that starts with the last position, which the chunk's last row alone sees, and whose values' scale is
     2^gap of the others': the other rows' bits are those without it."""
@@ -55,7 +55,8 @@ def test_attend_8bit_scale_that_a_row_does_not_see(R, c, hq, block, L, gap):
     got = attend()
     for a, b in zip(got, want):
         assert torch.equal(a[: c - 1], b[: c - 1])
-    assert bool(torch.isfinite(got[0]).all()) and torch.equal(got[1], want[1])
+    assert torch.equal(got[1], want[1])
+    assert gap == 200 or bool(torch.isfinite(got[0]).all())           # values of 2^122 may pass fp32 in the sums
     assert bool((got[0][c - 1] != want[0][c - 1]).any())
 
 
